@@ -1,0 +1,104 @@
+// Shared by the kernels of attention with key ranges: what a query row sees,
+// the group-row numbering and the gradient's row state in the workspace.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <limits.h>
+#include <stdint.h>
+
+#include "internal.h"
+
+namespace flashbob {
+namespace attn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kSMs = 152;          // grids are sized for the GB300
+constexpr int kBoundRows = 64;     // group rows summarised by one bounds entry
+constexpr int kRowPad = 128;       // group rows are padded to this in the workspace
+
+// The keys lo <= j < hi that a query sees and its position; an empty range
+// is lo = INT_MAX, hi = 0, so that it never widens a hull.
+struct RowView {
+  int lo, hi, pos;
+};
+
+__device__ __forceinline__ RowView empty_view() { return {INT_MAX, 0, 0}; }
+
+__device__ __forceinline__ RowView row_view(const int* __restrict__ ranges,
+                                            const int* __restrict__ q_pos, size_t bq, int i,
+                                            int Nk, int causal) {
+  RowView v{0, Nk, q_pos ? q_pos[bq + i] : i};
+  if (ranges) {  // clamped: whatever the array holds, no key outside 0 .. Nk - 1 is read
+    const int2 r = reinterpret_cast<const int2*>(ranges)[bq + i];
+    v.lo = max(r.x, 0);
+    v.hi = min(r.y, Nk);
+  }
+  if (causal && v.pos < v.hi) v.hi = v.pos + 1;
+  if (v.lo >= v.hi) v.lo = INT_MAX, v.hi = 0;
+  return v;
+}
+
+// Minimum and maximum over a warp.
+__device__ __forceinline__ int warp_min(int v) { return __reduce_min_sync(0xffffffffu, v); }
+__device__ __forceinline__ int warp_max(int v) { return __reduce_max_sync(0xffffffffu, v); }
+
+// Row state that the gradient kernels read, one entry for each group row,
+// rows padded to a multiple of kRowPad per (batch, key/value head):
+//   info  {lo, hi, pos, slope log2 e (as bits)},
+//   ld    {L log2 e, D}; +inf in place of L for rows that see nothing and for
+//         the padding, so that P = exp2(s - L) is 0 there,
+// and for each kBoundRows rows {min lo, max hi, max lo, min hi}: the hull of
+// their ranges and their intersection (the padding takes no part).
+struct GradRows {
+  int4* bounds;
+  int4* info;
+  float2* ld;
+  int pitch;  // padded rows per (batch, key/value head)
+};
+
+__host__ __device__ inline int padded_rows(int rows) {
+  return (rows + kRowPad - 1) / kRowPad * kRowPad;
+}
+
+__host__ __device__ inline GradRows grad_rows(void* workspace, int groups, int rows) {
+  GradRows g;
+  g.pitch = padded_rows(rows);
+  const size_t n = static_cast<size_t>(groups) * g.pitch;
+  g.bounds = static_cast<int4*>(workspace);
+  g.info = g.bounds + n / kBoundRows;
+  g.ld = reinterpret_cast<float2*>(g.info + n);
+  return g;
+}
+
+// Partial results of a split forward: for split s and global row r (row-major
+// [B, H, Nq]) the unnormalised sum over its keys [s][r][d], its maximum and
+// its sum of weights (log2 units).
+struct Partials {
+  float* o;
+  float2* ml;
+};
+
+__host__ __device__ inline Partials partials(void* workspace, size_t rows, int d, int splits) {
+  Partials p;
+  p.ml = static_cast<float2*>(workspace);
+  p.o = reinterpret_cast<float*>(p.ml + ((rows * splits + 1) & ~static_cast<size_t>(1)));
+  return p;
+}
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Four consecutive elements, aligned to their size.
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
+  const uint2 r = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u),
+                     __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xFFFF0000u));
+}
+
+}  // namespace attn
+}  // namespace flashbob

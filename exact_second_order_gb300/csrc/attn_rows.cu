@@ -1,0 +1,253 @@
+// Row-wise kernels around attention with key ranges: the ranges themselves
+// (from document offsets and prefixes), the row state of the gradient, and
+// the join of a forward that was split over the keys.
+#include <math.h>
+
+#include "attn_common.cuh"
+
+namespace flashbob {
+namespace {
+using namespace attn;
+
+// ---------------------------------------------------------------------------
+// Key ranges.  Query i of batch entry b sits at p = q_start[b] + i; its
+// document is the last one that starts at or before p (binary search over the
+// M + 1 sorted offsets, in shared memory where they fit).
+// ---------------------------------------------------------------------------
+constexpr int kRangeThreads = 256;
+constexpr int kRangeRows = 1024;       // rows per block
+constexpr int kRangeOffsets = 8192;    // offsets that are kept in shared memory
+
+__global__ void __launch_bounds__(kRangeThreads)
+    ranges_kernel(const int* __restrict__ off, const int* __restrict__ prefix,
+                  const int* __restrict__ q_start, int* __restrict__ ranges,
+                  int* __restrict__ q_pos, int M, int Nq, int Nk, int causal) {
+  __shared__ int s_off[kRangeOffsets];
+  const int b = blockIdx.y;
+  const int start = q_start ? q_start[b] : 0;
+  const int* o = off ? off + static_cast<size_t>(b) * (M + 1) : nullptr;
+  const int* pre = prefix ? prefix + static_cast<size_t>(b) * M : nullptr;
+  if (o && M < kRangeOffsets) {
+    for (int k = threadIdx.x; k <= M; k += kRangeThreads) s_off[k] = o[k];
+    __syncthreads();
+    o = s_off;
+  }
+  for (int u = 0; u < kRangeRows / kRangeThreads; ++u) {
+    const long long i = static_cast<long long>(blockIdx.x) * kRangeRows + u * kRangeThreads +
+                        threadIdx.x;
+    if (i >= Nq) return;
+    const int p = static_cast<int>(static_cast<unsigned>(start) + static_cast<unsigned>(i));
+    int lo = 0, hi = 0;
+    bool inside = p >= 0;
+    if (o) {
+      int a = 0, z = M + 1;  // first offset above p lies in [a, z]
+      while (a < z) {
+        const int mid = (a + z) >> 1;
+        if (o[mid] <= p) a = mid + 1;
+        else z = mid;
+      }
+      const int m = a - 1;  // the document
+      inside = inside && m >= 0 && m < M;
+      if (inside) {
+        lo = o[m];
+        hi = o[m + 1];
+        // lo <= p, so lo + prefix cannot pass p + 1 by more than the prefix:
+        // compared as a difference it cannot overflow.
+        if (causal) {
+          const int after = pre ? max(p - lo, pre[m] - 1) : p - lo;
+          hi = after < hi - lo ? lo + after + 1 : hi;
+        }
+      }
+    } else if (inside) {
+      hi = causal && p < Nk ? p + 1 : Nk;
+    }
+    hi = min(hi, Nk);
+    const size_t at = static_cast<size_t>(b) * Nq + i;
+    reinterpret_cast<int2*>(ranges)[at] = inside ? make_int2(lo, hi) : make_int2(0, 0);
+    if (q_pos) q_pos[at] = p;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Row state of the gradient.  Eight lanes take a row: D = dO . O in fp32,
+// the row's range, position and slope, and the bounds of 64 rows.
+// ---------------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ float dot_part(const T* __restrict__ x, const T* __restrict__ y, int d,
+                                          int lane8) {
+  float s = 0.f;
+  if ((d & 3) == 0) {
+    for (int k = 4 * lane8; k < d; k += 32) {
+      const float4 a = ld4(x + k), b = ld4(y + k);
+      s = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s))));
+    }
+  } else {
+    for (int k = lane8; k < d; k += 8) s = fmaf(to_f(x[k]), to_f(y[k]), s);
+  }
+  return s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+    grad_rows_kernel(const T* __restrict__ O, const T* __restrict__ dO,
+                     const float* __restrict__ L, const int* __restrict__ ranges,
+                     const int* __restrict__ q_pos, const float* __restrict__ slopes,
+                     void* workspace, int B, int H, int Hkv, int Nq, int Nk, int d, int causal) {
+  __shared__ int s_bound[4][8];
+  const int G = H / Hkv, rows = G * Nq;
+  const int g = blockIdx.z * Hkv + blockIdx.y;
+  const GradRows out = grad_rows(workspace, B * Hkv, rows);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lane8 = lane & 7;
+  int b_lo = INT_MAX, b_hi = 0, i_lo = 0, i_hi = INT_MAX;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int r = blockIdx.x * kBoundRows + warp * 8 + u * 4 + (lane >> 3);
+    float dot = 0.f;
+    RowView v = empty_view();
+    float l = 0.f;
+    const bool live = r < rows;
+    const size_t row = static_cast<size_t>(g) * rows + r;
+    if (live) {
+      v = row_view(ranges, q_pos, static_cast<size_t>(blockIdx.z) * Nq, r % Nq, Nk, causal);
+      if (v.hi > 0) {  // a row that sees nothing may hold anything
+        dot = dot_part(O + row * d, dO + row * d, d, lane8);
+        l = L[row];
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (live) {
+      b_lo = min(b_lo, v.lo);
+      b_hi = max(b_hi, v.hi);
+      i_lo = max(i_lo, v.lo);
+      i_hi = min(i_hi, v.hi);
+    }
+    if (lane8 == 0) {
+      const size_t at = static_cast<size_t>(g) * out.pitch + r;
+      const float slope = slopes && live ? slopes[blockIdx.y * G + r / Nq] * kLog2e : 0.f;
+      out.info[at] = make_int4(v.lo, v.hi, v.pos, __float_as_int(slope));
+      out.ld[at] = v.hi > 0 ? make_float2(l * kLog2e, dot) : make_float2(INFINITY, 0.f);
+    }
+  }
+  b_lo = warp_min(b_lo);
+  b_hi = warp_max(b_hi);
+  i_lo = warp_max(i_lo);
+  i_hi = warp_min(i_hi);
+  if (lane == 0) {
+    s_bound[0][warp] = b_lo;
+    s_bound[1][warp] = b_hi;
+    s_bound[2][warp] = i_lo;
+    s_bound[3][warp] = i_hi;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int4 x = make_int4(INT_MAX, 0, 0, INT_MAX);
+    for (int w = 0; w < 8; ++w) {
+      x.x = min(x.x, s_bound[0][w]);
+      x.y = max(x.y, s_bound[1][w]);
+      x.z = max(x.z, s_bound[2][w]);
+      x.w = min(x.w, s_bound[3][w]);
+    }
+    out.bounds[static_cast<size_t>(g) * (out.pitch / kBoundRows) + blockIdx.x] = x;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Join of a split forward: with the splits' maxima m_s and sums l_s (log2
+// units) and unnormalised O_s, m = max m_s, w_s = exp2(m_s - m),
+// O = sum w_s O_s / sum w_s l_s, L = (m + log2 sum w_s l_s) ln 2.  One warp a
+// row; always in the order of the splits.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(128)
+    join_kernel(void* workspace, T* __restrict__ O, float* __restrict__ L, size_t rows, int d,
+                int splits) {
+  const size_t row = static_cast<size_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  const Partials p = partials(workspace, rows, d, splits);
+  float m = -INFINITY;
+  for (int s = 0; s < splits; ++s) m = fmaxf(m, p.ml[s * rows + row].x);
+  float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < splits; ++s) {
+    const float2 ml = p.ml[s * rows + row];
+    if (ml.x == -INFINITY) continue;  // the split saw no key: its O_s is not written
+    const float w = exp2f(ml.x - m);
+    l = fmaf(w, ml.y, l);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (lane + 32 * c < d) acc[c] = fmaf(w, p.o[(s * rows + row) * d + lane + 32 * c], acc[c]);
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (lane + 32 * c < d) put(O + row * d + lane + 32 * c, acc[c] * inv);
+  if (lane == 0) L[row] = (m + log2f(l)) * kLn2;  // -inf for a row that sees nothing
+}
+
+template <typename T>
+cudaError_t launch_grad_rows(const AttnArgs& a) {
+  const int rows = a.H / a.Hkv * a.Nq;
+  const dim3 grid(padded_rows(rows) / kBoundRows, a.Hkv, a.B);
+  grad_rows_kernel<T><<<grid, 256, 0, a.stream>>>(
+      static_cast<const T*>(a.O), static_cast<const T*>(a.dO), a.L, a.ranges, a.q_pos, a.slopes,
+      a.workspace, a.B, a.H, a.Hkv, a.Nq, a.Nk, a.d, a.causal ? 1 : 0);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_join(const AttnArgs& a, int splits) {
+  const size_t rows = static_cast<size_t>(a.B) * a.H * a.Nq;
+  join_kernel<T><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, a.stream>>>(
+      a.workspace, static_cast<T*>(a.O), a.L, rows, a.d, splits);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t attn_grad_rows(const AttnArgs& a) {
+  return a.bf16 ? launch_grad_rows<__nv_bfloat16>(a) : launch_grad_rows<float>(a);
+}
+
+cudaError_t attn_join(const AttnArgs& a, int splits) {
+  return a.bf16 ? launch_join<__nv_bfloat16>(a, splits) : launch_join<float>(a, splits);
+}
+
+cudaError_t attn_ranges(const int* doc_offsets, const int* prefix, const int* q_start, int* ranges,
+                        int* q_pos, int B, int M, int Nq, int Nk, bool causal,
+                        cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((static_cast<long long>(Nq) + kRangeRows - 1) / kRangeRows),
+                  B);
+  ranges_kernel<<<grid, kRangeThreads, 0, stream>>>(doc_offsets, prefix, q_start, ranges, q_pos, M,
+                                                    Nq, Nk, causal ? 1 : 0);
+  return cudaGetLastError();
+}
+
+size_t attn_forward_workspace(const AttnArgs& a) {
+  const int splits = attn_splits(a);
+  if (splits == 1) return 0;
+  const size_t rows = static_cast<size_t>(a.B) * a.H * a.Nq;
+  const Partials p = partials(nullptr, rows, a.d, splits);
+  return reinterpret_cast<size_t>(p.o) + rows * splits * a.d * sizeof(float);
+}
+
+size_t attn_grad_workspace(const AttnArgs& a) {
+  const int rows = a.H / a.Hkv * a.Nq, groups = a.B * a.Hkv;
+  const GradRows g = grad_rows(nullptr, groups, rows);
+  return reinterpret_cast<size_t>(g.ld) +
+         static_cast<size_t>(groups) * g.pitch * sizeof(float2);
+}
+
+// A grid that leaves SMs idle is cut along the keys, so that the tiles of one
+// row block run side by side and are joined afterwards.
+int attn_splits(const AttnArgs& a) {
+  const long long blocks = static_cast<long long>(a.B) * a.Hkv *
+                           ((static_cast<long long>(a.H / a.Hkv) * a.Nq + 63) / 64);
+  const int tiles = (a.Nk + 63) / 64;
+  if (blocks * 2 > kSMs) return 1;
+  const long long s = kSMs / blocks;
+  const long long most = tiles / 4 > 1 ? tiles / 4 : 1;  // four tiles at least in each run
+  return static_cast<int>(s < most ? s : most);
+}
+
+}  // namespace flashbob

@@ -41,6 +41,33 @@ flashbob_status check_sizes(int B, int H, int Hkv, int Nq, int Nk, int d, float 
   return FLASHBOB_OK;
 }
 
+// One buffer of a call: `bytes` from p, read or written; p may be null where
+// the call allows it.
+struct Buf {
+  const void* p;
+  size_t bytes;
+  bool out;
+  bool optional = false;
+};
+
+// Null pointers, alignment, and outputs that overlap an input or another output.
+flashbob_status check_buffers(const Buf* bufs, int n) {
+  for (int i = 0; i < n; ++i)
+    if (!bufs[i].p && !bufs[i].optional) return FLASHBOB_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i)
+    if (!aligned16(bufs[i].p)) return FLASHBOB_ERR_MISALIGNED;
+  for (int i = 0; i < n; ++i) {
+    if (!bufs[i].out || !bufs[i].p) continue;
+    const Range o{(uintptr_t)bufs[i].p, (uintptr_t)bufs[i].p + bufs[i].bytes};
+    for (int j = 0; j < n; ++j) {
+      if (j == i || !bufs[j].p) continue;
+      const Range r{(uintptr_t)bufs[j].p, (uintptr_t)bufs[j].p + bufs[j].bytes};
+      if (overlaps(o, r)) return FLASHBOB_ERR_INVALID_ARG;
+    }
+  }
+  return FLASHBOB_OK;
+}
+
 flashbob_status check_dtype(flashbob_dtype t) {
   return (t == FLASHBOB_F32 || t == FLASHBOB_BF16) ? FLASHBOB_OK : FLASHBOB_ERR_INVALID_ARG;
 }
@@ -303,6 +330,232 @@ flashbob_status flashbob_attention_jvp(const void* Q, const void* K, const void*
   if (error_word_ptr(&a.err) != cudaSuccess) return FLASHBOB_ERR_CUDA;
   const cudaError_t e = tc_jvp_supported(a) ? tc_jvp(a) : simt_jvp(a);
   return e == cudaSuccess ? FLASHBOB_OK : FLASHBOB_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace flashbob {
+namespace {
+
+// Sizes and scalars of the attention calls with key ranges.
+flashbob_status check_attention(const AttnArgs& a, int causal, flashbob_dtype in_dtype) {
+  flashbob_status st = check_dtype(in_dtype);
+  if (st != FLASHBOB_OK) return st;
+  if (causal != 0 && causal != 1) return FLASHBOB_ERR_INVALID_ARG;
+  if (!(isfinite(a.cap) && a.cap >= 0.f)) return FLASHBOB_ERR_INVALID_ARG;
+  st = check_sizes(a.B, a.H, a.Hkv, a.Nq, a.Nk, a.d, a.tau);
+  if (st != FLASHBOB_OK) return st;
+  // The rows of a group of query heads are counted in 32 bits, padding
+  // included, and so are the keys with the tile beyond the last.
+  if (static_cast<long long>(a.H / a.Hkv) * a.Nq > INT_MAX - 1024 || a.Nk > INT_MAX - 1024)
+    return FLASHBOB_ERR_UNSUPPORTED;
+  return FLASHBOB_OK;
+}
+
+// Sizes of the norm-and-rotation calls.  R may be 0 (no rotation); B * N
+// counts grid blocks.
+flashbob_status check_norm(const NormArgs& a, flashbob_dtype in_dtype, int interleaved) {
+  flashbob_status st = check_dtype(in_dtype);
+  if (st != FLASHBOB_OK) return st;
+  if (interleaved != 0 && interleaved != 1) return FLASHBOB_ERR_INVALID_ARG;
+  if (a.B <= 0 || a.N <= 0 || a.H <= 0 || a.Hkv <= 0 || a.Nk <= 0 || a.d <= 0 || a.R < 0 ||
+      a.R > a.d || a.R % 2 != 0 || a.axes < 1)
+    return FLASHBOB_ERR_INVALID_ARG;
+  if (!(isfinite(a.eps) && a.eps > 0.f)) return FLASHBOB_ERR_INVALID_ARG;
+  if (!a.wq != !a.wk) return FLASHBOB_ERR_INVALID_ARG;
+  if (a.R > 0 && !a.freqs) return FLASHBOB_ERR_INVALID_ARG;
+  if (!a.positions && a.axes != 1) return FLASHBOB_ERR_INVALID_ARG;
+  if (a.d > 128 || a.axes > 4 || a.H > kMaxGridY || a.Hkv > kMaxGridY ||
+      static_cast<long long>(a.B) * a.N > INT_MAX)
+    return FLASHBOB_ERR_UNSUPPORTED;
+  return FLASHBOB_OK;
+}
+
+}  // namespace
+}  // namespace flashbob
+
+extern "C" {
+
+flashbob_status flashbob_attention_workspace(int B, int H, int Hkv, int Nq, int Nk, int d,
+                                             flashbob_dtype in_dtype, size_t* forward,
+                                             size_t* gradient) {
+  AttnArgs a{};
+  a.B = B, a.H = H, a.Hkv = Hkv, a.Nq = Nq, a.Nk = Nk, a.d = d, a.tau = 1.f;
+  a.bf16 = in_dtype == FLASHBOB_BF16;
+  const flashbob_status st = check_attention(a, 0, in_dtype);
+  if (st != FLASHBOB_OK) return st;
+  if (forward) *forward = attn_forward_workspace(a);
+  if (gradient) *gradient = attn_grad_workspace(a);
+  return FLASHBOB_OK;
+}
+
+flashbob_status flashbob_attention(const void* Q, const void* K, const void* V, const int* ranges,
+                                   const int* q_pos, const float* slopes, float tau, float cap,
+                                   void* O, float* L, void* workspace, size_t workspace_bytes,
+                                   int B, int H, int Hkv, int Nq, int Nk, int d, int causal,
+                                   flashbob_dtype in_dtype, void* stream) {
+  AttnArgs a{};
+  a.Q = Q, a.K = K, a.V = V, a.ranges = ranges, a.q_pos = q_pos, a.slopes = slopes;
+  a.tau = tau, a.cap = cap, a.O = O, a.L = L, a.workspace = workspace;
+  a.B = B, a.H = H, a.Hkv = Hkv, a.Nq = Nq, a.Nk = Nk, a.d = d;
+  a.causal = causal == 1, a.bf16 = in_dtype == FLASHBOB_BF16, a.stream = (cudaStream_t)stream;
+  flashbob_status st = check_attention(a, causal, in_dtype);
+  if (st != FLASHBOB_OK) return st;
+  const size_t rows = (size_t)B * H * Nq, krows = (size_t)B * Hkv * Nk, e = a.bf16 ? 2 : 4;
+  const size_t need = attn_forward_workspace(a);
+  const Buf bufs[] = {{Q, rows * d * e, false},
+                      {K, krows * d * e, false},
+                      {V, krows * d * e, false},
+                      {ranges, (size_t)B * Nq * 8, false, true},
+                      {q_pos, (size_t)B * Nq * 4, false, true},
+                      {slopes, (size_t)H * 4, false, true},
+                      {O, rows * d * e, true},
+                      {L, rows * 4, true},
+                      {workspace, need, true, need == 0}};
+  st = check_buffers(bufs, 9);
+  if (st != FLASHBOB_OK) return st;
+  if (workspace_bytes < need) return FLASHBOB_ERR_INVALID_ARG;
+  if (error_word_ptr(&a.err) != cudaSuccess) return FLASHBOB_ERR_CUDA;
+  return simt_attn(a) == cudaSuccess ? FLASHBOB_OK : FLASHBOB_ERR_CUDA;
+}
+
+flashbob_status flashbob_attention_grad(const void* Q, const void* K, const void* V, const void* O,
+                                        const float* L, const void* dO, const int* ranges,
+                                        const int* q_pos, const float* slopes, float tau,
+                                        float cap, void* dQ, void* dK, void* dV, void* workspace,
+                                        size_t workspace_bytes, int B, int H, int Hkv, int Nq,
+                                        int Nk, int d, int causal, flashbob_dtype in_dtype,
+                                        void* stream) {
+  AttnArgs a{};
+  a.Q = Q, a.K = K, a.V = V, a.ranges = ranges, a.q_pos = q_pos, a.slopes = slopes;
+  a.tau = tau, a.cap = cap, a.O = const_cast<void*>(O), a.L = const_cast<float*>(L), a.dO = dO;
+  a.dQ = dQ, a.dK = dK, a.dV = dV, a.workspace = workspace;
+  a.B = B, a.H = H, a.Hkv = Hkv, a.Nq = Nq, a.Nk = Nk, a.d = d;
+  a.causal = causal == 1, a.bf16 = in_dtype == FLASHBOB_BF16, a.stream = (cudaStream_t)stream;
+  flashbob_status st = check_attention(a, causal, in_dtype);
+  if (st != FLASHBOB_OK) return st;
+  const size_t rows = (size_t)B * H * Nq, krows = (size_t)B * Hkv * Nk, e = a.bf16 ? 2 : 4;
+  const size_t need = attn_grad_workspace(a);
+  const Buf bufs[] = {{Q, rows * d * e, false},
+                      {K, krows * d * e, false},
+                      {V, krows * d * e, false},
+                      {O, rows * d * e, false},
+                      {L, rows * 4, false},
+                      {dO, rows * d * e, false},
+                      {ranges, (size_t)B * Nq * 8, false, true},
+                      {q_pos, (size_t)B * Nq * 4, false, true},
+                      {slopes, (size_t)H * 4, false, true},
+                      {dQ, rows * d * e, true},
+                      {dK, krows * d * e, true},
+                      {dV, krows * d * e, true},
+                      {workspace, need, true}};
+  st = check_buffers(bufs, 13);
+  if (st != FLASHBOB_OK) return st;
+  if (workspace_bytes < need) return FLASHBOB_ERR_INVALID_ARG;
+  if (error_word_ptr(&a.err) != cudaSuccess) return FLASHBOB_ERR_CUDA;
+  return simt_attn_grad(a) == cudaSuccess ? FLASHBOB_OK : FLASHBOB_ERR_CUDA;
+}
+
+flashbob_status flashbob_attention_ranges(const int* doc_offsets, const int* prefix,
+                                          const int* q_start, int* ranges, int* q_pos, int B,
+                                          int M, int Nq, int Nk, int causal, void* stream) {
+  if (causal != 0 && causal != 1) return FLASHBOB_ERR_INVALID_ARG;
+  if (B <= 0 || Nq <= 0 || Nk <= 0 || M < 0) return FLASHBOB_ERR_INVALID_ARG;
+  if (doc_offsets ? M < 1 : M != 0 || prefix) return FLASHBOB_ERR_INVALID_ARG;
+  if (B > kMaxGridY || M > INT_MAX - 1) return FLASHBOB_ERR_UNSUPPORTED;
+  const Buf bufs[] = {{doc_offsets, (size_t)B * (M + 1) * 4, false, true},
+                      {prefix, (size_t)B * M * 4, false, true},
+                      {q_start, (size_t)B * 4, false, true},
+                      {ranges, (size_t)B * Nq * 8, true},
+                      {q_pos, (size_t)B * Nq * 4, true, true}};
+  const flashbob_status st = check_buffers(bufs, 5);
+  if (st != FLASHBOB_OK) return st;
+  return attn_ranges(doc_offsets, prefix, q_start, ranges, q_pos, B, M, Nq, Nk, causal == 1,
+                     (cudaStream_t)stream) == cudaSuccess
+             ? FLASHBOB_OK
+             : FLASHBOB_ERR_CUDA;
+}
+
+flashbob_status flashbob_qk_norm_rope(const void* QKV, const float* wq, const float* wk,
+                                      const float* freqs, const int* positions,
+                                      const int* kv_start, float eps, void* Q, void* K, void* V,
+                                      int B, int N, int H, int Hkv, int Nk, int d, int R, int axes,
+                                      int interleaved, flashbob_dtype in_dtype, void* stream) {
+  NormArgs a{};
+  a.QKV = QKV, a.wq = wq, a.wk = wk, a.freqs = freqs, a.positions = positions, a.eps = eps;
+  a.Q = Q, a.K = K, a.V = V, a.kv_start = kv_start;
+  a.B = B, a.N = N, a.H = H, a.Hkv = Hkv, a.Nk = Nk, a.d = d, a.R = R, a.axes = axes;
+  a.interleaved = interleaved == 1, a.bf16 = in_dtype == FLASHBOB_BF16;
+  a.stream = (cudaStream_t)stream;
+  flashbob_status st = check_norm(a, in_dtype, interleaved);
+  if (st != FLASHBOB_OK) return st;
+  // Without kv_start every token needs its row of K and V.
+  if (!kv_start && Nk < N) return FLASHBOB_ERR_INVALID_ARG;
+  const size_t e = a.bf16 ? 2 : 4, tokens = (size_t)B * N, cache = (size_t)B * Hkv * Nk * d * e;
+  const Buf bufs[] = {{QKV, tokens * (H + 2 * (size_t)Hkv) * d * e, false},
+                      {wq, (size_t)d * 4, false, true},
+                      {wk, (size_t)d * 4, false, true},
+                      {freqs, (size_t)axes * (R / 2) * 4, false, true},
+                      {positions, axes * tokens * 4, false, true},
+                      {kv_start, (size_t)B * 4, false, true},
+                      {Q, tokens * H * d * e, true},
+                      {K, cache, true},
+                      {V, cache, true}};
+  st = check_buffers(bufs, 9);
+  if (st != FLASHBOB_OK) return st;
+  return qk_norm(a) == cudaSuccess ? FLASHBOB_OK : FLASHBOB_ERR_CUDA;
+}
+
+flashbob_status flashbob_qk_norm_rope_workspace(int B, int N, int H, int Hkv, int d,
+                                                flashbob_dtype in_dtype, size_t* gradient) {
+  NormArgs a{};
+  const float one = 1.f;
+  a.wq = a.wk = &one;
+  a.B = B, a.N = N, a.H = H, a.Hkv = Hkv, a.Nk = 1, a.d = d, a.axes = 1, a.eps = 1.f;
+  const flashbob_status st = check_norm(a, in_dtype, 0);
+  if (st != FLASHBOB_OK) return st;
+  if (gradient) *gradient = norm_grad_workspace(a);
+  return FLASHBOB_OK;
+}
+
+flashbob_status flashbob_qk_norm_rope_grad(const void* QKV, const float* wq, const float* wk,
+                                           const float* freqs, const int* positions, float eps,
+                                           const void* dQ, const void* dK, const void* dV,
+                                           void* dQKV, float* dwq, float* dwk, void* workspace,
+                                           size_t workspace_bytes, int B, int N, int H, int Hkv,
+                                           int d, int R, int axes, int interleaved,
+                                           flashbob_dtype in_dtype, flashbob_dtype grad_dtype,
+                                           void* stream) {
+  NormArgs a{};
+  a.QKV = QKV, a.wq = wq, a.wk = wk, a.freqs = freqs, a.positions = positions, a.eps = eps;
+  a.Q = const_cast<void*>(dQ), a.K = const_cast<void*>(dK), a.V = const_cast<void*>(dV);
+  a.dQKV = dQKV, a.dwq = dwq, a.dwk = dwk, a.workspace = static_cast<float*>(workspace);
+  a.B = B, a.N = N, a.H = H, a.Hkv = Hkv, a.Nk = N, a.d = d, a.R = R, a.axes = axes;
+  a.interleaved = interleaved == 1, a.bf16 = in_dtype == FLASHBOB_BF16;
+  a.grad_bf16 = grad_dtype == FLASHBOB_BF16, a.stream = (cudaStream_t)stream;
+  flashbob_status st = check_dtype(grad_dtype);
+  if (st == FLASHBOB_OK) st = check_norm(a, in_dtype, interleaved);
+  if (st != FLASHBOB_OK) return st;
+  // The gains' gradients exist exactly where the gains do.
+  if (!dwq != !wq || !dwk != !wk) return FLASHBOB_ERR_INVALID_ARG;
+  const size_t e = a.bf16 ? 2 : 4, ge = a.grad_bf16 ? 2 : 4, tokens = (size_t)B * N;
+  const size_t all = tokens * (H + 2 * (size_t)Hkv) * d * e, need = norm_grad_workspace(a);
+  const Buf bufs[] = {{QKV, all, false},
+                      {wq, (size_t)d * 4, false, true},
+                      {wk, (size_t)d * 4, false, true},
+                      {freqs, (size_t)axes * (R / 2) * 4, false, true},
+                      {positions, axes * tokens * 4, false, true},
+                      {dQ, tokens * H * d * ge, false},
+                      {dK, tokens * Hkv * d * ge, false},
+                      {dV, tokens * Hkv * d * ge, false},
+                      {dQKV, all, true},
+                      {dwq, (size_t)d * 4, true, true},
+                      {dwk, (size_t)d * 4, true, true},
+                      {workspace, need, true, need == 0}};
+  st = check_buffers(bufs, 12);
+  if (st != FLASHBOB_OK) return st;
+  if (workspace_bytes < need) return FLASHBOB_ERR_INVALID_ARG;
+  return qk_norm_grad(a) == cudaSuccess ? FLASHBOB_OK : FLASHBOB_ERR_CUDA;
 }
 
 flashbob_status flashbob_check_wait_timeout(void* stream) {

@@ -52,6 +52,48 @@ struct JvpArgs {
   unsigned int* err;
 };
 
+// Attention with capped scores, a distance bias and key ranges, and its
+// gradient.  The G = H / Hkv query heads of a key/value head are one run of
+// G Nq "group rows" (contiguous in memory): row r is query r mod Nq of head
+// r / Nq of the group.
+struct AttnArgs {
+  const void *Q, *K, *V;
+  const int* ranges;    // [B, Nq, 2] or null
+  const int* q_pos;     // [B, Nq] or null
+  const float* slopes;  // [H] or null
+  float tau, cap;       // cap = 0: scores are not capped
+  void* O;              // in_dtype; the gradient reads it
+  float* L;
+  const void* dO;       // gradient only, like the next three
+  void *dQ, *dK, *dV;
+  void* workspace;
+  int B, H, Hkv;
+  int Nq, Nk, d;
+  bool causal;
+  bool bf16;
+  cudaStream_t stream;
+  unsigned int* err;
+};
+
+// Per-head norm and position rotation of the packed projection.
+struct NormArgs {
+  const void* QKV;           // [B, N, H + 2 Hkv, d]
+  const float *wq, *wk;      // [d] or both null
+  const float* freqs;        // [axes, R / 2]
+  const int* positions;      // [axes, B, N] or null
+  float eps;
+  void *Q, *K, *V;           // outputs; the gradients dQ, dK, dV in the backward call
+  const int* kv_start;       // [B] or null: first row of K and V for each batch entry
+  void* dQKV;                // backward only, like the next three
+  float *dwq, *dwk;
+  float* workspace;
+  int B, N, H, Hkv, Nk, d, R, axes;
+  bool interleaved;
+  bool bf16;                 // QKV, Q, K, V, dQKV
+  bool grad_bf16;            // dQ, dK, dV
+  cudaStream_t stream;
+};
+
 // Largest grid y and z extents: the kernels launch heads along y and
 // batches along z.
 constexpr int kMaxGridY = 65535;
@@ -102,6 +144,22 @@ cudaError_t tc_set_smem(const void* kernel, int bytes);
 // device: the largest S whose clusters of the split kernel all fit at once.
 cudaError_t tc_pass2_split(const void* split_kernel, size_t smem, int blocks, int tiles,
                            int* S);
+
+// Attention with key ranges (attn_simt.cu, attn_rows.cu).
+int attn_splits(const AttnArgs& a);            // runs of key tiles that one row block is cut into
+size_t attn_forward_workspace(const AttnArgs& a);
+size_t attn_grad_workspace(const AttnArgs& a);
+cudaError_t attn_join(const AttnArgs& a, int splits);  // partial results -> O, L
+cudaError_t attn_grad_rows(const AttnArgs& a);         // row state of the gradient -> workspace
+cudaError_t simt_attn(const AttnArgs& a);
+cudaError_t simt_attn_grad(const AttnArgs& a);
+cudaError_t attn_ranges(const int* doc_offsets, const int* prefix, const int* q_start, int* ranges,
+                        int* q_pos, int B, int M, int Nq, int Nk, bool causal,
+                        cudaStream_t stream);
+// Norm and rotation (qk_norm.cu).
+size_t norm_grad_workspace(const NormArgs& a);
+cudaError_t qk_norm(const NormArgs& a);
+cudaError_t qk_norm_grad(const NormArgs& a);
 
 // Device error word (one per device): a kernel writes a nonzero code when a
 // bounded wait gives up.  Codes: 1 = mbarrier wait timed out.

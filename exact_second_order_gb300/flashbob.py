@@ -32,6 +32,16 @@ _SIGNATURES = {
     "flashbob_bob_pass1": ([_P] * 10 + [_F] + [_P] * 4 + [_I] * 8 + [_P], _I),
     "flashbob_bob_pass2": ([_P] * 11 + [_F] + [_P] * 2 + [_I] * 8 + [_P], _I),
     "flashbob_attention_jvp": ([_P] * 8 + [_F] + [_P] * 2 + [_I] * 8 + [_P], _I),
+    "flashbob_attention_workspace": ([_I] * 7 + [ctypes.POINTER(ctypes.c_size_t)] * 2, _I),
+    "flashbob_attention": ([_P] * 6 + [_F, _F] + [_P] * 3 + [ctypes.c_size_t] + [_I] * 8 + [_P],
+                           _I),
+    "flashbob_attention_grad": ([_P] * 9 + [_F, _F] + [_P] * 4 + [ctypes.c_size_t] + [_I] * 8
+                                + [_P], _I),
+    "flashbob_attention_ranges": ([_P] * 5 + [_I] * 5 + [_P], _I),
+    "flashbob_qk_norm_rope": ([_P] * 6 + [_F] + [_P] * 3 + [_I] * 10 + [_P], _I),
+    "flashbob_qk_norm_rope_workspace": ([_I] * 6 + [ctypes.POINTER(ctypes.c_size_t)], _I),
+    "flashbob_qk_norm_rope_grad": ([_P] * 5 + [_F] + [_P] * 7 + [ctypes.c_size_t] + [_I] * 10
+                                   + [_P], _I),
     "flashbob_bob_launches": ([_I] * 7 + [ctypes.POINTER(_I)], _I),
     "flashbob_bob_tile_sizes": ([_I, _I] + [ctypes.POINTER(_I)] * 4
                                 + [ctypes.POINTER(ctypes.c_size_t)] * 2, _I),
@@ -223,6 +233,210 @@ def flashbob_attention_jvp(Q, K, V, O, L, UQ, UK, UV, tau: float, Od, Ld,
         raise FlashbobError(st, "flashbob_attention_jvp")
 
 
+def _check_tensor(where: str, name: str, t, shape, dtype, device) -> None:
+    """One tensor of a call: a contiguous CUDA tensor on ``device`` with the
+    shape and dtype of its role."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+        raise ValueError(f"{where}: {name} must be a CUDA tensor on {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{where}: {name} is {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous")
+
+
+def _check_attention(where: str, Q, K, inputs, L, slopes, ranges, q_pos):
+    """Checks of the attention calls with key ranges; ``inputs`` lists (name,
+    tensor, role) beside Q and K, all of Q's dtype.  Returns the sizes."""
+    import torch
+    for name, t in (("Q", Q), ("K", K)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{where}: {name} must be a 4-d tensor [B, heads, rows, d]")
+    B, H, Nq, d = Q.shape
+    Hkv, Nk = K.shape[1], K.shape[2]
+    dev, dt = Q.device, Q.dtype
+    shapes = {"q": (B, H, Nq, d), "k": (B, Hkv, Nk, d)}
+    for name, t, role in (("Q", Q, "q"), ("K", K, "k"), *inputs):
+        _check_tensor(where, name, t, shapes[role], dt, dev)
+    _check_tensor(where, "L", L, (B, H, Nq), torch.float32, dev)
+    if slopes is not None:
+        _check_tensor(where, "slopes", slopes, (H,), torch.float32, dev)
+    if ranges is not None:
+        _check_tensor(where, "ranges", ranges, (B, Nq, 2), torch.int32, dev)
+    if q_pos is not None:
+        _check_tensor(where, "q_pos", q_pos, (B, Nq), torch.int32, dev)
+    return B, H, Hkv, Nq, Nk, d
+
+
+def _bytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def flashbob_attention_workspace(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int,
+                                 in_dtype: int) -> tuple[int, int]:
+    """Workspace bytes of flashbob_attention and of flashbob_attention_grad."""
+    n = [ctypes.c_size_t() for _ in range(2)]
+    st = load_library().flashbob_attention_workspace(B, H, Hkv, Nq, Nk, d, in_dtype,
+                                                     *(ctypes.byref(x) for x in n))
+    if st != FLASHBOB_OK:
+        raise FlashbobError(st, "flashbob_attention_workspace")
+    return n[0].value, n[1].value
+
+
+def flashbob_attention(Q, K, V, ranges, q_pos, slopes, tau: float, cap: float, O, L, workspace,
+                       causal: bool = False, stream=None) -> None:
+    """O, L of attention with key ranges (see flashbob_attention in the header);
+    ``workspace`` is any contiguous CUDA tensor of enough bytes, or None."""
+    B, H, Hkv, Nq, Nk, d = _check_attention(
+        "flashbob_attention", Q, K, (("V", V, "k"), ("O", O, "q")), L, slopes, ranges, q_pos)
+    _check_workspace("flashbob_attention", workspace, Q.device)
+    with _device(Q):
+        st = load_library().flashbob_attention(
+            _ptr(Q), _ptr(K), _ptr(V), _ptr(ranges), _ptr(q_pos), _ptr(slopes), float(tau),
+            float(cap), _ptr(O), _ptr(L), _ptr(workspace), _bytes(workspace), B, H, Hkv, Nq, Nk,
+            d, int(causal), _dtype_code(Q), _stream_handle(stream))
+    if st != FLASHBOB_OK:
+        raise FlashbobError(st, "flashbob_attention")
+
+
+def flashbob_attention_grad(Q, K, V, O, L, dO, ranges, q_pos, slopes, tau: float, cap: float,
+                            dQ, dK, dV, workspace, causal: bool = False, stream=None) -> None:
+    """dQ, dK, dV of attention with key ranges (see flashbob_attention_grad)."""
+    B, H, Hkv, Nq, Nk, d = _check_attention(
+        "flashbob_attention_grad", Q, K,
+        (("V", V, "k"), ("O", O, "q"), ("dO", dO, "q"), ("dQ", dQ, "q"), ("dK", dK, "k"),
+         ("dV", dV, "k")), L, slopes, ranges, q_pos)
+    _check_workspace("flashbob_attention_grad", workspace, Q.device)
+    with _device(Q):
+        st = load_library().flashbob_attention_grad(
+            _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(L), _ptr(dO), _ptr(ranges), _ptr(q_pos),
+            _ptr(slopes), float(tau), float(cap), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(workspace),
+            _bytes(workspace), B, H, Hkv, Nq, Nk, d, int(causal), _dtype_code(Q),
+            _stream_handle(stream))
+    if st != FLASHBOB_OK:
+        raise FlashbobError(st, "flashbob_attention_grad")
+
+
+def _check_workspace(where: str, t, device) -> None:
+    import torch
+    if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == device
+                              and t.is_contiguous()):
+        raise ValueError(f"{where}: workspace must be a contiguous CUDA tensor on {device}")
+
+
+def flashbob_attention_ranges(doc_offsets, prefix, q_start, ranges, q_pos, Nk: int,
+                              causal: bool = False, stream=None) -> None:
+    """Key ranges of queries by document (see flashbob_attention_ranges)."""
+    import torch
+    where = "flashbob_attention_ranges"
+    if not isinstance(ranges, torch.Tensor) or ranges.dim() != 3:
+        raise ValueError(f"{where}: ranges must be a 3-d tensor [B, Nq, 2]")
+    B, Nq = ranges.shape[:2]
+    M = 0
+    if doc_offsets is not None:
+        if not isinstance(doc_offsets, torch.Tensor) or doc_offsets.dim() != 2:
+            raise ValueError(f"{where}: doc_offsets must be a 2-d tensor [B, M + 1]")
+        M = doc_offsets.shape[1] - 1
+    for name, t, shape in (("ranges", ranges, (B, Nq, 2)), ("q_pos", q_pos, (B, Nq)),
+                           ("doc_offsets", doc_offsets, (B, M + 1)), ("prefix", prefix, (B, M)),
+                           ("q_start", q_start, (B,))):
+        if t is not None:
+            _check_tensor(where, name, t, shape, torch.int32, ranges.device)
+    with _device(ranges):
+        st = load_library().flashbob_attention_ranges(
+            _ptr(doc_offsets), _ptr(prefix), _ptr(q_start), _ptr(ranges), _ptr(q_pos), B, M, Nq,
+            int(Nk), int(causal), _stream_handle(stream))
+    if st != FLASHBOB_OK:
+        raise FlashbobError(st, where)
+
+
+def _check_norm(where: str, QKV, H: int, Hkv: int, wq, wk, freqs, positions):
+    """Checks of the norm-and-rotation calls; returns B, N, d, R, axes."""
+    import torch
+    if not isinstance(QKV, torch.Tensor) or QKV.dim() != 4:
+        raise ValueError(f"{where}: QKV must be a 4-d tensor [B, N, H + 2 Hkv, d]")
+    B, N, _, d = QKV.shape
+    _check_tensor(where, "QKV", QKV, (B, N, H + 2 * Hkv, d), QKV.dtype, QKV.device)
+    R, axes = 0, 1
+    if freqs is not None:
+        if not isinstance(freqs, torch.Tensor) or freqs.dim() != 2:
+            raise ValueError(f"{where}: freqs must be a 2-d tensor [axes, R / 2]")
+        axes, R = freqs.shape[0], 2 * freqs.shape[1]
+        _check_tensor(where, "freqs", freqs, (axes, R // 2), torch.float32, QKV.device)
+    if positions is not None:
+        _check_tensor(where, "positions", positions, (axes, B, N), torch.int32, QKV.device)
+    for name, t in (("wq", wq), ("wk", wk)):
+        if t is not None:
+            _check_tensor(where, name, t, (d,), torch.float32, QKV.device)
+    return B, N, d, R, axes
+
+
+def flashbob_qk_norm_rope(QKV, wq, wk, freqs, positions, kv_start, eps: float, Q, K, V,
+                          interleaved: bool = False, stream=None) -> None:
+    """Head-major Q, K, V of the packed projection, normed and rotated (see
+    flashbob_qk_norm_rope in the header)."""
+    import torch
+    where = "flashbob_qk_norm_rope"
+    for name, t in (("Q", Q), ("K", K)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{where}: {name} must be a 4-d tensor [B, heads, rows, d]")
+    H, Hkv, Nk = Q.shape[1], K.shape[1], K.shape[2]
+    B, N, d, R, axes = _check_norm(where, QKV, H, Hkv, wq, wk, freqs, positions)
+    for name, t, shape in (("Q", Q, (B, H, N, d)), ("K", K, (B, Hkv, Nk, d)),
+                           ("V", V, (B, Hkv, Nk, d))):
+        _check_tensor(where, name, t, shape, QKV.dtype, QKV.device)
+    if kv_start is not None:
+        _check_tensor(where, "kv_start", kv_start, (B,), torch.int32, QKV.device)
+    with _device(QKV):
+        st = load_library().flashbob_qk_norm_rope(
+            _ptr(QKV), _ptr(wq), _ptr(wk), _ptr(freqs), _ptr(positions), _ptr(kv_start),
+            float(eps), _ptr(Q), _ptr(K), _ptr(V), B, N, H, Hkv, Nk, d, R, axes,
+            int(interleaved), _dtype_code(QKV), _stream_handle(stream))
+    if st != FLASHBOB_OK:
+        raise FlashbobError(st, where)
+
+
+def flashbob_qk_norm_rope_workspace(B: int, N: int, H: int, Hkv: int, d: int,
+                                    in_dtype: int) -> int:
+    """Workspace bytes of flashbob_qk_norm_rope_grad with gains."""
+    n = ctypes.c_size_t()
+    st = load_library().flashbob_qk_norm_rope_workspace(B, N, H, Hkv, d, in_dtype,
+                                                        ctypes.byref(n))
+    if st != FLASHBOB_OK:
+        raise FlashbobError(st, "flashbob_qk_norm_rope_workspace")
+    return n.value
+
+
+def flashbob_qk_norm_rope_grad(QKV, wq, wk, freqs, positions, eps: float, dQ, dK, dV, dQKV, dwq,
+                               dwk, workspace, interleaved: bool = False, stream=None) -> None:
+    """dQKV, dwq, dwk of flashbob_qk_norm_rope (see the header)."""
+    import torch
+    where = "flashbob_qk_norm_rope_grad"
+    for name, t in (("dQ", dQ), ("dK", dK)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{where}: {name} must be a 4-d tensor [B, heads, rows, d]")
+    H, Hkv = dQ.shape[1], dK.shape[1]
+    B, N, d, R, axes = _check_norm(where, QKV, H, Hkv, wq, wk, freqs, positions)
+    for name, t, shape in (("dQ", dQ, (B, H, N, d)), ("dK", dK, (B, Hkv, N, d)),
+                           ("dV", dV, (B, Hkv, N, d))):
+        _check_tensor(where, name, t, shape, dQ.dtype, QKV.device)
+    _check_tensor(where, "dQKV", dQKV, QKV.shape, QKV.dtype, QKV.device)
+    for name, t in (("dwq", dwq), ("dwk", dwk)):
+        if t is not None:
+            _check_tensor(where, name, t, (d,), torch.float32, QKV.device)
+    _check_workspace(where, workspace, QKV.device)
+    with _device(QKV):
+        st = load_library().flashbob_qk_norm_rope_grad(
+            _ptr(QKV), _ptr(wq), _ptr(wk), _ptr(freqs), _ptr(positions), float(eps), _ptr(dQ),
+            _ptr(dK), _ptr(dV), _ptr(dQKV), _ptr(dwq), _ptr(dwk), _ptr(workspace),
+            _bytes(workspace), B, N, H, Hkv, d, R, axes, int(interleaved), _dtype_code(QKV),
+            _dtype_code(dQ), _stream_handle(stream))
+    if st != FLASHBOB_OK:
+        raise FlashbobError(st, where)
+
+
 def flashbob_bob_launches(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int,
                           in_dtype: int) -> int:
     """Kernel launches of one flashbob_bob call with these sizes."""
@@ -322,3 +536,126 @@ def bob(Q, K, V, O, dO, L, D, UQ, UK, UV, tau: float, out: dict | None = None,
     flashbob_bob(Q, K, V, O, dO, L, D, UQ, UK, UV, tau, out["dQt"], out["dKt"], out["dVt"],
                  out["ddOt"], out["alpha"], out["E"], causal, stream)
     return out
+
+
+def _allocating_on(stream, device):
+    """Context in which torch allocates for ``stream``: what a wrapper
+    allocates and frees (a workspace) is then reused in that stream's order."""
+    import contextlib
+
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _workspace(nbytes: int, device):
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def attention(Q, K, V, tau: float, cap: float = 0.0, slopes=None, ranges=None, q_pos=None,
+              causal: bool = False, stream=None):
+    """O (of Q's dtype) and L of attention with capped scores, a distance bias
+    and key ranges; allocates them, and the workspace, on Q's device."""
+    import torch
+    _check_4d("attention", Q=Q, K=K)
+    B, H, Nq, d = Q.shape
+    with _device(Q), _allocating_on(stream, Q.device):
+        O = torch.empty_like(Q, memory_format=torch.contiguous_format)
+        L = torch.empty((B, H, Nq), dtype=torch.float32, device=Q.device)
+        need, _ = flashbob_attention_workspace(B, H, K.shape[1], Nq, K.shape[2], d,
+                                               _dtype_code(Q))
+        flashbob_attention(Q, K, V, ranges, q_pos, slopes, tau, cap, O, L,
+                           _workspace(need, Q.device), causal, stream)
+    return O, L
+
+
+def attention_grad(Q, K, V, O, L, dO, tau: float, cap: float = 0.0, slopes=None, ranges=None,
+                   q_pos=None, causal: bool = False, stream=None):
+    """dQ, dK, dV (of Q's dtype) of ``attention`` from its O and L and the
+    gradient dO; allocates them, and the workspace, on Q's device."""
+    import torch
+    _check_4d("attention_grad", Q=Q, K=K)
+    B, H, Nq, d = Q.shape
+    with _device(Q), _allocating_on(stream, Q.device):
+        dQ = torch.empty_like(Q, memory_format=torch.contiguous_format)
+        dK = torch.empty_like(K, memory_format=torch.contiguous_format)
+        dV = torch.empty_like(K, memory_format=torch.contiguous_format)
+        _, need = flashbob_attention_workspace(B, H, K.shape[1], Nq, K.shape[2], d,
+                                               _dtype_code(Q))
+        flashbob_attention_grad(Q, K, V, O, L, dO, ranges, q_pos, slopes, tau, cap, dQ, dK, dV,
+                                _workspace(need, Q.device), causal, stream)
+    return dQ, dK, dV
+
+
+def _check_4d(where: str, **tensors) -> None:
+    import torch
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
+            raise ValueError(f"{where}: {name} must be a 4-d CUDA tensor")
+
+
+def attention_ranges(B: int, Nq: int, Nk: int, doc_offsets=None, prefix=None, q_start=None,
+                     causal: bool = False, device=None, stream=None):
+    """ranges [B, Nq, 2] and q_pos [B, Nq] of queries by document, on the
+    device of the first array given (``device``, or the current one, if none)."""
+    import torch
+    for t in (doc_offsets, prefix, q_start):
+        if t is not None:
+            device = t.device
+            break
+    device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError(f"attention_ranges: the arrays must be on a CUDA device, not {device}")
+    with torch.cuda.device(device), _allocating_on(stream, device):
+        ranges = torch.empty((B, Nq, 2), dtype=torch.int32, device=device)
+        q_pos = torch.empty((B, Nq), dtype=torch.int32, device=device)
+        flashbob_attention_ranges(doc_offsets, prefix, q_start, ranges, q_pos, Nk, causal, stream)
+    return ranges, q_pos
+
+
+def qk_norm_rope(QKV, H: int, wq=None, wk=None, freqs=None, positions=None, eps: float = 1e-6,
+                 interleaved: bool = False, K=None, V=None, kv_start=None, stream=None):
+    """Q, K, V (head-major) of the packed projection QKV with H query heads:
+    the norm of queries and keys for each head and the rotation by position.
+    Allocates them on QKV's device; K and V may be given (a cache, whose rows
+    kv_start[b] + n are written)."""
+    import torch
+    _check_4d("qk_norm_rope", QKV=QKV)
+    B, N, heads, d = QKV.shape
+    if not 0 < H < heads or (heads - H) % 2:
+        raise ValueError(f"qk_norm_rope: {heads} heads are not {H} query heads and two equal "
+                         "groups of key and value heads")
+    if (K is None) != (V is None):
+        raise ValueError("qk_norm_rope: K and V are given together or not at all")
+    with _device(QKV), _allocating_on(stream, QKV.device):
+        Q = torch.empty((B, H, N, d), dtype=QKV.dtype, device=QKV.device)
+        if K is None:
+            if kv_start is not None:
+                raise ValueError("qk_norm_rope: kv_start needs K and V")
+            K, V = (torch.empty((B, (heads - H) // 2, N, d), dtype=QKV.dtype, device=QKV.device)
+                    for _ in range(2))
+        flashbob_qk_norm_rope(QKV, wq, wk, freqs, positions, kv_start, eps, Q, K, V, interleaved,
+                              stream)
+    return Q, K, V
+
+
+def qk_norm_rope_grad(QKV, dQ, dK, dV, wq=None, wk=None, freqs=None, positions=None,
+                      eps: float = 1e-6, interleaved: bool = False, stream=None):
+    """dQKV, dwq, dwk of ``qk_norm_rope`` from the gradients of Q, K and V
+    (fp32 or bf16); dwq and dwk are None without gains."""
+    import torch
+    _check_4d("qk_norm_rope_grad", QKV=QKV, dQ=dQ, dK=dK)
+    B, N, _, d = QKV.shape
+    with _device(QKV), _allocating_on(stream, QKV.device):
+        dQKV = torch.empty_like(QKV, memory_format=torch.contiguous_format)
+        dwq = None if wq is None else torch.empty_like(wq)
+        dwk = None if wk is None else torch.empty_like(wk)
+        need = 0 if wq is None else flashbob_qk_norm_rope_workspace(
+            B, N, dQ.shape[1], dK.shape[1], d, _dtype_code(QKV))
+        flashbob_qk_norm_rope_grad(QKV, wq, wk, freqs, positions, eps, dQ, dK, dV, dQKV, dwq, dwk,
+                                   _workspace(need, QKV.device), interleaved, stream)
+    return dQKV, dwq, dwk

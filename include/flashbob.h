@@ -174,6 +174,121 @@ flashbob_status flashbob_attention_jvp(const void* Q, const void* K, const void*
                                        int causal, flashbob_dtype in_dtype, void* stream);
 
 /*
+ * Attention with capped scores, a distance bias and key ranges, with its
+ * gradient; the key ranges of packed documents; and the step before it, the
+ * norm and rotation of queries and keys.  No counterpart on the pages: they
+ * are what a layer needs around the calls above.  The same conventions hold
+ * (layout, ownership, streams, errors, limits as flashbob_prep), but O and
+ * the gradients are of in_dtype here, each rounded once from fp32 sums; L is
+ * fp32.  No atomics: the same call gives the same bits.
+ *
+ * With z_ij = tau q_i . k_j of query i (head h) and key j,
+ *     c_ij = cap tanh(z_ij / cap)  (cap > 0; cap = 0: c = z),
+ *     s_ij = c_ij - slopes[h] |pos_i - j|,
+ *     query i sees key j if lo_i <= j < hi_i, and j <= pos_i when causal = 1;
+ *     L_i = log sum exp(s_ij) over the keys it sees, O_i = sum P_ij V_j.
+ * A query that sees no key gets O = 0, L = -inf and dQ = 0, and takes no
+ * part in any gradient.  What a key row holds that no query of the batch
+ * entry sees reaches nothing if it lies outside the run from the first to
+ * the last key that is seen there, and its dK and dV are 0: the rest of a
+ * cache, or padding, may hold anything (NaN too), and so may the Q, O and dO
+ * of a query that sees no key.  Key rows inside that run must be finite.
+ *   ranges: int32 [B,Nq,2], (lo, hi) of every query; NULL: (0, Nk).  Values
+ *        are clamped to 0 .. Nk; lo >= hi is an empty range.
+ *   q_pos: int32 [B,Nq], the position of every query; NULL: its index.
+ *   slopes: fp32 [H], finite; NULL: no bias.  A constant: it has no gradient.
+ *   cap: finite and >= 0.
+ *   Limits: as flashbob_prep; (H / Hkv) * Nq and Nk below 2^31 - 1024.
+ *
+ * flashbob_attention: O [B,H,Nq,d] of in_dtype, L [B,H,Nq] fp32.
+ *   workspace: `forward` bytes of flashbob_attention_workspace (may be NULL
+ *        when that is 0), needed when a call has few query rows and the keys
+ *        are cut into runs that are joined by a second launch; overwritten.
+ * flashbob_attention_grad: from O and L of flashbob_attention with the same
+ *   ranges, q_pos, slopes, tau, cap and causal, and the gradient dO
+ *   [B,H,Nq,d] of in_dtype: dQ [B,H,Nq,d], dK, dV [B,Hkv,Nk,d] of in_dtype
+ *   (shared heads summed).  Three launches: the row state (D and what each
+ *   row sees) into `gradient` bytes of workspace, dQ (row-resident), dK and
+ *   dV (column-resident).
+ * Calls on different streams, or in different graphs that may run at the
+ * same time, must not share a workspace.
+ */
+flashbob_status flashbob_attention_workspace(int B, int H, int Hkv, int Nq, int Nk, int d,
+                                             flashbob_dtype in_dtype, size_t* forward,
+                                             size_t* gradient);
+
+flashbob_status flashbob_attention(const void* Q, const void* K, const void* V, const int* ranges,
+                                   const int* q_pos, const float* slopes, float tau, float cap,
+                                   void* O, float* L, void* workspace, size_t workspace_bytes,
+                                   int B, int H, int Hkv, int Nq, int Nk, int d, int causal,
+                                   flashbob_dtype in_dtype, void* stream);
+
+flashbob_status flashbob_attention_grad(const void* Q, const void* K, const void* V, const void* O,
+                                        const float* L, const void* dO, const int* ranges,
+                                        const int* q_pos, const float* slopes, float tau,
+                                        float cap, void* dQ, void* dK, void* dV, void* workspace,
+                                        size_t workspace_bytes, int B, int H, int Hkv, int Nq,
+                                        int Nk, int d, int causal, flashbob_dtype in_dtype,
+                                        void* stream);
+
+/*
+ * flashbob_attention_ranges: the ranges and positions of queries by document.
+ * Query i of batch entry b is at position p = q_start[b] + i (q_start NULL:
+ * p = i).  Document m of b is the positions doc_offsets[b][m] <= p <
+ * doc_offsets[b][m + 1] (int32 [B,M+1], not decreasing; equal neighbours are
+ * an empty document); doc_offsets NULL (M = 0): one document, the Nk keys.
+ *     lo = the document's start,
+ *     hi = causal ? min(end, max(p + 1, lo + prefix[b][m])) : end,
+ * hi at most Nk, (0, 0) for a position in no document.  prefix (int32 [B,M],
+ * NULL: 0): so many of a document's first keys are seen by all of it.
+ *   out: ranges int32 [B,Nq,2]; q_pos int32 [B,Nq] (may be NULL).
+ */
+flashbob_status flashbob_attention_ranges(const int* doc_offsets, const int* prefix,
+                                          const int* q_start, int* ranges, int* q_pos, int B,
+                                          int M, int Nq, int Nk, int causal, void* stream);
+
+/*
+ * flashbob_qk_norm_rope: from the packed projection QKV [B,N,H+2Hkv,d]
+ * (H query, Hkv key, Hkv value heads) to head-major Q [B,H,N,d] and K, V
+ * [B,Hkv,Nk,d], all of in_dtype.  For every query and key head
+ *     y = x w / sqrt(mean(x^2) + eps)   (w: wq or wk, fp32 [d]; both NULL: 1),
+ * then the first R elements turn in pairs: pair k = elements (k, k + R/2), or
+ * (2k, 2k + 1) when interleaved = 1, by angle_k = sum_a positions[a][b][n]
+ * freqs[a][k].  positions: int32 [axes,B,N] (NULL: n; axes = 1 only); freqs:
+ * fp32 [axes,R/2] (may be NULL when R = 0).  Several axes (time, height,
+ * width): a pair that goes by one axis has frequency 0 on the others.  Angles
+ * are exact for any position; sums are fp32.  Values are copied.
+ *   kv_start: int32 [B] or NULL (0): token n of b goes to row kv_start[b] + n
+ *        of K and V (a cache); a row outside 0 .. Nk - 1 is dropped and no
+ *        other row is touched.  NULL needs Nk >= N.
+ *   eps: finite and > 0.  Limits: d <= 128, 0 <= R <= d even, axes <= 4,
+ *        H, Hkv <= 65535, B * N < 2^31.  One launch.
+ * flashbob_qk_norm_rope_grad: from QKV and the gradients dQ [B,H,N,d], dK, dV
+ * [B,Hkv,N,d] (Nk = N, no kv_start) of grad_dtype: dQKV of in_dtype and, where
+ * gains are given, dwq, dwk fp32 [d] (else both NULL).  fp32 gradients are
+ * those of flashbob_bob, bf16 those of flashbob_attention_grad.
+ *   workspace: `gradient` bytes of flashbob_qk_norm_rope_workspace (may be
+ *        NULL without gains).  Two launches (one without gains).
+ */
+flashbob_status flashbob_qk_norm_rope(const void* QKV, const float* wq, const float* wk,
+                                      const float* freqs, const int* positions,
+                                      const int* kv_start, float eps, void* Q, void* K, void* V,
+                                      int B, int N, int H, int Hkv, int Nk, int d, int R, int axes,
+                                      int interleaved, flashbob_dtype in_dtype, void* stream);
+
+flashbob_status flashbob_qk_norm_rope_workspace(int B, int N, int H, int Hkv, int d,
+                                                flashbob_dtype in_dtype, size_t* gradient);
+
+flashbob_status flashbob_qk_norm_rope_grad(const void* QKV, const float* wq, const float* wk,
+                                           const float* freqs, const int* positions, float eps,
+                                           const void* dQ, const void* dK, const void* dV,
+                                           void* dQKV, float* dwq, float* dwk, void* workspace,
+                                           size_t workspace_bytes, int B, int N, int H, int Hkv,
+                                           int d, int R, int axes, int interleaved,
+                                           flashbob_dtype in_dtype, flashbob_dtype grad_dtype,
+                                           void* stream);
+
+/*
  * flashbob_bob_launches: how many kernel launches one flashbob_bob call with
  * these sizes makes on the current device: pass 1 and pass 2, where pass 1
  * of the tensor-core path at d = 128 is two launches (the JVP with alpha,
