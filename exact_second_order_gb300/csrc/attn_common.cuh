@@ -47,14 +47,14 @@ __device__ __forceinline__ int warp_max(int v) { return __reduce_max_sync(0xffff
 // Row state that the gradient kernels read, one entry for each group row,
 // rows padded to a multiple of kRowPad per (batch, key/value head):
 //   info  {lo, hi, pos, slope log2 e (as bits)},
-//   ld    {L log2 e, D}; +inf in place of L for rows that see nothing and for
-//         the padding, so that P = exp2(s - L) is 0 there,
+//   l2, dd  L log2 e and D; +inf in place of L for rows that see nothing and
+//         for the padding, so that P = exp2(s - L) is 0 there,
 // and for each kBoundRows rows {min lo, max hi, max lo, min hi}: the hull of
 // their ranges and their intersection (the padding takes no part).
 struct GradRows {
   int4* bounds;
   int4* info;
-  float2* ld;
+  float *l2, *dd;
   int pitch;  // padded rows per (batch, key/value head)
 };
 
@@ -68,7 +68,8 @@ __host__ __device__ inline GradRows grad_rows(void* workspace, int groups, int r
   const size_t n = static_cast<size_t>(groups) * g.pitch;
   g.bounds = static_cast<int4*>(workspace);
   g.info = g.bounds + n / kBoundRows;
-  g.ld = reinterpret_cast<float2*>(g.info + n);
+  g.l2 = reinterpret_cast<float*>(g.info + n);
+  g.dd = g.l2 + n;
   return g;
 }
 

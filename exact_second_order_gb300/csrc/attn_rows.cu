@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(256)
       const size_t at = static_cast<size_t>(g) * out.pitch + r;
       const float slope = slopes && live ? slopes[blockIdx.y * G + r / Nq] * kLog2e : 0.f;
       out.info[at] = make_int4(v.lo, v.hi, v.pos, __float_as_int(slope));
-      out.ld[at] = v.hi > 0 ? make_float2(l * kLog2e, dot) : make_float2(INFINITY, 0.f);
+      out.l2[at] = v.hi > 0 ? l * kLog2e : INFINITY;
+      out.dd[at] = v.hi > 0 ? dot : 0.f;
     }
   }
   b_lo = warp_min(b_lo);
@@ -234,13 +235,13 @@ size_t attn_forward_workspace(const AttnArgs& a) {
 size_t attn_grad_workspace(const AttnArgs& a) {
   const int rows = a.H / a.Hkv * a.Nq, groups = a.B * a.Hkv;
   const GradRows g = grad_rows(nullptr, groups, rows);
-  return reinterpret_cast<size_t>(g.ld) +
-         static_cast<size_t>(groups) * g.pitch * sizeof(float2);
+  return reinterpret_cast<size_t>(g.dd) + static_cast<size_t>(groups) * g.pitch * sizeof(float);
 }
 
 // A grid that leaves SMs idle is cut along the keys, so that the tiles of one
 // row block run side by side and are joined afterwards.
 int attn_splits(const AttnArgs& a) {
+  if (tc_attn_supported(a)) return tc_attn_splits(a);
   const long long blocks = static_cast<long long>(a.B) * a.Hkv *
                            ((static_cast<long long>(a.H / a.Hkv) * a.Nq + 63) / 64);
   const int tiles = (a.Nk + 63) / 64;

@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(NT) attn_dq_kernel(const __grid_constant__ Att
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // The workspace is padded, so rows beyond the last have an entry too.
-    ld[i] = gr.ld[static_cast<size_t>(g) * gr.pitch + row0 + ty + 16 * i];
+    const size_t at = static_cast<size_t>(g) * gr.pitch + row0 + ty + 16 * i;
+    ld[i] = make_float2(gr.l2[at], gr.dd[at]);
 #pragma unroll
     for (int c = 0; c < DP / 16; ++c) acc[i][c] = 0.f;
   }
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(NT) attn_dkv_kernel(const __grid_constant__ At
     if (threadIdx.x < BT) {
       const size_t at = static_cast<size_t>(g) * gr.pitch + t * BT + threadIdx.x;
       info[threadIdx.x] = gr.info[at];
-      lds[threadIdx.x] = gr.ld[at];
+      lds[threadIdx.x] = make_float2(gr.l2[at], gr.dd[at]);
     }
     load_tile<T, DP>(Qs, Q, t * BT, 0, rows, a.d);
     load_tile<T, DP>(dOs, dO, t * BT, 0, rows, a.d);
@@ -472,9 +473,8 @@ cudaError_t run(const AttnArgs& a, bool grad) {
     e = cudaGetLastError();
     return e == cudaSuccess && splits > 1 ? attn_join(a, splits) : e;
   }
-  cudaError_t e = attn_grad_rows(a);
-  if (e == cudaSuccess)
-    e = launch(attn_dq_kernel<T, DP>, 4 * tile + square, dim3(blocks, a.Hkv, a.B), a.stream, a);
+  cudaError_t e =
+      launch(attn_dq_kernel<T, DP>, 4 * tile + square, dim3(blocks, a.Hkv, a.B), a.stream, a);
   if (e == cudaSuccess)
     e = launch(attn_dkv_kernel<T, DP>, 4 * tile + 2 * square,
                dim3((a.Nk + BT - 1) / BT, a.Hkv, a.B), a.stream, a);

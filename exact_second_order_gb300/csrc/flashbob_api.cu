@@ -416,7 +416,8 @@ flashbob_status flashbob_attention(const void* Q, const void* K, const void* V, 
   if (st != FLASHBOB_OK) return st;
   if (workspace_bytes < need) return FLASHBOB_ERR_INVALID_ARG;
   if (error_word_ptr(&a.err) != cudaSuccess) return FLASHBOB_ERR_CUDA;
-  return simt_attn(a) == cudaSuccess ? FLASHBOB_OK : FLASHBOB_ERR_CUDA;
+  const cudaError_t ce = tc_attn_supported(a) ? tc_attn(a) : simt_attn(a);
+  return ce == cudaSuccess ? FLASHBOB_OK : FLASHBOB_ERR_CUDA;
 }
 
 flashbob_status flashbob_attention_grad(const void* Q, const void* K, const void* V, const void* O,
@@ -453,7 +454,12 @@ flashbob_status flashbob_attention_grad(const void* Q, const void* K, const void
   if (st != FLASHBOB_OK) return st;
   if (workspace_bytes < need) return FLASHBOB_ERR_INVALID_ARG;
   if (error_word_ptr(&a.err) != cudaSuccess) return FLASHBOB_ERR_CUDA;
-  return simt_attn_grad(a) == cudaSuccess ? FLASHBOB_OK : FLASHBOB_ERR_CUDA;
+  cudaError_t ce = attn_grad_rows(a);
+  if (ce == cudaSuccess) {
+    if (!tc_attn_supported(a)) ce = simt_attn_grad(a);
+    else if ((ce = tc_attn_dq(a)) == cudaSuccess) ce = tc_attn_dkv(a);
+  }
+  return ce == cudaSuccess ? FLASHBOB_OK : FLASHBOB_ERR_CUDA;
 }
 
 flashbob_status flashbob_attention_ranges(const int* doc_offsets, const int* prefix,

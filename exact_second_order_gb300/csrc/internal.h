@@ -151,8 +151,13 @@ size_t attn_forward_workspace(const AttnArgs& a);
 size_t attn_grad_workspace(const AttnArgs& a);
 cudaError_t attn_join(const AttnArgs& a, int splits);  // partial results -> O, L
 cudaError_t attn_grad_rows(const AttnArgs& a);         // row state of the gradient -> workspace
+bool tc_attn_supported(const AttnArgs& a);  // bf16, d = 64 or 128
+int tc_attn_splits(const AttnArgs& a);
+cudaError_t tc_attn(const AttnArgs& a);
+cudaError_t tc_attn_dq(const AttnArgs& a);
+cudaError_t tc_attn_dkv(const AttnArgs& a);
 cudaError_t simt_attn(const AttnArgs& a);
-cudaError_t simt_attn_grad(const AttnArgs& a);
+cudaError_t simt_attn_grad(const AttnArgs& a);  // dQ, dK, dV after attn_grad_rows
 cudaError_t attn_ranges(const int* doc_offsets, const int* prefix, const int* q_start, int* ranges,
                         int* q_pos, int B, int M, int Nq, int Nk, bool causal,
                         cudaStream_t stream);

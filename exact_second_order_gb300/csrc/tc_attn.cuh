@@ -1,0 +1,164 @@
+// Shared by the tensor-core kernels of attention with key ranges (bf16,
+// d = 64 and 128): block numbering, what the 128 rows of a block see, and the
+// score of a raw product in log2 units.
+#pragma once
+
+#include "attn_common.cuh"
+#include "tc_common.cuh"
+
+namespace flashbob {
+namespace attn {
+
+// rcp.approx (1 ulp) of a value in [1, inf]: 1 / inf is 0.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// `bytes` (a multiple of 16) from global to shared memory, both 16-byte
+// aligned, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          tc::smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+
+// Row blocks are launched heads fastest and from the last rows of a head to
+// the first, so that under a causal mask the long blocks start first and the
+// short ones fill the end.  A rank is the r-th block of `blocks` row blocks
+// of one group; the blocks of its G heads interleave when they do not
+// straddle heads.
+__device__ __forceinline__ int row_block(int rank, int blocks, int G, int Nq, int rows_per_block) {
+  if (G > 1 && Nq % rows_per_block == 0) {
+    const int per = Nq / rows_per_block;
+    return (rank % G) * per + per - 1 - rank / G;
+  }
+  return blocks - 1 - rank;
+}
+
+// The view of one group row r (r >= rows: sees nothing) and its slope.
+struct GroupRow {
+  RowView v;
+  float slope2;  // slope log2 e
+};
+
+__device__ __forceinline__ GroupRow group_row(const AttnArgs& a, int b, int hkv, int r, int rows) {
+  GroupRow g{empty_view(), 0.f};
+  if (r < rows) {
+    const int h = r / a.Nq, i = r - h * a.Nq;
+    g.v = row_view(a.ranges, a.q_pos, static_cast<size_t>(b) * a.Nq, i, a.Nk, a.causal);
+    if (a.slopes) g.slope2 = a.slopes[hkv * (a.H / a.Hkv) + h] * kLog2e;
+  }
+  return g;
+}
+
+// Hull [lo, hi) and intersection [in_lo, in_hi) of the ranges of 128 rows
+// (in_lo is INT_MAX when a row sees nothing, unless it lies beyond the last).
+struct Hull {
+  int lo, hi, in_lo, in_hi;
+};
+
+__device__ __forceinline__ void warp_hull(const RowView& v, bool live, int lane, int* out4) {
+  const int lo = warp_min(v.lo), hi = warp_max(v.hi);
+  const int in_lo = warp_max(live ? v.lo : 0), in_hi = warp_min(live ? v.hi : INT_MAX);
+  if (lane == 0) {
+    out4[0] = lo;
+    out4[1] = hi;
+    out4[2] = in_lo;
+    out4[3] = in_hi;
+  }
+}
+
+__device__ __forceinline__ Hull join_hulls(const int (*h)[4], int n) {
+  Hull r{INT_MAX, 0, 0, INT_MAX};
+  for (int i = 0; i < n; ++i) {
+    r.lo = min(r.lo, h[i][0]);
+    r.hi = max(r.hi, h[i][1]);
+    r.in_lo = max(r.in_lo, h[i][2]);
+    r.in_hi = min(r.in_hi, h[i][3]);
+  }
+  return r;
+}
+
+// Scores of raw products in log2 units:
+//   not capped: raw c1;   capped: c2 tanh(raw tau / cap) with tanh x =
+//   1 - 2 / (1 + e^{2 x}), two MUFU operations, absolute error a few 2^-24
+//   (tanh.approx would leave 2^-11, which exp turns into percents of P);
+//   biased: minus slope2 |j - pos|.
+template <bool CAP, bool BIAS>
+struct Score {
+  float c1;      // tau log2 e; capped: 2 tau log2 e / cap
+  float c2;      // cap log2 e
+  float slope2;
+
+  __device__ __forceinline__ Score(const AttnArgs& a, float slope) {
+    c1 = CAP ? 2.f * a.tau / a.cap * kLog2e : a.tau * kLog2e;
+    c2 = a.cap * kLog2e;
+    slope2 = slope;
+  }
+  // r with tanh = 1 - 2 r and 1 - tanh^2 = 4 r (1 - r).
+  __device__ __forceinline__ float half_gap(float raw) const {
+    return rcp_approx(1.f + tc::ex2_approx(raw * c1));
+  }
+  // raw (not capped) or r (capped) plus the bias at j - pos = dist; minus m.
+  __device__ __forceinline__ float2 from(float2 x, float dist, float m, float slope) const {
+    const float2 nm = make_float2(-m, -m);
+    float2 s = CAP ? tc::ffma2(x, make_float2(-2.f * c2, -2.f * c2), make_float2(c2 - m, c2 - m))
+                   : tc::ffma2(x, make_float2(c1, c1), nm);
+    if (BIAS) {
+      s.x = fmaf(-slope, fabsf(dist), s.x);
+      s.y = fmaf(-slope, fabsf(dist + 1.f), s.y);
+    }
+    return s;
+  }
+};
+
+// 128 x DH accumulator columns of TMEM lane r (two warpgroups take half the
+// columns each), times `scale`, as bf16 rows in shared memory (pitch DH + 8:
+// 16-byte accesses of 8 consecutive rows fall on all 32 banks), then to
+// `rows` consecutive global rows with coalesced 16-byte stores.  `zero`: the
+// accumulator was never written.  256 elementwise threads, named barrier 1.
+template <int DH>
+__device__ __forceinline__ void store_block(uint32_t acc, float scale, bool zero, uint8_t* stage,
+                                            int wg, int r, int tid, int rows, bool ok,
+                                            __nv_bfloat16* __restrict__ out) {
+  constexpr int kPitch = DH * 2 + 16;
+#pragma unroll
+  for (int c = 0; c < DH / 2; c += 16) {
+    const int col = DH / 2 * wg + c;
+    uint32_t v[16], w[8];
+    tc::tmem_ld16(acc + col, v);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      w[k] = zero ? 0u : tc::pack_bf16x2(scale * tc::u2f(v[2 * k]), scale * tc::u2f(v[2 * k + 1]));
+    uint4* d = reinterpret_cast<uint4*>(stage + r * kPitch + col * 2);
+    d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+  tc::named_bar_sync(1, 256);
+  if (ok) {
+    constexpr int kChunks = DH / 8;
+    for (int f = tid; f < rows * kChunks; f += 256)
+      reinterpret_cast<uint4*>(out)[f] =
+          *reinterpret_cast<const uint4*>(stage + (f / kChunks) * kPitch + (f % kChunks) * 16);
+  }
+}
+
+// Zeroes row r (128 bytes in each 64-column half) of a tile in shared memory.
+template <int NH, uint32_t HALF>
+__device__ __forceinline__ void zero_row(uint8_t (*tile)[HALF], int r) {
+#pragma unroll
+  for (int h = 0; h < NH; ++h) {
+    uint4* v = reinterpret_cast<uint4*>(tile[h] + r * 128);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+}  // namespace attn
+}  // namespace flashbob

@@ -1,0 +1,464 @@
+// dK and dV of attention with key ranges on sm_103a tensor cores: bf16, head
+// dim 64 or 128.  128 keys (K, V) stay on chip; the tiles of 128 group rows
+// that see any of them stream past, all heads that share the keys in one run,
+// so that the sums over rows and heads stay on chip:
+//   S^T = K Q^T, dP^T = V dO^T;  P = exp2(score(S) - L log2 e),
+//   dS = P (dP - D) (1 - tanh^2),  dV += P^T dO,  dK += dS^T Q (times tau).
+//
+// 320 threads: warp 0 finds the tiles (the bounds of 32 at a time against the
+// block's keys) and loads them with their row state; warp 1 allocates TMEM
+// and issues the MMAs; warps 2-5 / 6-9 are elementwise warpgroups that take
+// rows 0-63 / 64-127 of every tile, one key per thread.  How many tiles there
+// are is known only to warp 0: each ring slot says which tile it holds, and a
+// last slot says that there are no more.
+// TMEM at d = 64: S^T, dP^T (128 columns each), operands P^T and dS^T (64
+// each), dK, dV (64 each): the scores are handed back when they are in
+// registers, and those of tile n + 1 run beside the arithmetic of tile n.
+// At d = 128 dK and dV take 256 columns and the operands lie on the scores
+// they came from; the pipe runs dV(n), S(n + 1), dK(n), dP(n + 1), so that
+// P(n + 1) is formed beside dK(n) and dP(n + 1), and dS beside dV and S.
+#include "tc_attn.cuh"
+
+namespace flashbob {
+namespace {
+using namespace tc;
+using namespace attn;
+
+constexpr int BM = kTcRows, BQ = 128;
+constexpr int NTHREADS = 320;
+constexpr uint32_t HALF = BM * 64 * 2;  // 128 rows x 64 columns
+constexpr uint32_t kS = 0, kP = 128;
+
+template <int DH>
+struct Cols {
+  static constexpr bool kInPlace = DH == 128;
+  static constexpr uint32_t dK = kInPlace ? 256 : 384, dV = dK + DH;
+  // Operand K step kk (16 rows): its own area, or on the scores of the
+  // warpgroup that wrote it.
+  static __device__ __forceinline__ uint32_t p(int kk) {
+    return kInPlace ? kS + 64 * (kk >> 2) + 8 * (kk & 3) : 256 + 8 * kk;
+  }
+  static __device__ __forceinline__ uint32_t ds(int kk) {
+    return kInPlace ? kP + 64 * (kk >> 2) + 8 * (kk & 3) : 320 + 8 * kk;
+  }
+  static_assert(dV + DH <= 512, "TMEM columns");
+};
+
+struct Slot {
+  int tile;          // -1: no more
+  int in_lo, in_hi;  // intersection of the rows' ranges (in_lo INT_MAX: a row sees nothing)
+};
+
+template <int DH>
+struct SmemK {
+  static constexpr int NH = DH / 64;
+  static constexpr int NST = DH == 64 ? 5 : 2;
+  alignas(1024) uint8_t k[NH][HALF];
+  alignas(1024) uint8_t v[NH][HALF];
+  alignas(1024) uint8_t q[NST][NH][HALF];
+  alignas(1024) uint8_t go[NST][NH][HALF];  // dO
+  alignas(16) float l2[NST][BQ];
+  alignas(16) float dd[NST][BQ];
+  alignas(16) int4 info[NST][BQ];
+  Slot slot[NST];
+  uint64_t bar_kv;
+  uint64_t q_full[NST], q_empty[NST];  // Q, the row state and the slot
+  uint64_t o_full[NST], o_empty[NST];  // dO
+  uint64_t s_full, s_free;
+  uint64_t p_full, p_free;
+  uint64_t w_ready, w_free;   // P^T written (8 warps) / read by dV
+  uint64_t ds_ready, ds_free;  // dS^T written (8 warps) / read by dK
+  uint64_t out_full;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+template <int DH, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    tc_dkv_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mdO,
+                  const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
+                  const __grid_constant__ AttnArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  using Smem = SmemK<DH>;
+  using C = Cols<DH>;
+  constexpr int NH = Smem::NH, NST = Smem::NST;
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                      ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int heads = a.B * a.Hkv, rows = a.H / a.Hkv * a.Nq;
+  const int g = blockIdx.x % heads, j0 = static_cast<int>(blockIdx.x / heads) * BM;
+  volatile int* abort_flag = &sm.abort_flag;
+  unsigned int* err = a.err;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.bar_kv, 1);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&sm.q_full[s], 1);
+      mbar_init(&sm.q_empty[s], 1);
+      mbar_init(&sm.o_full[s], 1);
+      mbar_init(&sm.o_empty[s], 1);
+    }
+    mbar_init(&sm.s_full, 1);
+    mbar_init(&sm.p_full, 1);
+    mbar_init(&sm.w_free, 1);
+    mbar_init(&sm.ds_free, 1);
+    mbar_init(&sm.out_full, 1);
+    mbar_init(&sm.s_free, 8);
+    mbar_init(&sm.p_free, 8);
+    mbar_init(&sm.w_ready, 8);
+    mbar_init(&sm.ds_ready, 8);
+    sm.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = sm.tmem_base;
+
+  if (warp == 0) {
+    const GradRows st = grad_rows(a.workspace, heads, rows);
+    const size_t base = static_cast<size_t>(g) * st.pitch;
+    const int4* bounds = st.bounds + base / kBoundRows;
+    const int tiles = st.pitch / BQ;
+    if (lane == 0) {
+      tma_prefetch_desc(&mQ);
+      tma_prefetch_desc(&mdO);
+      mbar_expect_tx(&sm.bar_kv, 2 * NH * HALF);
+      for (int h = 0; h < NH; ++h) {
+        tma_load_3d(sm.k[h], &mK, &sm.bar_kv, 64 * h, j0, g);
+        tma_load_3d(sm.v[h], &mV, &sm.bar_kv, 64 * h, j0, g);
+      }
+    }
+    int nq = 0, no = 0;  // Q and dO loads issued
+    bool ok = true;
+    for (int t0 = 0; ok && t0 < tiles; t0 += 32) {
+      int4 b = make_int4(INT_MAX, 0, 0, INT_MAX);
+      if (t0 + lane < tiles) {
+        const int4 x = bounds[2 * (t0 + lane)], y = bounds[2 * (t0 + lane) + 1];
+        b = make_int4(min(x.x, y.x), max(x.y, y.y), max(x.z, y.z), min(x.w, y.w));
+      }
+      unsigned hits = __ballot_sync(0xffffffffu, b.x < j0 + BM && b.y > j0);
+      for (; ok && hits; hits &= hits - 1) {
+        const int k = __ffs(hits) - 1, tile = t0 + k, s = nq % NST;
+        const int in_lo = __shfl_sync(0xffffffffu, b.z, k);
+        const int in_hi = __shfl_sync(0xffffffffu, b.w, k);
+        if (nq >= NST) ok = mbar_wait_warp(&sm.q_empty[s], ((nq / NST) - 1) & 1, abort_flag, err);
+        if (!ok) break;
+        if (lane == 0) {
+          sm.slot[s] = Slot{tile, in_lo, in_hi};
+          mbar_expect_tx(&sm.q_full[s], NH * HALF + BQ * 24);
+          for (int h = 0; h < NH; ++h)
+            tma_load_3d(sm.q[s][h], &mQ, &sm.q_full[s], 64 * h, tile * BQ, g);
+          const size_t at = base + static_cast<size_t>(tile) * BQ;
+          bulk_load(sm.l2[s], st.l2 + at, BQ * 4, &sm.q_full[s]);
+          bulk_load(sm.dd[s], st.dd + at, BQ * 4, &sm.q_full[s]);
+          bulk_load(sm.info[s], st.info + at, BQ * 16, &sm.q_full[s]);
+        }
+        ++nq;
+        if (no >= NST) ok = mbar_wait_warp(&sm.o_empty[s], ((no / NST) - 1) & 1, abort_flag, err);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_expect_tx(&sm.o_full[s], NH * HALF);
+          for (int h = 0; h < NH; ++h)
+            tma_load_3d(sm.go[s][h], &mdO, &sm.o_full[s], 64 * h, tile * BQ, g);
+        }
+        ++no;
+      }
+    }
+    if (lane == 0) {
+      // No copy may still be in flight when the block exits; then the slot
+      // that ends the run (waited for before, so no phase is reused).
+      drain_wait(&sm.bar_kv, 0);
+      for (int n = nq > NST ? nq - NST : 0; n < nq; ++n)
+        drain_wait(&sm.q_full[n % NST], (n / NST) & 1);
+      for (int n = no > NST ? no - NST : 0; n < no; ++n)
+        drain_wait(&sm.o_full[n % NST], (n / NST) & 1);
+      const int s = nq % NST;
+      if (ok && (nq < NST || mbar_wait(&sm.q_empty[s], ((nq / NST) - 1) & 1, abort_flag, err))) {
+        sm.slot[s].tile = -1;
+        mbar_arrive(&sm.q_full[s]);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    constexpr uint32_t idS = idesc_bf16(BM, BQ, false);
+    constexpr uint32_t idO = idesc_bf16(BM, DH, true);
+    const uint64_t dK = smem_desc_sw128(smem_u32(sm.k[0]), 16, 1024);
+    const uint64_t dV = smem_desc_sw128(smem_u32(sm.v[0]), 16, 1024);
+    const uint64_t dQ = smem_desc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
+    const uint64_t dG = smem_desc_sw128(smem_u32(sm.go[0][0]), 16, 1024);
+    const uint64_t dQm = smem_desc_sw128(smem_u32(sm.q[0][0]), HALF, 1024);  // MN-major
+    const uint64_t dGm = smem_desc_sw128(smem_u32(sm.go[0][0]), HALF, 1024);
+    constexpr uint64_t kTile = (uint64_t)(NH * HALF) >> 4;
+    auto scores = [&](uint32_t col, uint64_t da, uint64_t db) {
+#pragma unroll
+      for (int kk = 0; kk < DH / 16; ++kk) {
+        const uint64_t o = ((kk >> 2) * HALF + 32 * (kk & 3)) >> 4;
+        mma_ss(tbase + col, da + o, db + o, idS, kk > 0);
+      }
+    };
+    if (elect_one()) {
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool got = mbar_wait(bar, parity, abort_flag, err);
+        tc_fence_after();
+        return got;
+      };
+      auto issue_s = [&](int n) {
+        scores(kS, dK, dQ + (n % NST) * kTile);
+        mma_commit(&sm.s_full);
+      };
+      auto issue_p = [&](int n) {  // also waits for dO
+        if (!wait(&sm.o_full[n % NST], (n / NST) & 1)) return false;
+        scores(kP, dV, dG + (n % NST) * kTile);
+        mma_commit(&sm.p_full);
+        return true;
+      };
+      auto issue_dv = [&](int n) {
+        const uint64_t b = dGm + (n % NST) * kTile;
+#pragma unroll
+        for (int c = 0; c < BQ / 16; ++c)
+          mma_ts(tbase + C::dV, tbase + C::p(c), b + ((16 * 128 * c) >> 4), idO, n > 0 || c > 0);
+        mma_commit(&sm.w_free);
+        mma_commit(&sm.o_empty[n % NST]);
+      };
+      auto issue_dk = [&](int n) {
+        const uint64_t b = dQm + (n % NST) * kTile;
+#pragma unroll
+        for (int c = 0; c < BQ / 16; ++c)
+          mma_ts(tbase + C::dK, tbase + C::ds(c), b + ((16 * 128 * c) >> 4), idO, n > 0 || c > 0);
+        mma_commit(&sm.ds_free);
+        mma_commit(&sm.q_empty[n % NST]);
+      };
+      bool ok = wait(&sm.bar_kv, 0) && wait(&sm.q_full[0], 0);
+      bool more = ok && sm.slot[0].tile >= 0;
+      if (more) {
+        issue_s(0);
+        ok = issue_p(0);
+      }
+      for (int n = 0; ok && more; ++n) {
+        const int s1 = (n + 1) % NST;
+        const uint32_t f1 = ((n + 1) / NST) & 1;
+        if (C::kInPlace) {
+          ok = wait(&sm.w_ready, n & 1);
+          if (!ok) break;
+          issue_dv(n);
+          ok = wait(&sm.q_full[s1], f1);
+          if (!ok) break;
+          more = sm.slot[s1].tile >= 0;
+          if (more) issue_s(n + 1);  // after dV(n) has read P on S's columns
+          ok = wait(&sm.ds_ready, n & 1);
+          if (!ok) break;
+          issue_dk(n);
+          if (more) ok = issue_p(n + 1);
+        } else {
+          ok = wait(&sm.q_full[s1], f1);
+          if (!ok) break;
+          more = sm.slot[s1].tile >= 0;
+          if (more) {
+            ok = wait(&sm.s_free, n & 1);
+            if (!ok) break;
+            issue_s(n + 1);
+            ok = wait(&sm.p_free, n & 1) && issue_p(n + 1);
+            if (!ok) break;
+          }
+          ok = wait(&sm.w_ready, n & 1);
+          if (!ok) break;
+          issue_dv(n);
+          ok = wait(&sm.ds_ready, n & 1);
+          if (!ok) break;
+          issue_dk(n);
+        }
+      }
+      mma_commit(&sm.out_full);
+    }
+    __syncwarp();
+  } else {
+    const int wg = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const int key = j0 + r, c0 = 64 * wg;
+    const int key_end = min(j0 + BM, a.Nk);
+    const Score<CAP, BIAS> score(a, 0.f);
+    bool ok = true;
+    int n = 0;
+    for (;; ++n) {
+      const int st = n % NST;
+      ok = mbar_wait_warp(&sm.q_full[st], (n / NST) & 1, abort_flag, err);
+      if (!ok) break;
+      const Slot slot = sm.slot[st];
+      if (slot.tile < 0) break;
+      const bool masked = slot.in_lo > j0 || slot.in_hi < key_end;
+      ok = mbar_wait_warp(&sm.s_full, n & 1, abort_flag, err);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[4][16], pk[4][8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld16(tbase + lane_off + kS + c0 + 16 * q, s[q]);
+      tmem_wait_ld();
+      if (!C::kInPlace) {
+        tc_fence_before();
+        warp_arrive(&sm.s_free);
+      }
+      unsigned long long seen = ~0ull;  // masked tiles: which of the 64 rows see this key
+      if (masked) {
+        seen = 0;
+        for (int i = 0; i < 64; ++i) {
+          const int4 in = sm.info[st][c0 + i];
+          if (key >= in.x && key < in.y) seen |= 1ull << i;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const float4 l2 = *reinterpret_cast<const float4*>(&sm.l2[st][c0 + 16 * q + e]);
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            float2 x = f2(s[q][e + k], s[q][e + k + 1]);
+            const float2 nl = k == 0 ? make_float2(-l2.x, -l2.y) : make_float2(-l2.z, -l2.w);
+            float2 t;
+            if (CAP) {
+              x = make_float2(score.half_gap(x.x), score.half_gap(x.y));
+              t = ffma2(x, make_float2(-2.f * score.c2, -2.f * score.c2),
+                        fadd2(nl, make_float2(score.c2, score.c2)));
+            } else {
+              t = ffma2(x, make_float2(score.c1, score.c1), nl);
+            }
+            if (BIAS) {
+              const int4 i0 = sm.info[st][c0 + 16 * q + e + k];
+              const int4 i1 = sm.info[st][c0 + 16 * q + e + k + 1];
+              t.x = fmaf(-__int_as_float(i0.w), fabsf(static_cast<float>(key - i0.z)), t.x);
+              t.y = fmaf(-__int_as_float(i1.w), fabsf(static_cast<float>(key - i1.z)), t.y);
+            }
+            float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+            if (masked) {
+              const int i = 16 * q + e + k;
+              if (!(seen >> i & 1)) p.x = 0.f;
+              if (!(seen >> (i + 1) & 1)) p.y = 0.f;
+            }
+            pk[q][(e + k) >> 1] = pack_bf16x2(p.x, p.y);
+            if (CAP)  // 1 - tanh^2 = 4 r (1 - r)
+              p = fmul2(fmul2(p, fmul2(x, make_float2(4.f, 4.f))),
+                        fadd2(make_float2(1.f, 1.f), make_float2(-x.x, -x.y)));
+            s[q][e + k] = __float_as_uint(p.x);
+            s[q][e + k + 1] = __float_as_uint(p.y);
+          }
+        }
+      if (!C::kInPlace && n > 0) {
+        ok = mbar_wait_warp(&sm.w_free, (n - 1) & 1, abort_flag, err);
+        if (!ok) break;
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_st8(tbase + lane_off + C::p(4 * wg + q), pk[q]);
+      if (slot.in_lo == INT_MAX) {
+        // Rows that see nothing meet P = dS = 0: make Q and dO 0 there, once
+        // both score products have read them.
+        ok = mbar_wait_warp(&sm.p_full, n & 1, abort_flag, err);
+        if (!ok) break;
+        if (sm.info[st][r].y == 0) zero_row<NH, HALF>(wg == 0 ? sm.q[st] : sm.go[st], r);
+        fence_proxy_async_smem();
+        // dV(n) reads rows that the other warpgroup zeroes, too: it waits for
+        // both warpgroups' arrivals below.
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(&sm.w_ready);
+      ok = mbar_wait_warp(&sm.p_full, n & 1, abort_flag, err);
+      if (!ok) break;
+      tc_fence_after();
+      // dP in two halves: all of it beside the weights would not fit the registers.
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t x[2][16];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          tmem_ld16(tbase + lane_off + kP + c0 + 32 * h + 16 * q, x[q]);
+        tmem_wait_ld();
+        if (!C::kInPlace && h == 1) {
+          tc_fence_before();
+          warp_arrive(&sm.p_free);
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const int i0 = 32 * h + 16 * q + e;
+            const float4 dd = *reinterpret_cast<const float4*>(&sm.dd[st][c0 + i0]);
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              const float2 nd = k == 0 ? make_float2(-dd.x, -dd.y) : make_float2(-dd.z, -dd.w);
+              float2 ds = fmul2(f2(s[2 * h + q][e + k], s[2 * h + q][e + k + 1]),
+                                fadd2(f2(x[q][e + k], x[q][e + k + 1]), nd));
+              if (masked) {  // dP of a row that sees nothing may be NaN
+                if (!(seen >> (i0 + k) & 1)) ds.x = 0.f;
+                if (!(seen >> (i0 + k + 1) & 1)) ds.y = 0.f;
+              }
+              pk[2 * h + q][(e + k) >> 1] = pack_bf16x2(ds.x, ds.y);
+            }
+          }
+      }
+      if (!C::kInPlace && n > 0) {
+        ok = mbar_wait_warp(&sm.ds_free, (n - 1) & 1, abort_flag, err);
+        if (!ok) break;
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_st8(tbase + lane_off + C::ds(4 * wg + q), pk[q]);
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(&sm.ds_ready);
+    }
+    ok = mbar_wait_warp(&sm.out_full, 0, abort_flag, err) && ok;
+    ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+    tc_fence_after();
+    constexpr uint32_t kStage = BM * (DH * 2 + 16);
+    static_assert(kStage <= sizeof(sm.q) && kStage <= sizeof(sm.go), "staging fits in the ring");
+    const size_t at = (static_cast<size_t>(g) * a.Nk + j0) * DH;
+    store_block<DH>(tbase + lane_off + C::dK, a.tau, n == 0, &sm.q[0][0][0], wg, r,
+                    threadIdx.x - 64, key_end - j0, ok, static_cast<__nv_bfloat16*>(a.dK) + at);
+    store_block<DH>(tbase + lane_off + C::dV, 1.f, n == 0, &sm.go[0][0][0], wg, r,
+                    threadIdx.x - 64, key_end - j0, ok, static_cast<__nv_bfloat16*>(a.dV) + at);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+template <int DH, bool CAP, bool BIAS>
+cudaError_t launch(const AttnArgs& a) {
+  const int heads = a.B * a.Hkv, rows = a.H / a.Hkv * a.Nq;
+  CUtensorMap mq, mo, mk, mv;
+  cudaError_t e = tc_map_bf16(&mq, a.Q, heads, rows, BQ, DH);
+  if (e == cudaSuccess) e = tc_map_bf16(&mo, a.dO, heads, rows, BQ, DH);
+  if (e == cudaSuccess) e = tc_map_bf16(&mk, a.K, heads, a.Nk, BM, DH);
+  if (e == cudaSuccess) e = tc_map_bf16(&mv, a.V, heads, a.Nk, BM, DH);
+  if (e != cudaSuccess) return e;
+  constexpr size_t smem = sizeof(SmemK<DH>) + 1024;
+  static_assert(smem <= 232448, "shared memory");
+  const auto kernel = tc_dkv_kernel<DH, CAP, BIAS>;
+  e = tc_set_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const long long grid = static_cast<long long>((a.Nk + BM - 1) / BM) * heads;
+  if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+  kernel<<<static_cast<unsigned>(grid), NTHREADS, smem, a.stream>>>(mq, mo, mk, mv, a);
+  return cudaGetLastError();
+}
+
+template <int DH>
+cudaError_t launch(const AttnArgs& a) {
+  const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;
+  return cap ? (bias ? launch<DH, true, true>(a) : launch<DH, true, false>(a))
+             : (bias ? launch<DH, false, true>(a) : launch<DH, false, false>(a));
+}
+
+}  // namespace
+
+cudaError_t tc_attn_dkv(const AttnArgs& a) { return a.d == 64 ? launch<64>(a) : launch<128>(a); }
+
+}  // namespace flashbob

@@ -1,0 +1,324 @@
+// dQ of attention with key ranges on sm_103a tensor cores: bf16, head dim 64
+// or 128.  128 group rows (Q, dO) stay on chip, the key tiles of their hull
+// stream past:
+//   S = Q K^T, dP = dO V^T;  P = exp2(score(S) - L log2 e),
+//   dS = P (dP - D) (1 - tanh^2),  dQ += dS K;  dQ = tau dQ at the end.
+//
+// 320 threads: warp 0 TMA, warp 1 TMEM allocation and MMA issue, warps 2-5 /
+// 6-9 elementwise warpgroups that take columns 0-63 / 64-127 of every tile.
+// S and dP are handed back as soon as they are in registers, and dS (bf16)
+// has columns of its own, so the score products of tile t + 1 run while the
+// warpgroups work on tile t.  Per 128 x 128 tile the tensor pipe needs
+// (tcgen05 issue costs) 868 cycles at d = 64 and 1536 at d = 128.
+// K and V have rings of their own: a V tile is free after dP, a K tile only
+// after dQ.
+// TMEM: S [0,128), dP [128,256), dS operand [256,320), dQ from 320 on.
+#include "tc_attn.cuh"
+
+namespace flashbob {
+namespace {
+using namespace tc;
+using namespace attn;
+
+constexpr int BM = kTcRows, BN = 128;
+constexpr int NTHREADS = 320;
+constexpr uint32_t HALF = BM * 64 * 2;  // 128 rows x 64 columns
+constexpr uint32_t kS = 0, kP = 128, kOp = 256, kAcc = 320;
+
+template <int DH>
+struct SmemQ {
+  static constexpr int NH = DH / 64;
+  static constexpr int NK = DH == 64 ? 6 : 3, NV = DH == 64 ? 5 : 2;
+  alignas(1024) uint8_t q[NH][HALF];
+  alignas(1024) uint8_t go[NH][HALF];  // dO
+  alignas(1024) uint8_t k[NK][NH][HALF];
+  alignas(1024) uint8_t v[NV][NH][HALF];
+  int hull[4][4];
+  uint64_t bar_q;
+  uint64_t k_full[NK], k_empty[NK];
+  uint64_t v_full[NV], v_empty[NV];
+  uint64_t s_full, s_free;    // S of a tile is complete / read (8 warps)
+  uint64_t p_full, p_free;    // the same for dP
+  uint64_t op_ready, op_free;  // dS written (8 warps) / read by the MMAs
+  uint64_t out_full;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// Weights of 64 columns in place of the raw scores, times 1 - tanh^2.
+template <bool CAP, bool BIAS, bool MASKED>
+__device__ __forceinline__ void weights(const Score<CAP, BIAS>& sc, uint32_t (&s)[4][16], int jbase,
+                                        int lo, int hi, float dist, float l2) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      float2 x = f2(s[q][e], s[q][e + 1]);
+      if (CAP) x = make_float2(sc.half_gap(x.x), sc.half_gap(x.y));
+      const float2 t = sc.from(x, dist + (16 * q + e), l2, sc.slope2);
+      float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+      if (CAP)  // 4 r (1 - r)
+        p = fmul2(fmul2(p, fmul2(x, make_float2(4.f, 4.f))),
+                  fadd2(make_float2(1.f, 1.f), make_float2(-x.x, -x.y)));
+      if (MASKED) {
+        const int j = jbase + 16 * q + e;
+        if (j < lo || j >= hi) p.x = 0.f;
+        if (j + 1 < lo || j + 1 >= hi) p.y = 0.f;
+      }
+      s[q][e] = __float_as_uint(p.x);
+      s[q][e + 1] = __float_as_uint(p.y);
+    }
+}
+
+template <int DH, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    tc_dq_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mdO,
+                 const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
+                 const __grid_constant__ AttnArgs a, int blocks) {
+  extern __shared__ uint8_t smem_raw[];
+  using Smem = SmemQ<DH>;
+  constexpr int NH = Smem::NH, NK = Smem::NK, NV = Smem::NV;
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                      ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int heads = a.B * a.Hkv, G = a.H / a.Hkv, rows = G * a.Nq;
+  const int g = blockIdx.x % heads;
+  const int row0 = row_block(blockIdx.x / heads, blocks, G, a.Nq, BM) * BM;
+  volatile int* abort_flag = &sm.abort_flag;
+  unsigned int* err = a.err;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.bar_q, 1);
+    for (int s = 0; s < NK; ++s) mbar_init(&sm.k_full[s], 1), mbar_init(&sm.k_empty[s], 1);
+    for (int s = 0; s < NV; ++s) mbar_init(&sm.v_full[s], 1), mbar_init(&sm.v_empty[s], 1);
+    mbar_init(&sm.s_full, 1);
+    mbar_init(&sm.p_full, 1);
+    mbar_init(&sm.op_free, 1);
+    mbar_init(&sm.out_full, 1);
+    mbar_init(&sm.s_free, 8);
+    mbar_init(&sm.p_free, 8);
+    mbar_init(&sm.op_ready, 8);
+    sm.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+  const int wg = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane, row = row0 + r;
+  GroupRow gr{empty_view(), 0.f};
+  float l2 = INFINITY, dd = 0.f;
+  if (warp >= 2) {
+    gr = group_row(a, g / a.Hkv, g % a.Hkv, row, rows);
+    if (wg == 0) warp_hull(gr.v, row < rows, lane, sm.hull[quad]);
+    const GradRows st = grad_rows(a.workspace, heads, rows);
+    const size_t at = static_cast<size_t>(g) * st.pitch + row;  // the pitch covers the block
+    l2 = st.l2[at];
+    dd = st.dd[at];
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = sm.tmem_base;
+  const Hull hull = join_hulls(sm.hull, 4);
+  const int tb = hull.lo < hull.hi ? hull.lo / BN : 0;
+  const int T = hull.lo < hull.hi ? (hull.hi + BN - 1) / BN - tb : 0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&mK);
+      tma_prefetch_desc(&mV);
+      mbar_expect_tx(&sm.bar_q, 2 * NH * HALF);
+      for (int h = 0; h < NH; ++h) {
+        tma_load_3d(sm.q[h], &mQ, &sm.bar_q, 64 * h, row0, g);
+        tma_load_3d(sm.go[h], &mdO, &sm.bar_q, 64 * h, row0, g);
+      }
+      int nk = 0, nv = 0;
+      for (int t = 0; t < T; ++t) {
+        const int sk = t % NK, sv = t % NV;
+        if (t >= NK && !mbar_wait(&sm.k_empty[sk], ((t / NK) - 1) & 1, abort_flag, err)) break;
+        mbar_expect_tx(&sm.k_full[sk], NH * HALF);
+        for (int h = 0; h < NH; ++h)
+          tma_load_3d(sm.k[sk][h], &mK, &sm.k_full[sk], 64 * h, (tb + t) * BN, g);
+        nk = t + 1;
+        if (t >= NV && !mbar_wait(&sm.v_empty[sv], ((t / NV) - 1) & 1, abort_flag, err)) break;
+        mbar_expect_tx(&sm.v_full[sv], NH * HALF);
+        for (int h = 0; h < NH; ++h)
+          tma_load_3d(sm.v[sv][h], &mV, &sm.v_full[sv], 64 * h, (tb + t) * BN, g);
+        nv = t + 1;
+      }
+      drain_wait(&sm.bar_q, 0);
+      for (int t = nk > NK ? nk - NK : 0; t < nk; ++t) drain_wait(&sm.k_full[t % NK], (t / NK) & 1);
+      for (int t = nv > NV ? nv - NV : 0; t < nv; ++t) drain_wait(&sm.v_full[t % NV], (t / NV) & 1);
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t idS = idesc_bf16(BM, BN, false);
+    constexpr uint32_t idO = idesc_bf16(BM, DH, true);
+    const uint64_t dQ = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
+    const uint64_t dG = smem_desc_sw128(smem_u32(sm.go[0]), 16, 1024);
+    const uint64_t dK = smem_desc_sw128(smem_u32(sm.k[0][0]), 16, 1024);
+    const uint64_t dV = smem_desc_sw128(smem_u32(sm.v[0][0]), 16, 1024);
+    const uint64_t dKm = smem_desc_sw128(smem_u32(sm.k[0][0]), HALF, 1024);  // MN-major
+    constexpr uint64_t kTile = (uint64_t)(NH * HALF) >> 4;
+    auto scores = [&](uint32_t col, uint64_t da, uint64_t db) {
+#pragma unroll
+      for (int kk = 0; kk < DH / 16; ++kk) {
+        const uint64_t o = ((kk >> 2) * HALF + 32 * (kk & 3)) >> 4;
+        mma_ss(tbase + col, da + o, db + o, idS, kk > 0);
+      }
+    };
+    if (elect_one()) {
+      bool ok = mbar_wait(&sm.bar_q, 0, abort_flag, err);
+      auto issue_s = [&](int t) {
+        if (!mbar_wait(&sm.k_full[t % NK], (t / NK) & 1, abort_flag, err)) return false;
+        tc_fence_after();
+        scores(kS, dQ, dK + (t % NK) * kTile);
+        mma_commit(&sm.s_full);
+        return true;
+      };
+      auto issue_p = [&](int t) {
+        if (!mbar_wait(&sm.v_full[t % NV], (t / NV) & 1, abort_flag, err)) return false;
+        tc_fence_after();
+        scores(kP, dG, dV + (t % NV) * kTile);
+        mma_commit(&sm.p_full);
+        mma_commit(&sm.v_empty[t % NV]);
+        return true;
+      };
+      if (ok && T > 0) ok = issue_s(0) && issue_p(0);
+      for (int t = 0; ok && t < T; ++t) {
+        if (t + 1 < T) {
+          ok = mbar_wait(&sm.s_free, t & 1, abort_flag, err) && issue_s(t + 1) &&
+               mbar_wait(&sm.p_free, t & 1, abort_flag, err) && issue_p(t + 1);
+          if (!ok) break;
+        }
+        ok = mbar_wait(&sm.op_ready, t & 1, abort_flag, err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t dk = dKm + (t % NK) * kTile;
+#pragma unroll
+        for (int c = 0; c < BN / 16; ++c)
+          mma_ts(tbase + kAcc, tbase + kOp + 8 * c, dk + ((16 * 128 * c) >> 4), idO,
+                 t > 0 || c > 0);
+        mma_commit(&sm.op_free);
+        mma_commit(&sm.k_empty[t % NK]);
+      }
+      mma_commit(&sm.out_full);
+    }
+    __syncwarp();
+  } else {
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const int lo = gr.v.lo, hi = gr.v.hi;
+    const Score<CAP, BIAS> score(a, gr.slope2);
+    bool ok = true;
+    for (int t = 0; t < T; ++t) {
+      const int tile0 = (tb + t) * BN, col0 = tile0 + 64 * wg;
+      ok = mbar_wait_warp(&sm.s_full, t & 1, abort_flag, err);
+      if (!ok) break;
+      tc_fence_after();
+      const bool masked = col0 < hull.in_lo || col0 + 64 > hull.in_hi;
+      const float dist = BIAS ? static_cast<float>(col0 - gr.v.pos) : 0.f;
+      uint32_t s[4][16];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld16(tbase + lane_off + kS + 64 * wg + 16 * q, s[q]);
+      tmem_wait_ld();
+      tc_fence_before();
+      warp_arrive(&sm.s_free);
+      if (masked) weights<CAP, BIAS, true>(score, s, col0, lo, hi, dist, l2);
+      else weights<CAP, BIAS, false>(score, s, col0, lo, hi, dist, l2);
+      ok = mbar_wait_warp(&sm.p_full, t & 1, abort_flag, err);
+      if (!ok) break;
+      tc_fence_after();
+      // dP in two halves: all of it beside the weights would not fit the registers.
+      uint32_t pk[4][8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t x[2][16];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          tmem_ld16(tbase + lane_off + kP + 64 * wg + 32 * h + 16 * q, x[q]);
+        tmem_wait_ld();
+        if (h == 1) {
+          tc_fence_before();
+          warp_arrive(&sm.p_free);
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            float2 ds = fmul2(f2(s[2 * h + q][e], s[2 * h + q][e + 1]),
+                              fadd2(f2(x[q][e], x[q][e + 1]), make_float2(-dd, -dd)));
+            if (masked) {  // dP of a hidden key may be NaN
+              const int j = col0 + 32 * h + 16 * q + e;
+              if (j < lo || j >= hi) ds.x = 0.f;
+              if (j + 1 < lo || j + 1 >= hi) ds.y = 0.f;
+            }
+            pk[2 * h + q][e >> 1] = pack_bf16x2(ds.x, ds.y);
+          }
+      }
+      if (t > 0) {
+        ok = mbar_wait_warp(&sm.op_free, (t - 1) & 1, abort_flag, err);
+        if (!ok) break;
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        tmem_st8(tbase + lane_off + kOp + 32 * wg + 8 * q, pk[q]);
+      if (tile0 < hull.lo || tile0 + BN > hull.hi) {
+        // K rows that no row of the block sees meet dS = 0: make them 0 too.
+        if (wg == 0 && (tile0 + r < hull.lo || tile0 + r >= hull.hi))
+          zero_row<NH, HALF>(sm.k[t % NK], r);
+        fence_proxy_async_smem();
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(&sm.op_ready);
+    }
+    ok = mbar_wait_warp(&sm.out_full, 0, abort_flag, err) && ok;
+    ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+    tc_fence_after();
+    static_assert(BM * (DH * 2 + 16) <= sizeof(sm.k), "epilogue staging fits in the ring");
+    store_block<DH>(tbase + lane_off + kAcc, a.tau, T == 0, &sm.k[0][0][0], wg, r,
+                    threadIdx.x - 64, min(BM, rows - row0), ok,
+                    static_cast<__nv_bfloat16*>(a.dQ) +
+                        (static_cast<size_t>(g) * rows + row0) * DH);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+template <int DH, bool CAP, bool BIAS>
+cudaError_t launch(const AttnArgs& a) {
+  const int heads = a.B * a.Hkv, rows = a.H / a.Hkv * a.Nq;
+  CUtensorMap mq, mo, mk, mv;
+  cudaError_t e = tc_map_bf16(&mq, a.Q, heads, rows, BM, DH);
+  if (e == cudaSuccess) e = tc_map_bf16(&mo, a.dO, heads, rows, BM, DH);
+  if (e == cudaSuccess) e = tc_map_bf16(&mk, a.K, heads, a.Nk, BN, DH);
+  if (e == cudaSuccess) e = tc_map_bf16(&mv, a.V, heads, a.Nk, BN, DH);
+  if (e != cudaSuccess) return e;
+  constexpr size_t smem = sizeof(SmemQ<DH>) + 1024;
+  static_assert(smem <= 232448, "shared memory");
+  const auto kernel = tc_dq_kernel<DH, CAP, BIAS>;
+  e = tc_set_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const int blocks = (rows + BM - 1) / BM;
+  const long long grid = static_cast<long long>(blocks) * heads;
+  if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+  kernel<<<static_cast<unsigned>(grid), NTHREADS, smem, a.stream>>>(mq, mo, mk, mv, a, blocks);
+  return cudaGetLastError();
+}
+
+template <int DH>
+cudaError_t launch(const AttnArgs& a) {
+  const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;
+  return cap ? (bias ? launch<DH, true, true>(a) : launch<DH, true, false>(a))
+             : (bias ? launch<DH, false, true>(a) : launch<DH, false, false>(a));
+}
+
+}  // namespace
+
+cudaError_t tc_attn_dq(const AttnArgs& a) { return a.d == 64 ? launch<64>(a) : launch<128>(a); }
+
+}  // namespace flashbob

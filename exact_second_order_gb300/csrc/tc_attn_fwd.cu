@@ -1,0 +1,495 @@
+// Attention with key ranges on sm_103a tensor cores: bf16, head dim 64 or 128.
+//   S = Q K^T,  s = score(S) (scale, cap, bias; log2 units),
+//   P~ = exp2(s - m) with a running row maximum m,  l = sum P~,
+//   O = (sum P~ V) / l,  L = (m + log2 l) ln 2.
+//
+// 320 threads: warp 0 TMA, warp 1 TMEM allocation and MMA issue, warps 2-5
+// and 6-9 elementwise warpgroups.  The block's work is a run of units; unit u
+// goes to warpgroup u mod 2 and one of three score buffers in TMEM, where P~
+// (bf16) replaces the scores as the A operand of P~ V.  Each warpgroup has its
+// own O~ accumulator and raises its m only when a unit's maximum exceeds it by
+// more than 8 (log2 units), so O~ is rarely rescaled.
+//   MT = 2: 256 group rows a block, warpgroup w holds rows 128 w .. and both
+//     take every key tile, so a tile from L2 feeds twice the products: for
+//     calls with enough rows.
+//   MT = 1: 128 group rows, the warpgroups take alternate key tiles and merge
+//     their (m, l, O~) at the end: for few rows (tokens over a cache), where
+//     the keys are also cut into runs of blocks joined by a second launch.
+// Key tiles outside the hull of the block's ranges are not visited; tiles
+// inside every row's range run without a mask.  V rows outside the hull are
+// zeroed in shared memory before they meet P~ = 0, so a cache may hold
+// anything behind its last key.
+// TMEM: O~ of warpgroups 0 and 1 (DH columns each), then three score buffers.
+#include "tc_attn.cuh"
+
+namespace flashbob {
+namespace {
+using namespace tc;
+using namespace attn;
+
+constexpr int BM = kTcRows;
+constexpr int NTHREADS = 320;
+constexpr int NBUF = 3;
+constexpr uint32_t HALF_BLOCK = BM * 64 * 2;
+constexpr float kRescale = 8.f;
+
+template <int DH, int MT>
+struct Cfg {
+  static constexpr int kHalves = DH / 64;
+  static constexpr int kBN = DH == 64 ? 128 : 64;
+  static constexpr uint32_t kHalfTile = kBN * 64 * 2;
+  static constexpr int kStages = (MT == 2 ? 5 : 6) - (DH == 64 ? 0 : 1);
+  static_assert(2 * DH + NBUF * kBN <= 512, "TMEM columns");
+};
+
+constexpr int kStageLd = 64 + 4;  // epilogue: 64 columns of every row at a time
+
+template <int DH, int MT>
+struct SmemF {
+  static constexpr int NST = Cfg<DH, MT>::kStages;
+  static constexpr int NH = Cfg<DH, MT>::kHalves;
+  alignas(1024) uint8_t q[MT][NH][HALF_BLOCK];
+  alignas(1024) uint8_t kv[NST][2][NH][Cfg<DH, MT>::kHalfTile];
+  float part_m[2][BM];
+  float part_l[2][BM];
+  int hull[8][4];  // of each elementwise warp's rows
+  uint64_t bar_q;
+  uint64_t kv_full[NST];
+  uint64_t kv_empty[NST];
+  uint64_t sc_full[NBUF];
+  uint64_t op_ready[NBUF];
+  uint64_t pv_done[2];
+  uint64_t out_full;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// The score's input of 64 columns: raw, or in place the r of the cap.
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ void prepare64(const Score<CAP, BIAS>& sc, uint32_t (&s)[4][16]) {
+  if (CAP) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[q][e] = __float_as_uint(sc.half_gap(u2f(s[q][e])));
+  }
+}
+
+// Largest visible score of 64 columns from jbase on (log2 units, relative to
+// nothing).  Without a bias the score grows with the raw product, so the
+// maximum is taken over those.
+template <bool CAP, bool BIAS, bool MASKED>
+__device__ __forceinline__ float max64(const Score<CAP, BIAS>& sc, const uint32_t (&s)[4][16],
+                                       int jbase, int lo, int hi, float dist) {
+  float mr = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      const int j = jbase + 16 * q + e;
+      float2 x = f2(s[q][e], s[q][e + 1]);
+      if (BIAS) x = sc.from(x, dist + (16 * q + e), 0.f, sc.slope2);
+      if (!MASKED || (j >= lo && j < hi)) mr = fmaxf(mr, x.x);
+      if (!MASKED || (j + 1 >= lo && j + 1 < hi)) mr = fmaxf(mr, x.y);
+    }
+  return mr;
+}
+
+// P~ of 64 columns as bf16 pairs, added to the row sum (before rounding).
+template <bool CAP, bool BIAS, bool MASKED>
+__device__ __forceinline__ void weights64(const Score<CAP, BIAS>& sc, const uint32_t (&s)[4][16],
+                                          int jbase, int lo, int hi, float dist, float m,
+                                          float& l, uint32_t (&pk)[4][8]) {
+  float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      const float2 t = sc.from(f2(s[q][e], s[q][e + 1]), dist + (16 * q + e), m, sc.slope2);
+      float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+      if (MASKED) {
+        const int j = jbase + 16 * q + e;
+        if (j < lo || j >= hi) p.x = 0.f;
+        if (j + 1 < lo || j + 1 >= hi) p.y = 0.f;
+      }
+      acc = fadd2(acc, p);
+      pk[q][e >> 1] = pack_bf16x2(p.x, p.y);
+    }
+  l += acc.x + acc.y;
+}
+
+template <int DH, int MT, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    tc_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+                   const __grid_constant__ CUtensorMap mV, const __grid_constant__ AttnArgs a,
+                   int blocks, int splits) {
+  extern __shared__ uint8_t smem_raw[];
+  using C = Cfg<DH, MT>;
+  constexpr int NST = C::kStages, NH = C::kHalves, BN = C::kBN;
+  constexpr uint32_t HT = C::kHalfTile;
+  constexpr uint32_t kScore = 2 * DH;
+  SmemF<DH, MT>& sm = *reinterpret_cast<SmemF<DH, MT>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int heads = a.B * a.Hkv, G = a.H / a.Hkv, rows = G * a.Nq;
+  const int g = blockIdx.x % heads, rest = blockIdx.x / heads;
+  const int split = rest % splits;
+  const int row0 = row_block(rest / splits, blocks, G, a.Nq, MT * BM) * (MT * BM);
+  volatile int* abort_flag = &sm.abort_flag;
+  unsigned int* err = a.err;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.bar_q, 1);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&sm.kv_full[s], 1);
+      mbar_init(&sm.kv_empty[s], 1);
+    }
+    for (int b = 0; b < NBUF; ++b) {
+      mbar_init(&sm.sc_full[b], 1);
+      mbar_init(&sm.op_ready[b], 4);
+    }
+    mbar_init(&sm.pv_done[0], 1);
+    mbar_init(&sm.pv_done[1], 1);
+    mbar_init(&sm.out_full, 1);
+    sm.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+  // Elementwise threads: TMEM lane r of row block w.
+  const int wg = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane;
+  GroupRow gr{empty_view(), 0.f};
+  const int row = row0 + r + (MT == 2 ? BM * wg : 0);
+  if (warp >= 2) {
+    gr = group_row(a, g / a.Hkv, g % a.Hkv, row, rows);
+    warp_hull(gr.v, row < rows, lane, sm.hull[4 * wg + quad]);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = sm.tmem_base;
+  const Hull hull = join_hulls(sm.hull, 8);
+  // Key tiles of the hull, and this split's run of them.
+  const int t_lo = hull.lo < hull.hi ? hull.lo / BN : 0;
+  const int t_n = hull.lo < hull.hi ? (hull.hi + BN - 1) / BN - t_lo : 0;
+  const int tb = t_lo + static_cast<int>(static_cast<long long>(t_n) * split / splits);
+  const int T = t_lo + static_cast<int>(static_cast<long long>(t_n) * (split + 1) / splits) - tb;
+  const int U = MT * T;  // units
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&mK);
+      tma_prefetch_desc(&mV);
+      mbar_expect_tx(&sm.bar_q, MT * NH * HALF_BLOCK);
+      for (int w = 0; w < MT; ++w)
+        for (int h = 0; h < NH; ++h)
+          tma_load_3d(sm.q[w][h], &mQ, &sm.bar_q, 64 * h, row0 + BM * w, g);
+      int issued = 0;
+      for (int t = 0; t < T; ++t) {
+        const int s = t % NST;
+        if (t >= NST && !mbar_wait(&sm.kv_empty[s], ((t / NST) - 1) & 1, abort_flag, err)) break;
+        mbar_expect_tx(&sm.kv_full[s], 2 * NH * HT);
+        for (int h = 0; h < NH; ++h)
+          tma_load_3d(sm.kv[s][0][h], &mK, &sm.kv_full[s], 64 * h, (tb + t) * BN, g);
+        for (int h = 0; h < NH; ++h)
+          tma_load_3d(sm.kv[s][1][h], &mV, &sm.kv_full[s], 64 * h, (tb + t) * BN, g);
+        issued = t + 1;
+      }
+      drain_wait(&sm.bar_q, 0);
+      for (int t = issued > NST ? issued - NST : 0; t < issued; ++t)
+        drain_wait(&sm.kv_full[t % NST], (t / NST) & 1);
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t idS = idesc_bf16(BM, BN, false);
+    constexpr uint32_t idO = idesc_bf16(BM, DH, true);
+    const uint64_t dQ = smem_desc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
+    const uint64_t dK0 = smem_desc_sw128(smem_u32(sm.kv[0][0][0]), 16, 1024);
+    const uint64_t dV0 = smem_desc_sw128(smem_u32(sm.kv[0][1][0]), HT, 1024);
+    constexpr uint64_t kStage = sizeof(sm.kv[0]) >> 4;
+    auto tile = [](int u) { return MT == 2 ? u >> 1 : u; };
+    auto issue_scores = [&](int u) {
+      const uint64_t so = (tile(u) % NST) * kStage;
+      const uint64_t qo = MT == 2 ? (u & 1) * (uint64_t)((NH * HALF_BLOCK) >> 4) : 0;
+      const uint32_t sc = tbase + kScore + BN * (u % NBUF);
+#pragma unroll
+      for (int kk = 0; kk < DH / 16; ++kk) {
+        const uint32_t h = kk >> 2, o = 32 * (kk & 3);
+        mma_ss(sc, dQ + qo + ((h * HALF_BLOCK + o) >> 4), dK0 + so + ((h * HT + o) >> 4), idS,
+               kk > 0);
+      }
+      mma_commit(&sm.sc_full[u % NBUF]);
+    };
+    auto issue_pv = [&](int u) {
+      const int s = tile(u) % NST;
+      const uint32_t sc = tbase + kScore + BN * (u % NBUF);
+      const uint64_t dv = dV0 + s * kStage;
+      const uint32_t acc_col = tbase + DH * (u & 1);
+#pragma unroll
+      for (int c = 0; c < BN / 16; ++c)
+        mma_ts(acc_col, sc + 8 * c, dv + ((16 * 128 * c) >> 4), idO, (u >= 2 || c > 0));
+      mma_commit(&sm.pv_done[u & 1]);
+      if (MT == 1 || (u & 1)) mma_commit(&sm.kv_empty[s]);
+    };
+    if (elect_one()) {
+      bool ok = mbar_wait(&sm.bar_q, 0, abort_flag, err);
+      tc_fence_after();
+      for (int u = 0; ok && u < NBUF && u < U; ++u) {
+        ok = mbar_wait(&sm.kv_full[tile(u) % NST], (tile(u) / NST) & 1, abort_flag, err);
+        tc_fence_after();
+        if (ok) issue_scores(u);
+      }
+      for (int u = 0; ok && u < U; ++u) {
+        ok = mbar_wait(&sm.op_ready[u % NBUF], (u / NBUF) & 1, abort_flag, err);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv(u);
+        if (u + NBUF < U) {
+          const int tn = tile(u + NBUF);
+          ok = mbar_wait(&sm.kv_full[tn % NST], (tn / NST) & 1, abort_flag, err);
+          if (!ok) break;
+          tc_fence_after();
+          issue_scores(u + NBUF);
+        }
+      }
+      mma_commit(&sm.out_full);
+    }
+    __syncwarp();
+  } else {
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t acc_own = tbase + lane_off + DH * wg;
+    const int lo = gr.v.lo, hi = gr.v.hi;
+    const Hull own = MT == 2 ? join_hulls(sm.hull + 4 * wg, 4) : hull;
+    const Score<CAP, BIAS> score(a, gr.slope2);
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    int n = 0;  // units of this warpgroup
+    for (int u = wg; u < U; u += 2, ++n) {
+      const int col0 = (tb + (MT == 2 ? u >> 1 : u)) * BN;
+      ok = ok && mbar_wait_warp(&sm.sc_full[u % NBUF], (u / NBUF) & 1, abort_flag, err);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t sc = tbase + lane_off + kScore + BN * (u % NBUF);
+      const bool masked = col0 < own.in_lo || col0 + BN > own.in_hi;
+      const float dist = BIAS ? static_cast<float>(col0 - gr.v.pos) : 0.f;
+      // Two 64-column groups at d = 64: the second is read twice, so that one
+      // group is held in registers at a time, and P~ of columns 16 c .. goes
+      // to columns 8 c .., onto scores already used.
+      float mr = -INFINITY;
+      uint32_t s[4][16];
+      auto load64 = [&](int c) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld16(sc + c + 16 * q, s[q]);
+        tmem_wait_ld();
+      };
+      auto max_of = [&](int c) {
+        if (BIAS) prepare64(score, s);
+        mr = fmaxf(mr, masked ? max64<CAP, BIAS, true>(score, s, col0 + c, lo, hi, dist + c)
+                              : max64<CAP, BIAS, false>(score, s, col0 + c, lo, hi, dist + c));
+      };
+      if (BN == 128) {
+        load64(64);
+        max_of(64);
+      }
+      load64(0);
+      max_of(0);
+      float mt = mr;
+      if (!BIAS) {
+        mt = mr * score.c1;
+        if (CAP && mr != -INFINITY) mt = fmaf(-2.f * score.c2, score.half_gap(mr), score.c2);
+      }
+      const bool raise = mt > m + kRescale;
+      const float factor = raise ? (m == -INFINITY ? 0.f : ex2_approx(m - mt)) : 1.f;
+      if (raise) {
+        l *= factor;
+        m = mt;
+      }
+      if (__any_sync(0xffffffffu, raise && factor < 1.f) && n > 0) {
+        ok = mbar_wait_warp(&sm.pv_done[wg], (n - 1) & 1, abort_flag, err);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < DH / 16; ++c) {
+          uint32_t v[16];
+          tmem_ld16(acc_own + 16 * c, v);
+          tmem_wait_ld();
+          uint32_t w0[8], w1[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            w0[k] = __float_as_uint(u2f(v[k]) * factor);
+            w1[k] = __float_as_uint(u2f(v[8 + k]) * factor);
+          }
+          tmem_st8(acc_own + 16 * c, w0);
+          tmem_st8(acc_own + 16 * c + 8, w1);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < BN; c += 64) {
+        if (c > 0) load64(c);
+        if (!BIAS || c > 0) prepare64(score, s);
+        uint32_t pk[4][8];
+        if (masked) weights64<CAP, BIAS, true>(score, s, col0 + c, lo, hi, dist + c, m, l, pk);
+        else weights64<CAP, BIAS, false>(score, s, col0 + c, lo, hi, dist + c, m, l, pk);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_st8(sc + c / 2 + 8 * q, pk[q]);
+      }
+      if (col0 < hull.lo || col0 + BN > hull.hi) {
+        // V rows that no row of the block sees meet P~ = 0: make them 0 too.
+        const int t = MT == 2 ? u >> 1 : u;
+        if (r < BN && (col0 + r < hull.lo || col0 + r >= hull.hi)) {
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            uint4* v = reinterpret_cast<uint4*>(sm.kv[t % NST][1][h] + r * 128);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        fence_proxy_async_smem();
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(&sm.op_ready[u % NBUF]);
+    }
+
+    ok = mbar_wait_warp(&sm.out_full, 0, abort_flag, err) && ok;
+    ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+    tc_fence_after();
+    // MT = 1: merge the warpgroups' (m, l, O~): m* = max, s_w = exp2(m_w - m*),
+    // O~ = s_0 O~_0 + s_1 O~_1, l = s_0 l_0 + s_1 l_1.  An accumulator whose
+    // warpgroup had no unit was never written.
+    float mm = m, lsum = l, s0 = 1.f, s1 = 0.f;
+    if (MT == 1) {
+      sm.part_m[wg][r] = m;
+      sm.part_l[wg][r] = l;
+      named_bar_sync(1, 256);
+      const float m0 = sm.part_m[0][r], m1 = sm.part_m[1][r];
+      mm = fmaxf(m0, m1);
+      s0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - mm);
+      s1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - mm);
+      lsum = s0 * sm.part_l[0][r] + s1 * sm.part_l[1][r];
+    }
+    const bool any0 = T > 0, any1 = MT == 1 ? T > 1 : false;
+    const float inv = splits > 1 ? 1.f : lsum > 0.f ? 1.f / lsum : 0.f;
+    s0 = any0 ? s0 * inv : 0.f;
+    s1 = any1 ? s1 * inv : 0.f;
+    const size_t all = static_cast<size_t>(a.B) * a.H * a.Nq;
+    const size_t base = static_cast<size_t>(g) * rows;  // first row of the group
+    const Partials part = partials(a.workspace, all, DH, splits);
+    if (ok && row < rows && (MT == 2 || wg == 0)) {
+      if (splits > 1) part.ml[split * all + base + row] = make_float2(mm, lsum);
+      else a.L[base + row] = (mm + __log2f(lsum)) * kLn2;
+    }
+    // Every MMA is done, so the ring is idle: 64 columns of O at a time go
+    // through it and leave with coalesced stores.
+    float* st = reinterpret_cast<float*>(&sm.kv[0][0][0][0]);
+    static_assert(MT * BM * kStageLd * 4 <= sizeof(sm.kv), "epilogue staging fits in the ring");
+    const int tid = threadIdx.x - 64;
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      if (h > 0) named_bar_sync(1, 256);
+      constexpr int kCols = MT == 2 ? 64 : 32;  // MT = 1: each warpgroup forms half the columns
+      const int c0 = MT == 2 ? 0 : 32 * wg;
+      const int sr = MT == 2 ? BM * wg + r : r;
+#pragma unroll
+      for (int c = 0; c < kCols; c += 16) {
+        const uint32_t col = 64 * h + c0 + c;
+        uint32_t v0[16], v1[16];
+        if (MT == 2) {
+          tmem_ld16(acc_own + col, v0);
+        } else {
+          tmem_ld16(tbase + lane_off + col, v0);
+          tmem_ld16(tbase + lane_off + DH + col, v1);
+        }
+        tmem_wait_ld();
+        float4* s4 = reinterpret_cast<float4*>(st + sr * kStageLd + c0 + c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float o[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            o[q] = any0 ? s0 * u2f(v0[4 * k + q]) : 0.f;
+            if (MT == 1 && any1) o[q] = fmaf(s1, u2f(v1[4 * k + q]), o[q]);
+          }
+          s4[k] = make_float4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      named_bar_sync(1, 256);
+      const int live = min(MT * BM, rows - row0);
+      if (ok) {
+        for (int f = tid; f < live * 16; f += 256) {
+          const int rr = f >> 4, c4 = f & 15;
+          const float4 v = *reinterpret_cast<const float4*>(st + rr * kStageLd + 4 * c4);
+          const size_t at = (base + row0 + rr) * DH + 64 * h + 4 * c4;
+          if (splits > 1) {
+            *reinterpret_cast<float4*>(part.o + split * all * DH + at) = v;
+          } else {
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + at) =
+                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+template <int DH, int MT, bool CAP, bool BIAS>
+cudaError_t launch(const AttnArgs& a, int splits) {
+  const int heads = a.B * a.Hkv, rows = a.H / a.Hkv * a.Nq;
+  CUtensorMap mq, mk, mv;
+  cudaError_t e = tc_map_bf16(&mq, a.Q, heads, rows, BM, DH);
+  if (e == cudaSuccess) e = tc_map_bf16(&mk, a.K, heads, a.Nk, Cfg<DH, MT>::kBN, DH);
+  if (e == cudaSuccess) e = tc_map_bf16(&mv, a.V, heads, a.Nk, Cfg<DH, MT>::kBN, DH);
+  if (e != cudaSuccess) return e;
+  const size_t smem = sizeof(SmemF<DH, MT>) + 1024;
+  static_assert(sizeof(SmemF<DH, MT>) + 1024 <= 232448, "shared memory");
+  const auto kernel = tc_attn_kernel<DH, MT, CAP, BIAS>;
+  e = tc_set_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const int blocks = (rows + MT * BM - 1) / (MT * BM);
+  const long long grid = static_cast<long long>(blocks) * splits * heads;
+  if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+  kernel<<<static_cast<unsigned>(grid), NTHREADS, smem, a.stream>>>(mq, mk, mv, a, blocks, splits);
+  return cudaGetLastError();
+}
+
+template <int DH, int MT>
+cudaError_t launch(const AttnArgs& a, int splits) {
+  const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;
+  return cap ? (bias ? launch<DH, MT, true, true>(a, splits) : launch<DH, MT, true, false>(a, splits))
+             : (bias ? launch<DH, MT, false, true>(a, splits)
+                     : launch<DH, MT, false, false>(a, splits));
+}
+
+}  // namespace
+
+bool tc_attn_supported(const AttnArgs& a) { return a.bf16 && (a.d == 64 || a.d == 128); }
+
+// 256 rows a block once such blocks fill the GPU, 128 below.
+static bool two_blocks(const AttnArgs& a) {
+  const long long rows = static_cast<long long>(a.H / a.Hkv) * a.Nq;
+  return static_cast<long long>(a.B) * a.Hkv * ((rows + 255) / 256) >= kSMs;
+}
+
+int tc_attn_splits(const AttnArgs& a) {
+  const long long rows = static_cast<long long>(a.H / a.Hkv) * a.Nq;
+  const long long blocks = static_cast<long long>(a.B) * a.Hkv * ((rows + BM - 1) / BM);
+  if (two_blocks(a) || blocks * 2 > kSMs) return 1;
+  const long long s = kSMs / blocks, most = a.Nk / 512 > 1 ? a.Nk / 512 : 1;
+  return static_cast<int>(s < most ? s : most);
+}
+
+cudaError_t tc_attn(const AttnArgs& a) {
+  const int splits = tc_attn_splits(a);
+  cudaError_t e;
+  if (two_blocks(a)) e = a.d == 64 ? launch<64, 2>(a, splits) : launch<128, 2>(a, splits);
+  else e = a.d == 64 ? launch<64, 1>(a, splits) : launch<128, 1>(a, splits);
+  return e == cudaSuccess && splits > 1 ? attn_join(a, splits) : e;
+}
+
+}  // namespace flashbob

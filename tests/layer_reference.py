@@ -9,12 +9,15 @@ same sum over absolute values.  All else is fp32: a relative error e of P
 covers the score's dot product (d + 4 roundings of 2^-24 of the absolute
 products, in the forward's score and again in L), the bias, the tanh, the
 exponential and the row sum.  D = dO . O is computed from the rounded O.
+Numbers below 2^-126, the smallest normal number of fp32 and of bf16, may be
+flushed to 0: 2^-126 absolute for each weight that a query gives a key it sees
+(and so |dP - D| times that for dS), and for dS itself.
 """
 import math
 
 import torch
 
-F64 = torch.float64
+TINY = 2.0 ** -126
 
 
 def visible(B, Nq, Nk, ranges, q_pos, causal, device="cuda"):
@@ -62,9 +65,10 @@ def attention(Q, K, V, tau, cap=0.0, slopes=None, ranges=None, q_pos=None, causa
     e = torch.where(see, e, 0.0)
     eL = e.amax(dim=3, keepdim=True) + (Nk + 8) * 2.0 ** -24  # of L, absolute
     eP = e + eL + torch.where(alive, L.abs(), 0.0) * 2.0 ** -22 + 2.0 ** -20  # of P, relative
+    bP = torch.where(see, P * (u + eP) + TINY, 0.0)  # of P, absolute
     O = P @ v
     aO = P @ v.abs()
-    bO = u * O.abs() + (P * (u + eP)) @ v.abs()
+    bO = u * O.abs() + bP @ v.abs()
     val = {"O": O, "L": L[..., 0]}
     bound = {"O": bO, "L": (eL + L.abs() * 2.0 ** -22)[..., 0]}
     if dO is None:
@@ -77,7 +81,8 @@ def attention(Q, K, V, tau, cap=0.0, slopes=None, ranges=None, q_pos=None, causa
     dS = P * (dP - D) * damp
     # damp = 1 - tanh^2 is off by twice what tanh is (2^-21).
     eS = (P * damp * (eD + (d + 4) * 2.0 ** -24 * (w.abs() @ v.abs().transpose(2, 3)))
-          + dS.abs() * (eP + u + 2.0 ** -22) + P * (dP - D).abs() * (2.0 ** -19 if cap else 0.0))
+          + dS.abs() * (eP + u + 2.0 ** -22) + P * (dP - D).abs() * (2.0 ** -19 if cap else 0.0)
+          + torch.where(see, TINY * (1 + (dP - D).abs()), 0.0))
 
     def shared(x):
         return x.view(B, Hkv, G, Nk, d).sum(dim=2)
@@ -88,7 +93,7 @@ def attention(Q, K, V, tau, cap=0.0, slopes=None, ranges=None, q_pos=None, causa
     val |= {"dQ": dQ, "dK": dK, "dV": dV}
     bound |= {"dQ": u * dQ.abs() + tau * eS @ k.abs(),
               "dK": u * dK.abs() + shared(tau * eS.transpose(2, 3) @ q.abs()),
-              "dV": u * dV.abs() + shared((P * (u + eP)).transpose(2, 3) @ w.abs())}
+              "dV": u * dV.abs() + shared(bP.transpose(2, 3) @ w.abs())}
     return val, bound
 
 
