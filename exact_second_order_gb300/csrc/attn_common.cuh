@@ -49,18 +49,27 @@ __device__ __forceinline__ int warp_max(int v) { return __reduce_max_sync(0xffff
 //   info  {lo, hi, pos, slope log2 e (as bits)},
 //   l2, dd  L log2 e and D; +inf in place of L for rows that see nothing and
 //         for the padding, so that P = exp2(s - L) is 0 there,
+//   ex      (bf16 with d = 64 only) -L / tau and -D as sums of three bf16 parts
+//         (exact to 2^-24), the B operand of one more K step of the score
+//         products: columns 0 - 2 and 3 - 5 of 16, in core matrices of 8 rows
+//         x 16 bytes (row r of 128: (r / 8) 256 + (r % 8) 16, columns 8 - 15
+//         128 bytes further); the L columns are 0 for capped scores,
 // and for each kBoundRows rows {min lo, max hi, max lo, min hi}: the hull of
 // their ranges and their intersection (the padding takes no part).
 struct GradRows {
   int4* bounds;
   int4* info;
   float *l2, *dd;
+  uint8_t* ex;  // kExRow bytes a row
   int pitch;  // padded rows per (batch, key/value head)
 };
 
 __host__ __device__ inline int padded_rows(int rows) {
   return (rows + kRowPad - 1) / kRowPad * kRowPad;
 }
+
+constexpr int kExRow = 32;
+constexpr float kFar = 1e30f;  // L / tau of a row that sees nothing: its P is exactly 0
 
 __host__ __device__ inline GradRows grad_rows(void* workspace, int groups, int rows) {
   GradRows g;
@@ -70,6 +79,7 @@ __host__ __device__ inline GradRows grad_rows(void* workspace, int groups, int r
   g.info = g.bounds + n / kBoundRows;
   g.l2 = reinterpret_cast<float*>(g.info + n);
   g.dd = g.l2 + n;
+  g.ex = reinterpret_cast<uint8_t*>(g.dd + n);
   return g;
 }
 

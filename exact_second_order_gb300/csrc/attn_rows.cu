@@ -4,6 +4,7 @@
 #include <math.h>
 
 #include "attn_common.cuh"
+#include "tc_common.cuh"
 
 namespace flashbob {
 namespace {
@@ -92,7 +93,8 @@ __global__ void __launch_bounds__(256)
     grad_rows_kernel(const T* __restrict__ O, const T* __restrict__ dO,
                      const float* __restrict__ L, const int* __restrict__ ranges,
                      const int* __restrict__ q_pos, const float* __restrict__ slopes,
-                     void* workspace, int B, int H, int Hkv, int Nq, int Nk, int d, int causal) {
+                     void* workspace, int B, int H, int Hkv, int Nq, int Nk, int d, int causal,
+                     float inv_tau, int ex) {
   __shared__ int s_bound[4][8];
   const int G = H / Hkv, rows = G * Nq;
   const int g = blockIdx.z * Hkv + blockIdx.y;
@@ -128,6 +130,15 @@ __global__ void __launch_bounds__(256)
       out.info[at] = make_int4(v.lo, v.hi, v.pos, __float_as_int(slope));
       out.l2[at] = v.hi > 0 ? l * kLog2e : INFINITY;
       out.dd[at] = v.hi > 0 ? dot : 0.f;
+      if (ex) {  // inv_tau = 0 for capped scores
+        const uint2 el = tc::split3_bf16(inv_tau == 0.f ? 0.f : v.hi > 0 ? -l * inv_tau : -kFar);
+        const uint2 ed = tc::split3_bf16(v.hi > 0 ? -dot : 0.f);
+        uint8_t* row = out.ex + (at / kRowPad) * kRowPad * kExRow + (at % kRowPad / 8) * 256 +
+                       (at % 8) * 16;
+        *reinterpret_cast<uint4*>(row) =
+            make_uint4(el.x, el.y | (ed.x << 16), (ed.x >> 16) | (ed.y << 16), 0u);
+        *reinterpret_cast<uint4*>(row + 128) = make_uint4(0u, 0u, 0u, 0u);
+      }
     }
   }
   b_lo = warp_min(b_lo);
@@ -192,7 +203,8 @@ cudaError_t launch_grad_rows(const AttnArgs& a) {
   const dim3 grid(padded_rows(rows) / kBoundRows, a.Hkv, a.B);
   grad_rows_kernel<T><<<grid, 256, 0, a.stream>>>(
       static_cast<const T*>(a.O), static_cast<const T*>(a.dO), a.L, a.ranges, a.q_pos, a.slopes,
-      a.workspace, a.B, a.H, a.Hkv, a.Nq, a.Nk, a.d, a.causal ? 1 : 0);
+      a.workspace, a.B, a.H, a.Hkv, a.Nq, a.Nk, a.d, a.causal ? 1 : 0,
+      a.cap > 0.f ? 0.f : 1.f / a.tau, a.bf16 && a.d == 64 ? 1 : 0);
   return cudaGetLastError();
 }
 
@@ -235,7 +247,8 @@ size_t attn_forward_workspace(const AttnArgs& a) {
 size_t attn_grad_workspace(const AttnArgs& a) {
   const int rows = a.H / a.Hkv * a.Nq, groups = a.B * a.Hkv;
   const GradRows g = grad_rows(nullptr, groups, rows);
-  return reinterpret_cast<size_t>(g.dd) + static_cast<size_t>(groups) * g.pitch * sizeof(float);
+  return reinterpret_cast<size_t>(g.ex) +
+         (a.bf16 && a.d == 64 ? static_cast<size_t>(groups) * g.pitch * kExRow : 0);
 }
 
 // A grid that leaves SMs idle is cut along the keys, so that the tiles of one

@@ -27,6 +27,57 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+// Bounded waits that suspend the thread until the phase completes, or for
+// kHintNs at a time.  The loops of the shared header read the global timer on
+// entry and poll often; here a wake-up is what an MMA round trip waits for, and
+// polling warps take issue slots from the working ones (4% of the gradient).
+// As everywhere, a wait that gives up (2 s) records error code 1 and raises
+// the flag that makes the others of the block give up.
+constexpr uint32_t kHintNs = 1000000;
+constexpr int kMaxTries = 2000;
+
+__device__ __forceinline__ bool try_hint(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(tc::smem_u32(bar)), "r"(parity), "r"(kHintNs)
+      : "memory");
+  return ok != 0;
+}
+static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity,
+                                              volatile int* abort_flag, unsigned int* err) {
+#pragma unroll 1
+  for (int i = 0; i < kMaxTries; ++i) {
+    if (try_hint(bar, parity)) return true;
+    if (*abort_flag) return false;
+  }
+  *abort_flag = 1;
+  atomicExch(err, 1u);
+  return false;
+}
+// One thread.
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                         unsigned int* err) {
+  return try_hint(bar, parity) || wait_slow(bar, parity, abort_flag, err);
+}
+// A whole warp (all lanes wait; the vote keeps the result uniform).
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          unsigned int* err) {
+  return __all_sync(0xffffffffu, wait_one(bar, parity, abort_flag, err));
+}
+// On two barriers: the polls are issued together, and only a barrier that is
+// not there yet is waited for.
+__device__ __forceinline__ bool wait_both_warp(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
+                                               volatile int* abort_flag, unsigned int* err) {
+  const bool ra = tc::mbar_try_wait(a, pa), rb = tc::mbar_try_wait(b, pb);
+  const bool ok = (ra && rb) || ((ra || wait_slow(a, pa, abort_flag, err)) &&
+                                 (rb || wait_slow(b, pb, abort_flag, err)));
+  return __all_sync(0xffffffffu, ok);
+}
+
 // Row blocks are launched heads fastest and from the last rows of a head to
 // the first, so that under a causal mask the long blocks start first and the
 // short ones fill the end.  A rank is the r-th block of `blocks` row blocks
@@ -117,19 +168,19 @@ struct Score {
   }
 };
 
-// 128 x DH accumulator columns of TMEM lane r (two warpgroups take half the
-// columns each), times `scale`, as bf16 rows in shared memory (pitch DH + 8:
+// 128 x DH accumulator columns of TMEM lane r (NWG warpgroups share the
+// columns), times `scale`, as bf16 rows in shared memory (pitch DH + 8:
 // 16-byte accesses of 8 consecutive rows fall on all 32 banks), then to
 // `rows` consecutive global rows with coalesced 16-byte stores.  `zero`: the
-// accumulator was never written.  256 elementwise threads, named barrier 1.
-template <int DH>
+// accumulator was never written.  All elementwise threads, named barrier 1.
+template <int DH, int NWG>
 __device__ __forceinline__ void store_block(uint32_t acc, float scale, bool zero, uint8_t* stage,
                                             int wg, int r, int tid, int rows, bool ok,
                                             __nv_bfloat16* __restrict__ out) {
   constexpr int kPitch = DH * 2 + 16;
 #pragma unroll
-  for (int c = 0; c < DH / 2; c += 16) {
-    const int col = DH / 2 * wg + c;
+  for (int c = 0; c < DH / NWG; c += 16) {
+    const int col = DH / NWG * wg + c;
     uint32_t v[16], w[8];
     tc::tmem_ld16(acc + col, v);
     tc::tmem_wait_ld();
@@ -140,12 +191,25 @@ __device__ __forceinline__ void store_block(uint32_t acc, float scale, bool zero
     d[0] = make_uint4(w[0], w[1], w[2], w[3]);
     d[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
-  tc::named_bar_sync(1, 256);
+  tc::named_bar_sync(1, 128 * NWG);
   if (ok) {
     constexpr int kChunks = DH / 8;
-    for (int f = tid; f < rows * kChunks; f += 256)
+    for (int f = tid; f < rows * kChunks; f += 128 * NWG)
       reinterpret_cast<uint4*>(out)[f] =
           *reinterpret_cast<const uint4*>(stage + (f / kChunks) * kPitch + (f % kChunks) * 16);
+  }
+}
+
+// Row r of a 64-column tile in the 128-byte swizzle (16-byte chunk c at chunk
+// c ^ (r mod 8)) as the A operand in TMEM: K step kk at columns 8 kk.
+__device__ __forceinline__ void row_to_tmem(const uint8_t* tile, int r, uint32_t taddr) {
+  const uint8_t* row = tile + r * 128;
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {
+    const uint4 a = *reinterpret_cast<const uint4*>(row + (((2 * kk) ^ (r & 7)) << 4));
+    const uint4 b = *reinterpret_cast<const uint4*>(row + (((2 * kk + 1) ^ (r & 7)) << 4));
+    const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    tc::tmem_st8(taddr + 8 * kk, v);
   }
 }
 

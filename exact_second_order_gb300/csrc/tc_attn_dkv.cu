@@ -5,17 +5,23 @@
 //   S^T = K Q^T, dP^T = V dO^T;  P = exp2(score(S) - L log2 e),
 //   dS = P (dP - D) (1 - tanh^2),  dV += P^T dO,  dK += dS^T Q (times tau).
 //
-// 320 threads: warp 0 finds the tiles (the bounds of 32 at a time against the
+// 576 threads: warp 0 finds the tiles (the bounds of 32 at a time against the
 // block's keys) and loads them with their row state; warp 1 allocates TMEM
-// and issues the MMAs; warps 2-5 / 6-9 are elementwise warpgroups that take
-// rows 0-63 / 64-127 of every tile, one key per thread.  How many tiles there
+// and issues the MMAs; then come four elementwise warpgroups that take 32 rows
+// of every tile each, one key per thread.  How many tiles there
 // are is known only to warp 0: each ring slot says which tile it holds, and a
 // last slot says that there are no more.
 // TMEM at d = 64: S^T, dP^T (128 columns each), operands P^T and dS^T (64
 // each), dK, dV (64 each): the scores are handed back when they are in
 // registers, and those of tile n + 1 run beside the arithmetic of tile n.
-// At d = 128 dK and dV take 256 columns and the operands lie on the scores
-// they came from; the pipe runs dV(n), S(n + 1), dK(n), dP(n + 1), so that
+// At d = 64 the row scalars ride in the score products: one more K step of an
+// A operand of ones against the rows' -L / tau and -D leaves S^T - L / tau (for
+// capped scores S^T) and dP^T - D in TMEM.  Read from shared memory instead,
+// 32 values of each for every warp and tile, they cost 350 of 1150 us (8
+// heads, 16384 rows); at d = 128, where the operands' own traffic bounds the
+// kernel, nothing, so there they are read.
+// At d = 128 dK and dV take 256 columns: one buffer of each, P^T on S^T and
+// dS^T on dP^T; the pipe runs dV(n), S(n + 1), dK(n), dP(n + 1), so that
 // P(n + 1) is formed beside dK(n) and dP(n + 1), and dS beside dV and S.
 #include "tc_attn.cuh"
 
@@ -25,21 +31,24 @@ using namespace tc;
 using namespace attn;
 
 constexpr int BM = kTcRows, BQ = 128;
-constexpr int NTHREADS = 320;
+#ifndef X_NWG
+#define X_NWG 4
+#endif
+constexpr int NWG = X_NWG, CW = BQ / NWG, NC = CW / 32;  // warpgroups; rows of each, in chunks of 32
+constexpr int NTHREADS = 64 + 128 * NWG;
 constexpr uint32_t HALF = BM * 64 * 2;  // 128 rows x 64 columns
-constexpr uint32_t kS = 0, kP = 128;
 
 template <int DH>
 struct Cols {
-  static constexpr bool kInPlace = DH == 128;
-  static constexpr uint32_t dK = kInPlace ? 256 : 384, dV = dK + DH;
-  // Operand K step kk (16 rows): its own area, or on the scores of the
+  static constexpr bool kOwn = DH == 64;  // the operands have columns of their own
+  static constexpr uint32_t S = 0, dP = 128, dK = kOwn ? 384 : 256, dV = dK + DH;
+  // Operand K step kk (16 rows): in its own area, or on the scores of the
   // warpgroup that wrote it.
-  static __device__ __forceinline__ uint32_t p(int kk) {
-    return kInPlace ? kS + 64 * (kk >> 2) + 8 * (kk & 3) : 256 + 8 * kk;
+  static __device__ __forceinline__ constexpr uint32_t p(int kk) {
+    return kOwn ? 256 + 8 * kk : S + CW * (kk / (CW / 16)) + 8 * (kk % (CW / 16));
   }
-  static __device__ __forceinline__ uint32_t ds(int kk) {
-    return kInPlace ? kP + 64 * (kk >> 2) + 8 * (kk & 3) : 320 + 8 * kk;
+  static __device__ __forceinline__ constexpr uint32_t ds(int kk) {
+    return kOwn ? 320 + 8 * kk : dP + CW * (kk / (CW / 16)) + 8 * (kk % (CW / 16));
   }
   static_assert(dV + DH <= 512, "TMEM columns");
 };
@@ -52,11 +61,14 @@ struct Slot {
 template <int DH>
 struct SmemK {
   static constexpr int NH = DH / 64;
-  static constexpr int NST = DH == 64 ? 5 : 2;
+  static constexpr bool kFold = DH == 64;  // row scalars in the score products
+  static constexpr int NST = DH == 64 ? 4 : 2;
   alignas(1024) uint8_t k[NH][HALF];
   alignas(1024) uint8_t v[NH][HALF];
   alignas(1024) uint8_t q[NST][NH][HALF];
   alignas(1024) uint8_t go[NST][NH][HALF];  // dO
+  alignas(1024) uint8_t ex[kFold ? NST : 1][kFold ? BQ * kExRow : 16];
+  alignas(128) uint8_t ones[kFold ? 2 : 1][kFold ? BM * kExRow : 16];  // of L and of D
   alignas(16) float l2[NST][BQ];
   alignas(16) float dd[NST][BQ];
   alignas(16) int4 info[NST][BQ];
@@ -64,14 +76,131 @@ struct SmemK {
   uint64_t bar_kv;
   uint64_t q_full[NST], q_empty[NST];  // Q, the row state and the slot
   uint64_t o_full[NST], o_empty[NST];  // dO
-  uint64_t s_full, s_free;
-  uint64_t p_full, p_free;
-  uint64_t w_ready, w_free;   // P^T written (8 warps) / read by dV
-  uint64_t ds_ready, ds_free;  // dS^T written (8 warps) / read by dK
+  uint64_t s_full, s_free;  // S^T of a tile is complete / d = 64: read
+  uint64_t p_full, p_free;  // the same for dP^T
+  uint64_t w_ready;         // d = 128: P^T written
+  uint64_t ds_ready;        // dS^T (d = 64: and P^T) written
+  uint64_t op_free;         // d = 64: both read by dV and dK
   uint64_t out_full;
   uint32_t tmem_base;
   int abort_flag;
 };
+
+// 32 rows of one key: P as bf16 pairs, and P (1 - tanh^2) in place of the
+// raw scores.
+template <bool CAP, bool BIAS, bool MASKED>
+__device__ __forceinline__ void weights(const Score<CAP, BIAS>& score, uint32_t (&s)[2][16],
+                                        const float* l2s, const int4* info, int key,
+                                        uint32_t seen, uint32_t (&pk)[2][8]) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      const float4 l2 = *reinterpret_cast<const float4*>(l2s + 16 * q + e);
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        const int i = 16 * q + e + k;
+        float2 x = f2(s[q][e + k], s[q][e + k + 1]);
+        const float2 nl = k == 0 ? make_float2(-l2.x, -l2.y) : make_float2(-l2.z, -l2.w);
+        float2 t;
+        if (CAP) {
+          x = make_float2(score.half_gap(x.x), score.half_gap(x.y));
+          t = ffma2(x, make_float2(-2.f * score.c2, -2.f * score.c2),
+                    fadd2(nl, make_float2(score.c2, score.c2)));
+        } else {
+          t = ffma2(x, make_float2(score.c1, score.c1), nl);
+        }
+        if (BIAS) {
+          const int4 a = info[i], b = info[i + 1];
+          t.x = fmaf(-__int_as_float(a.w), fabsf(static_cast<float>(key - a.z)), t.x);
+          t.y = fmaf(-__int_as_float(b.w), fabsf(static_cast<float>(key - b.z)), t.y);
+        }
+        float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+        if (MASKED) {
+          if (!(seen >> i & 1)) p.x = 0.f;
+          if (!(seen >> (i + 1) & 1)) p.y = 0.f;
+        }
+        pk[q][(e + k) >> 1] = pack_bf16x2(p.x, p.y);
+        if (CAP)  // 1 - tanh^2 = 4 r (1 - r)
+          p = fmul2(fmul2(p, fmul2(x, make_float2(4.f, 4.f))),
+                    fadd2(make_float2(1.f, 1.f), make_float2(-x.x, -x.y)));
+        s[q][e + k] = __float_as_uint(p.x);
+        s[q][e + k + 1] = __float_as_uint(p.y);
+      }
+    }
+}
+
+// P and dS of 32 rows of one key in one pass, so that the exponentials (MUFU)
+// of some rows run beside the multiplications of others.  s holds S^T - L / tau
+// (capped: S^T), x holds dP^T - D.
+template <bool CAP, bool BIAS, bool MASKED>
+__device__ __forceinline__ void both(const Score<CAP, BIAS>& score, const uint32_t (&s)[2][16],
+                                     const uint32_t (&x)[2][16], const float* l2s,
+                                     const int4* info, int key, uint32_t seen,
+                                     uint32_t (&pk)[2][8], uint32_t (&o)[2][8]) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      float4 l2 = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (CAP) l2 = *reinterpret_cast<const float4*>(l2s + 16 * q + e);
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        const int i = 16 * q + e + k;
+        float2 z = f2(s[q][e + k], s[q][e + k + 1]);
+        float2 t;
+        if (CAP) {
+          const float2 nl = k == 0 ? make_float2(-l2.x, -l2.y) : make_float2(-l2.z, -l2.w);
+          z = make_float2(score.half_gap(z.x), score.half_gap(z.y));
+          t = ffma2(z, make_float2(-2.f * score.c2, -2.f * score.c2),
+                    fadd2(nl, make_float2(score.c2, score.c2)));
+        } else {
+          t = fmul2(z, make_float2(score.c1, score.c1));
+        }
+        if (BIAS) {
+          const int4 a = info[i], b = info[i + 1];
+          t.x = fmaf(-__int_as_float(a.w), fabsf(static_cast<float>(key - a.z)), t.x);
+          t.y = fmaf(-__int_as_float(b.w), fabsf(static_cast<float>(key - b.z)), t.y);
+        }
+        float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+        float2 ds = f2(x[q][e + k], x[q][e + k + 1]);
+        if (CAP)  // 1 - tanh^2 = 4 r (1 - r)
+          ds = fmul2(fmul2(ds, fmul2(z, make_float2(4.f, 4.f))),
+                     fadd2(make_float2(1.f, 1.f), make_float2(-z.x, -z.y)));
+        ds = fmul2(p, ds);
+        if (MASKED) {  // S and dP of a row that sees nothing may be NaN
+          if (!(seen >> i & 1)) p.x = ds.x = 0.f;
+          if (!(seen >> (i + 1) & 1)) p.y = ds.y = 0.f;
+        }
+        pk[q][(e + k) >> 1] = pack_bf16x2(p.x, p.y);
+        o[q][(e + k) >> 1] = pack_bf16x2(ds.x, ds.y);
+      }
+    }
+}
+
+// dS = P (dP - D) of 32 rows of one key as bf16 pairs.
+template <bool MASKED>
+__device__ __forceinline__ void grads(const uint32_t (&p)[2][16], const uint32_t (&x)[2][16],
+                                      const float* dds, uint32_t seen, uint32_t (&o)[2][8]) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      const float4 dd = *reinterpret_cast<const float4*>(dds + 16 * q + e);
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        const int i = 16 * q + e + k;
+        const float2 nd = k == 0 ? make_float2(-dd.x, -dd.y) : make_float2(-dd.z, -dd.w);
+        float2 ds = fmul2(f2(p[q][e + k], p[q][e + k + 1]),
+                          fadd2(f2(x[q][e + k], x[q][e + k + 1]), nd));
+        if (MASKED) {  // dP of a row that sees nothing may be NaN
+          if (!(seen >> i & 1)) ds.x = 0.f;
+          if (!(seen >> (i + 1) & 1)) ds.y = 0.f;
+        }
+        o[q][(e + k) >> 1] = pack_bf16x2(ds.x, ds.y);
+      }
+    }
+}
 
 template <int DH, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(NTHREADS, 1)
@@ -100,17 +229,26 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     mbar_init(&sm.s_full, 1);
     mbar_init(&sm.p_full, 1);
-    mbar_init(&sm.w_free, 1);
-    mbar_init(&sm.ds_free, 1);
+    mbar_init(&sm.op_free, 1);
+    mbar_init(&sm.s_free, 4 * NWG);
+    mbar_init(&sm.p_free, 4 * NWG);
+    mbar_init(&sm.w_ready, 4 * NWG);
+    mbar_init(&sm.ds_ready, 4 * NWG);
     mbar_init(&sm.out_full, 1);
-    mbar_init(&sm.s_free, 8);
-    mbar_init(&sm.p_free, 8);
-    mbar_init(&sm.w_ready, 8);
-    mbar_init(&sm.ds_ready, 8);
     sm.abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+  if (Smem::kFold && threadIdx.x >= 64 && threadIdx.x < 64 + 2 * BM) {
+    // Ones in columns 0 - 2 (L) and 3 - 5 (D) of 16, one row a thread.
+    const int k = (threadIdx.x - 64) / BM, r = (threadIdx.x - 64) % BM;
+    const uint32_t one = 0x3F80u;  // bf16 1.0
+    uint8_t* row = sm.ones[k] + (r >> 3) * 256 + (r & 7) * 16;
+    *reinterpret_cast<uint4*>(row) = k == 0 ? make_uint4(one | (one << 16), one, 0u, 0u)
+                                            : make_uint4(0u, one << 16, one | (one << 16), 0u);
+    *reinterpret_cast<uint4*>(row + 128) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -143,20 +281,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int k = __ffs(hits) - 1, tile = t0 + k, s = nq % NST;
         const int in_lo = __shfl_sync(0xffffffffu, b.z, k);
         const int in_hi = __shfl_sync(0xffffffffu, b.w, k);
-        if (nq >= NST) ok = mbar_wait_warp(&sm.q_empty[s], ((nq / NST) - 1) & 1, abort_flag, err);
+        if (nq >= NST) ok = wait_warp(&sm.q_empty[s], ((nq / NST) - 1) & 1, abort_flag, err);
         if (!ok) break;
         if (lane == 0) {
           sm.slot[s] = Slot{tile, in_lo, in_hi};
-          mbar_expect_tx(&sm.q_full[s], NH * HALF + BQ * 24);
+          constexpr bool kL2 = !Smem::kFold || CAP;  // L is read by the warpgroups
+          mbar_expect_tx(&sm.q_full[s], NH * HALF + BQ * 16 + (kL2 ? BQ * 4 : 0) +
+                                            (Smem::kFold ? BQ * kExRow : BQ * 4));
           for (int h = 0; h < NH; ++h)
             tma_load_3d(sm.q[s][h], &mQ, &sm.q_full[s], 64 * h, tile * BQ, g);
           const size_t at = base + static_cast<size_t>(tile) * BQ;
-          bulk_load(sm.l2[s], st.l2 + at, BQ * 4, &sm.q_full[s]);
-          bulk_load(sm.dd[s], st.dd + at, BQ * 4, &sm.q_full[s]);
+          if (kL2) bulk_load(sm.l2[s], st.l2 + at, BQ * 4, &sm.q_full[s]);
+          if (Smem::kFold) bulk_load(sm.ex[s], st.ex + at * kExRow, BQ * kExRow, &sm.q_full[s]);
+          else bulk_load(sm.dd[s], st.dd + at, BQ * 4, &sm.q_full[s]);
           bulk_load(sm.info[s], st.info + at, BQ * 16, &sm.q_full[s]);
         }
         ++nq;
-        if (no >= NST) ok = mbar_wait_warp(&sm.o_empty[s], ((no / NST) - 1) & 1, abort_flag, err);
+        if (no >= NST) ok = wait_warp(&sm.o_empty[s], ((no / NST) - 1) & 1, abort_flag, err);
         if (!ok) break;
         if (lane == 0) {
           mbar_expect_tx(&sm.o_full[s], NH * HALF);
@@ -175,7 +316,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int n = no > NST ? no - NST : 0; n < no; ++n)
         drain_wait(&sm.o_full[n % NST], (n / NST) & 1);
       const int s = nq % NST;
-      if (ok && (nq < NST || mbar_wait(&sm.q_empty[s], ((nq / NST) - 1) & 1, abort_flag, err))) {
+      if (ok && (nq < NST || wait_one(&sm.q_empty[s], ((nq / NST) - 1) & 1, abort_flag, err))) {
         sm.slot[s].tile = -1;
         mbar_arrive(&sm.q_full[s]);
       }
@@ -191,6 +332,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint64_t dQm = smem_desc_sw128(smem_u32(sm.q[0][0]), HALF, 1024);  // MN-major
     const uint64_t dGm = smem_desc_sw128(smem_u32(sm.go[0][0]), HALF, 1024);
     constexpr uint64_t kTile = (uint64_t)(NH * HALF) >> 4;
+    const uint64_t dOnes = smem_desc_noswz(smem_u32(sm.ones[0]), 128, 256);
+    const uint64_t dEx = smem_desc_noswz(smem_u32(sm.ex[0]), 128, 256);
+    constexpr uint64_t kEx = (BQ * kExRow) >> 4;
     auto scores = [&](uint32_t col, uint64_t da, uint64_t db) {
 #pragma unroll
       for (int kk = 0; kk < DH / 16; ++kk) {
@@ -200,46 +344,64 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     };
     if (elect_one()) {
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const bool got = mbar_wait(bar, parity, abort_flag, err);
+        const bool got = wait_one(bar, parity, abort_flag, err);
         tc_fence_after();
         return got;
       };
       auto issue_s = [&](int n) {
-        scores(kS, dK, dQ + (n % NST) * kTile);
+        scores(C::S, dK, dQ + (n % NST) * kTile);
+        if (Smem::kFold && !CAP) mma_ss(tbase + C::S, dOnes, dEx + (n % NST) * kEx, idS, 1);
         mma_commit(&sm.s_full);
       };
-      auto issue_p = [&](int n) {  // also waits for dO
-        if (!wait(&sm.o_full[n % NST], (n / NST) & 1)) return false;
-        scores(kP, dV, dG + (n % NST) * kTile);
+      auto issue_p = [&](int n) {
+        scores(C::dP, dV, dG + (n % NST) * kTile);
+        if (Smem::kFold) mma_ss(tbase + C::dP, dOnes + kEx, dEx + (n % NST) * kEx, idS, 1);
         mma_commit(&sm.p_full);
-        return true;
       };
       auto issue_dv = [&](int n) {
         const uint64_t b = dGm + (n % NST) * kTile;
 #pragma unroll
         for (int c = 0; c < BQ / 16; ++c)
-          mma_ts(tbase + C::dV, tbase + C::p(c), b + ((16 * 128 * c) >> 4), idO, n > 0 || c > 0);
-        mma_commit(&sm.w_free);
+          mma_ts(tbase + C::dV, tbase + C::p(c), b + ((16 * 128 * c) >> 4), idO,
+                 n > 0 || c > 0);
         mma_commit(&sm.o_empty[n % NST]);
       };
       auto issue_dk = [&](int n) {
         const uint64_t b = dQm + (n % NST) * kTile;
 #pragma unroll
         for (int c = 0; c < BQ / 16; ++c)
-          mma_ts(tbase + C::dK, tbase + C::ds(c), b + ((16 * 128 * c) >> 4), idO, n > 0 || c > 0);
-        mma_commit(&sm.ds_free);
+          mma_ts(tbase + C::dK, tbase + C::ds(c), b + ((16 * 128 * c) >> 4), idO,
+                 n > 0 || c > 0);
+        mma_commit(&sm.op_free);
         mma_commit(&sm.q_empty[n % NST]);
       };
       bool ok = wait(&sm.bar_kv, 0) && wait(&sm.q_full[0], 0);
       bool more = ok && sm.slot[0].tile >= 0;
       if (more) {
         issue_s(0);
-        ok = issue_p(0);
+        ok = wait(&sm.o_full[0], 0);
+        if (ok) issue_p(0);
       }
       for (int n = 0; ok && more; ++n) {
         const int s1 = (n + 1) % NST;
         const uint32_t f1 = ((n + 1) / NST) & 1;
-        if (C::kInPlace) {
+        if (C::kOwn) {
+          ok = wait(&sm.q_full[s1], f1);
+          if (!ok) break;
+          more = sm.slot[s1].tile >= 0;
+          if (more) {
+            ok = wait(&sm.s_free, n & 1);
+            if (!ok) break;
+            issue_s(n + 1);
+            ok = wait(&sm.o_full[s1], f1) && wait(&sm.p_free, n & 1);
+            if (!ok) break;
+            issue_p(n + 1);
+          }
+          ok = wait(&sm.ds_ready, n & 1);
+          if (!ok) break;
+          issue_dv(n);
+          issue_dk(n);
+        } else {
           ok = wait(&sm.w_ready, n & 1);
           if (!ok) break;
           issue_dv(n);
@@ -250,24 +412,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           ok = wait(&sm.ds_ready, n & 1);
           if (!ok) break;
           issue_dk(n);
-          if (more) ok = issue_p(n + 1);
-        } else {
-          ok = wait(&sm.q_full[s1], f1);
-          if (!ok) break;
-          more = sm.slot[s1].tile >= 0;
           if (more) {
-            ok = wait(&sm.s_free, n & 1);
-            if (!ok) break;
-            issue_s(n + 1);
-            ok = wait(&sm.p_free, n & 1) && issue_p(n + 1);
-            if (!ok) break;
+            ok = wait(&sm.o_full[s1], f1);
+            if (ok) issue_p(n + 1);
           }
-          ok = wait(&sm.w_ready, n & 1);
-          if (!ok) break;
-          issue_dv(n);
-          ok = wait(&sm.ds_ready, n & 1);
-          if (!ok) break;
-          issue_dk(n);
         }
       }
       mma_commit(&sm.out_full);
@@ -276,148 +424,122 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   } else {
     const int wg = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-    const int key = j0 + r, c0 = 64 * wg;
+    const int key = j0 + r, c0 = CW * wg;
     const int key_end = min(j0 + BM, a.Nk);
     const Score<CAP, BIAS> score(a, 0.f);
     bool ok = true;
     int n = 0;
     for (;; ++n) {
       const int st = n % NST;
-      ok = mbar_wait_warp(&sm.q_full[st], (n / NST) & 1, abort_flag, err);
+      ok = wait_warp(&sm.q_full[st], (n / NST) & 1, abort_flag, err);
       if (!ok) break;
       const Slot slot = sm.slot[st];
       if (slot.tile < 0) break;
       const bool masked = slot.in_lo > j0 || slot.in_hi < key_end;
-      ok = mbar_wait_warp(&sm.s_full, n & 1, abort_flag, err);
+      ok = wait_warp(&sm.s_full, n & 1, abort_flag, err);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[4][16], pk[4][8];
+      uint32_t s[NC][2][16], x[2][16], pk[2][8], gk[2][8];
+      auto load = [&](uint32_t col, int c, uint32_t (&d)[2][16]) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld16(tbase + lane_off + kS + c0 + 16 * q, s[q]);
+        for (int q = 0; q < 2; ++q) tmem_ld16(tbase + lane_off + col + c0 + 32 * c + 16 * q, d[q]);
+      };
+      const float *l2 = &sm.l2[st][c0], *dd = &sm.dd[st][c0];
+      const int4* info = &sm.info[st][c0];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) load(C::S, c, s[c]);
       tmem_wait_ld();
-      if (!C::kInPlace) {
+      if (C::kOwn) {
         tc_fence_before();
         warp_arrive(&sm.s_free);
       }
-      unsigned long long seen = ~0ull;  // masked tiles: which of the 64 rows see this key
-      if (masked) {
-        seen = 0;
-        for (int i = 0; i < 64; ++i) {
-          const int4 in = sm.info[st][c0 + i];
-          if (key >= in.x && key < in.y) seen |= 1ull << i;
-        }
-      }
+      uint32_t seen[NC];  // masked tiles: which rows see this key
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const float4 l2 = *reinterpret_cast<const float4*>(&sm.l2[st][c0 + 16 * q + e]);
-#pragma unroll
-          for (int k = 0; k < 4; k += 2) {
-            float2 x = f2(s[q][e + k], s[q][e + k + 1]);
-            const float2 nl = k == 0 ? make_float2(-l2.x, -l2.y) : make_float2(-l2.z, -l2.w);
-            float2 t;
-            if (CAP) {
-              x = make_float2(score.half_gap(x.x), score.half_gap(x.y));
-              t = ffma2(x, make_float2(-2.f * score.c2, -2.f * score.c2),
-                        fadd2(nl, make_float2(score.c2, score.c2)));
-            } else {
-              t = ffma2(x, make_float2(score.c1, score.c1), nl);
-            }
-            if (BIAS) {
-              const int4 i0 = sm.info[st][c0 + 16 * q + e + k];
-              const int4 i1 = sm.info[st][c0 + 16 * q + e + k + 1];
-              t.x = fmaf(-__int_as_float(i0.w), fabsf(static_cast<float>(key - i0.z)), t.x);
-              t.y = fmaf(-__int_as_float(i1.w), fabsf(static_cast<float>(key - i1.z)), t.y);
-            }
-            float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-            if (masked) {
-              const int i = 16 * q + e + k;
-              if (!(seen >> i & 1)) p.x = 0.f;
-              if (!(seen >> (i + 1) & 1)) p.y = 0.f;
-            }
-            pk[q][(e + k) >> 1] = pack_bf16x2(p.x, p.y);
-            if (CAP)  // 1 - tanh^2 = 4 r (1 - r)
-              p = fmul2(fmul2(p, fmul2(x, make_float2(4.f, 4.f))),
-                        fadd2(make_float2(1.f, 1.f), make_float2(-x.x, -x.y)));
-            s[q][e + k] = __float_as_uint(p.x);
-            s[q][e + k + 1] = __float_as_uint(p.y);
+      for (int c = 0; c < NC; ++c) {
+        seen[c] = ~0u;
+        if (masked) {
+          seen[c] = 0;
+          for (int i = 0; i < 32; ++i) {
+            const int2 in = *reinterpret_cast<const int2*>(&info[32 * c + i]);
+            if (key >= in.x && key < in.y) seen[c] |= 1u << i;
           }
         }
-      if (!C::kInPlace && n > 0) {
-        ok = mbar_wait_warp(&sm.w_free, (n - 1) & 1, abort_flag, err);
-        if (!ok) break;
-        tc_fence_after();
       }
+      if (!C::kOwn) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_st8(tbase + lane_off + C::p(4 * wg + q), pk[q]);
-      if (slot.in_lo == INT_MAX) {
-        // Rows that see nothing meet P = dS = 0: make Q and dO 0 there, once
-        // both score products have read them.
-        ok = mbar_wait_warp(&sm.p_full, n & 1, abort_flag, err);
-        if (!ok) break;
-        if (sm.info[st][r].y == 0) zero_row<NH, HALF>(wg == 0 ? sm.q[st] : sm.go[st], r);
-        fence_proxy_async_smem();
-        // dV(n) reads rows that the other warpgroup zeroes, too: it waits for
-        // both warpgroups' arrivals below.
+        for (int c = 0; c < NC; ++c) {
+          if (masked)
+            weights<CAP, BIAS, true>(score, s[c], l2 + 32 * c, info + 32 * c, key, seen[c], pk);
+          else
+            weights<CAP, BIAS, false>(score, s[c], l2 + 32 * c, info + 32 * c, key, seen[c], pk);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            tmem_st8(tbase + lane_off + C::p((CW / 16) * wg + 2 * c + q), pk[q]);
+        }
+        if (slot.in_lo != INT_MAX) {
+          tmem_wait_st();
+          tc_fence_before();
+          warp_arrive(&sm.w_ready);
+        }
       }
-      tmem_wait_st();
-      tc_fence_before();
-      warp_arrive(&sm.w_ready);
-      ok = mbar_wait_warp(&sm.p_full, n & 1, abort_flag, err);
+      ok = wait_warp(&sm.p_full, n & 1, abort_flag, err);
       if (!ok) break;
       tc_fence_after();
-      // dP in two halves: all of it beside the weights would not fit the registers.
+      if (slot.in_lo == INT_MAX) {
+        // Rows that see nothing meet P = dS = 0: make Q and dO 0 there, now
+        // that both score products have read them; dV(n) and dK(n) wait for
+        // the arrivals of all warpgroups below, so they find every zero.
+        if (wg < 2 && sm.info[st][r].y == 0)
+          zero_row<NH, HALF>(wg == 0 ? sm.q[st] : sm.go[st], r);
+        fence_proxy_async_smem();
+        if (!C::kOwn) {
+          tmem_wait_st();
+          tc_fence_before();
+          warp_arrive(&sm.w_ready);
+        }
+      }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t x[2][16];
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          tmem_ld16(tbase + lane_off + kP + c0 + 32 * h + 16 * q, x[q]);
+      for (int c = 0; c < NC; ++c) {
+        load(C::dP, c, x);
         tmem_wait_ld();
-        if (!C::kInPlace && h == 1) {
+        if (C::kOwn && c == NC - 1) {
           tc_fence_before();
           warp_arrive(&sm.p_free);
         }
+        if (C::kOwn) {
+          if (masked)
+            both<CAP, BIAS, true>(score, s[c], x, l2 + 32 * c, info + 32 * c, key, seen[c], pk, gk);
+          else
+            both<CAP, BIAS, false>(score, s[c], x, l2 + 32 * c, info + 32 * c, key, seen[c], pk, gk);
+          if (c == 0 && n > 0) {
+            ok = wait_warp(&sm.op_free, (n - 1) & 1, abort_flag, err);
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            tmem_st8(tbase + lane_off + C::p((CW / 16) * wg + 2 * c + q), pk[q]);
+        } else {
+          if (masked) grads<true>(s[c], x, dd + 32 * c, seen[c], gk);
+          else grads<false>(s[c], x, dd + 32 * c, seen[c], gk);
+        }
 #pragma unroll
         for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const int i0 = 32 * h + 16 * q + e;
-            const float4 dd = *reinterpret_cast<const float4*>(&sm.dd[st][c0 + i0]);
-#pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-              const float2 nd = k == 0 ? make_float2(-dd.x, -dd.y) : make_float2(-dd.z, -dd.w);
-              float2 ds = fmul2(f2(s[2 * h + q][e + k], s[2 * h + q][e + k + 1]),
-                                fadd2(f2(x[q][e + k], x[q][e + k + 1]), nd));
-              if (masked) {  // dP of a row that sees nothing may be NaN
-                if (!(seen >> (i0 + k) & 1)) ds.x = 0.f;
-                if (!(seen >> (i0 + k + 1) & 1)) ds.y = 0.f;
-              }
-              pk[2 * h + q][(e + k) >> 1] = pack_bf16x2(ds.x, ds.y);
-            }
-          }
+          tmem_st8(tbase + lane_off + C::ds((CW / 16) * wg + 2 * c + q), gk[q]);
       }
-      if (!C::kInPlace && n > 0) {
-        ok = mbar_wait_warp(&sm.ds_free, (n - 1) & 1, abort_flag, err);
-        if (!ok) break;
-        tc_fence_after();
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_st8(tbase + lane_off + C::ds(4 * wg + q), pk[q]);
+      if (!ok) break;
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(&sm.ds_ready);
     }
-    ok = mbar_wait_warp(&sm.out_full, 0, abort_flag, err) && ok;
+    ok = wait_warp(&sm.out_full, 0, abort_flag, err) && ok;
     ok = __all_sync(0xffffffffu, ok && !*abort_flag);
     tc_fence_after();
     constexpr uint32_t kStage = BM * (DH * 2 + 16);
     static_assert(kStage <= sizeof(sm.q) && kStage <= sizeof(sm.go), "staging fits in the ring");
     const size_t at = (static_cast<size_t>(g) * a.Nk + j0) * DH;
-    store_block<DH>(tbase + lane_off + C::dK, a.tau, n == 0, &sm.q[0][0][0], wg, r,
+    store_block<DH, NWG>(tbase + lane_off + C::dK, a.tau, n == 0, &sm.q[0][0][0], wg, r,
                     threadIdx.x - 64, key_end - j0, ok, static_cast<__nv_bfloat16*>(a.dK) + at);
-    store_block<DH>(tbase + lane_off + C::dV, 1.f, n == 0, &sm.go[0][0][0], wg, r,
+    store_block<DH, NWG>(tbase + lane_off + C::dV, 1.f, n == 0, &sm.go[0][0][0], wg, r,
                     threadIdx.x - 64, key_end - j0, ok, static_cast<__nv_bfloat16*>(a.dV) + at);
   }
 

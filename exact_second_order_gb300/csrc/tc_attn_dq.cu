@@ -4,15 +4,22 @@
 //   S = Q K^T, dP = dO V^T;  P = exp2(score(S) - L log2 e),
 //   dS = P (dP - D) (1 - tanh^2),  dQ += dS K;  dQ = tau dQ at the end.
 //
-// 320 threads: warp 0 TMA, warp 1 TMEM allocation and MMA issue, warps 2-5 /
-// 6-9 elementwise warpgroups that take columns 0-63 / 64-127 of every tile.
-// S and dP are handed back as soon as they are in registers, and dS (bf16)
-// has columns of its own, so the score products of tile t + 1 run while the
-// warpgroups work on tile t.  Per 128 x 128 tile the tensor pipe needs
-// (tcgen05 issue costs) 868 cycles at d = 64 and 1536 at d = 128.
+// 576 threads: warp 0 TMA, warp 1 TMEM allocation and MMA issue, then four
+// elementwise warpgroups that take 32 columns of every tile each (two of 64
+// columns left the schedulers idle 60% of the time, waiting on latencies).
+// S has two buffers, and dS (bf16) of a tile lies on the scores it came from,
+// so S(t + 1) is issued right behind dQ(t - 1); dP has one, handed back as soon
+// as it is in registers.  So the score products of tile t + 1 run while the
+// warpgroups work on tile t.  Hand-offs are few, because a wait costs a hundred
+// cycles or more even when the phase has completed.  Per 128 x 128 tile the
+// tensor pipe needs (tcgen05 issue costs) 868 cycles at d = 64 and 1536 at
+// d = 128.
 // K and V have rings of their own: a V tile is free after dP, a K tile only
 // after dQ.
-// TMEM: S [0,128), dP [128,256), dS operand [256,320), dQ from 320 on.
+// TMEM: S [0,128) and [128,256), dP [256,384), dQ from 384 on; at d = 64 also
+// Q and dO as A operands ([448,480) and [480,512)): read from shared memory,
+// they and the key tiles and the TMA writes need as many cycles of its 128
+// bytes as the MMAs take.
 #include "tc_attn.cuh"
 
 namespace flashbob {
@@ -21,9 +28,19 @@ using namespace tc;
 using namespace attn;
 
 constexpr int BM = kTcRows, BN = 128;
-constexpr int NTHREADS = 320;
+#ifndef X_NWG
+#define X_NWG 4
+#endif
+constexpr int NWG = X_NWG, CW = BN / NWG, NC = CW / 32;  // warpgroups; columns of each, in chunks of 32
+constexpr int NTHREADS = 64 + 128 * NWG;
 constexpr uint32_t HALF = BM * 64 * 2;  // 128 rows x 64 columns
-constexpr uint32_t kS = 0, kP = 128, kOp = 256, kAcc = 320;
+constexpr uint32_t kP = 256, kAcc = 384, kQA = 448, kGA = 480;
+__device__ __forceinline__ constexpr uint32_t s_col(int t) { return 128 * (t & 1); }
+// K step c (16 keys) of tile t's dS operand, on the scores of the warpgroup
+// that wrote it.
+__device__ __forceinline__ constexpr uint32_t op_col(int t, int c) {
+  return s_col(t) + CW * (c / (CW / 16)) + 8 * (c % (CW / 16));
+}
 
 template <int DH>
 struct SmemQ {
@@ -34,32 +51,63 @@ struct SmemQ {
   alignas(1024) uint8_t k[NK][NH][HALF];
   alignas(1024) uint8_t v[NV][NH][HALF];
   int hull[4][4];
-  uint64_t bar_q;
+  uint64_t bar_q, a_ready;    // Q and dO in shared memory / in TMEM (8 warps)
   uint64_t k_full[NK], k_empty[NK];
   uint64_t v_full[NV], v_empty[NV];
-  uint64_t s_full, s_free;    // S of a tile is complete / read (8 warps)
-  uint64_t p_full, p_free;    // the same for dP
-  uint64_t op_ready, op_free;  // dS written (8 warps) / read by the MMAs
+  uint64_t s_full[2];         // S of a tile is complete
+  uint64_t p_full, p_free;    // dP of a tile is complete / read
+  uint64_t op_ready[2];       // dS written
   uint64_t out_full;
   uint32_t tmem_base;
   int abort_flag;
 };
 
-// Weights of 64 columns in place of the raw scores, times 1 - tanh^2.
+// dS of 32 columns as bf16 pairs from the raw scores s and dP x.  One pass
+// over both, so that the exponentials (MUFU) of some columns run beside the
+// multiplications of others.
 template <bool CAP, bool BIAS, bool MASKED>
-__device__ __forceinline__ void weights(const Score<CAP, BIAS>& sc, uint32_t (&s)[4][16], int jbase,
-                                        int lo, int hi, float dist, float l2) {
+__device__ __forceinline__ void grads(const Score<CAP, BIAS>& sc, const uint32_t (&s)[2][16],
+                                      const uint32_t (&x)[2][16], int jbase, int lo, int hi,
+                                      float dist, float l2, float dd, uint32_t (&o)[2][8]) {
+  const float2 nd = make_float2(-dd, -dd);
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
+  for (int q = 0; q < 2; ++q)
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
-      float2 x = f2(s[q][e], s[q][e + 1]);
-      if (CAP) x = make_float2(sc.half_gap(x.x), sc.half_gap(x.y));
-      const float2 t = sc.from(x, dist + (16 * q + e), l2, sc.slope2);
+      float2 z = f2(s[q][e], s[q][e + 1]);
+      if (CAP) z = make_float2(sc.half_gap(z.x), sc.half_gap(z.y));
+      const float2 t = sc.from(z, dist + (16 * q + e), l2, sc.slope2);
+      const float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+      float2 ds = fadd2(f2(x[q][e], x[q][e + 1]), nd);
+      if (CAP)  // 1 - tanh^2 = 4 r (1 - r)
+        ds = fmul2(fmul2(ds, fmul2(z, make_float2(4.f, 4.f))),
+                   fadd2(make_float2(1.f, 1.f), make_float2(-z.x, -z.y)));
+      ds = fmul2(p, ds);
+      if (MASKED) {  // S and dP of a hidden key may be NaN
+        const int j = jbase + 16 * q + e;
+        if (j < lo || j >= hi) ds.x = 0.f;
+        if (j + 1 < lo || j + 1 >= hi) ds.y = 0.f;
+      }
+      o[q][e >> 1] = pack_bf16x2(ds.x, ds.y);
+    }
+}
+
+// The same in two steps: P (1 - tanh^2) of 32 columns in place of the raw
+// scores, then dS.
+template <bool CAP, bool BIAS, bool MASKED>
+__device__ __forceinline__ void weights(const Score<CAP, BIAS>& sc, uint32_t (&s)[2][16], int jbase,
+                                        int lo, int hi, float dist, float l2) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      float2 z = f2(s[q][e], s[q][e + 1]);
+      if (CAP) z = make_float2(sc.half_gap(z.x), sc.half_gap(z.y));
+      const float2 t = sc.from(z, dist + (16 * q + e), l2, sc.slope2);
       float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-      if (CAP)  // 4 r (1 - r)
-        p = fmul2(fmul2(p, fmul2(x, make_float2(4.f, 4.f))),
-                  fadd2(make_float2(1.f, 1.f), make_float2(-x.x, -x.y)));
+      if (CAP)
+        p = fmul2(fmul2(p, fmul2(z, make_float2(4.f, 4.f))),
+                  fadd2(make_float2(1.f, 1.f), make_float2(-z.x, -z.y)));
       if (MASKED) {
         const int j = jbase + 16 * q + e;
         if (j < lo || j >= hi) p.x = 0.f;
@@ -67,6 +115,23 @@ __device__ __forceinline__ void weights(const Score<CAP, BIAS>& sc, uint32_t (&s
       }
       s[q][e] = __float_as_uint(p.x);
       s[q][e + 1] = __float_as_uint(p.y);
+    }
+}
+template <bool MASKED>
+__device__ __forceinline__ void finish(const uint32_t (&s)[2][16], const uint32_t (&x)[2][16],
+                                       int jbase, int lo, int hi, float dd, uint32_t (&o)[2][8]) {
+  const float2 nd = make_float2(-dd, -dd);
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      float2 ds = fmul2(f2(s[q][e], s[q][e + 1]), fadd2(f2(x[q][e], x[q][e + 1]), nd));
+      if (MASKED) {
+        const int j = jbase + 16 * q + e;
+        if (j < lo || j >= hi) ds.x = 0.f;
+        if (j + 1 < lo || j + 1 >= hi) ds.y = 0.f;
+      }
+      o[q][e >> 1] = pack_bf16x2(ds.x, ds.y);
     }
 }
 
@@ -89,15 +154,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(&sm.bar_q, 1);
+    mbar_init(&sm.a_ready, 8);
     for (int s = 0; s < NK; ++s) mbar_init(&sm.k_full[s], 1), mbar_init(&sm.k_empty[s], 1);
     for (int s = 0; s < NV; ++s) mbar_init(&sm.v_full[s], 1), mbar_init(&sm.v_empty[s], 1);
-    mbar_init(&sm.s_full, 1);
     mbar_init(&sm.p_full, 1);
-    mbar_init(&sm.op_free, 1);
+    mbar_init(&sm.p_free, 4 * NWG);
+    for (int b = 0; b < 2; ++b) mbar_init(&sm.s_full[b], 1), mbar_init(&sm.op_ready[b], 4 * NWG);
     mbar_init(&sm.out_full, 1);
-    mbar_init(&sm.s_free, 8);
-    mbar_init(&sm.p_free, 8);
-    mbar_init(&sm.op_ready, 8);
     sm.abort_flag = 0;
     fence_barrier_init();
   }
@@ -133,12 +196,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       int nk = 0, nv = 0;
       for (int t = 0; t < T; ++t) {
         const int sk = t % NK, sv = t % NV;
-        if (t >= NK && !mbar_wait(&sm.k_empty[sk], ((t / NK) - 1) & 1, abort_flag, err)) break;
+        if (t >= NK && !wait_one(&sm.k_empty[sk], ((t / NK) - 1) & 1, abort_flag, err)) break;
         mbar_expect_tx(&sm.k_full[sk], NH * HALF);
         for (int h = 0; h < NH; ++h)
           tma_load_3d(sm.k[sk][h], &mK, &sm.k_full[sk], 64 * h, (tb + t) * BN, g);
         nk = t + 1;
-        if (t >= NV && !mbar_wait(&sm.v_empty[sv], ((t / NV) - 1) & 1, abort_flag, err)) break;
+        if (t >= NV && !wait_one(&sm.v_empty[sv], ((t / NV) - 1) & 1, abort_flag, err)) break;
         mbar_expect_tx(&sm.v_full[sv], NH * HALF);
         for (int h = 0; h < NH; ++h)
           tma_load_3d(sm.v[sv][h], &mV, &sm.v_full[sv], 64 * h, (tb + t) * BN, g);
@@ -157,46 +220,56 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint64_t dV = smem_desc_sw128(smem_u32(sm.v[0][0]), 16, 1024);
     const uint64_t dKm = smem_desc_sw128(smem_u32(sm.k[0][0]), HALF, 1024);  // MN-major
     constexpr uint64_t kTile = (uint64_t)(NH * HALF) >> 4;
-    auto scores = [&](uint32_t col, uint64_t da, uint64_t db) {
+    auto scores = [&](uint32_t col, uint64_t da, uint32_t ta, uint64_t db) {
 #pragma unroll
       for (int kk = 0; kk < DH / 16; ++kk) {
         const uint64_t o = ((kk >> 2) * HALF + 32 * (kk & 3)) >> 4;
-        mma_ss(tbase + col, da + o, db + o, idS, kk > 0);
+        if (DH == 64) mma_ts(tbase + col, tbase + ta + 8 * kk, db + o, idS, kk > 0);
+        else mma_ss(tbase + col, da + o, db + o, idS, kk > 0);
       }
     };
     if (elect_one()) {
-      bool ok = mbar_wait(&sm.bar_q, 0, abort_flag, err);
+      bool ok = wait_one(DH == 64 ? &sm.a_ready : &sm.bar_q, 0, abort_flag, err);
       auto issue_s = [&](int t) {
-        if (!mbar_wait(&sm.k_full[t % NK], (t / NK) & 1, abort_flag, err)) return false;
         tc_fence_after();
-        scores(kS, dQ, dK + (t % NK) * kTile);
-        mma_commit(&sm.s_full);
-        return true;
+        scores(s_col(t), dQ, kQA, dK + (t % NK) * kTile);
+        mma_commit(&sm.s_full[t & 1]);
       };
       auto issue_p = [&](int t) {
-        if (!mbar_wait(&sm.v_full[t % NV], (t / NV) & 1, abort_flag, err)) return false;
         tc_fence_after();
-        scores(kP, dG, dV + (t % NV) * kTile);
+        scores(kP, dG, kGA, dV + (t % NV) * kTile);
         mma_commit(&sm.p_full);
         mma_commit(&sm.v_empty[t % NV]);
-        return true;
       };
-      if (ok && T > 0) ok = issue_s(0) && issue_p(0);
+      if (ok && T > 0) {
+        ok = wait_one(&sm.k_full[0], 0, abort_flag, err) &&
+             wait_one(&sm.v_full[0], 0, abort_flag, err);
+        if (ok) {
+          issue_s(0);
+          issue_p(0);
+        }
+      }
       for (int t = 0; ok && t < T; ++t) {
         if (t + 1 < T) {
-          ok = mbar_wait(&sm.s_free, t & 1, abort_flag, err) && issue_s(t + 1) &&
-               mbar_wait(&sm.p_free, t & 1, abort_flag, err) && issue_p(t + 1);
+          // Tile t - 1's dS, which lies on this buffer, was waited for and its
+          // dQ issued: the pipe runs in order.
+          const int n = t + 1;
+          ok = wait_one(&sm.k_full[n % NK], (n / NK) & 1, abort_flag, err);
           if (!ok) break;
+          issue_s(n);
+          ok = wait_one(&sm.v_full[n % NV], (n / NV) & 1, abort_flag, err) &&
+               wait_one(&sm.p_free, t & 1, abort_flag, err);
+          if (!ok) break;
+          issue_p(n);
         }
-        ok = mbar_wait(&sm.op_ready, t & 1, abort_flag, err);
+        ok = wait_one(&sm.op_ready[t & 1], (t >> 1) & 1, abort_flag, err);
         if (!ok) break;
         tc_fence_after();
         const uint64_t dk = dKm + (t % NK) * kTile;
 #pragma unroll
         for (int c = 0; c < BN / 16; ++c)
-          mma_ts(tbase + kAcc, tbase + kOp + 8 * c, dk + ((16 * 128 * c) >> 4), idO,
+          mma_ts(tbase + kAcc, tbase + op_col(t, c), dk + ((16 * 128 * c) >> 4), idO,
                  t > 0 || c > 0);
-        mma_commit(&sm.op_free);
         mma_commit(&sm.k_empty[t % NK]);
       }
       mma_commit(&sm.out_full);
@@ -207,74 +280,115 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int lo = gr.v.lo, hi = gr.v.hi;
     const Score<CAP, BIAS> score(a, gr.slope2);
     bool ok = true;
-    for (int t = 0; t < T; ++t) {
-      const int tile0 = (tb + t) * BN, col0 = tile0 + 64 * wg;
-      ok = mbar_wait_warp(&sm.s_full, t & 1, abort_flag, err);
-      if (!ok) break;
-      tc_fence_after();
-      const bool masked = col0 < hull.in_lo || col0 + 64 > hull.in_hi;
-      const float dist = BIAS ? static_cast<float>(col0 - gr.v.pos) : 0.f;
-      uint32_t s[4][16];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld16(tbase + lane_off + kS + 64 * wg + 16 * q, s[q]);
-      tmem_wait_ld();
-      tc_fence_before();
-      warp_arrive(&sm.s_free);
-      if (masked) weights<CAP, BIAS, true>(score, s, col0, lo, hi, dist, l2);
-      else weights<CAP, BIAS, false>(score, s, col0, lo, hi, dist, l2);
-      ok = mbar_wait_warp(&sm.p_full, t & 1, abort_flag, err);
-      if (!ok) break;
-      tc_fence_after();
-      // dP in two halves: all of it beside the weights would not fit the registers.
-      uint32_t pk[4][8];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t x[2][16];
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          tmem_ld16(tbase + lane_off + kP + 64 * wg + 32 * h + 16 * q, x[q]);
-        tmem_wait_ld();
-        if (h == 1) {
-          tc_fence_before();
-          warp_arrive(&sm.p_free);
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float2 ds = fmul2(f2(s[2 * h + q][e], s[2 * h + q][e + 1]),
-                              fadd2(f2(x[q][e], x[q][e + 1]), make_float2(-dd, -dd)));
-            if (masked) {  // dP of a hidden key may be NaN
-              const int j = col0 + 32 * h + 16 * q + e;
-              if (j < lo || j >= hi) ds.x = 0.f;
-              if (j + 1 < lo || j + 1 >= hi) ds.y = 0.f;
-            }
-            pk[2 * h + q][e >> 1] = pack_bf16x2(ds.x, ds.y);
-          }
-      }
-      if (t > 0) {
-        ok = mbar_wait_warp(&sm.op_free, (t - 1) & 1, abort_flag, err);
-        if (!ok) break;
-        tc_fence_after();
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        tmem_st8(tbase + lane_off + kOp + 32 * wg + 8 * q, pk[q]);
-      if (tile0 < hull.lo || tile0 + BN > hull.hi) {
-        // K rows that no row of the block sees meet dS = 0: make them 0 too.
-        if (wg == 0 && (tile0 + r < hull.lo || tile0 + r >= hull.hi))
-          zero_row<NH, HALF>(sm.k[t % NK], r);
-        fence_proxy_async_smem();
-      }
+    if (DH == 64 && wg < 2) {
+      ok = wait_warp(&sm.bar_q, 0, abort_flag, err);
+      row_to_tmem(wg ? sm.go[0] : sm.q[0], r, tbase + lane_off + (wg ? kGA : kQA));
       tmem_wait_st();
       tc_fence_before();
-      warp_arrive(&sm.op_ready);
+      warp_arrive(&sm.a_ready);
     }
-    ok = mbar_wait_warp(&sm.out_full, 0, abort_flag, err) && ok;
+    uint32_t s[NC][2][16], x[2][16], pk[2][8];
+    auto col_of = [&](int t, int c) { return (tb + t) * BN + CW * wg + 32 * c; };
+    auto masked_at = [&](int t) {
+      return col_of(t, 0) < hull.in_lo || col_of(t, NC) > hull.in_hi;
+    };
+    auto dist_at = [&](int t, int c) {
+      return BIAS ? static_cast<float>(col_of(t, c) - gr.v.pos) : 0.f;
+    };
+    auto load = [&](uint32_t col, int c, uint32_t (&d)[2][16]) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        tmem_ld16(tbase + lane_off + col + CW * wg + 32 * c + 16 * q, d[q]);
+    };
+    auto write = [&](int t, int c) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        tmem_st8(tbase + lane_off + op_col(t, (CW / 16) * wg + 2 * c + q), pk[q]);
+    };
+    auto written = [&](int t) {
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(&sm.op_ready[t & 1]);
+    };
+    if (wg < NWG / 2) {
+      // S and dP of a tile together.
+      for (int t = 0; t < T; ++t) {
+        ok = wait_both_warp(&sm.s_full[t & 1], (t >> 1) & 1, &sm.p_full, t & 1, abort_flag, err);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < NC; ++c) load(s_col(t), c, s[c]);
+        const bool masked = masked_at(t);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          load(kP, c, x);
+          tmem_wait_ld();
+          if (c == NC - 1) {
+            tc_fence_before();
+            warp_arrive(&sm.p_free);
+          }
+          if (masked)
+            grads<CAP, BIAS, true>(score, s[c], x, col_of(t, c), lo, hi, dist_at(t, c), l2, dd, pk);
+          else
+            grads<CAP, BIAS, false>(score, s[c], x, col_of(t, c), lo, hi, dist_at(t, c), l2, dd, pk);
+          write(t, c);
+        }
+        const int tile0 = (tb + t) * BN;
+        if (tile0 < hull.lo || tile0 + BN > hull.hi) {
+          // K rows that no row of the block sees meet dS = 0: make them 0 too.
+          if (wg == 0 && (tile0 + r < hull.lo || tile0 + r >= hull.hi))
+            zero_row<NH, HALF>(sm.k[t % NK], r);
+          fence_proxy_async_smem();
+        }
+        written(t);
+      }
+    } else {
+      // Half a tile ahead: the weights of tile t + 1 are formed behind dS of
+      // tile t.  So on every scheduler half of the warps use the MUFU pipe
+      // while the others load, multiply and store.
+      auto ahead = [&](int t) {
+        ok = wait_warp(&sm.s_full[t & 1], (t >> 1) & 1, abort_flag, err);
+        if (!ok) return;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < NC; ++c) load(s_col(t), c, s[c]);
+        tmem_wait_ld();
+        const bool masked = masked_at(t);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          if (masked)
+            weights<CAP, BIAS, true>(score, s[c], col_of(t, c), lo, hi, dist_at(t, c), l2);
+          else
+            weights<CAP, BIAS, false>(score, s[c], col_of(t, c), lo, hi, dist_at(t, c), l2);
+        }
+      };
+      if (T > 0) ahead(0);
+      for (int t = 0; ok && t < T; ++t) {
+        ok = wait_warp(&sm.p_full, t & 1, abort_flag, err);
+        if (!ok) break;
+        tc_fence_after();
+        const bool masked = masked_at(t);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          load(kP, c, x);
+          tmem_wait_ld();
+          if (c == NC - 1) {
+            tc_fence_before();
+            warp_arrive(&sm.p_free);
+          }
+          if (masked) finish<true>(s[c], x, col_of(t, c), lo, hi, dd, pk);
+          else finish<false>(s[c], x, col_of(t, c), lo, hi, dd, pk);
+          write(t, c);
+        }
+        written(t);
+        if (t + 1 < T) ahead(t + 1);
+      }
+    }
+    ok = wait_warp(&sm.out_full, 0, abort_flag, err) && ok;
     ok = __all_sync(0xffffffffu, ok && !*abort_flag);
     tc_fence_after();
     static_assert(BM * (DH * 2 + 16) <= sizeof(sm.k), "epilogue staging fits in the ring");
-    store_block<DH>(tbase + lane_off + kAcc, a.tau, T == 0, &sm.k[0][0][0], wg, r,
+    store_block<DH, NWG>(tbase + lane_off + kAcc, a.tau, T == 0, &sm.k[0][0][0], wg, r,
                     threadIdx.x - 64, min(BM, rows - row0), ok,
                     static_cast<__nv_bfloat16*>(a.dQ) +
                         (static_cast<size_t>(g) * rows + row0) * DH);

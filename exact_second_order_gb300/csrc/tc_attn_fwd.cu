@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       int issued = 0;
       for (int t = 0; t < T; ++t) {
         const int s = t % NST;
-        if (t >= NST && !mbar_wait(&sm.kv_empty[s], ((t / NST) - 1) & 1, abort_flag, err)) break;
+        if (t >= NST && !wait_one(&sm.kv_empty[s], ((t / NST) - 1) & 1, abort_flag, err)) break;
         mbar_expect_tx(&sm.kv_full[s], 2 * NH * HT);
         for (int h = 0; h < NH; ++h)
           tma_load_3d(sm.kv[s][0][h], &mK, &sm.kv_full[s], 64 * h, (tb + t) * BN, g);
@@ -230,21 +230,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (MT == 1 || (u & 1)) mma_commit(&sm.kv_empty[s]);
     };
     if (elect_one()) {
-      bool ok = mbar_wait(&sm.bar_q, 0, abort_flag, err);
+      bool ok = wait_one(&sm.bar_q, 0, abort_flag, err);
       tc_fence_after();
       for (int u = 0; ok && u < NBUF && u < U; ++u) {
-        ok = mbar_wait(&sm.kv_full[tile(u) % NST], (tile(u) / NST) & 1, abort_flag, err);
+        ok = wait_one(&sm.kv_full[tile(u) % NST], (tile(u) / NST) & 1, abort_flag, err);
         tc_fence_after();
         if (ok) issue_scores(u);
       }
       for (int u = 0; ok && u < U; ++u) {
-        ok = mbar_wait(&sm.op_ready[u % NBUF], (u / NBUF) & 1, abort_flag, err);
+        ok = wait_one(&sm.op_ready[u % NBUF], (u / NBUF) & 1, abort_flag, err);
         if (!ok) break;
         tc_fence_after();
         issue_pv(u);
         if (u + NBUF < U) {
           const int tn = tile(u + NBUF);
-          ok = mbar_wait(&sm.kv_full[tn % NST], (tn / NST) & 1, abort_flag, err);
+          ok = wait_one(&sm.kv_full[tn % NST], (tn / NST) & 1, abort_flag, err);
           if (!ok) break;
           tc_fence_after();
           issue_scores(u + NBUF);
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     int n = 0;  // units of this warpgroup
     for (int u = wg; u < U; u += 2, ++n) {
       const int col0 = (tb + (MT == 2 ? u >> 1 : u)) * BN;
-      ok = ok && mbar_wait_warp(&sm.sc_full[u % NBUF], (u / NBUF) & 1, abort_flag, err);
+      ok = ok && wait_warp(&sm.sc_full[u % NBUF], (u / NBUF) & 1, abort_flag, err);
       if (!ok) break;
       tc_fence_after();
       const uint32_t sc = tbase + lane_off + kScore + BN * (u % NBUF);
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         m = mt;
       }
       if (__any_sync(0xffffffffu, raise && factor < 1.f) && n > 0) {
-        ok = mbar_wait_warp(&sm.pv_done[wg], (n - 1) & 1, abort_flag, err);
+        ok = wait_warp(&sm.pv_done[wg], (n - 1) & 1, abort_flag, err);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       warp_arrive(&sm.op_ready[u % NBUF]);
     }
 
-    ok = mbar_wait_warp(&sm.out_full, 0, abort_flag, err) && ok;
+    ok = wait_warp(&sm.out_full, 0, abort_flag, err) && ok;
     ok = __all_sync(0xffffffffu, ok && !*abort_flag);
     tc_fence_after();
     // MT = 1: merge the warpgroups' (m, l, O~): m* = max, s_w = exp2(m_w - m*),
