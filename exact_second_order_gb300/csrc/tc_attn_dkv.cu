@@ -100,16 +100,10 @@ __device__ __forceinline__ void weights(const Score<CAP, BIAS>& score, uint32_t 
 #pragma unroll
       for (int k = 0; k < 4; k += 2) {
         const int i = 16 * q + e + k;
-        float2 x = f2(s[q][e + k], s[q][e + k + 1]);
+        const float2 x = f2(s[q][e + k], s[q][e + k + 1]);
         const float2 nl = k == 0 ? make_float2(-l2.x, -l2.y) : make_float2(-l2.z, -l2.w);
-        float2 t;
-        if (CAP) {
-          x = make_float2(score.half_gap(x.x), score.half_gap(x.y));
-          t = ffma2(x, make_float2(-2.f * score.c2, -2.f * score.c2),
-                    fadd2(nl, make_float2(score.c2, score.c2)));
-        } else {
-          t = ffma2(x, make_float2(score.c1, score.c1), nl);
-        }
+        const float c = CAP ? score.c2 : score.c1;
+        float2 t = ffma2(x, make_float2(c, c), nl);
         if (BIAS) {
           const int4 a = info[i], b = info[i + 1];
           t.x = fmaf(-__int_as_float(a.w), fabsf(static_cast<float>(key - a.z)), t.x);
@@ -121,9 +115,7 @@ __device__ __forceinline__ void weights(const Score<CAP, BIAS>& score, uint32_t 
           if (!(seen >> (i + 1) & 1)) p.y = 0.f;
         }
         pk[q][(e + k) >> 1] = pack_bf16x2(p.x, p.y);
-        if (CAP)  // 1 - tanh^2 = 4 r (1 - r)
-          p = fmul2(fmul2(p, fmul2(x, make_float2(4.f, 4.f))),
-                    fadd2(make_float2(1.f, 1.f), make_float2(-x.x, -x.y)));
+        p = score.damp(p, x);
         s[q][e + k] = __float_as_uint(p.x);
         s[q][e + k + 1] = __float_as_uint(p.y);
       }
@@ -132,7 +124,7 @@ __device__ __forceinline__ void weights(const Score<CAP, BIAS>& score, uint32_t 
 
 // P and dS of 32 rows of one key in one pass, so that the exponentials (MUFU)
 // of some rows run beside the multiplications of others.  s holds S^T - L / tau
-// (capped: S^T), x holds dP^T - D.
+// (capped: the tanh), x holds dP^T - D.
 template <bool CAP, bool BIAS, bool MASKED>
 __device__ __forceinline__ void both(const Score<CAP, BIAS>& score, const uint32_t (&s)[2][16],
                                      const uint32_t (&x)[2][16], const float* l2s,
@@ -147,13 +139,11 @@ __device__ __forceinline__ void both(const Score<CAP, BIAS>& score, const uint32
 #pragma unroll
       for (int k = 0; k < 4; k += 2) {
         const int i = 16 * q + e + k;
-        float2 z = f2(s[q][e + k], s[q][e + k + 1]);
+        const float2 z = f2(s[q][e + k], s[q][e + k + 1]);
         float2 t;
         if (CAP) {
           const float2 nl = k == 0 ? make_float2(-l2.x, -l2.y) : make_float2(-l2.z, -l2.w);
-          z = make_float2(score.half_gap(z.x), score.half_gap(z.y));
-          t = ffma2(z, make_float2(-2.f * score.c2, -2.f * score.c2),
-                    fadd2(nl, make_float2(score.c2, score.c2)));
+          t = ffma2(z, make_float2(score.c2, score.c2), nl);
         } else {
           t = fmul2(z, make_float2(score.c1, score.c1));
         }
@@ -163,11 +153,7 @@ __device__ __forceinline__ void both(const Score<CAP, BIAS>& score, const uint32
           t.y = fmaf(-__int_as_float(b.w), fabsf(static_cast<float>(key - b.z)), t.y);
         }
         float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-        float2 ds = f2(x[q][e + k], x[q][e + k + 1]);
-        if (CAP)  // 1 - tanh^2 = 4 r (1 - r)
-          ds = fmul2(fmul2(ds, fmul2(z, make_float2(4.f, 4.f))),
-                     fadd2(make_float2(1.f, 1.f), make_float2(-z.x, -z.y)));
-        ds = fmul2(p, ds);
+        float2 ds = fmul2(p, score.damp(f2(x[q][e + k], x[q][e + k + 1]), z));
         if (MASKED) {  // S and dP of a row that sees nothing may be NaN
           if (!(seen >> i & 1)) p.x = ds.x = 0.f;
           if (!(seen >> (i + 1) & 1)) p.y = ds.y = 0.f;
@@ -468,6 +454,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (!C::kOwn) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
+          score.tanh_of(s[c]);
           if (masked)
             weights<CAP, BIAS, true>(score, s[c], l2 + 32 * c, info + 32 * c, key, seen[c], pk);
           else
@@ -507,6 +494,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           warp_arrive(&sm.p_free);
         }
         if (C::kOwn) {
+          score.tanh_of(s[c]);
           if (masked)
             both<CAP, BIAS, true>(score, s[c], x, l2 + 32 * c, info + 32 * c, key, seen[c], pk, gk);
           else

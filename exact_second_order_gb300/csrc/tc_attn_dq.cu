@@ -62,7 +62,8 @@ struct SmemQ {
   int abort_flag;
 };
 
-// dS of 32 columns as bf16 pairs from the raw scores s and dP x.  One pass
+// dS of 32 columns as bf16 pairs from the raw products (capped: their tanh) s
+// and dP x.  One pass
 // over both, so that the exponentials (MUFU) of some columns run beside the
 // multiplications of others.
 template <bool CAP, bool BIAS, bool MASKED>
@@ -74,15 +75,10 @@ __device__ __forceinline__ void grads(const Score<CAP, BIAS>& sc, const uint32_t
   for (int q = 0; q < 2; ++q)
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
-      float2 z = f2(s[q][e], s[q][e + 1]);
-      if (CAP) z = make_float2(sc.half_gap(z.x), sc.half_gap(z.y));
+      const float2 z = f2(s[q][e], s[q][e + 1]);
       const float2 t = sc.from(z, dist + (16 * q + e), l2, sc.slope2);
       const float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-      float2 ds = fadd2(f2(x[q][e], x[q][e + 1]), nd);
-      if (CAP)  // 1 - tanh^2 = 4 r (1 - r)
-        ds = fmul2(fmul2(ds, fmul2(z, make_float2(4.f, 4.f))),
-                   fadd2(make_float2(1.f, 1.f), make_float2(-z.x, -z.y)));
-      ds = fmul2(p, ds);
+      float2 ds = fmul2(p, sc.damp(fadd2(f2(x[q][e], x[q][e + 1]), nd), z));
       if (MASKED) {  // S and dP of a hidden key may be NaN
         const int j = jbase + 16 * q + e;
         if (j < lo || j >= hi) ds.x = 0.f;
@@ -101,13 +97,9 @@ __device__ __forceinline__ void weights(const Score<CAP, BIAS>& sc, uint32_t (&s
   for (int q = 0; q < 2; ++q)
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
-      float2 z = f2(s[q][e], s[q][e + 1]);
-      if (CAP) z = make_float2(sc.half_gap(z.x), sc.half_gap(z.y));
+      const float2 z = f2(s[q][e], s[q][e + 1]);
       const float2 t = sc.from(z, dist + (16 * q + e), l2, sc.slope2);
-      float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-      if (CAP)
-        p = fmul2(fmul2(p, fmul2(z, make_float2(4.f, 4.f))),
-                  fadd2(make_float2(1.f, 1.f), make_float2(-z.x, -z.y)));
+      float2 p = sc.damp(make_float2(ex2_approx(t.x), ex2_approx(t.y)), z);
       if (MASKED) {
         const int j = jbase + 16 * q + e;
         if (j < lo || j >= hi) p.x = 0.f;
@@ -327,6 +319,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tc_fence_before();
             warp_arrive(&sm.p_free);
           }
+          score.tanh_of(s[c]);
           if (masked)
             grads<CAP, BIAS, true>(score, s[c], x, col_of(t, c), lo, hi, dist_at(t, c), l2, dd, pk);
           else
@@ -356,6 +349,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const bool masked = masked_at(t);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
+          score.tanh_of(s[c]);
           if (masked)
             weights<CAP, BIAS, true>(score, s[c], col_of(t, c), lo, hi, dist_at(t, c), l2);
           else

@@ -64,17 +64,6 @@ struct SmemF {
   int abort_flag;
 };
 
-// The score's input of 64 columns: raw, or in place the r of the cap.
-template <bool CAP, bool BIAS>
-__device__ __forceinline__ void prepare64(const Score<CAP, BIAS>& sc, uint32_t (&s)[4][16]) {
-  if (CAP) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s[q][e] = __float_as_uint(sc.half_gap(u2f(s[q][e])));
-  }
-}
-
 // Largest visible score of 64 columns from jbase on (log2 units, relative to
 // nothing).  Without a bias the score grows with the raw product, so the
 // maximum is taken over those.
@@ -281,7 +270,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         tmem_wait_ld();
       };
       auto max_of = [&](int c) {
-        if (BIAS) prepare64(score, s);
+        if (BIAS) score.tanh_of(s);
         mr = fmaxf(mr, masked ? max64<CAP, BIAS, true>(score, s, col0 + c, lo, hi, dist + c)
                               : max64<CAP, BIAS, false>(score, s, col0 + c, lo, hi, dist + c));
       };
@@ -294,7 +283,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       float mt = mr;
       if (!BIAS) {
         mt = mr * score.c1;
-        if (CAP && mr != -INFINITY) mt = fmaf(-2.f * score.c2, score.half_gap(mr), score.c2);
+        if (CAP && mr != -INFINITY) mt = score.c2 * score.tanh_exact(mr);
       }
       const bool raise = mt > m + kRescale;
       const float factor = raise ? (m == -INFINITY ? 0.f : ex2_approx(m - mt)) : 1.f;
@@ -324,7 +313,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
       for (int c = 0; c < BN; c += 64) {
         if (c > 0) load64(c);
-        if (!BIAS || c > 0) prepare64(score, s);
+        if (!BIAS || c > 0) score.tanh_of(s);
         uint32_t pk[4][8];
         if (masked) weights64<CAP, BIAS, true>(score, s, col0 + c, lo, hi, dist + c, m, l, pk);
         else weights64<CAP, BIAS, false>(score, s, col0 + c, lo, hi, dist + c, m, l, pk);
