@@ -7,10 +7,12 @@
 //   dx = r (g - x r mean(g x r)).
 //
 // Every element is read and written once: memory bounds both directions.  A
-// row (one head of one token) is taken by 8 lanes (d <= 64) or 16, four pairs
-// each, so that both elements of a pair sit in one lane: the rotation needs
-// no exchange and the row sums are three or four shuffles.  Angles are
-// computed once for each token and pair and shared by its heads.
+// token is taken by 8 lanes (d <= 64) or 16, each with four pairs of every
+// head's row, so both elements of a pair sit in one lane, the row sums are three
+// or four shuffles, and the token's cosines and sines stay in 8 registers while
+// its heads stream past, several rows in flight (a block of 4 tokens with the
+// angles in shared memory, computed before the first load, ran at 2.1 TB/s).
+// Neighbouring tokens of a block write neighbouring rows of a head.
 //
 // Angles as fractions of a turn in 64-bit fixed point: f / (2 pi) mod 1 is
 // scaled by 2^64 (from fp64, so to 2^-53), and the integer product with the
@@ -18,6 +20,8 @@
 // angle of any position is exact to about 2^-24 of a half turn, which a
 // product in 32 bits would lose from a position of a few hundred on.
 #include <math.h>
+
+#include <type_traits>
 
 #include "attn_common.cuh"
 
@@ -27,7 +31,8 @@ using namespace attn;
 
 constexpr int NT = 256;
 constexpr int kMaxAxes = 4;
-constexpr int kGradBlocks = 4 * kSMs;  // blocks of the gradient: one partial dw each
+constexpr unsigned kForwardBlocks = 4 * kSMs;
+constexpr unsigned kGradBlocks = 4 * kSMs;  // one partial dw each
 
 // 2 pi / f turns ... the frequency as a 64-bit fraction of a turn per position.
 __device__ __forceinline__ unsigned long long turn_step(float f) {
@@ -129,220 +134,276 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// Turn the lane's pairs by (cos, sin) of pairs 4 c ..; sign = -1 turns back.
-__device__ __forceinline__ void rotate(float (&v)[8], const float2* cs, int c, int half,
-                                       float sign) {
+// Turn the lane's pairs by (cos, sin); SIGN = -1 turns back.  Pairs that do not
+// turn have (1, 0).
+template <int SIGN>
+__device__ __forceinline__ void rotate(float (&v)[8], const float2 (&cs)[4]) {
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    if (4 * c + u < half) {
-      const float2 t = cs[4 * c + u];
-      const float a = v[2 * u], b = v[2 * u + 1], sn = sign * t.y;
-      v[2 * u] = a * t.x - b * sn;
-      v[2 * u + 1] = b * t.x + a * sn;
-    }
+    const float a = v[2 * u], b = v[2 * u + 1], sn = SIGN * cs[u].y;
+    v[2 * u] = a * cs[u].x - b * sn;
+    v[2 * u + 1] = b * cs[u].x + a * sn;
   }
 }
 
-// Tables of a block in dynamic shared memory: the steps [axes][half], then
-// (cos, sin) of its tokens [TOK][half].
 __device__ __forceinline__ void fill_steps(unsigned long long* steps, const NormArgs& a) {
   for (int k = threadIdx.x; k < a.axes * (a.R / 2); k += NT) steps[k] = turn_step(a.freqs[k]);
+  __syncthreads();
 }
 
-template <int TOK>
-__device__ __forceinline__ void fill_turns(float2* cs, const unsigned long long* steps,
-                                           const NormArgs& a, size_t token0, size_t tokens) {
+__device__ __forceinline__ void token_turns(float2 (&cs)[4], const unsigned long long* steps,
+                                            const NormArgs& a, int c, size_t tokens,
+                                            size_t token) {
   const int half = a.R / 2;
-  for (int x = threadIdx.x; x < TOK * half; x += NT) {
-    const size_t token = token0 + x / half;
-    if (token < tokens)
-      cs[x] = turn(steps, half, x % half, a.axes, a.positions, tokens, token,
-                   static_cast<int>(token % a.N));
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    cs[u] = 4 * c + u < half ? turn(steps, half, 4 * c + u, a.axes, a.positions, tokens, token,
+                                    static_cast<int>(token % a.N))
+                             : make_float2(1.f, 0.f);
+}
+
+// The lane's eight elements as loaded, unpacked at use: fewer registers for
+// rows in flight.
+template <typename T, bool VEC>
+struct Raw {
+  float v[8];
+  __device__ __forceinline__ void load(const T* x, const Shape& s, int c) {
+    load_row<VEC>(x, s, c, v);
   }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = 0.f;
+  }
+  __device__ __forceinline__ void get(float (&o)[8], const Shape&, int) const {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) o[u] = v[u];
+  }
+};
+template <>
+struct Raw<__nv_bfloat16, true> {
+  uint2 a, b;
+  __device__ __forceinline__ void load(const __nv_bfloat16* x, const Shape& s, int c) {
+    if (8 * c >= s.d) return zero();
+    const bool apart = 4 * c < s.half && !s.interleaved;
+    a = *reinterpret_cast<const uint2*>(x + (apart ? 4 * c : 8 * c));
+    b = *reinterpret_cast<const uint2*>(x + (apart ? s.half + 4 * c : 8 * c + 4));
+  }
+  __device__ __forceinline__ void zero() { a = b = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void get(float (&o)[8], const Shape& s, int c) const {
+    const float4 x = make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xFFFF0000u),
+                                 __uint_as_float(a.y << 16), __uint_as_float(a.y & 0xFFFF0000u));
+    const float4 y = make_float4(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xFFFF0000u),
+                                 __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xFFFF0000u));
+    if (4 * c < s.half && !s.interleaved) {
+      o[0] = x.x, o[2] = x.y, o[4] = x.z, o[6] = x.w;
+      o[1] = y.x, o[3] = y.y, o[5] = y.z, o[7] = y.w;
+    } else {
+      o[0] = x.x, o[1] = x.y, o[2] = x.z, o[3] = x.w;
+      o[4] = y.x, o[5] = y.y, o[6] = y.z, o[7] = y.w;
+    }
+  }
+};
+
+// Which of a token's heads a block takes: part blockIdx.y of gridDim.y of the
+// query heads, of the key heads and of the value heads.
+__device__ __forceinline__ int2 head_part(int heads) {
+  return make_int2(heads * static_cast<int>(blockIdx.y) / static_cast<int>(gridDim.y),
+                   heads * (static_cast<int>(blockIdx.y) + 1) / static_cast<int>(gridDim.y));
 }
 
 // ---------------------------------------------------------------------------
-// Forward.  A block takes TOK tokens; its row slots walk the heads and take
-// TOK tokens of a head at a time, all loads before any arithmetic.
+// Forward.
 // ---------------------------------------------------------------------------
-template <typename T, int LPR, bool VEC, int TOK>
-__global__ void __launch_bounds__(NT) norm_kernel(const __grid_constant__ NormArgs a) {
-  extern __shared__ unsigned long long smem[];
-  const int half = a.R / 2;
-  float2* cs = reinterpret_cast<float2*>(smem + a.axes * half);
-  const size_t tokens = static_cast<size_t>(a.B) * a.N;
-  const size_t token0 = static_cast<size_t>(blockIdx.x) * TOK;
-  const Shape s{a.d, half, a.interleaved};
-  const int c = threadIdx.x % LPR, slot = threadIdx.x / LPR, heads = a.H + 2 * a.Hkv;
-  const T* X = static_cast<const T*>(a.QKV);
+constexpr int kRows = 8;  // rows in flight
 
-  fill_steps(smem, a);
-  __syncthreads();
-  fill_turns<TOK>(cs, smem, a, token0, tokens);
-  __syncthreads();
-  // A warp's slots run the same number of steps: the shuffles need all lanes.
-  for (int h0 = 0; h0 < heads; h0 += NT / LPR) {
-    const int h = h0 + slot;
-    float v[TOK][8];
+template <typename T, int LPR, bool VEC>
+__global__ void __launch_bounds__(NT) norm_kernel(const __grid_constant__ NormArgs a) {
+  extern __shared__ unsigned long long steps[];
+  const size_t tokens = static_cast<size_t>(a.B) * a.N;
+  const Shape s{a.d, a.R / 2, a.interleaved};
+  const int c = threadIdx.x % LPR, slot = threadIdx.x / LPR, heads = a.H + 2 * a.Hkv;
+  constexpr int kSlots = NT / LPR;
+  fill_steps(steps, a);
+  // The lanes of a warp stay together (the shuffles need them all); a slot
+  // without a token only loads and stores nothing.
+  for (size_t first = static_cast<size_t>(blockIdx.x) * kSlots; first < tokens;
+       first += static_cast<size_t>(gridDim.x) * kSlots) {
+    const size_t token = first + slot;
+    const bool live = token < tokens;
+    const size_t b = live ? token / a.N : 0, n = live ? token % a.N : 0;
+    const T* X = static_cast<const T*>(a.QKV) + (live ? token : 0) * heads * a.d;
+    const long long kv = static_cast<long long>(n) + (a.kv_start && live ? a.kv_start[b] : 0);
+    const bool kept = kv >= 0 && kv < a.Nk;  // a row outside the cache is dropped
+    float2 cs[4];
+    bool turned = false;
+    auto run = [&](auto kind, int nh, int h0, T* out, size_t pitch, const float* gain, bool keep) {
+      constexpr int kKind = decltype(kind)::value;  // 0 query, 1 key, 2 value
+      const int2 part = head_part(nh);
+      float w[8];
+      if (kKind < 2 && gain) load_row<VEC>(gain, s, c, w);
+      for (int h = part.x; h < part.y; h += kRows) {
+        Raw<T, VEC> x[kRows];
 #pragma unroll
-    for (int u = 0; u < TOK; ++u) {
-      if (h < heads && token0 + u < tokens) {
-        load_row<VEC>(X + ((token0 + u) * heads + h) * a.d, s, c, v[u]);
-      } else {
+        for (int u = 0; u < kRows; ++u) {
+          if (live && h + u < part.y) x[u].load(X + static_cast<size_t>(h0 + h + u) * a.d, s, c);
+          else x[u].zero();
+        }
+        if (kKind < 2 && !turned) {  // behind the first loads
+          token_turns(cs, steps, a, c, tokens, live ? token : 0);
+          turned = true;
+        }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
+        for (int u = 0; u < kRows; ++u) {
+          float v[8];
+          x[u].get(v, s, c);
+          if (kKind < 2) {
+            float sq = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sq = fmaf(v[e], v[e], sq);
+            const float r = rsqrtf(row_sum<LPR>(sq) / a.d + a.eps);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = gain ? v[e] * r * w[e] : v[e] * r;
+            rotate<1>(v, cs);
+          }
+          if (live && keep && h + u < part.y) store_row<VEC>(out + (h + u) * pitch, s, c, v);
+        }
       }
-    }
-    const bool is_q = h < a.H, is_v = h >= a.H + a.Hkv;
-    const float* gain = is_q ? a.wq : a.wk;
-    float w[8];
-    if (gain && !is_v) load_row<VEC>(gain, s, c, w);
-    else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = 1.f;
-    }
-#pragma unroll
-    for (int u = 0; u < TOK; ++u) {
-      float sq = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sq = fmaf(v[u][e], v[u][e], sq);
-      sq = row_sum<LPR>(sq);
-      if (!is_v) {
-        const float r = rsqrtf(sq / a.d + a.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[u][e] = v[u][e] * r * w[e];
-        rotate(v[u], cs + u * half, c, half, 1.f);
-      }
-      if (h >= heads || token0 + u >= tokens) continue;
-      const int b = static_cast<int>((token0 + u) / a.N), n = static_cast<int>((token0 + u) % a.N);
-      if (is_q) {
-        store_row<VEC>(static_cast<T*>(a.Q) + ((static_cast<size_t>(b) * a.H + h) * a.N + n) * a.d,
-                       s, c, v[u]);
-      } else {
-        const int hk = is_v ? h - a.H - a.Hkv : h - a.H;
-        const long long row = static_cast<long long>(n) + (a.kv_start ? a.kv_start[b] : 0);
-        if (row >= 0 && row < a.Nk)  // a row outside the cache is dropped
-          store_row<VEC>(static_cast<T*>(is_v ? a.V : a.K) +
-                             ((static_cast<size_t>(b) * a.Hkv + hk) * a.Nk + row) * a.d,
-                         s, c, v[u]);
-      }
-    }
+    };
+    T* Q = static_cast<T*>(a.Q) + (b * a.H * a.N + n) * a.d;
+    const size_t kvrow = (b * a.Hkv * static_cast<size_t>(a.Nk) + (kept ? kv : 0)) * a.d;
+    const size_t kvpitch = static_cast<size_t>(a.Nk) * a.d;
+    run(std::integral_constant<int, 0>(), a.H, 0, Q, static_cast<size_t>(a.N) * a.d, a.wq, true);
+    run(std::integral_constant<int, 1>(), a.Hkv, a.H, static_cast<T*>(a.K) + kvrow, kvpitch, a.wk,
+        kept);
+    run(std::integral_constant<int, 2>(), a.Hkv, a.H + a.Hkv, static_cast<T*>(a.V) + kvrow, kvpitch,
+        nullptr, kept);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Gradient.  A fixed number of blocks walks the tokens; each lane keeps dw of
-// its eight columns for q and k, the block sums its row slots in order and
-// leaves one partial, and a second kernel sums the partials in order: the
-// result does not depend on timing.
+// its eight columns for q and k, the block sums its slots in order and leaves
+// one partial, and a second kernel sums the partials in order: the result does
+// not depend on timing.
 // ---------------------------------------------------------------------------
-template <typename T, typename TG, int LPR, bool VEC, int TOK>
+constexpr int kGradRows = 4;  // rows of x and of dz in flight
+
+template <typename T, typename TG, int LPR, bool VEC>
 __global__ void __launch_bounds__(NT) norm_grad_kernel(const __grid_constant__ NormArgs a) {
-  extern __shared__ unsigned long long smem[];
-  __shared__ float part[NT * 8];
-  const int half = a.R / 2;
-  float2* cs = reinterpret_cast<float2*>(smem + a.axes * half);
+  extern __shared__ unsigned long long steps[];
+  __shared__ float part_dw[NT * 8];
   const size_t tokens = static_cast<size_t>(a.B) * a.N;
-  const Shape s{a.d, half, a.interleaved};
+  const Shape s{a.d, a.R / 2, a.interleaved};
   const int c = threadIdx.x % LPR, slot = threadIdx.x / LPR, heads = a.H + 2 * a.Hkv;
-  const T* X = static_cast<const T*>(a.QKV);
-  T* dX = static_cast<T*>(a.dQKV);
+  constexpr int kSlots = NT / LPR;
   float dw[2][8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
-
-  fill_steps(smem, a);
-  for (size_t token0 = static_cast<size_t>(blockIdx.x) * TOK; token0 < tokens;
-       token0 += static_cast<size_t>(gridDim.x) * TOK) {
-    __syncthreads();
-    fill_turns<TOK>(cs, smem, a, token0, tokens);
-    __syncthreads();
-    for (int h0 = 0; h0 < heads; h0 += NT / LPR) {
-      const int h = h0 + slot;
-      const bool is_q = h < a.H, is_v = h >= a.H + a.Hkv;
-      const int hk = is_v ? h - a.H - a.Hkv : h - a.H;
-      float x[TOK][8], g[TOK][8];
-#pragma unroll
-      for (int u = 0; u < TOK; ++u) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[u][e] = g[u][e] = 0.f;
-        if (h < heads && token0 + u < tokens) {
-          const size_t b = (token0 + u) / a.N, n = (token0 + u) % a.N;
-          const TG* dz = static_cast<const TG*>(is_q ? a.Q : is_v ? a.V : a.K) +
-                         ((is_q ? b * a.H + h : b * a.Hkv + hk) * a.N + n) * a.d;
-          load_row<VEC>(dz, s, c, g[u]);
-          if (!is_v) load_row<VEC>(X + ((token0 + u) * heads + h) * a.d, s, c, x[u]);
-        }
-      }
-      const float* gain = is_q ? a.wq : a.wk;
+  fill_steps(steps, a);
+  for (size_t first = static_cast<size_t>(blockIdx.x) * kSlots; first < tokens;
+       first += static_cast<size_t>(gridDim.x) * kSlots) {
+    const size_t token = first + slot;
+    const bool live = token < tokens;
+    const size_t b = live ? token / a.N : 0, n = live ? token % a.N : 0;
+    const T* X = static_cast<const T*>(a.QKV) + (live ? token : 0) * heads * a.d;
+    T* dX = static_cast<T*>(a.dQKV) + (live ? token : 0) * heads * a.d;
+    const size_t pitch = static_cast<size_t>(a.N) * a.d;
+    float2 cs[4];
+    bool turned = false;
+    auto run = [&](auto kind, int nh, int h0, const TG* dz, const float* gain) {
+      constexpr int kKind = decltype(kind)::value;
+      const int2 part = head_part(nh);
       float w[8];
-      if (gain && !is_v) load_row<VEC>(gain, s, c, w);
-      else {
+      if (kKind < 2 && gain) load_row<VEC>(gain, s, c, w);
+      for (int h = part.x; h < part.y; h += kGradRows) {
+        Raw<T, VEC> rx[kGradRows];
+        Raw<TG, VEC> rg[kGradRows];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 1.f;
-      }
-#pragma unroll
-      for (int u = 0; u < TOK; ++u) {
-        float sq = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sq = fmaf(x[u][e], x[u][e], sq);
-        const float r = rsqrtf(row_sum<LPR>(sq) / a.d + a.eps);
-        float dot = 0.f;
-        if (!is_v) {
-          rotate(g[u], cs + u * half, c, half, -1.f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[u][e] *= r;
-            const float y = g[u][e] * x[u][e];
-            dw[0][e] += is_q ? y : 0.f;
-            dw[1][e] += is_q ? 0.f : y;
-            g[u][e] *= w[e];
-            dot = fmaf(g[u][e], x[u][e], dot);
+        for (int u = 0; u < kGradRows; ++u) {
+          if (live && h + u < part.y) {
+            rg[u].load(dz + (h + u) * pitch, s, c);
+            if (kKind < 2) rx[u].load(X + static_cast<size_t>(h0 + h + u) * a.d, s, c);
+          } else {
+            rg[u].zero();
+            if (kKind < 2) rx[u].zero();
           }
         }
-        dot = row_sum<LPR>(dot) / a.d;
-        if (!is_v) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) g[u][e] = r * (g[u][e] - x[u][e] * dot);
+        if (kKind < 2 && !turned) {
+          token_turns(cs, steps, a, c, tokens, live ? token : 0);
+          turned = true;
         }
-        if (h < heads && token0 + u < tokens)
-          store_row<VEC>(dX + ((token0 + u) * heads + h) * a.d, s, c, g[u]);
+#pragma unroll
+        for (int u = 0; u < kGradRows; ++u) {
+          float g[8];
+          rg[u].get(g, s, c);
+          if (kKind < 2) {
+            float x[8];
+            rx[u].get(x, s, c);
+            float sq = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
+            const float r = rsqrtf(row_sum<LPR>(sq) / a.d + a.eps);
+            rotate<-1>(g, cs);
+            float dot = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              x[e] *= r;
+              if (gain) {
+                dw[kKind & 1][e] = fmaf(g[e], x[e], dw[kKind & 1][e]);
+                g[e] *= w[e];
+              }
+              dot = fmaf(g[e], x[e], dot);
+            }
+            dot = row_sum<LPR>(dot) / a.d;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = r * (g[e] - x[e] * dot);
+          }
+          if (live && h + u < part.y)
+            store_row<VEC>(dX + static_cast<size_t>(h0 + h + u) * a.d, s, c, g);
+        }
       }
-    }
+    };
+    const size_t row = (b * a.H * a.N + n) * a.d, kvrow = (b * a.Hkv * a.N + n) * a.d;
+    run(std::integral_constant<int, 0>(), a.H, 0, static_cast<const TG*>(a.Q) + row, a.wq);
+    run(std::integral_constant<int, 1>(), a.Hkv, a.H, static_cast<const TG*>(a.K) + kvrow, a.wk);
+    run(std::integral_constant<int, 2>(), a.Hkv, a.H + a.Hkv, static_cast<const TG*>(a.V) + kvrow,
+        nullptr);
   }
   if (a.dwq == nullptr) return;
+  const size_t block = static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) part[(slot * LPR + c) * 8 + e] = dw[k][e];
+    for (int e = 0; e < 8; ++e) part_dw[(slot * LPR + c) * 8 + e] = dw[k][e];
     __syncthreads();
     for (int x = threadIdx.x; x < LPR * 8; x += NT) {
       float sum = 0.f;
-      for (int q = 0; q < NT / LPR; ++q) sum += part[q * LPR * 8 + x];
+      for (int q = 0; q < kSlots; ++q) sum += part_dw[q * LPR * 8 + x];
       // Position x of the lanes' order; the sum kernel puts it in place.
-      a.workspace[(static_cast<size_t>(blockIdx.x) * 2 + k) * 128 + x] = sum;
+      a.workspace[(block * 2 + k) * 128 + x] = sum;
     }
   }
 }
 
-// dw[k][element] = the sum of the blocks' partials in their order.  256
-// threads: 32 columns by 8 runs of partials, joined in order.
-__global__ void __launch_bounds__(NT) norm_dw_kernel(const float* __restrict__ part, int blocks,
-                                                     float* __restrict__ dwq,
-                                                     float* __restrict__ dwk, int d, int half,
-                                                     int interleaved, int vec) {
-  __shared__ float s[8][32];
+// dw[k][element] = the sum of the blocks' partials in their order: 32 columns
+// by 32 runs of partials, joined in order.
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int blocks,
+                                                       float* __restrict__ dwq,
+                                                       float* __restrict__ dwk, int d, int half,
+                                                       int interleaved) {
+  __shared__ float s[32][33];
   const int k = blockIdx.y, x = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
   float sum = 0.f;
-  const int b0 = static_cast<int>(static_cast<long long>(blocks) * run / 8);
-  const int b1 = static_cast<int>(static_cast<long long>(blocks) * (run + 1) / 8);
+  const int b0 = blocks * run / 32, b1 = blocks * (run + 1) / 32;
+#pragma unroll 4
   for (int b = b0; b < b1; ++b) sum += part[(static_cast<size_t>(b) * 2 + k) * 128 + x];
   s[run][threadIdx.x & 31] = sum;
   __syncthreads();
   if (run) return;
   sum = 0.f;
-  for (int q = 0; q < 8; ++q) sum += s[q][threadIdx.x];
+#pragma unroll
+  for (int q = 0; q < 32; ++q) sum += s[q][threadIdx.x];
   const Shape sh{d, half, interleaved != 0};
   // Element e = x % 8 of lane x / 8: pair 4 (x / 8) + e / 2.
   const int2 at = pair_at(sh, 4 * (x >> 3) + ((x & 7) >> 1));
@@ -350,46 +411,44 @@ __global__ void __launch_bounds__(NT) norm_dw_kernel(const float* __restrict__ p
   if (col < d) (k ? dwk : dwq)[col] = sum;
 }
 
-template <typename T, int LPR, bool VEC, int TOK>
+// Vector accesses: a lane's elements are one aligned run (neighbouring pairs),
+// or two when the halves of its pairs are, and all of them turn or none.
+bool vec_ok(const NormArgs& a) { return a.d % 8 == 0 && (a.interleaved || a.R % 8 == 0); }
+
+// Blocks: kSlots tokens each up to `most`; few tokens are also cut by heads, so
+// that a short call (the new tokens of a batch) spreads over the SMs.
+dim3 norm_grid(const NormArgs& a, int lpr, unsigned most) {
+  const size_t slots = NT / lpr, blocks = (static_cast<size_t>(a.B) * a.N + slots - 1) / slots;
+  const unsigned x = static_cast<unsigned>(blocks < most ? blocks : most);
+  const int heads = a.H > a.Hkv ? a.H : a.Hkv;
+  unsigned y = kSMs / x;
+  if (y > static_cast<unsigned>((heads + 3) / 4)) y = (heads + 3) / 4;
+  return dim3(x, y < 1 ? 1 : y);
+}
+
+template <typename T, int LPR, bool VEC>
 cudaError_t forward(const NormArgs& a) {
-  const size_t tokens = static_cast<size_t>(a.B) * a.N;
-  const size_t smem = static_cast<size_t>(a.R / 2) * (8 * a.axes + 8 * TOK);
-  norm_kernel<T, LPR, VEC, TOK>
-      <<<static_cast<unsigned>((tokens + TOK - 1) / TOK), NT, smem, a.stream>>>(a);
+  const size_t smem = static_cast<size_t>(a.R / 2) * 8 * a.axes;
+  norm_kernel<T, LPR, VEC><<<norm_grid(a, LPR, kForwardBlocks), NT, smem, a.stream>>>(a);
   return cudaGetLastError();
 }
 
-bool vec_ok(const NormArgs& a) { return a.d % 8 == 0 && a.R % 8 == 0; }
-
 template <typename T>
 cudaError_t forward(const NormArgs& a) {
-  // Four tokens a block once there are enough blocks to fill the GPU twice.
-  const bool many = static_cast<size_t>(a.B) * a.N >= 4u * 2u * kSMs;
-  if (a.d <= 64) {
-    if (vec_ok(a)) return many ? forward<T, 8, true, 4>(a) : forward<T, 8, true, 1>(a);
-    return many ? forward<T, 8, false, 4>(a) : forward<T, 8, false, 1>(a);
-  }
-  if (vec_ok(a)) return many ? forward<T, 16, true, 4>(a) : forward<T, 16, true, 1>(a);
-  return many ? forward<T, 16, false, 4>(a) : forward<T, 16, false, 1>(a);
-}
-
-constexpr int kGradTok = 2;
-
-unsigned grad_blocks(const NormArgs& a) {
-  const size_t n = (static_cast<size_t>(a.B) * a.N + kGradTok - 1) / kGradTok;
-  return static_cast<unsigned>(n < kGradBlocks ? n : kGradBlocks);
+  if (a.d <= 64) return vec_ok(a) ? forward<T, 8, true>(a) : forward<T, 8, false>(a);
+  return vec_ok(a) ? forward<T, 16, true>(a) : forward<T, 16, false>(a);
 }
 
 template <typename T, typename TG, int LPR, bool VEC>
 cudaError_t backward(const NormArgs& a) {
-  const unsigned blocks = grad_blocks(a);
-  const size_t smem = static_cast<size_t>(a.R / 2) * (8 * a.axes + 8 * kGradTok);
-  norm_grad_kernel<T, TG, LPR, VEC, kGradTok><<<blocks, NT, smem, a.stream>>>(a);
+  const dim3 grid = norm_grid(a, LPR, kGradBlocks);
+  const size_t smem = static_cast<size_t>(a.R / 2) * 8 * a.axes;
+  norm_grad_kernel<T, TG, LPR, VEC><<<grid, NT, smem, a.stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.dwq == nullptr) return e;
-  norm_dw_kernel<<<dim3(LPR / 4, 2), NT, 0, a.stream>>>(a.workspace, static_cast<int>(blocks),
-                                                        a.dwq, a.dwk, a.d, a.R / 2,
-                                                        a.interleaved ? 1 : 0, VEC ? 1 : 0);
+  norm_dw_kernel<<<dim3(LPR / 4, 2), 1024, 0, a.stream>>>(
+      a.workspace, static_cast<int>(grid.x * grid.y), a.dwq, a.dwk, a.d, a.R / 2,
+      a.interleaved ? 1 : 0);
   return cudaGetLastError();
 }
 
@@ -402,7 +461,9 @@ cudaError_t backward(const NormArgs& a) {
 }  // namespace
 
 size_t norm_grad_workspace(const NormArgs& a) {
-  return a.wq ? static_cast<size_t>(grad_blocks(a)) * 2 * 128 * sizeof(float) : 0;
+  if (!a.wq) return 0;
+  const dim3 grid = norm_grid(a, a.d <= 64 ? 8 : 16, kGradBlocks);
+  return static_cast<size_t>(grid.x) * grid.y * 2 * 128 * sizeof(float);
 }
 
 cudaError_t qk_norm(const NormArgs& a) {

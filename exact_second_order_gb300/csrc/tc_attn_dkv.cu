@@ -31,10 +31,7 @@ using namespace tc;
 using namespace attn;
 
 constexpr int BM = kTcRows, BQ = 128;
-#ifndef X_NWG
-#define X_NWG 4
-#endif
-constexpr int NWG = X_NWG, CW = BQ / NWG, NC = CW / 32;  // warpgroups; rows of each, in chunks of 32
+constexpr int NWG = 4, CW = BQ / NWG, NC = CW / 32;  // warpgroups; rows of each, in chunks of 32
 constexpr int NTHREADS = 64 + 128 * NWG;
 constexpr uint32_t HALF = BM * 64 * 2;  // 128 rows x 64 columns
 

@@ -28,10 +28,7 @@ using namespace tc;
 using namespace attn;
 
 constexpr int BM = kTcRows, BN = 128;
-#ifndef X_NWG
-#define X_NWG 4
-#endif
-constexpr int NWG = X_NWG, CW = BN / NWG, NC = CW / 32;  // warpgroups; columns of each, in chunks of 32
+constexpr int NWG = 4, CW = BN / NWG, NC = CW / 32;  // warpgroups; columns of each, in chunks of 32
 constexpr int NTHREADS = 64 + 128 * NWG;
 constexpr uint32_t HALF = BM * 64 * 2;  // 128 rows x 64 columns
 constexpr uint32_t kP = 256, kAcc = 384, kQA = 448, kGA = 480;

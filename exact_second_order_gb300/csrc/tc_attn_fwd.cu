@@ -248,6 +248,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int lo = gr.v.lo, hi = gr.v.hi;
     const Hull own = MT == 2 ? join_hulls(sm.hull + 4 * wg, 4) : hull;
     const Score<CAP, BIAS> score(a, gr.slope2);
+    const bool any_row = row0 + (MT == 2 ? BM * wg : 0) + quad * 32 < rows;
+    // V rows that no row of the block sees meet P~ = 0: make them 0 too.
+    auto clear_hidden = [&](int u, int col0) {
+      if (col0 < hull.lo || col0 + BN > hull.hi) {
+        if (r < BN && (col0 + r < hull.lo || col0 + r >= hull.hi))
+          zero_row<NH, HT>(sm.kv[(MT == 2 ? u >> 1 : u) % NST][1], r);
+        fence_proxy_async_smem();
+      }
+    };
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     int n = 0;  // units of this warpgroup
@@ -259,6 +268,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const uint32_t sc = tbase + lane_off + kScore + BN * (u % NBUF);
       const bool masked = col0 < own.in_lo || col0 + BN > own.in_hi;
       const float dist = BIAS ? static_cast<float>(col0 - gr.v.pos) : 0.f;
+      if (!any_row) {  // tokens over a cache fill few of the 128 rows
+        clear_hidden(u, col0);
+        warp_arrive(&sm.op_ready[u % NBUF]);
+        continue;
+      }
       // Two 64-column groups at d = 64: the second is read twice, so that one
       // group is held in registers at a time, and P~ of columns 16 c .. goes
       // to columns 8 c .., onto scores already used.
@@ -320,19 +334,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_st8(sc + c / 2 + 8 * q, pk[q]);
       }
-      if (col0 < hull.lo || col0 + BN > hull.hi) {
-        // V rows that no row of the block sees meet P~ = 0: make them 0 too.
-        const int t = MT == 2 ? u >> 1 : u;
-        if (r < BN && (col0 + r < hull.lo || col0 + r >= hull.hi)) {
-#pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            uint4* v = reinterpret_cast<uint4*>(sm.kv[t % NST][1][h] + r * 128);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
-          }
-        }
-        fence_proxy_async_smem();
-      }
+      clear_hidden(u, col0);
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(&sm.op_ready[u % NBUF]);
@@ -459,18 +461,28 @@ cudaError_t launch(const AttnArgs& a, int splits) {
 
 bool tc_attn_supported(const AttnArgs& a) { return a.bf16 && (a.d == 64 || a.d == 128); }
 
-// 256 rows a block once such blocks fill the GPU, 128 below.
-static bool two_blocks(const AttnArgs& a) {
+namespace {
+
+// 256 rows a block where a group has more than 128 and such blocks fill the
+// GPU; 128 rows below.
+bool two_blocks(const AttnArgs& a) {
   const long long rows = static_cast<long long>(a.H / a.Hkv) * a.Nq;
-  return static_cast<long long>(a.B) * a.Hkv * ((rows + 255) / 256) >= kSMs;
+  return rows > BM && static_cast<long long>(a.B) * a.Hkv * ((rows + 255) / 256) >= kSMs;
 }
 
+}  // namespace
+
+// How many runs the keys are cut into: as many as fill the SMs once, with
+// kSplitKeys keys at least in each.  (More runs than SMs only add to the join:
+// 8 groups of 65536 keys 28 us, with twice the runs 40 us; 128 and 512 keys
+// were within 10% of 256.)
+constexpr int kSplitKeys = 256;
 int tc_attn_splits(const AttnArgs& a) {
   const long long rows = static_cast<long long>(a.H / a.Hkv) * a.Nq;
   const long long blocks = static_cast<long long>(a.B) * a.Hkv * ((rows + BM - 1) / BM);
-  if (two_blocks(a) || blocks * 2 > kSMs) return 1;
-  const long long s = kSMs / blocks, most = a.Nk / 512 > 1 ? a.Nk / 512 : 1;
-  return static_cast<int>(s < most ? s : most);
+  const long long want = kSMs / blocks, most = a.Nk / kSplitKeys;
+  const long long s = want < most ? want : most;
+  return two_blocks(a) || s < 1 ? 1 : static_cast<int>(s);
 }
 
 cudaError_t tc_attn(const AttnArgs& a) {

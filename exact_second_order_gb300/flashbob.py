@@ -7,7 +7,9 @@ library has not been built: there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -87,8 +89,8 @@ def _dtype_code(t) -> int:
 
 def _stream_handle(stream) -> int | None:
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current device's current stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -133,10 +135,15 @@ def _input_specs(Q, K, V, dO, UQ, UK, UV):
             ("UV", UV, "k", "in")]
 
 
+_NOTHING = contextlib.nullcontext()
+
+
 def _device(t):
     """The CUDA device context of tensor ``t``: the library works on the
     current device, so every call runs with its tensors' device current."""
     import torch
+    if t.is_cuda and torch.cuda.current_device() == t.get_device():
+        return _NOTHING
     return torch.cuda.device(t.device)
 
 
@@ -239,28 +246,32 @@ def _check_tensor(where: str, name: str, t, shape, dtype, device) -> None:
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
         raise ValueError(f"{where}: {name} must be a CUDA tensor on {device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{where}: {name} is {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be contiguous")
 
 
-def _check_attention(where: str, Q, K, inputs, L, slopes, ranges, q_pos):
-    """Checks of the attention calls with key ranges; ``inputs`` lists (name,
-    tensor, role) beside Q and K, all of Q's dtype.  Returns the sizes."""
+def _check_4d(where: str, **tensors) -> None:
     import torch
-    for name, t in (("Q", Q), ("K", K)):
-        if not isinstance(t, torch.Tensor) or t.dim() != 4:
-            raise ValueError(f"{where}: {name} must be a 4-d tensor [B, heads, rows, d]")
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
+            raise ValueError(f"{where}: {name} must be a 4-d CUDA tensor")
+
+
+def _check_attention(where: str, Q, K, V, slopes, ranges, q_pos):
+    """Checks of the inputs that the attention calls with key ranges share;
+    returns the sizes."""
+    import torch
+    _check_4d(where, Q=Q, K=K)
     B, H, Nq, d = Q.shape
-    Hkv, Nk = K.shape[1], K.shape[2]
+    _, Hkv, Nk, _ = K.shape
     dev, dt = Q.device, Q.dtype
-    shapes = {"q": (B, H, Nq, d), "k": (B, Hkv, Nk, d)}
-    for name, t, role in (("Q", Q, "q"), ("K", K, "k"), *inputs):
-        _check_tensor(where, name, t, shapes[role], dt, dev)
-    _check_tensor(where, "L", L, (B, H, Nq), torch.float32, dev)
+    _check_tensor(where, "Q", Q, (B, H, Nq, d), dt, dev)
+    _check_tensor(where, "K", K, (B, Hkv, Nk, d), dt, dev)
+    _check_tensor(where, "V", V, (B, Hkv, Nk, d), dt, dev)
     if slopes is not None:
         _check_tensor(where, "slopes", slopes, (H,), torch.float32, dev)
     if ranges is not None:
@@ -274,6 +285,7 @@ def _bytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
+@functools.lru_cache(maxsize=256)
 def flashbob_attention_workspace(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int,
                                  in_dtype: int) -> tuple[int, int]:
     """Workspace bytes of flashbob_attention and of flashbob_attention_grad."""
@@ -285,38 +297,63 @@ def flashbob_attention_workspace(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: 
     return n[0].value, n[1].value
 
 
+def _run_attention(sizes, Q, K, V, ranges, q_pos, slopes, tau, cap, O, L, workspace, causal,
+                   stream) -> None:
+    st = load_library().flashbob_attention(
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), _ptr(ranges), _ptr(q_pos), _ptr(slopes), tau,
+        cap, O.data_ptr(), L.data_ptr(), _ptr(workspace), _bytes(workspace), *sizes, int(causal),
+        _dtype_code(Q), _stream_handle(stream))
+    if st != FLASHBOB_OK:
+        raise FlashbobError(st, "flashbob_attention")
+
+
 def flashbob_attention(Q, K, V, ranges, q_pos, slopes, tau: float, cap: float, O, L, workspace,
                        causal: bool = False, stream=None) -> None:
     """O, L of attention with key ranges (see flashbob_attention in the header);
     ``workspace`` is any contiguous CUDA tensor of enough bytes, or None."""
-    B, H, Hkv, Nq, Nk, d = _check_attention(
-        "flashbob_attention", Q, K, (("V", V, "k"), ("O", O, "q")), L, slopes, ranges, q_pos)
-    _check_workspace("flashbob_attention", workspace, Q.device)
+    import torch
+    where = "flashbob_attention"
+    sizes = _check_attention(where, Q, K, V, slopes, ranges, q_pos)
+    _check_tensor(where, "O", O, Q.shape, Q.dtype, Q.device)
+    _check_tensor(where, "L", L, Q.shape[:3], torch.float32, Q.device)
+    _check_workspace(where, workspace, Q.device)
     with _device(Q):
-        st = load_library().flashbob_attention(
-            _ptr(Q), _ptr(K), _ptr(V), _ptr(ranges), _ptr(q_pos), _ptr(slopes), float(tau),
-            float(cap), _ptr(O), _ptr(L), _ptr(workspace), _bytes(workspace), B, H, Hkv, Nq, Nk,
-            d, int(causal), _dtype_code(Q), _stream_handle(stream))
+        _run_attention(sizes, Q, K, V, ranges, q_pos, slopes, tau, cap, O, L, workspace, causal,
+                       stream)
+
+
+def _run_attention_grad(sizes, Q, K, V, O, L, dO, ranges, q_pos, slopes, tau, cap, dQ, dK, dV,
+                        workspace, causal, stream) -> None:
+    st = load_library().flashbob_attention_grad(
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), L.data_ptr(), dO.data_ptr(),
+        _ptr(ranges), _ptr(q_pos), _ptr(slopes), tau, cap, dQ.data_ptr(), dK.data_ptr(),
+        dV.data_ptr(), _ptr(workspace), _bytes(workspace), *sizes, int(causal), _dtype_code(Q),
+        _stream_handle(stream))
     if st != FLASHBOB_OK:
-        raise FlashbobError(st, "flashbob_attention")
+        raise FlashbobError(st, "flashbob_attention_grad")
+
+
+def _check_attention_grad(where: str, Q, K, V, O, L, dO, slopes, ranges, q_pos):
+    import torch
+    sizes = _check_attention(where, Q, K, V, slopes, ranges, q_pos)
+    _check_tensor(where, "O", O, Q.shape, Q.dtype, Q.device)
+    _check_tensor(where, "L", L, Q.shape[:3], torch.float32, Q.device)
+    _check_tensor(where, "dO", dO, Q.shape, Q.dtype, Q.device)
+    return sizes
 
 
 def flashbob_attention_grad(Q, K, V, O, L, dO, ranges, q_pos, slopes, tau: float, cap: float,
                             dQ, dK, dV, workspace, causal: bool = False, stream=None) -> None:
     """dQ, dK, dV of attention with key ranges (see flashbob_attention_grad)."""
-    B, H, Hkv, Nq, Nk, d = _check_attention(
-        "flashbob_attention_grad", Q, K,
-        (("V", V, "k"), ("O", O, "q"), ("dO", dO, "q"), ("dQ", dQ, "q"), ("dK", dK, "k"),
-         ("dV", dV, "k")), L, slopes, ranges, q_pos)
-    _check_workspace("flashbob_attention_grad", workspace, Q.device)
+    where = "flashbob_attention_grad"
+    sizes = _check_attention_grad(where, Q, K, V, O, L, dO, slopes, ranges, q_pos)
+    _check_tensor(where, "dQ", dQ, Q.shape, Q.dtype, Q.device)
+    _check_tensor(where, "dK", dK, K.shape, Q.dtype, Q.device)
+    _check_tensor(where, "dV", dV, K.shape, Q.dtype, Q.device)
+    _check_workspace(where, workspace, Q.device)
     with _device(Q):
-        st = load_library().flashbob_attention_grad(
-            _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(L), _ptr(dO), _ptr(ranges), _ptr(q_pos),
-            _ptr(slopes), float(tau), float(cap), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(workspace),
-            _bytes(workspace), B, H, Hkv, Nq, Nk, d, int(causal), _dtype_code(Q),
-            _stream_handle(stream))
-    if st != FLASHBOB_OK:
-        raise FlashbobError(st, "flashbob_attention_grad")
+        _run_attention_grad(sizes, Q, K, V, O, L, dO, ranges, q_pos, slopes, tau, cap, dQ, dK, dV,
+                            workspace, causal, stream)
 
 
 def _check_workspace(where: str, t, device) -> None:
@@ -346,8 +383,8 @@ def flashbob_attention_ranges(doc_offsets, prefix, q_start, ranges, q_pos, Nk: i
             _check_tensor(where, name, t, shape, torch.int32, ranges.device)
     with _device(ranges):
         st = load_library().flashbob_attention_ranges(
-            _ptr(doc_offsets), _ptr(prefix), _ptr(q_start), _ptr(ranges), _ptr(q_pos), B, M, Nq,
-            int(Nk), int(causal), _stream_handle(stream))
+            _ptr(doc_offsets), _ptr(prefix), _ptr(q_start), ranges.data_ptr(), _ptr(q_pos), B, M,
+            Nq, int(Nk), int(causal), _stream_handle(stream))
     if st != FLASHBOB_OK:
         raise FlashbobError(st, where)
 
@@ -541,11 +578,9 @@ def bob(Q, K, V, O, dO, L, D, UQ, UK, UV, tau: float, out: dict | None = None,
 def _allocating_on(stream, device):
     """Context in which torch allocates for ``stream``: what a wrapper
     allocates and frees (a workspace) is then reused in that stream's order."""
-    import contextlib
-
     import torch
     if stream is None:
-        return contextlib.nullcontext()
+        return _NOTHING
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)
@@ -561,15 +596,13 @@ def attention(Q, K, V, tau: float, cap: float = 0.0, slopes=None, ranges=None, q
     """O (of Q's dtype) and L of attention with capped scores, a distance bias
     and key ranges; allocates them, and the workspace, on Q's device."""
     import torch
-    _check_4d("attention", Q=Q, K=K)
-    B, H, Nq, d = Q.shape
+    sizes = _check_attention("attention", Q, K, V, slopes, ranges, q_pos)
     with _device(Q), _allocating_on(stream, Q.device):
-        O = torch.empty_like(Q, memory_format=torch.contiguous_format)
-        L = torch.empty((B, H, Nq), dtype=torch.float32, device=Q.device)
-        need, _ = flashbob_attention_workspace(B, H, K.shape[1], Nq, K.shape[2], d,
-                                               _dtype_code(Q))
-        flashbob_attention(Q, K, V, ranges, q_pos, slopes, tau, cap, O, L,
-                           _workspace(need, Q.device), causal, stream)
+        need, _ = flashbob_attention_workspace(*sizes, _dtype_code(Q))
+        O = torch.empty_like(Q)
+        L = torch.empty(sizes[0], sizes[1], sizes[3], dtype=torch.float32, device=Q.device)
+        _run_attention(sizes, Q, K, V, ranges, q_pos, slopes, tau, cap, O, L,
+                       _workspace(need, Q.device), causal, stream)
     return O, L
 
 
@@ -578,24 +611,13 @@ def attention_grad(Q, K, V, O, L, dO, tau: float, cap: float = 0.0, slopes=None,
     """dQ, dK, dV (of Q's dtype) of ``attention`` from its O and L and the
     gradient dO; allocates them, and the workspace, on Q's device."""
     import torch
-    _check_4d("attention_grad", Q=Q, K=K)
-    B, H, Nq, d = Q.shape
+    sizes = _check_attention_grad("attention_grad", Q, K, V, O, L, dO, slopes, ranges, q_pos)
     with _device(Q), _allocating_on(stream, Q.device):
-        dQ = torch.empty_like(Q, memory_format=torch.contiguous_format)
-        dK = torch.empty_like(K, memory_format=torch.contiguous_format)
-        dV = torch.empty_like(K, memory_format=torch.contiguous_format)
-        _, need = flashbob_attention_workspace(B, H, K.shape[1], Nq, K.shape[2], d,
-                                               _dtype_code(Q))
-        flashbob_attention_grad(Q, K, V, O, L, dO, ranges, q_pos, slopes, tau, cap, dQ, dK, dV,
-                                _workspace(need, Q.device), causal, stream)
+        _, need = flashbob_attention_workspace(*sizes, _dtype_code(Q))
+        dQ, dK, dV = torch.empty_like(Q), torch.empty_like(K), torch.empty_like(K)
+        _run_attention_grad(sizes, Q, K, V, O, L, dO, ranges, q_pos, slopes, tau, cap, dQ, dK, dV,
+                            _workspace(need, Q.device), causal, stream)
     return dQ, dK, dV
-
-
-def _check_4d(where: str, **tensors) -> None:
-    import torch
-    for name, t in tensors.items():
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
-            raise ValueError(f"{where}: {name} must be a 4-d CUDA tensor")
 
 
 def attention_ranges(B: int, Nq: int, Nk: int, doc_offsets=None, prefix=None, q_start=None,
@@ -607,10 +629,11 @@ def attention_ranges(B: int, Nq: int, Nk: int, doc_offsets=None, prefix=None, q_
         if t is not None:
             device = t.device
             break
-    device = torch.device("cuda" if device is None else device)
+    device = torch.device("cuda") if device is None else torch.device(device)
     if device.type != "cuda":
         raise ValueError(f"attention_ranges: the arrays must be on a CUDA device, not {device}")
-    with torch.cuda.device(device), _allocating_on(stream, device):
+    here = device.index is None or device.index == torch.cuda.current_device()
+    with _NOTHING if here else torch.cuda.device(device), _allocating_on(stream, device):
         ranges = torch.empty((B, Nq, 2), dtype=torch.int32, device=device)
         q_pos = torch.empty((B, Nq), dtype=torch.int32, device=device)
         flashbob_attention_ranges(doc_offsets, prefix, q_start, ranges, q_pos, Nk, causal, stream)
