@@ -15,8 +15,8 @@
 // Neighbouring tokens of a block write neighbouring rows of a head.
 //
 // Angles as fractions of a turn in 64-bit fixed point: f / (2 pi) mod 1 is
-// scaled by 2^64 (from fp64, so to 2^-53), and the integer product with the
-// position wraps as the angle does.  Its top 32 bits go to sincospif, so the
+// scaled by 2^64, and the integer product with the position wraps as the angle
+// does.  Its top 32 bits go to sincospif, so the
 // angle of any position is exact to about 2^-24 of a half turn, which a
 // product in 32 bits would lose from a position of a few hundred on.
 #include <math.h>
@@ -31,14 +31,24 @@ using namespace attn;
 
 constexpr int NT = 256;
 constexpr int kMaxAxes = 4;
-constexpr unsigned kForwardBlocks = 4 * kSMs;
-constexpr unsigned kGradBlocks = 4 * kSMs;  // one partial dw each
+constexpr unsigned kForwardBlocks = 8 * kSMs;
+constexpr unsigned kGradBlocks = 2 * kSMs;  // along the tokens; one partial dw a block
 
-// 2 pi / f turns ... the frequency as a 64-bit fraction of a turn per position.
+// f / (2 pi) turns per position, as a fraction of a turn in 64 bits: the 24-bit
+// significand m of f = m 2^e times 2^66 / (2 pi) (64 bits, so to 2^-64), shifted
+// to 2^64 units of a turn.  (In fp64, whose rate here is a hundredth of fp32's,
+// this took longer than a short call's memory traffic.)
 __device__ __forceinline__ unsigned long long turn_step(float f) {
-  double t = static_cast<double>(f) * 0.15915494309189533577;  // 1 / (2 pi)
-  t -= floor(t);
-  return static_cast<unsigned long long>(t * 18446744073709551616.0);
+  constexpr unsigned long long kInv2Pi = 11743562013128004906ull;  // round(2^66 / (2 pi))
+  const uint32_t bits = __float_as_uint(f), ex = (bits >> 23) & 255u;
+  const unsigned long long m = ex ? (bits & 0x7FFFFFu) | 0x800000u : bits & 0x7FFFFFu;
+  const int shift = 152 - static_cast<int>(ex ? ex : 1);  // right, of the 88-bit product
+  const unsigned long long lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+  unsigned long long t;
+  if (shift <= 0) t = shift > -64 ? lo << -shift : 0;
+  else if (shift < 64) t = (lo >> shift) | (hi << (64 - shift));
+  else t = shift < 128 ? hi >> (shift - 64) : 0;
+  return bits >> 31 ? 0 - t : t;
 }
 
 // (cos, sin) of every pair of one token.
@@ -214,15 +224,17 @@ __device__ __forceinline__ int2 head_part(int heads) {
 // ---------------------------------------------------------------------------
 // Forward.
 // ---------------------------------------------------------------------------
-constexpr int kRows = 8;  // rows in flight
+constexpr int kRows = 4;  // rows in flight of each lane, with 64 registers and 4 blocks an SM:
+                         // 81 us (16384 tokens, 48 heads of 128); 8 rows and 2 blocks 91 us
 
 template <typename T, int LPR, bool VEC>
-__global__ void __launch_bounds__(NT) norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(NT, 4) norm_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ unsigned long long steps[];
   const size_t tokens = static_cast<size_t>(a.B) * a.N;
   const Shape s{a.d, a.R / 2, a.interleaved};
   const int c = threadIdx.x % LPR, slot = threadIdx.x / LPR, heads = a.H + 2 * a.Hkv;
   constexpr int kSlots = NT / LPR;
+  const float inv_d = 1.f / a.d;
   fill_steps(steps, a);
   // The lanes of a warp stay together (the shuffles need them all); a slot
   // without a token only loads and stores nothing.
@@ -260,7 +272,7 @@ __global__ void __launch_bounds__(NT) norm_kernel(const __grid_constant__ NormAr
             float sq = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) sq = fmaf(v[e], v[e], sq);
-            const float r = rsqrtf(row_sum<LPR>(sq) / a.d + a.eps);
+            const float r = rsqrtf(fmaf(row_sum<LPR>(sq), inv_d, a.eps));
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = gain ? v[e] * r * w[e] : v[e] * r;
             rotate<1>(v, cs);
@@ -286,7 +298,8 @@ __global__ void __launch_bounds__(NT) norm_kernel(const __grid_constant__ NormAr
 // one partial, and a second kernel sums the partials in order: the result does
 // not depend on timing.
 // ---------------------------------------------------------------------------
-constexpr int kGradRows = 4;  // rows of x and of dz in flight
+constexpr int kGradRows = 4;  // rows of x and of dz in flight, 2 blocks an SM: 134 us; 2 rows and
+                             // 3 or 4 blocks 160 us
 
 template <typename T, typename TG, int LPR, bool VEC>
 __global__ void __launch_bounds__(NT) norm_grad_kernel(const __grid_constant__ NormArgs a) {
@@ -296,6 +309,7 @@ __global__ void __launch_bounds__(NT) norm_grad_kernel(const __grid_constant__ N
   const Shape s{a.d, a.R / 2, a.interleaved};
   const int c = threadIdx.x % LPR, slot = threadIdx.x / LPR, heads = a.H + 2 * a.Hkv;
   constexpr int kSlots = NT / LPR;
+  const float inv_d = 1.f / a.d;
   float dw[2][8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
@@ -342,7 +356,7 @@ __global__ void __launch_bounds__(NT) norm_grad_kernel(const __grid_constant__ N
             float sq = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
-            const float r = rsqrtf(row_sum<LPR>(sq) / a.d + a.eps);
+            const float r = rsqrtf(fmaf(row_sum<LPR>(sq), inv_d, a.eps));
             rotate<-1>(g, cs);
             float dot = 0.f;
 #pragma unroll
@@ -354,7 +368,7 @@ __global__ void __launch_bounds__(NT) norm_grad_kernel(const __grid_constant__ N
               }
               dot = fmaf(g[e], x[e], dot);
             }
-            dot = row_sum<LPR>(dot) / a.d;
+            dot = row_sum<LPR>(dot) * inv_d;
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[e] = r * (g[e] - x[e] * dot);
           }
@@ -386,42 +400,43 @@ __global__ void __launch_bounds__(NT) norm_grad_kernel(const __grid_constant__ N
   }
 }
 
-// dw[k][element] = the sum of the blocks' partials in their order: 32 columns
-// by 32 runs of partials, joined in order.
+// dw[k][element] = the sum of the blocks' partials in a fixed order: 8 columns
+// a block, 128 runs of partials each, joined in order.
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int blocks,
                                                        float* __restrict__ dwq,
                                                        float* __restrict__ dwk, int d, int half,
                                                        int interleaved) {
-  __shared__ float s[32][33];
-  const int k = blockIdx.y, x = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
+  __shared__ float s[128][9];
+  const int k = blockIdx.y, run = threadIdx.x >> 3, x = blockIdx.x * 8 + (threadIdx.x & 7);
   float sum = 0.f;
-  const int b0 = blocks * run / 32, b1 = blocks * (run + 1) / 32;
 #pragma unroll 4
-  for (int b = b0; b < b1; ++b) sum += part[(static_cast<size_t>(b) * 2 + k) * 128 + x];
-  s[run][threadIdx.x & 31] = sum;
-  __syncthreads();
+  for (int b = run; b < blocks; b += 128) sum += part[(static_cast<size_t>(b) * 2 + k) * 128 + x];
+  s[run][threadIdx.x & 7] = sum;
+  for (int n = 64; n > 0; n >>= 1) {
+    __syncthreads();
+    if (run < n) s[run][threadIdx.x & 7] += s[run + n][threadIdx.x & 7];
+  }
   if (run) return;
-  sum = 0.f;
-#pragma unroll
-  for (int q = 0; q < 32; ++q) sum += s[q][threadIdx.x];
   const Shape sh{d, half, interleaved != 0};
   // Element e = x % 8 of lane x / 8: pair 4 (x / 8) + e / 2.
   const int2 at = pair_at(sh, 4 * (x >> 3) + ((x & 7) >> 1));
   const int col = x & 1 ? at.y : at.x;
-  if (col < d) (k ? dwk : dwq)[col] = sum;
+  if (col < d) (k ? dwk : dwq)[col] = s[0][threadIdx.x];
 }
 
 // Vector accesses: a lane's elements are one aligned run (neighbouring pairs),
 // or two when the halves of its pairs are, and all of them turn or none.
 bool vec_ok(const NormArgs& a) { return a.d % 8 == 0 && (a.interleaved || a.R % 8 == 0); }
 
-// Blocks: kSlots tokens each up to `most`; few tokens are also cut by heads, so
-// that a short call (the new tokens of a batch) spreads over the SMs.
+// Blocks: NT / LPR tokens each up to `most` blocks, and cut by heads (four at
+// least of the larger group) up to kMostBlocks: a short call (the new tokens of
+// a batch) spreads over the SMs, a long one leaves little of its last wave idle.
 dim3 norm_grid(const NormArgs& a, int lpr, unsigned most) {
+  constexpr unsigned kMostBlocks = 2 * kSMs;
   const size_t slots = NT / lpr, blocks = (static_cast<size_t>(a.B) * a.N + slots - 1) / slots;
   const unsigned x = static_cast<unsigned>(blocks < most ? blocks : most);
   const int heads = a.H > a.Hkv ? a.H : a.Hkv;
-  unsigned y = kSMs / x;
+  unsigned y = kMostBlocks / x;
   if (y > static_cast<unsigned>((heads + 3) / 4)) y = (heads + 3) / 4;
   return dim3(x, y < 1 ? 1 : y);
 }
@@ -446,7 +461,7 @@ cudaError_t backward(const NormArgs& a) {
   norm_grad_kernel<T, TG, LPR, VEC><<<grid, NT, smem, a.stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.dwq == nullptr) return e;
-  norm_dw_kernel<<<dim3(LPR / 4, 2), 1024, 0, a.stream>>>(
+  norm_dw_kernel<<<dim3(LPR, 2), 1024, 0, a.stream>>>(
       a.workspace, static_cast<int>(grid.x * grid.y), a.dwq, a.dwk, a.d, a.R / 2,
       a.interleaved ? 1 : 0);
   return cudaGetLastError();

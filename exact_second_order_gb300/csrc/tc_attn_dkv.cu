@@ -11,6 +11,9 @@
 // of every tile each, one key per thread.  How many tiles there
 // are is known only to warp 0: each ring slot says which tile it holds, and a
 // last slot says that there are no more.
+// When the key blocks are few, a cluster of S blocks shares one: rank q takes
+// every S-th of its tiles, and the partial sums meet in distributed shared
+// memory, in the order of the ranks, before the one write.
 // TMEM at d = 64: S^T, dP^T (128 columns each), operands P^T and dS^T (64
 // each), dK, dV (64 each): the scores are handed back when they are in
 // registers, and those of tile n + 1 run beside the arithmetic of tile n.
@@ -23,6 +26,8 @@
 // At d = 128 dK and dV take 256 columns: one buffer of each, P^T on S^T and
 // dS^T on dP^T; the pipe runs dV(n), S(n + 1), dK(n), dP(n + 1), so that
 // P(n + 1) is formed beside dK(n) and dP(n + 1), and dS beside dV and S.
+#include <stddef.h>
+
 #include "tc_attn.cuh"
 
 namespace flashbob {
@@ -54,6 +59,10 @@ struct Slot {
   int tile;          // -1: no more
   int in_lo, in_hi;  // intersection of the rows' ranges (in_lo INT_MAX: a row sees nothing)
 };
+
+// Cluster split: floats of a staged row dK | dV (padded by 4 against conflicts).
+template <int DH>
+constexpr int kPartLd = 2 * DH + 4;
 
 template <int DH>
 struct SmemK {
@@ -189,7 +198,7 @@ template <int DH, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(NTHREADS, 1)
     tc_dkv_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mdO,
                   const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
-                  const __grid_constant__ AttnArgs a) {
+                  const __grid_constant__ AttnArgs a, int S) {
   extern __shared__ uint8_t smem_raw[];
   using Smem = SmemK<DH>;
   using C = Cols<DH>;
@@ -198,7 +207,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                                       ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = a.B * a.Hkv, rows = a.H / a.Hkv * a.Nq;
-  const int g = blockIdx.x % heads, j0 = static_cast<int>(blockIdx.x / heads) * BM;
+  const int rank = blockIdx.x % S, g = blockIdx.x / S % heads;
+  const int j0 = static_cast<int>(blockIdx.x / S / heads) * BM;
   volatile int* abort_flag = &sm.abort_flag;
   unsigned int* err = a.err;
 
@@ -252,6 +262,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     }
     int nq = 0, no = 0;  // Q and dO loads issued
+    int hit = 0;         // tiles found
     bool ok = true;
     for (int t0 = 0; ok && t0 < tiles; t0 += 32) {
       int4 b = make_int4(INT_MAX, 0, 0, INT_MAX);
@@ -261,6 +272,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       unsigned hits = __ballot_sync(0xffffffffu, b.x < j0 + BM && b.y > j0);
       for (; ok && hits; hits &= hits - 1) {
+        if (hit++ % S != rank) continue;
         const int k = __ffs(hits) - 1, tile = t0 + k, s = nq % NST;
         const int in_lo = __shfl_sync(0xffffffffu, b.z, k);
         const int in_hi = __shfl_sync(0xffffffffu, b.w, k);
@@ -519,13 +531,66 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     ok = wait_warp(&sm.out_full, 0, abort_flag, err) && ok;
     ok = __all_sync(0xffffffffu, ok && !*abort_flag);
     tc_fence_after();
-    constexpr uint32_t kStage = BM * (DH * 2 + 16);
-    static_assert(kStage <= sizeof(sm.q) && kStage <= sizeof(sm.go), "staging fits in the ring");
-    const size_t at = (static_cast<size_t>(g) * a.Nk + j0) * DH;
-    store_block<DH, NWG>(tbase + lane_off + C::dK, a.tau, n == 0, &sm.q[0][0][0], wg, r,
-                    threadIdx.x - 64, key_end - j0, ok, static_cast<__nv_bfloat16*>(a.dK) + at);
-    store_block<DH, NWG>(tbase + lane_off + C::dV, 1.f, n == 0, &sm.go[0][0][0], wg, r,
-                    threadIdx.x - 64, key_end - j0, ok, static_cast<__nv_bfloat16*>(a.dV) + at);
+    if (S == 1) {
+      constexpr uint32_t kStage = BM * (DH * 2 + 16);
+      static_assert(kStage <= sizeof(sm.q) && kStage <= sizeof(sm.go), "staging fits in the ring");
+      const size_t at = (static_cast<size_t>(g) * a.Nk + j0) * DH;
+      store_block<DH, NWG>(tbase + lane_off + C::dK, a.tau, n == 0, &sm.q[0][0][0], wg, r,
+                           threadIdx.x - 64, key_end - j0, ok,
+                           static_cast<__nv_bfloat16*>(a.dK) + at);
+      store_block<DH, NWG>(tbase + lane_off + C::dV, 1.f, n == 0, &sm.go[0][0][0], wg, r,
+                           threadIdx.x - 64, key_end - j0, ok,
+                           static_cast<__nv_bfloat16*>(a.dV) + at);
+    } else {
+      // This block's partial rows dK | dV, fp32, over the idle tiles.
+      float* row = reinterpret_cast<float*>(&sm.k[0][0]) + r * kPartLd<DH>;
+#pragma unroll
+      for (int c = 0; c < 2 * DH / NWG; c += 16) {
+        const int col = 2 * DH / NWG * wg + c;
+        uint32_t v[16];
+        tmem_ld16(tbase + lane_off + C::dK + col, v);
+        tmem_wait_ld();
+        const float scale = col < DH ? a.tau : 1.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          reinterpret_cast<float4*>(row + col)[k] =
+              n == 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
+                     : make_float4(scale * u2f(v[4 * k]), scale * u2f(v[4 * k + 1]),
+                                   scale * u2f(v[4 * k + 2]), scale * u2f(v[4 * k + 3]));
+      }
+    }
+  }
+
+  if (S > 1) {
+    // Rank q sums key rows [128 q / S, 128 (q + 1) / S) over the cluster.  All
+    // threads pass both barriers; the second keeps every block's rows alive
+    // until all reads are done.
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 2) {
+      const int rb = BM * rank / S, re = min(BM * (rank + 1) / S, a.Nk - j0);
+      const uint32_t part = smem_u32(&sm.k[0][0]);
+      constexpr int kRow4 = DH / 2;  // float4 of a row dK | dV
+      for (int e = threadIdx.x - 64; e < (re - rb) * kRow4; e += 128 * NWG) {
+        const int rr = rb + e / kRow4, c4 = e % kRow4;
+        const uint32_t off = static_cast<uint32_t>((rr * kPartLd<DH> + 4 * c4) * 4);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < S; ++p) {
+          const float4 v = ld_shared_cluster_f4(mapa_shared(part + off, p));
+          sum.x += v.x;
+          sum.y += v.y;
+          sum.z += v.z;
+          sum.w += v.w;
+        }
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(4 * c4 < DH ? a.dK : a.dV);
+        const size_t at = (static_cast<size_t>(g) * a.Nk + j0 + rr) * DH + 4 * c4 % DH;
+        if (!*abort_flag)
+          *reinterpret_cast<uint2*>(out + at) =
+              make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+      }
+    }
+    __syncwarp();
+    cluster_sync();
   }
 
   tc_fence_before();
@@ -535,6 +600,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
+}
+
+// How many blocks share a key block: a power of two up to 8 that makes up to
+// kGridPerSM blocks for each SM, with two row tiles at least for each.  Unequal
+// key blocks (a causal mask) then even out, too: 128 of them with 4 to 64 tiles
+// took 166 us alone.
+constexpr int kGridPerSM = 4;
+int cluster_size(const AttnArgs& a) {
+  const long long blocks = static_cast<long long>((a.Nk + BM - 1) / BM) * a.B * a.Hkv;
+  const long long tiles = (static_cast<long long>(a.H / a.Hkv) * a.Nq + BQ - 1) / BQ;
+  int S = 1;
+  while (S < 8 && blocks * S * 2 <= kGridPerSM * kSMs && tiles >= S * 4) S *= 2;
+  return S;
 }
 
 template <int DH, bool CAP, bool BIAS>
@@ -551,10 +629,24 @@ cudaError_t launch(const AttnArgs& a) {
   const auto kernel = tc_dkv_kernel<DH, CAP, BIAS>;
   e = tc_set_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const long long grid = static_cast<long long>((a.Nk + BM - 1) / BM) * heads;
+  // The staged rows lie over K, V, Q and dO, which follow one another.
+  static_assert(BM * kPartLd<DH> * 4 <= offsetof(SmemK<DH>, ex), "partial rows fit in the tiles");
+  const int S = cluster_size(a);
+  const long long grid = static_cast<long long>((a.Nk + BM - 1) / BM) * heads * S;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  kernel<<<static_cast<unsigned>(grid), NTHREADS, smem, a.stream>>>(mq, mo, mk, mv, a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(NTHREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, mq, mo, mk, mv, a, S);
 }
 
 template <int DH>
