@@ -274,11 +274,8 @@ int attn_splits(const AttnArgs& a) {
   if (tc_attn_supported(a)) return tc_attn_splits(a);
   const long long blocks = static_cast<long long>(a.B) * a.Hkv *
                            ((static_cast<long long>(a.H / a.Hkv) * a.Nq + 63) / 64);
-  const int tiles = (a.Nk + 63) / 64;
-  if (blocks * 2 > kSMs) return 1;
-  const long long s = kSMs / blocks;
-  const long long most = tiles / 4 > 1 ? tiles / 4 : 1;  // four tiles at least in each run
-  return static_cast<int>(s < most ? s : most);
+  const long long tiles = (a.Nk + 63) / 64, s = kSMs / blocks;
+  return s < 2 || tiles < 2 ? 1 : static_cast<int>(s < tiles ? s : tiles);
 }
 
 }  // namespace flashbob

@@ -15,9 +15,14 @@
 // row sit in half a warp and row reductions are four shuffles.  A score step
 // of 4 along d costs 8 16-byte shared loads for 64 multiply-adds, rows
 // padded by 4 floats against bank conflicts: the multiply-adds bound it.
+// Grids that leave SMs idle are cut along the streamed side: the forward into
+// runs joined by a second launch, dQ and dK, dV into clusters whose blocks sum
+// their parts through distributed shared memory in the order of the ranks
+// (B2 H3 N333 d80: forward 59 -> 29 us, gradient 146 -> 60 us).
 #include <math.h>
 
 #include "attn_common.cuh"
+#include "tc_common.cuh"
 
 namespace flashbob {
 namespace {
@@ -166,6 +171,47 @@ __device__ __forceinline__ void load_rows(Rows& s, const AttnArgs& a, int row0, 
   __syncthreads();
 }
 
+// The block's 64 x d sums (times scale) to global rows row0 .. of `rows`.  In a
+// cluster of S blocks each stages its part in shared memory (pitch kLd) and
+// writes the rows of its rank.
+template <typename T, int DP>
+__device__ __forceinline__ void stage_rows(float* stage, const float (&acc)[4][DP / 16], int ty,
+                                           int tx, float scale) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < DP / 32; ++c)
+      *reinterpret_cast<float2*>(stage + (ty + 16 * i) * kLd<DP> + 2 * tx + 32 * c) =
+          make_float2(scale * acc[i][2 * c], scale * acc[i][2 * c + 1]);
+}
+template <typename T, int DP>
+__device__ __forceinline__ void write_rows(const float* stage, T* __restrict__ out, int live, int d,
+                                           int rank, int S) {
+  const int rb = BT * rank / S, re = min(BT * (rank + 1) / S, live);
+  const uint32_t base = tc::smem_u32(stage);
+  for (int x = threadIdx.x; x < (re - rb) * (DP / 4); x += NT) {
+    const int r = rb + x / (DP / 4), k = 4 * (x % (DP / 4));
+    if (k >= d) continue;
+    float4 sum = *reinterpret_cast<const float4*>(stage + r * kLd<DP> + k);
+    if (S > 1) {
+      sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int p = 0; p < S; ++p) {
+        const float4 v = tc::ld_shared_cluster_f4(
+            tc::mapa_shared(base + static_cast<uint32_t>((r * kLd<DP> + k) * 4), p));
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+      }
+    }
+    T* o = out + static_cast<size_t>(r) * d + k;
+    put(o, sum.x);
+    if (k + 1 < d) put(o + 1, sum.y);
+    if (k + 2 < d) put(o + 2, sum.z);
+    if (k + 3 < d) put(o + 3, sum.w);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Forward: one pass over the key tiles of the hull with the running maximum
 // and sum; with splits > 1 the block takes one run of those tiles and leaves
@@ -280,7 +326,8 @@ __global__ void __launch_bounds__(NT) attn_kernel(const __grid_constant__ AttnAr
 // dQ: 64 group rows resident, key tiles of the hull stream past.
 // ---------------------------------------------------------------------------
 template <typename T, int DP>
-__global__ void __launch_bounds__(NT) attn_dq_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(NT)
+    attn_dq_kernel(const __grid_constant__ AttnArgs a, int S) {
   extern __shared__ float sm[];
   float* Qs = sm;
   float* dOs = Qs + BT * kLd<DP>;
@@ -288,7 +335,8 @@ __global__ void __launch_bounds__(NT) attn_dq_kernel(const __grid_constant__ Att
   float* Vs = Ks + BT * kLd<DP>;
   float* Ps = Vs + BT * kLd<DP>;
   __shared__ Rows rs;
-  const int rows = a.H / a.Hkv * a.Nq, row0 = blockIdx.x * BT;
+  const int rank = blockIdx.x % S;
+  const int rows = a.H / a.Hkv * a.Nq, row0 = blockIdx.x / S * BT;
   const int g = blockIdx.z * a.Hkv + blockIdx.y;
   const T* Q = static_cast<const T*>(a.Q) + static_cast<size_t>(g) * rows * a.d;
   const T* dO = static_cast<const T*>(a.dO) + static_cast<size_t>(g) * rows * a.d;
@@ -313,7 +361,7 @@ __global__ void __launch_bounds__(NT) attn_dq_kernel(const __grid_constant__ Att
 #pragma unroll
     for (int c = 0; c < DP / 16; ++c) acc[i][c] = 0.f;
   }
-  for (int t = t0; t < t1; ++t) {
+  for (int t = t0 + rank; t < t1; t += S) {
     __syncthreads();
     load_tile<T, DP>(Ks, K, t * BT, first, last, a.d);
     load_tile<T, DP>(Vs, V, t * BT, first, last, a.d);
@@ -341,19 +389,13 @@ __global__ void __launch_bounds__(NT) attn_dq_kernel(const __grid_constant__ Att
     __syncwarp();
     out_tile<DP>(Ps, Ks, ty, tx, acc);
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = row0 + ty + 16 * i;
-    if (r >= rows) continue;
-    T* out = static_cast<T*>(a.dQ) + (static_cast<size_t>(g) * rows + r) * a.d;
-#pragma unroll
-    for (int c = 0; c < DP / 32; ++c)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int k = 2 * tx + 32 * c + e;
-        if (k < a.d) put(out + k, a.tau * acc[i][2 * c + e]);
-      }
-  }
+  __syncthreads();
+  stage_rows<T, DP>(Qs, acc, ty, tx, a.tau);
+  if (S > 1) tc::cluster_sync();
+  else __syncthreads();
+  write_rows<T, DP>(Qs, static_cast<T*>(a.dQ) + (static_cast<size_t>(g) * rows + row0) * a.d,
+                    rows - row0, a.d, rank, S);
+  if (S > 1) tc::cluster_sync();  // the staged rows stay until all are read
 }
 
 // ---------------------------------------------------------------------------
@@ -362,7 +404,8 @@ __global__ void __launch_bounds__(NT) attn_dq_kernel(const __grid_constant__ Att
 // its query heads on chip.
 // ---------------------------------------------------------------------------
 template <typename T, int DP>
-__global__ void __launch_bounds__(NT) attn_dkv_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(NT)
+    attn_dkv_kernel(const __grid_constant__ AttnArgs a, int S) {
   extern __shared__ float sm[];
   float* Ks = sm;
   float* Vs = Ks + BT * kLd<DP>;
@@ -372,7 +415,8 @@ __global__ void __launch_bounds__(NT) attn_dkv_kernel(const __grid_constant__ At
   float* Ss = Ps + BT * LP;
   __shared__ int4 info[BT];
   __shared__ float2 lds[BT];
-  const int rows = a.H / a.Hkv * a.Nq, key0 = blockIdx.x * BT;
+  const int rank = blockIdx.x % S;
+  const int rows = a.H / a.Hkv * a.Nq, key0 = blockIdx.x / S * BT;
   const int g = blockIdx.z * a.Hkv + blockIdx.y;
   const T* Q = static_cast<const T*>(a.Q) + static_cast<size_t>(g) * rows * a.d;
   const T* dO = static_cast<const T*>(a.dO) + static_cast<size_t>(g) * rows * a.d;
@@ -390,9 +434,11 @@ __global__ void __launch_bounds__(NT) attn_dkv_kernel(const __grid_constant__ At
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int c = 0; c < DP / 16; ++c) ak[i][c] = av[i][c] = 0.f;
+  int hit = 0;
   for (int t = 0; t * BT < rows; ++t) {
     const int4 b = bounds[t];
     if (b.x >= key0 + BT || b.y <= key0) continue;  // no row of the tile sees a key of the block
+    if (hit++ % S != rank) continue;
     __syncthreads();
     if (threadIdx.x < BT) {
       const size_t at = static_cast<size_t>(g) * gr.pitch + t * BT + threadIdx.x;
@@ -433,30 +479,41 @@ __global__ void __launch_bounds__(NT) attn_dkv_kernel(const __grid_constant__ At
     out_tile<DP>(Ps, dOs, ty, tx, av);
     out_tile<DP>(Ss, Qs, ty, tx, ak);
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int key = key0 + ty + 16 * i;
-    if (key >= a.Nk) continue;
-    const size_t at = (static_cast<size_t>(g) * a.Nk + key) * a.d;
-#pragma unroll
-    for (int c = 0; c < DP / 32; ++c)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int k = 2 * tx + 32 * c + e;
-        if (k < a.d) {
-          put(static_cast<T*>(a.dK) + at + k, a.tau * ak[i][2 * c + e]);
-          put(static_cast<T*>(a.dV) + at + k, av[i][2 * c + e]);
-        }
-      }
-  }
+  __syncthreads();
+  stage_rows<T, DP>(Qs, ak, ty, tx, a.tau);
+  stage_rows<T, DP>(dOs, av, ty, tx, 1.f);
+  if (S > 1) tc::cluster_sync();
+  else __syncthreads();
+  const size_t at = (static_cast<size_t>(g) * a.Nk + key0) * a.d;
+  write_rows<T, DP>(Qs, static_cast<T*>(a.dK) + at, a.Nk - key0, a.d, rank, S);
+  write_rows<T, DP>(dOs, static_cast<T*>(a.dV) + at, a.Nk - key0, a.d, rank, S);
+  if (S > 1) tc::cluster_sync();
+}
+
+// Blocks of a cluster that share one block's streamed tiles.
+int cluster_size(const AttnArgs& a, long long blocks, long long tiles) {
+  int S = 1;
+  while (S < 8 && blocks * a.Hkv * a.B * S * 2 <= 2 * kSMs && tiles >= S * 2) S *= 2;
+  return S;
 }
 
 template <typename K>
-cudaError_t launch(K kernel, size_t smem, dim3 grid, cudaStream_t stream, const AttnArgs& a) {
+cudaError_t launch(K kernel, size_t smem, int blocks, int S, const AttnArgs& a) {
   const cudaError_t e = tc_set_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  kernel<<<grid, NT, smem, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks * S, a.Hkv, a.B);
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, S);
 }
 
 template <typename T, int DP>
@@ -473,11 +530,12 @@ cudaError_t run(const AttnArgs& a, bool grad) {
     e = cudaGetLastError();
     return e == cudaSuccess && splits > 1 ? attn_join(a, splits) : e;
   }
-  cudaError_t e =
-      launch(attn_dq_kernel<T, DP>, 4 * tile + square, dim3(blocks, a.Hkv, a.B), a.stream, a);
+  const int key_blocks = (a.Nk + BT - 1) / BT;
+  cudaError_t e = launch(attn_dq_kernel<T, DP>, 4 * tile + square, blocks,
+                         cluster_size(a, blocks, key_blocks), a);
   if (e == cudaSuccess)
-    e = launch(attn_dkv_kernel<T, DP>, 4 * tile + 2 * square,
-               dim3((a.Nk + BT - 1) / BT, a.Hkv, a.B), a.stream, a);
+    e = launch(attn_dkv_kernel<T, DP>, 4 * tile + 2 * square, key_blocks,
+               cluster_size(a, key_blocks, blocks), a);
   return e;
 }
 
