@@ -9,12 +9,11 @@
 // (bf16) replaces the scores as the A operand of P~ V.  Each warpgroup has its
 // own O~ accumulator and raises its m only when a unit's maximum exceeds it by
 // more than 8 (log2 units), so O~ is rarely rescaled.
-//   MT = 2: 256 group rows a block, warpgroup w holds rows 128 w .. and both
-//     take every key tile, so a tile from L2 feeds twice the products: for
-//     calls with enough rows.
-//   MT = 1: 128 group rows, the warpgroups take alternate key tiles and merge
-//     their (m, l, O~) at the end: for few rows (tokens over a cache), where
-//     the keys are also cut into runs of blocks joined by a second launch.
+//   MT = 1: 128 group rows a block, the warpgroups take alternate key tiles and
+//     merge their (m, l, O~) at the end.  Where rows are few (tokens over a
+//     cache) the keys are also cut into runs of blocks joined by a second launch.
+//   MT = 2: 256 group rows, warpgroup w holds rows 128 w .. and both take every
+//     key tile, so a tile from L2 feeds twice the products (see two_blocks).
 // Key tiles outside the hull of the block's ranges are not visited; tiles
 // inside every row's range run without a mask.  V rows outside the hull are
 // zeroed in shared memory before they meet P~ = 0, so a cache may hold
@@ -463,11 +462,14 @@ bool tc_attn_supported(const AttnArgs& a) { return a.bf16 && (a.d == 64 || a.d =
 
 namespace {
 
-// 256 rows a block where a group has more than 128 and such blocks fill the
-// GPU; 128 rows below.
+// 256 rows a block at d = 128 where such blocks fill the GPU twice (B1 H8
+// N16384: 747 us, with 128 rows 791); 128 rows below (B2 H16 Hkv4 N2047: 79 us,
+// with 256 rows, 1.7 waves, 101) and at d = 64 always (524 us, with 256 rows
+// 581: the smaller tiles leave the key stream far from L2's rate).
 bool two_blocks(const AttnArgs& a) {
   const long long rows = static_cast<long long>(a.H / a.Hkv) * a.Nq;
-  return rows > BM && static_cast<long long>(a.B) * a.Hkv * ((rows + 255) / 256) >= kSMs;
+  return a.d == 128 && rows > BM &&
+         static_cast<long long>(a.B) * a.Hkv * ((rows + 255) / 256) >= 2 * kSMs;
 }
 
 }  // namespace
@@ -488,8 +490,8 @@ int tc_attn_splits(const AttnArgs& a) {
 cudaError_t tc_attn(const AttnArgs& a) {
   const int splits = tc_attn_splits(a);
   cudaError_t e;
-  if (two_blocks(a)) e = a.d == 64 ? launch<64, 2>(a, splits) : launch<128, 2>(a, splits);
-  else e = a.d == 64 ? launch<64, 1>(a, splits) : launch<128, 1>(a, splits);
+  if (a.d == 64) e = launch<64, 1>(a, splits);
+  else e = two_blocks(a) ? launch<128, 2>(a, splits) : launch<128, 1>(a, splits);
   return e == cudaSuccess && splits > 1 ? attn_join(a, splits) : e;
 }
 
