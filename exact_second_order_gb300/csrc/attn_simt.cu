@@ -512,7 +512,7 @@ cudaError_t launch(K kernel, size_t smem, int blocks, int S, const AttnArgs& a) 
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = S > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, a, S);
 }
 

@@ -645,7 +645,7 @@ cudaError_t launch(const AttnArgs& a) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = S > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, mq, mo, mk, mv, a, S);
 }
 

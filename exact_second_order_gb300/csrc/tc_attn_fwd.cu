@@ -476,9 +476,10 @@ bool two_blocks(const AttnArgs& a) {
 
 // How many runs the keys are cut into: as many as fill the SMs once, with
 // kSplitKeys keys at least in each.  (More runs than SMs only add to the join:
-// 8 groups of 65536 keys 28 us, with twice the runs 40 us; 128 and 512 keys
-// were within 10% of 256.)
-constexpr int kSplitKeys = 256;
+// 8 groups of 65536 keys 28 us, with twice the runs 40 us.  With 256 keys a run
+// the calls between 512 and 8192 keys gain up to 2 us of 20 on the GPU, but the
+// short ones wait for the host, and the join is another launch.)
+constexpr int kSplitKeys = 512;
 int tc_attn_splits(const AttnArgs& a) {
   const long long rows = static_cast<long long>(a.H / a.Hkv) * a.Nq;
   const long long blocks = static_cast<long long>(a.B) * a.Hkv * ((rows + BM - 1) / BM);

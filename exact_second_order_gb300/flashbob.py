@@ -12,6 +12,8 @@ import ctypes
 import functools
 import os
 
+torch = None  # bound by _ready(): building and loading the library need no torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libflashbob.so")
 
@@ -78,6 +80,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
+_bound = None  # the library, once torch is bound too
+
+
+def _ready() -> ctypes.CDLL:
+    """load_library() for the calls that work on tensors at once."""
+    global torch, _bound
+    import torch as module
+    torch = module
+    _bound = load_library()
+    return _bound
+
+
 def _dtype_code(t) -> int:
     import torch
     if t.dtype == torch.float32:
@@ -89,8 +103,8 @@ def _dtype_code(t) -> int:
 
 def _stream_handle(stream) -> int | None:
     import torch
-    if stream is None:  # the current device's current stream
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -135,15 +149,10 @@ def _input_specs(Q, K, V, dO, UQ, UK, UV):
             ("UV", UV, "k", "in")]
 
 
-_NOTHING = contextlib.nullcontext()
-
-
 def _device(t):
     """The CUDA device context of tensor ``t``: the library works on the
     current device, so every call runs with its tensors' device current."""
     import torch
-    if t.is_cuda and torch.cuda.current_device() == t.get_device():
-        return _NOTHING
     return torch.cuda.device(t.device)
 
 
@@ -240,49 +249,92 @@ def flashbob_attention_jvp(Q, K, V, O, L, UQ, UK, UV, tau: float, Od, Ld,
         raise FlashbobError(st, "flashbob_attention_jvp")
 
 
-def _check_tensor(where: str, name: str, t, shape, dtype, device) -> None:
-    """One tensor of a call: a contiguous CUDA tensor on ``device`` with the
+# ---------------------------------------------------------------------------
+# The operators around an attention layer.  Their calls are short (a token of
+# one request is ten microseconds of GPU time), so the checks ask a tensor each
+# thing once and the contexts are entered only where they change something.
+# ---------------------------------------------------------------------------
+
+def _cuda_index(where: str, name: str, t, shape_text: str, dims: int) -> int:
+    """The CUDA device of the tensor that fixes a call's sizes."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != dims:
+        raise ValueError(f"{where}: {name} must be a {dims}-d CUDA tensor {shape_text}")
+    return t.get_device()
+
+
+def _check_tensor(where: str, name: str, t, shape, dtype, index: int) -> None:
+    """One tensor of a call: contiguous, on CUDA device ``index``, with the
     shape and dtype of its role."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
-        raise ValueError(f"{where}: {name} must be a CUDA tensor on {device}")
+    try:
+        if (t.get_device() == index and t.shape == shape and t.dtype is dtype
+                and t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"{where}: {name} must be a CUDA tensor on cuda:{index}")
     if t.shape != shape:
         raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{where}: {name} is {t.dtype}, expected {dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{where}: {name} must be contiguous")
+    raise ValueError(f"{where}: {name} must be contiguous")
 
 
-def _check_4d(where: str, **tensors) -> None:
-    import torch
-    for name, t in tensors.items():
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
-            raise ValueError(f"{where}: {name} must be a 4-d CUDA tensor")
+def _check_workspace(where: str, t, index: int) -> None:
+    if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda
+                              and t.get_device() == index and t.is_contiguous()):
+        raise ValueError(f"{where}: workspace must be a contiguous CUDA tensor on cuda:{index}")
 
 
-def _check_attention(where: str, Q, K, V, slopes, ranges, q_pos):
-    """Checks of the inputs that the attention calls with key ranges share;
-    returns the sizes."""
-    import torch
-    _check_4d(where, Q=Q, K=K)
-    B, H, Nq, d = Q.shape
-    _, Hkv, Nk, _ = K.shape
-    dev, dt = Q.device, Q.dtype
-    _check_tensor(where, "Q", Q, (B, H, Nq, d), dt, dev)
-    _check_tensor(where, "K", K, (B, Hkv, Nk, d), dt, dev)
-    _check_tensor(where, "V", V, (B, Hkv, Nk, d), dt, dev)
-    if slopes is not None:
-        _check_tensor(where, "slopes", slopes, (H,), torch.float32, dev)
-    if ranges is not None:
-        _check_tensor(where, "ranges", ranges, (B, Nq, 2), torch.int32, dev)
-    if q_pos is not None:
-        _check_tensor(where, "q_pos", q_pos, (B, Nq), torch.int32, dev)
-    return B, H, Hkv, Nq, Nk, d
+@contextlib.contextmanager
+def _entered(index: int, stream):
+    with torch.cuda.device(index):
+        if stream is None:
+            yield
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=index)
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _elsewhere(index: int, stream):
+    """None when CUDA device ``index`` and its current stream are what a call
+    works on; else the context that makes them so.  What a wrapper allocates
+    and frees inside (a workspace) is then reused in that stream's order."""
+    if stream is None and torch._C._cuda_getDevice() == index:
+        return None
+    return _entered(index, stream)
+
+
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _bytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
+
+
+def _check_attention(where: str, Q, K, V, slopes, ranges, q_pos):
+    """Checks of the inputs that the attention calls with key ranges share;
+    returns the device, the sizes and the dtype code."""
+    index = _cuda_index(where, "Q", Q, "[B, H, Nq, d]", 4)
+    _cuda_index(where, "K", K, "[B, Hkv, Nk, d]", 4)
+    dt = Q.dtype
+    B, H, Nq, d = Q.shape
+    _, Hkv, Nk, _ = key = K.shape
+    if key[0] != B or key[3] != d:
+        raise ValueError(f"{where}: K has shape {tuple(key)}, expected {(B, Hkv, Nk, d)}")
+    _check_tensor(where, "Q", Q, Q.shape, dt, index)
+    _check_tensor(where, "K", K, key, dt, index)
+    _check_tensor(where, "V", V, key, dt, index)
+    if slopes is not None:
+        _check_tensor(where, "slopes", slopes, (H,), torch.float32, index)
+    if ranges is not None:
+        _check_tensor(where, "ranges", ranges, (B, Nq, 2), torch.int32, index)
+    if q_pos is not None:
+        _check_tensor(where, "q_pos", q_pos, (B, Nq), torch.int32, index)
+    return index, (B, H, Hkv, Nq, Nk, d), _dtype_code(Q)
 
 
 @functools.lru_cache(maxsize=256)
@@ -297,12 +349,12 @@ def flashbob_attention_workspace(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: 
     return n[0].value, n[1].value
 
 
-def _run_attention(sizes, Q, K, V, ranges, q_pos, slopes, tau, cap, O, L, workspace, causal,
-                   stream) -> None:
-    st = load_library().flashbob_attention(
-        Q.data_ptr(), K.data_ptr(), V.data_ptr(), _ptr(ranges), _ptr(q_pos), _ptr(slopes), tau,
-        cap, O.data_ptr(), L.data_ptr(), _ptr(workspace), _bytes(workspace), *sizes, int(causal),
-        _dtype_code(Q), _stream_handle(stream))
+def _run_attention(lib, index, sizes, code, Q, K, V, ranges, q_pos, slopes, tau, cap, O, L,
+                   workspace, causal) -> None:
+    st = lib.flashbob_attention(
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), _ptr(ranges), _ptr(q_pos), _ptr(slopes),
+        float(tau), float(cap), O.data_ptr(), L.data_ptr(), _ptr(workspace), _bytes(workspace), *sizes, int(causal),
+        code, _raw_stream(index))
     if st != FLASHBOB_OK:
         raise FlashbobError(st, "flashbob_attention")
 
@@ -311,130 +363,261 @@ def flashbob_attention(Q, K, V, ranges, q_pos, slopes, tau: float, cap: float, O
                        causal: bool = False, stream=None) -> None:
     """O, L of attention with key ranges (see flashbob_attention in the header);
     ``workspace`` is any contiguous CUDA tensor of enough bytes, or None."""
-    import torch
-    where = "flashbob_attention"
-    sizes = _check_attention(where, Q, K, V, slopes, ranges, q_pos)
-    _check_tensor(where, "O", O, Q.shape, Q.dtype, Q.device)
-    _check_tensor(where, "L", L, Q.shape[:3], torch.float32, Q.device)
-    _check_workspace(where, workspace, Q.device)
-    with _device(Q):
-        _run_attention(sizes, Q, K, V, ranges, q_pos, slopes, tau, cap, O, L, workspace, causal,
-                       stream)
+    lib, where = _bound or _ready(), "flashbob_attention"
+    index, sizes, code = _check_attention(where, Q, K, V, slopes, ranges, q_pos)
+    _check_tensor(where, "O", O, Q.shape, Q.dtype, index)
+    _check_tensor(where, "L", L, Q.shape[:3], torch.float32, index)
+    _check_workspace(where, workspace, index)
+    with _elsewhere(index, stream) or contextlib.nullcontext():
+        _run_attention(lib, index, sizes, code, Q, K, V, ranges, q_pos, slopes, tau, cap, O, L,
+                       workspace, causal)
 
 
-def _run_attention_grad(sizes, Q, K, V, O, L, dO, ranges, q_pos, slopes, tau, cap, dQ, dK, dV,
-                        workspace, causal, stream) -> None:
-    st = load_library().flashbob_attention_grad(
-        Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), L.data_ptr(), dO.data_ptr(),
-        _ptr(ranges), _ptr(q_pos), _ptr(slopes), tau, cap, dQ.data_ptr(), dK.data_ptr(),
-        dV.data_ptr(), _ptr(workspace), _bytes(workspace), *sizes, int(causal), _dtype_code(Q),
-        _stream_handle(stream))
-    if st != FLASHBOB_OK:
-        raise FlashbobError(st, "flashbob_attention_grad")
+def attention(Q, K, V, tau: float, cap: float = 0.0, slopes=None, ranges=None, q_pos=None,
+              causal: bool = False, stream=None):
+    """O (of Q's dtype) and L of attention with capped scores, a distance bias
+    and key ranges; allocates them, and the workspace, on Q's device."""
+    lib = _bound or _ready()
+    index, sizes, code = _check_attention("attention", Q, K, V, slopes, ranges, q_pos)
+    need = flashbob_attention_workspace(*sizes, code)[0]
+
+    def run():
+        O = torch.empty_like(Q)
+        L = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=Q.device) if need else None
+        _run_attention(lib, index, sizes, code, Q, K, V, ranges, q_pos, slopes, tau, cap, O, L,
+                       workspace, causal)
+        return O, L
+
+    context = _elsewhere(index, stream)
+    if context is None:
+        return run()
+    with context:
+        return run()
 
 
 def _check_attention_grad(where: str, Q, K, V, O, L, dO, slopes, ranges, q_pos):
-    import torch
-    sizes = _check_attention(where, Q, K, V, slopes, ranges, q_pos)
-    _check_tensor(where, "O", O, Q.shape, Q.dtype, Q.device)
-    _check_tensor(where, "L", L, Q.shape[:3], torch.float32, Q.device)
-    _check_tensor(where, "dO", dO, Q.shape, Q.dtype, Q.device)
-    return sizes
+    checked = _check_attention(where, Q, K, V, slopes, ranges, q_pos)
+    _check_tensor(where, "O", O, Q.shape, Q.dtype, checked[0])
+    _check_tensor(where, "L", L, Q.shape[:3], torch.float32, checked[0])
+    _check_tensor(where, "dO", dO, Q.shape, Q.dtype, checked[0])
+    return checked
+
+
+def _run_attention_grad(lib, index, sizes, code, Q, K, V, O, L, dO, ranges, q_pos, slopes, tau,
+                        cap, dQ, dK, dV, workspace, causal) -> None:
+    st = lib.flashbob_attention_grad(
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), L.data_ptr(), dO.data_ptr(),
+        _ptr(ranges), _ptr(q_pos), _ptr(slopes), float(tau), float(cap), dQ.data_ptr(), dK.data_ptr(),
+        dV.data_ptr(), _ptr(workspace), _bytes(workspace), *sizes, int(causal), code,
+        _raw_stream(index))
+    if st != FLASHBOB_OK:
+        raise FlashbobError(st, "flashbob_attention_grad")
 
 
 def flashbob_attention_grad(Q, K, V, O, L, dO, ranges, q_pos, slopes, tau: float, cap: float,
                             dQ, dK, dV, workspace, causal: bool = False, stream=None) -> None:
     """dQ, dK, dV of attention with key ranges (see flashbob_attention_grad)."""
-    where = "flashbob_attention_grad"
-    sizes = _check_attention_grad(where, Q, K, V, O, L, dO, slopes, ranges, q_pos)
-    _check_tensor(where, "dQ", dQ, Q.shape, Q.dtype, Q.device)
-    _check_tensor(where, "dK", dK, K.shape, Q.dtype, Q.device)
-    _check_tensor(where, "dV", dV, K.shape, Q.dtype, Q.device)
-    _check_workspace(where, workspace, Q.device)
-    with _device(Q):
-        _run_attention_grad(sizes, Q, K, V, O, L, dO, ranges, q_pos, slopes, tau, cap, dQ, dK, dV,
-                            workspace, causal, stream)
+    lib, where = _bound or _ready(), "flashbob_attention_grad"
+    index, sizes, code = _check_attention_grad(where, Q, K, V, O, L, dO, slopes, ranges, q_pos)
+    _check_tensor(where, "dQ", dQ, Q.shape, Q.dtype, index)
+    _check_tensor(where, "dK", dK, K.shape, Q.dtype, index)
+    _check_tensor(where, "dV", dV, K.shape, Q.dtype, index)
+    _check_workspace(where, workspace, index)
+    with _elsewhere(index, stream) or contextlib.nullcontext():
+        _run_attention_grad(lib, index, sizes, code, Q, K, V, O, L, dO, ranges, q_pos, slopes, tau,
+                            cap, dQ, dK, dV, workspace, causal)
 
 
-def _check_workspace(where: str, t, device) -> None:
-    import torch
-    if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == device
-                              and t.is_contiguous()):
-        raise ValueError(f"{where}: workspace must be a contiguous CUDA tensor on {device}")
+def attention_grad(Q, K, V, O, L, dO, tau: float, cap: float = 0.0, slopes=None, ranges=None,
+                   q_pos=None, causal: bool = False, stream=None):
+    """dQ, dK, dV (of Q's dtype) of ``attention`` from its O and L and the
+    gradient dO; allocates them, and the workspace, on Q's device."""
+    lib = _bound or _ready()
+    index, sizes, code = _check_attention_grad("attention_grad", Q, K, V, O, L, dO, slopes, ranges,
+                                               q_pos)
+    need = flashbob_attention_workspace(*sizes, code)[1]
+
+    def run():
+        dQ, dK, dV = torch.empty_like(Q), torch.empty_like(K), torch.empty_like(K)
+        workspace = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        _run_attention_grad(lib, index, sizes, code, Q, K, V, O, L, dO, ranges, q_pos, slopes, tau,
+                            cap, dQ, dK, dV, workspace, causal)
+        return dQ, dK, dV
+
+    context = _elsewhere(index, stream)
+    if context is None:
+        return run()
+    with context:
+        return run()
+
+
+def _check_ranges(where: str, index: int, doc_offsets, prefix, q_start, B: int) -> int:
+    """Checks of the arrays that ranges are built from; returns the documents."""
+    M = 0
+    if doc_offsets is not None:
+        _cuda_index(where, "doc_offsets", doc_offsets, "[B, M + 1]", 2)
+        M = doc_offsets.shape[1] - 1
+        _check_tensor(where, "doc_offsets", doc_offsets, (B, M + 1), torch.int32, index)
+    if prefix is not None:
+        _check_tensor(where, "prefix", prefix, (B, M), torch.int32, index)
+    if q_start is not None:
+        _check_tensor(where, "q_start", q_start, (B,), torch.int32, index)
+    return M
+
+
+def _run_ranges(lib, index, doc_offsets, prefix, q_start, ranges, q_pos, B, M, Nq, Nk,
+                causal) -> None:
+    st = lib.flashbob_attention_ranges(
+        _ptr(doc_offsets), _ptr(prefix), _ptr(q_start), ranges.data_ptr(), _ptr(q_pos), B, M, Nq,
+        int(Nk), int(causal), _raw_stream(index))
+    if st != FLASHBOB_OK:
+        raise FlashbobError(st, "flashbob_attention_ranges")
 
 
 def flashbob_attention_ranges(doc_offsets, prefix, q_start, ranges, q_pos, Nk: int,
                               causal: bool = False, stream=None) -> None:
     """Key ranges of queries by document (see flashbob_attention_ranges)."""
-    import torch
-    where = "flashbob_attention_ranges"
-    if not isinstance(ranges, torch.Tensor) or ranges.dim() != 3:
-        raise ValueError(f"{where}: ranges must be a 3-d tensor [B, Nq, 2]")
-    B, Nq = ranges.shape[:2]
-    M = 0
-    if doc_offsets is not None:
-        if not isinstance(doc_offsets, torch.Tensor) or doc_offsets.dim() != 2:
-            raise ValueError(f"{where}: doc_offsets must be a 2-d tensor [B, M + 1]")
-        M = doc_offsets.shape[1] - 1
-    for name, t, shape in (("ranges", ranges, (B, Nq, 2)), ("q_pos", q_pos, (B, Nq)),
-                           ("doc_offsets", doc_offsets, (B, M + 1)), ("prefix", prefix, (B, M)),
-                           ("q_start", q_start, (B,))):
-        if t is not None:
-            _check_tensor(where, name, t, shape, torch.int32, ranges.device)
-    with _device(ranges):
-        st = load_library().flashbob_attention_ranges(
-            _ptr(doc_offsets), _ptr(prefix), _ptr(q_start), ranges.data_ptr(), _ptr(q_pos), B, M,
-            Nq, int(Nk), int(causal), _stream_handle(stream))
-    if st != FLASHBOB_OK:
-        raise FlashbobError(st, where)
+    lib, where = _bound or _ready(), "flashbob_attention_ranges"
+    index = _cuda_index(where, "ranges", ranges, "[B, Nq, 2]", 3)
+    B, Nq, _ = ranges.shape
+    _check_tensor(where, "ranges", ranges, (B, Nq, 2), torch.int32, index)
+    if q_pos is not None:
+        _check_tensor(where, "q_pos", q_pos, (B, Nq), torch.int32, index)
+    M = _check_ranges(where, index, doc_offsets, prefix, q_start, B)
+    with _elsewhere(index, stream) or contextlib.nullcontext():
+        _run_ranges(lib, index, doc_offsets, prefix, q_start, ranges, q_pos, B, M, Nq, Nk, causal)
 
 
-def _check_norm(where: str, QKV, H: int, Hkv: int, wq, wk, freqs, positions):
-    """Checks of the norm-and-rotation calls; returns B, N, d, R, axes."""
-    import torch
-    if not isinstance(QKV, torch.Tensor) or QKV.dim() != 4:
-        raise ValueError(f"{where}: QKV must be a 4-d tensor [B, N, H + 2 Hkv, d]")
-    B, N, _, d = QKV.shape
-    _check_tensor(where, "QKV", QKV, (B, N, H + 2 * Hkv, d), QKV.dtype, QKV.device)
+def attention_ranges(B: int, Nq: int, Nk: int, doc_offsets=None, prefix=None, q_start=None,
+                     causal: bool = False, device=None, stream=None):
+    """ranges [B, Nq, 2] and q_pos [B, Nq] of queries by document, on the
+    device of the first array given (``device``, or the current one, if none)."""
+    lib, where = _bound or _ready(), "attention_ranges"
+    given = doc_offsets if doc_offsets is not None else q_start
+    if given is not None:
+        device = given.device
+    else:
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else \
+            torch.device(device)
+    if device.type != "cuda":
+        raise ValueError(f"{where}: the arrays must be on a CUDA device, not {device}")
+    index = torch.cuda.current_device() if device.index is None else device.index
+    M = _check_ranges(where, index, doc_offsets, prefix, q_start, B)
+
+    def run():
+        ranges = torch.empty((B, Nq, 2), dtype=torch.int32, device=device)
+        q_pos = torch.empty((B, Nq), dtype=torch.int32, device=device)
+        _run_ranges(lib, index, doc_offsets, prefix, q_start, ranges, q_pos, B, M, Nq, Nk, causal)
+        return ranges, q_pos
+
+    context = _elsewhere(index, stream)
+    if context is None:
+        return run()
+    with context:
+        return run()
+
+
+def _check_norm(where: str, QKV, wq, wk, freqs, positions):
+    """Checks of the norm-and-rotation calls; returns the device and B, N, the
+    heads, d, R, axes."""
+    index = _cuda_index(where, "QKV", QKV, "[B, N, H + 2 Hkv, d]", 4)
+    _check_tensor(where, "QKV", QKV, QKV.shape, QKV.dtype, index)
+    B, N, heads, d = QKV.shape
     R, axes = 0, 1
     if freqs is not None:
-        if not isinstance(freqs, torch.Tensor) or freqs.dim() != 2:
-            raise ValueError(f"{where}: freqs must be a 2-d tensor [axes, R / 2]")
-        axes, R = freqs.shape[0], 2 * freqs.shape[1]
-        _check_tensor(where, "freqs", freqs, (axes, R // 2), torch.float32, QKV.device)
+        _cuda_index(where, "freqs", freqs, "[axes, R / 2]", 2)
+        axes, R = freqs.shape
+        _check_tensor(where, "freqs", freqs, freqs.shape, torch.float32, index)
+        R *= 2
     if positions is not None:
-        _check_tensor(where, "positions", positions, (axes, B, N), torch.int32, QKV.device)
-    for name, t in (("wq", wq), ("wk", wk)):
-        if t is not None:
-            _check_tensor(where, name, t, (d,), torch.float32, QKV.device)
-    return B, N, d, R, axes
+        _check_tensor(where, "positions", positions, (axes, B, N), torch.int32, index)
+    if wq is not None:
+        _check_tensor(where, "wq", wq, (d,), torch.float32, index)
+    if wk is not None:
+        _check_tensor(where, "wk", wk, (d,), torch.float32, index)
+    return index, (B, N, heads, d, R, axes)
+
+
+def _check_cache(where: str, QKV, H: int, K, V, kv_start, index: int, sizes):
+    """K, V (and the rows they get) beside a checked projection; returns Hkv, Nk."""
+    B, _, heads, d, _, _ = sizes
+    _cuda_index(where, "K", K, "[B, Hkv, Nk, d]", 4)
+    Hkv, Nk = K.shape[1], K.shape[2]
+    if H + 2 * Hkv != heads:
+        raise ValueError(f"{where}: QKV has {heads} heads, expected {H} + 2 * {Hkv}")
+    _check_tensor(where, "K", K, (B, Hkv, Nk, d), QKV.dtype, index)
+    _check_tensor(where, "V", V, (B, Hkv, Nk, d), QKV.dtype, index)
+    if kv_start is not None:
+        _check_tensor(where, "kv_start", kv_start, (B,), torch.int32, index)
+    return Hkv, Nk
+
+
+def _run_norm(lib, index, sizes, QKV, wq, wk, freqs, positions, kv_start, eps, Q, K, V, H, Hkv,
+              Nk, interleaved) -> None:
+    B, N, _, d, R, axes = sizes
+    st = lib.flashbob_qk_norm_rope(
+        QKV.data_ptr(), _ptr(wq), _ptr(wk), _ptr(freqs), _ptr(positions), _ptr(kv_start), float(eps),
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), B, N, H, Hkv, Nk, d, R, axes, int(interleaved),
+        _dtype_code(QKV), _raw_stream(index))
+    if st != FLASHBOB_OK:
+        raise FlashbobError(st, "flashbob_qk_norm_rope")
 
 
 def flashbob_qk_norm_rope(QKV, wq, wk, freqs, positions, kv_start, eps: float, Q, K, V,
                           interleaved: bool = False, stream=None) -> None:
     """Head-major Q, K, V of the packed projection, normed and rotated (see
     flashbob_qk_norm_rope in the header)."""
-    import torch
-    where = "flashbob_qk_norm_rope"
-    for name, t in (("Q", Q), ("K", K)):
-        if not isinstance(t, torch.Tensor) or t.dim() != 4:
-            raise ValueError(f"{where}: {name} must be a 4-d tensor [B, heads, rows, d]")
-    H, Hkv, Nk = Q.shape[1], K.shape[1], K.shape[2]
-    B, N, d, R, axes = _check_norm(where, QKV, H, Hkv, wq, wk, freqs, positions)
-    for name, t, shape in (("Q", Q, (B, H, N, d)), ("K", K, (B, Hkv, Nk, d)),
-                           ("V", V, (B, Hkv, Nk, d))):
-        _check_tensor(where, name, t, shape, QKV.dtype, QKV.device)
-    if kv_start is not None:
-        _check_tensor(where, "kv_start", kv_start, (B,), torch.int32, QKV.device)
-    with _device(QKV):
-        st = load_library().flashbob_qk_norm_rope(
-            _ptr(QKV), _ptr(wq), _ptr(wk), _ptr(freqs), _ptr(positions), _ptr(kv_start),
-            float(eps), _ptr(Q), _ptr(K), _ptr(V), B, N, H, Hkv, Nk, d, R, axes,
-            int(interleaved), _dtype_code(QKV), _stream_handle(stream))
-    if st != FLASHBOB_OK:
-        raise FlashbobError(st, where)
+    lib, where = _bound or _ready(), "flashbob_qk_norm_rope"
+    index, sizes = _check_norm(where, QKV, wq, wk, freqs, positions)
+    _cuda_index(where, "Q", Q, "[B, H, N, d]", 4)
+    H = Q.shape[1]
+    _check_tensor(where, "Q", Q, (sizes[0], H, sizes[1], sizes[3]), QKV.dtype, index)
+    Hkv, Nk = _check_cache(where, QKV, H, K, V, kv_start, index, sizes)
+    with _elsewhere(index, stream) or contextlib.nullcontext():
+        _run_norm(lib, index, sizes, QKV, wq, wk, freqs, positions, kv_start, eps, Q, K, V, H, Hkv,
+                  Nk, interleaved)
 
 
+def qk_norm_rope(QKV, H: int, wq=None, wk=None, freqs=None, positions=None, eps: float = 1e-6,
+                 interleaved: bool = False, K=None, V=None, kv_start=None, stream=None):
+    """Q, K, V (head-major) of the packed projection QKV with H query heads:
+    the norm of queries and keys for each head and the rotation by position.
+    Allocates them on QKV's device; K and V may be given (a cache, whose rows
+    kv_start[b] + n are written)."""
+    lib, where = _bound or _ready(), "qk_norm_rope"
+    index, sizes = _check_norm(where, QKV, wq, wk, freqs, positions)
+    B, N, heads, d, _, _ = sizes
+    if not 0 < H < heads or (heads - H) % 2:
+        raise ValueError(f"{where}: {heads} heads are not {H} query heads and two equal groups of "
+                         "key and value heads")
+    if (K is None) != (V is None):
+        raise ValueError(f"{where}: K and V are given together or not at all")
+    if K is not None:
+        Hkv, Nk = _check_cache(where, QKV, H, K, V, kv_start, index, sizes)
+    elif kv_start is not None:
+        raise ValueError(f"{where}: kv_start needs K and V")
+    else:
+        Hkv, Nk = (heads - H) // 2, N
+
+    def run():
+        Q = torch.empty((B, H, N, d), dtype=QKV.dtype, device=QKV.device)
+        k, v = K, V
+        if k is None:
+            k = torch.empty((B, Hkv, N, d), dtype=QKV.dtype, device=QKV.device)
+            v = torch.empty_like(k)
+        _run_norm(lib, index, sizes, QKV, wq, wk, freqs, positions, kv_start, eps, Q, k, v, H, Hkv,
+                  Nk, interleaved)
+        return Q, k, v
+
+    context = _elsewhere(index, stream)
+    if context is None:
+        return run()
+    with context:
+        return run()
+
+
+@functools.lru_cache(maxsize=256)
 def flashbob_qk_norm_rope_workspace(B: int, N: int, H: int, Hkv: int, d: int,
                                     in_dtype: int) -> int:
     """Workspace bytes of flashbob_qk_norm_rope_grad with gains."""
@@ -446,32 +629,72 @@ def flashbob_qk_norm_rope_workspace(B: int, N: int, H: int, Hkv: int, d: int,
     return n.value
 
 
+def _check_norm_grad(where: str, QKV, dQ, dK, dV, wq, wk, freqs, positions):
+    index, sizes = _check_norm(where, QKV, wq, wk, freqs, positions)
+    B, N, heads, d, _, _ = sizes
+    _cuda_index(where, "dQ", dQ, "[B, H, N, d]", 4)
+    _cuda_index(where, "dK", dK, "[B, Hkv, N, d]", 4)
+    H, Hkv = dQ.shape[1], dK.shape[1]
+    if H + 2 * Hkv != heads:
+        raise ValueError(f"{where}: QKV has {heads} heads, expected {H} + 2 * {Hkv}")
+    _check_tensor(where, "dQ", dQ, (B, H, N, d), dQ.dtype, index)
+    _check_tensor(where, "dK", dK, (B, Hkv, N, d), dQ.dtype, index)
+    _check_tensor(where, "dV", dV, (B, Hkv, N, d), dQ.dtype, index)
+    return index, sizes, H, Hkv
+
+
+def _run_norm_grad(lib, index, sizes, H, Hkv, QKV, wq, wk, freqs, positions, eps, dQ, dK, dV, dQKV,
+                   dwq, dwk, workspace, interleaved) -> None:
+    B, N, _, d, R, axes = sizes
+    st = lib.flashbob_qk_norm_rope_grad(
+        QKV.data_ptr(), _ptr(wq), _ptr(wk), _ptr(freqs), _ptr(positions), float(eps), dQ.data_ptr(),
+        dK.data_ptr(), dV.data_ptr(), dQKV.data_ptr(), _ptr(dwq), _ptr(dwk), _ptr(workspace),
+        _bytes(workspace), B, N, H, Hkv, d, R, axes, int(interleaved), _dtype_code(QKV),
+        _dtype_code(dQ), _raw_stream(index))
+    if st != FLASHBOB_OK:
+        raise FlashbobError(st, "flashbob_qk_norm_rope_grad")
+
+
 def flashbob_qk_norm_rope_grad(QKV, wq, wk, freqs, positions, eps: float, dQ, dK, dV, dQKV, dwq,
                                dwk, workspace, interleaved: bool = False, stream=None) -> None:
     """dQKV, dwq, dwk of flashbob_qk_norm_rope (see the header)."""
-    import torch
-    where = "flashbob_qk_norm_rope_grad"
-    for name, t in (("dQ", dQ), ("dK", dK)):
-        if not isinstance(t, torch.Tensor) or t.dim() != 4:
-            raise ValueError(f"{where}: {name} must be a 4-d tensor [B, heads, rows, d]")
-    H, Hkv = dQ.shape[1], dK.shape[1]
-    B, N, d, R, axes = _check_norm(where, QKV, H, Hkv, wq, wk, freqs, positions)
-    for name, t, shape in (("dQ", dQ, (B, H, N, d)), ("dK", dK, (B, Hkv, N, d)),
-                           ("dV", dV, (B, Hkv, N, d))):
-        _check_tensor(where, name, t, shape, dQ.dtype, QKV.device)
-    _check_tensor(where, "dQKV", dQKV, QKV.shape, QKV.dtype, QKV.device)
-    for name, t in (("dwq", dwq), ("dwk", dwk)):
-        if t is not None:
-            _check_tensor(where, name, t, (d,), torch.float32, QKV.device)
-    _check_workspace(where, workspace, QKV.device)
-    with _device(QKV):
-        st = load_library().flashbob_qk_norm_rope_grad(
-            _ptr(QKV), _ptr(wq), _ptr(wk), _ptr(freqs), _ptr(positions), float(eps), _ptr(dQ),
-            _ptr(dK), _ptr(dV), _ptr(dQKV), _ptr(dwq), _ptr(dwk), _ptr(workspace),
-            _bytes(workspace), B, N, H, Hkv, d, R, axes, int(interleaved), _dtype_code(QKV),
-            _dtype_code(dQ), _stream_handle(stream))
-    if st != FLASHBOB_OK:
-        raise FlashbobError(st, where)
+    lib, where = _bound or _ready(), "flashbob_qk_norm_rope_grad"
+    index, sizes, H, Hkv = _check_norm_grad(where, QKV, dQ, dK, dV, wq, wk, freqs, positions)
+    _check_tensor(where, "dQKV", dQKV, QKV.shape, QKV.dtype, index)
+    if dwq is not None:
+        _check_tensor(where, "dwq", dwq, (sizes[3],), torch.float32, index)
+    if dwk is not None:
+        _check_tensor(where, "dwk", dwk, (sizes[3],), torch.float32, index)
+    _check_workspace(where, workspace, index)
+    with _elsewhere(index, stream) or contextlib.nullcontext():
+        _run_norm_grad(lib, index, sizes, H, Hkv, QKV, wq, wk, freqs, positions, eps, dQ, dK, dV,
+                       dQKV, dwq, dwk, workspace, interleaved)
+
+
+def qk_norm_rope_grad(QKV, dQ, dK, dV, wq=None, wk=None, freqs=None, positions=None,
+                      eps: float = 1e-6, interleaved: bool = False, stream=None):
+    """dQKV, dwq, dwk of ``qk_norm_rope`` from the gradients of Q, K and V
+    (fp32 or bf16); dwq and dwk are None without gains."""
+    lib = _bound or _ready()
+    index, sizes, H, Hkv = _check_norm_grad("qk_norm_rope_grad", QKV, dQ, dK, dV, wq, wk, freqs,
+                                            positions)
+    need = 0 if wq is None else flashbob_qk_norm_rope_workspace(
+        sizes[0], sizes[1], H, Hkv, sizes[3], _dtype_code(QKV))
+
+    def run():
+        dQKV = torch.empty_like(QKV)
+        dwq = None if wq is None else torch.empty_like(wq)
+        dwk = None if wk is None else torch.empty_like(wk)
+        workspace = torch.empty(need, dtype=torch.uint8, device=QKV.device) if need else None
+        _run_norm_grad(lib, index, sizes, H, Hkv, QKV, wq, wk, freqs, positions, eps, dQ, dK, dV,
+                       dQKV, dwq, dwk, workspace, interleaved)
+        return dQKV, dwq, dwk
+
+    context = _elsewhere(index, stream)
+    if context is None:
+        return run()
+    with context:
+        return run()
 
 
 def flashbob_bob_launches(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int,
@@ -573,112 +796,3 @@ def bob(Q, K, V, O, dO, L, D, UQ, UK, UV, tau: float, out: dict | None = None,
     flashbob_bob(Q, K, V, O, dO, L, D, UQ, UK, UV, tau, out["dQt"], out["dKt"], out["dVt"],
                  out["ddOt"], out["alpha"], out["E"], causal, stream)
     return out
-
-
-def _allocating_on(stream, device):
-    """Context in which torch allocates for ``stream``: what a wrapper
-    allocates and frees (a workspace) is then reused in that stream's order."""
-    import torch
-    if stream is None:
-        return _NOTHING
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    return torch.cuda.stream(stream)
-
-
-def _workspace(nbytes: int, device):
-    import torch
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-
-
-def attention(Q, K, V, tau: float, cap: float = 0.0, slopes=None, ranges=None, q_pos=None,
-              causal: bool = False, stream=None):
-    """O (of Q's dtype) and L of attention with capped scores, a distance bias
-    and key ranges; allocates them, and the workspace, on Q's device."""
-    import torch
-    sizes = _check_attention("attention", Q, K, V, slopes, ranges, q_pos)
-    with _device(Q), _allocating_on(stream, Q.device):
-        need, _ = flashbob_attention_workspace(*sizes, _dtype_code(Q))
-        O = torch.empty_like(Q)
-        L = torch.empty(sizes[0], sizes[1], sizes[3], dtype=torch.float32, device=Q.device)
-        _run_attention(sizes, Q, K, V, ranges, q_pos, slopes, tau, cap, O, L,
-                       _workspace(need, Q.device), causal, stream)
-    return O, L
-
-
-def attention_grad(Q, K, V, O, L, dO, tau: float, cap: float = 0.0, slopes=None, ranges=None,
-                   q_pos=None, causal: bool = False, stream=None):
-    """dQ, dK, dV (of Q's dtype) of ``attention`` from its O and L and the
-    gradient dO; allocates them, and the workspace, on Q's device."""
-    import torch
-    sizes = _check_attention_grad("attention_grad", Q, K, V, O, L, dO, slopes, ranges, q_pos)
-    with _device(Q), _allocating_on(stream, Q.device):
-        _, need = flashbob_attention_workspace(*sizes, _dtype_code(Q))
-        dQ, dK, dV = torch.empty_like(Q), torch.empty_like(K), torch.empty_like(K)
-        _run_attention_grad(sizes, Q, K, V, O, L, dO, ranges, q_pos, slopes, tau, cap, dQ, dK, dV,
-                            _workspace(need, Q.device), causal, stream)
-    return dQ, dK, dV
-
-
-def attention_ranges(B: int, Nq: int, Nk: int, doc_offsets=None, prefix=None, q_start=None,
-                     causal: bool = False, device=None, stream=None):
-    """ranges [B, Nq, 2] and q_pos [B, Nq] of queries by document, on the
-    device of the first array given (``device``, or the current one, if none)."""
-    import torch
-    for t in (doc_offsets, prefix, q_start):
-        if t is not None:
-            device = t.device
-            break
-    device = torch.device("cuda") if device is None else torch.device(device)
-    if device.type != "cuda":
-        raise ValueError(f"attention_ranges: the arrays must be on a CUDA device, not {device}")
-    here = device.index is None or device.index == torch.cuda.current_device()
-    with _NOTHING if here else torch.cuda.device(device), _allocating_on(stream, device):
-        ranges = torch.empty((B, Nq, 2), dtype=torch.int32, device=device)
-        q_pos = torch.empty((B, Nq), dtype=torch.int32, device=device)
-        flashbob_attention_ranges(doc_offsets, prefix, q_start, ranges, q_pos, Nk, causal, stream)
-    return ranges, q_pos
-
-
-def qk_norm_rope(QKV, H: int, wq=None, wk=None, freqs=None, positions=None, eps: float = 1e-6,
-                 interleaved: bool = False, K=None, V=None, kv_start=None, stream=None):
-    """Q, K, V (head-major) of the packed projection QKV with H query heads:
-    the norm of queries and keys for each head and the rotation by position.
-    Allocates them on QKV's device; K and V may be given (a cache, whose rows
-    kv_start[b] + n are written)."""
-    import torch
-    _check_4d("qk_norm_rope", QKV=QKV)
-    B, N, heads, d = QKV.shape
-    if not 0 < H < heads or (heads - H) % 2:
-        raise ValueError(f"qk_norm_rope: {heads} heads are not {H} query heads and two equal "
-                         "groups of key and value heads")
-    if (K is None) != (V is None):
-        raise ValueError("qk_norm_rope: K and V are given together or not at all")
-    with _device(QKV), _allocating_on(stream, QKV.device):
-        Q = torch.empty((B, H, N, d), dtype=QKV.dtype, device=QKV.device)
-        if K is None:
-            if kv_start is not None:
-                raise ValueError("qk_norm_rope: kv_start needs K and V")
-            K, V = (torch.empty((B, (heads - H) // 2, N, d), dtype=QKV.dtype, device=QKV.device)
-                    for _ in range(2))
-        flashbob_qk_norm_rope(QKV, wq, wk, freqs, positions, kv_start, eps, Q, K, V, interleaved,
-                              stream)
-    return Q, K, V
-
-
-def qk_norm_rope_grad(QKV, dQ, dK, dV, wq=None, wk=None, freqs=None, positions=None,
-                      eps: float = 1e-6, interleaved: bool = False, stream=None):
-    """dQKV, dwq, dwk of ``qk_norm_rope`` from the gradients of Q, K and V
-    (fp32 or bf16); dwq and dwk are None without gains."""
-    import torch
-    _check_4d("qk_norm_rope_grad", QKV=QKV, dQ=dQ, dK=dK)
-    B, N, _, d = QKV.shape
-    with _device(QKV), _allocating_on(stream, QKV.device):
-        dQKV = torch.empty_like(QKV, memory_format=torch.contiguous_format)
-        dwq = None if wq is None else torch.empty_like(wq)
-        dwk = None if wk is None else torch.empty_like(wk)
-        need = 0 if wq is None else flashbob_qk_norm_rope_workspace(
-            B, N, dQ.shape[1], dK.shape[1], d, _dtype_code(QKV))
-        flashbob_qk_norm_rope_grad(QKV, wq, wk, freqs, positions, eps, dQ, dK, dV, dQKV, dwq, dwk,
-                                   _workspace(need, QKV.device), interleaved, stream)
-    return dQKV, dwq, dwk
