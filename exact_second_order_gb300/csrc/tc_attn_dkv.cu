@@ -230,6 +230,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(&sm.out_full, 1);
     sm.abort_flag = 0;
     fence_barrier_init();
+    // K and V are under way while the bounds are read.
+    mbar_expect_tx(&sm.bar_kv, 2 * NH * HALF);
+    for (int h = 0; h < NH; ++h) {
+      tma_load_3d(sm.k[h], &mK, &sm.bar_kv, 64 * h, j0, g);
+      tma_load_3d(sm.v[h], &mV, &sm.bar_kv, 64 * h, j0, g);
+    }
   }
   if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
   if (Smem::kFold && threadIdx.x >= 64 && threadIdx.x < 64 + 2 * BM) {
@@ -255,11 +261,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (lane == 0) {
       tma_prefetch_desc(&mQ);
       tma_prefetch_desc(&mdO);
-      mbar_expect_tx(&sm.bar_kv, 2 * NH * HALF);
-      for (int h = 0; h < NH; ++h) {
-        tma_load_3d(sm.k[h], &mK, &sm.bar_kv, 64 * h, j0, g);
-        tma_load_3d(sm.v[h], &mV, &sm.bar_kv, 64 * h, j0, g);
-      }
     }
     int nq = 0, no = 0;  // Q and dO loads issued
     int hit = 0;         // tiles found

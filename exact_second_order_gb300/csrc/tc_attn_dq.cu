@@ -152,6 +152,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(&sm.out_full, 1);
     sm.abort_flag = 0;
     fence_barrier_init();
+    // Q and dO are under way while the ranges and the row state are read.
+    mbar_expect_tx(&sm.bar_q, 2 * NH * HALF);
+    for (int h = 0; h < NH; ++h) {
+      tma_load_3d(sm.q[h], &mQ, &sm.bar_q, 64 * h, row0, g);
+      tma_load_3d(sm.go[h], &mdO, &sm.bar_q, 64 * h, row0, g);
+    }
   }
   if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
   const int wg = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane, row = row0 + r;
@@ -177,11 +183,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (lane == 0) {
       tma_prefetch_desc(&mK);
       tma_prefetch_desc(&mV);
-      mbar_expect_tx(&sm.bar_q, 2 * NH * HALF);
-      for (int h = 0; h < NH; ++h) {
-        tma_load_3d(sm.q[h], &mQ, &sm.bar_q, 64 * h, row0, g);
-        tma_load_3d(sm.go[h], &mdO, &sm.bar_q, 64 * h, row0, g);
-      }
       int nk = 0, nv = 0;
       for (int t = 0; t < T; ++t) {
         const int sk = t % NK, sv = t % NV;

@@ -141,6 +141,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(&sm.out_full, 1);
     sm.abort_flag = 0;
     fence_barrier_init();
+    // Q is under way while the ranges are read.
+    mbar_expect_tx(&sm.bar_q, MT * NH * HALF_BLOCK);
+    for (int w = 0; w < MT; ++w)
+      for (int h = 0; h < NH; ++h)
+        tma_load_3d(sm.q[w][h], &mQ, &sm.bar_q, 64 * h, row0 + BM * w, g);
   }
   if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
   // Elementwise threads: TMEM lane r of row block w.
@@ -167,10 +172,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (lane == 0) {
       tma_prefetch_desc(&mK);
       tma_prefetch_desc(&mV);
-      mbar_expect_tx(&sm.bar_q, MT * NH * HALF_BLOCK);
-      for (int w = 0; w < MT; ++w)
-        for (int h = 0; h < NH; ++h)
-          tma_load_3d(sm.q[w][h], &mQ, &sm.bar_q, 64 * h, row0 + BM * w, g);
       int issued = 0;
       for (int t = 0; t < T; ++t) {
         const int s = t % NST;
