@@ -38,8 +38,8 @@ constexpr int kLd = DP + 4;   // pitch of a 64 x DP tile
 // dst[r][k] <- rows row0 .. row0 + 63 of src (pitch d), zero outside
 // [first, last) and beyond d.
 template <typename T, int DP>
-__device__ __forceinline__ void load_tile(float* dst, const T* __restrict__ src, int row0, int first,
-                                          int last, int d) {
+__device__ __forceinline__ void load_tile(float* dst, const T* __restrict__ src, int row0,
+                                          int first, int last, int d) {
   if ((d & 3) == 0) {
     for (int x = threadIdx.x; x < BT * (DP / 4); x += NT) {
       const int r = x / (DP / 4), k = 4 * (x % (DP / 4));
@@ -80,7 +80,8 @@ __device__ __forceinline__ void score_tile(const float* A, const float* Bm, int 
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         acc[i][j] = fmaf(a[i].x, b[j].x,
-                         fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, acc[i][j]))));
+                         fmaf(a[i].y, b[j].y,
+                              fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, acc[i][j]))));
   }
 }
 

@@ -345,6 +345,9 @@ flashbob_status check_attention(const AttnArgs& a, int causal, flashbob_dtype in
   if (!(isfinite(a.cap) && a.cap >= 0.f)) return FLASHBOB_ERR_INVALID_ARG;
   st = check_sizes(a.B, a.H, a.Hkv, a.Nq, a.Nk, a.d, a.tau);
   if (st != FLASHBOB_OK) return st;
+  // The kernels work with 1 / tau and with e^(2 tau q.k / cap).
+  if (!isfinite(1.f / a.tau) || (a.cap > 0.f && !isfinite(4.f * a.tau / a.cap)))
+    return FLASHBOB_ERR_INVALID_ARG;
   // The rows of a group of query heads are counted in 32 bits, padding
   // included, and so are the keys with the tile beyond the last.
   if (static_cast<long long>(a.H / a.Hkv) * a.Nq > INT_MAX - 1024 || a.Nk > INT_MAX - 1024)

@@ -13,6 +13,9 @@
 // its heads stream past, several rows in flight (a block of 4 tokens with the
 // angles in shared memory, computed before the first load, ran at 2.1 TB/s).
 // Neighbouring tokens of a block write neighbouring rows of a head.
+// Measured (16384 tokens, 32 + 2 * 8 heads of 128, bf16): 75 us forward, 80% of
+// the copy rate, 127 us gradient, 71%: the rows in flight are as many as the
+// registers of the resident blocks hold.
 //
 // Angles as fractions of a turn in 64-bit fixed point: f / (2 pi) mod 1 is
 // scaled by 2^64, and the integer product with the position wraps as the angle

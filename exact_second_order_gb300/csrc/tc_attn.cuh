@@ -12,7 +12,8 @@ namespace attn {
 // tanh x = x + x^3 (k0 + k1 x^2 + k2 x^4 + k3 x^6) for |x| <= 0.7: least
 // squares with weights adapted until the largest error is smallest (Lawson's
 // method).
-__device__ constexpr float kTanh[4] = {-0.3333006501197815f, 0.1327691525220871f, -0.050674621015787125f, 0.013599642552435398f};
+__device__ constexpr float kTanh[4] = {-0.3333006501197815f, 0.1327691525220871f,
+                                            -0.050674621015787125f, 0.013599642552435398f};
 
 // rcp.approx (1 ulp) of a value in [1, inf]: 1 / inf is 0.
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -150,7 +151,7 @@ __device__ __forceinline__ Hull join_hulls(const int (*h)[4], int n) {
 // exponential of the softmax those would be three an element, and the MUFU pipe
 // bounds the kernel: the forward of B1 H8 N16384 d64 took 1370 us with them,
 // against 570 without a cap.  (tanh.approx leaves 2^-11, which exp turns into
-// percents of P.)
+// percents of P.)  The polynomial brought it to 1100 us.
 template <bool CAP, bool BIAS>
 struct Score {
   float c1;      // tau log2 e; capped: tau / cap

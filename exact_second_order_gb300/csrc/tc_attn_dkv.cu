@@ -26,6 +26,8 @@
 // At d = 128 dK and dV take 256 columns: one buffer of each, P^T on S^T and
 // dS^T on dP^T; the pipe runs dV(n), S(n + 1), dK(n), dP(n + 1), so that
 // P(n + 1) is formed beside dK(n) and dP(n + 1), and dS beside dV and S.
+// Measured (B1 H8 N16384, no mask): 800 us at d = 64, 1374 TFLOP/s of its 8 N^2 d,
+// and 1420 us at d = 128, 1550 TFLOP/s; waits and arithmetic of a tile bound both.
 #include <stddef.h>
 
 #include "tc_attn.cuh"
@@ -508,7 +510,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (masked)
             both<CAP, BIAS, true>(score, s[c], x, l2 + 32 * c, info + 32 * c, key, seen[c], pk, gk);
           else
-            both<CAP, BIAS, false>(score, s[c], x, l2 + 32 * c, info + 32 * c, key, seen[c], pk, gk);
+            both<CAP, BIAS, false>(score, s[c], x, l2 + 32 * c, info + 32 * c, key, seen[c], pk,
+                                   gk);
           if (c == 0 && n > 0) {
             ok = wait_warp(&sm.op_free, (n - 1) & 1, abort_flag, err);
             tc_fence_after();

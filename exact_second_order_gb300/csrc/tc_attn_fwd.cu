@@ -19,6 +19,11 @@
 // zeroed in shared memory before they meet P~ = 0, so a cache may hold
 // anything behind its last key.
 // TMEM: O~ of warpgroups 0 and 1 (DH columns each), then three score buffers.
+// Measured (B1 H8 N16384, no mask): 521 us at d = 64, 1054 TFLOP/s, where the
+// hand-offs between MMAs and elementwise warps bound it (without arithmetic it
+// takes 515, with a quarter of the MMAs 480); 741 us at d = 128, 1480 TFLOP/s,
+// bound by the MMAs.  Tokens over a cache: 74% of the copy rate (32 requests of
+// up to 8192 keys, 8 heads of 128).
 #include "tc_attn.cuh"
 
 namespace flashbob {
@@ -452,7 +457,8 @@ cudaError_t launch(const AttnArgs& a, int splits) {
 template <int DH, int MT>
 cudaError_t launch(const AttnArgs& a, int splits) {
   const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;
-  return cap ? (bias ? launch<DH, MT, true, true>(a, splits) : launch<DH, MT, true, false>(a, splits))
+  return cap ? (bias ? launch<DH, MT, true, true>(a, splits)
+                     : launch<DH, MT, true, false>(a, splits))
              : (bias ? launch<DH, MT, false, true>(a, splits)
                      : launch<DH, MT, false, false>(a, splits));
 }

@@ -353,8 +353,8 @@ def _run_attention(lib, index, sizes, code, Q, K, V, ranges, q_pos, slopes, tau,
                    workspace, causal) -> None:
     st = lib.flashbob_attention(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), _ptr(ranges), _ptr(q_pos), _ptr(slopes),
-        float(tau), float(cap), O.data_ptr(), L.data_ptr(), _ptr(workspace), _bytes(workspace), *sizes, int(causal),
-        code, _raw_stream(index))
+        float(tau), float(cap), O.data_ptr(), L.data_ptr(), _ptr(workspace), _bytes(workspace),
+        *sizes, int(causal), code, _raw_stream(index))
     if st != FLASHBOB_OK:
         raise FlashbobError(st, "flashbob_attention")
 
@@ -408,8 +408,8 @@ def _run_attention_grad(lib, index, sizes, code, Q, K, V, O, L, dO, ranges, q_po
                         cap, dQ, dK, dV, workspace, causal) -> None:
     st = lib.flashbob_attention_grad(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), L.data_ptr(), dO.data_ptr(),
-        _ptr(ranges), _ptr(q_pos), _ptr(slopes), float(tau), float(cap), dQ.data_ptr(), dK.data_ptr(),
-        dV.data_ptr(), _ptr(workspace), _bytes(workspace), *sizes, int(causal), code,
+        _ptr(ranges), _ptr(q_pos), _ptr(slopes), float(tau), float(cap), dQ.data_ptr(),
+        dK.data_ptr(), dV.data_ptr(), _ptr(workspace), _bytes(workspace), *sizes, int(causal), code,
         _raw_stream(index))
     if st != FLASHBOB_OK:
         raise FlashbobError(st, "flashbob_attention_grad")
@@ -557,8 +557,8 @@ def _run_norm(lib, index, sizes, QKV, wq, wk, freqs, positions, kv_start, eps, Q
               Nk, interleaved) -> None:
     B, N, _, d, R, axes = sizes
     st = lib.flashbob_qk_norm_rope(
-        QKV.data_ptr(), _ptr(wq), _ptr(wk), _ptr(freqs), _ptr(positions), _ptr(kv_start), float(eps),
-        Q.data_ptr(), K.data_ptr(), V.data_ptr(), B, N, H, Hkv, Nk, d, R, axes, int(interleaved),
+        QKV.data_ptr(), _ptr(wq), _ptr(wk), _ptr(freqs), _ptr(positions), _ptr(kv_start),
+        float(eps), Q.data_ptr(), K.data_ptr(), V.data_ptr(), B, N, H, Hkv, Nk, d, R, axes, int(interleaved),
         _dtype_code(QKV), _raw_stream(index))
     if st != FLASHBOB_OK:
         raise FlashbobError(st, "flashbob_qk_norm_rope")

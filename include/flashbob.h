@@ -197,7 +197,7 @@ flashbob_status flashbob_attention_jvp(const void* Q, const void* K, const void*
  *        are clamped to 0 .. Nk; lo >= hi is an empty range.
  *   q_pos: int32 [B,Nq], the position of every query; NULL: its index.
  *   slopes: fp32 [H], finite; NULL: no bias.  A constant: it has no gradient.
- *   cap: finite and >= 0.
+ *   cap: finite and >= 0; 1 / tau and 4 tau / cap must be finite, too.
  *   Limits: as flashbob_prep; (H / Hkv) * Nq and Nk below 2^31 - 1024.
  *
  * flashbob_attention: O [B,H,Nq,d] of in_dtype, L [B,H,Nq] fp32.

@@ -255,6 +255,26 @@ def test_writes_its_outputs_and_nothing_else(dtype, d):
         assert torch.equal(v, want[k]), k
 
 
+def test_offsets_past_32_bits():
+    """A cache of 2.2e9 elements: only 300 keys at the very end of the last
+    batch entry are seen, the rest holds NaN."""
+    B, H, Hkv, Nk, d, n = 2, 4, 2, 4_300_000, 128, 300
+    g = torch.Generator(device="cuda").manual_seed(1)
+    K, V = (torch.full((B, Hkv, Nk, d), math.nan, dtype=BF, device="cuda") for _ in range(2))
+    for t in (K, V):
+        t[:, :, Nk - n:] = torch.randn((B, Hkv, n, d), generator=g, device="cuda").to(BF)
+    Q, dO = (torch.randn((B, H, 3, d), generator=g, device="cuda").to(BF) for _ in range(2))
+    ranges = torch.tensor([[Nk - n, Nk], [Nk - n, Nk - 1], [Nk, Nk]], dtype=torch.int32,
+                          device="cuda").expand(B, 3, 2).contiguous()
+    O, L = fb.attention(Q, K, V, 0.1, ranges=ranges)
+    dQ, dK, dV = fb.attention_grad(Q, K, V, O, L, dO, 0.1, ranges=ranges)
+    k, v = K[:, :, Nk - n:].contiguous(), V[:, :, Nk - n:].contiguous()
+    val, bound = ref.attention(Q, k, v, 0.1, ranges=ranges - (Nk - n), dO=dO)
+    got = dict(O=O, L=L, dQ=dQ, dK=dK[:, :, Nk - n:], dV=dV[:, :, Nk - n:])
+    check(got, val, bound)
+    assert not dK[:, :, :Nk - n].any() and not dV[:, :, :Nk - n].any()
+
+
 def test_ranges_match_their_definition():
     for B, M, Nq, Nk in ((1, 1, 1, 1), (3, 5, 300, 200), (2, 40, 5000, 5000), (1, 9000, 9500, 9500)):
         off = offsets(B, M, Nk - Nk // 10 if Nk > 1 else 1, seed=M)
