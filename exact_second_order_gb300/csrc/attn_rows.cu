@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kRangeThreads)
     if (o) {
       int a = 0, z = M + 1;  // first offset above p lies in [a, z]
       while (a < z) {
-        const int mid = (a + z) >> 1;
+        const int mid = a + ((z - a) >> 1);
         if (o[mid] <= p) a = mid + 1;
         else z = mid;
       }

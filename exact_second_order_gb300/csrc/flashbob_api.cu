@@ -345,8 +345,10 @@ flashbob_status check_attention(const AttnArgs& a, int causal, flashbob_dtype in
   if (!(isfinite(a.cap) && a.cap >= 0.f)) return FLASHBOB_ERR_INVALID_ARG;
   st = check_sizes(a.B, a.H, a.Hkv, a.Nq, a.Nk, a.d, a.tau);
   if (st != FLASHBOB_OK) return st;
-  // The kernels work with 1 / tau and with e^(2 tau q.k / cap).
-  if (!isfinite(1.f / a.tau) || (a.cap > 0.f && !isfinite(4.f * a.tau / a.cap)))
+  // The kernels work with L / tau, 1 / cap, tau / cap and multiples of cap:
+  // none of them may overflow or lose bits to underflow.
+  auto in_reach = [](float x) { return x >= 0x1p-120f && x <= 0x1p120f; };
+  if (!in_reach(a.tau) || (a.cap > 0.f && !(in_reach(a.cap) && in_reach(a.tau / a.cap))))
     return FLASHBOB_ERR_INVALID_ARG;
   // The rows of a group of query heads are counted in 32 bits, padding
   // included, and so are the keys with the tile beyond the last.

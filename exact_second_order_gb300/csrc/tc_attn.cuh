@@ -13,7 +13,7 @@ namespace attn {
 // squares with weights adapted until the largest error is smallest (Lawson's
 // method).
 __device__ constexpr float kTanh[4] = {-0.3333006501197815f, 0.1327691525220871f,
-                                            -0.050674621015787125f, 0.013599642552435398f};
+                                       -0.050674621015787125f, 0.013599642552435398f};
 
 // rcp.approx (1 ulp) of a value in [1, inf]: 1 / inf is 0.
 __device__ __forceinline__ float rcp_approx(float x) {

@@ -386,9 +386,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tc_fence_after();
     static_assert(BM * (DH * 2 + 16) <= sizeof(sm.k), "epilogue staging fits in the ring");
     store_block<DH, NWG>(tbase + lane_off + kAcc, a.tau, T == 0, &sm.k[0][0][0], wg, r,
-                    threadIdx.x - 64, min(BM, rows - row0), ok,
-                    static_cast<__nv_bfloat16*>(a.dQ) +
-                        (static_cast<size_t>(g) * rows + row0) * DH);
+                         threadIdx.x - 64, min(BM, rows - row0), ok,
+                         static_cast<__nv_bfloat16*>(a.dQ) +
+                             (static_cast<size_t>(g) * rows + row0) * DH);
   }
 
   tc_fence_before();

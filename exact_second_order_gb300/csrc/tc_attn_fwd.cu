@@ -20,9 +20,9 @@
 // anything behind its last key.
 // TMEM: O~ of warpgroups 0 and 1 (DH columns each), then three score buffers.
 // Measured (B1 H8 N16384, no mask): 521 us at d = 64, 1054 TFLOP/s, where the
-// hand-offs between MMAs and elementwise warps bound it (without arithmetic it
-// takes 515, with a quarter of the MMAs 480); 741 us at d = 128, 1480 TFLOP/s,
-// bound by the MMAs.  Tokens over a cache: 74% of the copy rate (32 requests of
+// hand-offs between MMAs and elementwise warps bound it (with MT = 2, 590 us, a
+// copy without arithmetic took 515, one with a quarter of the MMAs 480); 741 us
+// at d = 128, 1480 TFLOP/s, bound by the MMAs.  Tokens over a cache: 74% of the copy rate (32 requests of
 // up to 8192 keys, 8 heads of 128).
 #include "tc_attn.cuh"
 

@@ -195,9 +195,10 @@ flashbob_status flashbob_attention_jvp(const void* Q, const void* K, const void*
  * of a query that sees no key.  Key rows inside that run must be finite.
  *   ranges: int32 [B,Nq,2], (lo, hi) of every query; NULL: (0, Nk).  Values
  *        are clamped to 0 .. Nk; lo >= hi is an empty range.
- *   q_pos: int32 [B,Nq], the position of every query; NULL: its index.
+ *   q_pos: int32 [B,Nq], the position of every query; NULL: its index.  With
+ *        slopes, pos_i - j must be an int32.
  *   slopes: fp32 [H], finite; NULL: no bias.  A constant: it has no gradient.
- *   cap: finite and >= 0; 1 / tau and 4 tau / cap must be finite, too.
+ *   tau, and where cap > 0 cap and tau / cap: within 2^-120 .. 2^120.
  *   Limits: as flashbob_prep; (H / Hkv) * Nq and Nk below 2^31 - 1024.
  *
  * flashbob_attention: O [B,H,Nq,d] of in_dtype, L [B,H,Nq] fp32.
@@ -236,7 +237,8 @@ flashbob_status flashbob_attention_grad(const void* Q, const void* K, const void
  * Query i of batch entry b is at position p = q_start[b] + i (q_start NULL:
  * p = i).  Document m of b is the positions doc_offsets[b][m] <= p <
  * doc_offsets[b][m + 1] (int32 [B,M+1], not decreasing; equal neighbours are
- * an empty document); doc_offsets NULL (M = 0): one document, the Nk keys.
+ * an empty document); doc_offsets NULL (M = 0): one document of all positions
+ * from 0 on.
  *     lo = the document's start,
  *     hi = causal ? min(end, max(p + 1, lo + prefix[b][m])) : end,
  * hi at most Nk, (0, 0) for a position in no document.  prefix (int32 [B,M],

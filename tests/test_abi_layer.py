@@ -51,7 +51,8 @@ def grad(lib, p, tau=0.1, cap=0.0, ws=BIG, B=1, H=2, Hkv=1, Nq=8, Nk=8, d=64, ca
 BAD_SIZES = [dict(B=0), dict(H=-1), dict(Hkv=0), dict(Nq=0), dict(Nk=0), dict(d=0), dict(H=3, Hkv=2),
              dict(tau=0.0), dict(tau=math.nan), dict(tau=math.inf), dict(cap=-1.0),
              dict(cap=math.nan), dict(cap=math.inf), dict(causal=2), dict(dtype=5),
-             dict(tau=1e-42), dict(cap=1e-42)]
+             dict(tau=1e-42), dict(cap=1e-42), dict(tau=1e37), dict(cap=1e37),
+             dict(tau=1e-20, cap=1e20)]
 TOO_LARGE = [dict(d=129), dict(B=70000), dict(H=65535, Nq=2 ** 20), dict(Nk=2 ** 31 - 1000)]
 
 

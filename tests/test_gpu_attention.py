@@ -311,6 +311,11 @@ def test_ranges_match_their_definition():
     assert got.tolist() == [[[0, 5], [0, 6], [0, 7]], [[0, 0], [0, 1], [0, 2]]]
     assert fb.attention_ranges(1, 2, 10)[0].tolist() == [[[0, 10], [0, 10]]]
 
+    # without documents every position from 0 on is in the one there is
+    got, pos = fb.attention_ranges(1, 4, 5, q_start=torch.tensor([3], dtype=torch.int32).cuda(),
+                                   causal=True)
+    assert got[0].tolist() == [[0, 4], [0, 5], [0, 5], [0, 5]] and pos[0].tolist() == [3, 4, 5, 6]
+
 
 def test_wrong_arguments_are_refused():
     x, form = make(1, 2, 1, 8, 8, 64, BF, mask="docs")
