@@ -54,10 +54,14 @@ __device__ __forceinline__ int warp_max(int v) { return __reduce_max_sync(0xffff
 //         products: columns 0 - 2 and 3 - 5 of 16, in core matrices of 8 rows
 //         x 16 bytes (row r of 128: (r / 8) 256 + (r % 8) 16, columns 8 - 15
 //         128 bytes further); the L columns are 0 for capped scores,
-// and for each kBoundRows rows {min lo, max hi, max lo, min hi}: the hull of
-// their ranges and their intersection (the padding takes no part).
+// and for each kBoundRows rows {min lo, max hi, max lo, min hi}, the hull of
+// their ranges and their intersection (the padding takes no part), and
+//   lines   {kind, pos, slope log2 e (as bits), 0}: kind 1 where the positions of
+//         the rows count up by one from pos and their slopes are equal, 2 where
+//         there are no rows, else 0.
 struct GradRows {
   int4* bounds;
+  int4* lines;
   int4* info;
   float *l2, *dd;
   uint8_t* ex;  // kExRow bytes a row
@@ -76,7 +80,8 @@ __host__ __device__ inline GradRows grad_rows(void* workspace, int groups, int r
   g.pitch = padded_rows(rows);
   const size_t n = static_cast<size_t>(groups) * g.pitch;
   g.bounds = static_cast<int4*>(workspace);
-  g.info = g.bounds + n / kBoundRows;
+  g.lines = g.bounds + n / kBoundRows;
+  g.info = g.lines + n / kBoundRows;
   g.l2 = reinterpret_cast<float*>(g.info + n);
   g.dd = g.l2 + n;
   g.ex = reinterpret_cast<uint8_t*>(g.dd + n);

@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(256)
                      void* workspace, int B, int H, int Hkv, int Nq, int Nk, int d, int causal,
                      float inv_tau, int ex) {
   __shared__ int s_bound[4][8];
+  __shared__ int2 s_row[kBoundRows];  // position and slope
   const int G = H / Hkv, rows = G * Nq;
   const int g = blockIdx.z * Hkv + blockIdx.y;
   const GradRows out = grad_rows(workspace, B * Hkv, rows);
@@ -128,6 +129,7 @@ __global__ void __launch_bounds__(256)
       const size_t at = static_cast<size_t>(g) * out.pitch + r;
       const float slope = slopes && live ? slopes[blockIdx.y * G + r / Nq] * kLog2e : 0.f;
       out.info[at] = make_int4(v.lo, v.hi, v.pos, __float_as_int(slope));
+      s_row[warp * 8 + u * 4 + (lane >> 3)] = make_int2(v.pos, __float_as_int(slope));
       out.l2[at] = v.hi > 0 ? l * kLog2e : INFINITY;
       out.dd[at] = v.hi > 0 ? dot : 0.f;
       if (ex) {  // inv_tau = 0 for capped scores
@@ -161,6 +163,18 @@ __global__ void __launch_bounds__(256)
       x.w = min(x.w, s_bound[3][w]);
     }
     out.bounds[static_cast<size_t>(g) * (out.pitch / kBoundRows) + blockIdx.x] = x;
+  }
+  if (warp == 1) {
+    bool line = true;
+    for (int q = lane; q < kBoundRows; q += 32)
+      if (blockIdx.x * kBoundRows + q < static_cast<unsigned>(rows))
+        line = line && s_row[q].y == s_row[0].y &&
+               static_cast<unsigned>(s_row[q].x) == static_cast<unsigned>(s_row[0].x) + q;
+    line = __all_sync(0xffffffffu, line);
+    const int kind = blockIdx.x * kBoundRows >= static_cast<unsigned>(rows) ? 2 : line ? 1 : 0;
+    if (lane == 0)
+      out.lines[static_cast<size_t>(g) * (out.pitch / kBoundRows) + blockIdx.x] =
+          make_int4(kind, s_row[0].x, s_row[0].y, 0);
   }
 }
 

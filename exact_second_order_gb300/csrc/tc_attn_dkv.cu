@@ -30,6 +30,8 @@
 // and 1420 us at d = 128, 1550 TFLOP/s; waits and arithmetic of a tile bound both.
 #include <stddef.h>
 
+#include <type_traits>
+
 #include "tc_attn.cuh"
 
 namespace flashbob {
@@ -60,6 +62,8 @@ struct Cols {
 struct Slot {
   int tile;          // -1: no more
   int in_lo, in_hi;  // intersection of the rows' ranges (in_lo INT_MAX: a row sees nothing)
+  int line, pos;     // line: row i is at position pos + i, and all have one slope
+  float slope2;
 };
 
 // Cluster split: floats of a staged row dK | dV (padded by 4 against conflicts).
@@ -94,11 +98,33 @@ struct SmemK {
   int abort_flag;
 };
 
+// t minus the distance bias of rows i and i + 1.  LINE: row i is `dist` - i keys
+// away and the rows have the score's slope; else each row's position and slope
+// are read (one 16-byte shared load an element for every warp).
+template <bool LINE, bool CAP>
+__device__ __forceinline__ float2 less_bias(float2 t, const Score<CAP, true>& score,
+                                            const int4* info, int key, float dist, int i) {
+  if (LINE) {
+    t.x = fmaf(-score.slope2, fabsf(dist - i), t.x);
+    t.y = fmaf(-score.slope2, fabsf(dist - (i + 1)), t.y);
+  } else {
+    const int4 a = info[i], b = info[i + 1];
+    t.x = fmaf(-__int_as_float(a.w), fabsf(static_cast<float>(key - a.z)), t.x);
+    t.y = fmaf(-__int_as_float(b.w), fabsf(static_cast<float>(key - b.z)), t.y);
+  }
+  return t;
+}
+template <bool LINE, bool CAP>
+__device__ __forceinline__ float2 less_bias(float2 t, const Score<CAP, false>&, const int4*, int,
+                                            float, int) {
+  return t;
+}
+
 // 32 rows of one key: P as bf16 pairs, and P (1 - tanh^2) in place of the
 // raw scores.
-template <bool CAP, bool BIAS, bool MASKED>
+template <bool MASKED, bool LINE, bool CAP, bool BIAS>
 __device__ __forceinline__ void weights(const Score<CAP, BIAS>& score, uint32_t (&s)[2][16],
-                                        const float* l2s, const int4* info, int key,
+                                        const float* l2s, const int4* info, int key, float dist,
                                         uint32_t seen, uint32_t (&pk)[2][8]) {
 #pragma unroll
   for (int q = 0; q < 2; ++q)
@@ -111,12 +137,8 @@ __device__ __forceinline__ void weights(const Score<CAP, BIAS>& score, uint32_t 
         const float2 x = f2(s[q][e + k], s[q][e + k + 1]);
         const float2 nl = k == 0 ? make_float2(-l2.x, -l2.y) : make_float2(-l2.z, -l2.w);
         const float c = CAP ? score.c2 : score.c1;
-        float2 t = ffma2(x, make_float2(c, c), nl);
-        if (BIAS) {
-          const int4 a = info[i], b = info[i + 1];
-          t.x = fmaf(-__int_as_float(a.w), fabsf(static_cast<float>(key - a.z)), t.x);
-          t.y = fmaf(-__int_as_float(b.w), fabsf(static_cast<float>(key - b.z)), t.y);
-        }
+        const float2 t =
+            less_bias<LINE>(ffma2(x, make_float2(c, c), nl), score, info, key, dist, i);
         float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
         if (MASKED) {
           if (!(seen >> i & 1)) p.x = 0.f;
@@ -133,10 +155,10 @@ __device__ __forceinline__ void weights(const Score<CAP, BIAS>& score, uint32_t 
 // P and dS of 32 rows of one key in one pass, so that the exponentials (MUFU)
 // of some rows run beside the multiplications of others.  s holds S^T - L / tau
 // (capped: the tanh), x holds dP^T - D.
-template <bool CAP, bool BIAS, bool MASKED>
+template <bool MASKED, bool LINE, bool CAP, bool BIAS>
 __device__ __forceinline__ void both(const Score<CAP, BIAS>& score, const uint32_t (&s)[2][16],
                                      const uint32_t (&x)[2][16], const float* l2s,
-                                     const int4* info, int key, uint32_t seen,
+                                     const int4* info, int key, float dist, uint32_t seen,
                                      uint32_t (&pk)[2][8], uint32_t (&o)[2][8]) {
 #pragma unroll
   for (int q = 0; q < 2; ++q)
@@ -155,11 +177,7 @@ __device__ __forceinline__ void both(const Score<CAP, BIAS>& score, const uint32
         } else {
           t = fmul2(z, make_float2(score.c1, score.c1));
         }
-        if (BIAS) {
-          const int4 a = info[i], b = info[i + 1];
-          t.x = fmaf(-__int_as_float(a.w), fabsf(static_cast<float>(key - a.z)), t.x);
-          t.y = fmaf(-__int_as_float(b.w), fabsf(static_cast<float>(key - b.z)), t.y);
-        }
+        t = less_bias<LINE>(t, score, info, key, dist, i);
         float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
         float2 ds = fmul2(p, score.damp(f2(x[q][e + k], x[q][e + k + 1]), z));
         if (MASKED) {  // S and dP of a row that sees nothing may be NaN
@@ -194,6 +212,18 @@ __device__ __forceinline__ void grads(const uint32_t (&p)[2][16], const uint32_t
         o[q][(e + k) >> 1] = pack_bf16x2(ds.x, ds.y);
       }
     }
+}
+
+// f with the two conditions as constants (BIAS false: the second is false).
+template <bool BIAS, typename F>
+__device__ __forceinline__ void choose(bool masked, bool line, F&& f) {
+  if (BIAS && line) {
+    if (masked) f(std::true_type(), std::true_type());
+    else f(std::false_type(), std::true_type());
+  } else {
+    if (masked) f(std::true_type(), std::false_type());
+    else f(std::false_type(), std::false_type());
+  }
 }
 
 template <int DH, bool CAP, bool BIAS>
@@ -258,7 +288,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (warp == 0) {
     const GradRows st = grad_rows(a.workspace, heads, rows);
     const size_t base = static_cast<size_t>(g) * st.pitch;
-    const int4* bounds = st.bounds + base / kBoundRows;
+    const int4 *bounds = st.bounds + base / kBoundRows, *lines = st.lines + base / kBoundRows;
     const int tiles = st.pitch / BQ;
     if (lane == 0) {
       tma_prefetch_desc(&mQ);
@@ -268,10 +298,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     int hit = 0;         // tiles found
     bool ok = true;
     for (int t0 = 0; ok && t0 < tiles; t0 += 32) {
-      int4 b = make_int4(INT_MAX, 0, 0, INT_MAX);
+      int4 b = make_int4(INT_MAX, 0, 0, INT_MAX), line = make_int4(0, 0, 0, 0);
       if (t0 + lane < tiles) {
         const int4 x = bounds[2 * (t0 + lane)], y = bounds[2 * (t0 + lane) + 1];
         b = make_int4(min(x.x, y.x), max(x.y, y.y), max(x.z, y.z), min(x.w, y.w));
+        if (BIAS) {
+          line = lines[2 * (t0 + lane)];
+          const int4 z = lines[2 * (t0 + lane) + 1];
+          if (z.x != 2 && (z.x != 1 || z.z != line.z ||
+                           static_cast<unsigned>(z.y) !=
+                               static_cast<unsigned>(line.y) + static_cast<unsigned>(kBoundRows)))
+            line.x = 0;
+        }
       }
       unsigned hits = __ballot_sync(0xffffffffu, b.x < j0 + BM && b.y > j0);
       for (; ok && hits; hits &= hits - 1) {
@@ -279,10 +317,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int k = __ffs(hits) - 1, tile = t0 + k, s = nq % NST;
         const int in_lo = __shfl_sync(0xffffffffu, b.z, k);
         const int in_hi = __shfl_sync(0xffffffffu, b.w, k);
+        const int kind = BIAS ? __shfl_sync(0xffffffffu, line.x, k) : 0;
+        const int pos = BIAS ? __shfl_sync(0xffffffffu, line.y, k) : 0;
+        const int slope = BIAS ? __shfl_sync(0xffffffffu, line.z, k) : 0;
         if (nq >= NST) ok = wait_warp(&sm.q_empty[s], ((nq / NST) - 1) & 1, abort_flag, err);
         if (!ok) break;
         if (lane == 0) {
-          sm.slot[s] = Slot{tile, in_lo, in_hi};
+          sm.slot[s] = Slot{tile, in_lo, in_hi, kind, pos, __int_as_float(slope)};
           constexpr bool kL2 = !Smem::kFold || CAP;  // L is read by the warpgroups
           mbar_expect_tx(&sm.q_full[s], NH * HALF + BQ * 16 + (kL2 ? BQ * 4 : 0) +
                                             (Smem::kFold ? BQ * kExRow : BQ * 4));
@@ -424,7 +465,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const int key = j0 + r, c0 = CW * wg;
     const int key_end = min(j0 + BM, a.Nk);
-    const Score<CAP, BIAS> score(a, 0.f);
+    Score<CAP, BIAS> score(a, 0.f);
     bool ok = true;
     int n = 0;
     for (;; ++n) {
@@ -433,7 +474,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (!ok) break;
       const Slot slot = sm.slot[st];
       if (slot.tile < 0) break;
-      const bool masked = slot.in_lo > j0 || slot.in_hi < key_end;
+      const bool masked = slot.in_lo > j0 || slot.in_hi < key_end, line = BIAS && slot.line == 1;
+      const float dist = static_cast<float>(key - slot.pos) - c0;
+      score.slope2 = slot.slope2;
       ok = wait_warp(&sm.s_full, n & 1, abort_flag, err);
       if (!ok) break;
       tc_fence_after();
@@ -467,10 +510,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           score.tanh_of(s[c]);
-          if (masked)
-            weights<CAP, BIAS, true>(score, s[c], l2 + 32 * c, info + 32 * c, key, seen[c], pk);
-          else
-            weights<CAP, BIAS, false>(score, s[c], l2 + 32 * c, info + 32 * c, key, seen[c], pk);
+          auto form = [&](auto m, auto l) {
+            weights<decltype(m)::value, decltype(l)::value>(
+                score, s[c], l2 + 32 * c, info + 32 * c, key, dist - 32 * c, seen[c], pk);
+          };
+          choose<BIAS>(masked, line, form);
 #pragma unroll
           for (int q = 0; q < 2; ++q)
             tmem_st8(tbase + lane_off + C::p((CW / 16) * wg + 2 * c + q), pk[q]);
@@ -507,11 +551,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         if (C::kOwn) {
           score.tanh_of(s[c]);
-          if (masked)
-            both<CAP, BIAS, true>(score, s[c], x, l2 + 32 * c, info + 32 * c, key, seen[c], pk, gk);
-          else
-            both<CAP, BIAS, false>(score, s[c], x, l2 + 32 * c, info + 32 * c, key, seen[c], pk,
-                                   gk);
+          auto form = [&](auto m, auto l) {
+            both<decltype(m)::value, decltype(l)::value>(score, s[c], x, l2 + 32 * c,
+                                                         info + 32 * c, key, dist - 32 * c,
+                                                         seen[c], pk, gk);
+          };
+          choose<BIAS>(masked, line, form);
           if (c == 0 && n > 0) {
             ok = wait_warp(&sm.op_free, (n - 1) & 1, abort_flag, err);
             tc_fence_after();
