@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(256)
                      float inv_tau, int ex) {
   __shared__ int s_bound[4][8];
   __shared__ int2 s_row[kBoundRows];  // position and slope
+  release_next();
   const int G = H / Hkv, rows = G * Nq;
   const int g = blockIdx.z * Hkv + blockIdx.y;
   const GradRows out = grad_rows(workspace, B * Hkv, rows);
@@ -197,6 +198,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   const size_t row = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const Partials p = partials(workspace, rows, d, splits);
+  wait_ahead();
   float m = -INFINITY;
   for (int s = lane; s < splits; s += 32) m = fmaxf(m, p.ml[s * rows + row].x);
 #pragma unroll
@@ -242,9 +244,8 @@ template <typename T>
 cudaError_t launch_join(const AttnArgs& a, int splits) {
   const size_t rows = static_cast<size_t>(a.B) * a.H * a.Nq;
   const int warps = splits < kJoinWarps ? splits : kJoinWarps;
-  join_kernel<T><<<static_cast<unsigned>(rows), 32 * warps, 0, a.stream>>>(
-      a.workspace, static_cast<T*>(a.O), a.L, rows, a.d, splits);
-  return cudaGetLastError();
+  return launch_after(true, join_kernel<T>, dim3(static_cast<unsigned>(rows)), 32 * warps, 0, 1,
+                      a.stream, a.workspace, static_cast<T*>(a.O), a.L, rows, a.d, splits);
 }
 
 }  // namespace

@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(NT) attn_kernel(const __grid_constant__ AttnAr
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const float inv_cap = a.cap > 0.f ? 1.f / a.cap : 0.f;
 
+  if (splits > 1) release_next();
   load_rows(rs, a, row0, rows);
   const int first = rs.hull[0], last = rs.hull[1];
   const int t0 = first < last ? first / BT : 0, t1 = first < last ? (last + BT - 1) / BT : 0;
@@ -354,6 +355,9 @@ __global__ void __launch_bounds__(NT)
   load_tile<T, DP>(dOs, dO, row0, 0, rows, a.d);
   float2 ld[4];
   float acc[4][DP / 16];
+  wait_ahead();
+  __threadfence();  // the row state reaches the launch behind, too
+  release_next();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // The workspace is padded, so rows beyond the last have an entry too.
@@ -402,7 +406,8 @@ __global__ void __launch_bounds__(NT)
 // ---------------------------------------------------------------------------
 // dK, dV: 64 keys resident, the group rows that see any of them stream past
 // in tiles of 64 (their bounds say which), so a shared head's gradient sums
-// its query heads on chip.
+// its query heads on chip.  Starts when every block of dQ runs, which itself
+// waited for the row state; the last block outlasts dQ.
 // ---------------------------------------------------------------------------
 template <typename T, int DP>
 __global__ void __launch_bounds__(NT)
@@ -437,14 +442,14 @@ __global__ void __launch_bounds__(NT)
     for (int c = 0; c < DP / 16; ++c) ak[i][c] = av[i][c] = 0.f;
   int hit = 0;
   for (int t = 0; t * BT < rows; ++t) {
-    const int4 b = bounds[t];
+    const int4 b = __ldcg(bounds + t);
     if (b.x >= key0 + BT || b.y <= key0) continue;  // no row of the tile sees a key of the block
     if (hit++ % S != rank) continue;
     __syncthreads();
     if (threadIdx.x < BT) {
       const size_t at = static_cast<size_t>(g) * gr.pitch + t * BT + threadIdx.x;
-      info[threadIdx.x] = gr.info[at];
-      lds[threadIdx.x] = make_float2(gr.l2[at], gr.dd[at]);
+      info[threadIdx.x] = __ldcg(gr.info + at);
+      lds[threadIdx.x] = make_float2(__ldcg(gr.l2 + at), __ldcg(gr.dd + at));
     }
     load_tile<T, DP>(Qs, Q, t * BT, 0, rows, a.d);
     load_tile<T, DP>(dOs, dO, t * BT, 0, rows, a.d);
@@ -489,6 +494,8 @@ __global__ void __launch_bounds__(NT)
   write_rows<T, DP>(Qs, static_cast<T*>(a.dK) + at, a.Nk - key0, a.d, rank, S);
   write_rows<T, DP>(dOs, static_cast<T*>(a.dV) + at, a.Nk - key0, a.d, rank, S);
   if (S > 1) tc::cluster_sync();
+  if (blockIdx.x + 1 == gridDim.x && blockIdx.y + 1 == gridDim.y && blockIdx.z + 1 == gridDim.z)
+    wait_ahead();
 }
 
 // Blocks of a cluster that share one block's streamed tiles.
@@ -502,19 +509,7 @@ template <typename K>
 cudaError_t launch(K kernel, size_t smem, int blocks, int S, const AttnArgs& a) {
   const cudaError_t e = tc_set_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks * S, a.Hkv, a.B);
-  cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = a.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = S;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = S > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, a, S);
+  return launch_after(true, kernel, dim3(blocks * S, a.Hkv, a.B), NT, smem, S, a.stream, a, S);
 }
 
 template <typename T, int DP>

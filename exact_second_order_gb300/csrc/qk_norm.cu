@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(NT) norm_grad_kernel(const __grid_constant__ N
   float dw[2][8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
+  if (a.dwq) release_next();
   fill_steps(steps, a);
   for (size_t first = static_cast<size_t>(blockIdx.x) * kSlots; first < tokens;
        first += static_cast<size_t>(gridDim.x) * kSlots) {
@@ -412,6 +413,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__
   __shared__ float s[128][9];
   const int k = blockIdx.y, run = threadIdx.x >> 3, x = blockIdx.x * 8 + (threadIdx.x & 7);
   float sum = 0.f;
+  wait_ahead();
 #pragma unroll 4
   for (int b = run; b < blocks; b += 128) sum += part[(static_cast<size_t>(b) * 2 + k) * 128 + x];
   s[run][threadIdx.x & 7] = sum;
@@ -464,10 +466,9 @@ cudaError_t backward(const NormArgs& a) {
   norm_grad_kernel<T, TG, LPR, VEC><<<grid, NT, smem, a.stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.dwq == nullptr) return e;
-  norm_dw_kernel<<<dim3(LPR, 2), 1024, 0, a.stream>>>(
-      a.workspace, static_cast<int>(grid.x * grid.y), a.dwq, a.dwk, a.d, a.R / 2,
-      a.interleaved ? 1 : 0);
-  return cudaGetLastError();
+  return launch_after(true, norm_dw_kernel, dim3(LPR, 2), 1024, 0, 1, a.stream, a.workspace,
+                      static_cast<int>(grid.x * grid.y), a.dwq, a.dwk, a.d, a.R / 2,
+                      a.interleaved ? 1 : 0);
 }
 
 template <typename T, typename TG>

@@ -11,6 +11,9 @@
 // of every tile each, one key per thread.  How many tiles there
 // are is known only to warp 0: each ring slot says which tile it holds, and a
 // last slot says that there are no more.
+// The launch starts when every block of dQ runs (dQ waited for the row state),
+// so the blocks fill the SMs that dQ's last wave leaves; its last block outlasts
+// dQ, so whatever follows on the stream finds both done.
 // When the key blocks are few, a cluster of S blocks shares one: rank q takes
 // every S-th of its tiles, and the partial sums meet in distributed shared
 // memory, in the order of the ranks, before the one write.
@@ -300,11 +303,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int t0 = 0; ok && t0 < tiles; t0 += 32) {
       int4 b = make_int4(INT_MAX, 0, 0, INT_MAX), line = make_int4(0, 0, 0, 0);
       if (t0 + lane < tiles) {
-        const int4 x = bounds[2 * (t0 + lane)], y = bounds[2 * (t0 + lane) + 1];
+        const int4 x = __ldcg(bounds + 2 * (t0 + lane)), y = __ldcg(bounds + 2 * (t0 + lane) + 1);
         b = make_int4(min(x.x, y.x), max(x.y, y.y), max(x.z, y.z), min(x.w, y.w));
         if (BIAS) {
-          line = lines[2 * (t0 + lane)];
-          const int4 z = lines[2 * (t0 + lane) + 1];
+          line = __ldcg(lines + 2 * (t0 + lane));
+          const int4 z = __ldcg(lines + 2 * (t0 + lane) + 1);
           if (z.x != 2 && (z.x != 1 || z.z != line.z ||
                            static_cast<unsigned>(z.y) !=
                                static_cast<unsigned>(line.y) + static_cast<unsigned>(kBoundRows)))
@@ -649,6 +652,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
+  if (blockIdx.x + 1 == gridDim.x) wait_ahead();
 }
 
 // How many blocks share a key block: a power of two up to 8 that makes up to
@@ -683,19 +687,8 @@ cudaError_t launch(const AttnArgs& a) {
   const int S = cluster_size(a);
   const long long grid = static_cast<long long>((a.Nk + BM - 1) / BM) * heads * S;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(NTHREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = a.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = S;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = S > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, mq, mo, mk, mv, a, S);
+  return launch_after(true, kernel, dim3(static_cast<unsigned>(grid)), NTHREADS, smem, S, a.stream,
+                      mq, mo, mk, mv, a, S);
 }
 
 template <int DH>

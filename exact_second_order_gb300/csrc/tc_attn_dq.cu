@@ -162,6 +162,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       tma_load_3d(sm.q[h], &mQ, &sm.bar_q, 64 * h, row0, g);
       tma_load_3d(sm.go[h], &mdO, &sm.bar_q, 64 * h, row0, g);
     }
+    wait_ahead();
+    __threadfence();  // the row state reaches the launch behind, too
+    release_next();
   }
   if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
   const int wg = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane, row = row0 + r;
@@ -172,6 +175,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (wg == 0) warp_hull(gr.v, row < rows, lane, sm.hull[quad]);
     const GradRows st = grad_rows(a.workspace, heads, rows);
     const size_t at = static_cast<size_t>(g) * st.pitch + row;  // the pitch covers the block
+    wait_ahead();
     l2 = st.l2[at];
     dd = st.dd[at];
   }
@@ -417,8 +421,8 @@ cudaError_t launch(const AttnArgs& a) {
   const int blocks = (rows + BM - 1) / BM;
   const long long grid = static_cast<long long>(blocks) * heads;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  kernel<<<static_cast<unsigned>(grid), NTHREADS, smem, a.stream>>>(mq, mo, mk, mv, a, blocks);
-  return cudaGetLastError();
+  return launch_after(true, kernel, dim3(static_cast<unsigned>(grid)), NTHREADS, smem, 1, a.stream,
+                      mq, mo, mk, mv, a, blocks);
 }
 
 template <int DH>

@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   volatile int* abort_flag = &sm.abort_flag;
   unsigned int* err = a.err;
 
+  if (splits > 1) release_next();
   if (threadIdx.x == 0) {
     mbar_init(&sm.bar_q, 1);
     for (int s = 0; s < NST; ++s) {
