@@ -14,8 +14,10 @@
 // angles in shared memory, computed before the first load, ran at 2.1 TB/s).
 // Neighbouring tokens of a block write neighbouring rows of a head.
 // Measured (16384 tokens, 32 + 2 * 8 heads of 128, bf16): 75 us forward, 80% of
-// the copy rate, 127 us gradient, 71%: the rows in flight are as many as the
-// registers of the resident blocks hold.
+// the copy rate, 118 us gradient, 76%.  Bound by both the bytes in flight and the
+// issue (63% and 49% of the slots before the gradient loaded ahead): with the
+// rows in rings in shared memory 91 and 136 us, with 16 elements a lane 79 and
+// 140, with packed fp32 87 and 130 (graph replays, 81 and 124 for this).
 //
 // Angles as fractions of a turn in 64-bit fixed point: f / (2 pi) mod 1 is
 // scaled by 2^64, and the integer product with the position wraps as the angle
@@ -301,11 +303,13 @@ __global__ void __launch_bounds__(NT, 4) norm_kernel(const __grid_constant__ Nor
 // one partial, and a second kernel sums the partials in order: the result does
 // not depend on timing.
 // ---------------------------------------------------------------------------
-constexpr int kGradRows = 4;  // rows of x and of dz in flight, 2 blocks an SM: 134 us; 2 rows and
-                             // 3 or 4 blocks 160 us
+// Rows of x and of dz that each lane works on, with as many of the next ones in
+// flight and 2 blocks an SM: 124 us (16384 tokens, 48 heads of 128); 2 rows 129, 4
+// rows 136, 4 rows loaded and then worked on 134, 2 rows and 3 blocks 179.
+constexpr int kGradRows = 3;
 
 template <typename T, typename TG, int LPR, bool VEC>
-__global__ void __launch_bounds__(NT) norm_grad_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(NT, 2) norm_grad_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ unsigned long long steps[];
   __shared__ float part_dw[NT * 8];
   const size_t tokens = static_cast<size_t>(a.B) * a.N;
@@ -333,19 +337,30 @@ __global__ void __launch_bounds__(NT) norm_grad_kernel(const __grid_constant__ N
       const int2 part = head_part(nh);
       float w[8];
       if (kKind < 2 && gain) load_row<VEC>(gain, s, c, w);
+      Raw<T, VEC> nx[kGradRows];
+      Raw<TG, VEC> ng[kGradRows];
+      auto fetch = [&](int h) {
+#pragma unroll
+        for (int u = 0; u < kGradRows; ++u) {
+          if (live && h + u < part.y) {
+            ng[u].load(dz + (h + u) * pitch, s, c);
+            if (kKind < 2) nx[u].load(X + static_cast<size_t>(h0 + h + u) * a.d, s, c);
+          } else {
+            ng[u].zero();
+            if (kKind < 2) nx[u].zero();
+          }
+        }
+      };
+      fetch(part.x);
       for (int h = part.x; h < part.y; h += kGradRows) {
         Raw<T, VEC> rx[kGradRows];
         Raw<TG, VEC> rg[kGradRows];
 #pragma unroll
         for (int u = 0; u < kGradRows; ++u) {
-          if (live && h + u < part.y) {
-            rg[u].load(dz + (h + u) * pitch, s, c);
-            if (kKind < 2) rx[u].load(X + static_cast<size_t>(h0 + h + u) * a.d, s, c);
-          } else {
-            rg[u].zero();
-            if (kKind < 2) rx[u].zero();
-          }
+          rg[u] = ng[u];
+          if (kKind < 2) rx[u] = nx[u];
         }
+        fetch(h + kGradRows);
         if (kKind < 2 && !turned) {
           token_turns(cs, steps, a, c, tokens, live ? token : 0);
           turned = true;
