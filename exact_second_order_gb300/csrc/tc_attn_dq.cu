@@ -4,9 +4,11 @@
 //   S = Q K^T, dP = dO V^T;  P = exp2(score(S) - L log2 e),
 //   dS = P (dP - D) (1 - tanh^2),  dQ += dS K;  dQ = tau dQ at the end.
 //
-// 576 threads: warp 0 TMA, warp 1 TMEM allocation and MMA issue, then four
-// elementwise warpgroups that take 32 columns of every tile each (two of 64
-// columns left the schedulers idle 60% of the time, waiting on latencies).
+// Warp 0 TMA, warp 1 TMEM allocation and MMA issue, then four elementwise
+// warpgroups that take 32 columns of every tile each (two of 64 columns left the
+// schedulers idle 60% of the time, waiting on latencies).
+// SMALL (d = 64, few keys): tiles of 64 keys, two warpgroups, half of an SM's
+// TMEM and shared memory, so that two blocks fill and drain beside each other.
 // S has two buffers, and dS (bf16) of a tile lies on the scores it came from,
 // so S(t + 1) is issued right behind dQ(t - 1); dP has one, handed back as soon
 // as it is in registers.  So the score products of tile t + 1 run while the
@@ -16,10 +18,10 @@
 // d = 128.
 // K and V have rings of their own: a V tile is free after dP, a K tile only
 // after dQ.
-// TMEM: S [0,128) and [128,256), dP [256,384), dQ from 384 on; at d = 64 also
-// Q and dO as A operands ([448,480) and [480,512)): read from shared memory,
-// they and the key tiles and the TMA writes need as many cycles of its 128
-// bytes as the MMAs take.
+// TMEM (BN keys a tile): S [0, BN) and [BN, 2 BN), dP [2 BN, 3 BN), dQ from 3 BN
+// on; in the large blocks of d = 64 also Q and dO as A operands ([448,480) and
+// [480,512)): read from shared memory, they and the key tiles and the TMA writes
+// need as many cycles of its 128 bytes as the MMAs take.
 // Measured (B1 H8 N16384, no mask): 640 us at d = 64, 1289 TFLOP/s of its 6 N^2 d,
 // bound by the chain of waits and arithmetic of a tile (without arithmetic 436,
 // with a quarter of the MMAs 650); 865 us at d = 128, 1910 TFLOP/s, bound by the
@@ -31,26 +33,36 @@ namespace {
 using namespace tc;
 using namespace attn;
 
-constexpr int BM = kTcRows, BN = 128;
-constexpr int NWG = 4, CW = BN / NWG, NC = CW / 32;  // warpgroups; columns of each, in chunks of 32
-constexpr int NTHREADS = 64 + 128 * NWG;
+constexpr int BM = kTcRows;
+constexpr int CW = 32, NC = CW / 32;    // columns of a warpgroup, in chunks of 32
 constexpr uint32_t HALF = BM * 64 * 2;  // 128 rows x 64 columns
-constexpr uint32_t kP = 256, kAcc = 384, kQA = 448, kGA = 480;
-__device__ __forceinline__ constexpr uint32_t s_col(int t) { return 128 * (t & 1); }
-// K step c (16 keys) of tile t's dS operand, on the scores of the warpgroup
-// that wrote it.
-__device__ __forceinline__ constexpr uint32_t op_col(int t, int c) {
-  return s_col(t) + CW * (c / (CW / 16)) + 8 * (c % (CW / 16));
-}
 
-template <int DH>
+template <int DH, bool SMALL>
+struct Cfg {
+  static constexpr int BN = SMALL ? 64 : 128, NWG = BN / CW;
+  static constexpr int kThreads = 64 + 128 * NWG;
+  static constexpr uint32_t kTileHalf = BN * 64 * 2;  // 64 columns of a key tile
+  static constexpr uint32_t kP = 2 * BN, kAcc = 3 * BN, kQA = 448, kGA = 480;
+  static constexpr int kColumns = SMALL ? 256 : 512;
+  static constexpr bool kTmemA = DH == 64 && !SMALL;  // Q and dO as operands in TMEM
+  static __device__ __forceinline__ constexpr uint32_t s_col(int t) { return BN * (t & 1); }
+  // K step c (16 keys) of tile t's dS operand, on the scores of the warpgroup
+  // that wrote it.
+  static __device__ __forceinline__ constexpr uint32_t op_col(int t, int c) {
+    return s_col(t) + CW * (c / (CW / 16)) + 8 * (c % (CW / 16));
+  }
+  static_assert(kAcc + DH <= (kTmemA ? kQA : kColumns), "TMEM columns");
+};
+
+template <int DH, bool SMALL>
 struct SmemQ {
   static constexpr int NH = DH / 64;
-  static constexpr int NK = DH == 64 ? 6 : 3, NV = DH == 64 ? 5 : 2;
+  static constexpr int NK = SMALL ? 4 : DH == 64 ? 6 : 3, NV = SMALL ? 4 : DH == 64 ? 5 : 2;
+  static constexpr uint32_t kTileHalf = Cfg<DH, SMALL>::kTileHalf;
   alignas(1024) uint8_t q[NH][HALF];
   alignas(1024) uint8_t go[NH][HALF];  // dO
-  alignas(1024) uint8_t k[NK][NH][HALF];
-  alignas(1024) uint8_t v[NV][NH][HALF];
+  alignas(1024) uint8_t k[NK][NH][kTileHalf];
+  alignas(1024) uint8_t v[NV][NH][kTileHalf];
   int hull[4][4];
   uint64_t bar_q, a_ready;    // Q and dO in shared memory / in TMEM (8 warps)
   uint64_t k_full[NK], k_empty[NK];
@@ -128,13 +140,16 @@ __device__ __forceinline__ void finish(const uint32_t (&s)[2][16], const uint32_
     }
 }
 
-template <int DH, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(NTHREADS, 1)
+template <int DH, bool SMALL, bool CAP, bool BIAS>
+__global__ void __launch_bounds__((Cfg<DH, SMALL>::kThreads), (SMALL ? 2 : 1))
     tc_dq_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mdO,
                  const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
                  const __grid_constant__ AttnArgs a, int blocks) {
   extern __shared__ uint8_t smem_raw[];
-  using Smem = SmemQ<DH>;
+  using Smem = SmemQ<DH, SMALL>;
+  using C = Cfg<DH, SMALL>;
+  constexpr int BN = C::BN, NWG = C::NWG;
+  constexpr uint32_t TILE = C::kTileHalf;
   constexpr int NH = Smem::NH, NK = Smem::NK, NV = Smem::NV;
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                       ~static_cast<uintptr_t>(1023));
@@ -166,7 +181,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     __threadfence();  // the row state reaches the launch behind, too
     release_next();
   }
-  if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+  if (warp == 1) tmem_alloc(&sm.tmem_base, C::kColumns);
   const int wg = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane, row = row0 + r;
   GroupRow gr{empty_view(), 0.f};
   float l2 = INFINITY, dd = 0.f;
@@ -195,12 +210,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int t = 0; t < T; ++t) {
         const int sk = t % NK, sv = t % NV;
         if (t >= NK && !wait_one(&sm.k_empty[sk], ((t / NK) - 1) & 1, abort_flag, err)) break;
-        mbar_expect_tx(&sm.k_full[sk], NH * HALF);
+        mbar_expect_tx(&sm.k_full[sk], NH * TILE);
         for (int h = 0; h < NH; ++h)
           tma_load_3d(sm.k[sk][h], &mK, &sm.k_full[sk], 64 * h, (tb + t) * BN, g);
         nk = t + 1;
         if (t >= NV && !wait_one(&sm.v_empty[sv], ((t / NV) - 1) & 1, abort_flag, err)) break;
-        mbar_expect_tx(&sm.v_full[sv], NH * HALF);
+        mbar_expect_tx(&sm.v_full[sv], NH * TILE);
         for (int h = 0; h < NH; ++h)
           tma_load_3d(sm.v[sv][h], &mV, &sm.v_full[sv], 64 * h, (tb + t) * BN, g);
         nv = t + 1;
@@ -216,26 +231,27 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint64_t dG = smem_desc_sw128(smem_u32(sm.go[0]), 16, 1024);
     const uint64_t dK = smem_desc_sw128(smem_u32(sm.k[0][0]), 16, 1024);
     const uint64_t dV = smem_desc_sw128(smem_u32(sm.v[0][0]), 16, 1024);
-    const uint64_t dKm = smem_desc_sw128(smem_u32(sm.k[0][0]), HALF, 1024);  // MN-major
-    constexpr uint64_t kTile = (uint64_t)(NH * HALF) >> 4;
+    const uint64_t dKm = smem_desc_sw128(smem_u32(sm.k[0][0]), TILE, 1024);  // MN-major
+    constexpr uint64_t kTile = (uint64_t)(NH * TILE) >> 4;
     auto scores = [&](uint32_t col, uint64_t da, uint32_t ta, uint64_t db) {
 #pragma unroll
       for (int kk = 0; kk < DH / 16; ++kk) {
-        const uint64_t o = ((kk >> 2) * HALF + 32 * (kk & 3)) >> 4;
-        if (DH == 64) mma_ts(tbase + col, tbase + ta + 8 * kk, db + o, idS, kk > 0);
-        else mma_ss(tbase + col, da + o, db + o, idS, kk > 0);
+        const uint64_t oa = ((kk >> 2) * HALF + 32 * (kk & 3)) >> 4;
+        const uint64_t ob = ((kk >> 2) * TILE + 32 * (kk & 3)) >> 4;
+        if (C::kTmemA) mma_ts(tbase + col, tbase + ta + 8 * kk, db + ob, idS, kk > 0);
+        else mma_ss(tbase + col, da + oa, db + ob, idS, kk > 0);
       }
     };
     if (elect_one()) {
-      bool ok = wait_one(DH == 64 ? &sm.a_ready : &sm.bar_q, 0, abort_flag, err);
+      bool ok = wait_one(C::kTmemA ? &sm.a_ready : &sm.bar_q, 0, abort_flag, err);
       auto issue_s = [&](int t) {
         tc_fence_after();
-        scores(s_col(t), dQ, kQA, dK + (t % NK) * kTile);
+        scores(C::s_col(t), dQ, C::kQA, dK + (t % NK) * kTile);
         mma_commit(&sm.s_full[t & 1]);
       };
       auto issue_p = [&](int t) {
         tc_fence_after();
-        scores(kP, dG, kGA, dV + (t % NV) * kTile);
+        scores(C::kP, dG, C::kGA, dV + (t % NV) * kTile);
         mma_commit(&sm.p_full);
         mma_commit(&sm.v_empty[t % NV]);
       };
@@ -266,7 +282,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const uint64_t dk = dKm + (t % NK) * kTile;
 #pragma unroll
         for (int c = 0; c < BN / 16; ++c)
-          mma_ts(tbase + kAcc, tbase + op_col(t, c), dk + ((16 * 128 * c) >> 4), idO,
+          mma_ts(tbase + C::kAcc, tbase + C::op_col(t, c), dk + ((16 * 128 * c) >> 4), idO,
                  t > 0 || c > 0);
         mma_commit(&sm.k_empty[t % NK]);
       }
@@ -278,9 +294,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int lo = gr.v.lo, hi = gr.v.hi;
     const Score<CAP, BIAS> score(a, gr.slope2);
     bool ok = true;
-    if (DH == 64 && wg < 2) {
+    if (C::kTmemA && wg < 2) {
       ok = wait_warp(&sm.bar_q, 0, abort_flag, err);
-      row_to_tmem(wg ? sm.go[0] : sm.q[0], r, tbase + lane_off + (wg ? kGA : kQA));
+      row_to_tmem(wg ? sm.go[0] : sm.q[0], r, tbase + lane_off + (wg ? C::kGA : C::kQA));
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(&sm.a_ready);
@@ -301,7 +317,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     auto write = [&](int t, int c) {
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        tmem_st8(tbase + lane_off + op_col(t, (CW / 16) * wg + 2 * c + q), pk[q]);
+        tmem_st8(tbase + lane_off + C::op_col(t, (CW / 16) * wg + 2 * c + q), pk[q]);
     };
     auto written = [&](int t) {
       tmem_wait_st();
@@ -315,11 +331,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < NC; ++c) load(s_col(t), c, s[c]);
+        for (int c = 0; c < NC; ++c) load(C::s_col(t), c, s[c]);
         const bool masked = masked_at(t);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          load(kP, c, x);
+          load(C::kP, c, x);
           tmem_wait_ld();
           if (c == NC - 1) {
             tc_fence_before();
@@ -336,8 +352,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int tile0 = (tb + t) * BN;
         if (tile0 < hull.lo || tile0 + BN > hull.hi) {
           // K rows that no row of the block sees meet dS = 0: make them 0 too.
-          if (wg == 0 && (tile0 + r < hull.lo || tile0 + r >= hull.hi))
-            zero_row<NH, HALF>(sm.k[t % NK], r);
+          if (wg == 0 && r < BN && (tile0 + r < hull.lo || tile0 + r >= hull.hi))
+            zero_row<NH, TILE>(sm.k[t % NK], r);
           fence_proxy_async_smem();
         }
         written(t);
@@ -351,7 +367,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (!ok) return;
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < NC; ++c) load(s_col(t), c, s[c]);
+        for (int c = 0; c < NC; ++c) load(C::s_col(t), c, s[c]);
         tmem_wait_ld();
         const bool masked = masked_at(t);
 #pragma unroll
@@ -371,7 +387,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const bool masked = masked_at(t);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          load(kP, c, x);
+          load(C::kP, c, x);
           tmem_wait_ld();
           if (c == NC - 1) {
             tc_fence_before();
@@ -389,7 +405,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     ok = __all_sync(0xffffffffu, ok && !*abort_flag);
     tc_fence_after();
     static_assert(BM * (DH * 2 + 16) <= sizeof(sm.k), "epilogue staging fits in the ring");
-    store_block<DH, NWG>(tbase + lane_off + kAcc, a.tau, T == 0, &sm.k[0][0][0], wg, r,
+    store_block<DH, NWG>(tbase + lane_off + C::kAcc, a.tau, T == 0, &sm.k[0][0][0], wg, r,
                          threadIdx.x - 64, min(BM, rows - row0), ok,
                          static_cast<__nv_bfloat16*>(a.dQ) +
                              (static_cast<size_t>(g) * rows + row0) * DH);
@@ -400,40 +416,47 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tbase, 512);
+    tmem_dealloc(tbase, C::kColumns);
   }
 }
 
-template <int DH, bool CAP, bool BIAS>
+template <int DH, bool SMALL, bool CAP, bool BIAS>
 cudaError_t launch(const AttnArgs& a) {
   const int heads = a.B * a.Hkv, rows = a.H / a.Hkv * a.Nq;
+  using C = Cfg<DH, SMALL>;
   CUtensorMap mq, mo, mk, mv;
   cudaError_t e = tc_map_bf16(&mq, a.Q, heads, rows, BM, DH);
   if (e == cudaSuccess) e = tc_map_bf16(&mo, a.dO, heads, rows, BM, DH);
-  if (e == cudaSuccess) e = tc_map_bf16(&mk, a.K, heads, a.Nk, BN, DH);
-  if (e == cudaSuccess) e = tc_map_bf16(&mv, a.V, heads, a.Nk, BN, DH);
+  if (e == cudaSuccess) e = tc_map_bf16(&mk, a.K, heads, a.Nk, C::BN, DH);
+  if (e == cudaSuccess) e = tc_map_bf16(&mv, a.V, heads, a.Nk, C::BN, DH);
   if (e != cudaSuccess) return e;
-  constexpr size_t smem = sizeof(SmemQ<DH>) + 1024;
-  static_assert(smem <= 232448, "shared memory");
-  const auto kernel = tc_dq_kernel<DH, CAP, BIAS>;
+  constexpr size_t smem = sizeof(SmemQ<DH, SMALL>) + 1024;
+  static_assert(smem <= (SMALL ? 115712 : 232448), "shared memory");
+  const auto kernel = tc_dq_kernel<DH, SMALL, CAP, BIAS>;
   e = tc_set_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int blocks = (rows + BM - 1) / BM;
   const long long grid = static_cast<long long>(blocks) * heads;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  return launch_after(true, kernel, dim3(static_cast<unsigned>(grid)), NTHREADS, smem, 1, a.stream,
-                      mq, mo, mk, mv, a, blocks);
+  return launch_after(true, kernel, dim3(static_cast<unsigned>(grid)), C::kThreads, smem, 1,
+                      a.stream, mq, mo, mk, mv, a, blocks);
 }
 
-template <int DH>
+template <int DH, bool SMALL>
 cudaError_t launch(const AttnArgs& a) {
   const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;
-  return cap ? (bias ? launch<DH, true, true>(a) : launch<DH, true, false>(a))
-             : (bias ? launch<DH, false, true>(a) : launch<DH, false, false>(a));
+  return cap ? (bias ? launch<DH, SMALL, true, true>(a) : launch<DH, SMALL, true, false>(a))
+             : (bias ? launch<DH, SMALL, false, true>(a) : launch<DH, SMALL, false, false>(a));
 }
 
 }  // namespace
 
-cudaError_t tc_attn_dq(const AttnArgs& a) { return a.d == 64 ? launch<64>(a) : launch<128>(a); }
+// Small blocks up to 2048 keys (the gradient of B4 H12 d64: N1024 causal 61 -> 54
+// us, without a mask 75 -> 73; B2 H12 N2048 causal 75 -> 71, without 112 either
+// way).
+cudaError_t tc_attn_dq(const AttnArgs& a) {
+  if (a.d == 128) return launch<128, false>(a);
+  return a.Nk <= 2048 ? launch<64, true>(a) : launch<64, false>(a);
+}
 
 }  // namespace flashbob

@@ -3,22 +3,25 @@
 //   P~ = exp2(s - m) with a running row maximum m,  l = sum P~,
 //   O = (sum P~ V) / l,  L = (m + log2 l) ln 2.
 //
-// 320 threads: warp 0 TMA, warp 1 TMEM allocation and MMA issue, warps 2-5
-// and 6-9 elementwise warpgroups.  The block's work is a run of units; unit u
-// goes to warpgroup u mod 2 and one of three score buffers in TMEM, where P~
-// (bf16) replaces the scores as the A operand of P~ V.  Each warpgroup has its
-// own O~ accumulator and raises its m only when a unit's maximum exceeds it by
-// more than 8 (log2 units), so O~ is rarely rescaled.
+// Warp 0 TMA, warp 1 TMEM allocation and MMA issue, then NW = 2 elementwise
+// warpgroups.  The block's work is a run of units; unit u goes to warpgroup
+// u mod 2 and one of three score buffers in TMEM, where P~ (bf16) replaces the
+// scores as the A operand of P~ V.  Each warpgroup has its own O~ accumulator
+// and raises its m only when a unit's maximum exceeds it by more than 8 (log2
+// units), so O~ is rarely rescaled.
 //   MT = 1: 128 group rows a block, the warpgroups take alternate key tiles and
 //     merge their (m, l, O~) at the end.  Where rows are few (tokens over a
 //     cache) the keys are also cut into runs of blocks joined by a second launch.
 //   MT = 2: 256 group rows, warpgroup w holds rows 128 w .. and both take every
 //     key tile, so a tile from L2 feeds twice the products (see two_blocks).
+//   NW = 1 (d = 64, MT = 1): one warpgroup, tiles of 64 keys, half of an SM's
+//     TMEM and shared memory, so that two blocks fill and drain beside each
+//     other (see small_blocks).
 // Key tiles outside the hull of the block's ranges are not visited; tiles
 // inside every row's range run without a mask.  V rows outside the hull are
 // zeroed in shared memory before they meet P~ = 0, so a cache may hold
 // anything behind its last key.
-// TMEM: O~ of warpgroups 0 and 1 (DH columns each), then three score buffers.
+// TMEM: O~ of each warpgroup (DH columns), then three score buffers.
 // Measured (B1 H8 N16384, no mask): 521 us at d = 64, 1054 TFLOP/s, where the
 // hand-offs between MMAs and elementwise warps bound it (with MT = 2, 590 us, a
 // copy without arithmetic took 515, one with a quarter of the MMAs 480); 741 us
@@ -32,31 +35,33 @@ using namespace tc;
 using namespace attn;
 
 constexpr int BM = kTcRows;
-constexpr int NTHREADS = 320;
 constexpr int NBUF = 3;
 constexpr uint32_t HALF_BLOCK = BM * 64 * 2;
 constexpr float kRescale = 8.f;
 
-template <int DH, int MT>
+template <int DH, int MT, int NW>
 struct Cfg {
+  static constexpr int kThreads = 64 + 128 * NW;
   static constexpr int kHalves = DH / 64;
-  static constexpr int kBN = DH == 64 ? 128 : 64;
+  static constexpr int kBN = DH == 64 && NW == 2 ? 128 : 64;
   static constexpr uint32_t kHalfTile = kBN * 64 * 2;
-  static constexpr int kStages = (MT == 2 ? 5 : 6) - (DH == 64 ? 0 : 1);
-  static_assert(2 * DH + NBUF * kBN <= 512, "TMEM columns");
+  static constexpr int kStages = (MT == 2 || NW == 1 ? 5 : 6) - (DH == 64 ? 0 : 1);
+  static constexpr int kColumns = 256 * NW;
+  static_assert(NW * DH + NBUF * kBN <= kColumns, "TMEM columns");
+  static_assert(NBUF <= kStages, "the first scores need their tiles at once");
 };
 
 constexpr int kStageLd = 64 + 4;  // epilogue: 64 columns of every row at a time
 
-template <int DH, int MT>
+template <int DH, int MT, int NW>
 struct SmemF {
-  static constexpr int NST = Cfg<DH, MT>::kStages;
-  static constexpr int NH = Cfg<DH, MT>::kHalves;
+  using C = Cfg<DH, MT, NW>;
+  static constexpr int NST = C::kStages, NH = C::kHalves;
   alignas(1024) uint8_t q[MT][NH][HALF_BLOCK];
-  alignas(1024) uint8_t kv[NST][2][NH][Cfg<DH, MT>::kHalfTile];
+  alignas(1024) uint8_t kv[NST][2][NH][C::kHalfTile];
   float part_m[2][BM];
   float part_l[2][BM];
-  int hull[8][4];  // of each elementwise warp's rows
+  int hull[4 * NW][4];  // of each elementwise warp's rows
   uint64_t bar_q;
   uint64_t kv_full[NST];
   uint64_t kv_empty[NST];
@@ -111,17 +116,17 @@ __device__ __forceinline__ void weights64(const Score<CAP, BIAS>& sc, const uint
   l += acc.x + acc.y;
 }
 
-template <int DH, int MT, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(NTHREADS, 1)
+template <int DH, int MT, int NW, bool CAP, bool BIAS>
+__global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1))
     tc_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                    const __grid_constant__ CUtensorMap mV, const __grid_constant__ AttnArgs a,
                    int blocks, int splits) {
   extern __shared__ uint8_t smem_raw[];
-  using C = Cfg<DH, MT>;
+  using C = Cfg<DH, MT, NW>;
   constexpr int NST = C::kStages, NH = C::kHalves, BN = C::kBN;
   constexpr uint32_t HT = C::kHalfTile;
-  constexpr uint32_t kScore = 2 * DH;
-  SmemF<DH, MT>& sm = *reinterpret_cast<SmemF<DH, MT>*>(
+  constexpr uint32_t kScore = NW * DH;
+  SmemF<DH, MT, NW>& sm = *reinterpret_cast<SmemF<DH, MT, NW>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = a.B * a.Hkv, G = a.H / a.Hkv, rows = G * a.Nq;
@@ -153,7 +158,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int h = 0; h < NH; ++h)
         tma_load_3d(sm.q[w][h], &mQ, &sm.bar_q, 64 * h, row0 + BM * w, g);
   }
-  if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+  if (warp == 1) tmem_alloc(&sm.tmem_base, C::kColumns);
   // Elementwise threads: TMEM lane r of row block w.
   const int wg = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane;
   GroupRow gr{empty_view(), 0.f};
@@ -166,7 +171,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
-  const Hull hull = join_hulls(sm.hull, 8);
+  const Hull hull = join_hulls(sm.hull, 4 * NW);
   // Key tiles of the hull, and this split's run of them.
   const int t_lo = hull.lo < hull.hi ? hull.lo / BN : 0;
   const int t_n = hull.lo < hull.hi ? (hull.hi + BN - 1) / BN - t_lo : 0;
@@ -217,11 +222,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int s = tile(u) % NST;
       const uint32_t sc = tbase + kScore + BN * (u % NBUF);
       const uint64_t dv = dV0 + s * kStage;
-      const uint32_t acc_col = tbase + DH * (u & 1);
+      const uint32_t acc_col = tbase + DH * (u % NW);
 #pragma unroll
       for (int c = 0; c < BN / 16; ++c)
-        mma_ts(acc_col, sc + 8 * c, dv + ((16 * 128 * c) >> 4), idO, (u >= 2 || c > 0));
-      mma_commit(&sm.pv_done[u & 1]);
+        mma_ts(acc_col, sc + 8 * c, dv + ((16 * 128 * c) >> 4), idO, (u >= NW || c > 0));
+      mma_commit(&sm.pv_done[u % NW]);
       if (MT == 1 || (u & 1)) mma_commit(&sm.kv_empty[s]);
     };
     if (elect_one()) {
@@ -266,7 +271,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     int n = 0;  // units of this warpgroup
-    for (int u = wg; u < U; u += 2, ++n) {
+    for (int u = wg; u < U; u += NW, ++n) {
       const int col0 = (tb + (MT == 2 ? u >> 1 : u)) * BN;
       ok = ok && wait_warp(&sm.sc_full[u % NBUF], (u / NBUF) & 1, abort_flag, err);
       if (!ok) break;
@@ -353,17 +358,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // O~ = s_0 O~_0 + s_1 O~_1, l = s_0 l_0 + s_1 l_1.  An accumulator whose
     // warpgroup had no unit was never written.
     float mm = m, lsum = l, s0 = 1.f, s1 = 0.f;
-    if (MT == 1) {
+    if (MT == 1 && NW == 2) {
       sm.part_m[wg][r] = m;
       sm.part_l[wg][r] = l;
-      named_bar_sync(1, 256);
+      named_bar_sync(1, 128 * NW);
       const float m0 = sm.part_m[0][r], m1 = sm.part_m[1][r];
       mm = fmaxf(m0, m1);
       s0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - mm);
       s1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - mm);
       lsum = s0 * sm.part_l[0][r] + s1 * sm.part_l[1][r];
     }
-    const bool any0 = T > 0, any1 = MT == 1 ? T > 1 : false;
+    const bool any0 = T > 0, any1 = MT == 1 && NW == 2 && T > 1;
     const float inv = splits > 1 ? 1.f : lsum > 0.f ? 1.f / lsum : 0.f;
     s0 = any0 ? s0 * inv : 0.f;
     s1 = any1 ? s1 * inv : 0.f;
@@ -381,15 +386,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int tid = threadIdx.x - 64;
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
-      if (h > 0) named_bar_sync(1, 256);
-      constexpr int kCols = MT == 2 ? 64 : 32;  // MT = 1: each warpgroup forms half the columns
-      const int c0 = MT == 2 ? 0 : 32 * wg;
+      if (h > 0) named_bar_sync(1, 128 * NW);
+      // With one accumulator for two warpgroups each forms half the columns.
+      constexpr bool kShare = MT == 1 && NW == 2;
+      constexpr int kCols = kShare ? 32 : 64;
+      const int c0 = kShare ? 32 * wg : 0;
       const int sr = MT == 2 ? BM * wg + r : r;
 #pragma unroll
       for (int c = 0; c < kCols; c += 16) {
         const uint32_t col = 64 * h + c0 + c;
         uint32_t v0[16], v1[16];
-        if (MT == 2) {
+        if (!kShare) {
           tmem_ld16(acc_own + col, v0);
         } else {
           tmem_ld16(tbase + lane_off + col, v0);
@@ -403,15 +410,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             o[q] = any0 ? s0 * u2f(v0[4 * k + q]) : 0.f;
-            if (MT == 1 && any1) o[q] = fmaf(s1, u2f(v1[4 * k + q]), o[q]);
+            if (kShare && any1) o[q] = fmaf(s1, u2f(v1[4 * k + q]), o[q]);
           }
           s4[k] = make_float4(o[0], o[1], o[2], o[3]);
         }
       }
-      named_bar_sync(1, 256);
+      named_bar_sync(1, 128 * NW);
       const int live = min(MT * BM, rows - row0);
       if (ok) {
-        for (int f = tid; f < live * 16; f += 256) {
+        for (int f = tid; f < live * 16; f += 128 * NW) {
           const int rr = f >> 4, c4 = f & 15;
           const float4 v = *reinterpret_cast<const float4*>(st + rr * kStageLd + 4 * c4);
           const size_t at = (base + row0 + rr) * DH + 64 * h + 4 * c4;
@@ -431,37 +438,38 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tbase, 512);
+    tmem_dealloc(tbase, C::kColumns);
   }
 }
 
-template <int DH, int MT, bool CAP, bool BIAS>
+template <int DH, int MT, int NW, bool CAP, bool BIAS>
 cudaError_t launch(const AttnArgs& a, int splits) {
   const int heads = a.B * a.Hkv, rows = a.H / a.Hkv * a.Nq;
+  using C = Cfg<DH, MT, NW>;
   CUtensorMap mq, mk, mv;
   cudaError_t e = tc_map_bf16(&mq, a.Q, heads, rows, BM, DH);
-  if (e == cudaSuccess) e = tc_map_bf16(&mk, a.K, heads, a.Nk, Cfg<DH, MT>::kBN, DH);
-  if (e == cudaSuccess) e = tc_map_bf16(&mv, a.V, heads, a.Nk, Cfg<DH, MT>::kBN, DH);
+  if (e == cudaSuccess) e = tc_map_bf16(&mk, a.K, heads, a.Nk, C::kBN, DH);
+  if (e == cudaSuccess) e = tc_map_bf16(&mv, a.V, heads, a.Nk, C::kBN, DH);
   if (e != cudaSuccess) return e;
-  const size_t smem = sizeof(SmemF<DH, MT>) + 1024;
-  static_assert(sizeof(SmemF<DH, MT>) + 1024 <= 232448, "shared memory");
-  const auto kernel = tc_attn_kernel<DH, MT, CAP, BIAS>;
+  constexpr size_t smem = sizeof(SmemF<DH, MT, NW>) + 1024;
+  static_assert(smem <= (NW == 1 ? 115712 : 232448), "shared memory");
+  const auto kernel = tc_attn_kernel<DH, MT, NW, CAP, BIAS>;
   e = tc_set_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int blocks = (rows + MT * BM - 1) / (MT * BM);
   const long long grid = static_cast<long long>(blocks) * splits * heads;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  kernel<<<static_cast<unsigned>(grid), NTHREADS, smem, a.stream>>>(mq, mk, mv, a, blocks, splits);
+  kernel<<<static_cast<unsigned>(grid), C::kThreads, smem, a.stream>>>(mq, mk, mv, a, blocks, splits);
   return cudaGetLastError();
 }
 
-template <int DH, int MT>
+template <int DH, int MT, int NW>
 cudaError_t launch(const AttnArgs& a, int splits) {
   const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;
-  return cap ? (bias ? launch<DH, MT, true, true>(a, splits)
-                     : launch<DH, MT, true, false>(a, splits))
-             : (bias ? launch<DH, MT, false, true>(a, splits)
-                     : launch<DH, MT, false, false>(a, splits));
+  return cap ? (bias ? launch<DH, MT, NW, true, true>(a, splits)
+                     : launch<DH, MT, NW, true, false>(a, splits))
+             : (bias ? launch<DH, MT, NW, false, true>(a, splits)
+                     : launch<DH, MT, NW, false, false>(a, splits));
 }
 
 }  // namespace
@@ -478,6 +486,17 @@ bool two_blocks(const AttnArgs& a) {
   const long long rows = static_cast<long long>(a.H / a.Hkv) * a.Nq;
   return a.d == 128 && rows > BM &&
          static_cast<long long>(a.B) * a.Hkv * ((rows + 255) / 256) >= 2 * kSMs;
+}
+
+// Two small blocks an SM at d = 64 where a block's fixed cost counts: few keys
+// (B8 H12 N256 causal 20 -> 16 us, B4 H12 N1024 in 5 documents 32 -> 26; equal at
+// N1024 without a mask and at N2048 with a causal one, and 52 for 46 without),
+// and the tokens of many requests (B64 H8, 2048 keys: 73 -> 65 us).  At d = 128
+// only two stages fit (32 requests of 4096 keys: 124 for 108 us).
+bool small_blocks(const AttnArgs& a) {
+  const long long rows = static_cast<long long>(a.H / a.Hkv) * a.Nq;
+  return a.Nk <= 1024 ||
+         (rows <= BM && static_cast<long long>(a.B) * a.Hkv > kSMs);
 }
 
 }  // namespace
@@ -499,8 +518,8 @@ int tc_attn_splits(const AttnArgs& a) {
 cudaError_t tc_attn(const AttnArgs& a) {
   const int splits = tc_attn_splits(a);
   cudaError_t e;
-  if (a.d == 64) e = launch<64, 1>(a, splits);
-  else e = two_blocks(a) ? launch<128, 2>(a, splits) : launch<128, 1>(a, splits);
+  if (a.d == 64) e = small_blocks(a) ? launch<64, 1, 1>(a, splits) : launch<64, 1, 2>(a, splits);
+  else e = two_blocks(a) ? launch<128, 2, 2>(a, splits) : launch<128, 1, 2>(a, splits);
   return e == cudaSuccess && splits > 1 ? attn_join(a, splits) : e;
 }
 

@@ -122,6 +122,12 @@ CASES = [
     # long
     dict(H=2, Hkv=1, Nq=3000, Nk=3000, causal=True, cap=8.0),
     dict(H=1, Hkv=1, Nq=2500, Nk=2500, mask="docs", d=128),
+    # the large blocks of d = 64, and tokens of many requests
+    dict(B=2, H=2, Hkv=2, Nq=1300, Nk=1300, mask="docs", bias=True),
+    dict(H=4, Hkv=2, Nq=333, Nk=1200, mask="random", cap=3.0),
+    dict(B=2, H=2, Hkv=1, Nq=1100, Nk=1100, mask="prefix", cap=2.0, bias=True),
+    dict(H=2, Hkv=2, Nq=1100, Nk=1030, causal=True), dict(Nq=150, Nk=1100, mask="nothing"),
+    dict(B=80, H=4, Hkv=2, Nq=1, Nk=1500, mask="token", bias=True),
 ]
 
 
