@@ -73,11 +73,28 @@ __global__ void __launch_bounds__(kRangeThreads)
 // Row state of the gradient.  Eight lanes take a row: D = dO . O in fp32,
 // the row's range, position and slope, and the bounds of 64 rows.
 // ---------------------------------------------------------------------------
-template <typename T>
+template <typename T, int D>
 __device__ __forceinline__ float dot_part(const T* __restrict__ x, const T* __restrict__ y, int d,
                                           int lane8) {
   float s = 0.f;
-  if ((d & 3) == 0) {
+  if (D > 0) {  // bf16, d = D: 16-byte loads
+    uint4 a[D / 64 + 1], b[D / 64 + 1];
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) {
+      a[k] = reinterpret_cast<const uint4*>(x)[8 * k + lane8];
+      b[k] = reinterpret_cast<const uint4*>(y)[8 * k + lane8];
+    }
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) {
+      const uint32_t u[4] = {a[k].x, a[k].y, a[k].z, a[k].w};
+      const uint32_t v[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s = fmaf(__uint_as_float(u[e] << 16), __uint_as_float(v[e] << 16), s);
+        s = fmaf(__uint_as_float(u[e] & 0xFFFF0000u), __uint_as_float(v[e] & 0xFFFF0000u), s);
+      }
+    }
+  } else if ((d & 3) == 0) {
     for (int k = 4 * lane8; k < d; k += 32) {
       const float4 a = ld4(x + k), b = ld4(y + k);
       s = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s))));
@@ -88,7 +105,7 @@ __device__ __forceinline__ float dot_part(const T* __restrict__ x, const T* __re
   return s;
 }
 
-template <typename T>
+template <typename T, int D>
 __global__ void __launch_bounds__(256)
     grad_rows_kernel(const T* __restrict__ O, const T* __restrict__ dO,
                      const float* __restrict__ L, const int* __restrict__ ranges,
@@ -103,21 +120,26 @@ __global__ void __launch_bounds__(256)
   const GradRows out = grad_rows(workspace, B * Hkv, rows);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lane8 = lane & 7;
   int b_lo = INT_MAX, b_hi = 0, i_lo = 0, i_hi = INT_MAX;
+  // All loads of both rows first: none waits for another.
+  float dots[2] = {0.f, 0.f}, ls[2] = {0.f, 0.f};
+  RowView views[2] = {empty_view(), empty_view()};
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int r = blockIdx.x * kBoundRows + warp * 8 + u * 4 + (lane >> 3);
-    float dot = 0.f;
-    RowView v = empty_view();
-    float l = 0.f;
-    const bool live = r < rows;
     const size_t row = static_cast<size_t>(g) * rows + r;
-    if (live) {
-      v = row_view(ranges, q_pos, static_cast<size_t>(blockIdx.z) * Nq, r % Nq, Nk, causal);
-      if (v.hi > 0) {  // a row that sees nothing may hold anything
-        dot = dot_part(O + row * d, dO + row * d, d, lane8);
-        l = L[row];
-      }
+    if (r < rows) {
+      dots[u] = dot_part<T, D>(O + row * d, dO + row * d, d, lane8);
+      ls[u] = L[row];
+      views[u] = row_view(ranges, q_pos, static_cast<size_t>(blockIdx.z) * Nq, r % Nq, Nk, causal);
     }
+  }
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int r = blockIdx.x * kBoundRows + warp * 8 + u * 4 + (lane >> 3);
+    const bool live = r < rows;
+    const RowView v = views[u];
+    const float l = ls[u];
+    float dot = dots[u];  // used only where v.hi > 0: else the row may hold anything
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     if (live) {
@@ -229,11 +251,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   if (threadIdx.x == 0) L[row] = (m + log2f(l)) * kLn2;  // -inf for a row that sees nothing
 }
 
-template <typename T>
+template <typename T, int D>
 cudaError_t launch_grad_rows(const AttnArgs& a) {
   const int rows = a.H / a.Hkv * a.Nq;
   const dim3 grid(padded_rows(rows) / kBoundRows, a.Hkv, a.B);
-  grad_rows_kernel<T><<<grid, 256, 0, a.stream>>>(
+  grad_rows_kernel<T, D><<<grid, 256, 0, a.stream>>>(
       static_cast<const T*>(a.O), static_cast<const T*>(a.dO), a.L, a.ranges, a.q_pos, a.slopes,
       a.workspace, a.B, a.H, a.Hkv, a.Nq, a.Nk, a.d, a.causal ? 1 : 0,
       a.cap > 0.f ? 0.f : 1.f / a.tau, a.bf16 && a.d == 64 ? 1 : 0);
@@ -251,7 +273,10 @@ cudaError_t launch_join(const AttnArgs& a, int splits) {
 }  // namespace
 
 cudaError_t attn_grad_rows(const AttnArgs& a) {
-  return a.bf16 ? launch_grad_rows<__nv_bfloat16>(a) : launch_grad_rows<float>(a);
+  if (!a.bf16) return launch_grad_rows<float, 0>(a);
+  return a.d == 64    ? launch_grad_rows<__nv_bfloat16, 64>(a)
+         : a.d == 128 ? launch_grad_rows<__nv_bfloat16, 128>(a)
+                      : launch_grad_rows<__nv_bfloat16, 0>(a);
 }
 
 cudaError_t attn_join(const AttnArgs& a, int splits) {
