@@ -17,6 +17,10 @@
 //   NW = 1 (d = 64, MT = 1): one warpgroup, tiles of 64 keys, half of an SM's
 //     TMEM and shared memory, so that two blocks fill and drain beside each
 //     other (see small_blocks).
+//   TOKEN (MT = 1, up to 32 group rows): Q lies four times in the tile, once for
+//     each warp of a warpgroup, and each warp takes a quarter of the columns (its
+//     P~ is 0 in the others), so no warp works on a whole tile alone; the warps'
+//     parts are merged like those of the warpgroups.
 // Key tiles outside the hull of the block's ranges are not visited; tiles
 // inside every row's range run without a mask.  V rows outside the hull are
 // zeroed in shared memory before they meet P~ = 0, so a cache may hold
@@ -67,21 +71,21 @@ struct SmemF {
   uint64_t kv_empty[NST];
   uint64_t sc_full[NBUF];
   uint64_t op_ready[NBUF];
-  uint64_t pv_done[2];
+  uint64_t pv_done[2];  // of even and odd units
   uint64_t out_full;
   uint32_t tmem_base;
   int abort_flag;
 };
 
-// Largest visible score of 64 columns from jbase on (log2 units, relative to
+// Largest visible score of 16 NQ columns from jbase on (log2 units, relative to
 // nothing).  Without a bias the score grows with the raw product, so the
 // maximum is taken over those.
-template <bool CAP, bool BIAS, bool MASKED>
-__device__ __forceinline__ float max64(const Score<CAP, BIAS>& sc, const uint32_t (&s)[4][16],
-                                       int jbase, int lo, int hi, float dist) {
+template <bool MASKED, int NQ, bool CAP, bool BIAS>
+__device__ __forceinline__ float largest(const Score<CAP, BIAS>& sc, const uint32_t (&s)[NQ][16],
+                                         int jbase, int lo, int hi, float dist) {
   float mr = -INFINITY;
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
+  for (int q = 0; q < NQ; ++q)
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
       const int j = jbase + 16 * q + e;
@@ -93,14 +97,14 @@ __device__ __forceinline__ float max64(const Score<CAP, BIAS>& sc, const uint32_
   return mr;
 }
 
-// P~ of 64 columns as bf16 pairs, added to the row sum (before rounding).
-template <bool CAP, bool BIAS, bool MASKED>
-__device__ __forceinline__ void weights64(const Score<CAP, BIAS>& sc, const uint32_t (&s)[4][16],
-                                          int jbase, int lo, int hi, float dist, float m,
-                                          float& l, uint32_t (&pk)[4][8]) {
+// P~ of those columns as bf16 pairs, added to the row sum (before rounding).
+template <bool MASKED, int NQ, bool CAP, bool BIAS>
+__device__ __forceinline__ void weights(const Score<CAP, BIAS>& sc, const uint32_t (&s)[NQ][16],
+                                        int jbase, int lo, int hi, float dist, float m, float& l,
+                                        uint32_t (&pk)[NQ][8]) {
   float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
+  for (int q = 0; q < NQ; ++q)
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
       const float2 t = sc.from(f2(s[q][e], s[q][e + 1]), dist + (16 * q + e), m, sc.slope2);
@@ -116,7 +120,7 @@ __device__ __forceinline__ void weights64(const Score<CAP, BIAS>& sc, const uint
   l += acc.x + acc.y;
 }
 
-template <int DH, int MT, int NW, bool CAP, bool BIAS>
+template <int DH, int MT, int NW, bool TOKEN, bool CAP, bool BIAS>
 __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1))
     tc_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                    const __grid_constant__ CUtensorMap mV, const __grid_constant__ AttnArgs a,
@@ -155,14 +159,18 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
     // Q is under way while the ranges are read.
     mbar_expect_tx(&sm.bar_q, MT * NH * HALF_BLOCK);
     for (int w = 0; w < MT; ++w)
-      for (int h = 0; h < NH; ++h)
-        tma_load_3d(sm.q[w][h], &mQ, &sm.bar_q, 64 * h, row0 + BM * w, g);
+      for (int h = 0; h < NH; ++h) {
+        if (!TOKEN) tma_load_3d(sm.q[w][h], &mQ, &sm.bar_q, 64 * h, row0 + BM * w, g);
+        else  // boxes of 32 rows, the same four times
+          for (int q = 0; q < 4; ++q)
+            tma_load_3d(sm.q[w][h] + q * (HALF_BLOCK / 4), &mQ, &sm.bar_q, 64 * h, row0, g);
+      }
   }
   if (warp == 1) tmem_alloc(&sm.tmem_base, C::kColumns);
   // Elementwise threads: TMEM lane r of row block w.
   const int wg = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane;
   GroupRow gr{empty_view(), 0.f};
-  const int row = row0 + r + (MT == 2 ? BM * wg : 0);
+  const int row = row0 + (TOKEN ? lane : r) + (MT == 2 ? BM * wg : 0);
   if (warp >= 2) {
     gr = group_row(a, g / a.Hkv, g % a.Hkv, row, rows);
     warp_hull(gr.v, row < rows, lane, sm.hull[4 * wg + quad]);
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
 #pragma unroll
       for (int c = 0; c < BN / 16; ++c)
         mma_ts(acc_col, sc + 8 * c, dv + ((16 * 128 * c) >> 4), idO, (u >= NW || c > 0));
-      mma_commit(&sm.pv_done[u % NW]);
+      mma_commit(&sm.pv_done[u & 1]);
       if (MT == 1 || (u & 1)) mma_commit(&sm.kv_empty[s]);
     };
     if (elect_one()) {
@@ -259,7 +267,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
     const int lo = gr.v.lo, hi = gr.v.hi;
     const Hull own = MT == 2 ? join_hulls(sm.hull + 4 * wg, 4) : hull;
     const Score<CAP, BIAS> score(a, gr.slope2);
-    const bool any_row = row0 + (MT == 2 ? BM * wg : 0) + quad * 32 < rows;
+    const bool any_row = TOKEN || row0 + (MT == 2 ? BM * wg : 0) + quad * 32 < rows;
     // V rows that no row of the block sees meet P~ = 0: make them 0 too.
     auto clear_hidden = [&](int u, int col0) {
       if (col0 < hull.lo || col0 + BN > hull.hi) {
@@ -279,7 +287,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
       const uint32_t sc = tbase + lane_off + kScore + BN * (u % NBUF);
       const bool masked = col0 < own.in_lo || col0 + BN > own.in_hi;
       const float dist = BIAS ? static_cast<float>(col0 - gr.v.pos) : 0.f;
-      if (!any_row) {  // tokens over a cache fill few of the 128 rows
+      if (!any_row) {
         clear_hidden(u, col0);
         warp_arrive(&sm.op_ready[u % NBUF]);
         continue;
@@ -287,24 +295,27 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
       // Two 64-column groups at d = 64: the second is read twice, so that one
       // group is held in registers at a time, and P~ of columns 16 c .. goes
       // to columns 8 c .., onto scores already used.
+      // TOKEN: the columns of this warp alone.
+      constexpr int kGroup = TOKEN ? BN / 4 : 64, NQ = kGroup / 16;
+      const int c_own = TOKEN ? kGroup * quad : 0, c_end = TOKEN ? c_own + kGroup : BN;
       float mr = -INFINITY;
-      uint32_t s[4][16];
-      auto load64 = [&](int c) {
+      uint32_t s[NQ][16];
+      auto load = [&](int c) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld16(sc + c + 16 * q, s[q]);
+        for (int q = 0; q < NQ; ++q) tmem_ld16(sc + c + 16 * q, s[q]);
         tmem_wait_ld();
       };
       auto max_of = [&](int c) {
         if (BIAS) score.tanh_of(s);
-        mr = fmaxf(mr, masked ? max64<CAP, BIAS, true>(score, s, col0 + c, lo, hi, dist + c)
-                              : max64<CAP, BIAS, false>(score, s, col0 + c, lo, hi, dist + c));
+        mr = fmaxf(mr, masked ? largest<true>(score, s, col0 + c, lo, hi, dist + c)
+                              : largest<false>(score, s, col0 + c, lo, hi, dist + c));
       };
-      if (BN == 128) {
-        load64(64);
+      if (!TOKEN && BN == 128) {
+        load(64);
         max_of(64);
       }
-      load64(0);
-      max_of(0);
+      load(c_own);
+      max_of(c_own);
       float mt = mr;
       if (!BIAS) {
         mt = mr * score.c1;
@@ -317,7 +328,11 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
         m = mt;
       }
       if (__any_sync(0xffffffffu, raise && factor < 1.f) && n > 0) {
-        ok = wait_warp(&sm.pv_done[wg], (n - 1) & 1, abort_flag, err);
+        // The products of this warpgroup's last unit.  S(u) was issued behind
+        // those of unit u - 3, so of the barrier's phases only the last may be
+        // open, and its parity tells.
+        const int last = u - NW;
+        ok = wait_warp(&sm.pv_done[last & 1], (last >> 1) & 1, abort_flag, err);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -336,14 +351,20 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
         }
       }
 #pragma unroll
-      for (int c = 0; c < BN; c += 64) {
-        if (c > 0) load64(c);
-        if (!BIAS || c > 0) score.tanh_of(s);
-        uint32_t pk[4][8];
-        if (masked) weights64<CAP, BIAS, true>(score, s, col0 + c, lo, hi, dist + c, m, l, pk);
-        else weights64<CAP, BIAS, false>(score, s, col0 + c, lo, hi, dist + c, m, l, pk);
+      for (int c = c_own; c < c_end; c += kGroup) {
+        if (c > c_own) load(c);
+        if (!BIAS || c > c_own) score.tanh_of(s);
+        uint32_t pk[NQ][8];
+        if (masked) weights<true>(score, s, col0 + c, lo, hi, dist + c, m, l, pk);
+        else weights<false>(score, s, col0 + c, lo, hi, dist + c, m, l, pk);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_st8(sc + c / 2 + 8 * q, pk[q]);
+        for (int q = 0; q < NQ; ++q) tmem_st8(sc + c / 2 + 8 * q, pk[q]);
+      }
+      if (TOKEN) {  // P~ of the columns of the others
+        const uint32_t none[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int c = 0; c < BN / 16; ++c)
+          if (c / NQ != quad) tmem_st8(sc + 8 * c, none);
       }
       clear_hidden(u, col0);
       tmem_wait_st();
@@ -358,7 +379,19 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
     // O~ = s_0 O~_0 + s_1 O~_1, l = s_0 l_0 + s_1 l_1.  An accumulator whose
     // warpgroup had no unit was never written.
     float mm = m, lsum = l, s0 = 1.f, s1 = 0.f;
-    if (MT == 1 && NW == 2) {
+    if (TOKEN) {
+      // The same for the row's parts in all warps; each warp scales its own.
+      sm.part_m[wg][r] = m;
+      sm.part_l[wg][r] = l;
+      named_bar_sync(1, 128 * NW);
+      for (int w = 0; w < 4 * NW; ++w) mm = fmaxf(mm, sm.part_m[w / 4][32 * (w % 4) + lane]);
+      lsum = 0.f;
+      for (int w = 0; w < 4 * NW; ++w) {
+        const float mw = sm.part_m[w / 4][32 * (w % 4) + lane];
+        if (mw != -INFINITY) lsum += ex2_approx(mw - mm) * sm.part_l[w / 4][32 * (w % 4) + lane];
+      }
+      s0 = m == -INFINITY ? 0.f : ex2_approx(m - mm);
+    } else if (MT == 1 && NW == 2) {
       sm.part_m[wg][r] = m;
       sm.part_l[wg][r] = l;
       named_bar_sync(1, 128 * NW);
@@ -368,30 +401,31 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
       s1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - mm);
       lsum = s0 * sm.part_l[0][r] + s1 * sm.part_l[1][r];
     }
-    const bool any0 = T > 0, any1 = MT == 1 && NW == 2 && T > 1;
+    const bool any0 = T > (TOKEN ? wg : 0), any1 = !TOKEN && MT == 1 && NW == 2 && T > 1;
     const float inv = splits > 1 ? 1.f : lsum > 0.f ? 1.f / lsum : 0.f;
     s0 = any0 ? s0 * inv : 0.f;
     s1 = any1 ? s1 * inv : 0.f;
     const size_t all = static_cast<size_t>(a.B) * a.H * a.Nq;
     const size_t base = static_cast<size_t>(g) * rows;  // first row of the group
     const Partials part = partials(a.workspace, all, DH, splits);
-    if (ok && row < rows && (MT == 2 || wg == 0)) {
+    if (ok && row < rows && (MT == 2 || wg == 0) && (!TOKEN || quad == 0)) {
       if (splits > 1) part.ml[split * all + base + row] = make_float2(mm, lsum);
       else a.L[base + row] = (mm + __log2f(lsum)) * kLn2;
     }
     // Every MMA is done, so the ring is idle: 64 columns of O at a time go
     // through it and leave with coalesced stores.
     float* st = reinterpret_cast<float*>(&sm.kv[0][0][0][0]);
-    static_assert(MT * BM * kStageLd * 4 <= sizeof(sm.kv), "epilogue staging fits in the ring");
+    static_assert((TOKEN ? NW : MT) * BM * kStageLd * 4 <= sizeof(sm.kv),
+                  "epilogue staging fits in the ring");
     const int tid = threadIdx.x - 64;
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       if (h > 0) named_bar_sync(1, 128 * NW);
       // With one accumulator for two warpgroups each forms half the columns.
-      constexpr bool kShare = MT == 1 && NW == 2;
+      constexpr bool kShare = !TOKEN && MT == 1 && NW == 2;
       constexpr int kCols = kShare ? 32 : 64;
       const int c0 = kShare ? 32 * wg : 0;
-      const int sr = MT == 2 ? BM * wg + r : r;
+      const int sr = MT == 2 || TOKEN ? BM * wg + r : r;
 #pragma unroll
       for (int c = 0; c < kCols; c += 16) {
         const uint32_t col = 64 * h + c0 + c;
@@ -420,7 +454,15 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
       if (ok) {
         for (int f = tid; f < live * 16; f += 128 * NW) {
           const int rr = f >> 4, c4 = f & 15;
-          const float4 v = *reinterpret_cast<const float4*>(st + rr * kStageLd + 4 * c4);
+          float4 v = *reinterpret_cast<const float4*>(st + rr * kStageLd + 4 * c4);
+          if (TOKEN) {
+#pragma unroll
+            for (int w = 1; w < 4 * NW; ++w) {
+              const float4 x =
+                  *reinterpret_cast<const float4*>(st + (32 * w + rr) * kStageLd + 4 * c4);
+              v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            }
+          }
           const size_t at = (base + row0 + rr) * DH + 64 * h + 4 * c4;
           if (splits > 1) {
             *reinterpret_cast<float4*>(part.o + split * all * DH + at) = v;
@@ -442,18 +484,18 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
   }
 }
 
-template <int DH, int MT, int NW, bool CAP, bool BIAS>
+template <int DH, int MT, int NW, bool TOKEN, bool CAP, bool BIAS>
 cudaError_t launch(const AttnArgs& a, int splits) {
   const int heads = a.B * a.Hkv, rows = a.H / a.Hkv * a.Nq;
   using C = Cfg<DH, MT, NW>;
   CUtensorMap mq, mk, mv;
-  cudaError_t e = tc_map_bf16(&mq, a.Q, heads, rows, BM, DH);
+  cudaError_t e = tc_map_bf16(&mq, a.Q, heads, rows, TOKEN ? BM / 4 : BM, DH);
   if (e == cudaSuccess) e = tc_map_bf16(&mk, a.K, heads, a.Nk, C::kBN, DH);
   if (e == cudaSuccess) e = tc_map_bf16(&mv, a.V, heads, a.Nk, C::kBN, DH);
   if (e != cudaSuccess) return e;
   constexpr size_t smem = sizeof(SmemF<DH, MT, NW>) + 1024;
   static_assert(smem <= (NW == 1 ? 115712 : 232448), "shared memory");
-  const auto kernel = tc_attn_kernel<DH, MT, NW, CAP, BIAS>;
+  const auto kernel = tc_attn_kernel<DH, MT, NW, TOKEN, CAP, BIAS>;
   e = tc_set_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int blocks = (rows + MT * BM - 1) / (MT * BM);
@@ -463,13 +505,13 @@ cudaError_t launch(const AttnArgs& a, int splits) {
   return cudaGetLastError();
 }
 
-template <int DH, int MT, int NW>
+template <int DH, int MT, int NW, bool TOKEN = false>
 cudaError_t launch(const AttnArgs& a, int splits) {
   const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;
-  return cap ? (bias ? launch<DH, MT, NW, true, true>(a, splits)
-                     : launch<DH, MT, NW, true, false>(a, splits))
-             : (bias ? launch<DH, MT, NW, false, true>(a, splits)
-                     : launch<DH, MT, NW, false, false>(a, splits));
+  return cap ? (bias ? launch<DH, MT, NW, TOKEN, true, true>(a, splits)
+                     : launch<DH, MT, NW, TOKEN, true, false>(a, splits))
+             : (bias ? launch<DH, MT, NW, TOKEN, false, true>(a, splits)
+                     : launch<DH, MT, NW, TOKEN, false, false>(a, splits));
 }
 
 }  // namespace
@@ -518,7 +560,14 @@ int tc_attn_splits(const AttnArgs& a) {
 cudaError_t tc_attn(const AttnArgs& a) {
   const int splits = tc_attn_splits(a);
   cudaError_t e;
-  if (a.d == 64) e = small_blocks(a) ? launch<64, 1, 1>(a, splits) : launch<64, 1, 2>(a, splits);
+  // Up to 32 group rows: the TOKEN kernels (32 requests of up to 8192 keys, capped,
+  // H32 Hkv8 d128: 137 -> 130 us; one of 1000 keys, H12 d64: 17.5 -> 13.5 us).
+  const bool token = static_cast<long long>(a.H / a.Hkv) * a.Nq <= BM / 4;
+  if (a.d == 64 && small_blocks(a))
+    e = token ? launch<64, 1, 1, true>(a, splits) : launch<64, 1, 1>(a, splits);
+  else if (a.d == 64)
+    e = token ? launch<64, 1, 2, true>(a, splits) : launch<64, 1, 2>(a, splits);
+  else if (token) e = launch<128, 1, 2, true>(a, splits);
   else e = two_blocks(a) ? launch<128, 2, 2>(a, splits) : launch<128, 1, 2>(a, splits);
   return e == cudaSuccess && splits > 1 ? attn_join(a, splits) : e;
 }

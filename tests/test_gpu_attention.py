@@ -128,6 +128,8 @@ CASES = [
     dict(B=2, H=2, Hkv=1, Nq=1100, Nk=1100, mask="prefix", cap=2.0, bias=True),
     dict(H=2, Hkv=2, Nq=1100, Nk=1030, causal=True), dict(Nq=150, Nk=1100, mask="nothing"),
     dict(B=80, H=4, Hkv=2, Nq=1, Nk=1500, mask="token", bias=True),
+    dict(B=40, H=8, Hkv=2, Nq=12, Nk=1000, mask="token", bias=True),  # the maxima keep rising
+    dict(B=40, H=8, Hkv=2, Nq=12, Nk=1100, mask="token", bias=True, d=128),
 ]
 
 
