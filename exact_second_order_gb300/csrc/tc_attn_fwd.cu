@@ -43,32 +43,43 @@ constexpr int NBUF = 3;
 constexpr uint32_t HALF_BLOCK = BM * 64 * 2;
 constexpr float kRescale = 8.f;
 
-template <int DH, int MT, int NW>
+template <int DH, int MT, int NW, bool TOKEN>
 struct Cfg {
   static constexpr int kThreads = 64 + 128 * NW;
   static constexpr int kHalves = DH / 64;
   static constexpr int kBN = DH == 64 && NW == 2 ? 128 : 64;
   static constexpr uint32_t kHalfTile = kBN * 64 * 2;
-  static constexpr int kStages = (MT == 2 || NW == 1 ? 5 : 6) - (DH == 64 ? 0 : 1);
+  // K and V arrive and leave together: the MMA warp's waits count where the MMAs
+  // bound the kernel (with rings of their own 890 us for 741 at B1 H8 N16384
+  // d128).  For tokens, which the loads bound, they do not: a K tile is free after
+  // its scores, a V tile three units later (an SM then reads a cache at more than
+  // 45 GB/s: 130 -> 122 us for the 32 requests below).
+  static constexpr bool kJoint = !TOKEN;
+  static constexpr int kPairs = (MT == 2 || NW == 1 ? 5 : 6) - (DH == 64 ? 0 : 1);
+  static constexpr int kK = kJoint ? kPairs : 5;
+  static constexpr int kV = kJoint ? kPairs : DH == 64 && NW == 2 ? 7 : 6;
+  static constexpr int k_tile(int s) { return kJoint ? 2 * s : s; }  // in the one array of tiles
+  static constexpr int v_tile(int s) { return kJoint ? 2 * s + 1 : kK + s; }
   static constexpr int kColumns = 256 * NW;
   static_assert(NW * DH + NBUF * kBN <= kColumns, "TMEM columns");
-  static_assert(NBUF <= kStages, "the first scores need their tiles at once");
+  static_assert(NBUF <= kK && NBUF <= kV, "the first scores need their tiles at once");
+  static_assert(!kJoint || kK == kV, "one ring");
 };
 
 constexpr int kStageLd = 64 + 4;  // epilogue: 64 columns of every row at a time
 
-template <int DH, int MT, int NW>
+template <int DH, int MT, int NW, bool TOKEN>
 struct SmemF {
-  using C = Cfg<DH, MT, NW>;
-  static constexpr int NST = C::kStages, NH = C::kHalves;
+  using C = Cfg<DH, MT, NW, TOKEN>;
+  static constexpr int NK = C::kK, NV = C::kV, NH = C::kHalves;
   alignas(1024) uint8_t q[MT][NH][HALF_BLOCK];
-  alignas(1024) uint8_t kv[NST][2][NH][C::kHalfTile];
+  alignas(1024) uint8_t kv[NK + NV][NH][C::kHalfTile];
   float part_m[2][BM];
   float part_l[2][BM];
   int hull[4 * NW][4];  // of each elementwise warp's rows
   uint64_t bar_q;
-  uint64_t kv_full[NST];
-  uint64_t kv_empty[NST];
+  uint64_t k_full[NK], k_empty[NK];
+  uint64_t v_full[NV], v_empty[NV];
   uint64_t sc_full[NBUF];
   uint64_t op_ready[NBUF];
   uint64_t pv_done[2];  // of even and odd units
@@ -121,16 +132,16 @@ __device__ __forceinline__ void weights(const Score<CAP, BIAS>& sc, const uint32
 }
 
 template <int DH, int MT, int NW, bool TOKEN, bool CAP, bool BIAS>
-__global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1))
+__global__ void __launch_bounds__((Cfg<DH, MT, NW, TOKEN>::kThreads), (NW == 1 ? 2 : 1))
     tc_attn_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                    const __grid_constant__ CUtensorMap mV, const __grid_constant__ AttnArgs a,
                    int blocks, int splits) {
   extern __shared__ uint8_t smem_raw[];
-  using C = Cfg<DH, MT, NW>;
-  constexpr int NST = C::kStages, NH = C::kHalves, BN = C::kBN;
+  using C = Cfg<DH, MT, NW, TOKEN>;
+  constexpr int NK = C::kK, NV = C::kV, NH = C::kHalves, BN = C::kBN;
   constexpr uint32_t HT = C::kHalfTile;
   constexpr uint32_t kScore = NW * DH;
-  SmemF<DH, MT, NW>& sm = *reinterpret_cast<SmemF<DH, MT, NW>*>(
+  SmemF<DH, MT, NW, TOKEN>& sm = *reinterpret_cast<SmemF<DH, MT, NW, TOKEN>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = a.B * a.Hkv, G = a.H / a.Hkv, rows = G * a.Nq;
@@ -143,10 +154,8 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
   if (splits > 1) release_next();
   if (threadIdx.x == 0) {
     mbar_init(&sm.bar_q, 1);
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(&sm.kv_full[s], 1);
-      mbar_init(&sm.kv_empty[s], 1);
-    }
+    for (int s = 0; s < NK; ++s) mbar_init(&sm.k_full[s], 1), mbar_init(&sm.k_empty[s], 1);
+    for (int s = 0; s < NV; ++s) mbar_init(&sm.v_full[s], 1), mbar_init(&sm.v_empty[s], 1);
     for (int b = 0; b < NBUF; ++b) {
       mbar_init(&sm.sc_full[b], 1);
       mbar_init(&sm.op_ready[b], 4);
@@ -191,31 +200,42 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
     if (lane == 0) {
       tma_prefetch_desc(&mK);
       tma_prefetch_desc(&mV);
-      int issued = 0;
+      int nk = 0, nv = 0;
       for (int t = 0; t < T; ++t) {
-        const int s = t % NST;
-        if (t >= NST && !wait_one(&sm.kv_empty[s], ((t / NST) - 1) & 1, abort_flag, err)) break;
-        mbar_expect_tx(&sm.kv_full[s], 2 * NH * HT);
+        const int sk = t % NK, sv = t % NV;
+        uint64_t* v_bar = C::kJoint ? &sm.k_full[sk] : &sm.v_full[sv];
+        if (!C::kJoint && t >= NK &&
+            !wait_one(&sm.k_empty[sk], ((t / NK) - 1) & 1, abort_flag, err))
+          break;
+        if (C::kJoint && t >= NV &&
+            !wait_one(&sm.v_empty[sv], ((t / NV) - 1) & 1, abort_flag, err))
+          break;
+        mbar_expect_tx(&sm.k_full[sk], (C::kJoint ? 2 : 1) * NH * HT);
         for (int h = 0; h < NH; ++h)
-          tma_load_3d(sm.kv[s][0][h], &mK, &sm.kv_full[s], 64 * h, (tb + t) * BN, g);
+          tma_load_3d(sm.kv[C::k_tile(sk)][h], &mK, &sm.k_full[sk], 64 * h, (tb + t) * BN, g);
+        nk = t + 1;
+        if (!C::kJoint) {
+          if (t >= NV && !wait_one(&sm.v_empty[sv], ((t / NV) - 1) & 1, abort_flag, err)) break;
+          mbar_expect_tx(v_bar, NH * HT);
+        }
         for (int h = 0; h < NH; ++h)
-          tma_load_3d(sm.kv[s][1][h], &mV, &sm.kv_full[s], 64 * h, (tb + t) * BN, g);
-        issued = t + 1;
+          tma_load_3d(sm.kv[C::v_tile(sv)][h], &mV, v_bar, 64 * h, (tb + t) * BN, g);
+        if (!C::kJoint) nv = t + 1;
       }
       drain_wait(&sm.bar_q, 0);
-      for (int t = issued > NST ? issued - NST : 0; t < issued; ++t)
-        drain_wait(&sm.kv_full[t % NST], (t / NST) & 1);
+      for (int t = nk > NK ? nk - NK : 0; t < nk; ++t) drain_wait(&sm.k_full[t % NK], (t / NK) & 1);
+      for (int t = nv > NV ? nv - NV : 0; t < nv; ++t) drain_wait(&sm.v_full[t % NV], (t / NV) & 1);
     }
   } else if (warp == 1) {
     constexpr uint32_t idS = idesc_bf16(BM, BN, false);
     constexpr uint32_t idO = idesc_bf16(BM, DH, true);
     const uint64_t dQ = smem_desc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
-    const uint64_t dK0 = smem_desc_sw128(smem_u32(sm.kv[0][0][0]), 16, 1024);
-    const uint64_t dV0 = smem_desc_sw128(smem_u32(sm.kv[0][1][0]), HT, 1024);
-    constexpr uint64_t kStage = sizeof(sm.kv[0]) >> 4;
+    const uint64_t dK0 = smem_desc_sw128(smem_u32(sm.kv[C::k_tile(0)][0]), 16, 1024);
+    const uint64_t dV0 = smem_desc_sw128(smem_u32(sm.kv[C::v_tile(0)][0]), HT, 1024);
+    constexpr uint64_t kStep = (C::k_tile(1) * sizeof(sm.kv[0])) >> 4;  // V's is the same
     auto tile = [](int u) { return MT == 2 ? u >> 1 : u; };
     auto issue_scores = [&](int u) {
-      const uint64_t so = (tile(u) % NST) * kStage;
+      const uint64_t so = (tile(u) % NK) * kStep;
       const uint64_t qo = MT == 2 ? (u & 1) * (uint64_t)((NH * HALF_BLOCK) >> 4) : 0;
       const uint32_t sc = tbase + kScore + BN * (u % NBUF);
 #pragma unroll
@@ -225,34 +245,36 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
                kk > 0);
       }
       mma_commit(&sm.sc_full[u % NBUF]);
+      if (!C::kJoint) mma_commit(&sm.k_empty[tile(u) % NK]);
     };
     auto issue_pv = [&](int u) {
-      const int s = tile(u) % NST;
+      const int s = tile(u) % NV;
       const uint32_t sc = tbase + kScore + BN * (u % NBUF);
-      const uint64_t dv = dV0 + s * kStage;
+      const uint64_t dv = dV0 + s * kStep;
       const uint32_t acc_col = tbase + DH * (u % NW);
 #pragma unroll
       for (int c = 0; c < BN / 16; ++c)
         mma_ts(acc_col, sc + 8 * c, dv + ((16 * 128 * c) >> 4), idO, (u >= NW || c > 0));
       mma_commit(&sm.pv_done[u & 1]);
-      if (MT == 1 || (u & 1)) mma_commit(&sm.kv_empty[s]);
+      if (MT == 1 || (u & 1)) mma_commit(&sm.v_empty[s]);
     };
     if (elect_one()) {
       bool ok = wait_one(&sm.bar_q, 0, abort_flag, err);
       tc_fence_after();
       for (int u = 0; ok && u < NBUF && u < U; ++u) {
-        ok = wait_one(&sm.kv_full[tile(u) % NST], (tile(u) / NST) & 1, abort_flag, err);
+        ok = wait_one(&sm.k_full[tile(u) % NK], (tile(u) / NK) & 1, abort_flag, err);
         tc_fence_after();
         if (ok) issue_scores(u);
       }
       for (int u = 0; ok && u < U; ++u) {
-        ok = wait_one(&sm.op_ready[u % NBUF], (u / NBUF) & 1, abort_flag, err);
+        ok = (C::kJoint || wait_one(&sm.v_full[u % NV], (u / NV) & 1, abort_flag, err)) &&
+             wait_one(&sm.op_ready[u % NBUF], (u / NBUF) & 1, abort_flag, err);
         if (!ok) break;
         tc_fence_after();
         issue_pv(u);
         if (u + NBUF < U) {
           const int tn = tile(u + NBUF);
-          ok = wait_one(&sm.kv_full[tn % NST], (tn / NST) & 1, abort_flag, err);
+          ok = wait_one(&sm.k_full[tn % NK], (tn / NK) & 1, abort_flag, err);
           if (!ok) break;
           tc_fence_after();
           issue_scores(u + NBUF);
@@ -270,11 +292,14 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
     const bool any_row = TOKEN || row0 + (MT == 2 ? BM * wg : 0) + quad * 32 < rows;
     // V rows that no row of the block sees meet P~ = 0: make them 0 too.
     auto clear_hidden = [&](int u, int col0) {
-      if (col0 < hull.lo || col0 + BN > hull.hi) {
-        if (r < BN && (col0 + r < hull.lo || col0 + r >= hull.hi))
-          zero_row<NH, HT>(sm.kv[(MT == 2 ? u >> 1 : u) % NST][1], r);
-        fence_proxy_async_smem();
-      }
+      if (col0 >= hull.lo && col0 + BN <= hull.hi) return true;
+      const int t = MT == 2 ? u >> 1 : u;
+      if (!C::kJoint && !wait_warp(&sm.v_full[t % NV], (t / NV) & 1, abort_flag, err))
+        return false;
+      if (r < BN && (col0 + r < hull.lo || col0 + r >= hull.hi))
+        zero_row<NH, HT>(sm.kv[C::v_tile(t % NV)], r);
+      fence_proxy_async_smem();
+      return true;
     };
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -288,7 +313,8 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
       const bool masked = col0 < own.in_lo || col0 + BN > own.in_hi;
       const float dist = BIAS ? static_cast<float>(col0 - gr.v.pos) : 0.f;
       if (!any_row) {
-        clear_hidden(u, col0);
+        ok = clear_hidden(u, col0);
+        if (!ok) break;
         warp_arrive(&sm.op_ready[u % NBUF]);
         continue;
       }
@@ -366,7 +392,8 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
         for (int c = 0; c < BN / 16; ++c)
           if (c / NQ != quad) tmem_st8(sc + 8 * c, none);
       }
-      clear_hidden(u, col0);
+      ok = clear_hidden(u, col0);
+      if (!ok) break;
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(&sm.op_ready[u % NBUF]);
@@ -414,7 +441,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
     }
     // Every MMA is done, so the ring is idle: 64 columns of O at a time go
     // through it and leave with coalesced stores.
-    float* st = reinterpret_cast<float*>(&sm.kv[0][0][0][0]);
+    float* st = reinterpret_cast<float*>(&sm.kv[0][0][0]);
     static_assert((TOKEN ? NW : MT) * BM * kStageLd * 4 <= sizeof(sm.kv),
                   "epilogue staging fits in the ring");
     const int tid = threadIdx.x - 64;
@@ -487,13 +514,13 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW>::kThreads), (NW == 1 ? 2 : 1)
 template <int DH, int MT, int NW, bool TOKEN, bool CAP, bool BIAS>
 cudaError_t launch(const AttnArgs& a, int splits) {
   const int heads = a.B * a.Hkv, rows = a.H / a.Hkv * a.Nq;
-  using C = Cfg<DH, MT, NW>;
+  using C = Cfg<DH, MT, NW, TOKEN>;
   CUtensorMap mq, mk, mv;
   cudaError_t e = tc_map_bf16(&mq, a.Q, heads, rows, TOKEN ? BM / 4 : BM, DH);
   if (e == cudaSuccess) e = tc_map_bf16(&mk, a.K, heads, a.Nk, C::kBN, DH);
   if (e == cudaSuccess) e = tc_map_bf16(&mv, a.V, heads, a.Nk, C::kBN, DH);
   if (e != cudaSuccess) return e;
-  constexpr size_t smem = sizeof(SmemF<DH, MT, NW>) + 1024;
+  constexpr size_t smem = sizeof(SmemF<DH, MT, NW, TOKEN>) + 1024;
   static_assert(smem <= (NW == 1 ? 115712 : 232448), "shared memory");
   const auto kernel = tc_attn_kernel<DH, MT, NW, TOKEN, CAP, BIAS>;
   e = tc_set_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
