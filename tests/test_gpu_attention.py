@@ -128,6 +128,10 @@ CASES = [
     dict(B=2, H=2, Hkv=1, Nq=1100, Nk=1100, mask="prefix", cap=2.0, bias=True),
     dict(H=2, Hkv=2, Nq=1100, Nk=1030, causal=True), dict(Nq=150, Nk=1100, mask="nothing"),
     dict(B=80, H=4, Hkv=2, Nq=1, Nk=1500, mask="token", bias=True),
+    # biases at positions in no order
+    dict(B=2, H=4, Hkv=2, Nq=300, Nk=420, mask="random", bias=True),
+    dict(B=2, H=4, Hkv=2, Nq=300, Nk=420, mask="random", bias=True, cap=3.0),
+    dict(H=2, Hkv=1, Nq=260, Nk=2300, mask="random", bias=True),
     dict(B=40, H=8, Hkv=2, Nq=12, Nk=1000, mask="token", bias=True),  # the maxima keep rising
     dict(B=40, H=8, Hkv=2, Nq=12, Nk=1100, mask="token", bias=True, d=128),
 ]
@@ -231,6 +235,51 @@ def test_captured_and_replayed(dtype, d, Nq):
     for out, want in zip(outs, fresh):
         for k in want:
             assert torch.equal(out[k], want[k]), k
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F32, 40)])
+def test_calls_behind_one_another_on_one_workspace(dtype, d):
+    """A gradient's launches overlap; what follows on the stream must find them
+    done: the next call on the same workspace, and a kernel that reads dQ."""
+    tau, sets = 0.2, []
+    for seed in (1, 2):
+        x, form = make(2, 6, 2, 700, 700, d, dtype, mask="docs", bias=True, seed=seed)
+        O, L = fb.attention(x["Q"], x["K"], x["V"], tau, **form)
+        sets.append((x, form, O, L))
+    x = sets[0][0]
+    bwd = fb.flashbob_attention_workspace(2, 6, 2, 700, 700, d, int(dtype == BF))[1]
+    workspace = torch.empty(bwd, dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(x[k]) for k in ("Q", "K", "V")]
+
+    def call(k):
+        x, form, O, L = sets[k]
+        fb.flashbob_attention_grad(x["Q"], x["K"], x["V"], O, L, x["dO"], form["ranges"],
+                                   form["q_pos"], form["slopes"], tau, 0.0, *outs, workspace)
+
+    want = []
+    for k in (0, 1):
+        call(k)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in outs])
+
+    def several():
+        got = []
+        for n in range(12):
+            call(n % 2)
+            got.append([t.clone() for t in outs])
+        return got
+
+    def same(got):
+        torch.cuda.synchronize()
+        return all(torch.equal(a, b) for n in range(12) for a, b in zip(got[n], want[n % 2]))
+
+    assert same(several())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = several()
+    for _ in range(3):
+        graph.replay()
+    assert same(got)
 
 
 @pytest.mark.parametrize("dtype,d", [(F32, 20), (BF, 64), (BF, 128)])
