@@ -9,11 +9,12 @@
 namespace flashbob {
 namespace attn {
 
-// tanh x = x + x^3 (k0 + k1 x^2 + k2 x^4 + k3 x^6) for |x| <= 0.7: least
-// squares with weights adapted until the largest error is smallest (Lawson's
-// method).
-__device__ constexpr float kTanh[4] = {-0.3333006501197815f, 0.1327691525220871f,
-                                       -0.050674621015787125f, 0.013599642552435398f};
+// tanh x = x + x^3 (k0 + k1 x^2 + k2 x^4) for |x| <= kTanhTo, off by 1.9e-7:
+// least squares with weights adapted until the largest error is smallest
+// (Lawson's method).
+__device__ constexpr float kTanh[3] = {-0.33326461911201477f, 0.13185861706733704f,
+                                       -0.044229257851839066f};
+constexpr float kTanhTo = 0.5f;
 
 // rcp.approx (1 ulp) of a value in [1, inf]: 1 / inf is 0.
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -144,24 +145,33 @@ __device__ __forceinline__ Hull join_hulls(const int (*h)[4], int n) {
 // Scores of raw products in log2 units:
 //   not capped: raw c1;  capped: c2 t with t = tanh(raw tau / cap), which
 //   tanh_of puts in place of the raw products;  biased: minus slope2 |j - pos|.
-// tanh of 16 n products: where all of the warp's arguments are at most 0.7 (the
-// cap is there for outliers) an odd polynomial, fitted to tanh in the maximum
-// norm (error 1.3e-7 absolute), in 3.5 packed fp32 instructions an element;
-// else 1 - 2 / (1 + e^{2 x}), two MUFU operations (a few 2^-24).  With the
-// exponential of the softmax those would be three an element, and the MUFU pipe
-// bounds the kernel: the forward of B1 H8 N16384 d64 took 1370 us with them,
-// against 570 without a cap.  (tanh.approx leaves 2^-11, which exp turns into
-// percents of P.)  The polynomial brought it to 1100 us.
+// tanh of 16 n products: where all of the warp's arguments are at most 0.5 (the
+// cap is there for outliers) an odd polynomial in the raw products, tau / cap in
+// its coefficients (error 2.3e-7 absolute with the roundings), in 2.5 packed fp32
+// instructions an element; else 1 - 2 / (1 + e^{2 x}), two MUFU operations (a few
+// 2^-24).  With the exponential of the softmax those would be three an element,
+// and the MUFU pipe bounds the kernel: the forward of B1 H8 N16384 d64 took 1370 us
+// with them, against 570 without a cap; 1100 with a polynomial to 0.7 (3.5
+// instructions, one more coefficient).  (tanh.approx leaves 2^-11, which exp
+// turns into percents of P.)
 template <bool CAP, bool BIAS>
 struct Score {
   float c1;      // tau log2 e; capped: tau / cap
   float c2;      // cap log2 e
   float slope2;
+  float a1, a2, a3;  // capped: k0 c1^3, k1 c1^5, k2 c1^7
+  float most_raw;    // the polynomial's range in raw products
 
   __device__ __forceinline__ Score(const AttnArgs& a, float slope) {
     c1 = CAP ? a.tau / a.cap : a.tau * kLog2e;
     c2 = a.cap * kLog2e;
     slope2 = slope;
+    const float q = c1 * c1;
+    a1 = kTanh[0] * (q * c1);
+    a2 = kTanh[1] * (q * q * c1);
+    a3 = kTanh[2] * (q * q * (q * c1));
+    // Beyond these c1^7 or raw^2 would leave fp32's range.
+    most_raw = c1 >= 0x1p-16f && c1 <= 0x1p16f ? kTanhTo / c1 : -1.f;
   }
   __device__ __forceinline__ float tanh_exact(float raw) const {
     return fmaf(-2.f, rcp_approx(1.f + tc::ex2_approx(raw * (2.f * kLog2e * c1))), 1.f);
@@ -174,7 +184,7 @@ struct Score {
     for (int q = 0; q < N; ++q)
 #pragma unroll
       for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(tc::u2f(s[q][e])));
-    if (__any_sync(0xffffffffu, !(most * c1 <= 0.7f))) {
+    if (__any_sync(0xffffffffu, !(most <= most_raw))) {
 #pragma unroll
       for (int q = 0; q < N; ++q)
 #pragma unroll
@@ -186,12 +196,11 @@ struct Score {
     for (int q = 0; q < N; ++q)
 #pragma unroll
       for (int e = 0; e < 16; e += 2) {
-        const float2 x = tc::fmul2(tc::f2(s[q][e], s[q][e + 1]), two(c1));
-        const float2 u = tc::fmul2(x, x);
-        float2 p = tc::ffma2(u, two(kTanh[3]), two(kTanh[2]));
-        p = tc::ffma2(p, u, two(kTanh[1]));
-        p = tc::ffma2(p, u, two(kTanh[0]));
-        const float2 t = tc::ffma2(tc::fmul2(x, u), p, x);
+        const float2 x = tc::f2(s[q][e], s[q][e + 1]), w = tc::fmul2(x, x);
+        float2 p = tc::ffma2(w, two(a3), two(a2));
+        p = tc::ffma2(p, w, two(a1));
+        p = tc::ffma2(p, w, two(c1));
+        const float2 t = tc::fmul2(x, p);
         s[q][e] = __float_as_uint(t.x);
         s[q][e + 1] = __float_as_uint(t.y);
       }
