@@ -152,7 +152,7 @@ __device__ __forceinline__ Hull join_hulls(const int (*h)[4], int n) {
 // 2^-24).  With the exponential of the softmax those would be three an element,
 // and the MUFU pipe bounds the kernel: the forward of B1 H8 N16384 d64 took 1370 us
 // with them, against 570 without a cap; 1100 with a polynomial to 0.7 (3.5
-// instructions, one more coefficient).  (tanh.approx leaves 2^-11, which exp
+// instructions, one more coefficient); now 929 and 519.  (tanh.approx leaves 2^-11, which exp
 // turns into percents of P.)
 template <bool CAP, bool BIAS>
 struct Score {
