@@ -655,17 +655,30 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (blockIdx.x + 1 == gridDim.x) wait_ahead();
 }
 
-// How many blocks share a key block: a power of two up to 8 that makes up to
-// kGridPerSM blocks for each SM, with two row tiles at least for each.  Unequal
-// key blocks (a causal mask) then even out, too: 128 of them with 4 to 64 tiles
-// took 166 us alone.
-constexpr int kGridPerSM = 4;
+// How many blocks share a key block: the power of two with the least of an
+// estimate in row tiles (1.65 us at d = 128, 0.93 at d = 64).  A block costs `own`
+// tiles to fill and drain, in a cluster `shared` (its launch and the exchange, 19
+// us); the longest block has all the tiles, the average one half of them under a
+// mask.  Clusters of 8 fit 16 times.  B2 H16 Hkv4 N2047 d128 causal, 128 key blocks
+// of up to 64 tiles: alone 109 us, in twos 86, in fours 109; B1 H8 N2048, 128 of up
+// to 16 (the whole gradient): 44, 54, 77; B1 H4 Hkv1 N4096, 32 of up to 128: in fours
+// 77, in eights 97.
 int cluster_size(const AttnArgs& a) {
-  const long long blocks = static_cast<long long>((a.Nk + BM - 1) / BM) * a.B * a.Hkv;
-  const long long tiles = (static_cast<long long>(a.H / a.Hkv) * a.Nq + BQ - 1) / BQ;
-  int S = 1;
-  while (S < 8 && blocks * S * 2 <= kGridPerSM * kSMs && tiles >= S * 4) S *= 2;
-  return S;
+  const double blocks = static_cast<double>((a.Nk + BM - 1) / BM) * a.B * a.Hkv;
+  const long long rows = static_cast<long long>(a.H / a.Hkv) * a.Nq;
+  const double tiles = static_cast<double>((rows + BQ - 1) / BQ);
+  const double mean = a.causal || a.ranges ? tiles / 2 : tiles;
+  const double own = a.d == 128 ? 5 : 9, shared = a.d == 128 ? 12 : 20;
+  int best = 1;
+  double least = 0;
+  for (int S = 1; S <= 8 && tiles >= S; S *= 2) {
+    const double fixed = S == 1 ? own : shared, waves = blocks * S / (S == 8 ? 128 : kSMs);
+    const double longest = fixed + tiles / S, all = waves * (fixed + mean / S);
+    if (S == 8 && waves > 1) break;
+    const double cost = waves > 1 && all > longest ? all : longest;
+    if (S == 1 || cost < least) best = S, least = cost;
+  }
+  return best;
 }
 
 template <int DH, bool CAP, bool BIAS>
