@@ -44,7 +44,7 @@ __device__ __forceinline__ RowView row_view(const int* __restrict__ ranges,
 __device__ __forceinline__ int warp_min(int v) { return __reduce_min_sync(0xffffffffu, v); }
 __device__ __forceinline__ int warp_max(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
-// Row state that the gradient kernels read, one entry for each group row,
+// Row state that the dK, dV kernels read, one entry for each group row,
 // rows padded to a multiple of kRowPad per (batch, key/value head):
 //   info  {lo, hi, pos, slope log2 e (as bits)},
 //   l2, dd  L log2 e and D; +inf in place of L for rows that see nothing and
@@ -106,6 +106,12 @@ __host__ __device__ inline Partials partials(void* workspace, size_t rows, int d
 // A call's later launches may start before the launch ahead has ended
 // (launch_after): wait_ahead returns when it has, with all that it wrote;
 // release_next lets the next launch start once every block has come here.
+// Only wait_ahead makes writes visible, and only those of the launch directly
+// ahead: what an early launch reads without it, or past it, has to be complete
+// before the call's first launch, which is never early.  So a gradient runs the
+// row state, then dK and dV (which wait for it), then dQ, which reads the call's
+// inputs alone.  Whatever follows a call on the stream waits for its last launch
+// alone, so the last block of an early launch always waits for the launch ahead.
 __device__ __forceinline__ void wait_ahead() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void release_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -149,6 +155,46 @@ __device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
   const uint2 r = *reinterpret_cast<const uint2*>(p);
   return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u),
                      __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xFFFF0000u));
+}
+
+// Lane `lane8` of eight: its part of the dot product of two rows.
+template <typename T, int D>
+__device__ __forceinline__ float dot_part(const T* __restrict__ x, const T* __restrict__ y, int d,
+                                          int lane8) {
+  float s = 0.f;
+  if (D > 0) {  // bf16, d = D: 16-byte loads
+    uint4 a[D / 64 + 1], b[D / 64 + 1];
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) {
+      a[k] = reinterpret_cast<const uint4*>(x)[8 * k + lane8];
+      b[k] = reinterpret_cast<const uint4*>(y)[8 * k + lane8];
+    }
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) {
+      const uint32_t u[4] = {a[k].x, a[k].y, a[k].z, a[k].w};
+      const uint32_t v[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s = fmaf(__uint_as_float(u[e] << 16), __uint_as_float(v[e] << 16), s);
+        s = fmaf(__uint_as_float(u[e] & 0xFFFF0000u), __uint_as_float(v[e] & 0xFFFF0000u), s);
+      }
+    }
+  } else if ((d & 3) == 0) {
+    for (int k = 4 * lane8; k < d; k += 32) {
+      const float4 a = ld4(x + k), b = ld4(y + k);
+      s = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s))));
+    }
+  } else {
+    for (int k = lane8; k < d; k += 8) s = fmaf(to_f(x[k]), to_f(y[k]), s);
+  }
+  return s;
+}
+
+// The same sum in all eight lanes (of a whole warp).
+__device__ __forceinline__ float sum8(float v) {
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
 }  // namespace attn

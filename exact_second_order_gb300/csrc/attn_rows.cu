@@ -70,41 +70,9 @@ __global__ void __launch_bounds__(kRangeThreads)
 }
 
 // ---------------------------------------------------------------------------
-// Row state of the gradient.  Eight lanes take a row: D = dO . O in fp32,
+// Row state that dK and dV read.  Eight lanes take a row: D = dO . O in fp32,
 // the row's range, position and slope, and the bounds of 64 rows.
 // ---------------------------------------------------------------------------
-template <typename T, int D>
-__device__ __forceinline__ float dot_part(const T* __restrict__ x, const T* __restrict__ y, int d,
-                                          int lane8) {
-  float s = 0.f;
-  if (D > 0) {  // bf16, d = D: 16-byte loads
-    uint4 a[D / 64 + 1], b[D / 64 + 1];
-#pragma unroll
-    for (int k = 0; k < D / 64; ++k) {
-      a[k] = reinterpret_cast<const uint4*>(x)[8 * k + lane8];
-      b[k] = reinterpret_cast<const uint4*>(y)[8 * k + lane8];
-    }
-#pragma unroll
-    for (int k = 0; k < D / 64; ++k) {
-      const uint32_t u[4] = {a[k].x, a[k].y, a[k].z, a[k].w};
-      const uint32_t v[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s = fmaf(__uint_as_float(u[e] << 16), __uint_as_float(v[e] << 16), s);
-        s = fmaf(__uint_as_float(u[e] & 0xFFFF0000u), __uint_as_float(v[e] & 0xFFFF0000u), s);
-      }
-    }
-  } else if ((d & 3) == 0) {
-    for (int k = 4 * lane8; k < d; k += 32) {
-      const float4 a = ld4(x + k), b = ld4(y + k);
-      s = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s))));
-    }
-  } else {
-    for (int k = lane8; k < d; k += 8) s = fmaf(to_f(x[k]), to_f(y[k]), s);
-  }
-  return s;
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
     grad_rows_kernel(const T* __restrict__ O, const T* __restrict__ dO,
@@ -139,9 +107,7 @@ __global__ void __launch_bounds__(256)
     const bool live = r < rows;
     const RowView v = views[u];
     const float l = ls[u];
-    float dot = dots[u];  // used only where v.hi > 0: else the row may hold anything
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    const float dot = sum8(dots[u]);  // used only where v.hi > 0: else the row may hold anything
     if (live) {
       b_lo = min(b_lo, v.lo);
       b_hi = max(b_hi, v.hi);

@@ -325,7 +325,9 @@ __global__ void __launch_bounds__(NT) attn_kernel(const __grid_constant__ AttnAr
 }
 
 // ---------------------------------------------------------------------------
-// dQ: 64 group rows resident, key tiles of the hull stream past.
+// dQ: 64 group rows resident, key tiles of the hull stream past.  Starts when
+// every block of dK and dV runs and reads nothing that they or the row state's
+// launch write (D is formed here); the last block outlasts them.
 // ---------------------------------------------------------------------------
 template <typename T, int DP>
 __global__ void __launch_bounds__(NT)
@@ -337,6 +339,7 @@ __global__ void __launch_bounds__(NT)
   float* Vs = Ks + BT * kLd<DP>;
   float* Ps = Vs + BT * kLd<DP>;
   __shared__ Rows rs;
+  __shared__ float2 lds[BT];
   const int rank = blockIdx.x % S;
   const int rows = a.H / a.Hkv * a.Nq, row0 = blockIdx.x / S * BT;
   const int g = blockIdx.z * a.Hkv + blockIdx.y;
@@ -344,7 +347,6 @@ __global__ void __launch_bounds__(NT)
   const T* dO = static_cast<const T*>(a.dO) + static_cast<size_t>(g) * rows * a.d;
   const T* K = static_cast<const T*>(a.K) + static_cast<size_t>(g) * a.Nk * a.d;
   const T* V = static_cast<const T*>(a.V) + static_cast<size_t>(g) * a.Nk * a.d;
-  const GradRows gr = grad_rows(a.workspace, a.B * a.Hkv, rows);
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const float inv_cap = a.cap > 0.f ? 1.f / a.cap : 0.f;
 
@@ -355,14 +357,23 @@ __global__ void __launch_bounds__(NT)
   load_tile<T, DP>(dOs, dO, row0, 0, rows, a.d);
   float2 ld[4];
   float acc[4][DP / 16];
-  wait_ahead();
-  __threadfence();  // the row state reaches the launch behind, too
-  release_next();
+  // L log2 e and D, eight lanes a row; a row that sees nothing may hold anything.
+  const T* O = static_cast<const T*>(a.O) + static_cast<size_t>(g) * rows * a.d;
+#pragma unroll
+  for (int u = 0; u < BT / (NT / 8); ++u) {
+    const int r = u * (NT / 8) + (threadIdx.x >> 3);
+    const size_t at = static_cast<size_t>(row0 + r) * a.d;
+    const float dot = sum8(row0 + r < rows ? dot_part<T, 0>(O + at, dO + at, a.d, threadIdx.x & 7)
+                                           : 0.f);
+    if ((threadIdx.x & 7) == 0)
+      lds[r] = rs.hi[r] > 0
+                   ? make_float2(a.L[static_cast<size_t>(g) * rows + row0 + r] * kLog2e, dot)
+                   : make_float2(INFINITY, 0.f);
+  }
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    // The workspace is padded, so rows beyond the last have an entry too.
-    const size_t at = static_cast<size_t>(g) * gr.pitch + row0 + ty + 16 * i;
-    ld[i] = make_float2(gr.l2[at], gr.dd[at]);
+    ld[i] = lds[ty + 16 * i];
 #pragma unroll
     for (int c = 0; c < DP / 16; ++c) acc[i][c] = 0.f;
   }
@@ -401,13 +412,15 @@ __global__ void __launch_bounds__(NT)
   write_rows<T, DP>(Qs, static_cast<T*>(a.dQ) + (static_cast<size_t>(g) * rows + row0) * a.d,
                     rows - row0, a.d, rank, S);
   if (S > 1) tc::cluster_sync();  // the staged rows stay until all are read
+  if (blockIdx.x + 1 == gridDim.x && blockIdx.y + 1 == gridDim.y && blockIdx.z + 1 == gridDim.z)
+    wait_ahead();
 }
 
 // ---------------------------------------------------------------------------
 // dK, dV: 64 keys resident, the group rows that see any of them stream past
 // in tiles of 64 (their bounds say which), so a shared head's gradient sums
-// its query heads on chip.  Starts when every block of dQ runs, which itself
-// waited for the row state; the last block outlasts dQ.
+// its query heads on chip.  Starts beside the row state's launch and waits for it
+// before it reads any of it.
 // ---------------------------------------------------------------------------
 template <typename T, int DP>
 __global__ void __launch_bounds__(NT)
@@ -435,6 +448,8 @@ __global__ void __launch_bounds__(NT)
 
   load_tile<T, DP>(Ks, K, key0, 0, a.Nk, a.d);
   load_tile<T, DP>(Vs, V, key0, 0, a.Nk, a.d);
+  release_next();
+  wait_ahead();  // the row state is written and visible
   float ak[4][DP / 16], av[4][DP / 16];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -494,8 +509,6 @@ __global__ void __launch_bounds__(NT)
   write_rows<T, DP>(Qs, static_cast<T*>(a.dK) + at, a.Nk - key0, a.d, rank, S);
   write_rows<T, DP>(dOs, static_cast<T*>(a.dV) + at, a.Nk - key0, a.d, rank, S);
   if (S > 1) tc::cluster_sync();
-  if (blockIdx.x + 1 == gridDim.x && blockIdx.y + 1 == gridDim.y && blockIdx.z + 1 == gridDim.z)
-    wait_ahead();
 }
 
 // Blocks of a cluster that share one block's streamed tiles: 4 at most (the
@@ -528,11 +541,11 @@ cudaError_t run(const AttnArgs& a, bool grad) {
     return e == cudaSuccess && splits > 1 ? attn_join(a, splits) : e;
   }
   const int key_blocks = (a.Nk + BT - 1) / BT;
-  cudaError_t e = launch(attn_dq_kernel<T, DP>, 4 * tile + square, blocks,
-                         cluster_size(a, blocks, key_blocks), a);
+  cudaError_t e = launch(attn_dkv_kernel<T, DP>, 4 * tile + 2 * square, key_blocks,
+                         cluster_size(a, key_blocks, blocks), a);
   if (e == cudaSuccess)
-    e = launch(attn_dkv_kernel<T, DP>, 4 * tile + 2 * square, key_blocks,
-               cluster_size(a, key_blocks, blocks), a);
+    e = launch(attn_dq_kernel<T, DP>, 4 * tile + square, blocks,
+               cluster_size(a, blocks, key_blocks), a);
   return e;
 }
 

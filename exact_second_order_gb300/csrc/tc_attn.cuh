@@ -34,6 +34,11 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+// Orders this thread's view of global memory before its bulk copies from it.
+__device__ __forceinline__ void fence_proxy_async_global() {
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+
 // Bounded waits that suspend the thread until the phase completes, or for
 // kHintNs at a time.  The loops of the shared header read the global timer on
 // entry and poll often; here a wake-up is what an MMA round trip waits for, and

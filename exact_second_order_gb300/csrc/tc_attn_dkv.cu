@@ -11,9 +11,8 @@
 // of every tile each, one key per thread.  How many tiles there
 // are is known only to warp 0: each ring slot says which tile it holds, and a
 // last slot says that there are no more.
-// The launch starts when every block of dQ runs (dQ waited for the row state),
-// so the blocks fill the SMs that dQ's last wave leaves; its last block outlasts
-// dQ, so whatever follows on the stream finds both done.
+// The launch starts beside the row state's, loads K and V, and waits for the row
+// state before warp 0 reads any of it.
 // When the key blocks are few, a cluster of S blocks shares one: rank q takes
 // every S-th of its tiles, and the partial sums meet in distributed shared
 // memory, in the order of the ranks, before the one write.
@@ -265,12 +264,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(&sm.out_full, 1);
     sm.abort_flag = 0;
     fence_barrier_init();
-    // K and V are under way while the bounds are read.
+    // K and V are under way while the row state is waited for.
     mbar_expect_tx(&sm.bar_kv, 2 * NH * HALF);
     for (int h = 0; h < NH; ++h) {
       tma_load_3d(sm.k[h], &mK, &sm.bar_kv, 64 * h, j0, g);
       tma_load_3d(sm.v[h], &mV, &sm.bar_kv, 64 * h, j0, g);
     }
+    release_next();
   }
   if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
   if (Smem::kFold && threadIdx.x >= 64 && threadIdx.x < 64 + 2 * BM) {
@@ -297,6 +297,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       tma_prefetch_desc(&mQ);
       tma_prefetch_desc(&mdO);
     }
+    wait_ahead();                // the row state is written and visible,
+    fence_proxy_async_global();  // to the bulk copies as well
     int nq = 0, no = 0;  // Q and dO loads issued
     int hit = 0;         // tiles found
     bool ok = true;
@@ -652,7 +654,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
-  if (blockIdx.x + 1 == gridDim.x) wait_ahead();
 }
 
 // How many blocks share a key block: the power of two with the least of an

@@ -18,6 +18,11 @@
 // d = 128.
 // K and V have rings of their own: a V tile is free after dP, a K tile only
 // after dQ.
+// The launch starts when every block of dK and dV runs, so its blocks fill the SMs
+// that their last wave leaves.  It reads nothing that the call's other launches
+// write, D is formed here from O and dO (a row's 256 to 512 bytes, beside the first
+// tiles' loads); its last block outlasts dK and dV, so whatever follows on the
+// stream finds all done.
 // TMEM (BN keys a tile): S [0, BN) and [BN, 2 BN), dP [2 BN, 3 BN), dQ from 3 BN
 // on; in the large blocks of d = 64 also Q and dO as A operands ([448,480) and
 // [480,512)): read from shared memory, they and the key tiles and the TMA writes
@@ -64,6 +69,7 @@ struct SmemQ {
   alignas(1024) uint8_t k[NK][NH][kTileHalf];
   alignas(1024) uint8_t v[NV][NH][kTileHalf];
   int hull[4][4];
+  float dd[BM];               // D
   uint64_t bar_q, a_ready;    // Q and dO in shared memory / in TMEM (8 warps)
   uint64_t k_full[NK], k_empty[NK];
   uint64_t v_full[NV], v_empty[NV];
@@ -177,9 +183,6 @@ __global__ void __launch_bounds__((Cfg<DH, SMALL>::kThreads), (SMALL ? 2 : 1))
       tma_load_3d(sm.q[h], &mQ, &sm.bar_q, 64 * h, row0, g);
       tma_load_3d(sm.go[h], &mdO, &sm.bar_q, 64 * h, row0, g);
     }
-    wait_ahead();
-    __threadfence();  // the row state reaches the launch behind, too
-    release_next();
   }
   if (warp == 1) tmem_alloc(&sm.tmem_base, C::kColumns);
   const int wg = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane, row = row0 + r;
@@ -188,16 +191,33 @@ __global__ void __launch_bounds__((Cfg<DH, SMALL>::kThreads), (SMALL ? 2 : 1))
   if (warp >= 2) {
     gr = group_row(a, g / a.Hkv, g % a.Hkv, row, rows);
     if (wg == 0) warp_hull(gr.v, row < rows, lane, sm.hull[quad]);
-    const GradRows st = grad_rows(a.workspace, heads, rows);
-    const size_t at = static_cast<size_t>(g) * st.pitch + row;  // the pitch covers the block
-    wait_ahead();
-    l2 = st.l2[at];
-    dd = st.dd[at];
+    // D of 16 NWG rows at a time, eight lanes a row.
+    constexpr int kPer = BM / (16 * NWG);
+    const size_t base = static_cast<size_t>(g) * rows + row0;
+    const auto* o = static_cast<const __nv_bfloat16*>(a.O) + base * DH;
+    const auto* go = static_cast<const __nv_bfloat16*>(a.dO) + base * DH;
+    const int first = (threadIdx.x - 64) >> 3;
+    float dots[kPer];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int q = first + 16 * NWG * u;
+      dots[u] = 0.f;
+      if (row0 + q < rows)
+        dots[u] = dot_part<__nv_bfloat16, DH>(o + static_cast<size_t>(q) * DH,
+                                              go + static_cast<size_t>(q) * DH, DH, lane & 7);
+    }
+    if (gr.v.hi > 0) l2 = a.L[base + r] * kLog2e;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const float dot = sum8(dots[u]);
+      if ((lane & 7) == 0) sm.dd[first + 16 * NWG * u] = dot;
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
+  if (warp >= 2 && gr.v.hi > 0) dd = sm.dd[r];  // else the row may hold anything
   const Hull hull = join_hulls(sm.hull, 4);
   const int tb = hull.lo < hull.hi ? hull.lo / BN : 0;
   const int T = hull.lo < hull.hi ? (hull.hi + BN - 1) / BN - tb : 0;
@@ -418,6 +438,7 @@ __global__ void __launch_bounds__((Cfg<DH, SMALL>::kThreads), (SMALL ? 2 : 1))
     tc_fence_after();
     tmem_dealloc(tbase, C::kColumns);
   }
+  if (blockIdx.x + 1 == gridDim.x) wait_ahead();
 }
 
 template <int DH, bool SMALL, bool CAP, bool BIAS>

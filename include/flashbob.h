@@ -209,8 +209,8 @@ flashbob_status flashbob_attention_jvp(const void* Q, const void* K, const void*
  *   ranges, q_pos, slopes, tau, cap and causal, and the gradient dO
  *   [B,H,Nq,d] of in_dtype: dQ [B,H,Nq,d], dK, dV [B,Hkv,Nk,d] of in_dtype
  *   (shared heads summed).  Three launches: the row state (D and what each
- *   row sees) into `gradient` bytes of workspace, dQ (row-resident), dK and
- *   dV (column-resident).
+ *   row sees) into `gradient` bytes of workspace, dK and dV
+ *   (column-resident), dQ (row-resident).
  * Calls on different streams, or in different graphs that may run at the
  * same time, must not share a workspace.
  */
