@@ -150,15 +150,21 @@ __device__ __forceinline__ Hull join_hulls(const int (*h)[4], int n) {
 // Scores of raw products in log2 units:
 //   not capped: raw c1;  capped: c2 t with t = tanh(raw tau / cap), which
 //   tanh_of puts in place of the raw products;  biased: minus slope2 |j - pos|.
-// tanh of 16 n products: where all of the warp's arguments are at most 0.5 (the
-// cap is there for outliers) an odd polynomial in the raw products, tau / cap in
-// its coefficients (error 2.3e-7 absolute with the roundings), in 2.5 packed fp32
-// instructions an element; else 1 - 2 / (1 + e^{2 x}), two MUFU operations (a few
-// 2^-24).  With the exponential of the softmax those would be three an element,
-// and the MUFU pipe bounds the kernel: the forward of B1 H8 N16384 d64 took 1370 us
-// with them, against 570 without a cap; 1100 with a polynomial to 0.7 (3.5
-// instructions, one more coefficient); now 929 and 519.  (tanh.approx leaves 2^-11, which exp
-// turns into percents of P.)
+// tanh x is an odd polynomial for |x| <= 0.5, whose first term is x itself (2^-21
+// relative with the roundings), beyond it 1 - 2 / (1 + e^{2 x}), two MUFU operations
+// (2^-23 absolute).  The cap multiplies that error: up to a cap of kMufuCap a group
+// of products with one beyond 0.5 takes the second form as a whole (at most 2^-17 of a
+// score, less than the rounding of its dot product); above, each product takes the
+// form of its own x, or a cap of 1e6 would cost 5% of O and one of 1e9 all of it.
+// Where all of a warp's arguments are small (mostly: the cap is there for outliers)
+// the polynomial runs alone, tau / cap in its coefficients, in 2.5 packed fp32
+// instructions an element.  With the exponential of the softmax the second form would
+// be three MUFU operations an element, and that pipe bounds the kernel: the forward of
+// B1 H8 N16384 d64 took 1370 us with them, against 570 without a cap; 1100 with a
+// polynomial to 0.7 (3.5 instructions, one more coefficient); now 929 and 519.
+// (tanh.approx leaves 2^-11, which exp turns into percents of P.)
+constexpr float kMufuCap = 64.f;
+
 template <bool CAP, bool BIAS>
 struct Score {
   float c1;      // tau log2 e; capped: tau / cap
@@ -175,11 +181,35 @@ struct Score {
     a1 = kTanh[0] * (q * c1);
     a2 = kTanh[1] * (q * q * c1);
     a3 = kTanh[2] * (q * q * (q * c1));
-    // Beyond these c1^7 or raw^2 would leave fp32's range.
+    // Beyond these c1^7 or raw^2 would leave fp32's range: the products are
+    // scaled first.
     most_raw = c1 >= 0x1p-16f && c1 <= 0x1p16f ? kTanhTo / c1 : -1.f;
   }
-  __device__ __forceinline__ float tanh_exact(float raw) const {
-    return fmaf(-2.f, rcp_approx(1.f + tc::ex2_approx(raw * (2.f * kLog2e * c1))), 1.f);
+  static __device__ __forceinline__ float tanh_large(float x2) {  // of x2 / (2 log2 e)
+    return fmaf(-2.f, rcp_approx(1.f + tc::ex2_approx(x2)), 1.f);
+  }
+  // v (k + a v^2 + b v^4 + c v^6)
+  static __device__ __forceinline__ float2 odd(float2 v, float k, float a, float b, float c) {
+    auto two = [](float x) { return make_float2(x, x); };
+    const float2 w = tc::fmul2(v, v);
+    float2 p = tc::ffma2(w, two(c), two(b));
+    p = tc::ffma2(p, w, two(a));
+    p = tc::ffma2(p, w, two(k));
+    return tc::fmul2(v, p);
+  }
+  // Each product by the form of its own argument; `small`: of all that are
+  // worked on together none is beyond 0.5.
+  __device__ __forceinline__ float2 tanh_each(float2 raw, bool small) const {
+    const float2 x = tc::fmul2(raw, make_float2(c1, c1));
+    float2 t = odd(x, 1.f, kTanh[0], kTanh[1], kTanh[2]);
+    if (small) return t;
+    if (!(fabsf(x.x) <= kTanhTo)) t.x = tanh_large(x.x * (2.f * kLog2e));
+    if (!(fabsf(x.y) <= kTanhTo)) t.y = tanh_large(x.y * (2.f * kLog2e));
+    return t;
+  }
+  __device__ __forceinline__ float tanh_one(float raw) const {
+    if (c2 <= kMufuCap * kLog2e) return tanh_large(raw * (2.f * kLog2e * c1));
+    return tanh_each(make_float2(raw, raw), false).x;
   }
   template <int N>
   __device__ __forceinline__ void tanh_of(uint32_t (&s)[N][16]) const {
@@ -189,23 +219,31 @@ struct Score {
     for (int q = 0; q < N; ++q)
 #pragma unroll
       for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(tc::u2f(s[q][e])));
-    if (__any_sync(0xffffffffu, !(most <= most_raw))) {
+    if (__builtin_expect(__any_sync(0xffffffffu, !(most <= most_raw)), 0)) {
+      if (c2 <= kMufuCap * kLog2e) {
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            s[q][e] = __float_as_uint(tanh_large(tc::u2f(s[q][e]) * (2.f * kLog2e * c1)));
+        return;
+      }
+      const bool small = __all_sync(0xffffffffu, most * c1 <= kTanhTo);
 #pragma unroll
       for (int q = 0; q < N; ++q)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s[q][e] = __float_as_uint(tanh_exact(tc::u2f(s[q][e])));
+        for (int e = 0; e < 16; e += 2) {
+          const float2 t = tanh_each(tc::f2(s[q][e], s[q][e + 1]), small);
+          s[q][e] = __float_as_uint(t.x);
+          s[q][e + 1] = __float_as_uint(t.y);
+        }
       return;
     }
-    auto two = [](float v) { return make_float2(v, v); };
 #pragma unroll
     for (int q = 0; q < N; ++q)
 #pragma unroll
       for (int e = 0; e < 16; e += 2) {
-        const float2 x = tc::f2(s[q][e], s[q][e + 1]), w = tc::fmul2(x, x);
-        float2 p = tc::ffma2(w, two(a3), two(a2));
-        p = tc::ffma2(p, w, two(a1));
-        p = tc::ffma2(p, w, two(c1));
-        const float2 t = tc::fmul2(x, p);
+        const float2 t = odd(tc::f2(s[q][e], s[q][e + 1]), c1, a1, a2, a3);
         s[q][e] = __float_as_uint(t.x);
         s[q][e + 1] = __float_as_uint(t.y);
       }

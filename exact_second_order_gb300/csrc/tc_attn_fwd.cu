@@ -345,7 +345,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW, TOKEN>::kThreads), (NW == 1 ?
       float mt = mr;
       if (!BIAS) {
         mt = mr * score.c1;
-        if (CAP && mr != -INFINITY) mt = score.c2 * score.tanh_exact(mr);
+        if (CAP && mr != -INFINITY) mt = score.c2 * score.tanh_one(mr);
       }
       const bool raise = mt > m + kRescale;
       const float factor = raise ? (m == -INFINITY ? 0.f : ex2_approx(m - mt)) : 1.f;
