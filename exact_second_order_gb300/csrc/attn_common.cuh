@@ -48,12 +48,13 @@ __device__ __forceinline__ int warp_max(int v) { return __reduce_max_sync(0xffff
 // rows padded to a multiple of kRowPad per (batch, key/value head):
 //   info  {lo, hi, pos, slope log2 e (as bits)},
 //   l2, dd  L log2 e and D; +inf in place of L for rows that see nothing and
-//         for the padding, so that P = exp2(s - L) is 0 there,
+//         for the padding,
 //   ex      (bf16 with d = 64 only) -L / tau and -D as sums of three bf16 parts
 //         (exact to 2^-24), the B operand of one more K step of the score
 //         products: columns 0 - 2 and 3 - 5 of 16, in core matrices of 8 rows
 //         x 16 bytes (row r of 128: (r / 8) 256 + (r % 8) 16, columns 8 - 15
-//         128 bytes further); the L columns are 0 for capped scores,
+//         128 bytes further); the L columns are 0 for capped scores, and for
+//         rows that see nothing and the padding (their tiles run masked),
 // and for each kBoundRows rows {min lo, max hi, max lo, min hi}, the hull of
 // their ranges and their intersection (the padding takes no part), and
 //   lines   {kind, pos, slope log2 e (as bits), 0}: kind 1 where the positions of
@@ -73,7 +74,6 @@ __host__ __device__ inline int padded_rows(int rows) {
 }
 
 constexpr int kExRow = 32;
-constexpr float kFar = 1e30f;  // L / tau of a row that sees nothing: its P is exactly 0
 
 __host__ __device__ inline GradRows grad_rows(void* workspace, int groups, int rows) {
   GradRows g;

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(256)
       out.l2[at] = v.hi > 0 ? l * kLog2e : INFINITY;
       out.dd[at] = v.hi > 0 ? dot : 0.f;
       if (ex) {  // inv_tau = 0 for capped scores
-        const uint2 el = tc::split3_bf16(inv_tau == 0.f ? 0.f : v.hi > 0 ? -l * inv_tau : -kFar);
+        const uint2 el = tc::split3_bf16(v.hi > 0 && inv_tau != 0.f ? -l * inv_tau : 0.f);
         const uint2 ed = tc::split3_bf16(v.hi > 0 ? -dot : 0.f);
         uint8_t* row = out.ex + (at / kRowPad) * kRowPad * kExRow + (at % kRowPad / 8) * 256 +
                        (at % 8) * 16;

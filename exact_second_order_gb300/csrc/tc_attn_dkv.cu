@@ -479,7 +479,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (!ok) break;
       const Slot slot = sm.slot[st];
       if (slot.tile < 0) break;
-      const bool masked = slot.in_lo > j0 || slot.in_hi < key_end, line = BIAS && slot.line == 1;
+      // Rows behind the last (zeros) run masked: their P is not 0, a bias may even
+      // make it infinite.
+      const bool masked = slot.in_lo > j0 || slot.in_hi < key_end || rows - slot.tile * BQ < BQ;
+      const bool line = BIAS && slot.line == 1;
       const float dist = static_cast<float>(key - slot.pos) - c0;
       score.slope2 = slot.slope2;
       ok = wait_warp(&sm.s_full, n & 1, abort_flag, err);
