@@ -461,7 +461,7 @@ flashbob_status flashbob_attention_grad(const void* Q, const void* K, const void
   if (error_word_ptr(&a.err) != cudaSuccess) return FLASHBOB_ERR_CUDA;
   cudaError_t ce = attn_grad_rows(a);
   if (ce == cudaSuccess) {
-    if (!tc_attn_supported(a)) ce = simt_attn_grad(a);
+    if (!tc_attn_grad_supported(a)) ce = simt_attn_grad(a);
     else if ((ce = tc_attn_dkv(a)) == cudaSuccess) ce = tc_attn_dq(a);
   }
   return ce == cudaSuccess ? FLASHBOB_OK : FLASHBOB_ERR_CUDA;

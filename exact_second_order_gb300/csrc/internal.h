@@ -152,6 +152,7 @@ size_t attn_grad_workspace(const AttnArgs& a);
 cudaError_t attn_join(const AttnArgs& a, int splits);  // partial results -> O, L
 cudaError_t attn_grad_rows(const AttnArgs& a);         // row state of the gradient -> workspace
 bool tc_attn_supported(const AttnArgs& a);  // bf16, d = 64 or 128
+bool tc_attn_grad_supported(const AttnArgs& a);  // and tau in reach
 int tc_attn_splits(const AttnArgs& a);
 cudaError_t tc_attn(const AttnArgs& a);
 cudaError_t tc_attn_dq(const AttnArgs& a);

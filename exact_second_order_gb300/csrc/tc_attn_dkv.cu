@@ -717,6 +717,14 @@ cudaError_t launch(const AttnArgs& a) {
 
 }  // namespace
 
+// At d = 64 without a cap L / tau is an operand: far outside tau's usual range it
+// would overflow (a bias can make L large) or lose its low parts to underflow, and
+// the gradient runs on CUDA cores, whose row state is the same.
+bool tc_attn_grad_supported(const AttnArgs& a) {
+  return tc_attn_supported(a) &&
+         (a.d != 64 || a.cap > 0.f || (a.tau >= 0x1p-60f && a.tau <= 0x1p60f));
+}
+
 cudaError_t tc_attn_dkv(const AttnArgs& a) { return a.d == 64 ? launch<64>(a) : launch<128>(a); }
 
 }  // namespace flashbob

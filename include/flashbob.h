@@ -197,7 +197,8 @@ flashbob_status flashbob_attention_jvp(const void* Q, const void* K, const void*
  *        are clamped to 0 .. Nk; lo >= hi is an empty range.
  *   q_pos: int32 [B,Nq], the position of every query; NULL: its index.  With
  *        slopes, pos_i - j must be an int32.
- *   slopes: fp32 [H], finite; NULL: no bias.  A constant: it has no gradient.
+ *   slopes: fp32 [H], |slopes[h] (pos_i - j)| below 2^60; NULL: no bias.  A
+ *        constant: it has no gradient.
  *   tau, and where cap > 0 cap and tau / cap: within 2^-120 .. 2^120.
  *   Limits: as flashbob_prep; (H / Hkv) * Nq and Nk below 2^31 - 1024.
  *

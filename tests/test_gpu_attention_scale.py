@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from tests import layer_reference as ref
-from tests.test_gpu_attention import BF, check, make, run
+from tests.test_gpu_attention import BF, F32, check, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -24,6 +24,28 @@ def scaled(shape, e, slope, far=0):
         form["q_pos"] = (torch.arange(shape["Nq"], device="cuda").expand(shape["B"], -1)
                          + far).int().contiguous()
     return x, form, 2.0 ** e / math.sqrt(shape["d"])
+
+
+def shape_rows(x):
+    """Query rows that share a key head."""
+    return x["Q"].shape[1] // x["K"].shape[1] * x["Q"].shape[2]
+
+
+@pytest.mark.parametrize("slope,far", [(0.0, 0), (-0.7, 0), (1.0, 0), (1.0, 3000)])
+@pytest.mark.parametrize("e", [-115, -61, -40, 40, 61, 115])
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F32, 64)])
+def test_ends_of_the_range_of_tau(dtype, d, e, slope, far):
+    x, form, tau = scaled(dict(B=1, H=2, Hkv=1, Nq=150, Nk=200, d=d, dtype=dtype), e, slope, far)
+    got = run(x, form, tau, 0.0, False)
+    val, bound = ref.attention(x["Q"], x["K"], x["V"], tau, dO=x["dO"], **form)
+    # The sums of dS k and dS^T q are formed before the factor tau, from keys and
+    # queries of 2^(-e / 2): a product below 2^-126, the smallest normal number of
+    # fp32, may be flushed to 0, 2^-126 absolute for each of the sum's terms, and
+    # tau multiplies it (at e = 115 weights below 2^-69 are lost that way).  The
+    # results, scaled by 2^(e / 2), may be flushed once more.
+    for k, n in (("dQ", x["K"].shape[2]), ("dK", shape_rows(x))):
+        bound[k] = bound[k] + (n * tau + 1) * 2.0 ** -126
+    check(got, val, bound)
 
 
 @pytest.mark.parametrize("slope", [-1.0, 0.0])
