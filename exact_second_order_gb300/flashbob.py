@@ -286,15 +286,25 @@ def _check_workspace(where: str, t, index: int) -> None:
         raise ValueError(f"{where}: workspace must be a contiguous CUDA tensor on cuda:{index}")
 
 
+def _torch_stream(index: int, stream):
+    """The torch stream of a stream argument: a torch stream or a handle, 0 for
+    the default stream (torch's ExternalStream would take a stream of its pool
+    for 0)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(getattr(stream, "cuda_stream", stream))
+    if handle == 0:
+        return torch.cuda.default_stream(index)
+    return torch.cuda.ExternalStream(handle, device=index)
+
+
 @contextlib.contextmanager
 def _entered(index: int, stream):
     with torch.cuda.device(index):
         if stream is None:
             yield
         else:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=index)
-            with torch.cuda.stream(stream):
+            with torch.cuda.stream(_torch_stream(index, stream)):
                 yield
 
 
