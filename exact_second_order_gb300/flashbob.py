@@ -290,6 +290,9 @@ def _torch_stream(index: int, stream):
     """The torch stream of a stream argument: a torch stream or a handle, 0 for
     the default stream (torch's ExternalStream would take a stream of its pool
     for 0)."""
+    device = getattr(stream, "device", None)
+    if device is not None and device.index != index:
+        raise ValueError(f"the stream is on {device}, the tensors are on cuda:{index}")
     if isinstance(stream, torch.cuda.Stream):
         return stream
     handle = int(getattr(stream, "cuda_stream", stream))

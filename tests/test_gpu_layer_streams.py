@@ -45,3 +45,12 @@ def test_the_stream_that_is_given_is_the_one_that_works(monkeypatch):
                 torch.cuda.synchronize()
                 assert used == [handle], (k, given)
                 assert torch.cuda.current_stream() == other
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Elsewhere:
+        cuda_stream, device = 0, torch.device("cuda", 1)
+
+    for k, call in enumerate(calls()):
+        with pytest.raises(ValueError):
+            call(Elsewhere())
