@@ -211,16 +211,18 @@ struct Score {
     if (c2 <= kMufuCap * kLog2e) return tanh_large(raw * (2.f * kLog2e * c1));
     return tanh_each(make_float2(raw, raw), false).x;
   }
+  // In `masked` tiles always each by its own: products that nobody sees must not
+  // decide which form the others take, or they would reach last bits.
   template <int N>
-  __device__ __forceinline__ void tanh_of(uint32_t (&s)[N][16]) const {
+  __device__ __forceinline__ void tanh_of(uint32_t (&s)[N][16], bool masked) const {
     if (!CAP) return;
     float most = 0.f;
 #pragma unroll
     for (int q = 0; q < N; ++q)
 #pragma unroll
       for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(tc::u2f(s[q][e])));
-    if (__builtin_expect(__any_sync(0xffffffffu, !(most <= most_raw)), 0)) {
-      if (c2 <= kMufuCap * kLog2e) {
+    if (__builtin_expect(masked || __any_sync(0xffffffffu, !(most <= most_raw)), 0)) {
+      if (!masked && c2 <= kMufuCap * kLog2e) {
 #pragma unroll
         for (int q = 0; q < N; ++q)
 #pragma unroll
@@ -228,6 +230,7 @@ struct Score {
             s[q][e] = __float_as_uint(tanh_large(tc::u2f(s[q][e]) * (2.f * kLog2e * c1)));
         return;
       }
+      // `small` decides over instructions, not over any product's result.
       const bool small = __all_sync(0xffffffffu, most * c1 <= kTanhTo);
 #pragma unroll
       for (int q = 0; q < N; ++q)

@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (!C::kOwn) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          score.tanh_of(s[c]);
+          score.tanh_of(s[c], masked);
           auto form = [&](auto m, auto l) {
             weights<decltype(m)::value, decltype(l)::value>(
                 score, s[c], l2 + 32 * c, info + 32 * c, key, dist - 32 * c, seen[c], pk);
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           warp_arrive(&sm.p_free);
         }
         if (C::kOwn) {
-          score.tanh_of(s[c]);
+          score.tanh_of(s[c], masked);
           auto form = [&](auto m, auto l) {
             both<decltype(m)::value, decltype(l)::value>(score, s[c], x, l2 + 32 * c,
                                                          info + 32 * c, key, dist - 32 * c,

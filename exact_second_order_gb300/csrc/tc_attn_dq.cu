@@ -361,7 +361,7 @@ __global__ void __launch_bounds__((Cfg<DH, SMALL>::kThreads), (SMALL ? 2 : 1))
             tc_fence_before();
             warp_arrive(&sm.p_free);
           }
-          score.tanh_of(s[c]);
+          score.tanh_of(s[c], masked);
           if (masked)
             grads<CAP, BIAS, true>(score, s[c], x, col_of(t, c), lo, hi, dist_at(t, c), l2, dd, pk);
           else
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__((Cfg<DH, SMALL>::kThreads), (SMALL ? 2 : 1))
         const bool masked = masked_at(t);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          score.tanh_of(s[c]);
+          score.tanh_of(s[c], masked);
           if (masked)
             weights<CAP, BIAS, true>(score, s[c], col_of(t, c), lo, hi, dist_at(t, c), l2);
           else

@@ -332,7 +332,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW, TOKEN>::kThreads), (NW == 1 ?
         tmem_wait_ld();
       };
       auto max_of = [&](int c) {
-        if (BIAS) score.tanh_of(s);
+        if (BIAS) score.tanh_of(s, masked);
         mr = fmaxf(mr, masked ? largest<true>(score, s, col0 + c, lo, hi, dist + c)
                               : largest<false>(score, s, col0 + c, lo, hi, dist + c));
       };
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, NW, TOKEN>::kThreads), (NW == 1 ?
 #pragma unroll
       for (int c = c_own; c < c_end; c += kGroup) {
         if (c > c_own) load(c);
-        if (!BIAS || c > c_own) score.tanh_of(s);
+        if (!BIAS || c > c_own) score.tanh_of(s, masked);
         uint32_t pk[NQ][8];
         if (masked) weights<true>(score, s, col0 + c, lo, hi, dist + c, m, l, pk);
         else weights<false>(score, s, col0 + c, lo, hi, dist + c, m, l, pk);
