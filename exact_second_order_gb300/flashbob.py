@@ -280,6 +280,13 @@ def _check_tensor(where: str, name: str, t, shape, dtype, index: int) -> None:
     raise ValueError(f"{where}: {name} must be contiguous")
 
 
+def _check_sizes(where: str, *sizes: int) -> None:
+    """The C ABI takes sizes as int, and ctypes keeps the low 32 bits of a
+    larger one without a word."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"{where}: sizes must be below 2^31, got {max(sizes)}")
+
+
 def _check_workspace(where: str, t, index: int) -> None:
     if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda
                               and t.get_device() == index and t.is_contiguous()):
@@ -338,6 +345,7 @@ def _check_attention(where: str, Q, K, V, slopes, ranges, q_pos):
     _, Hkv, Nk, _ = key = K.shape
     if key[0] != B or key[3] != d:
         raise ValueError(f"{where}: K has shape {tuple(key)}, expected {(B, Hkv, Nk, d)}")
+    _check_sizes(where, B, H, Hkv, Nq, Nk)
     _check_tensor(where, "Q", Q, Q.shape, dt, index)
     _check_tensor(where, "K", K, key, dt, index)
     _check_tensor(where, "V", V, key, dt, index)
@@ -354,6 +362,7 @@ def _check_attention(where: str, Q, K, V, slopes, ranges, q_pos):
 def flashbob_attention_workspace(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int,
                                  in_dtype: int) -> tuple[int, int]:
     """Workspace bytes of flashbob_attention and of flashbob_attention_grad."""
+    _check_sizes("flashbob_attention_workspace", B, H, Hkv, Nq, Nk, d)
     n = [ctypes.c_size_t() for _ in range(2)]
     st = load_library().flashbob_attention_workspace(B, H, Hkv, Nq, Nk, d, in_dtype,
                                                      *(ctypes.byref(x) for x in n))
@@ -465,12 +474,15 @@ def attention_grad(Q, K, V, O, L, dO, tau: float, cap: float = 0.0, slopes=None,
         return run()
 
 
-def _check_ranges(where: str, index: int, doc_offsets, prefix, q_start, B: int) -> int:
+def _check_ranges(where: str, index: int, doc_offsets, prefix, q_start, B: int, Nq: int,
+                  Nk: int) -> int:
     """Checks of the arrays that ranges are built from; returns the documents."""
+    _check_sizes(where, B, Nq, Nk)
     M = 0
     if doc_offsets is not None:
         _cuda_index(where, "doc_offsets", doc_offsets, "[B, M + 1]", 2)
         M = doc_offsets.shape[1] - 1
+        _check_sizes(where, M)
         _check_tensor(where, "doc_offsets", doc_offsets, (B, M + 1), torch.int32, index)
     if prefix is not None:
         _check_tensor(where, "prefix", prefix, (B, M), torch.int32, index)
@@ -497,7 +509,7 @@ def flashbob_attention_ranges(doc_offsets, prefix, q_start, ranges, q_pos, Nk: i
     _check_tensor(where, "ranges", ranges, (B, Nq, 2), torch.int32, index)
     if q_pos is not None:
         _check_tensor(where, "q_pos", q_pos, (B, Nq), torch.int32, index)
-    M = _check_ranges(where, index, doc_offsets, prefix, q_start, B)
+    M = _check_ranges(where, index, doc_offsets, prefix, q_start, B, Nq, Nk)
     with _elsewhere(index, stream) or contextlib.nullcontext():
         _run_ranges(lib, index, doc_offsets, prefix, q_start, ranges, q_pos, B, M, Nq, Nk, causal)
 
@@ -516,7 +528,7 @@ def attention_ranges(B: int, Nq: int, Nk: int, doc_offsets=None, prefix=None, q_
     if device.type != "cuda":
         raise ValueError(f"{where}: the arrays must be on a CUDA device, not {device}")
     index = torch.cuda.current_device() if device.index is None else device.index
-    M = _check_ranges(where, index, doc_offsets, prefix, q_start, B)
+    M = _check_ranges(where, index, doc_offsets, prefix, q_start, B, Nq, Nk)
 
     def run():
         ranges = torch.empty((B, Nq, 2), dtype=torch.int32, device=device)
@@ -537,10 +549,12 @@ def _check_norm(where: str, QKV, wq, wk, freqs, positions):
     index = _cuda_index(where, "QKV", QKV, "[B, N, H + 2 Hkv, d]", 4)
     _check_tensor(where, "QKV", QKV, QKV.shape, QKV.dtype, index)
     B, N, heads, d = QKV.shape
+    _check_sizes(where, B, N, heads, d)
     R, axes = 0, 1
     if freqs is not None:
         _cuda_index(where, "freqs", freqs, "[axes, R / 2]", 2)
         axes, R = freqs.shape
+        _check_sizes(where, axes, 2 * R)
         _check_tensor(where, "freqs", freqs, freqs.shape, torch.float32, index)
         R *= 2
     if positions is not None:
@@ -557,6 +571,7 @@ def _check_cache(where: str, QKV, H: int, K, V, kv_start, index: int, sizes):
     B, _, heads, d, _, _ = sizes
     _cuda_index(where, "K", K, "[B, Hkv, Nk, d]", 4)
     Hkv, Nk = K.shape[1], K.shape[2]
+    _check_sizes(where, Nk)
     if H + 2 * Hkv != heads:
         raise ValueError(f"{where}: QKV has {heads} heads, expected {H} + 2 * {Hkv}")
     _check_tensor(where, "K", K, (B, Hkv, Nk, d), QKV.dtype, index)
@@ -634,6 +649,7 @@ def qk_norm_rope(QKV, H: int, wq=None, wk=None, freqs=None, positions=None, eps:
 def flashbob_qk_norm_rope_workspace(B: int, N: int, H: int, Hkv: int, d: int,
                                     in_dtype: int) -> int:
     """Workspace bytes of flashbob_qk_norm_rope_grad with gains."""
+    _check_sizes("flashbob_qk_norm_rope_workspace", B, N, H, Hkv, d)
     n = ctypes.c_size_t()
     st = load_library().flashbob_qk_norm_rope_workspace(B, N, H, Hkv, d, in_dtype,
                                                         ctypes.byref(n))
