@@ -13,8 +13,9 @@
 // its heads stream past, several rows in flight (a block of 4 tokens with the
 // angles in shared memory, computed before the first load, ran at 2.1 TB/s).
 // Neighbouring tokens of a block write neighbouring rows of a head.
-// Measured (16384 tokens, 32 + 2 * 8 heads of 128, bf16): 75 us forward, 80% of
-// the copy rate, 118 us gradient, 76%.  Bound by both the bytes in flight and the
+// Measured (16384 tokens, 32 + 2 * 8 heads of 128, bf16): 76 us forward, 79% of
+// the copy rate, 118 us gradient, 72% (x of the value heads is not read), and 5 us
+// for the sum of dw.  Bound by both the bytes in flight and the
 // issue (63% and 49% of the slots before the gradient loaded ahead): with the
 // rows in rings in shared memory 91 and 136 us, with 16 elements a lane 79 and
 // 140, with packed fp32 87 and 130 (graph replays, 81 and 124 for this).

@@ -161,7 +161,9 @@ __device__ __forceinline__ Hull join_hulls(const int (*h)[4], int n) {
 // instructions an element.  With the exponential of the softmax the second form would
 // be three MUFU operations an element, and that pipe bounds the kernel: the forward of
 // B1 H8 N16384 d64 took 1370 us with them, against 570 without a cap; 1100 with a
-// polynomial to 0.7 (3.5 instructions, one more coefficient); now 929 and 519.
+// polynomial to 0.7 (3.5 instructions, one more coefficient); now 921 and 516, and
+// 1310 where every group of products has one beyond 0.5 (with a cap above kMufuCap
+// 1540).
 // (tanh.approx leaves 2^-11, which exp turns into percents of P.)
 constexpr float kMufuCap = 64.f;
 

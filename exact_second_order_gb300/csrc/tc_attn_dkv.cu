@@ -28,8 +28,10 @@
 // At d = 128 dK and dV take 256 columns: one buffer of each, P^T on S^T and
 // dS^T on dP^T; the pipe runs dV(n), S(n + 1), dK(n), dP(n + 1), so that
 // P(n + 1) is formed beside dK(n) and dP(n + 1), and dS beside dV and S.
-// Measured (B1 H8 N16384, no mask): 800 us at d = 64, 1374 TFLOP/s of its 8 N^2 d,
-// and 1420 us at d = 128, 1550 TFLOP/s; waits and arithmetic of a tile bound both.
+// P^T and dS^T are rounded to bf16, as operands beside the bf16 dO and Q (tc_attn_dq.cu
+// has the errors).
+// Measured (B1 H8 N16384, no mask): 840 us at d = 64, 1309 TFLOP/s of its 8 N^2 d,
+// and 1460 us at d = 128, 1506 TFLOP/s; waits and arithmetic of a tile bound both.
 #include <stddef.h>
 
 #include <type_traits>

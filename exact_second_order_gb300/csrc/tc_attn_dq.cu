@@ -27,10 +27,15 @@
 // on; in the large blocks of d = 64 also Q and dO as A operands ([448,480) and
 // [480,512)): read from shared memory, they and the key tiles and the TMA writes
 // need as many cycles of its 128 bytes as the MMAs take.
-// Measured (B1 H8 N16384, no mask): 640 us at d = 64, 1289 TFLOP/s of its 6 N^2 d,
-// bound by the chain of waits and arithmetic of a tile (without arithmetic 436,
-// with a quarter of the MMAs 650); 865 us at d = 128, 1910 TFLOP/s, bound by the
-// MMAs.
+// dS is rounded to bf16, K, the MMA's other operand, being bf16: the dQ of normal
+// inputs is off by 1.7e-3 in norm for it, as much again for its own rounding, and
+// 0.7e-3 for D, which is formed from the O that the call gets, rounded to bf16 (2.4
+// to 2.7e-3 in all; more where a row sees few keys and dP - D cancels).  Two bf16
+// parts of dS would add half of the MMAs.
+// Measured (B1 H8 N16384, no mask): 649 us at d = 64, 1270 TFLOP/s of its 6 N^2 d,
+// bound by the chain of waits and arithmetic of a tile (when it took 640, without
+// arithmetic 436, with a quarter of the MMAs 650); 893 us at d = 128, 1847 TFLOP/s,
+// bound by the MMAs.
 #include "tc_attn.cuh"
 
 namespace flashbob {

@@ -26,11 +26,14 @@
 // zeroed in shared memory before they meet P~ = 0, so a cache may hold
 // anything behind its last key.
 // TMEM: O~ of each warpgroup (DH columns), then three score buffers.
-// Measured (B1 H8 N16384, no mask): 521 us at d = 64, 1054 TFLOP/s, where the
+// P~ is rounded to bf16, the MMA's other operand V being bf16 (a product of two
+// halves of P~ would double its MMAs); l sums it unrounded.  O is off by 2.3e-3 in
+// norm for that and its own rounding (alone 1.7e-3).
+// Measured (B1 H8 N16384, no mask): 516 us at d = 64, 1066 TFLOP/s, where the
 // hand-offs between MMAs and elementwise warps bound it (with MT = 2, 590 us, a
-// copy without arithmetic took 515, one with a quarter of the MMAs 480); 741 us
-// at d = 128, 1480 TFLOP/s, bound by the MMAs.  Tokens over a cache: 74% of the copy rate (32 requests of
-// up to 8192 keys, 8 heads of 128).
+// copy without arithmetic took 515, one with a quarter of the MMAs 480); 737 us
+// at d = 128, 1492 TFLOP/s, bound by the MMAs.  Tokens over a cache: 82% of the copy
+// rate (32 requests of up to 8192 keys, 8 heads of 128, 122 us).
 #include "tc_attn.cuh"
 
 namespace flashbob {
