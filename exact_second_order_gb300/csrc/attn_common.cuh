@@ -103,6 +103,11 @@ __host__ __device__ inline Partials partials(void* workspace, size_t rows, int d
   return p;
 }
 
+inline size_t partial_bytes(size_t rows, int d, int splits) {
+  return reinterpret_cast<size_t>(partials(nullptr, rows, d, splits).o) +
+         rows * splits * d * sizeof(float);
+}
+
 // A call's later launches may start before the launch ahead has ended
 // (launch_after): wait_ahead returns when it has, with all that it wrote;
 // release_next lets the next launch start once every block has come here.

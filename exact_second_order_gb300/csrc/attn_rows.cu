@@ -263,10 +263,7 @@ cudaError_t attn_ranges(const int* doc_offsets, const int* prefix, const int* q_
 
 size_t attn_forward_workspace(const AttnArgs& a) {
   const int splits = attn_splits(a);
-  if (splits == 1) return 0;
-  const size_t rows = static_cast<size_t>(a.B) * a.H * a.Nq;
-  const Partials p = partials(nullptr, rows, a.d, splits);
-  return reinterpret_cast<size_t>(p.o) + rows * splits * a.d * sizeof(float);
+  return splits == 1 ? 0 : partial_bytes(static_cast<size_t>(a.B) * a.H * a.Nq, a.d, splits);
 }
 
 size_t attn_grad_workspace(const AttnArgs& a) {
@@ -279,7 +276,10 @@ size_t attn_grad_workspace(const AttnArgs& a) {
 // A grid that leaves SMs idle is cut along the keys, so that the tiles of one
 // row block run side by side and are joined afterwards.
 int attn_splits(const AttnArgs& a) {
-  if (tc_attn_supported(a)) return tc_attn_splits(a);
+  return tc_attn_supported(a) ? tc_attn_splits(a) : simt_splits(a);
+}
+
+int simt_splits(const AttnArgs& a) {
   const long long blocks = static_cast<long long>(a.B) * a.Hkv *
                            ((static_cast<long long>(a.H / a.Hkv) * a.Nq + 63) / 64);
   const long long tiles = (a.Nk + 63) / 64, s = kSMs / blocks;

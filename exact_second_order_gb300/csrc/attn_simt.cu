@@ -21,7 +21,7 @@
 // (B2 H3 N333 d80: forward 59 -> 29 us, gradient 146 -> 60 us).
 #include <math.h>
 
-#include "attn_common.cuh"
+#include "paged.cuh"
 #include "tc_common.cuh"
 
 namespace flashbob {
@@ -58,6 +58,47 @@ __device__ __forceinline__ void load_tile(float* dst, const T* __restrict__ src,
     }
   }
 }
+
+// The same of a group's keys or values: whole rows in memory, or pages of T or of
+// e4m3 codes (scaled), whose missing pages are zero.
+template <typename T>
+struct DenseKeys {
+  __device__ __forceinline__ explicit DenseKeys(const AttnArgs&) {}
+  template <int DP>
+  __device__ __forceinline__ void load(float* dst, const AttnArgs& a, bool values, int row0,
+                                       int first, int last) const {
+    const size_t g = static_cast<size_t>(blockIdx.z) * a.Hkv + blockIdx.y;
+    load_tile<T, DP>(dst, static_cast<const T*>(values ? a.V : a.K) + g * a.Nk * a.d, row0, first,
+                     last, a.d);
+  }
+};
+
+template <typename T, bool CODES>
+struct PagedKeys {
+  const PageArgs& p;
+  __device__ __forceinline__ explicit PagedKeys(const PagedAttnArgs& a) : p(a.page) {}
+  template <int DP>
+  __device__ __forceinline__ void load(float* dst, const AttnArgs& a, bool values, int row0,
+                                       int first, int last) const {
+    const void* pool = values ? a.V : a.K;
+    const float* scales = values ? p.v_scale : p.k_scale;
+    for (int x = threadIdx.x; x < BT * DP; x += NT) {
+      const int r = x / DP, k = x % DP, j = row0 + r;
+      float v = 0.f;
+      if (j >= first && j < last && k < a.d) {
+        const int page = paged::page_at(p, blockIdx.z, j);
+        if (paged::page_ok(p, page)) {
+          const size_t at = paged::page_row(p, page, a.Hkv, blockIdx.y, j) * a.d + k;
+          if (CODES)
+            v = paged::from_codes(static_cast<const uint8_t*>(pool)[at]).x *
+                scales[static_cast<size_t>(page) * a.Hkv + blockIdx.y];
+          else v = to_f(static_cast<const T*>(pool)[at]);
+        }
+      }
+      dst[r * kLd<DP> + k] = v;
+    }
+  }
+};
 
 // acc[i][j] = A[ty + 16 i] . B[tx + 16 j]
 template <int DP>
@@ -218,8 +259,8 @@ __device__ __forceinline__ void write_rows(const float* stage, T* __restrict__ o
 // and sum; with splits > 1 the block takes one run of those tiles and leaves
 // its unnormalised sums in the workspace.
 // ---------------------------------------------------------------------------
-template <typename T, int DP>
-__global__ void __launch_bounds__(NT) attn_kernel(const __grid_constant__ AttnArgs a, int splits) {
+template <typename T, int DP, typename KEYS, typename ARGS>
+__global__ void __launch_bounds__(NT) attn_kernel(const __grid_constant__ ARGS a, int splits) {
   extern __shared__ float sm[];
   float* Qs = sm;
   float* Ks = Qs + BT * kLd<DP>;
@@ -230,8 +271,7 @@ __global__ void __launch_bounds__(NT) attn_kernel(const __grid_constant__ AttnAr
   const int split = blockIdx.x % splits, row0 = blockIdx.x / splits * BT;
   const int g = blockIdx.z * a.Hkv + blockIdx.y;
   const T* Q = static_cast<const T*>(a.Q) + static_cast<size_t>(g) * rows * a.d;
-  const T* K = static_cast<const T*>(a.K) + static_cast<size_t>(g) * a.Nk * a.d;
-  const T* V = static_cast<const T*>(a.V) + static_cast<size_t>(g) * a.Nk * a.d;
+  const KEYS keys(a);
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const float inv_cap = a.cap > 0.f ? 1.f / a.cap : 0.f;
 
@@ -254,8 +294,8 @@ __global__ void __launch_bounds__(NT) attn_kernel(const __grid_constant__ AttnAr
   for (int t = tb; t < te; ++t) {
     __syncthreads();
     // Rows outside the hull are zero: what they hold must not reach O.
-    load_tile<T, DP>(Ks, K, t * BT, first, last, a.d);
-    load_tile<T, DP>(Vs, V, t * BT, first, last, a.d);
+    keys.template load<DP>(Ks, a, false, t * BT, first, last);
+    keys.template load<DP>(Vs, a, true, t * BT, first, last);
     __syncthreads();
     float s[4][4];
     score_tile<DP>(Qs, Ks, ty, tx, s);
@@ -526,20 +566,35 @@ cudaError_t launch(K kernel, size_t smem, int blocks, int S, const AttnArgs& a) 
   return launch_after(true, kernel, dim3(blocks * S, a.Hkv, a.B), NT, smem, S, a.stream, a, S);
 }
 
-template <typename T, int DP>
-cudaError_t run(const AttnArgs& a, bool grad) {
-  constexpr size_t tile = BT * kLd<DP> * sizeof(float), square = BT * LP * sizeof(float);
+template <int DP>
+constexpr size_t kTileBytes = BT * kLd<DP> * sizeof(float);
+constexpr size_t kSquareBytes = BT * LP * sizeof(float);
+
+template <typename T, int DP, typename KEYS, typename ARGS>
+cudaError_t forward(const ARGS& a) {
   const int blocks = static_cast<int>((static_cast<long long>(a.H / a.Hkv) * a.Nq + BT - 1) / BT);
-  if (!grad) {
-    const int splits = attn_splits(a);
-    const size_t smem = 3 * tile + square;
-    cudaError_t e = tc_set_smem(reinterpret_cast<const void*>(attn_kernel<T, DP>),
-                                static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    attn_kernel<T, DP><<<dim3(blocks * splits, a.Hkv, a.B), NT, smem, a.stream>>>(a, splits);
-    e = cudaGetLastError();
-    return e == cudaSuccess && splits > 1 ? attn_join(a, splits) : e;
-  }
+  const int splits = simt_splits(a);
+  const size_t smem = 3 * kTileBytes<DP> + kSquareBytes;
+  const auto kernel = attn_kernel<T, DP, KEYS, ARGS>;
+  cudaError_t e = tc_set_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  kernel<<<dim3(blocks * splits, a.Hkv, a.B), NT, smem, a.stream>>>(a, splits);
+  e = cudaGetLastError();
+  return e == cudaSuccess && splits > 1 ? attn_join(a, splits) : e;
+}
+
+template <typename T, typename KEYS, typename ARGS>
+cudaError_t forward(const ARGS& a) {
+  return a.d <= 32   ? forward<T, 32, KEYS>(a)
+         : a.d <= 64 ? forward<T, 64, KEYS>(a)
+         : a.d <= 96 ? forward<T, 96, KEYS>(a)
+                     : forward<T, 128, KEYS>(a);
+}
+
+template <typename T, int DP>
+cudaError_t backward(const AttnArgs& a) {
+  constexpr size_t tile = kTileBytes<DP>, square = kSquareBytes;
+  const int blocks = static_cast<int>((static_cast<long long>(a.H / a.Hkv) * a.Nq + BT - 1) / BT);
   const int key_blocks = (a.Nk + BT - 1) / BT;
   cudaError_t e = launch(attn_dkv_kernel<T, DP>, 4 * tile + 2 * square, key_blocks,
                          cluster_size(a, key_blocks, blocks), a);
@@ -550,21 +605,30 @@ cudaError_t run(const AttnArgs& a, bool grad) {
 }
 
 template <typename T>
-cudaError_t run(const AttnArgs& a, bool grad) {
-  return a.d <= 32   ? run<T, 32>(a, grad)
-         : a.d <= 64 ? run<T, 64>(a, grad)
-         : a.d <= 96 ? run<T, 96>(a, grad)
-                     : run<T, 128>(a, grad);
+cudaError_t backward(const AttnArgs& a) {
+  return a.d <= 32   ? backward<T, 32>(a)
+         : a.d <= 64 ? backward<T, 64>(a)
+         : a.d <= 96 ? backward<T, 96>(a)
+                     : backward<T, 128>(a);
 }
 
 }  // namespace
 
 cudaError_t simt_attn(const AttnArgs& a) {
-  return a.bf16 ? run<__nv_bfloat16>(a, false) : run<float>(a, false);
+  return a.bf16 ? forward<__nv_bfloat16, DenseKeys<__nv_bfloat16>>(a)
+                : forward<float, DenseKeys<float>>(a);
+}
+
+cudaError_t simt_paged(const PagedAttnArgs& a) {
+  if (a.page.e4m3)
+    return a.bf16 ? forward<__nv_bfloat16, PagedKeys<__nv_bfloat16, true>>(a)
+                  : forward<float, PagedKeys<float, true>>(a);
+  return a.bf16 ? forward<__nv_bfloat16, PagedKeys<__nv_bfloat16, false>>(a)
+                : forward<float, PagedKeys<float, false>>(a);
 }
 
 cudaError_t simt_attn_grad(const AttnArgs& a) {
-  return a.bf16 ? run<__nv_bfloat16>(a, true) : run<float>(a, true);
+  return a.bf16 ? backward<__nv_bfloat16>(a) : backward<float>(a);
 }
 
 }  // namespace flashbob

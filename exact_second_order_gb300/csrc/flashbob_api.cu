@@ -358,15 +358,17 @@ flashbob_status check_attention(const AttnArgs& a, int causal, flashbob_dtype in
 }
 
 // Sizes of the norm-and-rotation calls.  R may be 0 (no rotation); B * N
-// counts grid blocks.
-flashbob_status check_norm(const NormArgs& a, flashbob_dtype in_dtype, int interleaved) {
+// counts grid blocks.  eps = 0, no norm, where `bare` allows it.
+flashbob_status check_norm(const NormArgs& a, flashbob_dtype in_dtype, int interleaved,
+                           bool bare = false) {
   flashbob_status st = check_dtype(in_dtype);
   if (st != FLASHBOB_OK) return st;
   if (interleaved != 0 && interleaved != 1) return FLASHBOB_ERR_INVALID_ARG;
   if (a.B <= 0 || a.N <= 0 || a.H <= 0 || a.Hkv <= 0 || a.Nk <= 0 || a.d <= 0 || a.R < 0 ||
       a.R > a.d || a.R % 2 != 0 || a.axes < 1)
     return FLASHBOB_ERR_INVALID_ARG;
-  if (!(isfinite(a.eps) && a.eps > 0.f)) return FLASHBOB_ERR_INVALID_ARG;
+  if (!(isfinite(a.eps) && (a.eps > 0.f || (bare && a.eps == 0.f && !a.wq && !a.wk))))
+    return FLASHBOB_ERR_INVALID_ARG;
   if (!a.wq != !a.wk) return FLASHBOB_ERR_INVALID_ARG;
   if (a.R > 0 && !a.freqs) return FLASHBOB_ERR_INVALID_ARG;
   if (!a.positions && a.axes != 1) return FLASHBOB_ERR_INVALID_ARG;
@@ -374,6 +376,29 @@ flashbob_status check_norm(const NormArgs& a, flashbob_dtype in_dtype, int inter
       static_cast<long long>(a.B) * a.N > INT_MAX)
     return FLASHBOB_ERR_UNSUPPORTED;
   return FLASHBOB_OK;
+}
+
+// A paged cache beside tensors of `dtype`; fills the sizes in.
+flashbob_status check_pages(PageArgs& p, int P, int T, int M, flashbob_dtype dtype,
+                            flashbob_dtype cache_dtype) {
+  const flashbob_status st = check_dtype(dtype);
+  if (st != FLASHBOB_OK) return st;
+  if (cache_dtype != dtype && cache_dtype != FLASHBOB_E4M3) return FLASHBOB_ERR_INVALID_ARG;
+  if (P <= 0 || T <= 0 || M <= 0) return FLASHBOB_ERR_INVALID_ARG;
+  p.P = P, p.T = T, p.M = M, p.e4m3 = cache_dtype == FLASHBOB_E4M3;
+  p.shift = T == 16 ? 4 : T == 32 ? 5 : T == 64 ? 6 : T == 128 ? 7 : 0;
+  if (p.shift == 0 || static_cast<long long>(M) * T > INT_MAX - 1024)
+    return FLASHBOB_ERR_UNSUPPORTED;
+  return FLASHBOB_OK;
+}
+
+// Scales come with an 8-bit cache and with no other.
+flashbob_status check_scales(const PageArgs& p) {
+  return !p.k_scale == p.e4m3 || !p.v_scale == p.e4m3 ? FLASHBOB_ERR_INVALID_ARG : FLASHBOB_OK;
+}
+
+size_t pool_bytes(const PageArgs& p, int Hkv, int d, int element) {
+  return static_cast<size_t>(p.P) * Hkv * p.T * d * (p.e4m3 ? 1 : element);
 }
 
 }  // namespace
@@ -567,6 +592,135 @@ flashbob_status flashbob_qk_norm_rope_grad(const void* QKV, const float* wq, con
   if (st != FLASHBOB_OK) return st;
   if (workspace_bytes < need) return FLASHBOB_ERR_INVALID_ARG;
   return qk_norm_grad(a) == cudaSuccess ? FLASHBOB_OK : FLASHBOB_ERR_CUDA;
+}
+
+flashbob_status flashbob_cache_append(const void* QKV, const float* wq, const float* wk,
+                                      const float* freqs, const int* positions,
+                                      const int* kv_start, const int* counts, const int* table,
+                                      float eps, void* Q, void* K, void* V, float* k_scale,
+                                      float* v_scale, int B, int N, int H, int Hkv, int P, int T,
+                                      int M, int d, int R, int axes, int interleaved,
+                                      flashbob_dtype in_dtype, flashbob_dtype cache_dtype,
+                                      void* stream) {
+  AppendArgs a{};
+  a.QKV = QKV, a.wq = wq, a.wk = wk, a.freqs = freqs, a.positions = positions, a.eps = eps;
+  a.Q = Q, a.K = K, a.V = V, a.kv_start = kv_start, a.counts = counts;
+  a.page.table = table, a.page.k_scale = k_scale, a.page.v_scale = v_scale;
+  flashbob_status st = check_pages(a.page, P, T, M, in_dtype, cache_dtype);
+  if (st != FLASHBOB_OK) return st;
+  a.B = B, a.N = N, a.H = H, a.Hkv = Hkv, a.Nk = M * T, a.d = d, a.R = R, a.axes = axes;
+  a.interleaved = interleaved == 1, a.bf16 = in_dtype == FLASHBOB_BF16;
+  a.stream = (cudaStream_t)stream;
+  st = check_norm(a, in_dtype, interleaved, true);
+  if (st == FLASHBOB_OK) st = check_scales(a.page);
+  if (st != FLASHBOB_OK) return st;
+  // Tokens and their pages are counted in 32 bits, a page beyond the last included.
+  if (N > INT_MAX - 1024) return FLASHBOB_ERR_UNSUPPORTED;
+  const size_t e = a.bf16 ? 2 : 4, tokens = (size_t)B * N, pool = pool_bytes(a.page, Hkv, d, (int)e);
+  const size_t scales = (size_t)P * Hkv * 4;
+  const Buf bufs[] = {{QKV, tokens * (H + 2 * (size_t)Hkv) * d * e, false},
+                      {wq, (size_t)d * 4, false, true},
+                      {wk, (size_t)d * 4, false, true},
+                      {freqs, (size_t)axes * (R / 2) * 4, false, true},
+                      {positions, axes * tokens * 4, false, true},
+                      {kv_start, (size_t)B * 4, false, true},
+                      {counts, (size_t)B * 4, false, true},
+                      {table, (size_t)B * M * 4, false},
+                      {Q, tokens * H * d * e, true},
+                      {K, pool, true},
+                      {V, pool, true},
+                      {k_scale, scales, true, true},
+                      {v_scale, scales, true, true}};
+  st = check_buffers(bufs, 13);
+  if (st != FLASHBOB_OK) return st;
+  return cache_append(a) == cudaSuccess ? FLASHBOB_OK : FLASHBOB_ERR_CUDA;
+}
+
+flashbob_status flashbob_cache_read(const void* K, const void* V, const float* k_scale,
+                                    const float* v_scale, const int* table, const int* lens,
+                                    void* Kd, void* Vd, int B, int Hkv, int P, int T, int M,
+                                    int Nk, int d, flashbob_dtype cache_dtype,
+                                    flashbob_dtype out_dtype, void* stream) {
+  ReadArgs a{};
+  a.K = K, a.V = V, a.lens = lens, a.Kd = Kd, a.Vd = Vd;
+  a.page.table = table;
+  a.page.k_scale = const_cast<float*>(k_scale), a.page.v_scale = const_cast<float*>(v_scale);
+  flashbob_status st = check_pages(a.page, P, T, M, out_dtype, cache_dtype);
+  if (st != FLASHBOB_OK) return st;
+  a.B = B, a.Hkv = Hkv, a.Nk = Nk, a.d = d, a.bf16 = out_dtype == FLASHBOB_BF16;
+  a.stream = (cudaStream_t)stream;
+  if (B <= 0 || Hkv <= 0 || Nk <= 0 || d <= 0 || Nk > M * T) return FLASHBOB_ERR_INVALID_ARG;
+  if (d > 128 || B > kMaxGridY || Hkv > kMaxGridY) return FLASHBOB_ERR_UNSUPPORTED;
+  st = check_scales(a.page);
+  if (st != FLASHBOB_OK) return st;
+  const size_t e = a.bf16 ? 2 : 4, pool = pool_bytes(a.page, Hkv, d, (int)e);
+  const size_t scales = (size_t)P * Hkv * 4, out = (size_t)B * Hkv * Nk * d * e;
+  const Buf bufs[] = {{K, pool, false},
+                      {V, pool, false},
+                      {k_scale, scales, false, true},
+                      {v_scale, scales, false, true},
+                      {table, (size_t)B * M * 4, false},
+                      {lens, (size_t)B * 4, false, true},
+                      {Kd, out, true},
+                      {Vd, out, true}};
+  st = check_buffers(bufs, 8);
+  if (st != FLASHBOB_OK) return st;
+  return cache_read(a) == cudaSuccess ? FLASHBOB_OK : FLASHBOB_ERR_CUDA;
+}
+
+flashbob_status flashbob_attention_paged_workspace(int B, int H, int Hkv, int Nq, int T, int M,
+                                                   int d, flashbob_dtype in_dtype,
+                                                   flashbob_dtype cache_dtype, size_t* forward) {
+  PagedAttnArgs a{};
+  flashbob_status st = check_pages(a.page, 1, T, M, in_dtype, cache_dtype);
+  if (st != FLASHBOB_OK) return st;
+  a.B = B, a.H = H, a.Hkv = Hkv, a.Nq = Nq, a.Nk = M * T, a.d = d, a.tau = 1.f;
+  a.bf16 = in_dtype == FLASHBOB_BF16;
+  st = check_attention(a, 0, in_dtype);
+  if (st != FLASHBOB_OK) return st;
+  if (forward) *forward = paged_workspace(a);
+  return FLASHBOB_OK;
+}
+
+flashbob_status flashbob_attention_paged(const void* Q, const void* K, const void* V,
+                                         const float* k_scale, const float* v_scale,
+                                         const int* table, const int* ranges, const int* q_pos,
+                                         const float* slopes, float tau, float cap, void* O,
+                                         float* L, void* workspace, size_t workspace_bytes, int B,
+                                         int H, int Hkv, int Nq, int P, int T, int M, int d,
+                                         int causal, flashbob_dtype in_dtype,
+                                         flashbob_dtype cache_dtype, void* stream) {
+  PagedAttnArgs a{};
+  a.page.table = table;
+  a.page.k_scale = const_cast<float*>(k_scale), a.page.v_scale = const_cast<float*>(v_scale);
+  flashbob_status st = check_pages(a.page, P, T, M, in_dtype, cache_dtype);
+  if (st != FLASHBOB_OK) return st;
+  a.Q = Q, a.K = K, a.V = V, a.ranges = ranges, a.q_pos = q_pos, a.slopes = slopes;
+  a.tau = tau, a.cap = cap, a.O = O, a.L = L, a.workspace = workspace;
+  a.B = B, a.H = H, a.Hkv = Hkv, a.Nq = Nq, a.Nk = M * T, a.d = d;
+  a.causal = causal == 1, a.bf16 = in_dtype == FLASHBOB_BF16, a.stream = (cudaStream_t)stream;
+  st = check_attention(a, causal, in_dtype);
+  if (st == FLASHBOB_OK) st = check_scales(a.page);
+  if (st != FLASHBOB_OK) return st;
+  const size_t rows = (size_t)B * H * Nq, e = a.bf16 ? 2 : 4, need = paged_workspace(a);
+  const size_t pool = pool_bytes(a.page, Hkv, d, (int)e), scales = (size_t)P * Hkv * 4;
+  const Buf bufs[] = {{Q, rows * d * e, false},
+                      {K, pool, false},
+                      {V, pool, false},
+                      {k_scale, scales, false, true},
+                      {v_scale, scales, false, true},
+                      {table, (size_t)B * M * 4, false},
+                      {ranges, (size_t)B * Nq * 8, false, true},
+                      {q_pos, (size_t)B * Nq * 4, false, true},
+                      {slopes, (size_t)H * 4, false, true},
+                      {O, rows * d * e, true},
+                      {L, rows * 4, true},
+                      {workspace, need, true, need == 0}};
+  st = check_buffers(bufs, 12);
+  if (st != FLASHBOB_OK) return st;
+  if (workspace_bytes < need) return FLASHBOB_ERR_INVALID_ARG;
+  if (error_word_ptr(&a.err) != cudaSuccess) return FLASHBOB_ERR_CUDA;
+  return paged_attn(a) == cudaSuccess ? FLASHBOB_OK : FLASHBOB_ERR_CUDA;
 }
 
 flashbob_status flashbob_check_wait_timeout(void* stream) {

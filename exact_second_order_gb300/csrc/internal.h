@@ -94,6 +94,40 @@ struct NormArgs {
   cudaStream_t stream;
 };
 
+// A paged cache: K and V pools [P, Hkv, T, d], T = 1 << shift tokens a page, and
+// the pages of each batch entry in order, table [B, M].  In e4m3 a page and head
+// has one scale for its keys and one for its values, [P, Hkv].
+struct PageArgs {
+  const int* table;
+  float *k_scale, *v_scale;  // null unless e4m3
+  int P, T, shift, M;
+  bool e4m3;
+};
+
+// Attention over the pages: K and V are the pools and Nk = M T.
+struct PagedAttnArgs : AttnArgs {
+  PageArgs page;
+};
+
+// The projection into the pages: K and V are the pools, Nk = M T, kv_start is
+// where each batch entry's tokens go and counts how many are kept ([B] or null).
+// eps = 0: no norm.
+struct AppendArgs : NormArgs {
+  PageArgs page;
+  const int* counts;
+};
+
+// Pages to head-major K and V [B, Hkv, Nk, d].
+struct ReadArgs {
+  PageArgs page;
+  const void *K, *V;  // pools
+  const int* lens;    // [B] or null
+  void *Kd, *Vd;
+  int B, Hkv, Nk, d;
+  bool bf16;  // of Kd, Vd; and of the pools unless e4m3
+  cudaStream_t stream;
+};
+
 // Largest grid y and z extents: the kernels launch heads along y and
 // batches along z.
 constexpr int kMaxGridY = 65535;
@@ -166,6 +200,13 @@ cudaError_t attn_ranges(const int* doc_offsets, const int* prefix, const int* q_
 size_t norm_grad_workspace(const NormArgs& a);
 cudaError_t qk_norm(const NormArgs& a);
 cudaError_t qk_norm_grad(const NormArgs& a);
+// Paged cache (cache_pages.cu, paged_token.cu, tc_paged.cu).
+cudaError_t cache_append(const AppendArgs& a);
+cudaError_t cache_read(const ReadArgs& a);
+size_t paged_workspace(const PagedAttnArgs& a);
+cudaError_t paged_attn(const PagedAttnArgs& a);
+cudaError_t simt_paged(const PagedAttnArgs& a);  // any d <= 128
+int simt_splits(const AttnArgs& a);
 
 // Device error word (one per device): a kernel writes a nonzero code when a
 // bounded wait gives up.  Codes: 1 = mbarrier wait timed out.

@@ -25,6 +25,7 @@ FLASHBOB_ERR_CUDA = 4
 FLASHBOB_ERR_TIMEOUT = 5
 FLASHBOB_F32 = 0
 FLASHBOB_BF16 = 1
+FLASHBOB_E4M3 = 2
 
 # Every entry point the header declares, with its ctypes signature.
 _P = ctypes.c_void_p
@@ -46,6 +47,11 @@ _SIGNATURES = {
     "flashbob_qk_norm_rope_workspace": ([_I] * 6 + [ctypes.POINTER(ctypes.c_size_t)], _I),
     "flashbob_qk_norm_rope_grad": ([_P] * 5 + [_F] + [_P] * 7 + [ctypes.c_size_t] + [_I] * 10
                                    + [_P], _I),
+    "flashbob_cache_append": ([_P] * 8 + [_F] + [_P] * 5 + [_I] * 12 + [_P], _I),
+    "flashbob_cache_read": ([_P] * 8 + [_I] * 9 + [_P], _I),
+    "flashbob_attention_paged_workspace": ([_I] * 9 + [ctypes.POINTER(ctypes.c_size_t)], _I),
+    "flashbob_attention_paged": ([_P] * 9 + [_F, _F] + [_P] * 3 + [ctypes.c_size_t] + [_I] * 11
+                                 + [_P], _I),
     "flashbob_bob_launches": ([_I] * 7 + [ctypes.POINTER(_I)], _I),
     "flashbob_bob_tile_sizes": ([_I, _I] + [ctypes.POINTER(_I)] * 4
                                 + [ctypes.POINTER(ctypes.c_size_t)] * 2, _I),
@@ -718,6 +724,211 @@ def qk_norm_rope_grad(QKV, dQ, dK, dV, wq=None, wk=None, freqs=None, positions=N
         _run_norm_grad(lib, index, sizes, H, Hkv, QKV, wq, wk, freqs, positions, eps, dQ, dK, dV,
                        dQKV, dwq, dwk, workspace, interleaved)
         return dQKV, dwq, dwk
+
+    context = _elsewhere(index, stream)
+    if context is None:
+        return run()
+    with context:
+        return run()
+
+
+# ---------------------------------------------------------------------------
+# The paged cache.
+# ---------------------------------------------------------------------------
+
+class PagedCache:
+    """The pools of a paged cache: K and V [P, Hkv, T, d] in float32, bfloat16 or
+    float8_e4m3fn, the last with k_scale and v_scale, float32 [P, Hkv] (see the
+    header).  The tensors are the caller's; the handle has been checked once and is
+    what the calls below take.  It is not meant to be changed."""
+
+    __slots__ = ("K", "V", "k_scale", "v_scale", "index", "P", "Hkv", "T", "d", "dtype", "code")
+
+    def __init__(self, K, V, k_scale=None, v_scale=None):
+        _bound or _ready()
+        where = "PagedCache"
+        index = _cuda_index(where, "K", K, "[P, Hkv, T, d]", 4)
+        P, Hkv, T, d = K.shape
+        _check_sizes(where, P, Hkv, T, d)
+        if T not in (16, 32, 64, 128):
+            raise ValueError(f"{where}: pages have 16, 32, 64 or 128 tokens, not {T}")
+        codes = K.dtype == torch.float8_e4m3fn
+        if not codes and K.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"{where}: unsupported cache dtype {K.dtype}")
+        _check_tensor(where, "K", K, K.shape, K.dtype, index)
+        _check_tensor(where, "V", V, K.shape, K.dtype, index)
+        for name, scale in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if codes:
+                _check_tensor(where, name, scale, (P, Hkv), torch.float32, index)
+            elif scale is not None:
+                raise ValueError(f"{where}: {name} belongs to a float8_e4m3fn cache alone")
+        self.K, self.V, self.k_scale, self.v_scale = K, V, k_scale, v_scale
+        self.index, self.P, self.Hkv, self.T, self.d, self.dtype = index, P, Hkv, T, d, K.dtype
+        self.code = FLASHBOB_E4M3 if codes else _dtype_code(K)
+
+    @classmethod
+    def empty(cls, P: int, Hkv: int, T: int, d: int, dtype=None, device=None):
+        """A cache of P pages of zeros (scales 1), in float8_e4m3fn unless ``dtype``
+        says otherwise."""
+        _bound or _ready()
+        dtype = torch.float8_e4m3fn if dtype is None else dtype
+        device = torch.device("cuda" if device is None else device)
+        K, V = (torch.zeros((P, Hkv, T, d), dtype=dtype, device=device) for _ in range(2))
+        if dtype != torch.float8_e4m3fn:
+            return cls(K, V)
+        return cls(K, V, *(torch.ones((P, Hkv), dtype=torch.float32, device=device)
+                           for _ in range(2)))
+
+    def pointers(self):
+        """Of K, V, k_scale and v_scale (None without scales)."""
+        return self.K.data_ptr(), self.V.data_ptr(), _ptr(self.k_scale), _ptr(self.v_scale)
+
+
+def _check_paged(where: str, name: str, t, cache, table, B: int) -> int:
+    """The cache and the table beside tensor ``t`` that shares the cache's type
+    unless that has 8 bits; returns the table's columns."""
+    if not isinstance(cache, PagedCache):
+        raise TypeError(f"{where}: cache must be a PagedCache")
+    index = cache.index
+    if t is not None:
+        if t.get_device() != index:
+            raise ValueError(f"{where}: {name} must be on the cache's device, cuda:{index}")
+        if cache.code != FLASHBOB_E4M3 and t.dtype is not cache.dtype:
+            raise TypeError(f"{where}: {name} is {t.dtype}, the cache {cache.dtype}")
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError(f"{where}: table must be a 2-d CUDA tensor [B, M]")
+    M = table.shape[1]
+    _check_tensor(where, "table", table, (B, M), torch.int32, index)
+    if M * cache.T > 0x7FFFFFFF:
+        raise ValueError(f"{where}: sizes must be below 2^31, got {M * cache.T}")
+    return M
+
+
+def cache_append(QKV, H: int, cache, table, kv_start=None, counts=None, wq=None, wk=None,
+                 freqs=None, positions=None, eps=None, interleaved: bool = False, stream=None):
+    """Q (head-major) of the packed projection QKV with H query heads; its keys and
+    values go into the pages of ``cache`` that ``table`` [B, M] names, token n of b to
+    place kv_start[b] + n if n < counts[b].  Queries and keys are normed where ``eps``
+    is given and turned by position where ``freqs`` is (see flashbob_cache_append)."""
+    lib, where = _bound or _ready(), "cache_append"
+    index, (B, N, heads, d, R, axes) = _check_norm(where, QKV, wq, wk, freqs, positions)
+    M = _check_paged(where, "QKV", QKV, cache, table, B)
+    if not 0 < H or H + 2 * cache.Hkv != heads or d != cache.d:
+        raise ValueError(f"{where}: QKV has {heads} heads of {d}, expected {H} + 2 * {cache.Hkv} "
+                         f"of {cache.d}")
+    if eps is None and (wq is not None or wk is not None):
+        raise ValueError(f"{where}: gains need eps")
+    if eps is not None and not eps > 0:
+        raise ValueError(f"{where}: eps must be > 0, or None for no norm")
+    if kv_start is not None:
+        _check_tensor(where, "kv_start", kv_start, (B,), torch.int32, index)
+    if counts is not None:
+        _check_tensor(where, "counts", counts, (B,), torch.int32, index)
+
+    def run():
+        Q = torch.empty((B, H, N, d), dtype=QKV.dtype, device=QKV.device)
+        st = lib.flashbob_cache_append(
+            QKV.data_ptr(), _ptr(wq), _ptr(wk), _ptr(freqs), _ptr(positions), _ptr(kv_start),
+            _ptr(counts), table.data_ptr(), 0.0 if eps is None else float(eps), Q.data_ptr(),
+            *cache.pointers(), B, N, H, cache.Hkv, cache.P, cache.T, M, d, R, axes,
+            int(interleaved), _dtype_code(QKV), cache.code, _raw_stream(index))
+        if st != FLASHBOB_OK:
+            raise FlashbobError(st, where)
+        return Q
+
+    context = _elsewhere(index, stream)
+    if context is None:
+        return run()
+    with context:
+        return run()
+
+
+def cache_read(cache, table, Nk: int, lens=None, dtype=None, stream=None):
+    """K and V, head-major [B, Hkv, Nk, d], of the first Nk tokens of every row of
+    ``table``, 0 from token lens[b] on; bfloat16 (``dtype``: or float32) from an 8-bit
+    cache, else in the cache's type (see flashbob_cache_read)."""
+    lib, where = _bound or _ready(), "cache_read"
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError(f"{where}: table must be a 2-d CUDA tensor [B, M]")
+    B = table.shape[0]
+    M = _check_paged(where, "table", None, cache, table, B)
+    _check_sizes(where, B, Nk)
+    if dtype is None:
+        dtype = torch.bfloat16 if cache.code == FLASHBOB_E4M3 else cache.dtype
+    code = FLASHBOB_BF16 if dtype is torch.bfloat16 else FLASHBOB_F32
+    if dtype is not torch.bfloat16 and dtype is not torch.float32 or \
+            cache.code != FLASHBOB_E4M3 and dtype is not cache.dtype:
+        raise TypeError(f"{where}: a cache of {cache.dtype} is not read as {dtype}")
+    if not 0 < Nk <= M * cache.T:
+        raise ValueError(f"{where}: Nk is {Nk}, the table has {M} pages of {cache.T}")
+    if lens is not None:
+        _check_tensor(where, "lens", lens, (B,), torch.int32, cache.index)
+
+    def run():
+        K = torch.empty((B, cache.Hkv, Nk, cache.d), dtype=dtype, device=table.device)
+        V = torch.empty_like(K)
+        st = lib.flashbob_cache_read(
+            *cache.pointers(), table.data_ptr(), _ptr(lens), K.data_ptr(), V.data_ptr(), B,
+            cache.Hkv, cache.P, cache.T, M, Nk, cache.d, cache.code, code,
+            _raw_stream(cache.index))
+        if st != FLASHBOB_OK:
+            raise FlashbobError(st, where)
+        return K, V
+
+    context = _elsewhere(cache.index, stream)
+    if context is None:
+        return run()
+    with context:
+        return run()
+
+
+@functools.lru_cache(maxsize=256)
+def flashbob_attention_paged_workspace(B: int, H: int, Hkv: int, Nq: int, T: int, M: int, d: int,
+                                       in_dtype: int, cache_dtype: int) -> int:
+    """Workspace bytes of flashbob_attention_paged."""
+    _check_sizes("flashbob_attention_paged_workspace", B, H, Hkv, Nq, T, M, d)
+    n = ctypes.c_size_t()
+    st = load_library().flashbob_attention_paged_workspace(B, H, Hkv, Nq, T, M, d, in_dtype,
+                                                           cache_dtype, ctypes.byref(n))
+    if st != FLASHBOB_OK:
+        raise FlashbobError(st, "flashbob_attention_paged_workspace")
+    return n.value
+
+
+def attention_paged(Q, cache, table, tau: float, cap: float = 0.0, slopes=None, ranges=None,
+                    q_pos=None, causal: bool = False, stream=None):
+    """O (of Q's dtype) and L of ``attention`` over the keys and values in the pages
+    of ``cache`` that ``table`` [B, M] names (M T keys; ranges say what each query
+    sees of them); allocates them, and the workspace, on Q's device."""
+    lib, where = _bound or _ready(), "attention_paged"
+    index = _cuda_index(where, "Q", Q, "[B, H, Nq, d]", 4)
+    B, H, Nq, d = shape = Q.shape
+    M = _check_paged(where, "Q", Q, cache, table, B)
+    if d != cache.d:
+        raise ValueError(f"{where}: Q has heads of {d}, the cache of {cache.d}")
+    _check_sizes(where, B, H, Nq)
+    _check_tensor(where, "Q", Q, shape, Q.dtype, index)
+    if slopes is not None:
+        _check_tensor(where, "slopes", slopes, (H,), torch.float32, index)
+    if ranges is not None:
+        _check_tensor(where, "ranges", ranges, (B, Nq, 2), torch.int32, index)
+    if q_pos is not None:
+        _check_tensor(where, "q_pos", q_pos, (B, Nq), torch.int32, index)
+    code = _dtype_code(Q)
+    need = flashbob_attention_paged_workspace(B, H, cache.Hkv, Nq, cache.T, M, d, code, cache.code)
+
+    def run():
+        O = torch.empty_like(Q)
+        L = torch.empty((B, H, Nq), dtype=torch.float32, device=Q.device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=Q.device) if need else None
+        st = lib.flashbob_attention_paged(
+            Q.data_ptr(), *cache.pointers(), table.data_ptr(), _ptr(ranges), _ptr(q_pos),
+            _ptr(slopes), float(tau), float(cap), O.data_ptr(), L.data_ptr(), _ptr(workspace),
+            need, B, H, cache.Hkv, Nq, cache.P, cache.T, M, d, int(causal), code, cache.code,
+            _raw_stream(index))
+        if st != FLASHBOB_OK:
+            raise FlashbobError(st, where)
+        return O, L
 
     context = _elsewhere(index, stream)
     if context is None:

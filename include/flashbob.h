@@ -67,7 +67,11 @@ typedef enum {
   FLASHBOB_ERR_TIMEOUT = 5      /* a kernel's bounded wait gave up            */
 } flashbob_status;
 
-typedef enum { FLASHBOB_F32 = 0, FLASHBOB_BF16 = 1 } flashbob_dtype;
+typedef enum {
+  FLASHBOB_F32 = 0,
+  FLASHBOB_BF16 = 1,
+  FLASHBOB_E4M3 = 2 /* 8-bit floating point; the pages of a cache only */
+} flashbob_dtype;
 
 /*
  * flashbob_prep: forward row state for the BoB ([FAB] sections 一/二,
@@ -290,6 +294,80 @@ flashbob_status flashbob_qk_norm_rope_grad(const void* QKV, const float* wq, con
                                            int d, int R, int axes, int interleaved,
                                            flashbob_dtype in_dtype, flashbob_dtype grad_dtype,
                                            void* stream);
+
+/*
+ * A paged cache of keys and values, and the operators on it.  No counterpart on
+ * the pages of the method.  The conventions of the calls above hold.
+ *   K, V: the pools, [P,Hkv,T,d] of cache_dtype: P pages of T tokens (16, 32, 64
+ *        or 128).  cache_dtype is the type of the call's other tensors, or
+ *        FLASHBOB_E4M3.
+ *   table: int32 [B,M], the pages of each batch entry in order: token j of b is
+ *        row j % T of page table[b][j / T].  An entry outside 0 .. P - 1 is a page
+ *        of zeros, and tokens appended to it are dropped; entries behind the last
+ *        token are not read.  Batch entries may share pages that are only read.
+ *   k_scale, v_scale: fp32 [P,Hkv] with FLASHBOB_E4M3, else NULL: a page's codes
+ *        times its scale are its values.  Scales are powers of two within
+ *        2^-60 .. 2^60, as flashbob_cache_append writes them; any have to be finite
+ *        and > 0 (what the pages of a cache hold before the first append does not
+ *        matter).  Where a scale is no power of two, values may be rounded to bf16
+ *        before a product.
+ *
+ * flashbob_cache_append: the projection, as flashbob_qk_norm_rope, into the pages.
+ *   Token n of b becomes token kv_start[b] + n of the cache (kv_start int32 [B],
+ *   NULL: 0) if n < counts[b] (counts int32 [B], NULL: N) and that is within
+ *   0 .. M T - 1; others are dropped.  Q is written for all tokens.  positions NULL
+ *   (axes = 1 only): kv_start[b] + n.  eps = 0: no norm (then no gains); eps > 0 as
+ *   there.  Rows of a page that get no token are left as they are, but for this:
+ *   With FLASHBOB_E4M3 the scale s of a page and head is the least power of two
+ *   with 448 s >= the largest finite magnitude of its new tokens; where a token
+ *   goes behind row 0 and the page's scale is larger already, it stays, and where
+ *   it is smaller the rows ahead are rounded again, to the new one.  An append that
+ *   writes row 0 starts its page anew, and what lay behind the last new token of a
+ *   page is lost with it.  Rounding is to nearest, ties to even; beyond 448 s
+ *   (s at most 2^60, and infinities) becomes 448 s, NaN stays NaN.
+ *   Two batch entries must not append to one page in one call.  One launch.
+ */
+flashbob_status flashbob_cache_append(const void* QKV, const float* wq, const float* wk,
+                                      const float* freqs, const int* positions,
+                                      const int* kv_start, const int* counts, const int* table,
+                                      float eps, void* Q, void* K, void* V, float* k_scale,
+                                      float* v_scale, int B, int N, int H, int Hkv, int P, int T,
+                                      int M, int d, int R, int axes, int interleaved,
+                                      flashbob_dtype in_dtype, flashbob_dtype cache_dtype,
+                                      void* stream);
+
+/*
+ * flashbob_cache_read: tokens 0 .. Nk - 1 (Nk <= M T) of every batch entry as
+ * head-major Kd, Vd [B,Hkv,Nk,d] of out_dtype; 0 from token lens[b] on (lens
+ * int32 [B], NULL: Nk).  One launch.
+ */
+flashbob_status flashbob_cache_read(const void* K, const void* V, const float* k_scale,
+                                    const float* v_scale, const int* table, const int* lens,
+                                    void* Kd, void* Vd, int B, int Hkv, int P, int T, int M,
+                                    int Nk, int d, flashbob_dtype cache_dtype,
+                                    flashbob_dtype out_dtype, void* stream);
+
+/*
+ * flashbob_attention_paged: O [B,H,Nq,d] of in_dtype and L [B,H,Nq] of
+ * flashbob_attention over the keys and values of the pages, Nk = M T: the same
+ * ranges, q_pos, slopes, tau, cap and causal, the same limits, and the same about
+ * what nobody sees (the rest of a page, and pages behind the last token, may hold
+ * anything).  One launch, and one more where the keys are cut into runs.
+ *   workspace: `forward` bytes of flashbob_attention_paged_workspace (may be NULL
+ *        when that is 0); overwritten.
+ */
+flashbob_status flashbob_attention_paged_workspace(int B, int H, int Hkv, int Nq, int T, int M,
+                                                   int d, flashbob_dtype in_dtype,
+                                                   flashbob_dtype cache_dtype, size_t* forward);
+
+flashbob_status flashbob_attention_paged(const void* Q, const void* K, const void* V,
+                                         const float* k_scale, const float* v_scale,
+                                         const int* table, const int* ranges, const int* q_pos,
+                                         const float* slopes, float tau, float cap, void* O,
+                                         float* L, void* workspace, size_t workspace_bytes, int B,
+                                         int H, int Hkv, int Nq, int P, int T, int M, int d,
+                                         int causal, flashbob_dtype in_dtype,
+                                         flashbob_dtype cache_dtype, void* stream);
 
 /*
  * flashbob_bob_launches: how many kernel launches one flashbob_bob call with
