@@ -1,14 +1,567 @@
-// Attention over a paged cache: which kernel takes a call.
+// Attention of a few query rows over a paged cache: bf16 queries, head dim 64 or
+// 128, pages in e4m3 or bf16, up to 32 group rows (single tokens, drafted ones).
+//   S^T = K Q^T,  x = score(S) (scale, cap, bias; log2 units),
+//   y = x + log2 s_V,  p = exp2(y - R) with a running reference R >= max y - 8,
+//   l = sum p / s_V,  O^T = (sum V^T p) / l,  L = (R + log2 l) ln 2,
+// where K and V are a page's codes: the scale of the keys goes into the scores, that
+// of the values into the exponent of the weights, so that a product's operands are
+// codes (exact in fp16) and weights of at most 2^8 (16 bits each, 11 significant),
+// however far the pages' scales are apart.  Q is scaled row by row, by a power of
+// two, into fp16's reach.
+//
+// The keys' bytes bound it (2 d bytes a key and head for e4m3), not the products: a
+// warp holds all rows and streams pages alone, 16 tokens at a time, through a ring of
+// its own in shared memory (16-byte asynchronous copies, no block-wide barrier before
+// the end).  With tokens along M and rows along N = 8 a product (mma.sync m16n8k16)
+// wastes nothing on rows that are not there: tcgen05 would want 64 rows or more, and
+// its operands in shared memory in 16 bits, twice the bytes that arrive.  Along the
+// contracted side any order will do, so a lane takes whole 16-byte runs of a key's
+// code (four steps of 4 elements) and of a value's (its own head columns of tokens
+// 2 t, 2 t + 1, 2 t + 8, 2 t + 9, paired by byte permutes), and a chunk's place in its
+// row is swizzled so that both reads are without bank conflicts.  The weights go from
+// accumulator to operand by two 8 x 8 transposes.
+// The warps' parts meet in shared memory; where groups are few the keys are cut into
+// runs whose parts a second launch joins.
 #include "paged.cuh"
+#include "tc_attn.cuh"
 
 namespace flashbob {
+namespace {
+using namespace attn;
+using namespace paged;
+using tc::ex2_approx;
+using tc::smem_u32;
 
-size_t paged_workspace(const PagedAttnArgs& a) {
-  const int splits = simt_splits(a);
-  return splits == 1 ? 0
-                     : attn::partial_bytes(static_cast<size_t>(a.B) * a.H * a.Nq, a.d, splits);
+constexpr int NW = 8;
+constexpr int kUnit = 16;  // tokens; a page is one unit or several
+constexpr float kRaise = 8.f;
+constexpr int kMostRows = 32;
+
+template <int DH, bool CODES, int NT>
+struct Tok {
+  static constexpr int kRow = DH * (CODES ? 1 : 2);     // bytes of a token's row
+  static constexpr int kTile = kUnit * kRow;            // of a unit's keys, or values
+  static constexpr int kRun = CODES ? 16 : 8;           // elements in 16 bytes
+  static constexpr int kK = DH / 16;                    // steps of the score products
+  static constexpr int kMT = DH / 16;                   // row tiles of O^T
+  // Two blocks an SM where registers and shared memory allow.
+  static constexpr bool kTwo = NT == 1 && kTile <= 2048;
+  static constexpr int kRing = kTwo ? 12288 : 24576;    // bytes of a warp's ring
+  static constexpr int kStages = kRing / (2 * kTile);
+  static constexpr int kPitch = DH + 4;                 // of a row of O in shared memory
+  static constexpr bool kQInSmem = NT == 4;
+  static constexpr int kQBytes = kQInSmem ? NT * kK * 32 * 8 : 0;
+  static constexpr int kSmem = NW * kRing + kQBytes;
+  static_assert(NT * 8 * (kPitch + 2) * 4 <= kRing, "a warp's part fits in its ring");
+  static_assert(kStages >= 3 && kStages < 32, "ring");
+};
+
+// Byte offset of 16-byte chunk c of token row r in a tile.  Keys: lanes read chunks
+// t + 4 q of rows g, a phase of eight lanes the rows 2 p and 2 p + 1; values: chunk g of
+// rows 2 t (+ 1, + 8, + 9), a phase two chunks of four rows.
+template <int ROW>
+__device__ __forceinline__ uint32_t place(int r, int c) {
+  if (ROW == 64) {  // two rows a line of 128 bytes
+    const int line = r >> 1;
+    return line * 128 + (((((r & 1) << 2) | c) ^ ((line & 3) << 1)) << 4);
+  }
+  return r * ROW + ((c ^ ((r & 7) ^ ((r & 1) << 2))) << 4);
 }
 
-cudaError_t paged_attn(const PagedAttnArgs& a) { return simt_paged(a); }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+template <bool CODES>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1) {
+  if (CODES)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t w;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(w) : "r"(v));
+  return w;
+}
+
+template <bool CODES>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  if (!CODES) return tc::pack_bf16x2(lo, hi);
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// tanh of x, each value by the form for its size.
+__device__ __forceinline__ float tanh_score(float x) {
+  if (fabsf(x) <= kTanhTo)
+    return Score<true, false>::odd(make_float2(x, x), 1.f, kTanh[0], kTanh[1], kTanh[2]).x;
+  return Score<true, false>::tanh_large(x * (2.f * kLog2e));
+}
+
+// 2^-e for a row whose largest finite magnitude is in [2^e, 2^(e + 1)), 1 for a row of zeros.
+__device__ __forceinline__ float row_shrink(float most) {
+  const int e = static_cast<int>(__float_as_uint(most) >> 23);
+  return e == 0 ? 1.f : __uint_as_float(static_cast<uint32_t>(max(254 - e, 1)) << 23);
+}
+
+template <int DH, bool CODES, int NT, bool PLAIN>
+__global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
+    token_kernel(const __grid_constant__ PagedAttnArgs a, int splits) {
+  using C = Tok<DH, CODES, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const PageArgs& pg = a.page;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int group = blockIdx.x / splits, split = blockIdx.x % splits;
+  const int b = group / a.Hkv, hkv = group % a.Hkv, rows = a.H / a.Hkv * a.Nq;
+  if (splits > 1) release_next();
+
+  // What each row sees (lane r: row r), and their hull; the same in every warp.
+  const GroupRow own = group_row(a, b, hkv, lane, rows);
+  const int h_lo = warp_min(own.v.lo), h_hi = warp_max(own.v.hi);
+  const int in_lo = warp_max(lane < rows ? own.v.lo : 0);
+  const int in_hi = warp_min(lane < rows ? own.v.hi : INT_MAX);
+  const int u_lo = h_lo < h_hi ? h_lo / kUnit : 0;
+  const int u_n = h_lo < h_hi ? (h_hi + kUnit - 1) / kUnit - u_lo : 0;
+  const int ub = u_lo + static_cast<int>(static_cast<long long>(u_n) * split / splits);
+  const int ue = u_lo + static_cast<int>(static_cast<long long>(u_n) * (split + 1) / splits);
+  const int first = ub + warp, count = ue > first ? (ue - first + NW - 1) / NW : 0;
+
+  // Pages and scales of this warp's next 32 units, one a lane, and of the 32 behind.
+  struct Meta {
+    int page;
+    float ks, vs;
+  };
+  auto meta_of = [&](int n) {
+    Meta m{-1, 1.f, 1.f};
+    if (n < count) {
+      const int page = page_at(pg, b, (first + NW * n) * kUnit);
+      if (page_ok(pg, page)) {
+        m.page = page;
+        if (CODES) {
+          const size_t at = static_cast<size_t>(page) * a.Hkv + hkv;
+          m.ks = pg.k_scale[at];
+          m.vs = pg.v_scale[at];
+        }
+      }
+    }
+    return m;
+  };
+  Meta cur = meta_of(lane), nxt = meta_of(32 + lane);
+  int batch = 0;
+
+  const uint32_t ring = smem_u32(smem) + warp * C::kRing;
+  auto issue = [&](int n) {
+    if (n < count) {
+      const int page = __shfl_sync(0xffffffffu, (n >> 5) == batch ? cur.page : nxt.page, n & 31);
+      const bool there = page >= 0;
+      const int j = (first + NW * n) * kUnit;
+      const size_t at = there ? page_row(pg, page, a.Hkv, hkv, j) * C::kRow : 0;
+      const uint8_t* K = static_cast<const uint8_t*>(a.K) + at;
+      const uint8_t* V = static_cast<const uint8_t*>(a.V) + at;
+      const uint32_t dst = ring + (n % C::kStages) * (2 * C::kTile);
+#pragma unroll
+      for (int i = 0; i < C::kRow / 32; ++i) {
+        const int x = lane + 32 * i, off = there ? 16 * x : 0;
+        const uint32_t p = place<C::kRow>(x / (C::kRow / 16), x % (C::kRow / 16));
+        copy16(dst + p, K + off, there);
+        copy16(dst + C::kTile + p, V + off, there);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int n = 0; n < C::kStages - 1; ++n) issue(n);
+
+  // Q as the B operand: columns are rows 8 nt + g; lane t's elements of step (q, s) are
+  // those of the key chunks that it reads.
+  uint32_t qf[C::kQInSmem ? 1 : NT][C::kK][2];
+  uint2* q_smem = reinterpret_cast<uint2*>(smem + NW * C::kRing);
+  float c1[NT][2];  // from a product to the score: rows 8 nt + 2 t, + 1
+  float slope2[NT][2];
+  int pos[NT][2];
+  const __nv_bfloat16* Q =
+      static_cast<const __nv_bfloat16*>(a.Q) + static_cast<size_t>(group) * rows * DH;
+  const float c0 = a.cap > 0.f ? a.tau / a.cap : a.tau * kLog2e, c2 = a.cap * kLog2e;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = 8 * nt + g;
+    uint2 w[C::kK];
+    float most = 0.f;
+#pragma unroll
+    for (int k = 0; k < C::kK; ++k) {
+      const int q = k / (C::kRun / 4), s = k % (C::kRun / 4);
+      w[k] = r < rows ? *reinterpret_cast<const uint2*>(Q + static_cast<size_t>(r) * DH +
+                                                        (t + 4 * q) * C::kRun + 4 * s)
+                      : make_uint2(0u, 0u);
+      if (CODES) {
+        const uint32_t e[4] = {w[k].x << 16, w[k].x & 0xFFFF0000u, w[k].y << 16,
+                               w[k].y & 0xFFFF0000u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most = fmaxf(most, finite_abs(__uint_as_float(e[i])));
+      }
+    }
+    float shrink = 1.f;
+    if (CODES) {
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      shrink = row_shrink(most);
+#pragma unroll
+      for (int k = 0; k < C::kK; ++k) {
+        w[k].x = pack<true>(__uint_as_float(w[k].x << 16) * shrink,
+                            __uint_as_float(w[k].x & 0xFFFF0000u) * shrink);
+        w[k].y = pack<true>(__uint_as_float(w[k].y << 16) * shrink,
+                            __uint_as_float(w[k].y & 0xFFFF0000u) * shrink);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < C::kK; ++k) {
+      if (C::kQInSmem) {
+        if (warp == 0) q_smem[(nt * C::kK + k) * 32 + lane] = w[k];
+      } else {
+        qf[C::kQInSmem ? 0 : nt][k][0] = w[k].x;
+        qf[C::kQInSmem ? 0 : nt][k][1] = w[k].y;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = 8 * nt + 2 * t + j;
+      c1[nt][j] = c0 / __shfl_sync(0xffffffffu, shrink, 4 * (2 * t + j));
+      if (!PLAIN) {
+        slope2[nt][j] = __shfl_sync(0xffffffffu, own.slope2, row);
+        pos[nt][j] = __shfl_sync(0xffffffffu, own.v.pos, row);
+      }
+    }
+  }
+  if (C::kQInSmem) __syncthreads();
+
+  float R[NT][2], l[NT][2], O[NT][C::kMT][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    R[nt][0] = R[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < C::kMT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) O[nt][i][e] = 0.f;
+  }
+
+  for (int n = 0; n < count; ++n) {
+    if ((n >> 5) != batch) {
+      cur = nxt;
+      nxt = meta_of(n + 32 + lane);
+      batch = n >> 5;
+    }
+    issue(n + C::kStages - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
+    __syncwarp();
+    const uint32_t kt = ring + (n % C::kStages) * (2 * C::kTile), vt = kt + C::kTile;
+    const int j0 = (first + NW * n) * kUnit;
+
+    float S[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) S[nt][0] = S[nt][1] = S[nt][2] = S[nt][3] = 0.f;
+#pragma unroll
+    for (int q = 0; q < DH / (4 * C::kRun); ++q) {
+      const uint4 x = lds16(kt + place<C::kRow>(g, t + 4 * q));
+      const uint4 y = lds16(kt + place<C::kRow>(g + 8, t + 4 * q));
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int s = 0; s < C::kRun / 4; ++s) {
+        uint32_t f[4];
+        if (CODES) {
+          f[0] = codes_to_half2(static_cast<uint16_t>(xs[s]));
+          f[1] = codes_to_half2(static_cast<uint16_t>(ys[s]));
+          f[2] = codes_to_half2(static_cast<uint16_t>(xs[s] >> 16));
+          f[3] = codes_to_half2(static_cast<uint16_t>(ys[s] >> 16));
+        } else {
+          f[0] = xs[2 * s % 4], f[1] = ys[2 * s % 4];
+          f[2] = xs[(2 * s + 1) % 4], f[3] = ys[(2 * s + 1) % 4];
+        }
+        const int k = q * (C::kRun / 4) + s;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (C::kQInSmem) {
+            const uint2 w = q_smem[(nt * C::kK + k) * 32 + lane];
+            mma<CODES>(S[nt], f, w.x, w.y);
+          } else {
+            mma<CODES>(S[nt], f, qf[C::kQInSmem ? 0 : nt][k][0], qf[C::kQInSmem ? 0 : nt][k][1]);
+          }
+        }
+      }
+    }
+
+    // Scores: element e of S[nt] is token g + 8 (e / 2), row 8 nt + 2 t + e % 2.
+    float ks = 1.f, lv = 0.f, inv_vs = 1.f;
+    if (CODES) {
+      ks = __shfl_sync(0xffffffffu, cur.ks, n & 31);
+      const float vs = __shfl_sync(0xffffffffu, cur.vs, n & 31);
+      lv = __log2f(vs);
+      inv_vs = 1.f / vs;
+    }
+    const bool masked = j0 < in_lo || j0 + kUnit > in_hi;
+    bool raise = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = j0 + g + 8 * (e >> 1);
+        float x = S[nt][e] * (c1[nt][e & 1] * ks);
+        if (!PLAIN) {
+          if (a.cap > 0.f) x = c2 * tanh_score(x);
+          if (a.slopes)
+            x = fmaf(-slope2[nt][e & 1], fabsf(static_cast<float>(j - pos[nt][e & 1])), x);
+        }
+        if (CODES) x += lv;
+        S[nt][e] = x;
+      }
+    if (masked) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int lo = __shfl_sync(0xffffffffu, own.v.lo, 8 * nt + 2 * t + e);
+          const int hi = __shfl_sync(0xffffffffu, own.v.hi, 8 * nt + 2 * t + e);
+          if (j0 + g < lo || j0 + g >= hi) S[nt][e] = -INFINITY;
+          if (j0 + g + 8 < lo || j0 + g + 8 >= hi) S[nt][e + 2] = -INFINITY;
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        raise = raise || fmaxf(S[nt][e], S[nt][e + 2]) > R[nt][e] + kRaise;
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float m = fmaxf(S[nt][e], S[nt][e + 2]);
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          m = fmaxf(R[nt][e], m);
+          const float f = R[nt][e] == -INFINITY ? 0.f : ex2_approx(R[nt][e] - m);
+          R[nt][e] = m;
+          l[nt][e] *= f;
+#pragma unroll
+          for (int i = 0; i < C::kMT; ++i) {
+            O[nt][i][e] *= f;
+            O[nt][i][e + 2] *= f;
+          }
+        }
+    }
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float base = R[nt][e & 1] == -INFINITY ? 0.f : R[nt][e & 1];  // nothing seen yet
+        p[e] = ex2_approx(S[nt][e] - base);
+      }
+      l[nt][0] = fmaf(inv_vs, p[0] + p[2], l[nt][0]);
+      l[nt][1] = fmaf(inv_vs, p[1] + p[3], l[nt][1]);
+      pb[nt][0] = transpose8(pack<CODES>(p[0], p[1]));
+      pb[nt][1] = transpose8(pack<CODES>(p[2], p[3]));
+    }
+
+    // Values of tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9 (v[0 .. 3]), this lane's columns: what
+    // lies outside the hull may be anything and is made 0.
+    constexpr int kWords = DH / 8 * (CODES ? 1 : 2) / 4;  // 32-bit words of a lane's columns
+    uint32_t v[4][kWords];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 2 * t + (i & 1) + 8 * (i >> 1);
+      if (kWords == 2) {
+        const uint2 x = lds8(vt + place<C::kRow>(r, g >> 1) + 8 * (g & 1));
+        v[i][0] = x.x, v[i][1] = x.y;
+      } else {
+#pragma unroll
+        for (int q = 0; q < kWords / 4; ++q) {
+          const uint4 x = lds16(vt + place<C::kRow>(r, g + 8 * q));
+          v[i][4 * q] = x.x, v[i][4 * q + 1] = x.y, v[i][4 * q + 2] = x.z, v[i][4 * q + 3] = x.w;
+        }
+      }
+    }
+    if (j0 < h_lo || j0 + kUnit > h_hi) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = j0 + 2 * t + (i & 1) + 8 * (i >> 1);
+        if (j < h_lo || j >= h_hi)
+#pragma unroll
+          for (int q = 0; q < kWords; ++q) v[i][q] = 0u;
+      }
+    }
+    // Row tile i: rows g and g + 8 are the lane's columns 2 i and 2 i + 1 (column()).
+#pragma unroll
+    for (int q = 0; q < kWords; ++q) {
+      uint32_t f[CODES ? 2 : 1][4];
+      if (CODES) {
+        const uint32_t x = __byte_perm(v[0][q], v[1][q], 0x5140);
+        const uint32_t y = __byte_perm(v[0][q], v[1][q], 0x7362);
+        const uint32_t z = __byte_perm(v[2][q], v[3][q], 0x5140);
+        const uint32_t w = __byte_perm(v[2][q], v[3][q], 0x7362);
+        f[0][0] = codes_to_half2(static_cast<uint16_t>(x));
+        f[0][1] = codes_to_half2(static_cast<uint16_t>(x >> 16));
+        f[0][2] = codes_to_half2(static_cast<uint16_t>(z));
+        f[0][3] = codes_to_half2(static_cast<uint16_t>(z >> 16));
+        f[CODES ? 1 : 0][0] = codes_to_half2(static_cast<uint16_t>(y));
+        f[CODES ? 1 : 0][1] = codes_to_half2(static_cast<uint16_t>(y >> 16));
+        f[CODES ? 1 : 0][2] = codes_to_half2(static_cast<uint16_t>(w));
+        f[CODES ? 1 : 0][3] = codes_to_half2(static_cast<uint16_t>(w >> 16));
+      } else {
+        f[0][0] = __byte_perm(v[0][q], v[1][q], 0x5410);
+        f[0][1] = __byte_perm(v[0][q], v[1][q], 0x7632);
+        f[0][2] = __byte_perm(v[2][q], v[3][q], 0x5410);
+        f[0][3] = __byte_perm(v[2][q], v[3][q], 0x7632);
+      }
+#pragma unroll
+      for (int i = 0; i < (CODES ? 2 : 1); ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma<CODES>(O[nt][(CODES ? 2 : 1) * q + i], f[i], pb[nt][0], pb[nt][1]);
+    }
+    __syncwarp();  // the next copies overwrite this unit
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+
+  // The warps' parts: O row by row, then R and l of each row.
+  float* part = reinterpret_cast<float*>(smem + warp * C::kRing);
+  constexpr int kRowsPadded = 8 * NT, kRL = kRowsPadded * C::kPitch;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float s = l[nt][e];
+      s += __shfl_xor_sync(0xffffffffu, s, 4);
+      s += __shfl_xor_sync(0xffffffffu, s, 8);
+      s += __shfl_xor_sync(0xffffffffu, s, 16);
+      const int row = 8 * nt + 2 * t + e;
+      if (g == 0) {
+        part[kRL + row] = R[nt][e];
+        part[kRL + kRowsPadded + row] = s;
+      }
+#pragma unroll
+      for (int i = 0; i < C::kMT; ++i) {
+        const int column = CODES ? DH / 8 * g + 2 * i : 64 * (i / 4) + 8 * g + 2 * (i % 4);
+        *reinterpret_cast<float2*>(part + row * C::kPitch + column) =
+            make_float2(O[nt][i][e], O[nt][i][e + 2]);
+      }
+    }
+  __syncthreads();
+  const size_t all = static_cast<size_t>(a.B) * a.H * a.Nq;
+  const size_t base = static_cast<size_t>(group) * rows;
+  const Partials out = partials(a.workspace, all, DH, splits);
+  for (int x = threadIdx.x; x < rows * (DH / 4); x += 32 * NW) {
+    const int row = x / (DH / 4), c = 4 * (x % (DH / 4));
+    const float* w0 = reinterpret_cast<const float*>(smem);
+    constexpr int kStep = C::kRing / 4;
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) m = fmaxf(m, w0[w * kStep + kRL + row]);
+    float sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float* p = w0 + w * kStep;
+      const float r = p[kRL + row], f = r == -INFINITY ? 0.f : ex2_approx(r - m);
+      const float4 v = *reinterpret_cast<const float4*>(p + row * C::kPitch + c);
+      sum = fmaf(f, p[kRL + kRowsPadded + row], sum);
+      o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
+      o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+    }
+    if (splits > 1) {
+      const size_t at = split * all + base + row;
+      *reinterpret_cast<float4*>(out.o + at * DH + c) = o;
+      if (c == 0) out.ml[at] = make_float2(m, sum);
+    } else {
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + (base + row) * DH + c) =
+          make_uint2(tc::pack_bf16x2(o.x * inv, o.y * inv), tc::pack_bf16x2(o.z * inv, o.w * inv));
+      if (c == 0) a.L[base + row] = (m + __log2f(sum)) * kLn2;
+    }
+  }
+}
+
+bool token_supported(const PagedAttnArgs& a) {
+  return a.bf16 && (a.d == 64 || a.d == 128) &&
+         static_cast<long long>(a.H / a.Hkv) * a.Nq <= kMostRows;
+}
+
+int token_splits(const PagedAttnArgs& a) {
+  const long long groups = static_cast<long long>(a.B) * a.Hkv;
+  const long long want = 6LL * kSMs / groups, most = a.Nk / 512;
+  const long long s = want < most ? want : most;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
+template <int DH, bool CODES, int NT, bool PLAIN>
+cudaError_t launch(const PagedAttnArgs& a, int splits) {
+  using C = Tok<DH, CODES, NT>;
+  const auto kernel = token_kernel<DH, CODES, NT, PLAIN>;
+  cudaError_t e = tc_set_smem(reinterpret_cast<const void*>(kernel), C::kSmem);
+  if (e != cudaSuccess) return e;
+  const long long grid = static_cast<long long>(a.B) * a.Hkv * splits;
+  if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+  kernel<<<static_cast<unsigned>(grid), 32 * NW, C::kSmem, a.stream>>>(a, splits);
+  return cudaGetLastError();
+}
+
+template <int DH, bool CODES>
+cudaError_t launch(const PagedAttnArgs& a, int splits) {
+  const int rows = a.H / a.Hkv * a.Nq;
+  const bool plain = a.cap == 0.f && !a.slopes;
+  if (rows <= 8)
+    return plain ? launch<DH, CODES, 1, true>(a, splits) : launch<DH, CODES, 1, false>(a, splits);
+  if (rows <= 16)
+    return plain ? launch<DH, CODES, 2, true>(a, splits) : launch<DH, CODES, 2, false>(a, splits);
+  return plain ? launch<DH, CODES, 4, true>(a, splits) : launch<DH, CODES, 4, false>(a, splits);
+}
+
+cudaError_t token_attn(const PagedAttnArgs& a) {
+  const int splits = token_splits(a);
+  cudaError_t e;
+  if (a.d == 64) e = a.page.e4m3 ? launch<64, true>(a, splits) : launch<64, false>(a, splits);
+  else e = a.page.e4m3 ? launch<128, true>(a, splits) : launch<128, false>(a, splits);
+  return e == cudaSuccess && splits > 1 ? attn_join(a, splits) : e;
+}
+
+}  // namespace
+
+size_t paged_workspace(const PagedAttnArgs& a) {
+  const int splits = token_supported(a) ? token_splits(a) : simt_splits(a);
+  return splits == 1 ? 0 : partial_bytes(static_cast<size_t>(a.B) * a.H * a.Nq, a.d, splits);
+}
+
+cudaError_t paged_attn(const PagedAttnArgs& a) {
+  return token_supported(a) ? token_attn(a) : simt_paged(a);
+}
 
 }  // namespace flashbob
