@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libflashbob.so")
 SOURCES = ["flashbob_api.cu", "simt.cu", "tc_host.cu", "tc_pass1.cu", "tc_pass2.cu", "tc_prep.cu",
            "tc_pass1_d128.cu", "tc_pass2_d128.cu", "tc_jvp.cu", "tc_jvp_d128.cu", "selftest.cu",
            "attn_rows.cu", "attn_simt.cu", "tc_attn_fwd.cu", "tc_attn_dq.cu",
-           "tc_attn_dkv.cu", "qk_norm.cu", "cache_pages.cu", "paged_token.cu"]
+           "tc_attn_dkv.cu", "qk_norm.cu", "cache_pages.cu", "paged_token.cu",
+           "tc_paged.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", os.path.join(os.path.dirname(HERE), "include")]

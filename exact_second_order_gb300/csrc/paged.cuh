@@ -61,5 +61,12 @@ __device__ __forceinline__ float2 from_codes(uint32_t c) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// 2^-e for a row whose largest finite magnitude is in [2^e, 2^(e + 1)), 1 for a row of
+// zeros: scales it into fp16's reach.
+__device__ __forceinline__ float row_shrink(float most) {
+  const int e = static_cast<int>(__float_as_uint(most) >> 23);
+  return e == 0 ? 1.f : __uint_as_float(static_cast<uint32_t>(max(254 - e, 1)) << 23);
+}
+
 }  // namespace paged
 }  // namespace flashbob

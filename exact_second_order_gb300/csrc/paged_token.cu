@@ -124,12 +124,6 @@ __device__ __forceinline__ float tanh_score(float x) {
   return Score<true, false>::tanh_large(x * (2.f * kLog2e));
 }
 
-// 2^-e for a row whose largest finite magnitude is in [2^e, 2^(e + 1)), 1 for a row of zeros.
-__device__ __forceinline__ float row_shrink(float most) {
-  const int e = static_cast<int>(__float_as_uint(most) >> 23);
-  return e == 0 ? 1.f : __uint_as_float(static_cast<uint32_t>(max(254 - e, 1)) << 23);
-}
-
 template <int DH, bool CODES, int NT, bool PLAIN>
 __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
     token_kernel(const __grid_constant__ PagedAttnArgs a, int splits) {
@@ -553,15 +547,20 @@ cudaError_t token_attn(const PagedAttnArgs& a) {
   return e == cudaSuccess && splits > 1 ? attn_join(a, splits) : e;
 }
 
+int splits_of(const PagedAttnArgs& a) {
+  return token_supported(a) ? token_splits(a)
+         : tc_paged_supported(a) ? tc_paged_splits(a) : simt_splits(a);
+}
+
 }  // namespace
 
 size_t paged_workspace(const PagedAttnArgs& a) {
-  const int splits = token_supported(a) ? token_splits(a) : simt_splits(a);
+  const int splits = splits_of(a);
   return splits == 1 ? 0 : partial_bytes(static_cast<size_t>(a.B) * a.H * a.Nq, a.d, splits);
 }
 
 cudaError_t paged_attn(const PagedAttnArgs& a) {
-  return token_supported(a) ? token_attn(a) : simt_paged(a);
+  return token_supported(a) ? token_attn(a) : tc_paged_supported(a) ? tc_paged(a) : simt_paged(a);
 }
 
 }  // namespace flashbob

@@ -1,0 +1,703 @@
+// Attention of many query rows over a paged cache on sm_103a tensor cores: bf16
+// queries, head dim 64 or 128, pages in e4m3 or bf16.
+//   S = Q K^T,  y = score(S) + log2 s_V (scale, cap, bias; log2 units),
+//   P~ = exp2(y - m) with a running row reference m >= max y - 8,
+//   l = sum P~ / s_V,  O = (sum P~ V) / l,  L = (m + log2 l) ln 2,
+// where K and V are a page's codes: s_K goes into the score of its 16-column chunks
+// and s_V into the exponent of their weights, so the MMAs' operands are codes (exact in
+// fp16) and weights of at most 2^8, however far the pages' scales are apart.  Q is
+// scaled row by row, by a power of two, into fp16's reach; a bf16 cache runs in bf16.
+//
+// As in the dense kernel, two elementwise warpgroups work on score tiles in TMEM, P~
+// takes the scores' place as the A operand of P~ V, and one thread issues the MMAs.
+// The tiles' producer is different: e4m3 has no MMA with a 16-bit partner, so a
+// warpgroup takes 16-byte runs of codes from the pages (two tiles ahead, in
+// registers), turns them into fp16 and stores them in the operands' swizzled layout;
+// a bf16 cache goes there by asynchronous copies.  Rows outside the hull of what the
+// block sees, and pages outside the pool, become zeros on the way.
+//   MT = 2: 256 group rows a block, warpgroup w holds rows 128 w .., so that a
+//     converted tile feeds twice the products.
+//   MT = 1: 128 rows, the warpgroups take alternate key tiles and merge their (m, l,
+//     O~) at the end; few blocks are also cut along the keys and joined by a second
+//     launch.
+// Key tiles have 128 keys: a score MMA with N = 64 costs 48 cycles for 32 of products,
+// with N = 128 64 for 64.
+#include "paged.cuh"
+#include "tc_attn.cuh"
+
+namespace flashbob {
+namespace {
+using namespace tc;
+using namespace attn;
+using namespace paged;
+
+constexpr int BM = kTcRows;
+constexpr int BN = 128;
+constexpr int kChunks = BN / 16;  // 16 keys lie on one page
+constexpr int kThreads = 416;     // elementwise warps 0 - 7, producers 8 - 11, MMA 12
+constexpr uint32_t HALF_BLOCK = BM * 64 * 2;
+constexpr uint32_t HT = BN * 64 * 2;  // 64 columns of a tile
+constexpr float kRescale = 8.f;
+
+template <int DH, int MT>
+struct Cfg {
+  static constexpr int NH = DH / 64;
+  static constexpr int NBUF = DH == 64 ? 3 : 2;  // score buffers: O~ takes the rest of TMEM
+  static constexpr int kStages = DH == 64 ? 5 : MT == 2 ? 2 : 3;  // of keys; as many of values
+  static constexpr int NK = kStages, NV = DH == 128 && MT == 1 ? 2 : kStages;
+  // Scales of tile t are written when the scores of tile t - NK are done, which were
+  // issued behind the products of a unit NBUF earlier: that one's readers are through.
+  static constexpr int NS = NK + NBUF;
+  static_assert(2 * DH + NBUF * BN <= 512, "TMEM columns");
+};
+
+template <int DH, int MT>
+struct Smem {
+  using C = Cfg<DH, MT>;
+  alignas(1024) uint8_t q[MT][C::NH][HALF_BLOCK];
+  alignas(1024) uint8_t kv[C::NK + C::NV][C::NH][HT];
+  float4 scale[C::NS][kChunks];  // s_K, log2 s_V, 1 / s_V of each chunk of a tile
+  float shrink[MT * BM];
+  float part_m[2][BM], part_l[2][BM];
+  int hull[8][4];  // of each elementwise warp's rows
+  uint64_t k_full[C::NK], k_empty[C::NK], v_full[C::NV], v_empty[C::NV];
+  uint64_t sc_full[C::NBUF], op_ready[C::NBUF];
+  uint64_t pv_done[2];  // of even and odd units
+  uint64_t out_full;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+__host__ __device__ constexpr uint32_t idesc(bool codes, int N, bool b_mn_major) {
+  return idesc_bf16(BM, N, b_mn_major) & (codes ? ~((1u << 7) | (1u << 10)) : ~0u);  // fp16: 0
+}
+
+template <bool CODES>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  if (!CODES) return pack_bf16x2(lo, hi);
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Scores of 64 columns from jbase on, 16 of a page each.  CAP: `s` holds raw products
+// times tau / cap, and where `turned` their tanh.
+template <bool CODES, bool CAP, bool BIAS>
+struct PagedScore {
+  Score<CAP, BIAS> sc;
+  float c1;  // not capped: log2 units a product; capped: tau / cap
+  float c2;
+
+  __device__ __forceinline__ PagedScore(const AttnArgs& a, float slope, float grow) : sc(a, slope) {
+    c1 = sc.c1 * grow;
+    c2 = sc.c2;
+    sc.c1 = 1.f;  // its tanh is of products that are scaled already
+    sc.a1 = kTanh[0], sc.a2 = kTanh[1], sc.a3 = kTanh[2];
+    sc.most_raw = kTanhTo;
+  }
+  __device__ __forceinline__ void scale(uint32_t (&s)[4][16], const float4* chunk) const {
+    if (!CAP) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float f = CODES ? c1 * chunk[q].x : c1;
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const float2 x = fmul2(f2(s[q][e], s[q][e + 1]), make_float2(f, f));
+        s[q][e] = __float_as_uint(x.x);
+        s[q][e + 1] = __float_as_uint(x.y);
+      }
+    }
+  }
+  __device__ __forceinline__ float factor(const float4& chunk) const {
+    return CAP ? c2 : CODES ? c1 * chunk.x : c1;
+  }
+  __device__ __forceinline__ float2 at(float2 x, float f, float off, float dist) const {
+    float2 y = ffma2(x, make_float2(f, f), make_float2(off, off));
+    if (BIAS) {
+      y.x = fmaf(-sc.slope2, fabsf(dist), y.x);
+      y.y = fmaf(-sc.slope2, fabsf(dist + 1.f), y.y);
+    }
+    return y;
+  }
+  // The largest y.  Without a bias it grows with the raw product.
+  template <bool MASKED>
+  __device__ __forceinline__ float largest(const uint32_t (&s)[4][16], const float4* chunk,
+                                           int jbase, int lo, int hi, float dist) const {
+    float most = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float mr = -INFINITY;
+      const float lv = CODES ? chunk[q].y : 0.f, f = factor(chunk[q]);
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const int j = jbase + 16 * q + e;
+        float2 x = f2(s[q][e], s[q][e + 1]);
+        if (BIAS) x = at(x, f, lv, dist + (16 * q + e));
+        if (!MASKED || (j >= lo && j < hi)) mr = fmaxf(mr, x.x);
+        if (!MASKED || (j + 1 >= lo && j + 1 < hi)) mr = fmaxf(mr, x.y);
+      }
+      if (!BIAS && mr != -INFINITY) mr = fmaf(f, CAP ? sc.tanh_one(mr) : mr, lv);
+      most = fmaxf(most, mr);
+    }
+    return most;
+  }
+  // P~ to the TMEM columns from `out` on.
+  template <bool MASKED>
+  __device__ __forceinline__ void weights(const uint32_t (&s)[4][16], const float4* chunk,
+                                          int jbase, int lo, int hi, float dist, float m, float& l,
+                                          uint32_t out) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float2 acc = make_float2(0.f, 0.f);
+      uint32_t pk[8];
+      const float f = factor(chunk[q]), off = CODES ? chunk[q].y - m : -m;
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const float2 y = at(f2(s[q][e], s[q][e + 1]), f, off, dist + (16 * q + e));
+        float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+        if (MASKED) {
+          const int j = jbase + 16 * q + e;
+          if (j < lo || j >= hi) p.x = 0.f;
+          if (j + 1 < lo || j + 1 >= hi) p.y = 0.f;
+        }
+        acc = fadd2(acc, p);
+        pk[e >> 1] = pack<CODES>(p.x, p.y);
+      }
+      tmem_st8(out + 8 * q, pk);
+      l = CODES ? fmaf(chunk[q].z, acc.x + acc.y, l) : l + (acc.x + acc.y);
+    }
+  }
+};
+
+// One tile of keys or values, by the four producer warps: a thread's 16-byte runs of
+// the pages' rows.  Run i of a thread is column run x % kPerRow of row x / kPerRow, x =
+// tid + 128 i.
+template <int DH, bool CODES>
+struct Feed {
+  static constexpr int kRow = DH * (CODES ? 1 : 2);
+  static constexpr int kPerRow = kRow / 16;
+  static constexpr int kRuns = BN * kPerRow / 128;
+  static constexpr int kRowStep = 128 / kPerRow;
+};
+
+template <int DH, int MT, bool CODES, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 1)
+    tc_paged_kernel(const __grid_constant__ PagedAttnArgs a, int blocks, int splits) {
+  extern __shared__ uint8_t smem_raw[];
+  using C = Cfg<DH, MT>;
+  constexpr int NK = C::NK, NV = C::NV, NH = C::NH, NBUF = C::NBUF;
+  constexpr uint32_t kScore = 2 * DH;
+  Smem<DH, MT>& sm = *reinterpret_cast<Smem<DH, MT>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int heads = a.B * a.Hkv, G = a.H / a.Hkv, rows = G * a.Nq;
+  const int g = blockIdx.x % heads, rest = blockIdx.x / heads;
+  const int b = g / a.Hkv, hkv = g % a.Hkv;
+  const int split = rest % splits;
+  const int row0 = row_block(rest / splits, blocks, G, a.Nq, MT * BM) * (MT * BM);
+  volatile int* abort_flag = &sm.abort_flag;
+  unsigned int* err = a.err;
+
+  if (splits > 1) release_next();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NK; ++s) mbar_init(&sm.k_full[s], 4), mbar_init(&sm.k_empty[s], 1);
+    for (int s = 0; s < NV; ++s) mbar_init(&sm.v_full[s], 4), mbar_init(&sm.v_empty[s], 1);
+    for (int s = 0; s < NBUF; ++s) mbar_init(&sm.sc_full[s], 1), mbar_init(&sm.op_ready[s], 4);
+    mbar_init(&sm.pv_done[0], 1);
+    mbar_init(&sm.pv_done[1], 1);
+    mbar_init(&sm.out_full, 1);
+    sm.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 12) tmem_alloc(&sm.tmem_base, 512);
+  const int wg = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+  GroupRow gr{empty_view(), 0.f};
+  const int row = row0 + r + (MT == 2 ? BM * wg : 0);
+  if (warp < 8) {
+    gr = group_row(a, b, hkv, row, rows);
+    warp_hull(gr.v, row < rows, lane, sm.hull[warp]);
+    // Q: half a warp takes a row at a time, 8 or 4 elements a lane.
+    constexpr int kE = DH / 16, kPass = MT * BM / 16;
+    const int c = lane & 15;
+    const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.Q) +
+                             (static_cast<size_t>(g) * rows + row0) * DH + c * kE;
+#pragma unroll 4
+    for (int p = 0; p < kPass; ++p) {
+      const int qr = 16 * p + 2 * warp + (lane >> 4);
+      uint32_t w[kE / 2];
+#pragma unroll
+      for (int k = 0; k < kE / 2; ++k) w[k] = 0u;
+      if (row0 + qr < rows) {
+        if (kE == 8) {
+          const uint4 v = *reinterpret_cast<const uint4*>(Q + static_cast<size_t>(qr) * DH);
+          w[0] = v.x, w[1] = v.y, w[kE / 2 - 2] = v.z, w[kE / 2 - 1] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(Q + static_cast<size_t>(qr) * DH);
+          w[0] = v.x, w[1] = v.y;
+        }
+      }
+      if (CODES) {
+        float most = 0.f;
+#pragma unroll
+        for (int k = 0; k < kE / 2; ++k)
+          most = fmaxf(most, fmaxf(finite_abs(u2f(w[k] << 16)), finite_abs(u2f(w[k] & 0xFFFF0000u))));
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        const float shrink = row_shrink(most);
+#pragma unroll
+        for (int k = 0; k < kE / 2; ++k)
+          w[k] = pack<true>(u2f(w[k] << 16) * shrink, u2f(w[k] & 0xFFFF0000u) * shrink);
+        if (c == 0) sm.shrink[qr] = shrink;
+      }
+      uint8_t* dst = sm.q[qr / BM][c * kE / 64] + (qr % BM) * 128;
+      const int off = (c * kE % 64) * 2;  // byte in the 128-byte row; 16-byte runs are swizzled
+      dst += (((off >> 4) ^ (qr & 7)) << 4) + (off & 15);
+      if (kE == 8)
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[kE / 2 - 2], w[kE / 2 - 1]);
+      else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = sm.tmem_base;
+  const Hull hull = join_hulls(sm.hull, 8);
+  // Key tiles of the hull, and this split's run of them.
+  const int t_lo = hull.lo < hull.hi ? hull.lo / BN : 0;
+  const int t_n = hull.lo < hull.hi ? (hull.hi + BN - 1) / BN - t_lo : 0;
+  const int tb = t_lo + static_cast<int>(static_cast<long long>(t_n) * split / splits);
+  const int T = t_lo + static_cast<int>(static_cast<long long>(t_n) * (split + 1) / splits) - tb;
+  const int U = MT * T;  // units
+
+  if (warp == 12) {
+    constexpr uint32_t idS = idesc(CODES, BN, false), idO = idesc(CODES, DH, true);
+    const uint64_t dQ = smem_desc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
+    const uint64_t dK0 = smem_desc_sw128(smem_u32(sm.kv[0][0]), 16, 1024);
+    const uint64_t dV0 = smem_desc_sw128(smem_u32(sm.kv[NK][0]), HT, 1024);
+    constexpr uint64_t kStep = (NH * HT) >> 4;
+    auto tile = [](int u) { return MT == 2 ? u >> 1 : u; };
+    auto issue_scores = [&](int u) {
+      const uint64_t so = (tile(u) % NK) * kStep;
+      const uint64_t qo = MT == 2 ? (u & 1) * (uint64_t)((NH * HALF_BLOCK) >> 4) : 0;
+      const uint32_t sc = tbase + kScore + BN * (u % NBUF);
+#pragma unroll
+      for (int kk = 0; kk < DH / 16; ++kk) {
+        const uint32_t h = kk >> 2, o = 32 * (kk & 3);
+        mma_ss(sc, dQ + qo + ((h * HALF_BLOCK + o) >> 4), dK0 + so + ((h * HT + o) >> 4), idS,
+               kk > 0);
+      }
+      mma_commit(&sm.sc_full[u % NBUF]);
+      if (MT == 1 || (u & 1)) mma_commit(&sm.k_empty[tile(u) % NK]);
+    };
+    auto issue_pv = [&](int u) {
+      const int s = tile(u) % NV;
+      const uint32_t sc = tbase + kScore + BN * (u % NBUF);
+      const uint64_t dv = dV0 + s * kStep;
+      const uint32_t acc_col = tbase + DH * (u & 1);
+#pragma unroll
+      for (int c = 0; c < BN / 16; ++c)
+        mma_ts(acc_col, sc + 8 * c, dv + ((16 * 128 * c) >> 4), idO, (u >= 2 || c > 0));
+      mma_commit(&sm.pv_done[u & 1]);
+      if (MT == 1 || (u & 1)) mma_commit(&sm.v_empty[s]);
+    };
+    if (elect_one()) {
+      bool ok = true;
+      auto scores = [&](int u) {
+        const int t = tile(u);
+        ok = wait_one(&sm.k_full[t % NK], (t / NK) & 1, abort_flag, err);
+        tc_fence_after();
+        if (ok) issue_scores(u);
+      };
+      for (int u = 0; ok && u < NBUF && u < U; ++u) scores(u);
+      for (int u = 0; ok && u < U; ++u) {
+        const int t = tile(u);
+        ok = wait_one(&sm.v_full[t % NV], (t / NV) & 1, abort_flag, err) &&
+             wait_one(&sm.op_ready[u % NBUF], (u / NBUF) & 1, abort_flag, err);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv(u);
+        if (u + NBUF < U) scores(u + NBUF);
+      }
+      mma_commit(&sm.out_full);
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    using F = Feed<DH, CODES>;
+    const int tid = threadIdx.x - 256, col = tid % F::kPerRow, r0 = tid / F::kPerRow;
+    // Pages (and scales) of the next 32 chunks from this warp's position on, one a lane.
+    struct Meta {
+      int page;
+      float ks, vs;
+    };
+    const int chunks = T * kChunks, chunk0 = tb * kChunks;
+    auto meta_of = [&](int n) {
+      Meta m{-1, 1.f, 1.f};
+      const int j = (chunk0 + n) * 16;
+      if (n < chunks && j < hull.hi && j + 16 > hull.lo) {
+        const int page = page_at(a.page, b, j);
+        if (page_ok(a.page, page)) {
+          m.page = page;
+          if (CODES) {
+            const size_t at = static_cast<size_t>(page) * a.Hkv + hkv;
+            m.ks = a.page.k_scale[at];
+            m.vs = a.page.v_scale[at];
+          }
+        }
+      }
+      return m;
+    };
+    constexpr int kAhead = 32 / kChunks;  // tiles that 32 chunks are
+    Meta cur = meta_of(lane), nxt = meta_of(32 + lane);
+    int batch = 0;
+    // Address of run i of tile t, or null where there is nothing to read.
+    auto source = [&](int t, int i, bool values) -> const uint8_t* {
+      const int rr = r0 + F::kRowStep * i, j = (tb + t) * BN + rr;
+      const int n = t * kChunks + (rr >> 4);
+      const int page = __shfl_sync(0xffffffffu, (t / kAhead) == batch ? cur.page : nxt.page, n & 31);
+      if (page < 0 || j < hull.lo || j >= hull.hi) return nullptr;
+      return static_cast<const uint8_t*>(values ? a.V : a.K) +
+             page_row(a.page, page, a.Hkv, hkv, j) * F::kRow + 16 * col;
+    };
+    auto advance = [&](int t) {  // tile t is the next to be read
+      if (t / kAhead != batch) {
+        cur = nxt;
+        batch = t / kAhead;
+        nxt = meta_of((batch + 1) * 32 + lane);
+      }
+    };
+    auto free_slot = [&](int t, bool values) {
+      const int N = values ? NV : NK;
+      return t < N || wait_warp(values ? &sm.v_empty[t % NV] : &sm.k_empty[t % NK],
+                                ((t / N) - 1) & 1, abort_flag, err);
+    };
+    auto put_scales = [&](int t) {
+      if (!CODES || warp != 8) return;
+      const int n = t * kChunks + (lane & (kChunks - 1));
+      const bool now = (t / kAhead) == batch;
+      const float ks = __shfl_sync(0xffffffffu, now ? cur.ks : nxt.ks, n & 31);
+      const float vs = __shfl_sync(0xffffffffu, now ? cur.vs : nxt.vs, n & 31);
+      if (lane < kChunks) sm.scale[t % C::NS][lane] = make_float4(ks, __log2f(vs), 1.f / vs, 0.f);
+    };
+    auto slot = [&](int t, bool values) {
+      return smem_u32(sm.kv[values ? NK + t % NV : t % NK][0]);
+    };
+    auto done = [&](int t, bool values) {
+      fence_proxy_async_smem();
+      warp_arrive(values ? &sm.v_full[t % NV] : &sm.k_full[t % NK]);
+    };
+    bool ok = true;
+    if (CODES) {
+      // Both of a tile in registers, keys first: the next tile's are on their way while
+      // this one's are turned into fp16.
+      uint4 k[F::kRuns], v[F::kRuns];
+      auto load = [&](uint4 (&x)[F::kRuns], int t, bool values) {
+#pragma unroll
+        for (int i = 0; i < F::kRuns; ++i) {
+          const uint8_t* p = source(t, i, values);
+          x[i] = p ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+        }
+      };
+      auto store = [&](const uint4 (&x)[F::kRuns], int t, bool values) {
+        const uint32_t base = slot(t, values);
+        const uint32_t half = 16 * col / 64, c = (16 * col % 64) / 8;  // 16-byte run of fp16
+#pragma unroll
+        for (int i = 0; i < F::kRuns; ++i) {
+          const int rr = r0 + F::kRowStep * i;
+          const uint32_t line = base + half * HT + rr * 128;
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t h[8];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            h[2 * q] = codes_to_half2(static_cast<uint16_t>(w[q]));
+            h[2 * q + 1] = codes_to_half2(static_cast<uint16_t>(w[q] >> 16));
+          }
+          // The lanes of the second 64 columns store their runs in the other order:
+          // the same banks would meet otherwise.
+          const bool swap = half != 0;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const bool second = (u == 1) != swap;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             line + (((c + (second ? 1 : 0)) ^ (rr & 7)) << 4)),
+                         "r"(second ? h[4] : h[0]), "r"(second ? h[5] : h[1]),
+                         "r"(second ? h[6] : h[2]), "r"(second ? h[7] : h[3])
+                         : "memory");
+          }
+        }
+      };
+      if (T > 0) load(k, 0, false), load(v, 0, true);
+      for (int t = 0; ok && t < T; ++t) {
+        ok = free_slot(t, false);
+        if (!ok) break;
+        put_scales(t);
+        store(k, t, false);
+        done(t, false);
+        if (t + 1 < T) load(k, t + 1, false);
+        ok = free_slot(t, true);
+        if (!ok) break;
+        store(v, t, true);
+        done(t, true);
+        if (t + 1 < T) load(v, t + 1, true);
+        advance(t + 1);
+      }
+    } else {
+      // Straight into the slots; a copy is handed over when the next one is under way.
+      auto copy = [&](int t, bool values) {
+        const uint32_t base = slot(t, values);
+#pragma unroll
+        for (int i = 0; i < F::kRuns; ++i) {
+          const int rr = r0 + F::kRowStep * i;
+          const uint8_t* p = source(t, i, values);
+          const uint32_t dst = base + (col / 8) * HT + rr * 128 + (((col % 8) ^ (rr & 7)) << 4);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                       "l"(p ? p : static_cast<const uint8_t*>(a.K)), "r"(p ? 16 : 0)
+                       : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      for (int i = 0; ok && i <= 2 * T; ++i) {  // keys of tile 0, values of tile 0, ...
+        if (i < 2 * T) {
+          if (!(i & 1)) advance(i >> 1);
+          ok = free_slot(i >> 1, i & 1);
+          if (!ok) break;
+          copy(i >> 1, i & 1);
+        }
+        if (i == 0) continue;
+        if (i < 2 * T) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+        done((i - 1) >> 1, (i - 1) & 1);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+  } else {
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t acc_own = tbase + lane_off + DH * wg;
+    const int lo = gr.v.lo, hi = gr.v.hi;
+    const Hull own = MT == 2 ? join_hulls(sm.hull + 4 * wg, 4) : hull;
+    const float grow = CODES ? 1.f / sm.shrink[(MT == 2 ? BM * wg : 0) + r] : 1.f;
+    const PagedScore<CODES, CAP, BIAS> score(a, gr.slope2, grow);
+    const bool any_row = row0 + (MT == 2 ? BM * wg : 0) + quad * 32 < rows;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    int n = 0;  // units of this warpgroup
+    for (int u = wg; u < U; u += 2, ++n) {
+      const int t = MT == 2 ? u >> 1 : u, col0 = (tb + t) * BN;
+      ok = wait_warp(&sm.sc_full[u % NBUF], (u / NBUF) & 1, abort_flag, err);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t sc = tbase + lane_off + kScore + BN * (u % NBUF);
+      const bool masked = col0 < own.in_lo || col0 + BN > own.in_hi;
+      const float dist = BIAS ? static_cast<float>(col0 - gr.v.pos) : 0.f;
+      const float4* chunk = sm.scale[t % C::NS];
+      if (!any_row) {
+        warp_arrive(&sm.op_ready[u % NBUF]);
+        continue;
+      }
+      // Two groups of 64 columns: the second is read twice, so that one group is held in
+      // registers at a time, and P~ of columns 16 c .. goes to columns 8 c .., onto scores
+      // already used.
+      uint32_t s[4][16];
+      auto load = [&](int c) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld16(sc + c + 16 * q, s[q]);
+        tmem_wait_ld();
+        score.scale(s, chunk + c / 16);
+        if (CAP && BIAS) score.sc.tanh_of(s, masked);
+      };
+      auto max_of = [&](int c) {
+        return masked ? score.template largest<true>(s, chunk + c / 16, col0 + c, lo, hi, dist + c)
+                      : score.template largest<false>(s, chunk + c / 16, col0 + c, lo, hi, dist + c);
+      };
+      load(64);
+      float mt = max_of(64);
+      load(0);
+      mt = fmaxf(mt, max_of(0));
+      const bool raise = mt > m + kRescale;
+      const float fac = raise ? (m == -INFINITY ? 0.f : ex2_approx(m - mt)) : 1.f;
+      if (raise) {
+        l *= fac;
+        m = mt;
+      }
+      if (__any_sync(0xffffffffu, raise && fac < 1.f) && n > 0) {
+        // The products of this warpgroup's last unit.  S(u) was issued behind those of
+        // unit u - NBUF, so of the barrier's phases only the last may be open.
+        const int last = u - 2;
+        ok = wait_warp(&sm.pv_done[last & 1], (last >> 1) & 1, abort_flag, err);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < DH / 16; ++c) {
+          uint32_t v[16];
+          tmem_ld16(acc_own + 16 * c, v);
+          tmem_wait_ld();
+          uint32_t w0[8], w1[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            w0[k] = __float_as_uint(u2f(v[k]) * fac);
+            w1[k] = __float_as_uint(u2f(v[8 + k]) * fac);
+          }
+          tmem_st8(acc_own + 16 * c, w0);
+          tmem_st8(acc_own + 16 * c + 8, w1);
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : m;  // nothing seen so far: all weights 0
+#pragma unroll
+      for (int c = 0; c < BN; c += 64) {
+        if (c > 0) load(c);
+        if (!BIAS) score.sc.tanh_of(s, masked);
+        const float4* sca = chunk + c / 16;
+        if (masked)
+          score.template weights<true>(s, sca, col0 + c, lo, hi, dist + c, base, l, sc + c / 2);
+        else
+          score.template weights<false>(s, sca, col0 + c, lo, hi, dist + c, base, l, sc + c / 2);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(&sm.op_ready[u % NBUF]);
+    }
+
+    ok = wait_warp(&sm.out_full, 0, abort_flag, err) && ok;
+    ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+    tc_fence_after();
+    // MT = 1: merge the warpgroups' (m, l, O~): m* = max, s_w = exp2(m_w - m*),
+    // O~ = s_0 O~_0 + s_1 O~_1, l = s_0 l_0 + s_1 l_1.  An accumulator whose
+    // warpgroup had no unit was never written.
+    float mm = m, lsum = l, s0 = 1.f, s1 = 0.f;
+    if (MT == 1) {
+      sm.part_m[wg][r] = m;
+      sm.part_l[wg][r] = l;
+      named_bar_sync(1, 256);
+      const float m0 = sm.part_m[0][r], m1 = sm.part_m[1][r];
+      mm = fmaxf(m0, m1);
+      s0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - mm);
+      s1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - mm);
+      lsum = s0 * sm.part_l[0][r] + s1 * sm.part_l[1][r];
+    }
+    const bool any0 = T > 0, any1 = MT == 1 && T > 1;
+    const float inv = splits > 1 ? 1.f : lsum > 0.f ? 1.f / lsum : 0.f;
+    s0 = any0 ? s0 * inv : 0.f;
+    s1 = any1 ? s1 * inv : 0.f;
+    const size_t all = static_cast<size_t>(a.B) * a.H * a.Nq;
+    const size_t base = static_cast<size_t>(g) * rows;  // first row of the group
+    const Partials part = partials(a.workspace, all, DH, splits);
+    if (ok && row < rows && (MT == 2 || wg == 0)) {
+      if (splits > 1) part.ml[split * all + base + row] = make_float2(mm, lsum);
+      else a.L[base + row] = (mm + __log2f(lsum)) * kLn2;
+    }
+    // Every MMA is done, so the ring is idle: 64 columns of O at a time go through it
+    // and leave with coalesced stores.
+    constexpr int kStageLd = 64 + 4;
+    float* st = reinterpret_cast<float*>(&sm.kv[0][0][0]);
+    static_assert(MT * BM * kStageLd * 4 <= sizeof(sm.kv), "epilogue staging fits in the ring");
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      if (h > 0) named_bar_sync(1, 256);
+      // With two accumulators for the same rows each warpgroup forms half the columns.
+      constexpr int kCols = MT == 1 ? 32 : 64;
+      const int c0 = MT == 1 ? 32 * wg : 0, sr = MT == 2 ? BM * wg + r : r;
+#pragma unroll
+      for (int c = 0; c < kCols; c += 16) {
+        const uint32_t col = 64 * h + c0 + c;
+        uint32_t v0[16], v1[16];
+        if (MT == 2) {
+          tmem_ld16(acc_own + col, v0);
+        } else {
+          tmem_ld16(tbase + lane_off + col, v0);
+          tmem_ld16(tbase + lane_off + DH + col, v1);
+        }
+        tmem_wait_ld();
+        float4* s4 = reinterpret_cast<float4*>(st + sr * kStageLd + c0 + c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float o[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            o[q] = any0 ? s0 * u2f(v0[4 * k + q]) : 0.f;
+            if (MT == 1 && any1) o[q] = fmaf(s1, u2f(v1[4 * k + q]), o[q]);
+          }
+          s4[k] = make_float4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      named_bar_sync(1, 256);
+      const int live = min(MT * BM, rows - row0);
+      if (ok) {
+        for (int f = threadIdx.x; f < live * 16; f += 256) {
+          const int rr = f >> 4, c4 = f & 15;
+          const float4 v = *reinterpret_cast<const float4*>(st + rr * kStageLd + 4 * c4);
+          const size_t at = (base + row0 + rr) * DH + 64 * h + 4 * c4;
+          if (splits > 1)
+            *reinterpret_cast<float4*>(part.o + split * all * DH + at) = v;
+          else
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + at) =
+                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+template <int DH, int MT, bool CODES, bool CAP, bool BIAS>
+cudaError_t launch(const PagedAttnArgs& a, int splits) {
+  constexpr size_t smem = sizeof(Smem<DH, MT>) + 1024;
+  static_assert(smem <= 232448, "shared memory");
+  const auto kernel = tc_paged_kernel<DH, MT, CODES, CAP, BIAS>;
+  const cudaError_t e = tc_set_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const int rows = a.H / a.Hkv * a.Nq, blocks = (rows + MT * BM - 1) / (MT * BM);
+  const long long grid = static_cast<long long>(blocks) * splits * a.B * a.Hkv;
+  if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+  kernel<<<static_cast<unsigned>(grid), kThreads, smem, a.stream>>>(a, blocks, splits);
+  return cudaGetLastError();
+}
+
+template <int DH, int MT, bool CODES>
+cudaError_t launch(const PagedAttnArgs& a, int splits) {
+  const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;
+  return cap ? (bias ? launch<DH, MT, CODES, true, true>(a, splits)
+                     : launch<DH, MT, CODES, true, false>(a, splits))
+             : (bias ? launch<DH, MT, CODES, false, true>(a, splits)
+                     : launch<DH, MT, CODES, false, false>(a, splits));
+}
+
+template <int DH, int MT>
+cudaError_t launch(const PagedAttnArgs& a, int splits) {
+  return a.page.e4m3 ? launch<DH, MT, true>(a, splits) : launch<DH, MT, false>(a, splits);
+}
+
+// 256 rows a block where such blocks fill the GPU; below, 128.
+bool two_blocks(const PagedAttnArgs& a) {
+  const long long rows = static_cast<long long>(a.H / a.Hkv) * a.Nq;
+  return rows > BM && static_cast<long long>(a.B) * a.Hkv * ((rows + 255) / 256) >= kSMs;
+}
+
+}  // namespace
+
+bool tc_paged_supported(const PagedAttnArgs& a) { return a.bf16 && (a.d == 64 || a.d == 128); }
+
+// Runs that the keys are cut into where blocks leave SMs idle, 512 keys at least in each.
+int tc_paged_splits(const PagedAttnArgs& a) {
+  if (two_blocks(a)) return 1;
+  const long long rows = static_cast<long long>(a.H / a.Hkv) * a.Nq;
+  const long long blocks = static_cast<long long>(a.B) * a.Hkv * ((rows + BM - 1) / BM);
+  const long long want = kSMs / blocks, most = a.Nk / 512;
+  const long long s = want < most ? want : most;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
+cudaError_t tc_paged(const PagedAttnArgs& a) {
+  const int splits = tc_paged_splits(a);
+  cudaError_t e;
+  if (a.d == 64) e = two_blocks(a) ? launch<64, 2>(a, 1) : launch<64, 1>(a, splits);
+  else e = two_blocks(a) ? launch<128, 2>(a, 1) : launch<128, 1>(a, splits);
+  return e == cudaSuccess && splits > 1 ? attn_join(a, splits) : e;
+}
+
+}  // namespace flashbob
