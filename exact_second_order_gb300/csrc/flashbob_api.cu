@@ -392,9 +392,11 @@ flashbob_status check_pages(PageArgs& p, int P, int T, int M, flashbob_dtype dty
   return FLASHBOB_OK;
 }
 
-// Scales come with an 8-bit cache and with no other.
-flashbob_status check_scales(const PageArgs& p) {
-  return !p.k_scale == p.e4m3 || !p.v_scale == p.e4m3 ? FLASHBOB_ERR_INVALID_ARG : FLASHBOB_OK;
+// Scales come with an 8-bit cache and with no other; a page and head is counted in 32
+// bits, one beyond the last included.
+flashbob_status check_pools(const PageArgs& p, int Hkv) {
+  if (!p.k_scale == p.e4m3 || !p.v_scale == p.e4m3) return FLASHBOB_ERR_INVALID_ARG;
+  return static_cast<long long>(p.P) * Hkv >= INT_MAX ? FLASHBOB_ERR_UNSUPPORTED : FLASHBOB_OK;
 }
 
 size_t pool_bytes(const PageArgs& p, int Hkv, int d, int element) {
@@ -612,7 +614,7 @@ flashbob_status flashbob_cache_append(const void* QKV, const float* wq, const fl
   a.interleaved = interleaved == 1, a.bf16 = in_dtype == FLASHBOB_BF16;
   a.stream = (cudaStream_t)stream;
   st = check_norm(a, in_dtype, interleaved, true);
-  if (st == FLASHBOB_OK) st = check_scales(a.page);
+  if (st == FLASHBOB_OK) st = check_pools(a.page, Hkv);
   if (st != FLASHBOB_OK) return st;
   // Tokens and their pages are counted in 32 bits, a page beyond the last included.
   if (N > INT_MAX - 1024) return FLASHBOB_ERR_UNSUPPORTED;
@@ -651,7 +653,7 @@ flashbob_status flashbob_cache_read(const void* K, const void* V, const float* k
   a.stream = (cudaStream_t)stream;
   if (B <= 0 || Hkv <= 0 || Nk <= 0 || d <= 0 || Nk > M * T) return FLASHBOB_ERR_INVALID_ARG;
   if (d > 128 || B > kMaxGridY || Hkv > kMaxGridY) return FLASHBOB_ERR_UNSUPPORTED;
-  st = check_scales(a.page);
+  st = check_pools(a.page, Hkv);
   if (st != FLASHBOB_OK) return st;
   const size_t e = a.bf16 ? 2 : 4, pool = pool_bytes(a.page, Hkv, d, (int)e);
   const size_t scales = (size_t)P * Hkv * 4, out = (size_t)B * Hkv * Nk * d * e;
@@ -700,7 +702,7 @@ flashbob_status flashbob_attention_paged(const void* Q, const void* K, const voi
   a.B = B, a.H = H, a.Hkv = Hkv, a.Nq = Nq, a.Nk = M * T, a.d = d;
   a.causal = causal == 1, a.bf16 = in_dtype == FLASHBOB_BF16, a.stream = (cudaStream_t)stream;
   st = check_attention(a, causal, in_dtype);
-  if (st == FLASHBOB_OK) st = check_scales(a.page);
+  if (st == FLASHBOB_OK) st = check_pools(a.page, Hkv);
   if (st != FLASHBOB_OK) return st;
   const size_t rows = (size_t)B * H * Nq, e = a.bf16 ? 2 : 4, need = paged_workspace(a);
   const size_t pool = pool_bytes(a.page, Hkv, d, (int)e), scales = (size_t)P * Hkv * 4;

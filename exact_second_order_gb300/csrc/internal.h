@@ -166,10 +166,12 @@ size_t tc_pass2_smem();
 size_t tc_pass1_d128_smem();
 size_t tc_pass2_d128_smem();
 // Tensor map of a bf16 [BH, N, dh] tensor with 128-byte-swizzled boxes of
-// `rows` x 64 elements (tc::make_map_bf16), kept in a small per-process
+// `rows` x 64 elements (tc::make_map), kept in a small per-process
 // cache keyed by every encoding argument: a map is a pure function of them,
 // so repeated calls on the same buffers skip the driver's encoder.
 cudaError_t tc_map_bf16(CUtensorMap* map, const void* base, int BH, int N, int rows, int dh);
+// The same, or of a tensor of bytes in boxes of whole rows (tc::make_map).
+cudaError_t tc_map(CUtensorMap* map, const void* base, int BH, int N, int rows, int dh, bool bytes);
 // cudaFuncSetAttribute(kernel, MaxDynamicSharedMemorySize, bytes), once per
 // (kernel, device, bytes).
 cudaError_t tc_set_smem(const void* kernel, int bytes);

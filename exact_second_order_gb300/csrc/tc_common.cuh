@@ -365,8 +365,10 @@ __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
 // [BH][N][dh] bf16 tensor (dh = 64 or 128), box {64, rows, 1}: one
 // 64-column (128-byte) slice of `rows` rows, 128-byte swizzle, zero fill out
 // of bounds.  A 128-column row is loaded as two boxes at x = 0 and x = 64.
-inline cudaError_t make_map_bf16(CUtensorMap* map, const void* base, int BH, int N, int rows,
-                                 int dh) {
+// `bytes`: elements of one byte, box {dh, rows, 1}: whole rows, in the swizzle
+// of their length (64 or 128 bytes).
+inline cudaError_t make_map(CUtensorMap* map, const void* base, int BH, int N, int rows, int dh,
+                            bool bytes) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (encode == nullptr) {
     cudaDriverEntryPointQueryResult q;
@@ -378,12 +380,15 @@ inline cudaError_t make_map_bf16(CUtensorMap* map, const void* base, int BH, int
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
   cuuint64_t dims[3] = {(cuuint64_t)dh, (cuuint64_t)N, (cuuint64_t)BH};
-  cuuint64_t strides[2] = {(cuuint64_t)dh * 2, (cuuint64_t)N * dh * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
+  const cuuint64_t row = static_cast<cuuint64_t>(dh) * (bytes ? 1 : 2);
+  cuuint64_t strides[2] = {row, (cuuint64_t)N * row};
+  cuuint32_t box[3] = {bytes ? (cuuint32_t)dh : 64, (cuuint32_t)rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-                      strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  CUresult r = encode(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                      3, const_cast<void*>(base), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      bytes && dh == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

@@ -83,6 +83,7 @@ namespace {
 struct MapEntry {
   const void* base = nullptr;
   int BH = 0, N = 0, rows = 0, dh = 0;
+  bool bytes = false;
   uint64_t used = 0;  // last use, for replacement
   CUtensorMap map;
 };
@@ -97,32 +98,38 @@ struct SmemSet {
 };
 
 std::mutex g_smem_mu;
-SmemSet g_smem[64];
+SmemSet g_smem[192];
 
 }  // namespace
 
-cudaError_t tc_map_bf16(CUtensorMap* map, const void* base, int BH, int N, int rows, int dh) {
+cudaError_t tc_map(CUtensorMap* map, const void* base, int BH, int N, int rows, int dh,
+                   bool bytes) {
   std::lock_guard<std::mutex> lock(g_map_mu);
   MapEntry* victim = &g_maps[0];
   for (MapEntry& m : g_maps) {
     if (m.base == base && m.BH == BH && m.N == N && m.rows == rows && m.dh == dh &&
-        base != nullptr) {
+        m.bytes == bytes && base != nullptr) {
       m.used = ++g_map_clock;
       *map = m.map;
       return cudaSuccess;
     }
     if (m.used < victim->used) victim = &m;
   }
-  const cudaError_t e = tc::make_map_bf16(map, base, BH, N, rows, dh);
+  const cudaError_t e = tc::make_map(map, base, BH, N, rows, dh, bytes);
   if (e != cudaSuccess) return e;
   victim->base = base;
   victim->BH = BH;
   victim->N = N;
   victim->rows = rows;
   victim->dh = dh;
+  victim->bytes = bytes;
   victim->used = ++g_map_clock;
   victim->map = *map;
   return cudaSuccess;
+}
+
+cudaError_t tc_map_bf16(CUtensorMap* map, const void* base, int BH, int N, int rows, int dh) {
+  return tc_map(map, base, BH, N, rows, dh, false);
 }
 
 cudaError_t tc_set_smem(const void* kernel, int bytes) {

@@ -32,35 +32,44 @@ using namespace attn;
 using namespace paged;
 
 constexpr int BM = kTcRows;
-constexpr int BN = 128;
-constexpr int kChunks = BN / 16;  // 16 keys lie on one page
-constexpr int kThreads = 416;     // elementwise warps 0 - 7, producers 8 - 11, MMA 12
 constexpr uint32_t HALF_BLOCK = BM * 64 * 2;
-constexpr uint32_t HT = BN * 64 * 2;  // 64 columns of a tile
 constexpr float kRescale = 8.f;
 
-template <int DH, int MT>
+template <int DH, int MT, bool CODES>
 struct Cfg {
   static constexpr int NH = DH / 64;
-  static constexpr int NBUF = DH == 64 ? 3 : 2;  // score buffers: O~ takes the rest of TMEM
-  static constexpr int kStages = DH == 64 ? 5 : MT == 2 ? 2 : 3;  // of keys; as many of values
-  static constexpr int NK = kStages, NV = DH == 128 && MT == 1 ? 2 : kStages;
-  // Scales of tile t are written when the scores of tile t - NK are done, which were
-  // issued behind the products of a unit NBUF earlier: that one's readers are through.
-  static constexpr int NS = NK + NBUF;
+  static constexpr int BN = DH == 64 ? 128 : 64;  // keys of a tile
+  static constexpr int kChunks = BN / 16;         // 16 keys lie on one page
+  static constexpr uint32_t HT = BN * 64 * 2;     // bytes of 64 columns of a tile
+  static constexpr int NBUF = DH == 64 ? 3 : 4;   // score buffers: O~ takes the rest of TMEM
+  // Tiles of keys and of values as operands, and of codes on their way there.
+  static constexpr int NK = !CODES ? (DH == 64 ? 5 : 4) : DH == 64 ? 4 : 3;
+  static constexpr int NV = !CODES ? (DH == 64 || MT == 2 ? NK : 5) : DH == 64 || MT == 1 ? 3 : 2;
+  static constexpr int NI = CODES ? 8 : 0;
+  // The scales of tile t are written when the codes of item 2 t - NI have been taken, so
+  // the scores of tile t - NI / 2 - NK are done, which were issued behind the products of
+  // a unit NBUF earlier: its readers are through.
+  static constexpr int NS = NI / 2 + NK + NBUF;
+  // Elementwise warps 0 - 7, converters 8 - 11 (codes), loads, MMA.
+  static constexpr int kLoad = CODES ? 12 : 8, kMma = kLoad + 1, kThreads = 32 * (kMma + 1);
   static_assert(2 * DH + NBUF * BN <= 512, "TMEM columns");
+  // Keys and values arrive alternately, and the MMA warp waits for keys NBUF units ahead
+  // of the values that it frees.
+  static_assert(NK >= 2 && MT * NV >= NBUF - (MT == 1 ? 1 : 0), "no wait of one ring for the other");
 };
 
-template <int DH, int MT>
+template <int DH, int MT, bool CODES>
 struct Smem {
-  using C = Cfg<DH, MT>;
+  using C = Cfg<DH, MT, CODES>;
   alignas(1024) uint8_t q[MT][C::NH][HALF_BLOCK];
-  alignas(1024) uint8_t kv[C::NK + C::NV][C::NH][HT];
-  float4 scale[C::NS][kChunks];  // s_K, log2 s_V, 1 / s_V of each chunk of a tile
+  alignas(1024) uint8_t kv[C::NK + C::NV][C::NH][C::HT];
+  alignas(1024) uint8_t item[C::NI > 0 ? C::NI : 1][C::NI > 0 ? C::BN * DH : 16];  // codes
+  float4 scale[C::NS][C::kChunks];  // s_K, log2 s_V, 1 / s_V of each chunk of a tile
   float shrink[MT * BM];
   float part_m[2][BM], part_l[2][BM];
   int hull[8][4];  // of each elementwise warp's rows
   uint64_t k_full[C::NK], k_empty[C::NK], v_full[C::NV], v_empty[C::NV];
+  uint64_t i_full[C::NI + 1], i_empty[C::NI + 1];
   uint64_t sc_full[C::NBUF], op_ready[C::NBUF];
   uint64_t pv_done[2];  // of even and odd units
   uint64_t out_full;
@@ -168,25 +177,35 @@ struct PagedScore {
   }
 };
 
-// One tile of keys or values, by the four producer warps: a thread's 16-byte runs of
-// the pages' rows.  Run i of a thread is column run x % kPerRow of row x / kPerRow, x =
-// tid + 128 i.
-template <int DH, bool CODES>
+// The converters' 128 threads: run i of a thread is 16-byte run `col` of row row0 +
+// kStep i of an item.  Eight lanes read 16-byte runs of codes, and store runs of fp16, on
+// different banks: with rows of 128 bytes (two halves of fp16) four runs of one half of
+// rows r and r ^ 5, else four of two rows.
+template <int DH>
 struct Feed {
-  static constexpr int kRow = DH * (CODES ? 1 : 2);
-  static constexpr int kPerRow = kRow / 16;
-  static constexpr int kRuns = BN * kPerRow / 128;
-  static constexpr int kRowStep = 128 / kPerRow;
+  static constexpr int kPerRow = DH / 16, kStep = 128 / kPerRow;
+  int col, row0;
+  __device__ __forceinline__ explicit Feed(int tid) {
+    col = tid & 3;
+    row0 = tid >> 2;
+    if (DH == 128) {
+      col |= (tid >> 1) & 4;
+      row0 = ((tid >> 2 & 1) * 5) ^ ((tid >> 4 & 1) * 2) ^ ((tid >> 5 & 1) * 4) ^ ((tid >> 6 & 1) * 8);
+    }
+  }
 };
 
 template <int DH, int MT, bool CODES, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kThreads, 1)
-    tc_paged_kernel(const __grid_constant__ PagedAttnArgs a, int blocks, int splits) {
+__global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
+    tc_paged_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
+                    const __grid_constant__ PagedAttnArgs a, int blocks, int splits) {
   extern __shared__ uint8_t smem_raw[];
-  using C = Cfg<DH, MT>;
-  constexpr int NK = C::NK, NV = C::NV, NH = C::NH, NBUF = C::NBUF;
+  using C = Cfg<DH, MT, CODES>;
+  constexpr int NK = C::NK, NV = C::NV, NH = C::NH, NBUF = C::NBUF, BN = C::BN;
+  constexpr int kChunks = C::kChunks;
+  constexpr uint32_t HT = C::HT;
   constexpr uint32_t kScore = 2 * DH;
-  Smem<DH, MT>& sm = *reinterpret_cast<Smem<DH, MT>*>(
+  Smem<DH, MT, CODES>& sm = *reinterpret_cast<Smem<DH, MT, CODES>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = a.B * a.Hkv, G = a.H / a.Hkv, rows = G * a.Nq;
@@ -199,8 +218,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (splits > 1) release_next();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NK; ++s) mbar_init(&sm.k_full[s], 4), mbar_init(&sm.k_empty[s], 1);
-    for (int s = 0; s < NV; ++s) mbar_init(&sm.v_full[s], 4), mbar_init(&sm.v_empty[s], 1);
+    constexpr int kFull = CODES ? 4 : 1;
+    for (int s = 0; s < NK; ++s) mbar_init(&sm.k_full[s], kFull), mbar_init(&sm.k_empty[s], 1);
+    for (int s = 0; s < NV; ++s) mbar_init(&sm.v_full[s], kFull), mbar_init(&sm.v_empty[s], 1);
+    for (int s = 0; s < C::NI; ++s) mbar_init(&sm.i_full[s], 1), mbar_init(&sm.i_empty[s], 4);
     for (int s = 0; s < NBUF; ++s) mbar_init(&sm.sc_full[s], 1), mbar_init(&sm.op_ready[s], 4);
     mbar_init(&sm.pv_done[0], 1);
     mbar_init(&sm.pv_done[1], 1);
@@ -208,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm.abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 12) tmem_alloc(&sm.tmem_base, 512);
+  if (warp == C::kMma) tmem_alloc(&sm.tmem_base, 512);
   const int wg = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
   GroupRow gr{empty_view(), 0.f};
   const int row = row0 + r + (MT == 2 ? BM * wg : 0);
@@ -269,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int T = t_lo + static_cast<int>(static_cast<long long>(t_n) * (split + 1) / splits) - tb;
   const int U = MT * T;  // units
 
-  if (warp == 12) {
+  if (warp == C::kMma) {
     constexpr uint32_t idS = idesc(CODES, BN, false), idO = idesc(CODES, DH, true);
     const uint64_t dQ = smem_desc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
     const uint64_t dK0 = smem_desc_sw128(smem_u32(sm.kv[0][0]), 16, 1024);
@@ -321,26 +342,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(&sm.out_full);
     }
     __syncwarp();
-  } else if (warp >= 8) {
-    using F = Feed<DH, CODES>;
-    const int tid = threadIdx.x - 256, col = tid % F::kPerRow, r0 = tid / F::kPerRow;
-    // Pages (and scales) of the next 32 chunks from this warp's position on, one a lane.
+  } else if (warp == C::kLoad) {
+    // One lane for each of the next 32 chunks of 16 keys, and of the 32 behind: the page
+    // and head that holds it (one past the last where there is nothing to read, which
+    // the copies fill with zeros) and its scales.
     struct Meta {
-      int page;
+      int slab;
       float ks, vs;
     };
     const int chunks = T * kChunks, chunk0 = tb * kChunks;
+    const int box = min(a.page.T, BN), per = box / 16, boxes = BN / box;  // keys of one copy
     auto meta_of = [&](int n) {
-      Meta m{-1, 1.f, 1.f};
-      const int j = (chunk0 + n) * 16;
-      if (n < chunks && j < hull.hi && j + 16 > hull.lo) {
+      Meta m{a.page.P * a.Hkv, 1.f, 1.f};
+      const int j = (chunk0 + n) * 16 & ~(box - 1);
+      if (n < chunks && j < hull.hi && j + box > hull.lo) {
         const int page = page_at(a.page, b, j);
         if (page_ok(a.page, page)) {
-          m.page = page;
+          m.slab = page * a.Hkv + hkv;
           if (CODES) {
-            const size_t at = static_cast<size_t>(page) * a.Hkv + hkv;
-            m.ks = a.page.k_scale[at];
-            m.vs = a.page.v_scale[at];
+            m.ks = a.page.k_scale[m.slab];
+            m.vs = a.page.v_scale[m.slab];
           }
         }
       }
@@ -348,126 +369,115 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     constexpr int kAhead = 32 / kChunks;  // tiles that 32 chunks are
     Meta cur = meta_of(lane), nxt = meta_of(32 + lane);
-    int batch = 0;
-    // Address of run i of tile t, or null where there is nothing to read.
-    auto source = [&](int t, int i, bool values) -> const uint8_t* {
-      const int rr = r0 + F::kRowStep * i, j = (tb + t) * BN + rr;
-      const int n = t * kChunks + (rr >> 4);
-      const int page = __shfl_sync(0xffffffffu, (t / kAhead) == batch ? cur.page : nxt.page, n & 31);
-      if (page < 0 || j < hull.lo || j >= hull.hi) return nullptr;
-      return static_cast<const uint8_t*>(values ? a.V : a.K) +
-             page_row(a.page, page, a.Hkv, hkv, j) * F::kRow + 16 * col;
-    };
-    auto advance = [&](int t) {  // tile t is the next to be read
-      if (t / kAhead != batch) {
-        cur = nxt;
-        batch = t / kAhead;
-        nxt = meta_of((batch + 1) * 32 + lane);
-      }
-    };
-    auto free_slot = [&](int t, bool values) {
-      const int N = values ? NV : NK;
-      return t < N || wait_warp(values ? &sm.v_empty[t % NV] : &sm.k_empty[t % NK],
-                                ((t / N) - 1) & 1, abort_flag, err);
-    };
-    auto put_scales = [&](int t) {
-      if (!CODES || warp != 8) return;
-      const int n = t * kChunks + (lane & (kChunks - 1));
-      const bool now = (t / kAhead) == batch;
-      const float ks = __shfl_sync(0xffffffffu, now ? cur.ks : nxt.ks, n & 31);
-      const float vs = __shfl_sync(0xffffffffu, now ? cur.vs : nxt.vs, n & 31);
-      if (lane < kChunks) sm.scale[t % C::NS][lane] = make_float4(ks, __log2f(vs), 1.f / vs, 0.f);
-    };
-    auto slot = [&](int t, bool values) {
-      return smem_u32(sm.kv[values ? NK + t % NV : t % NK][0]);
-    };
-    auto done = [&](int t, bool values) {
-      fence_proxy_async_smem();
-      warp_arrive(values ? &sm.v_full[t % NV] : &sm.k_full[t % NK]);
-    };
     bool ok = true;
-    if (CODES) {
-      // Both of a tile in registers, keys first: the next tile's are on their way while
-      // this one's are turned into fp16.
-      uint4 k[F::kRuns], v[F::kRuns];
-      auto load = [&](uint4 (&x)[F::kRuns], int t, bool values) {
-#pragma unroll
-        for (int i = 0; i < F::kRuns; ++i) {
-          const uint8_t* p = source(t, i, values);
-          x[i] = p ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
-        }
-      };
-      auto store = [&](const uint4 (&x)[F::kRuns], int t, bool values) {
-        const uint32_t base = slot(t, values);
-        const uint32_t half = 16 * col / 64, c = (16 * col % 64) / 8;  // 16-byte run of fp16
-#pragma unroll
-        for (int i = 0; i < F::kRuns; ++i) {
-          const int rr = r0 + F::kRowStep * i;
-          const uint32_t line = base + half * HT + rr * 128;
-          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-          uint32_t h[8];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            h[2 * q] = codes_to_half2(static_cast<uint16_t>(w[q]));
-            h[2 * q + 1] = codes_to_half2(static_cast<uint16_t>(w[q] >> 16));
-          }
-          // The lanes of the second 64 columns store their runs in the other order:
-          // the same banks would meet otherwise.
-          const bool swap = half != 0;
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const bool second = (u == 1) != swap;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             line + (((c + (second ? 1 : 0)) ^ (rr & 7)) << 4)),
-                         "r"(second ? h[4] : h[0]), "r"(second ? h[5] : h[1]),
-                         "r"(second ? h[6] : h[2]), "r"(second ? h[7] : h[3])
-                         : "memory");
-          }
-        }
-      };
-      if (T > 0) load(k, 0, false), load(v, 0, true);
-      for (int t = 0; ok && t < T; ++t) {
-        ok = free_slot(t, false);
-        if (!ok) break;
-        put_scales(t);
-        store(k, t, false);
-        done(t, false);
-        if (t + 1 < T) load(k, t + 1, false);
-        ok = free_slot(t, true);
-        if (!ok) break;
-        store(v, t, true);
-        done(t, true);
-        if (t + 1 < T) load(v, t + 1, true);
-        advance(t + 1);
+    int started = 0;
+    for (int i = 0; ok && i < 2 * T; ++i) {  // keys of tile 0, values of tile 0, keys of 1 ..
+      const int t = i >> 1;
+      const bool values = i & 1;
+      if (!values && t > 0 && t % kAhead == 0) {
+        cur = nxt;
+        nxt = meta_of((t / kAhead + 1) * 32 + lane);
       }
-    } else {
-      // Straight into the slots; a copy is handed over when the next one is under way.
-      auto copy = [&](int t, bool values) {
-        const uint32_t base = slot(t, values);
-#pragma unroll
-        for (int i = 0; i < F::kRuns; ++i) {
-          const int rr = r0 + F::kRowStep * i;
-          const uint8_t* p = source(t, i, values);
-          const uint32_t dst = base + (col / 8) * HT + rr * 128 + (((col % 8) ^ (rr & 7)) << 4);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                       "l"(p ? p : static_cast<const uint8_t*>(a.K)), "r"(p ? 16 : 0)
-                       : "memory");
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      };
-      for (int i = 0; ok && i <= 2 * T; ++i) {  // keys of tile 0, values of tile 0, ...
-        if (i < 2 * T) {
-          if (!(i & 1)) advance(i >> 1);
-          ok = free_slot(i >> 1, i & 1);
-          if (!ok) break;
-          copy(i >> 1, i & 1);
-        }
-        if (i == 0) continue;
-        if (i < 2 * T) asm volatile("cp.async.wait_group 1;" ::: "memory");
-        else asm volatile("cp.async.wait_group 0;" ::: "memory");
-        done((i - 1) >> 1, (i - 1) & 1);
+      uint64_t* bar;
+      uint8_t* dst;
+      if (CODES) {
+        ok = i < C::NI || wait_warp(&sm.i_empty[i % (C::NI + !CODES)],
+                                    ((i / (C::NI + !CODES)) - 1) & 1, abort_flag, err);
+        bar = &sm.i_full[i % (C::NI + !CODES)];
+        dst = sm.item[i % (C::NI + !CODES)];
+      } else {
+        const int N = values ? NV : NK, s = t % N;
+        ok = t < N || wait_warp(values ? &sm.v_empty[s] : &sm.k_empty[s], ((t / N) - 1) & 1,
+                                abort_flag, err);
+        bar = values ? &sm.v_full[s] : &sm.k_full[s];
+        dst = sm.kv[values ? NK + s : s][0];
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!ok) break;
+      if (CODES && !values) {
+        const int n = t * kChunks + (lane & (kChunks - 1));
+        const float ks = __shfl_sync(0xffffffffu, cur.ks, n & 31);
+        const float vs = __shfl_sync(0xffffffffu, cur.vs, n & 31);
+        if (lane < kChunks)
+          sm.scale[t % C::NS][lane] = make_float4(ks, __log2f(vs), 1.f / vs, 0.f);
+        __syncwarp();
+      }
+      if (lane == 0) mbar_expect_tx(bar, CODES ? BN * DH : NH * HT);
+      const CUtensorMap* map = values ? &mV : &mK;
+      for (int x = 0; x < boxes; ++x) {
+        const int n = t * kChunks + per * x, slab = __shfl_sync(0xffffffffu, cur.slab, n & 31);
+        const int y = ((tb + t) * BN + box * x) & (a.page.T - 1);
+        if (lane == 0) {
+          for (int h = 0; h < (CODES ? 1 : NH); ++h)
+            tma_load_3d(dst + h * HT + box * x * (CODES ? DH : 128), map, bar, 64 * h, y, slab);
+        }
+      }
+      started = i + 1;
+    }
+    if (lane == 0) {  // what is under way has to land before the block ends
+      constexpr int kRing = CODES ? C::NI : 2 * (NK < NV ? NV : NK);
+      for (int i = started > kRing ? started - kRing : 0; i < started; ++i) {
+        const int t = i >> 1, N = i & 1 ? NV : NK;
+        if (CODES) drain_wait(&sm.i_full[i % (C::NI + !CODES)], (i / (C::NI + !CODES)) & 1);
+        else if (t + N >= (started + (i & 1 ? 0 : 1)) / 2)
+          drain_wait(i & 1 ? &sm.v_full[t % N] : &sm.k_full[t % N], (t / N) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (CODES && warp >= 8) {
+    const int tid = threadIdx.x - 256;
+    const Feed<DH> f(tid);
+    constexpr int kRuns = BN / Feed<DH>::kStep, kStep = Feed<DH>::kStep;
+    static_assert(kStep % 16 == 0, "a thread's runs have one place in the swizzles");
+    const uint32_t c = (16 * f.col % 64) / 8, line = (16 * f.col / 64) * HT + f.row0 * 128;
+    const uint32_t at0 = line + ((c ^ (f.row0 & 7)) << 4);
+    const uint32_t at1 = line + (((c + 1) ^ (f.row0 & 7)) << 4);
+    const uint32_t from =
+        f.row0 * DH + ((f.col ^ (DH == 128 ? f.row0 & 7 : (f.row0 >> 1) & 3)) << 4);
+    bool ok = true;
+    for (int i = 0; ok && i < 2 * T; ++i) {
+      const int t = i >> 1, it = i % (C::NI + !CODES);
+      const bool values = i & 1;
+      const int N = values ? NV : NK, s = t % N;
+      ok = wait_warp(&sm.i_full[it], (i / (C::NI + !CODES)) & 1, abort_flag, err) &&
+           (t < N || wait_warp(values ? &sm.v_empty[s] : &sm.k_empty[s], ((t / N) - 1) & 1,
+                               abort_flag, err));
+      if (!ok) break;
+      const uint32_t src = smem_u32(sm.item[it]) + from;
+      const uint32_t dst = smem_u32(sm.kv[values ? NK + s : s][0]);
+      uint32_t w[kRuns][4];
+#pragma unroll
+      for (int u = 0; u < kRuns; ++u)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[u][0]), "=r"(w[u][1]), "=r"(w[u][2]), "=r"(w[u][3])
+                     : "r"(src + u * kStep * DH)
+                     : "memory");
+      // What no row of the block sees may be anything: zeros, which weights of 0 meet.
+      const int j0 = (tb + t) * BN;
+      if (j0 < hull.lo || j0 + BN > hull.hi) {
+#pragma unroll
+        for (int u = 0; u < kRuns; ++u) {
+          const int j = j0 + f.row0 + kStep * u;
+          if (j < hull.lo || j >= hull.hi) w[u][0] = w[u][1] = w[u][2] = w[u][3] = 0u;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kRuns; ++u) {
+        uint32_t h[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          h[2 * q] = codes_to_half2(static_cast<uint16_t>(w[u][q]));
+          h[2 * q + 1] = codes_to_half2(static_cast<uint16_t>(w[u][q] >> 16));
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + at0 + u * kStep * 128),
+                     "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                     : "memory");
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + at1 + u * kStep * 128),
+                     "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
+                     : "memory");
+      }
+      fence_proxy_async_smem();
+      warp_arrive(values ? &sm.v_full[s] : &sm.k_full[s]);
+      if (lane == 0) mbar_arrive(&sm.i_empty[it]);
     }
   } else {
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
@@ -477,6 +487,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float grow = CODES ? 1.f / sm.shrink[(MT == 2 ? BM * wg : 0) + r] : 1.f;
     const PagedScore<CODES, CAP, BIAS> score(a, gr.slope2, grow);
     const bool any_row = row0 + (MT == 2 ? BM * wg : 0) + quad * 32 < rows;
+    // Values that no row of the block sees meet P~ = 0: make them 0 too (codes are
+    // already).
+    auto clear_hidden = [&](int t, int col0) {
+      if (CODES || (col0 >= hull.lo && col0 + BN <= hull.hi)) return true;
+      if (!wait_warp(&sm.v_full[t % NV], (t / NV) & 1, abort_flag, err)) return false;
+      if (r < BN && (col0 + r < hull.lo || col0 + r >= hull.hi))
+        zero_row<NH, HT>(sm.kv[NK + t % NV], r);
+      fence_proxy_async_smem();
+      return true;
+    };
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     int n = 0;  // units of this warpgroup
@@ -490,11 +510,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float dist = BIAS ? static_cast<float>(col0 - gr.v.pos) : 0.f;
       const float4* chunk = sm.scale[t % C::NS];
       if (!any_row) {
+        ok = clear_hidden(t, col0);
+        if (!ok) break;
         warp_arrive(&sm.op_ready[u % NBUF]);
         continue;
       }
-      // Two groups of 64 columns: the second is read twice, so that one group is held in
-      // registers at a time, and P~ of columns 16 c .. goes to columns 8 c .., onto scores
+      // Groups of 64 columns; of two the second is read twice, so that one is held in
+      // registers at a time.  P~ of columns 16 c .. goes to columns 8 c .., onto scores
       // already used.
       uint32_t s[4][16];
       auto load = [&](int c) {
@@ -508,8 +530,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return masked ? score.template largest<true>(s, chunk + c / 16, col0 + c, lo, hi, dist + c)
                       : score.template largest<false>(s, chunk + c / 16, col0 + c, lo, hi, dist + c);
       };
-      load(64);
-      float mt = max_of(64);
+      float mt = -INFINITY;
+      if (BN == 128) {
+        load(64);
+        mt = max_of(64);
+      }
       load(0);
       mt = fmaxf(mt, max_of(0));
       const bool raise = mt > m + kRescale;
@@ -551,6 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           score.template weights<false>(s, sca, col0 + c, lo, hi, dist + c, base, l, sc + c / 2);
       }
+      ok = clear_hidden(t, col0);
+      if (!ok) break;
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(&sm.op_ready[u % NBUF]);
@@ -637,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == C::kMma) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tbase, 512);
@@ -646,15 +673,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int DH, int MT, bool CODES, bool CAP, bool BIAS>
 cudaError_t launch(const PagedAttnArgs& a, int splits) {
-  constexpr size_t smem = sizeof(Smem<DH, MT>) + 1024;
+  constexpr size_t smem = sizeof(Smem<DH, MT, CODES>) + 1024;
   static_assert(smem <= 232448, "shared memory");
   const auto kernel = tc_paged_kernel<DH, MT, CODES, CAP, BIAS>;
-  const cudaError_t e = tc_set_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
+  CUtensorMap mk, mv;
+  const int slabs = a.page.P * a.Hkv, box = a.page.T < Cfg<DH, MT, CODES>::BN
+                                               ? a.page.T : Cfg<DH, MT, CODES>::BN;
+  cudaError_t e = tc_map(&mk, a.K, slabs, a.page.T, box, DH, CODES);
+  if (e == cudaSuccess) e = tc_map(&mv, a.V, slabs, a.page.T, box, DH, CODES);
+  if (e == cudaSuccess)
+    e = tc_set_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int rows = a.H / a.Hkv * a.Nq, blocks = (rows + MT * BM - 1) / (MT * BM);
   const long long grid = static_cast<long long>(blocks) * splits * a.B * a.Hkv;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  kernel<<<static_cast<unsigned>(grid), kThreads, smem, a.stream>>>(a, blocks, splits);
+  kernel<<<static_cast<unsigned>(grid), Cfg<DH, MT, CODES>::kThreads, smem, a.stream>>>(
+      mk, mv, a, blocks, splits);
   return cudaGetLastError();
 }
 

@@ -37,7 +37,7 @@ def attention(lib, p, tau=0.1, cap=0.0, ws=BIG, B=1, H=2, Hkv=1, Nq=8, P=99, T=1
 
 BAD_PAGES = [dict(P=0), dict(T=0), dict(T=-16), dict(M=0), dict(d=0), dict(B=0), dict(Hkv=0), dict(dtype=2), dict(dtype=5), dict(cache=0),
              dict(cache=3), dict(dtype=0, cache=1)]
-TOO_LARGE = [dict(T=8), dict(T=48), dict(T=256), dict(T=2 ** 31 - 1), dict(M=2 ** 27), dict(d=129)]
+TOO_LARGE = [dict(P=2 ** 30, Hkv=2, H=2), dict(T=8), dict(T=48), dict(T=256), dict(T=2 ** 31 - 1), dict(M=2 ** 27), dict(d=129)]
 
 
 def test_append_refuses(lib):
@@ -69,6 +69,7 @@ def test_read_refuses(lib):
     for kw in BAD_PAGES + [dict(Nk=0), dict(Nk=65)]:
         assert read(lib, ptrs(8), **kw) == INVALID, kw
     for kw in TOO_LARGE + [dict(Hkv=70000), dict(B=70000)]:
+        kw = {k: v for k, v in kw.items() if k != "H"}
         assert read(lib, ptrs(8), **kw) == UNSUPPORTED, kw
     assert read(lib, ptrs(8), cache=1) == INVALID
     for i, j in ((6, 0), (7, 1), (7, 6), (6, 4)):
