@@ -46,16 +46,20 @@ struct Cfg {
   static constexpr int NK = !CODES ? (DH == 64 ? 5 : 4) : DH == 64 ? 4 : 3;
   static constexpr int NV = !CODES ? (DH == 64 || MT == 2 ? NK : 5) : DH == 64 || MT == 1 ? 3 : 2;
   static constexpr int NI = CODES ? 8 : 0;
-  // The scales of tile t are written when the codes of item 2 t - NI have been taken, so
-  // the scores of tile t - NI / 2 - NK are done, which were issued behind the products of
-  // a unit NBUF earlier: its readers are through.
-  static constexpr int NS = NI / 2 + NK + NBUF;
+  // Keys come so many tiles ahead of values, as the MMA warp asks for them.
+  static constexpr int kLead = (NBUF + MT - 1) / MT;
+  // The scales of tile t are written when the codes that lay in its slot have been taken,
+  // those of tile t - NI / 2 - kLead at least; so the scores of the tile NK before that are
+  // done, which were issued behind the products of a unit NBUF earlier: its readers are
+  // through.
+  static constexpr int NS = NI / 2 + kLead + NK + NBUF;
   // Elementwise warps 0 - 7, converters 8 - 11 (codes), loads, MMA.
   static constexpr int kLoad = CODES ? 12 : 8, kMma = kLoad + 1, kThreads = 32 * (kMma + 1);
   static_assert(2 * DH + NBUF * BN <= 512, "TMEM columns");
-  // Keys and values arrive alternately, and the MMA warp waits for keys NBUF units ahead
-  // of the values that it frees.
-  static_assert(NK >= 2 && MT * NV >= NBUF - (MT == 1 ? 1 : 0), "no wait of one ring for the other");
+  // In the order of Order the slot that a tile takes is free without any later one: keys
+  // of tile t need the scores of t - NK, values the products of t - NV, which need no keys
+  // beyond those of t - NV + kLead.
+  static_assert(NK >= 2 && NV >= 2, "rings");
 };
 
 template <int DH, int MT, bool CODES>
@@ -176,6 +180,18 @@ struct PagedScore {
     }
   }
 };
+
+// Tiles in the order in which they are loaded, converted and asked for: the keys of the
+// first kLead, then values of tile t and keys of tile t + kLead.
+template <int LEAD, typename F>
+__device__ __forceinline__ void in_order(int T, const F& item) {
+  bool ok = true;
+  int i = 0;
+  for (int x = 0; ok && x < T + LEAD; ++x) {
+    if (x >= LEAD) ok = item(i++, x - LEAD, true);
+    if (ok && x < T) ok = item(i++, x, false);
+  }
+}
 
 // The converters' 128 threads: run i of a thread is 16-byte run `col` of row row0 +
 // kStep i of an item.  Eight lanes read 16-byte runs of codes, and store runs of fp16, on
@@ -368,31 +384,35 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       return m;
     };
     constexpr int kAhead = 32 / kChunks;  // tiles that 32 chunks are
-    Meta cur = meta_of(lane), nxt = meta_of(32 + lane);
-    bool ok = true;
-    int started = 0;
-    for (int i = 0; ok && i < 2 * T; ++i) {  // keys of tile 0, values of tile 0, keys of 1 ..
-      const int t = i >> 1;
-      const bool values = i & 1;
+    static_assert(C::kLead <= kAhead, "values are at most one batch behind the keys");
+    Meta prv, cur = meta_of(lane), nxt = meta_of(32 + lane);
+    prv = cur;
+    int batch = 0;
+    int nk = 0, nv = 0, ni = 0;  // started
+    in_order<C::kLead>(T, [&](int i, int t, bool values) {
+      const int N = values ? NV : NK, s = t % N, it = i % (C::NI + !CODES);
       if (!values && t > 0 && t % kAhead == 0) {
+        prv = cur;
         cur = nxt;
         nxt = meta_of((t / kAhead + 1) * 32 + lane);
+        batch = t / kAhead;
       }
       uint64_t* bar;
       uint8_t* dst;
+      bool ok;
       if (CODES) {
-        ok = i < C::NI || wait_warp(&sm.i_empty[i % (C::NI + !CODES)],
-                                    ((i / (C::NI + !CODES)) - 1) & 1, abort_flag, err);
-        bar = &sm.i_full[i % (C::NI + !CODES)];
-        dst = sm.item[i % (C::NI + !CODES)];
+        ok = i < C::NI ||
+             wait_warp(&sm.i_empty[it], ((i / (C::NI + !CODES)) - 1) & 1, abort_flag, err);
+        bar = &sm.i_full[it];
+        dst = sm.item[it];
       } else {
-        const int N = values ? NV : NK, s = t % N;
         ok = t < N || wait_warp(values ? &sm.v_empty[s] : &sm.k_empty[s], ((t / N) - 1) & 1,
                                 abort_flag, err);
         bar = values ? &sm.v_full[s] : &sm.k_full[s];
         dst = sm.kv[values ? NK + s : s][0];
       }
-      if (!ok) break;
+      if (!ok) return false;
+      const bool now = t / kAhead == batch;  // values may be of the batch before
       if (CODES && !values) {
         const int n = t * kChunks + (lane & (kChunks - 1));
         const float ks = __shfl_sync(0xffffffffu, cur.ks, n & 31);
@@ -404,22 +424,26 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       if (lane == 0) mbar_expect_tx(bar, CODES ? BN * DH : NH * HT);
       const CUtensorMap* map = values ? &mV : &mK;
       for (int x = 0; x < boxes; ++x) {
-        const int n = t * kChunks + per * x, slab = __shfl_sync(0xffffffffu, cur.slab, n & 31);
+        const int n = t * kChunks + per * x;
+        const int slab = __shfl_sync(0xffffffffu, now ? cur.slab : prv.slab, n & 31);
         const int y = ((tb + t) * BN + box * x) & (a.page.T - 1);
         if (lane == 0) {
           for (int h = 0; h < (CODES ? 1 : NH); ++h)
             tma_load_3d(dst + h * HT + box * x * (CODES ? DH : 128), map, bar, 64 * h, y, slab);
         }
       }
-      started = i + 1;
-    }
+      ni = i + 1;
+      if (values) nv = t + 1;
+      else nk = t + 1;
+      return true;
+    });
     if (lane == 0) {  // what is under way has to land before the block ends
-      constexpr int kRing = CODES ? C::NI : 2 * (NK < NV ? NV : NK);
-      for (int i = started > kRing ? started - kRing : 0; i < started; ++i) {
-        const int t = i >> 1, N = i & 1 ? NV : NK;
-        if (CODES) drain_wait(&sm.i_full[i % (C::NI + !CODES)], (i / (C::NI + !CODES)) & 1);
-        else if (t + N >= (started + (i & 1 ? 0 : 1)) / 2)
-          drain_wait(i & 1 ? &sm.v_full[t % N] : &sm.k_full[t % N], (t / N) & 1);
+      if (CODES) {
+        for (int i = ni > C::NI ? ni - C::NI : 0; i < ni; ++i)
+          drain_wait(&sm.i_full[i % (C::NI + !CODES)], (i / (C::NI + !CODES)) & 1);
+      } else {
+        for (int t = nk > NK ? nk - NK : 0; t < nk; ++t) drain_wait(&sm.k_full[t % NK], (t / NK) & 1);
+        for (int t = nv > NV ? nv - NV : 0; t < nv; ++t) drain_wait(&sm.v_full[t % NV], (t / NV) & 1);
       }
     }
     __syncwarp();
@@ -433,15 +457,12 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
     const uint32_t at1 = line + (((c + 1) ^ (f.row0 & 7)) << 4);
     const uint32_t from =
         f.row0 * DH + ((f.col ^ (DH == 128 ? f.row0 & 7 : (f.row0 >> 1) & 3)) << 4);
-    bool ok = true;
-    for (int i = 0; ok && i < 2 * T; ++i) {
-      const int t = i >> 1, it = i % (C::NI + !CODES);
-      const bool values = i & 1;
-      const int N = values ? NV : NK, s = t % N;
-      ok = wait_warp(&sm.i_full[it], (i / (C::NI + !CODES)) & 1, abort_flag, err) &&
+    in_order<C::kLead>(T, [&](int i, int t, bool values) {
+      const int N = values ? NV : NK, s = t % N, it = i % (C::NI + !CODES);
+      const bool ok = wait_warp(&sm.i_full[it], (i / (C::NI + !CODES)) & 1, abort_flag, err) &&
            (t < N || wait_warp(values ? &sm.v_empty[s] : &sm.k_empty[s], ((t / N) - 1) & 1,
                                abort_flag, err));
-      if (!ok) break;
+      if (!ok) return false;
       const uint32_t src = smem_u32(sm.item[it]) + from;
       const uint32_t dst = smem_u32(sm.kv[values ? NK + s : s][0]);
       uint32_t w[kRuns][4];
@@ -478,7 +499,8 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       fence_proxy_async_smem();
       warp_arrive(values ? &sm.v_full[s] : &sm.k_full[s]);
       if (lane == 0) mbar_arrive(&sm.i_empty[it]);
-    }
+      return true;
+    });
   } else {
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t acc_own = tbase + lane_off + DH * wg;
