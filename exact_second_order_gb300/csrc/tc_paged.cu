@@ -53,8 +53,9 @@ struct Cfg {
   // done, which were issued behind the products of a unit NBUF earlier: its readers are
   // through.
   static constexpr int NS = NI / 2 + kLead + NK + NBUF;
-  // Elementwise warps 0 - 7, converters 8 - 11 (codes), loads, MMA.
-  static constexpr int kLoad = CODES ? 12 : 8, kMma = kLoad + 1, kThreads = 32 * (kMma + 1);
+  // Elementwise warps 0 - 7, converters (codes), loads, MMA.  With two converters the
+  // elementwise threads have 168 registers, with four 128.
+  static constexpr int kConv = CODES ? 2 : 0, kLoad = 8 + kConv, kMma = kLoad + 1, kThreads = 32 * (kMma + 1);
   static_assert(2 * DH + NBUF * BN <= 512, "TMEM columns");
   // In the order of Order the slot that a tile takes is free without any later one: keys
   // of tile t need the scores of t - NK, values the products of t - NV, which need no keys
@@ -69,7 +70,6 @@ struct Smem {
   alignas(1024) uint8_t kv[C::NK + C::NV][C::NH][C::HT];
   alignas(1024) uint8_t item[C::NI > 0 ? C::NI : 1][C::NI > 0 ? C::BN * DH : 16];  // codes
   float4 scale[C::NS][C::kChunks];  // s_K, log2 s_V, 1 / s_V of each chunk of a tile
-  float shrink[MT * BM];
   float part_m[2][BM], part_l[2][BM];
   int hull[8][4];  // of each elementwise warp's rows
   uint64_t k_full[C::NK], k_empty[C::NK], v_full[C::NV], v_empty[C::NV];
@@ -77,6 +77,7 @@ struct Smem {
   uint64_t sc_full[C::NBUF], op_ready[C::NBUF];
   uint64_t pv_done[2];  // of even and odd units
   uint64_t out_full;
+  uint64_t q_full, q_ready;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -193,27 +194,28 @@ __device__ __forceinline__ void in_order(int T, const F& item) {
   }
 }
 
-// The converters' 128 threads: run i of a thread is 16-byte run `col` of row row0 +
+// The converters' threads: run i of a thread is 16-byte run `col` of row row0 +
 // kStep i of an item.  Eight lanes read 16-byte runs of codes, and store runs of fp16, on
 // different banks: with rows of 128 bytes (two halves of fp16) four runs of one half of
 // rows r and r ^ 5, else four of two rows.
-template <int DH>
+template <int DH, int NT>
 struct Feed {
-  static constexpr int kPerRow = DH / 16, kStep = 128 / kPerRow;
+  static constexpr int kPerRow = DH / 16, kStep = NT / kPerRow;
   int col, row0;
   __device__ __forceinline__ explicit Feed(int tid) {
     col = tid & 3;
     row0 = tid >> 2;
     if (DH == 128) {
       col |= (tid >> 1) & 4;
-      row0 = ((tid >> 2 & 1) * 5) ^ ((tid >> 4 & 1) * 2) ^ ((tid >> 5 & 1) * 4) ^ ((tid >> 6 & 1) * 8);
+      row0 = ((tid >> 2 & 1) * 5) ^ ((tid >> 4 & 1) * 2) ^ ((tid >> 5 & 1) * 4) ^ (tid >> 6 << 3);
     }
   }
 };
 
 template <int DH, int MT, bool CODES, bool CAP, bool BIAS>
 __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
-    tc_paged_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
+    tc_paged_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+                    const __grid_constant__ CUtensorMap mV,
                     const __grid_constant__ PagedAttnArgs a, int blocks, int splits) {
   extern __shared__ uint8_t smem_raw[];
   using C = Cfg<DH, MT, CODES>;
@@ -234,16 +236,23 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
 
   if (splits > 1) release_next();
   if (threadIdx.x == 0) {
-    constexpr int kFull = CODES ? 4 : 1;
+    constexpr int kFull = CODES ? C::kConv : 1;
     for (int s = 0; s < NK; ++s) mbar_init(&sm.k_full[s], kFull), mbar_init(&sm.k_empty[s], 1);
     for (int s = 0; s < NV; ++s) mbar_init(&sm.v_full[s], kFull), mbar_init(&sm.v_empty[s], 1);
-    for (int s = 0; s < C::NI; ++s) mbar_init(&sm.i_full[s], 1), mbar_init(&sm.i_empty[s], 4);
+    for (int s = 0; s < C::NI; ++s) mbar_init(&sm.i_full[s], 1), mbar_init(&sm.i_empty[s], C::kConv);
     for (int s = 0; s < NBUF; ++s) mbar_init(&sm.sc_full[s], 1), mbar_init(&sm.op_ready[s], 4);
     mbar_init(&sm.pv_done[0], 1);
     mbar_init(&sm.pv_done[1], 1);
     mbar_init(&sm.out_full, 1);
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_ready, 8);
     sm.abort_flag = 0;
     fence_barrier_init();
+    // Q is under way while the ranges are read.
+    mbar_expect_tx(&sm.q_full, MT * NH * HALF_BLOCK);
+    for (int w = 0; w < MT; ++w)
+      for (int h = 0; h < NH; ++h)
+        tma_load_3d(sm.q[w][h], &mQ, &sm.q_full, 64 * h, row0 + BM * w, g);
   }
   if (warp == C::kMma) tmem_alloc(&sm.tmem_base, 512);
   const int wg = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
@@ -252,47 +261,6 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
   if (warp < 8) {
     gr = group_row(a, b, hkv, row, rows);
     warp_hull(gr.v, row < rows, lane, sm.hull[warp]);
-    // Q: half a warp takes a row at a time, 8 or 4 elements a lane.
-    constexpr int kE = DH / 16, kPass = MT * BM / 16;
-    const int c = lane & 15;
-    const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(a.Q) +
-                             (static_cast<size_t>(g) * rows + row0) * DH + c * kE;
-#pragma unroll 4
-    for (int p = 0; p < kPass; ++p) {
-      const int qr = 16 * p + 2 * warp + (lane >> 4);
-      uint32_t w[kE / 2];
-#pragma unroll
-      for (int k = 0; k < kE / 2; ++k) w[k] = 0u;
-      if (row0 + qr < rows) {
-        if (kE == 8) {
-          const uint4 v = *reinterpret_cast<const uint4*>(Q + static_cast<size_t>(qr) * DH);
-          w[0] = v.x, w[1] = v.y, w[kE / 2 - 2] = v.z, w[kE / 2 - 1] = v.w;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(Q + static_cast<size_t>(qr) * DH);
-          w[0] = v.x, w[1] = v.y;
-        }
-      }
-      if (CODES) {
-        float most = 0.f;
-#pragma unroll
-        for (int k = 0; k < kE / 2; ++k)
-          most = fmaxf(most, fmaxf(finite_abs(u2f(w[k] << 16)), finite_abs(u2f(w[k] & 0xFFFF0000u))));
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-        const float shrink = row_shrink(most);
-#pragma unroll
-        for (int k = 0; k < kE / 2; ++k)
-          w[k] = pack<true>(u2f(w[k] << 16) * shrink, u2f(w[k] & 0xFFFF0000u) * shrink);
-        if (c == 0) sm.shrink[qr] = shrink;
-      }
-      uint8_t* dst = sm.q[qr / BM][c * kE / 64] + (qr % BM) * 128;
-      const int off = (c * kE % 64) * 2;  // byte in the 128-byte row; 16-byte runs are swizzled
-      dst += (((off >> 4) ^ (qr & 7)) << 4) + (off & 15);
-      if (kE == 8)
-        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[kE / 2 - 2], w[kE / 2 - 1]);
-      else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-    }
-    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
@@ -338,17 +306,21 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       if (MT == 1 || (u & 1)) mma_commit(&sm.v_empty[s]);
     };
     if (elect_one()) {
-      bool ok = true;
+      bool ok = wait_one(CODES ? &sm.q_ready : &sm.q_full, 0, abort_flag, err);
+      tc_fence_after();
       auto scores = [&](int u) {
-        const int t = tile(u);
-        ok = wait_one(&sm.k_full[t % NK], (t / NK) & 1, abort_flag, err);
-        tc_fence_after();
+        const int t = tile(u);  // MT = 2: the second unit of a tile finds it there
+        if (MT == 1 || !(u & 1)) {
+          ok = wait_one(&sm.k_full[t % NK], (t / NK) & 1, abort_flag, err);
+          tc_fence_after();
+        }
         if (ok) issue_scores(u);
       };
       for (int u = 0; ok && u < NBUF && u < U; ++u) scores(u);
       for (int u = 0; ok && u < U; ++u) {
         const int t = tile(u);
-        ok = wait_one(&sm.v_full[t % NV], (t / NV) & 1, abort_flag, err) &&
+        ok = ((MT == 2 && (u & 1)) ||
+              wait_one(&sm.v_full[t % NV], (t / NV) & 1, abort_flag, err)) &&
              wait_one(&sm.op_ready[u % NBUF], (u / NBUF) & 1, abort_flag, err);
         if (!ok) break;
         tc_fence_after();
@@ -438,6 +410,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       return true;
     });
     if (lane == 0) {  // what is under way has to land before the block ends
+      drain_wait(&sm.q_full, 0);
       if (CODES) {
         for (int i = ni > C::NI ? ni - C::NI : 0; i < ni; ++i)
           drain_wait(&sm.i_full[i % (C::NI + !CODES)], (i / (C::NI + !CODES)) & 1);
@@ -449,9 +422,10 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
     __syncwarp();
   } else if (CODES && warp >= 8) {
     const int tid = threadIdx.x - 256;
-    const Feed<DH> f(tid);
-    constexpr int kRuns = BN / Feed<DH>::kStep, kStep = Feed<DH>::kStep;
-    static_assert(kStep % 16 == 0, "a thread's runs have one place in the swizzles");
+    using F = Feed<DH, 32 * C::kConv + !CODES * 128>;
+    const F f(tid);
+    constexpr int kRuns = BN / F::kStep, kStep = F::kStep;
+    static_assert(kStep % 8 == 0, "a thread's runs have one place in the swizzles");
     const uint32_t c = (16 * f.col % 64) / 8, line = (16 * f.col / 64) * HT + f.row0 * 128;
     const uint32_t at0 = line + ((c ^ (f.row0 & 7)) << 4);
     const uint32_t at1 = line + (((c + 1) ^ (f.row0 & 7)) << 4);
@@ -506,7 +480,40 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
     const uint32_t acc_own = tbase + lane_off + DH * wg;
     const int lo = gr.v.lo, hi = gr.v.hi;
     const Hull own = MT == 2 ? join_hulls(sm.hull + 4 * wg, 4) : hull;
-    const float grow = CODES ? 1.f / sm.shrink[(MT == 2 ? BM * wg : 0) + r] : 1.f;
+    bool ok = wait_warp(&sm.q_full, 0, abort_flag, err);
+    float grow = 1.f;
+    if (CODES) {
+      // Q to fp16 in place, this thread's row (MT = 1: of two threads each writes half of
+      // the runs, when both have seen the row).
+      uint8_t* q = sm.q[MT == 2 ? wg : 0][0] + r * 128;
+      constexpr int kRuns = DH / 8;
+      auto run = [&](int k) {
+        return reinterpret_cast<uint4*>(q + (k / 8) * HALF_BLOCK + (((k % 8) ^ (r & 7)) << 4));
+      };
+      float most = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < kRuns; ++k) {
+        const uint4 v = *run(k);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          most = fmaxf(most, fmaxf(finite_abs(u2f(w[e] << 16)), finite_abs(u2f(w[e] & 0xFFFF0000u))));
+      }
+      const float shrink = row_shrink(most);
+      grow = 1.f / shrink;
+      if (MT == 1) named_bar_sync(1, 256);
+#pragma unroll 4
+      for (int k = MT == 1 ? wg * kRuns / 2 : 0; k < (MT == 1 ? (wg + 1) * kRuns / 2 : kRuns); ++k) {
+        const uint4 v = *run(k);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = pack<true>(u2f(w[e] << 16) * shrink, u2f(w[e] & 0xFFFF0000u) * shrink);
+        *run(k) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&sm.q_ready);
+    }
     const PagedScore<CODES, CAP, BIAS> score(a, gr.slope2, grow);
     const bool any_row = row0 + (MT == 2 ? BM * wg : 0) + quad * 32 < rows;
     // Values that no row of the block sees meet P~ = 0: make them 0 too (codes are
@@ -520,11 +527,10 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       return true;
     };
     float m = -INFINITY, l = 0.f;
-    bool ok = true;
     int n = 0;  // units of this warpgroup
     for (int u = wg; u < U; u += 2, ++n) {
       const int t = MT == 2 ? u >> 1 : u, col0 = (tb + t) * BN;
-      ok = wait_warp(&sm.sc_full[u % NBUF], (u / NBUF) & 1, abort_flag, err);
+      ok = ok && wait_warp(&sm.sc_full[u % NBUF], (u / NBUF) & 1, abort_flag, err);
       if (!ok) break;
       tc_fence_after();
       const uint32_t sc = tbase + lane_off + kScore + BN * (u % NBUF);
@@ -698,19 +704,20 @@ cudaError_t launch(const PagedAttnArgs& a, int splits) {
   constexpr size_t smem = sizeof(Smem<DH, MT, CODES>) + 1024;
   static_assert(smem <= 232448, "shared memory");
   const auto kernel = tc_paged_kernel<DH, MT, CODES, CAP, BIAS>;
-  CUtensorMap mk, mv;
+  CUtensorMap mq, mk, mv;
+  const int rows = a.H / a.Hkv * a.Nq, blocks = (rows + MT * BM - 1) / (MT * BM);
   const int slabs = a.page.P * a.Hkv, box = a.page.T < Cfg<DH, MT, CODES>::BN
                                                ? a.page.T : Cfg<DH, MT, CODES>::BN;
-  cudaError_t e = tc_map(&mk, a.K, slabs, a.page.T, box, DH, CODES);
+  cudaError_t e = tc_map_bf16(&mq, a.Q, a.B * a.Hkv, rows, BM, DH);
+  if (e == cudaSuccess) e = tc_map(&mk, a.K, slabs, a.page.T, box, DH, CODES);
   if (e == cudaSuccess) e = tc_map(&mv, a.V, slabs, a.page.T, box, DH, CODES);
   if (e == cudaSuccess)
     e = tc_set_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const int rows = a.H / a.Hkv * a.Nq, blocks = (rows + MT * BM - 1) / (MT * BM);
   const long long grid = static_cast<long long>(blocks) * splits * a.B * a.Hkv;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
   kernel<<<static_cast<unsigned>(grid), Cfg<DH, MT, CODES>::kThreads, smem, a.stream>>>(
-      mk, mv, a, blocks, splits);
+      mq, mk, mv, a, blocks, splits);
   return cudaGetLastError();
 }
 
