@@ -154,11 +154,14 @@ __device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s) 
   y = v;
 }
 
-template <typename T, bool CODES, int E8, bool VEC, int TG>
-__global__ void __launch_bounds__(kThreads, VEC && sizeof(T) == 2 ? 2 : 1)
+// KIND 0: any head; 1: vec_ok; 2: and every lane has whole eights of pairs apart that
+// turn (halves, R = d, d = 64 or 128), so nothing is asked lane by lane.
+template <typename T, bool CODES, int E8, int KIND, int TG>
+__global__ void __launch_bounds__(kThreads, KIND > 0 && sizeof(T) == 2 ? 2 : 1)
     append_kernel(const __grid_constant__ AppendArgs a, int TS, int pages) {
   extern __shared__ __align__(16) unsigned long long steps[];
   constexpr int HB = kInFlight / (E8 * TG);
+  constexpr bool VEC = KIND > 0, WHOLE = KIND == 2;
   __shared__ float s_most[2][kWarps * HB];
   const PageArgs& pg = a.page;
   const int b = blockIdx.x / pages, s = blockIdx.x % pages;
@@ -189,6 +192,14 @@ __global__ void __launch_bounds__(kThreads, VEC && sizeof(T) == 2 ? 2 : 1)
                (static_cast<size_t>(b) * a.N + nb) * heads * static_cast<size_t>(a.d);
   T* Q = static_cast<T*>(a.Q) + (static_cast<size_t>(b) * a.H * a.N + nb) * a.d;
   const size_t q_head = static_cast<size_t>(a.N) * a.d, q_token = static_cast<size_t>(heads) * a.d;
+  const T* x_of[TG];
+  T* q_of[TG];
+#pragma unroll
+  for (int g = 0; g < TG; ++g) {
+    const int n = min(ts + TS * g, ne - nb - 1);
+    x_of[g] = X + n * q_token;
+    q_of[g] = Q + n * a.d;
+  }
   Eight<T, VEC> x[HB][TG][E8];
   auto load = [&](int base) {
 #pragma unroll
@@ -197,10 +208,10 @@ __global__ void __launch_bounds__(kThreads, VEC && sizeof(T) == 2 ? 2 : 1)
       for (int g = 0; g < TG; ++g) {
         const int row = base + hs + HS * k, n = ts + TS * g;
         const bool there = row < r1 && nb + n < ne;
-        const T* p = X + (there ? n * q_token + row * a.d : 0);
+        const T* p = x_of[g] + (row < r1 ? row : 0) * a.d;
 #pragma unroll
         for (int e = 0; e < E8; ++e) {
-          if (there && own[e].live) x[k][g][e].load(p, shape, own[e]);
+          if (there && (WHOLE || own[e].live)) x[k][g][e].load(p, shape, own[e]);
           else x[k][g][e].zero();
         }
       }
@@ -244,16 +255,16 @@ __global__ void __launch_bounds__(kThreads, VEC && sizeof(T) == 2 ? 2 : 1)
       u = make_float4(u.x * r, u.y * r, u.z * r, u.w * r);
       v = make_float4(v.x * r, v.y * r, v.z * r, v.w * r);
       const float* gain = row < a.H ? a.wq : a.wk;
-      if (gain && o.live) {
+      if (gain && (WHOLE || o.live)) {
         Eight<float, VEC> w;
         w.load(gain, shape, o);
         u = make_float4(u.x * w.a.x, u.y * w.a.y, u.z * w.a.z, u.w * w.a.w);
         v = make_float4(v.x * w.b.x, v.y * w.b.y, v.z * w.b.z, v.w * w.b.w);
       }
     }
-    if (o.turning <= 0) return;
+    if (!WHOLE && o.turning <= 0) return;
     const float4 co = turns[2 * at * kThreads], si = turns[(2 * at + 1) * kThreads];
-    if (o.turning == 4 && o.apart) {
+    if (WHOLE || (o.turning == 4 && o.apart)) {
       turn_pair(u.x, v.x, co.x, si.x), turn_pair(u.y, v.y, co.y, si.y);
       turn_pair(u.z, v.z, co.z, si.z), turn_pair(u.w, v.w, co.w, si.w);
     } else if (o.apart) {  // a pair that does not turn is left alone: 0 times an infinity
@@ -291,12 +302,12 @@ __global__ void __launch_bounds__(kThreads, VEC && sizeof(T) == 2 ? 2 : 1)
         for (int g = 0; g < TG; ++g) {
           const int n = ts + TS * g;
           if (nb + n >= ne) continue;
-          T* out = Q + row * q_head + n * a.d;
+          T* out = q_of[g] + row * q_head;
 #pragma unroll
           for (int e = 0; e < E8; ++e) {
             float4 u, v;
             finish(x[k][g][e], own[e], row, g * E8 + e, r[k][g], u, v);
-            if (own[e].live) store_eight<T, VEC>(out, shape, own[e], u, v);
+            if (WHOLE || own[e].live) store_eight<T, VEC>(out, shape, own[e], u, v);
           }
         }
         continue;
@@ -311,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, VEC && sizeof(T) == 2 ? 2 : 1)
         for (int e = 0; e < E8; ++e) {
           float4 u, v;
           finish(x[k][g][e], own[e], row, g * E8 + e, r[k][g], u, v);
-          if (!own[e].live) continue;
+          if (!WHOLE && !own[e].live) continue;
           if (!CODES) {
             store_eight<T, VEC>(out, shape, own[e], u, v);
             continue;
@@ -365,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, VEC && sizeof(T) == 2 ? 2 : 1)
         for (int e = 0; e < E8; ++e) {
           float4 u, v;
           finish(x[k][g][e], own[e], row, g * E8 + e, r[k][g], u, v);
-          if (own[e].live)
+          if (WHOLE || own[e].live)
             store_codes<VEC>(pool + (first + n) * a.d, shape, own[e], u, v, inv);
         }
       }
@@ -379,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, VEC && sizeof(T) == 2 ? 2 : 1)
   }
 }
 
-template <typename T, bool CODES, int E8, bool VEC, int TG>
+template <typename T, bool CODES, int E8, int KIND, int TG>
 cudaError_t append(const AppendArgs& a, int TS) {
   const long long pages = (static_cast<long long>(a.N) + 2LL * a.page.T - 2) >> a.page.shift;
   const long long blocks = pages * a.B;
@@ -393,7 +404,7 @@ cudaError_t append(const AppendArgs& a, int TS) {
   // The frequencies' steps and the lanes' angles.
   const size_t smem = static_cast<size_t>((a.R / 2 * a.axes + 1) & ~1) * 8 +
                       kThreads * TG * E8 * 32;
-  const auto kernel = append_kernel<T, CODES, E8, VEC, TG>;
+  const auto kernel = append_kernel<T, CODES, E8, KIND, TG>;
   if (smem > 48 * 1024) {
     const cudaError_t e = tc_set_smem(reinterpret_cast<const void*>(kernel), 80 * 1024);
     if (e != cudaSuccess) return e;
@@ -410,15 +421,18 @@ cudaError_t append(const AppendArgs& a) {
   int window = 1;
   while (window < a.page.T && window < a.N) window *= 2;
   const int half = window < 2 ? 1 : window / 2;
-  const bool vec = vec_ok(a);
+  const bool vec = vec_ok(a), whole = !a.interleaved && a.R == a.d && (a.d == 64 || a.d == 128);
   if (!a.bf16)
-    return vec ? append<float, CODES, 2, true, 2>(a, half) : append<float, CODES, 2, false, 2>(a, half);
-  if (!vec) return append<__nv_bfloat16, CODES, 2, false, 2>(a, half);
+    return vec ? append<float, CODES, 2, 1, 2>(a, half) : append<float, CODES, 2, 0, 2>(a, half);
+  using B = __nv_bfloat16;
+  if (!vec) return append<B, CODES, 2, 0, 2>(a, half);
+  if (a.d <= 64 && whole)
+    return window <= 64 ? append<B, CODES, 1, 2, 1>(a, window) : append<B, CODES, 1, 2, 2>(a, half);
+  if (whole)
+    return window <= 64 ? append<B, CODES, 2, 2, 1>(a, window) : append<B, CODES, 2, 2, 2>(a, half);
   if (a.d <= 64)
-    return window <= 64 ? append<__nv_bfloat16, CODES, 1, true, 1>(a, window)
-                        : append<__nv_bfloat16, CODES, 1, true, 2>(a, half);
-  return window <= 64 ? append<__nv_bfloat16, CODES, 2, true, 1>(a, window)
-                      : append<__nv_bfloat16, CODES, 2, true, 2>(a, half);
+    return window <= 64 ? append<B, CODES, 1, 1, 1>(a, window) : append<B, CODES, 1, 1, 2>(a, half);
+  return window <= 64 ? append<B, CODES, 2, 1, 1>(a, window) : append<B, CODES, 2, 1, 2>(a, half);
 }
 
 // ---------------------------------------------------------------------------
