@@ -52,7 +52,7 @@ struct Tok {
   static constexpr bool kQInSmem = NT == 4;
   static constexpr int kQBytes = kQInSmem ? NT * kK * 32 * 8 : 0;
   static constexpr int kSmem = NW * kRing + kQBytes;
-  static_assert(NT * 8 * (kPitch + 2) * 4 <= kRing, "a warp's part fits in its ring");
+  static_assert(NT * 8 * (kPitch + 4) * 4 <= kRing, "a warp's part fits in its ring");
   static_assert(kStages >= 3 && kStages < 32, "ring");
 };
 
@@ -126,14 +126,15 @@ __device__ __forceinline__ float tanh_score(float x) {
 
 template <int DH, bool CODES, int NT, bool PLAIN>
 __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
-    token_kernel(const __grid_constant__ PagedAttnArgs a, int splits) {
+    token_kernel(const __grid_constant__ PagedAttnArgs a, int cluster, int partials) {
   using C = Tok<DH, CODES, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   const PageArgs& pg = a.page;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int splits = cluster * partials;
   const int group = blockIdx.x / splits, split = blockIdx.x % splits;
   const int b = group / a.Hkv, hkv = group % a.Hkv, rows = a.H / a.Hkv * a.Nq;
-  if (splits > 1) release_next();
+  if (partials > 1) release_next();
 
   // What each row sees (lane r: row r), and their hull; the same in every warp.
   const GroupRow own = group_row(a, b, hkv, lane, rows);
@@ -470,36 +471,84 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
       }
     }
   __syncthreads();
-  const size_t all = static_cast<size_t>(a.B) * a.H * a.Nq;
-  const size_t base = static_cast<size_t>(group) * rows;
-  const Partials out = partials(a.workspace, all, DH, splits);
-  for (int x = threadIdx.x; x < rows * (DH / 4); x += 32 * NW) {
-    const int row = x / (DH / 4), c = 4 * (x % (DH / 4));
-    const float* w0 = reinterpret_cast<const float*>(smem);
-    constexpr int kStep = C::kRing / 4;
-    float m = -INFINITY;
+  // Four columns of a row a thread: the warps' parts with their maximum as reference.
+  constexpr int kQuads = DH / 4, kMine = (kRowsPadded * kQuads + 32 * NW - 1) / (32 * NW);
+  float4 o[kMine];
+  float m[kMine], sum[kMine];
+  const float* w0 = reinterpret_cast<const float*>(smem);
 #pragma unroll
-    for (int w = 0; w < NW; ++w) m = fmaxf(m, w0[w * kStep + kRL + row]);
-    float sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < kMine; ++i) {
+    const int x = threadIdx.x + 32 * NW * i, row = x / kQuads, c = 4 * (x % kQuads);
+    o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    m[i] = -INFINITY;
+    sum[i] = 0.f;
+    if (row >= rows) continue;
+    constexpr int kStep = C::kRing / 4;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) m[i] = fmaxf(m[i], w0[w * kStep + kRL + row]);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       const float* p = w0 + w * kStep;
-      const float r = p[kRL + row], f = r == -INFINITY ? 0.f : ex2_approx(r - m);
+      const float r = p[kRL + row], f = r == -INFINITY ? 0.f : ex2_approx(r - m[i]);
       const float4 v = *reinterpret_cast<const float4*>(p + row * C::kPitch + c);
-      sum = fmaf(f, p[kRL + kRowsPadded + row], sum);
-      o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
-      o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+      sum[i] = fmaf(f, p[kRL + kRowsPadded + row], sum[i]);
+      o[i].x = fmaf(f, v.x, o[i].x), o[i].y = fmaf(f, v.y, o[i].y);
+      o[i].z = fmaf(f, v.z, o[i].z), o[i].w = fmaf(f, v.w, o[i].w);
     }
-    if (splits > 1) {
-      const size_t at = split * all + base + row;
-      *reinterpret_cast<float4*>(out.o + at * DH + c) = o;
-      if (c == 0) out.ml[at] = make_float2(m, sum);
+  }
+  // The same over the blocks of a cluster: block `rank` takes every cluster-th row.
+  const int rank = split % cluster;
+  if (cluster > 1) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int x = threadIdx.x + 32 * NW * i, row = x / kQuads, c = 4 * (x % kQuads);
+      if (row >= rows) continue;
+      float* p = reinterpret_cast<float*>(smem);
+      *reinterpret_cast<float4*>(p + row * C::kPitch + c) = o[i];
+      if (c == 0) *reinterpret_cast<float4*>(p + kRL + 4 * row) = make_float4(m[i], sum[i], 0.f, 0.f);
+    }
+    tc::cluster_sync();
+    const uint32_t here = smem_u32(smem);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int x = threadIdx.x + 32 * NW * i, row = x / kQuads, c = 4 * (x % kQuads);
+      if (row >= rows || row % cluster != rank) continue;
+      m[i] = -INFINITY;
+      sum[i] = 0.f;
+      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int q = 0; q < cluster; ++q)
+        m[i] = fmaxf(m[i], tc::ld_shared_cluster_f4(
+                               tc::mapa_shared(here + (kRL + 4 * row) * 4, q)).x);
+      for (int q = 0; q < cluster; ++q) {
+        const float4 ml = tc::ld_shared_cluster_f4(tc::mapa_shared(here + (kRL + 4 * row) * 4, q));
+        const float4 v =
+            tc::ld_shared_cluster_f4(tc::mapa_shared(here + (row * C::kPitch + c) * 4, q));
+        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m[i]);
+        sum[i] = fmaf(f, ml.y, sum[i]);
+        o[i].x = fmaf(f, v.x, o[i].x), o[i].y = fmaf(f, v.y, o[i].y);
+        o[i].z = fmaf(f, v.z, o[i].z), o[i].w = fmaf(f, v.w, o[i].w);
+      }
+    }
+    tc::cluster_sync();  // no block leaves while its memory is read
+  }
+  const size_t all = static_cast<size_t>(a.B) * a.H * a.Nq;
+  const size_t base = static_cast<size_t>(group) * rows;
+  const Partials out = attn::partials(a.workspace, all, DH, partials);
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int x = threadIdx.x + 32 * NW * i, row = x / kQuads, c = 4 * (x % kQuads);
+    if (row >= rows || row % cluster != rank) continue;
+    if (partials > 1) {
+      const size_t at = split / cluster * all + base + row;
+      *reinterpret_cast<float4*>(out.o + at * DH + c) = o[i];
+      if (c == 0) out.ml[at] = make_float2(m[i], sum[i]);
     } else {
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = sum[i] > 0.f ? 1.f / sum[i] : 0.f;
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + (base + row) * DH + c) =
-          make_uint2(tc::pack_bf16x2(o.x * inv, o.y * inv), tc::pack_bf16x2(o.z * inv, o.w * inv));
-      if (c == 0) a.L[base + row] = (m + __log2f(sum)) * kLn2;
+          make_uint2(tc::pack_bf16x2(o[i].x * inv, o[i].y * inv),
+                     tc::pack_bf16x2(o[i].z * inv, o[i].w * inv));
+      if (c == 0) a.L[base + row] = (m[i] + __log2f(sum[i])) * kLn2;
     }
   }
 }
@@ -509,46 +558,60 @@ bool token_supported(const PagedAttnArgs& a) {
          static_cast<long long>(a.H / a.Hkv) * a.Nq <= kMostRows;
 }
 
-int token_splits(const PagedAttnArgs& a) {
+// Blocks of an SM at a time (Tok::kTwo).
+int token_blocks_per_sm(const PagedAttnArgs& a) {
+  return a.H / a.Hkv * a.Nq <= 8 && (a.page.e4m3 || a.d == 64) ? 2 : 1;
+}
+
+// Runs that the keys are cut into, of 512 keys at least.
+struct TokenRuns {
+  int cluster;   // runs that meet in distributed shared memory
+  int partials;  // and so many of those are joined by a second launch
+};
+TokenRuns token_runs(const PagedAttnArgs& a) {
   const long long groups = static_cast<long long>(a.B) * a.Hkv;
-  const long long want = 6LL * kSMs / groups, most = a.Nk / 512;
-  const long long s = want < most ? want : most;
-  return s < 1 ? 1 : static_cast<int>(s);
+  const long long slots = static_cast<long long>(kSMs) * token_blocks_per_sm(a);
+  long long s = (2 * groups > slots ? 3 * slots : slots) / groups;
+  const long long most = a.Nk / 512;
+  s = s > most ? most : s;
+  if (s <= 1) return {1, 1};
+  if (s <= 8) return {static_cast<int>(s), 1};
+  return {8, static_cast<int>(s / 8)};
 }
 
 template <int DH, bool CODES, int NT, bool PLAIN>
-cudaError_t launch(const PagedAttnArgs& a, int splits) {
+cudaError_t launch(const PagedAttnArgs& a, const TokenRuns& runs) {
   using C = Tok<DH, CODES, NT>;
   const auto kernel = token_kernel<DH, CODES, NT, PLAIN>;
   cudaError_t e = tc_set_smem(reinterpret_cast<const void*>(kernel), C::kSmem);
   if (e != cudaSuccess) return e;
-  const long long grid = static_cast<long long>(a.B) * a.Hkv * splits;
+  const long long grid = static_cast<long long>(a.B) * a.Hkv * runs.cluster * runs.partials;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  kernel<<<static_cast<unsigned>(grid), 32 * NW, C::kSmem, a.stream>>>(a, splits);
-  return cudaGetLastError();
+  return launch_after(false, kernel, dim3(static_cast<unsigned>(grid)), 32 * NW, C::kSmem,
+                      runs.cluster, a.stream, a, runs.cluster, runs.partials);
 }
 
 template <int DH, bool CODES>
-cudaError_t launch(const PagedAttnArgs& a, int splits) {
+cudaError_t launch(const PagedAttnArgs& a, const TokenRuns& runs) {
   const int rows = a.H / a.Hkv * a.Nq;
   const bool plain = a.cap == 0.f && !a.slopes;
   if (rows <= 8)
-    return plain ? launch<DH, CODES, 1, true>(a, splits) : launch<DH, CODES, 1, false>(a, splits);
+    return plain ? launch<DH, CODES, 1, true>(a, runs) : launch<DH, CODES, 1, false>(a, runs);
   if (rows <= 16)
-    return plain ? launch<DH, CODES, 2, true>(a, splits) : launch<DH, CODES, 2, false>(a, splits);
-  return plain ? launch<DH, CODES, 4, true>(a, splits) : launch<DH, CODES, 4, false>(a, splits);
+    return plain ? launch<DH, CODES, 2, true>(a, runs) : launch<DH, CODES, 2, false>(a, runs);
+  return plain ? launch<DH, CODES, 4, true>(a, runs) : launch<DH, CODES, 4, false>(a, runs);
 }
 
 cudaError_t token_attn(const PagedAttnArgs& a) {
-  const int splits = token_splits(a);
+  const TokenRuns runs = token_runs(a);
   cudaError_t e;
-  if (a.d == 64) e = a.page.e4m3 ? launch<64, true>(a, splits) : launch<64, false>(a, splits);
-  else e = a.page.e4m3 ? launch<128, true>(a, splits) : launch<128, false>(a, splits);
-  return e == cudaSuccess && splits > 1 ? attn_join(a, splits) : e;
+  if (a.d == 64) e = a.page.e4m3 ? launch<64, true>(a, runs) : launch<64, false>(a, runs);
+  else e = a.page.e4m3 ? launch<128, true>(a, runs) : launch<128, false>(a, runs);
+  return e == cudaSuccess && runs.partials > 1 ? attn_join(a, runs.partials) : e;
 }
 
 int splits_of(const PagedAttnArgs& a) {
-  return token_supported(a) ? token_splits(a)
+  return token_supported(a) ? token_runs(a).partials
          : tc_paged_supported(a) ? tc_paged_splits(a) : simt_splits(a);
 }
 
