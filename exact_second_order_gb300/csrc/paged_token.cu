@@ -11,14 +11,15 @@
 //
 // The keys' bytes bound it (2 d bytes a key and head for e4m3), not the products: a
 // warp holds all rows and streams pages alone, 16 tokens at a time, through a ring of
-// its own in shared memory (16-byte asynchronous copies, no block-wide barrier before
-// the end).  With tokens along M and rows along N = 8 a product (mma.sync m16n8k16)
+// its own in shared memory (TMA boxes that one lane asks for, no block-wide barrier
+// between the first and the end).  With tokens along M and rows along N = 8 a product (mma.sync m16n8k16)
 // wastes nothing on rows that are not there: tcgen05 would want 64 rows or more, and
 // its operands in shared memory in 16 bits, twice the bytes that arrive.  Along the
 // contracted side any order will do, so a lane takes whole 16-byte runs of a key's
-// code (four steps of 4 elements) and of a value's (its own head columns of tokens
-// 2 t, 2 t + 1, 2 t + 8, 2 t + 9, paired by byte permutes), and a chunk's place in its
-// row is swizzled so that both reads are without bank conflicts.  The weights go from
+// code (four steps of 4 elements) and of a value's (its own head columns of four
+// tokens, paired by byte permutes); which token of a tile is which row of a product
+// (token_of) is chosen so that in the boxes' swizzle both reads are without bank
+// conflicts.  The weights go from
 // accumulator to operand by two 8 x 8 transposes.
 // The warps' parts meet in shared memory; where groups are few the keys are cut into
 // runs whose parts a second launch joins.
@@ -51,28 +52,28 @@ struct Tok {
   static constexpr int kPitch = DH + 4;                 // of a row of O in shared memory
   static constexpr bool kQInSmem = NT == 4;
   static constexpr int kQBytes = kQInSmem ? NT * kK * 32 * 8 : 0;
-  static constexpr int kSmem = NW * kRing + kQBytes;
+  static constexpr int kSmem = NW * kRing + kQBytes + 1024;
   static_assert(NT * 8 * (kPitch + 4) * 4 <= kRing, "a warp's part fits in its ring");
   static_assert(kStages >= 3 && kStages < 32, "ring");
 };
 
-// Byte offset of 16-byte chunk c of token row r in a tile.  Keys: lanes read chunks
-// t + 4 q of rows g, a phase of eight lanes the rows 2 p and 2 p + 1; values: chunk g of
-// rows 2 t (+ 1, + 8, + 9), a phase two chunks of four rows.
+// The token of eight that is row n of a product.  A phase of eight lanes reads keys of
+// rows 2 p and 2 p + 1, values of rows 0, 2, 4, 6 or 1, 3, 5, 7: rows of 128 bytes in
+// their swizzle (chunk c of row r at c ^ (r mod 8)) want these two to differ in bit 2 and
+// those four in bits 1 and 2, rows of 64 bytes (c ^ (r / 2 mod 4)) in bit 0 and in bits 0
+// and 2.
+template <int ROW>
+__device__ __forceinline__ int token_of(int n) {
+  const int t = n >> 1;
+  const int even = ROW == 64 ? (t & 1) | ((t & 2) << 1) : 2 * t;
+  return n & 1 ? even ^ (ROW == 64 ? 3 : 5) : even;
+}
+// Byte offset of 16-byte chunk c (of the first 128 bytes) of token row r in a tile.
 template <int ROW>
 __device__ __forceinline__ uint32_t place(int r, int c) {
-  if (ROW == 64) {  // two rows a line of 128 bytes
-    const int line = r >> 1;
-    return line * 128 + (((((r & 1) << 2) | c) ^ ((line & 3) << 1)) << 4);
-  }
-  return r * ROW + ((c ^ ((r & 7) ^ ((r & 1) << 2))) << 4);
+  return ROW == 64 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4) : r * 128 + ((c ^ (r & 7)) << 4);
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(there ? 16 : 0)
-               : "memory");
-}
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -126,18 +127,30 @@ __device__ __forceinline__ float tanh_score(float x) {
 
 template <int DH, bool CODES, int NT, bool PLAIN>
 __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
-    token_kernel(const __grid_constant__ PagedAttnArgs a, int cluster, int partials) {
+    token_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
+                 const __grid_constant__ PagedAttnArgs a, int cluster, int partials, int parts) {
   using C = Tok<DH, CODES, NT>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[NW][C::kStages];
+  __shared__ int abort_word;
+  // The same offset in every block of a cluster: its blocks read each other's.
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  volatile int* abort_flag = &abort_word;
   const PageArgs& pg = a.page;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int splits = cluster * partials;
-  const int group = blockIdx.x / splits, split = blockIdx.x % splits;
-  const int b = group / a.Hkv, hkv = group % a.Hkv, rows = a.H / a.Hkv * a.Nq;
+  // Runs of keys fastest, so that a cluster has one part of one group's rows.
+  const int splits = cluster * partials, split = blockIdx.x % splits;
+  const int group = blockIdx.x / splits / parts, r0 = 8 * NT * (blockIdx.x / splits % parts);
+  const int b = group / a.Hkv, hkv = group % a.Hkv, all_rows = a.H / a.Hkv * a.Nq;
+  const int rows = min(all_rows - r0, 8 * NT);
   if (partials > 1) release_next();
+  if (threadIdx.x < NW * C::kStages) tc::mbar_init(&full[0][0] + threadIdx.x, 1);
+  if (threadIdx.x == 0) abort_word = 0;
+  tc::fence_barrier_init();
 
   // What each row sees (lane r: row r), and their hull; the same in every warp.
-  const GroupRow own = group_row(a, b, hkv, lane, rows);
+  const GroupRow own = group_row(a, b, hkv, r0 + lane, r0 + rows);
   const int h_lo = warp_min(own.v.lo), h_hi = warp_max(own.v.hi);
   const int in_lo = warp_max(lane < rows ? own.v.lo : 0);
   const int in_hi = warp_min(lane < rows ? own.v.hi : INT_MAX);
@@ -149,19 +162,18 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
 
   // Pages and scales of this warp's next 32 units, one a lane, and of the 32 behind.
   struct Meta {
-    int page;
-    float ks, vs;
+    int slab;  // page and head; one past the last where there is nothing: zeros
+    float ks, lv;
   };
   auto meta_of = [&](int n) {
-    Meta m{-1, 1.f, 1.f};
+    Meta m{pg.P * a.Hkv, 1.f, 0.f};
     if (n < count) {
       const int page = page_at(pg, b, (first + NW * n) * kUnit);
       if (page_ok(pg, page)) {
-        m.page = page;
+        m.slab = page * a.Hkv + hkv;
         if (CODES) {
-          const size_t at = static_cast<size_t>(page) * a.Hkv + hkv;
-          m.ks = pg.k_scale[at];
-          m.vs = pg.v_scale[at];
+          m.ks = pg.k_scale[m.slab];
+          m.lv = __log2f(pg.v_scale[m.slab]);
         }
       }
     }
@@ -169,26 +181,24 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
   };
   Meta cur = meta_of(lane), nxt = meta_of(32 + lane);
   int batch = 0;
+  __syncthreads();  // the barriers are there
 
-  const uint32_t ring = smem_u32(smem) + warp * C::kRing;
+  uint8_t* const ring = smem + warp * C::kRing;
   auto issue = [&](int n) {
     if (n < count) {
-      const int page = __shfl_sync(0xffffffffu, (n >> 5) == batch ? cur.page : nxt.page, n & 31);
-      const bool there = page >= 0;
-      const int j = (first + NW * n) * kUnit;
-      const size_t at = there ? page_row(pg, page, a.Hkv, hkv, j) * C::kRow : 0;
-      const uint8_t* K = static_cast<const uint8_t*>(a.K) + at;
-      const uint8_t* V = static_cast<const uint8_t*>(a.V) + at;
-      const uint32_t dst = ring + (n % C::kStages) * (2 * C::kTile);
+      const int slab = __shfl_sync(0xffffffffu, (n >> 5) == batch ? cur.slab : nxt.slab, n & 31);
+      if (lane == 0) {
+        const int s = n % C::kStages, y = ((first + NW * n) * kUnit) & (pg.T - 1);
+        uint8_t* dst = ring + s * (2 * C::kTile);
+        uint64_t* bar = &full[warp][s];
+        tc::mbar_expect_tx(bar, 2 * C::kTile);
 #pragma unroll
-      for (int i = 0; i < C::kRow / 32; ++i) {
-        const int x = lane + 32 * i, off = there ? 16 * x : 0;
-        const uint32_t p = place<C::kRow>(x / (C::kRow / 16), x % (C::kRow / 16));
-        copy16(dst + p, K + off, there);
-        copy16(dst + C::kTile + p, V + off, there);
+        for (int h = 0; h < C::kRow; h += 128) {
+          tc::tma_load_3d(dst + h * kUnit, &mK, bar, h / 2, y, slab);
+          tc::tma_load_3d(dst + C::kTile + h * kUnit, &mV, bar, h / 2, y, slab);
+        }
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
   for (int n = 0; n < C::kStages - 1; ++n) issue(n);
@@ -201,7 +211,7 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
   float slope2[NT][2];
   int pos[NT][2];
   const __nv_bfloat16* Q =
-      static_cast<const __nv_bfloat16*>(a.Q) + static_cast<size_t>(group) * rows * DH;
+      static_cast<const __nv_bfloat16*>(a.Q) + (static_cast<size_t>(group) * all_rows + r0) * DH;
   const float c0 = a.cap > 0.f ? a.tau / a.cap : a.tau * kLog2e, c2 = a.cap * kLog2e;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -266,16 +276,27 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
       for (int e = 0; e < 4; ++e) O[nt][i][e] = 0.f;
   }
 
-  for (int n = 0; n < count; ++n) {
+  // This lane's runs in a tile: keys of row g (and 8 further) in two halves of 64 bytes,
+  // values of rows 2 t and 2 t + 1 (and 8 further).
+  constexpr int kTok = C::kRow == 64 ? 64 : 128;  // bytes from token to token
+  const int tok = token_of<C::kRow>(g), tok0 = token_of<C::kRow>(2 * t);
+  const int tok1 = token_of<C::kRow>(2 * t + 1);
+  const uint32_t k_at[2] = {place<C::kRow>(tok, t), place<C::kRow>(tok, t + 4)};
+  const uint32_t v_at[2] = {
+      C::kTile + (C::kRow == 64 ? place<64>(tok0, g >> 1) + 8 * (g & 1) : place<C::kRow>(tok0, g)),
+      C::kTile + (C::kRow == 64 ? place<64>(tok1, g >> 1) + 8 * (g & 1) : place<C::kRow>(tok1, g))};
+  bool ok = true;
+  int n = 0;
+  for (; n < count; ++n) {
     if ((n >> 5) != batch) {
       cur = nxt;
       nxt = meta_of(n + 32 + lane);
       batch = n >> 5;
     }
     issue(n + C::kStages - 1);
-    asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
-    __syncwarp();
-    const uint32_t kt = ring + (n % C::kStages) * (2 * C::kTile), vt = kt + C::kTile;
+    ok = wait_warp(&full[warp][n % C::kStages], (n / C::kStages) & 1, abort_flag, a.err);
+    if (!ok) break;
+    const uint32_t kt = smem_u32(ring) + (n % C::kStages) * (2 * C::kTile);
     const int j0 = (first + NW * n) * kUnit;
 
     float S[NT][4];
@@ -283,8 +304,8 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
     for (int nt = 0; nt < NT; ++nt) S[nt][0] = S[nt][1] = S[nt][2] = S[nt][3] = 0.f;
 #pragma unroll
     for (int q = 0; q < DH / (4 * C::kRun); ++q) {
-      const uint4 x = lds16(kt + place<C::kRow>(g, t + 4 * q));
-      const uint4 y = lds16(kt + place<C::kRow>(g + 8, t + 4 * q));
+      const uint32_t at = kt + k_at[q & 1] + (q >> 1) * (128 * kUnit);
+      const uint4 x = lds16(at), y = lds16(at + 8 * kTok);
       const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
       for (int s = 0; s < C::kRun / 4; ++s) {
@@ -311,29 +332,30 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
       }
     }
 
-    // Scores: element e of S[nt] is token g + 8 (e / 2), row 8 nt + 2 t + e % 2.
-    float ks = 1.f, lv = 0.f, inv_vs = 1.f;
+    // Scores: element e of S[nt] is the token of row g + 8 (e / 2), row 8 nt + 2 t + e % 2.
+    float ks = 1.f, lv = 0.f;
     if (CODES) {
       ks = __shfl_sync(0xffffffffu, cur.ks, n & 31);
-      const float vs = __shfl_sync(0xffffffffu, cur.vs, n & 31);
-      lv = __log2f(vs);
-      inv_vs = 1.f / vs;
+      lv = __shfl_sync(0xffffffffu, cur.lv, n & 31);
     }
+    const float inv_vs = CODES ? ex2_approx(-lv) : 1.f;
+    const int j_of = j0 + tok;
     const bool masked = j0 < in_lo || j0 + kUnit > in_hi;
     bool raise = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int j = j0 + g + 8 * (e >> 1);
-        float x = S[nt][e] * (c1[nt][e & 1] * ks);
-        if (!PLAIN) {
-          if (a.cap > 0.f) x = c2 * tanh_score(x);
-          if (a.slopes)
-            x = fmaf(-slope2[nt][e & 1], fabsf(static_cast<float>(j - pos[nt][e & 1])), x);
+        const int j = j_of + 8 * (e >> 1);
+        if (PLAIN) {
+          S[nt][e] = fmaf(S[nt][e], c1[nt][e & 1] * ks, lv);
+          continue;
         }
-        if (CODES) x += lv;
-        S[nt][e] = x;
+        float x = S[nt][e] * (c1[nt][e & 1] * ks);
+        if (a.cap > 0.f) x = c2 * tanh_score(x);
+        if (a.slopes)
+          x = fmaf(-slope2[nt][e & 1], fabsf(static_cast<float>(j - pos[nt][e & 1])), x);
+        S[nt][e] = x + lv;
       }
     if (masked) {
 #pragma unroll
@@ -342,8 +364,8 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
         for (int e = 0; e < 2; ++e) {
           const int lo = __shfl_sync(0xffffffffu, own.v.lo, 8 * nt + 2 * t + e);
           const int hi = __shfl_sync(0xffffffffu, own.v.hi, 8 * nt + 2 * t + e);
-          if (j0 + g < lo || j0 + g >= hi) S[nt][e] = -INFINITY;
-          if (j0 + g + 8 < lo || j0 + g + 8 >= hi) S[nt][e + 2] = -INFINITY;
+          if (j_of < lo || j_of >= hi) S[nt][e] = -INFINITY;
+          if (j_of + 8 < lo || j_of + 8 >= hi) S[nt][e + 2] = -INFINITY;
         }
     }
 #pragma unroll
@@ -386,20 +408,20 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
       pb[nt][1] = transpose8(pack<CODES>(p[2], p[3]));
     }
 
-    // Values of tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9 (v[0 .. 3]), this lane's columns: what
+    // Values of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 (v[0 .. 3]), this lane's columns: what
     // lies outside the hull may be anything and is made 0.
     constexpr int kWords = DH / 8 * (CODES ? 1 : 2) / 4;  // 32-bit words of a lane's columns
     uint32_t v[4][kWords];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = 2 * t + (i & 1) + 8 * (i >> 1);
+      const uint32_t at = kt + v_at[i & 1] + (i >> 1) * (8 * kTok);
       if (kWords == 2) {
-        const uint2 x = lds8(vt + place<C::kRow>(r, g >> 1) + 8 * (g & 1));
+        const uint2 x = lds8(at);
         v[i][0] = x.x, v[i][1] = x.y;
       } else {
 #pragma unroll
         for (int q = 0; q < kWords / 4; ++q) {
-          const uint4 x = lds16(vt + place<C::kRow>(r, g + 8 * q));
+          const uint4 x = lds16(at + q * (128 * kUnit));
           v[i][4 * q] = x.x, v[i][4 * q + 1] = x.y, v[i][4 * q + 2] = x.z, v[i][4 * q + 3] = x.w;
         }
       }
@@ -407,7 +429,7 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
     if (j0 < h_lo || j0 + kUnit > h_hi) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int j = j0 + 2 * t + (i & 1) + 8 * (i >> 1);
+        const int j = j0 + (i & 1 ? tok1 : tok0) + 8 * (i >> 1);
         if (j < h_lo || j >= h_hi)
 #pragma unroll
           for (int q = 0; q < kWords; ++q) v[i][q] = 0u;
@@ -444,7 +466,9 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
     }
     __syncwarp();  // the next copies overwrite this unit
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (!ok && lane == 0)  // what is under way has to land before the block ends
+    for (int k = n; k < min(n + C::kStages, count); ++k)
+      tc::drain_wait(&full[warp][k % C::kStages], (k / C::kStages) & 1);
   __syncwarp();
 
   // The warps' parts: O row by row, then R and l of each row.
@@ -533,7 +557,7 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
     tc::cluster_sync();  // no block leaves while its memory is read
   }
   const size_t all = static_cast<size_t>(a.B) * a.H * a.Nq;
-  const size_t base = static_cast<size_t>(group) * rows;
+  const size_t base = static_cast<size_t>(group) * all_rows + r0;
   const Partials out = attn::partials(a.workspace, all, DH, partials);
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
@@ -583,12 +607,17 @@ template <int DH, bool CODES, int NT, bool PLAIN>
 cudaError_t launch(const PagedAttnArgs& a, const TokenRuns& runs) {
   using C = Tok<DH, CODES, NT>;
   const auto kernel = token_kernel<DH, CODES, NT, PLAIN>;
-  cudaError_t e = tc_set_smem(reinterpret_cast<const void*>(kernel), C::kSmem);
+  CUtensorMap mk, mv;
+  cudaError_t e = tc_map(&mk, a.K, a.page.P * a.Hkv, a.page.T, kUnit, DH, CODES);
+  if (e == cudaSuccess) e = tc_map(&mv, a.V, a.page.P * a.Hkv, a.page.T, kUnit, DH, CODES);
+  if (e == cudaSuccess) e = tc_set_smem(reinterpret_cast<const void*>(kernel), C::kSmem);
   if (e != cudaSuccess) return e;
-  const long long grid = static_cast<long long>(a.B) * a.Hkv * runs.cluster * runs.partials;
+  const int parts = (a.H / a.Hkv * a.Nq + 8 * NT - 1) / (8 * NT);
+  const long long grid =
+      static_cast<long long>(a.B) * a.Hkv * parts * runs.cluster * runs.partials;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
   return launch_after(false, kernel, dim3(static_cast<unsigned>(grid)), 32 * NW, C::kSmem,
-                      runs.cluster, a.stream, a, runs.cluster, runs.partials);
+                      runs.cluster, a.stream, mk, mv, a, runs.cluster, runs.partials, parts);
 }
 
 template <int DH, bool CODES>
