@@ -21,8 +21,15 @@
 // (token_of) is chosen so that in the boxes' swizzle both reads are without bank
 // conflicts.  The weights go from
 // accumulator to operand by two 8 x 8 transposes.
-// The warps' parts meet in shared memory; where groups are few the keys are cut into
-// runs whose parts a second launch joins.
+// The warps' parts meet in shared memory.  A group's keys are cut into runs: where the
+// groups are few, as many as fill the SMs once, in clusters whose parts meet in
+// distributed shared memory (and across clusters in a second launch); where they are
+// more, two waves of them, longest requests first, joined by a second launch (clusters
+// that wait for one another's SMs cost several us a wave).  Equal shares of all units,
+// one a block, with a block's work going on from group to group, took longer: a group's
+// beginning is a chain of four memory latencies (ranges, pages, codes, and Q), which
+// blocks beside each other hide and a single one does not (32 requests of up to 8192
+// keys 87 us for 75, 16 with 4 drafted tokens 46 for 32, after a flush of the L2).
 #include "paged.cuh"
 #include "tc_attn.cuh"
 
@@ -37,6 +44,14 @@ constexpr int NW = 8;
 constexpr int kUnit = 16;  // tokens; a page is one unit or several
 constexpr float kRaise = 8.f;
 constexpr int kMostRows = 32;
+constexpr int kMostSorted = 128;  // batch entries; of more than that few blocks are the end
+
+// Runs that a group's keys are cut into, of 512 keys at least.
+struct TokenRuns {
+  int cluster;   // runs that meet in distributed shared memory
+  int partials;  // and so many of those are joined by a second launch
+  int sorted;    // blocks of long batch entries first
+};
 
 template <int DH, bool CODES, int NT>
 struct Tok {
@@ -128,29 +143,54 @@ __device__ __forceinline__ float tanh_score(float x) {
 template <int DH, bool CODES, int NT, bool PLAIN>
 __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
     token_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
-                 const __grid_constant__ PagedAttnArgs a, int cluster, int partials, int parts) {
+                 const __grid_constant__ PagedAttnArgs a, const TokenRuns runs) {
   using C = Tok<DH, CODES, NT>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[NW][C::kStages];
-  __shared__ int abort_word;
+  __shared__ int abort_word, entry, keys_of[kMostSorted];
   // The same offset in every block of a cluster: its blocks read each other's.
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   volatile int* abort_flag = &abort_word;
   const PageArgs& pg = a.page;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  // Runs of keys fastest, so that a cluster has one part of one group's rows.
-  const int splits = cluster * partials, split = blockIdx.x % splits;
-  const int group = blockIdx.x / splits / parts, r0 = 8 * NT * (blockIdx.x / splits % parts);
-  const int b = group / a.Hkv, hkv = group % a.Hkv, all_rows = a.H / a.Hkv * a.Nq;
-  const int rows = min(all_rows - r0, 8 * NT);
+  const int cluster = runs.cluster, partials = runs.partials, splits = cluster * partials;
+  const int nth = blockIdx.x / splits, split = blockIdx.x % splits;
+  const int hkv = nth % a.Hkv, rows = a.H / a.Hkv * a.Nq;
   if (partials > 1) release_next();
+  if (threadIdx.x == 0) {
+    tc::tma_prefetch_desc(&mK);
+    tc::tma_prefetch_desc(&mV);
+  }
+  int b = nth / a.Hkv;
+  if (runs.sorted) {
+    if (threadIdx.x < a.B) {
+      int lo = INT_MAX, hi = 0;
+      for (int i = 0; i < a.Nq; ++i) {
+        const RowView v = row_view(a.ranges, a.q_pos, static_cast<size_t>(threadIdx.x) * a.Nq, i,
+                                   a.Nk, a.causal);
+        lo = min(lo, v.lo), hi = max(hi, v.hi);
+      }
+      keys_of[threadIdx.x] = lo < hi ? hi - lo : 0;
+    }
+    __syncthreads();
+    if (threadIdx.x < a.B) {
+      const int mine = keys_of[threadIdx.x];
+      int rank = 0;
+      for (int i = 0; i < a.B; ++i)
+        rank += keys_of[i] > mine || (keys_of[i] == mine && i < static_cast<int>(threadIdx.x));
+      if (rank == b) entry = threadIdx.x;
+    }
+    __syncthreads();
+    b = entry;
+  }
+  const int group = b * a.Hkv + hkv;
   if (threadIdx.x < NW * C::kStages) tc::mbar_init(&full[0][0] + threadIdx.x, 1);
   if (threadIdx.x == 0) abort_word = 0;
   tc::fence_barrier_init();
 
   // What each row sees (lane r: row r), and their hull; the same in every warp.
-  const GroupRow own = group_row(a, b, hkv, r0 + lane, r0 + rows);
+  const GroupRow own = group_row(a, b, hkv, lane, rows);
   const int h_lo = warp_min(own.v.lo), h_hi = warp_max(own.v.hi);
   const int in_lo = warp_max(lane < rows ? own.v.lo : 0);
   const int in_hi = warp_min(lane < rows ? own.v.hi : INT_MAX);
@@ -211,7 +251,7 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
   float slope2[NT][2];
   int pos[NT][2];
   const __nv_bfloat16* Q =
-      static_cast<const __nv_bfloat16*>(a.Q) + (static_cast<size_t>(group) * all_rows + r0) * DH;
+      static_cast<const __nv_bfloat16*>(a.Q) + static_cast<size_t>(group) * rows * DH;
   const float c0 = a.cap > 0.f ? a.tau / a.cap : a.tau * kLog2e, c2 = a.cap * kLog2e;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -557,7 +597,7 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
     tc::cluster_sync();  // no block leaves while its memory is read
   }
   const size_t all = static_cast<size_t>(a.B) * a.H * a.Nq;
-  const size_t base = static_cast<size_t>(group) * all_rows + r0;
+  const size_t base = static_cast<size_t>(group) * rows;
   const Partials out = attn::partials(a.workspace, all, DH, partials);
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
@@ -587,20 +627,19 @@ int token_blocks_per_sm(const PagedAttnArgs& a) {
   return a.H / a.Hkv * a.Nq <= 8 && (a.page.e4m3 || a.d == 64) ? 2 : 1;
 }
 
-// Runs that the keys are cut into, of 512 keys at least.
-struct TokenRuns {
-  int cluster;   // runs that meet in distributed shared memory
-  int partials;  // and so many of those are joined by a second launch
-};
 TokenRuns token_runs(const PagedAttnArgs& a) {
   const long long groups = static_cast<long long>(a.B) * a.Hkv;
   const long long slots = static_cast<long long>(kSMs) * token_blocks_per_sm(a);
-  long long s = (2 * groups > slots ? 3 * slots : slots) / groups;
+  const bool many = 2 * groups > slots;
+  long long s = (many ? 2 * slots : slots) / groups;
   const long long most = a.Nk / 512;
   s = s > most ? most : s;
-  if (s <= 1) return {1, 1};
-  if (s <= 8) return {static_cast<int>(s), 1};
-  return {8, static_cast<int>(s / 8)};
+  s = s < 1 ? 1 : s;
+  if (many) {
+    const bool sorted = a.ranges && a.B > 1 && a.B <= kMostSorted && s * groups > slots;
+    return {1, static_cast<int>(s), sorted ? 1 : 0};
+  }
+  return s <= 8 ? TokenRuns{static_cast<int>(s), 1, 0} : TokenRuns{8, static_cast<int>(s / 8), 0};
 }
 
 template <int DH, bool CODES, int NT, bool PLAIN>
@@ -612,12 +651,10 @@ cudaError_t launch(const PagedAttnArgs& a, const TokenRuns& runs) {
   if (e == cudaSuccess) e = tc_map(&mv, a.V, a.page.P * a.Hkv, a.page.T, kUnit, DH, CODES);
   if (e == cudaSuccess) e = tc_set_smem(reinterpret_cast<const void*>(kernel), C::kSmem);
   if (e != cudaSuccess) return e;
-  const int parts = (a.H / a.Hkv * a.Nq + 8 * NT - 1) / (8 * NT);
-  const long long grid =
-      static_cast<long long>(a.B) * a.Hkv * parts * runs.cluster * runs.partials;
+  const long long grid = static_cast<long long>(a.B) * a.Hkv * runs.cluster * runs.partials;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
   return launch_after(false, kernel, dim3(static_cast<unsigned>(grid)), 32 * NW, C::kSmem,
-                      runs.cluster, a.stream, mk, mv, a, runs.cluster, runs.partials, parts);
+                      runs.cluster, a.stream, mk, mv, a, runs);
 }
 
 template <int DH, bool CODES>

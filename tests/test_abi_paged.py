@@ -30,7 +30,7 @@ def read(lib, p, B=2, Hkv=2, P=9, T=16, M=4, Nk=64, d=64, cache=2, dtype=1):
     return lib.flashbob_cache_read(*p, B, Hkv, P, T, M, Nk, d, cache, dtype, None)
 
 
-def attention(lib, p, tau=0.1, cap=0.0, ws=BIG, B=1, H=2, Hkv=1, Nq=8, P=99, T=16, M=300, d=64, causal=0, dtype=1, cache=2):
+def attention(lib, p, tau=0.1, cap=0.0, ws=BIG, B=1, H=2, Hkv=1, Nq=8, P=99, T=16, M=3000, d=64, causal=0, dtype=1, cache=2):
     return lib.flashbob_attention_paged(*p[:9], tau, cap, p[9], p[10], p[11], ws, B, H, Hkv, Nq, P, T, M, d, causal, dtype, cache,
                                         None)
 

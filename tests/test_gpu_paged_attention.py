@@ -114,11 +114,15 @@ PROMPTS = [case(*c) for c in (
     (2, 12, 4, 256, 30, 32, 64), (1, 1, 1, 33, 200, 16, 128), (1, 16, 16, 640, 11, 64, 128),
     (2, 4, 2, 129, 5, 64, 128, BF, BF), (1, 6, 2, 200, 40, 16, 64, BF, BF),
     (1, 8, 8, 700, 7, 128, 128, BF, BF))]
+# Requests of unequal length whose keys are shared out evenly among the blocks.
+SHARED = [case(*c) for c in (
+    (7, 8, 2, 1, 20, 64, 128), (3, 32, 2, 2, 130, 16, 64), (40, 4, 4, 1, 16, 64, 64), (9, 8, 8, 3, 9, 128, 128),
+    (2, 3, 1, 5, 64, 16, 128), (130, 2, 1, 1, 64, 16, 64), (4, 16, 1, 1, 17, 64, 128, BF, BF), (6, 24, 2, 2, 40, 32, 64, BF, BF))]
 OTHERS = [case(*c) for c in (
     (1, 1, 1, 1, 1, 16, 1, F32, E4M3), (2, 3, 3, 33, 5, 16, 80, F32, E4M3), (1, 4, 2, 3, 20, 64, 64, F32, F32),
     (2, 2, 1, 65, 3, 128, 128, F32, E4M3), (1, 6, 3, 5, 9, 32, 34, BF, E4M3), (2, 2, 2, 70, 9, 32, 96, BF, BF),
     (1, 5, 1, 9, 3, 16, 127, F32, F32))]
-ALL = TOKENS + PROMPTS + OTHERS
+ALL = TOKENS + SHARED + PROMPTS + OTHERS
 
 
 @pytest.mark.parametrize("c", ALL, ids=name)
@@ -135,7 +139,7 @@ def test_caps_and_biases(c, cap, bias):
     check(c, cap=cap, bias=bias, mask="random", seed=4)
 
 
-@pytest.mark.parametrize("c", [TOKENS[3], TOKENS[16], PROMPTS[1], PROMPTS[9], OTHERS[1]], ids=name)
+@pytest.mark.parametrize("c", [TOKENS[3], TOKENS[16], SHARED[0], SHARED[7], PROMPTS[1], PROMPTS[9], OTHERS[1]], ids=name)
 @pytest.mark.parametrize("mask", ["none", "one", "nothing"])
 def test_few_and_all_keys(c, mask):
     check(c, mask=mask, seed=5)
@@ -194,7 +198,7 @@ def test_the_same_as_dense_keys():
     assert float((L - L2).abs().max()) <= 2e-5 and float((O.float() - O2.float()).abs().max()) <= 2e-2
 
 
-@pytest.mark.parametrize("c", [TOKENS[6], TOKENS[12], PROMPTS[1], OTHERS[1]], ids=name)
+@pytest.mark.parametrize("c", [TOKENS[6], TOKENS[12], SHARED[0], SHARED[7], PROMPTS[1], OTHERS[1]], ids=name)
 def test_same_bits_on_another_stream_and_replayed(c):
     Q, pools, _, table, form = make(**c)
     cache = fb.PagedCache(*pools)
