@@ -42,12 +42,17 @@ struct Cfg {
   static constexpr int kChunks = BN / 16;         // 16 keys lie on one page
   static constexpr uint32_t HT = BN * 64 * 2;     // bytes of 64 columns of a tile
   static constexpr int NBUF = DH == 64 ? 3 : 4;   // score buffers: O~ takes the rest of TMEM
-  // Tiles of keys and of values as operands, and of codes on their way there.
-  static constexpr int NK = !CODES ? (DH == 64 ? 5 : 4) : DH == 64 ? 4 : 3;
-  static constexpr int NV = !CODES ? (DH == 64 || MT == 2 ? NK : 5) : DH == 64 || MT == 1 ? 3 : 2;
+  // Tiles of keys and of values as operands, and of codes on their way there.  Where they
+  // arrive and leave together (kJoint) the MMA warp waits and commits less; converters,
+  // which work in order, want slots of their own for keys that are asked for earlier.
+  static constexpr bool kJoint = !CODES;
+  static constexpr int NK = kJoint ? (MT == 2 ? 5 : 6) - (DH == 64 ? 0 : 1) : DH == 64 ? 4 : 3;
+  static constexpr int NV = kJoint ? NK : DH == 64 || MT == 1 ? 3 : 2;
+  static constexpr int k_tile(int s) { return kJoint ? 2 * s : s; }  // in the one array of tiles
+  static constexpr int v_tile(int s) { return kJoint ? 2 * s + 1 : NK + s; }
   static constexpr int NI = CODES ? 8 : 0;
   // Keys come so many tiles ahead of values, as the MMA warp asks for them.
-  static constexpr int kLead = (NBUF + MT - 1) / MT;
+  static constexpr int kLead = kJoint ? 0 : (NBUF + MT - 1) / MT;
   // The scales of tile t are written when the codes that lay in its slot have been taken,
   // those of tile t - NI / 2 - kLead at least; so the scores of the tile NK before that are
   // done, which were issued behind the products of a unit NBUF earlier: its readers are
@@ -60,7 +65,7 @@ struct Cfg {
   // In the order of Order the slot that a tile takes is free without any later one: keys
   // of tile t need the scores of t - NK, values the products of t - NV, which need no keys
   // beyond those of t - NV + kLead.
-  static_assert(NK >= 2 && NV >= 2, "rings");
+  static_assert(NK >= 2 && NV >= 2 && (!kJoint || NBUF <= MT * NK), "rings");
 };
 
 template <int DH, int MT, bool CODES>
@@ -183,14 +188,16 @@ struct PagedScore {
 };
 
 // Tiles in the order in which they are loaded, converted and asked for: the keys of the
-// first kLead, then values of tile t and keys of tile t + kLead.
+// first kLead, then values of tile t and keys of tile t + kLead (kLead = 0: keys and
+// values of each tile).
 template <int LEAD, typename F>
 __device__ __forceinline__ void in_order(int T, const F& item) {
   bool ok = true;
   int i = 0;
   for (int x = 0; ok && x < T + LEAD; ++x) {
-    if (x >= LEAD) ok = item(i++, x - LEAD, true);
-    if (ok && x < T) ok = item(i++, x, false);
+    if (LEAD == 0) ok = item(i++, x, false);
+    if (ok && x >= LEAD) ok = item(i++, x - LEAD, true);
+    if (LEAD > 0 && ok && x < T) ok = item(i++, x, false);
   }
 }
 
@@ -277,9 +284,9 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
   if (warp == C::kMma) {
     constexpr uint32_t idS = idesc(CODES, BN, false), idO = idesc(CODES, DH, true);
     const uint64_t dQ = smem_desc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
-    const uint64_t dK0 = smem_desc_sw128(smem_u32(sm.kv[0][0]), 16, 1024);
-    const uint64_t dV0 = smem_desc_sw128(smem_u32(sm.kv[NK][0]), HT, 1024);
-    constexpr uint64_t kStep = (NH * HT) >> 4;
+    const uint64_t dK0 = smem_desc_sw128(smem_u32(sm.kv[C::k_tile(0)][0]), 16, 1024);
+    const uint64_t dV0 = smem_desc_sw128(smem_u32(sm.kv[C::v_tile(0)][0]), HT, 1024);
+    constexpr uint64_t kStep = (C::k_tile(1) * NH * HT) >> 4;  // V's is the same
     auto tile = [](int u) { return MT == 2 ? u >> 1 : u; };
     auto issue_scores = [&](int u) {
       const uint64_t so = (tile(u) % NK) * kStep;
@@ -292,7 +299,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
                kk > 0);
       }
       mma_commit(&sm.sc_full[u % NBUF]);
-      if (MT == 1 || (u & 1)) mma_commit(&sm.k_empty[tile(u) % NK]);
+      if (!C::kJoint && (MT == 1 || (u & 1))) mma_commit(&sm.k_empty[tile(u) % NK]);
     };
     auto issue_pv = [&](int u) {
       const int s = tile(u) % NV;
@@ -319,7 +326,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       for (int u = 0; ok && u < NBUF && u < U; ++u) scores(u);
       for (int u = 0; ok && u < U; ++u) {
         const int t = tile(u);
-        ok = ((MT == 2 && (u & 1)) ||
+        ok = (C::kJoint || (MT == 2 && (u & 1)) ||
               wait_one(&sm.v_full[t % NV], (t / NV) & 1, abort_flag, err)) &&
              wait_one(&sm.op_ready[u % NBUF], (u / NBUF) & 1, abort_flag, err);
         if (!ok) break;
@@ -360,30 +367,25 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
     Meta prv, cur = meta_of(lane), nxt = meta_of(32 + lane);
     prv = cur;
     int batch = 0;
-    int nk = 0, nv = 0, ni = 0;  // started
+    int nk = 0, ni = 0;  // tiles and items that are under way
     in_order<C::kLead>(T, [&](int i, int t, bool values) {
-      const int N = values ? NV : NK, s = t % N, it = i % (C::NI + !CODES);
+      const int s = t % NK, it = i % (C::NI + !CODES);
       if (!values && t > 0 && t % kAhead == 0) {
         prv = cur;
         cur = nxt;
         nxt = meta_of((t / kAhead + 1) * 32 + lane);
         batch = t / kAhead;
       }
-      uint64_t* bar;
-      uint8_t* dst;
-      bool ok;
-      if (CODES) {
+      // A joint slot is waited for with the keys, and its barrier counts both.
+      bool ok = true;
+      if (CODES)
         ok = i < C::NI ||
              wait_warp(&sm.i_empty[it], ((i / (C::NI + !CODES)) - 1) & 1, abort_flag, err);
-        bar = &sm.i_full[it];
-        dst = sm.item[it];
-      } else {
-        ok = t < N || wait_warp(values ? &sm.v_empty[s] : &sm.k_empty[s], ((t / N) - 1) & 1,
-                                abort_flag, err);
-        bar = values ? &sm.v_full[s] : &sm.k_full[s];
-        dst = sm.kv[values ? NK + s : s][0];
-      }
+      else if (!values)
+        ok = t < NV || wait_warp(&sm.v_empty[s], ((t / NV) - 1) & 1, abort_flag, err);
       if (!ok) return false;
+      uint64_t* bar = CODES ? &sm.i_full[it] : &sm.k_full[s];
+      uint8_t* dst = CODES ? sm.item[it] : sm.kv[values ? C::v_tile(s) : C::k_tile(s)][0];
       const bool now = t / kAhead == batch;  // values may be of the batch before
       if (CODES && !values) {
         const int n = t * kChunks + (lane & (kChunks - 1));
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
           sm.scale[t % C::NS][lane] = make_float4(ks, __log2f(vs), 1.f / vs, 0.f);
         __syncwarp();
       }
-      if (lane == 0) mbar_expect_tx(bar, CODES ? BN * DH : NH * HT);
+      if (lane == 0 && (CODES || !values)) mbar_expect_tx(bar, CODES ? BN * DH : 2 * NH * HT);
       const CUtensorMap* map = values ? &mV : &mK;
       for (int x = 0; x < boxes; ++x) {
         const int n = t * kChunks + per * x;
@@ -405,8 +407,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
         }
       }
       ni = i + 1;
-      if (values) nv = t + 1;
-      else nk = t + 1;
+      nk = t + 1;
       return true;
     });
     if (lane == 0) {  // what is under way has to land before the block ends
@@ -416,7 +417,6 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
           drain_wait(&sm.i_full[i % (C::NI + !CODES)], (i / (C::NI + !CODES)) & 1);
       } else {
         for (int t = nk > NK ? nk - NK : 0; t < nk; ++t) drain_wait(&sm.k_full[t % NK], (t / NK) & 1);
-        for (int t = nv > NV ? nv - NV : 0; t < nv; ++t) drain_wait(&sm.v_full[t % NV], (t / NV) & 1);
       }
     }
     __syncwarp();
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
                                abort_flag, err));
       if (!ok) return false;
       const uint32_t src = smem_u32(sm.item[it]) + from;
-      const uint32_t dst = smem_u32(sm.kv[values ? NK + s : s][0]);
+      const uint32_t dst = smem_u32(sm.kv[values ? C::v_tile(s) : C::k_tile(s)][0]);
       uint32_t w[kRuns][4];
 #pragma unroll
       for (int u = 0; u < kRuns; ++u)
@@ -520,9 +520,9 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
     // already).
     auto clear_hidden = [&](int t, int col0) {
       if (CODES || (col0 >= hull.lo && col0 + BN <= hull.hi)) return true;
-      if (!wait_warp(&sm.v_full[t % NV], (t / NV) & 1, abort_flag, err)) return false;
+      if (!wait_warp(&sm.k_full[t % NK], (t / NK) & 1, abort_flag, err)) return false;
       if (r < BN && (col0 + r < hull.lo || col0 + r >= hull.hi))
-        zero_row<NH, HT>(sm.kv[NK + t % NV], r);
+        zero_row<NH, HT>(sm.kv[C::v_tile(t % NV)], r);
       fence_proxy_async_smem();
       return true;
     };
