@@ -57,7 +57,8 @@ struct Cfg {
   // those of tile t - NI / 2 - kLead at least; so the scores of the tile NK before that are
   // done, which were issued behind the products of a unit NBUF earlier: its readers are
   // through.
-  static constexpr int NS = NI / 2 + kLead + NK + NBUF;
+  static constexpr int NS = 16;
+  static_assert(NS >= NI / 2 + kLead + NK + NBUF, "scales");
   // Elementwise warps 0 - 7, converters (codes), loads, MMA.  With two converters the
   // elementwise threads have 168 registers, with four 128.
   static constexpr int kConv = CODES ? 2 : 0, kLoad = 8 + kConv, kMma = kLoad + 1, kThreads = 32 * (kMma + 1);
@@ -343,20 +344,20 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
     // the copies fill with zeros) and its scales.
     struct Meta {
       int slab;
-      float ks, vs;
+      float4 scale;  // s_K, log2 s_V, 1 / s_V
     };
     const int chunks = T * kChunks, chunk0 = tb * kChunks;
-    const int box = min(a.page.T, BN), per = box / 16, boxes = BN / box;  // keys of one copy
+    const int box = min(a.page.T, BN);  // keys of one copy
     auto meta_of = [&](int n) {
-      Meta m{a.page.P * a.Hkv, 1.f, 1.f};
+      Meta m{a.page.P * a.Hkv, make_float4(1.f, 0.f, 1.f, 0.f)};
       const int j = (chunk0 + n) * 16 & ~(box - 1);
       if (n < chunks && j < hull.hi && j + box > hull.lo) {
         const int page = page_at(a.page, b, j);
         if (page_ok(a.page, page)) {
           m.slab = page * a.Hkv + hkv;
           if (CODES) {
-            m.ks = a.page.k_scale[m.slab];
-            m.vs = a.page.v_scale[m.slab];
+            const float vs = a.page.v_scale[m.slab];
+            m.scale = make_float4(a.page.k_scale[m.slab], __log2f(vs), 1.f / vs, 0.f);
           }
         }
       }
@@ -366,7 +367,12 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
     static_assert(C::kLead <= kAhead, "values are at most one batch behind the keys");
     Meta prv, cur = meta_of(lane), nxt = meta_of(32 + lane);
     prv = cur;
-    int batch = 0;
+    // This lane's chunk: of the tiles `turn` of kAhead, at byte `to` of a tile, and
+    // whether it asks for a box there (the lane of the box's first chunk does).
+    const int turn = lane / kChunks, chunk = lane % kChunks;
+    const bool asks = (16 * chunk & (box - 1)) == 0;
+    const uint32_t to = 16 * chunk * (CODES ? DH : 128);
+    const int page_y = (tb * BN + 16 * chunk) & (a.page.T - 1), turn_y = BN & (a.page.T - 1);
     int nk = 0, ni = 0;  // tiles and items that are under way
     in_order<C::kLead>(T, [&](int i, int t, bool values) {
       const int s = t % NK, it = i % (C::NI + !CODES);
@@ -374,7 +380,6 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
         prv = cur;
         cur = nxt;
         nxt = meta_of((t / kAhead + 1) * 32 + lane);
-        batch = t / kAhead;
       }
       // A joint slot is waited for with the keys, and its barrier counts both.
       bool ok = true;
@@ -385,29 +390,23 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
         ok = t < NV || wait_warp(&sm.v_empty[s], ((t / NV) - 1) & 1, abort_flag, err);
       if (!ok) return false;
       uint64_t* bar = CODES ? &sm.i_full[it] : &sm.k_full[s];
-      uint8_t* dst = CODES ? sm.item[it] : sm.kv[values ? C::v_tile(s) : C::k_tile(s)][0];
-      const bool now = t / kAhead == batch;  // values may be of the batch before
+      const bool mine = turn == t % kAhead;
+      // Values may be of the batch before: the keys are nk - 1 tiles on.
+      const int slab = values && t / kAhead != (nk - 1) / kAhead ? prv.slab : cur.slab;
       if (CODES && !values) {
-        const int n = t * kChunks + (lane & (kChunks - 1));
-        const float ks = __shfl_sync(0xffffffffu, cur.ks, n & 31);
-        const float vs = __shfl_sync(0xffffffffu, cur.vs, n & 31);
-        if (lane < kChunks)
-          sm.scale[t % C::NS][lane] = make_float4(ks, __log2f(vs), 1.f / vs, 0.f);
+        if (mine) sm.scale[t % C::NS][chunk] = cur.scale;
         __syncwarp();
       }
       if (lane == 0 && (CODES || !values)) mbar_expect_tx(bar, CODES ? BN * DH : 2 * NH * HT);
-      const CUtensorMap* map = values ? &mV : &mK;
-      for (int x = 0; x < boxes; ++x) {
-        const int n = t * kChunks + per * x;
-        const int slab = __shfl_sync(0xffffffffu, now ? cur.slab : prv.slab, n & 31);
-        const int y = ((tb + t) * BN + box * x) & (a.page.T - 1);
-        if (lane == 0) {
-          for (int h = 0; h < (CODES ? 1 : NH); ++h)
-            tma_load_3d(dst + h * HT + box * x * (CODES ? DH : 128), map, bar, 64 * h, y, slab);
-        }
+      if (mine && asks) {
+        uint8_t* dst = (CODES ? sm.item[it] : sm.kv[values ? C::v_tile(s) : C::k_tile(s)][0]) + to;
+        const CUtensorMap* map = values ? &mV : &mK;
+        const int y = (page_y + t * turn_y) & (a.page.T - 1);
+        tma_load_3d(dst, map, bar, 0, y, slab);
+        if (!CODES && NH == 2) tma_load_3d(dst + HT, map, bar, 64, y, slab);
       }
       ni = i + 1;
-      nk = t + 1;
+      if (!values) nk = t + 1;
       return true;
     });
     if (lane == 0) {  // what is under way has to land before the block ends
