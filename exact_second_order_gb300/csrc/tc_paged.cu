@@ -41,7 +41,9 @@ struct Cfg {
   static constexpr int BN = DH == 64 ? 128 : 64;  // keys of a tile
   static constexpr int kChunks = BN / 16;         // 16 keys lie on one page
   static constexpr uint32_t HT = BN * 64 * 2;     // bytes of 64 columns of a tile
-  static constexpr int NBUF = DH == 64 ? 3 : 4;   // score buffers: O~ takes the rest of TMEM
+  // Score buffers (O~ takes the rest of TMEM).  With MT = 1 a fourth asks for keys so early
+  // that the ring has none under way: 82 us for 99 at B2 H16 Hkv4 N1000 of 5000 keys d128.
+  static constexpr int NBUF = DH == 64 || MT == 1 ? 3 : 4;
   // Tiles of keys and of values as operands, and of codes on their way there.  Where they
   // arrive and leave together (kJoint) the MMA warp waits and commits less; converters,
   // which work in order, want slots of their own for keys that are asked for earlier.
@@ -60,8 +62,9 @@ struct Cfg {
   static constexpr int NS = 16;
   static_assert(NS >= NI / 2 + kLead + NK + NBUF, "scales");
   // Elementwise warps 0 - 7, converters (codes), loads, MMA.  With two converters the
-  // elementwise threads have 168 registers, with four 128.
-  static constexpr int kConv = CODES ? 2 : 0, kLoad = 8 + kConv, kMma = kLoad + 1, kThreads = 32 * (kMma + 1);
+  // elementwise threads have 168 registers, with four 128: MT = 2 1416 us for 1445 at four
+  // prompts of 2048 behind 14336, MT = 1, with twice the tiles a product, 128 for 122 above.
+  static constexpr int kConv = !CODES ? 0 : MT == 2 ? 2 : 4, kLoad = 8 + kConv, kMma = kLoad + 1, kThreads = 32 * (kMma + 1);
   static_assert(2 * DH + NBUF * BN <= 512, "TMEM columns");
   // In the order of Order the slot that a tile takes is free without any later one: keys
   // of tile t need the scores of t - NK, values the products of t - NV, which need no keys
@@ -268,7 +271,8 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
   const int row = row0 + r + (MT == 2 ? BM * wg : 0);
   if (warp < 8) {
     gr = group_row(a, b, hkv, row, rows);
-    warp_hull(gr.v, row < rows, lane, sm.hull[warp]);
+    // Rows that see nothing (padding of a batch) do not make every tile a masked one.
+    warp_hull(gr.v, row < rows && gr.v.hi > 0, lane, sm.hull[warp]);
   }
   tc_fence_before();
   __syncthreads();
@@ -525,6 +529,9 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       fence_proxy_async_smem();
       return true;
     };
+    // A row that sees nothing, whatever its Q is: all its weights are 0 (or NaN), and O is
+    // not taken from them.
+    const bool blind = hi <= 0;
     float m = -INFINITY, l = 0.f;
     int n = 0;  // units of this warpgroup
     for (int u = wg; u < U; u += 2, ++n) {
@@ -564,7 +571,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       }
       load(0);
       mt = fmaxf(mt, max_of(0));
-      const bool raise = mt > m + kRescale;
+      const bool raise = !blind && mt > m + kRescale;
       const float fac = raise ? (m == -INFINITY ? 0.f : ex2_approx(m - mt)) : 1.f;
       if (raise) {
         l *= fac;
@@ -592,7 +599,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
           tmem_st8(acc_own + 16 * c + 8, w1);
         }
       }
-      const float base = m == -INFINITY ? 0.f : m;  // nothing seen so far: all weights 0
+      const float base = blind ? INFINITY : m == -INFINITY ? 0.f : m;  // nothing seen so far: 0
 #pragma unroll
       for (int c = 0; c < BN; c += 64) {
         if (c > 0) load(c);
@@ -627,7 +634,8 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       s1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - mm);
       lsum = s0 * sm.part_l[0][r] + s1 * sm.part_l[1][r];
     }
-    const bool any0 = T > 0, any1 = MT == 1 && T > 1;
+    if (blind) lsum = 0.f;
+    const bool any0 = T > 0 && !blind, any1 = MT == 1 && T > 1 && !blind;
     const float inv = splits > 1 ? 1.f : lsum > 0.f ? 1.f / lsum : 0.f;
     s0 = any0 ? s0 * inv : 0.f;
     s1 = any1 ? s1 * inv : 0.f;
@@ -734,10 +742,12 @@ cudaError_t launch(const PagedAttnArgs& a, int splits) {
   return a.page.e4m3 ? launch<DH, MT, true>(a, splits) : launch<DH, MT, false>(a, splits);
 }
 
-// 256 rows a block where such blocks fill the GPU; below, 128.
+// 256 rows a block where such blocks have three quarters of the SMs or more; below, 128
+// (1024 rows of 32 heads behind 4096 keys, d128 e4m3: 89 us for 133; half as many rows 90
+// for 78).
 bool two_blocks(const PagedAttnArgs& a) {
   const long long rows = static_cast<long long>(a.H / a.Hkv) * a.Nq;
-  return rows > BM && static_cast<long long>(a.B) * a.Hkv * ((rows + 255) / 256) >= kSMs;
+  return rows > BM && static_cast<long long>(a.B) * a.Hkv * ((rows + 255) / 256) >= kSMs * 3 / 4;
 }
 
 }  // namespace
