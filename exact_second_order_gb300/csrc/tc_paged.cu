@@ -737,17 +737,16 @@ cudaError_t launch(const PagedAttnArgs& a, int splits) {
                      : launch<DH, MT, CODES, false, false>(a, splits));
 }
 
-template <int DH, int MT>
-cudaError_t launch(const PagedAttnArgs& a, int splits) {
-  return a.page.e4m3 ? launch<DH, MT, true>(a, splits) : launch<DH, MT, false>(a, splits);
-}
-
-// 256 rows a block where such blocks have three quarters of the SMs or more; below, 128
-// (1024 rows of 32 heads behind 4096 keys, d128 e4m3: 89 us for 133; half as many rows 90
-// for 78).
+// 256 rows a block at d = 128 where such blocks have three quarters of the SMs or more (1024
+// rows of 32 heads behind 4096 keys, e4m3: 89 us for 126 with 128 rows; half as many rows 90
+// for 75).  At d = 64 only with codes, whose conversion is shared, and from one and a half
+// waves on (2048 rows of 32 heads behind 14336 keys: 341 for 433; 16-bit 292 for 298; four
+// windows of 1024 keys, 192 such blocks, 69 for 61, 16-bit 65 for 52).
 bool two_blocks(const PagedAttnArgs& a) {
   const long long rows = static_cast<long long>(a.H / a.Hkv) * a.Nq;
-  return rows > BM && static_cast<long long>(a.B) * a.Hkv * ((rows + 255) / 256) >= kSMs * 3 / 4;
+  const long long blocks = static_cast<long long>(a.B) * a.Hkv * ((rows + 255) / 256);
+  return rows > BM && (a.d == 128 ? 4 * blocks >= 3 * kSMs
+                                  : a.page.e4m3 && 2 * blocks >= 3 * kSMs);
 }
 
 }  // namespace
@@ -767,8 +766,15 @@ int tc_paged_splits(const PagedAttnArgs& a) {
 cudaError_t tc_paged(const PagedAttnArgs& a) {
   const int splits = tc_paged_splits(a);
   cudaError_t e;
-  if (a.d == 64) e = two_blocks(a) ? launch<64, 2>(a, 1) : launch<64, 1>(a, splits);
-  else e = two_blocks(a) ? launch<128, 2>(a, 1) : launch<128, 1>(a, splits);
+  const bool two = two_blocks(a);
+  if (a.d == 64)
+    e = two              ? launch<64, 2, true>(a, 1)
+        : a.page.e4m3    ? launch<64, 1, true>(a, splits)
+                         : launch<64, 1, false>(a, splits);
+  else if (a.page.e4m3)
+    e = two ? launch<128, 2, true>(a, 1) : launch<128, 1, true>(a, splits);
+  else
+    e = two ? launch<128, 2, false>(a, 1) : launch<128, 1, false>(a, splits);
   return e == cudaSuccess && splits > 1 ? attn_join(a, splits) : e;
 }
 
