@@ -24,9 +24,13 @@ using namespace paged;
 // token slots of eight lanes (E8 times eight elements each), TG tokens a slot, and where
 // the tokens are few HS slots beside each other for different heads.  A lane keeps its
 // tokens' angles in shared memory and walks the heads with E8 TG HB = 4 such eights in
-// flight; the page's largest magnitude meets in shuffles and, across warps, in shared memory, and the rows
-// are turned again for their codes (cheaper than to keep them: 64 registers and two
-// blocks an SM).  Every element is read and written once: memory bounds it.
+// flight; the page's largest magnitude meets in shuffles and, across warps, in shared
+// memory, and the rows are turned again for their codes (cheaper than to keep them: 64
+// registers and two blocks an SM).  Every element is read and written once.
+// Measured (two prompts of 8192 tokens, H32 Hkv8 d128, e4m3): 88 us, 4.2 TB/s of the 369 MB,
+// 62% of the copy rate.  It is bound by the bytes in flight and by issue (54% of the slots):
+// four eights with the next four behind them and 119 registers 118 us, sixteen lanes a row
+// 107, questions asked lane by lane (KIND 1) 105.
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 512;
 constexpr int kInFlight = 4;

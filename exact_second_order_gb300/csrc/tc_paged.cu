@@ -10,18 +10,26 @@
 //
 // As in the dense kernel, two elementwise warpgroups work on score tiles in TMEM, P~
 // takes the scores' place as the A operand of P~ V, and one thread issues the MMAs.
-// The tiles' producer is different: e4m3 has no MMA with a 16-bit partner, so a
-// warpgroup takes 16-byte runs of codes from the pages (two tiles ahead, in
-// registers), turns them into fp16 and stores them in the operands' swizzled layout;
-// a bf16 cache goes there by asynchronous copies.  Rows outside the hull of what the
-// block sees, and pages outside the pool, become zeros on the way.
+// One warp looks up the pages, 32 chunks of 16 keys at a time, one a lane, and each lane
+// asks for the boxes of its own chunks; a page outside the pool is a slab past the end,
+// which TMA fills with zeros.  e4m3 has no MMA with a 16-bit partner, so its boxes land
+// in a ring of codes, and converter warps turn them into fp16 in the operands' swizzled
+// layout, keys so many tiles ahead of values as the MMA warp asks for them (in_order).  They
+// load nothing from global memory themselves: the proxy fence behind their stores waits
+// for every load of the thread that is under way (with the next tiles' codes in registers
+// the kernel took 854 us, with more of them 1037, with the ring 452 in the end).
 //   MT = 2: 256 group rows a block, warpgroup w holds rows 128 w .., so that a
 //     converted tile feeds twice the products.
 //   MT = 1: 128 rows, the warpgroups take alternate key tiles and merge their (m, l,
 //     O~) at the end; few blocks are also cut along the keys and joined by a second
 //     launch.
-// Key tiles have 128 keys: a score MMA with N = 64 costs 48 cycles for 32 of products,
-// with N = 128 64 for 64.
+// Measured (H32 Hkv8 d128, 2048 rows behind 14336 keys): 452 us, 1141 TFLOP/s, in 1.7 waves;
+// dense bf16 keys 429.  Four such prompts, padded, 1318 us, a bf16 cache 1111, dense keys
+// 1109 to 1125.  At d = 128 the MMAs of 64-key tiles cost 641 cycles for 512 of products and
+// shared memory gives them 100 of its 128 bytes a cycle: the converters' 32 KB a tile take
+// most of the rest, and 52% of the tensor pipe's cycles are busy (16-bit caches 64%).  Tiles
+// of 128 keys would cost less, but with two score buffers only a warpgroup waits for its
+// MMAs (749 us before the ring).
 #include "paged.cuh"
 #include "tc_attn.cuh"
 
@@ -66,7 +74,7 @@ struct Cfg {
   // prompts of 2048 behind 14336, MT = 1, with twice the tiles a product, 128 for 122 above.
   static constexpr int kConv = !CODES ? 0 : MT == 2 ? 2 : 4, kLoad = 8 + kConv, kMma = kLoad + 1, kThreads = 32 * (kMma + 1);
   static_assert(2 * DH + NBUF * BN <= 512, "TMEM columns");
-  // In the order of Order the slot that a tile takes is free without any later one: keys
+  // In the order of in_order the slot that a tile takes is free without any later one: keys
   // of tile t need the scores of t - NK, values the products of t - NV, which need no keys
   // beyond those of t - NV + kLead.
   static_assert(NK >= 2 && NV >= 2 && (!kJoint || NBUF <= MT * NK), "rings");
