@@ -71,8 +71,9 @@ struct Cfg {
   static_assert(NS >= NI / 2 + kLead + NK + NBUF, "scales");
   // Elementwise warps 0 - 7, converters (codes), loads, MMA.  With two converters the
   // elementwise threads have 168 registers, with four 128: MT = 2 1416 us for 1445 at four
-  // prompts of 2048 behind 14336, MT = 1, with twice the tiles a product, 128 for 122 above.
-  static constexpr int kConv = !CODES ? 0 : MT == 2 ? 2 : 4, kLoad = 8 + kConv, kMma = kLoad + 1, kThreads = 32 * (kMma + 1);
+  // prompts of 2048 behind 14336; MT = 1, with twice the tiles a product, 128 for 122 above.
+  static constexpr int kConv = !CODES ? 0 : MT == 2 ? 2 : 4;
+  static constexpr int kLoad = 8 + kConv, kMma = kLoad + 1, kThreads = 32 * (kMma + 1);
   static_assert(2 * DH + NBUF * BN <= 512, "TMEM columns");
   // In the order of in_order the slot that a tile takes is free without any later one: keys
   // of tile t need the scores of t - NK, values the products of t - NV, which need no keys
@@ -110,8 +111,8 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Scores of 64 columns from jbase on, 16 of a page each.  CAP: `s` holds raw products
-// times tau / cap, and where `turned` their tanh.
+// Scores of 64 columns from jbase on, 16 of a page each.  CAP: `s` holds products times
+// tau / cap (scale), and for `weights`, and with a bias for `largest`, their tanh.
 template <bool CODES, bool CAP, bool BIAS>
 struct PagedScore {
   Score<CAP, BIAS> sc;
@@ -445,8 +446,8 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
     in_order<C::kLead>(T, [&](int i, int t, bool values) {
       const int N = values ? NV : NK, s = t % N, it = i % (C::NI + !CODES);
       const bool ok = wait_warp(&sm.i_full[it], (i / (C::NI + !CODES)) & 1, abort_flag, err) &&
-           (t < N || wait_warp(values ? &sm.v_empty[s] : &sm.k_empty[s], ((t / N) - 1) & 1,
-                               abort_flag, err));
+                      (t < N || wait_warp(values ? &sm.v_empty[s] : &sm.k_empty[s],
+                                          ((t / N) - 1) & 1, abort_flag, err));
       if (!ok) return false;
       const uint32_t src = smem_u32(sm.item[it]) + from;
       const uint32_t dst = smem_u32(sm.kv[values ? C::v_tile(s) : C::k_tile(s)][0]);
