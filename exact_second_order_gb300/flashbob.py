@@ -98,13 +98,18 @@ def _ready() -> ctypes.CDLL:
     return _bound
 
 
+_dtype_codes = {}  # filled once torch is bound
+
+
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.float32:
-        return FLASHBOB_F32
-    if t.dtype == torch.bfloat16:
-        return FLASHBOB_BF16
-    raise TypeError(f"unsupported input dtype {t.dtype}")
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
+        import torch
+        _dtype_codes.update({torch.float32: FLASHBOB_F32, torch.bfloat16: FLASHBOB_BF16})
+        code = _dtype_codes.get(t.dtype)
+        if code is None:
+            raise TypeError(f"unsupported input dtype {t.dtype}")
+    return code
 
 
 def _stream_handle(stream) -> int | None:
@@ -284,6 +289,11 @@ def _check_tensor(where: str, name: str, t, shape, dtype, index: int) -> None:
     if t.dtype is not dtype:
         raise TypeError(f"{where}: {name} is {t.dtype}, expected {dtype}")
     raise ValueError(f"{where}: {name} must be contiguous")
+
+
+def _check_contiguous(where: str, name: str, t) -> None:
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous")
 
 
 def _check_sizes(where: str, *sizes: int) -> None:
@@ -553,7 +563,7 @@ def _check_norm(where: str, QKV, wq, wk, freqs, positions):
     """Checks of the norm-and-rotation calls; returns the device and B, N, the
     heads, d, R, axes."""
     index = _cuda_index(where, "QKV", QKV, "[B, N, H + 2 Hkv, d]", 4)
-    _check_tensor(where, "QKV", QKV, QKV.shape, QKV.dtype, index)
+    _check_contiguous(where, "QKV", QKV)
     B, N, heads, d = QKV.shape
     _check_sizes(where, B, N, heads, d)
     R, axes = 0, 1
@@ -902,12 +912,12 @@ def attention_paged(Q, cache, table, tau: float, cap: float = 0.0, slopes=None, 
     sees of them); allocates them, and the workspace, on Q's device."""
     lib, where = _bound or _ready(), "attention_paged"
     index = _cuda_index(where, "Q", Q, "[B, H, Nq, d]", 4)
-    B, H, Nq, d = shape = Q.shape
+    B, H, Nq, d = Q.shape
     M = _check_paged(where, "Q", Q, cache, table, B)
     if d != cache.d:
         raise ValueError(f"{where}: Q has heads of {d}, the cache of {cache.d}")
     _check_sizes(where, B, H, Nq)
-    _check_tensor(where, "Q", Q, shape, Q.dtype, index)
+    _check_contiguous(where, "Q", Q)
     if slopes is not None:
         _check_tensor(where, "slopes", slopes, (H,), torch.float32, index)
     if ranges is not None:
