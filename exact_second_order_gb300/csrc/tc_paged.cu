@@ -73,6 +73,10 @@ struct Cfg {
   // elementwise threads have 168 registers, with four 128: MT = 2 1416 us for 1445 at four
   // prompts of 2048 behind 14336; MT = 1, with twice the tiles a product, 128 for 122 above.
   static constexpr int kConv = !CODES ? 0 : MT == 2 ? 2 : 4;
+  // Of four, two turn keys and two values, neither waiting for the other's slots (500 rows of
+  // 32 heads behind 4620 keys, d128: 75 us in turn, 67 in teams).
+  static constexpr bool kTeams = kConv == 4;
+  static constexpr int kTeam = kTeams ? 2 : kConv;  // converters of an item
   static constexpr int kLoad = 8 + kConv, kMma = kLoad + 1, kThreads = 32 * (kMma + 1);
   static_assert(2 * DH + NBUF * BN <= 512, "TMEM columns");
   // In the order of in_order the slot that a tile takes is free without any later one: keys
@@ -256,10 +260,10 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
 
   if (splits > 1) release_next();
   if (threadIdx.x == 0) {
-    constexpr int kFull = CODES ? C::kConv : 1;
+    constexpr int kFull = CODES ? C::kTeam : 1;
     for (int s = 0; s < NK; ++s) mbar_init(&sm.k_full[s], kFull), mbar_init(&sm.k_empty[s], 1);
     for (int s = 0; s < NV; ++s) mbar_init(&sm.v_full[s], kFull), mbar_init(&sm.v_empty[s], 1);
-    for (int s = 0; s < C::NI; ++s) mbar_init(&sm.i_full[s], 1), mbar_init(&sm.i_empty[s], C::kConv);
+    for (int s = 0; s < C::NI; ++s) mbar_init(&sm.i_full[s], 1), mbar_init(&sm.i_empty[s], C::kTeam);
     for (int s = 0; s < NBUF; ++s) mbar_init(&sm.sc_full[s], 1), mbar_init(&sm.op_ready[s], 4);
     mbar_init(&sm.pv_done[0], 1);
     mbar_init(&sm.pv_done[1], 1);
@@ -433,8 +437,9 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
     }
     __syncwarp();
   } else if (CODES && warp >= 8) {
-    const int tid = threadIdx.x - 256;
-    using F = Feed<DH, 32 * C::kConv + !CODES * 128>;
+    const bool of_values = warp >= 8 + C::kTeam;  // of two teams
+    const int tid = threadIdx.x - 256 - (of_values ? 32 * C::kTeam : 0);
+    using F = Feed<DH, CODES ? 32 * C::kTeam : 128>;
     const F f(tid);
     constexpr int kRuns = BN / F::kStep, kStep = F::kStep;
     static_assert(kStep % 8 == 0, "a thread's runs have one place in the swizzles");
@@ -444,6 +449,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
     const uint32_t from =
         f.row0 * DH + ((f.col ^ (DH == 128 ? f.row0 & 7 : (f.row0 >> 1) & 3)) << 4);
     in_order<C::kLead>(T, [&](int i, int t, bool values) {
+      if (C::kTeams && values != of_values) return true;
       const int N = values ? NV : NK, s = t % N, it = i % (C::NI + !CODES);
       const bool ok = wait_warp(&sm.i_full[it], (i / (C::NI + !CODES)) & 1, abort_flag, err) &&
                       (t < N || wait_warp(values ? &sm.v_empty[s] : &sm.k_empty[s],
