@@ -446,30 +446,37 @@ cudaError_t append(const AppendArgs& a) {
 constexpr int kReadThreads = 256;
 constexpr int kReadRuns = 4;  // in flight of each thread
 
-__device__ __forceinline__ void st32(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
+// 32 bytes at p, which is 32-byte aligned (`wide`) or 16-byte aligned.
+__device__ __forceinline__ void st32(void* p, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    uint4* q = static_cast<uint4*>(p);
+    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
-__device__ __forceinline__ void st16(__nv_bfloat16* p, const float (&f)[16]) {
+__device__ __forceinline__ void st16(__nv_bfloat16* p, const float (&f)[16], bool wide) {
   uint32_t w[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) w[k] = tc::pack_bf16x2(f[2 * k], f[2 * k + 1]);
-  st32(p, w);
+  st32(p, w, wide);
 }
-__device__ __forceinline__ void st16(float* p, const float (&f)[16]) {
+__device__ __forceinline__ void st16(float* p, const float (&f)[16], bool wide) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t w[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(f[8 * h + k]);
-    st32(p + 8 * h, w);
+    st32(p + 8 * h, w, wide);
   }
 }
 
 template <typename T, bool CODES, bool VEC>
 __global__ void __launch_bounds__(kReadThreads)
-    read_kernel(const __grid_constant__ ReadArgs a, int runs, int blocks) {
+    read_kernel(const __grid_constant__ ReadArgs a, int runs, int blocks, bool wide) {
   constexpr int E = !VEC ? 1 : CODES ? 16 : 16 / static_cast<int>(sizeof(T));
   const int g = blockIdx.x / blocks, b = g / a.Hkv, hkv = g % a.Hkv;
   const int per = kReadThreads / runs, r = threadIdx.x / runs, k = threadIdx.x % runs * E;
@@ -513,7 +520,7 @@ __global__ void __launch_bounds__(kReadThreads)
     }
     // 16 values: one store of 32 bytes, or two (four of 8 bytes, a quarter of each sector
     // at a time: 221 us for four requests of 32768 tokens of 8 heads of 128, now 116, 94%
-    // of the copy rate).
+    // of the copy rate); 16 bytes a store where Kd or Vd is only that far aligned.
     float f[16];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -521,7 +528,7 @@ __global__ void __launch_bounds__(kReadThreads)
       f[4 * q] = lo.x * scale[u], f[4 * q + 1] = lo.y * scale[u];
       f[4 * q + 2] = hi.x * scale[u], f[4 * q + 3] = hi.y * scale[u];
     }
-    st16(o, f);
+    st16(o, f, wide);
   }
 }
 
@@ -532,8 +539,10 @@ cudaError_t read(const ReadArgs& a) {
   const long long blocks = (static_cast<long long>(a.Nk) + rows - 1) / rows;
   const long long grid = blocks * a.B * a.Hkv;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+  // Rows of 16 values keep the alignment of the first one.
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.Kd) | reinterpret_cast<uintptr_t>(a.Vd)) & 31) == 0;
   read_kernel<T, CODES, VEC><<<dim3(static_cast<unsigned>(grid), 2), kReadThreads, 0, a.stream>>>(
-      a, runs, static_cast<int>(blocks));
+      a, runs, static_cast<int>(blocks), wide);
   return cudaGetLastError();
 }
 
