@@ -123,8 +123,11 @@ struct PagedScore {
   float c1;  // not capped: log2 units a product; capped: tau / cap
   float c2;
 
-  __device__ __forceinline__ PagedScore(const AttnArgs& a, float slope, float grow) : sc(a, slope) {
-    c1 = sc.c1 * grow;
+  // `blind`: of a row that sees nothing.  Its tiles need not run masked, so its products, 0
+  // or NaN here, must take no part in a warp's vote on the form of tanh.
+  __device__ __forceinline__ PagedScore(const AttnArgs& a, float slope, float grow, bool blind)
+      : sc(a, slope) {
+    c1 = CAP && blind ? 0.f : sc.c1 * grow;
     c2 = sc.c2;
     sc.c1 = 1.f;  // its tanh is of products that are scaled already
     sc.a1 = kTanh[0], sc.a2 = kTanh[1], sc.a3 = kTanh[2];
@@ -532,7 +535,10 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       fence_proxy_async_smem();
       warp_arrive(&sm.q_ready);
     }
-    const PagedScore<CODES, CAP, BIAS> score(a, gr.slope2, grow);
+    // A row that sees nothing, whatever its Q is: all its weights are 0 (or NaN), and O is
+    // not taken from them.
+    const bool blind = hi <= 0;
+    const PagedScore<CODES, CAP, BIAS> score(a, gr.slope2, grow, blind);
     const bool any_row = row0 + (MT == 2 ? BM * wg : 0) + quad * 32 < rows;
     // Values that no row of the block sees meet P~ = 0: make them 0 too (codes are
     // already).
@@ -544,9 +550,6 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       fence_proxy_async_smem();
       return true;
     };
-    // A row that sees nothing, whatever its Q is: all its weights are 0 (or NaN), and O is
-    // not taken from them.
-    const bool blind = hi <= 0;
     float m = -INFINITY, l = 0.f;
     int n = 0;  // units of this warpgroup
     for (int u = wg; u < U; u += 2, ++n) {
