@@ -199,7 +199,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     const float2 ml = p.ml[s * rows + row];
     // A split that saw no key has m_s = -inf and O_s = 0.
     const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
-    l = fmaf(w, ml.y, l);
+    // The reference of a cache in 8 bits holds its pages' scales, so that sums of weights
+    // that count may be further apart than fp32's least 2^-126: far factors in two steps.
+    // (Elsewhere such a part does not reach the sum's last bit.)
+    const float far = fminf(ml.x - m + 100.f, 0.f);
+    l = far < 0.f && ml.x != -INFINITY ? fmaf(0x1p-100f, ml.y * exp2f(far), l) : fmaf(w, ml.y, l);
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       if (lane + 32 * c < d) acc[c] = fmaf(w, p.o[(s * rows + row) * d + lane + 32 * c], acc[c]);

@@ -12,6 +12,7 @@
 #include <cuda_fp8.h>
 
 #include "attn_common.cuh"
+#include "tc_common.cuh"
 
 namespace flashbob {
 namespace paged {
@@ -39,6 +40,27 @@ __device__ __forceinline__ float scale_for(float most) {
 // A scale that a page has, whatever the array holds.
 __device__ __forceinline__ float held_scale(float s) {
   return fminf(fmaxf(s, 0x1p-60f), 0x1p60f);
+}
+
+// The weights of the tensor-core forms are p = exp2(x + log2 s_V - R), with R >= the
+// largest x + log2 s_V - 8, and a row's sum is that of exp2(x - R).  So a sum is at least
+// the largest scale's inverse, 2^-60; but p of a page with a small scale s_V falls below
+// fp32's least 2^-126 where exp2(x - R) is still 2^-126 / s_V, and that may be most of the
+// sum (pages of zeros have the least scale, 2^-60).  For few rows p is a square there,
+// whose root does not leave fp32's reach.  For many, where every exponential counts,
+// p / s_V is added for scales from 2^-20 on (what it loses is 2^-46 of the sum at most:
+// nothing that a row of 2^20 keys would notice), and the others get a second exponential.
+constexpr float kLeastLog = -20.f;
+
+// Parts of a row meet with factors 2^d (d <= 0).  References hold their pages' scales, so
+// a part may count although its factor is below 2^-126; then it takes two: `far` is 2^d, at
+// least 2^-100, and `rest` what is missing, 1 for all that are nearer.  The products with V
+// need `far` alone: what 2^-100 leaves of them is nothing beside the nearer part's.
+struct PartFactor {
+  float far, rest;
+};
+__device__ __forceinline__ PartFactor part_factor(float d) {
+  return {tc::ex2_approx(fmaxf(d, -100.f)), tc::ex2_approx(fminf(d + 100.f, 0.f))};
 }
 
 // |x| for the largest magnitude: NaN and infinity do not count.

@@ -2,7 +2,7 @@
 // 128, pages in e4m3 or bf16, up to 32 group rows (single tokens, drafted ones).
 //   S^T = K Q^T,  x = score(S) (scale, cap, bias; log2 units),
 //   y = x + log2 s_V,  p = exp2(y - R) with a running reference R >= max y - 8,
-//   l = sum p / s_V,  O^T = (sum V^T p) / l,  L = (R + log2 l) ln 2,
+//   l = sum exp2(x - R),  O^T = (sum V^T p) / l,  L = (R + log2 l) ln 2,
 // where K and V are a page's codes: the scale of the keys goes into the scores, that
 // of the values into the exponent of the weights, so that a product's operands are
 // codes (exact in fp16) and weights of at most 2^8 (16 bits each, 11 significant),
@@ -424,9 +424,11 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
           m = fmaxf(R[nt][e], m);
-          const float f = R[nt][e] == -INFINITY ? 0.f : ex2_approx(R[nt][e] - m);
+          const PartFactor pf = part_factor(R[nt][e] - m);
+          const float f = R[nt][e] == -INFINITY ? 0.f : pf.far;
           R[nt][e] = m;
           l[nt][e] *= f;
+          if (CODES) l[nt][e] *= pf.rest;
 #pragma unroll
           for (int i = 0; i < C::kMT; ++i) {
             O[nt][i][e] *= f;
@@ -441,10 +443,12 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float base = R[nt][e & 1] == -INFINITY ? 0.f : R[nt][e & 1];  // nothing seen yet
-        p[e] = ex2_approx(S[nt][e] - base);
+        // Codes: as a square, whose root lasts where p is below 2^-126 (paged.cuh).  A
+        // branch for pages with small scales took as long or longer.
+        p[e] = ex2_approx(CODES ? 0.5f * (S[nt][e] - base) : S[nt][e] - base);
+        l[nt][e & 1] = fmaf(CODES ? p[e] * inv_vs : 1.f, p[e], l[nt][e & 1]);
+        if (CODES) p[e] *= p[e];
       }
-      l[nt][0] = fmaf(inv_vs, p[0] + p[2], l[nt][0]);
-      l[nt][1] = fmaf(inv_vs, p[1] + p[3], l[nt][1]);
       pb[nt][0] = transpose8(pack<CODES>(p[0], p[1]));
       pb[nt][1] = transpose8(pack<CODES>(p[2], p[3]));
     }
@@ -554,9 +558,11 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       const float* p = w0 + w * kStep;
-      const float r = p[kRL + row], f = r == -INFINITY ? 0.f : ex2_approx(r - m[i]);
+      const float r = p[kRL + row];
+      const PartFactor pf = part_factor(r - m[i]);
+      const float f = r == -INFINITY ? 0.f : pf.far;
       const float4 v = *reinterpret_cast<const float4*>(p + row * C::kPitch + c);
-      sum[i] = fmaf(f, p[kRL + kRowsPadded + row], sum[i]);
+      sum[i] = fmaf(f, p[kRL + kRowsPadded + row] * (CODES ? pf.rest : 1.f), sum[i]);
       o[i].x = fmaf(f, v.x, o[i].x), o[i].y = fmaf(f, v.y, o[i].y);
       o[i].z = fmaf(f, v.z, o[i].z), o[i].w = fmaf(f, v.w, o[i].w);
     }
@@ -589,8 +595,9 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
         const float4 ml = tc::ld_shared_cluster_f4(tc::mapa_shared(here + (kRL + 4 * row) * 4, q));
         const float4 v =
             tc::ld_shared_cluster_f4(tc::mapa_shared(here + (row * C::kPitch + c) * 4, q));
-        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m[i]);
-        sum[i] = fmaf(f, ml.y, sum[i]);
+        const PartFactor pf = part_factor(ml.x - m[i]);
+        const float f = ml.x == -INFINITY ? 0.f : pf.far;
+        sum[i] = fmaf(f, ml.y * (CODES ? pf.rest : 1.f), sum[i]);
         o[i].x = fmaf(f, v.x, o[i].x), o[i].y = fmaf(f, v.y, o[i].y);
         o[i].z = fmaf(f, v.z, o[i].z), o[i].w = fmaf(f, v.w, o[i].w);
       }

@@ -2,7 +2,7 @@
 // queries, head dim 64 or 128, pages in e4m3 or bf16.
 //   S = Q K^T,  y = score(S) + log2 s_V (scale, cap, bias; log2 units),
 //   P~ = exp2(y - m) with a running row reference m >= max y - 8,
-//   l = sum P~ / s_V,  O = (sum P~ V) / l,  L = (m + log2 l) ln 2,
+//   l = sum exp2(score(S) - m),  O = (sum P~ V) / l,  L = (m + log2 l) ln 2,
 // where K and V are a page's codes: s_K goes into the score of its 16-column chunks
 // and s_V into the exponent of their weights, so the MMAs' operands are codes (exact in
 // fp16) and weights of at most 2^8, however far the pages' scales are apart.  Q is
@@ -91,7 +91,9 @@ struct Smem {
   alignas(1024) uint8_t q[MT][C::NH][HALF_BLOCK];
   alignas(1024) uint8_t kv[C::NK + C::NV][C::NH][C::HT];
   alignas(1024) uint8_t item[C::NI > 0 ? C::NI : 1][C::NI > 0 ? C::BN * DH : 16];  // codes
-  float4 scale[C::NS][C::kChunks];  // s_K, log2 s_V, 1 / s_V of each chunk of a tile
+  // Of each chunk of a tile: s_K, log2 s_V, 1 / s_V or 0 (kLeastLog), and whether any chunk of
+  // the tile has 0 there.
+  float4 scale[C::NS][C::kChunks];
   float part_m[2][BM], part_l[2][BM];
   int hull[8][4];  // of each elementwise warp's rows
   uint64_t k_full[C::NK], k_empty[C::NK], v_full[C::NV], v_empty[C::NV];
@@ -204,6 +206,36 @@ struct PagedScore {
       tmem_st8(out + 8 * q, pk);
       l = CODES ? fmaf(chunk[q].z, acc.x + acc.y, l) : l + (acc.x + acc.y);
     }
+  }
+  // What the chunks of a tile with the least scales add to a row's sum, from the scores of
+  // their 16 columns in TMEM (from `at0` on), before weights take their place.  Rare, and a
+  // call: inlined it took the hot path's registers (capped prompts at d = 64 355 -> 387 us).
+  static __device__ __noinline__ float least(const PagedScore me, uint32_t at0,
+                                             const float4* chunk, int chunks, int jbase, int lo,
+                                             int hi, float dist, float m) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int q = 0; q < chunks; ++q) {
+      if (chunk[q].z != 0.f) continue;
+      uint32_t s[1][16];
+      tmem_ld16(at0 + 16 * q, s[0]);
+      tmem_wait_ld();
+      if (CAP) {
+        const float f = me.c1 * chunk[q].x;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[0][e] = __float_as_uint(f * u2f(s[0][e]));
+        me.sc.tanh_of(s, true);
+      }
+      const float f = me.factor(chunk[q]);
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const float2 y = me.at(f2(s[0][e], s[0][e + 1]), f, -m, dist + (16 * q + e));
+        const int j = jbase + 16 * q + e;
+        if (j >= lo && j < hi) sum += ex2_approx(y.x);
+        if (j + 1 >= lo && j + 1 < hi) sum += ex2_approx(y.y);
+      }
+    }
+    return sum;
   }
 };
 
@@ -364,7 +396,7 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
     // the copies fill with zeros) and its scales.
     struct Meta {
       int slab;
-      float4 scale;  // s_K, log2 s_V, 1 / s_V
+      float4 scale;  // as in Smem
     };
     const int chunks = T * kChunks, chunk0 = tb * kChunks;
     const int box = min(a.page.T, BN);  // keys of one copy
@@ -377,7 +409,8 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
           m.slab = page * a.Hkv + hkv;
           if (CODES) {
             const float vs = a.page.v_scale[m.slab];
-            m.scale = make_float4(a.page.k_scale[m.slab], __log2f(vs), 1.f / vs, 0.f);
+            const float lv = __log2f(vs);
+            m.scale = make_float4(a.page.k_scale[m.slab], lv, lv < kLeastLog ? 0.f : 1.f / vs, 0.f);
           }
         }
       }
@@ -414,7 +447,10 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       // Values may be of the batch before: the keys are nk - 1 tiles on.
       const int slab = values && t / kAhead != (nk - 1) / kAhead ? prv.slab : cur.slab;
       if (CODES && !values) {
-        if (mine) sm.scale[t % C::NS][chunk] = cur.scale;
+        const bool least = __any_sync(0xffffffffu, mine && cur.scale.z == 0.f);
+        if (mine)
+          sm.scale[t % C::NS][chunk] =
+              make_float4(cur.scale.x, cur.scale.y, cur.scale.z, least ? 1.f : 0.f);
         __syncwarp();
       }
       if (lane == 0 && (CODES || !values)) mbar_expect_tx(bar, CODES ? BN * DH : 2 * NH * HT);
@@ -590,9 +626,11 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       load(0);
       mt = fmaxf(mt, max_of(0));
       const bool raise = !blind && mt > m + kRescale;
-      const float fac = raise ? (m == -INFINITY ? 0.f : ex2_approx(m - mt)) : 1.f;
+      const PartFactor pf = part_factor(m - mt);
+      const float fac = raise ? (m == -INFINITY ? 0.f : pf.far) : 1.f;
       if (raise) {
         l *= fac;
+        if (CODES) l *= pf.rest;
         m = mt;
       }
       if (__any_sync(0xffffffffu, raise && fac < 1.f) && n > 0) {
@@ -618,6 +656,8 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
         }
       }
       const float base = blind ? INFINITY : m == -INFINITY ? 0.f : m;  // nothing seen so far: 0
+      if (CODES && __builtin_expect(chunk[0].w != 0.f, 0))
+        l += PagedScore<CODES, CAP, BIAS>::least(score, sc, chunk, kChunks, col0, lo, hi, dist, base);
 #pragma unroll
       for (int c = 0; c < BN; c += 64) {
         if (c > 0) load(c);
@@ -648,9 +688,11 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       named_bar_sync(1, 256);
       const float m0 = sm.part_m[0][r], m1 = sm.part_m[1][r];
       mm = fmaxf(m0, m1);
-      s0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - mm);
-      s1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - mm);
-      lsum = s0 * sm.part_l[0][r] + s1 * sm.part_l[1][r];
+      const PartFactor f0 = part_factor(m0 - mm), f1 = part_factor(m1 - mm);
+      s0 = m0 == -INFINITY ? 0.f : f0.far;
+      s1 = m1 == -INFINITY ? 0.f : f1.far;
+      lsum = CODES ? s0 * (sm.part_l[0][r] * f0.rest) + s1 * (sm.part_l[1][r] * f1.rest)
+                   : s0 * sm.part_l[0][r] + s1 * sm.part_l[1][r];
     }
     if (blind) lsum = 0.f;
     const bool any0 = T > 0 && !blind, any1 = MT == 1 && T > 1 && !blind;
