@@ -571,9 +571,8 @@ constexpr size_t kTileBytes = BT * kLd<DP> * sizeof(float);
 constexpr size_t kSquareBytes = BT * LP * sizeof(float);
 
 template <typename T, int DP, typename KEYS, typename ARGS>
-cudaError_t forward(const ARGS& a) {
+cudaError_t forward(const ARGS& a, int splits) {
   const int blocks = static_cast<int>((static_cast<long long>(a.H / a.Hkv) * a.Nq + BT - 1) / BT);
-  const int splits = simt_splits(a);
   const size_t smem = 3 * kTileBytes<DP> + kSquareBytes;
   const auto kernel = attn_kernel<T, DP, KEYS, ARGS>;
   cudaError_t e = tc_set_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
@@ -584,11 +583,11 @@ cudaError_t forward(const ARGS& a) {
 }
 
 template <typename T, typename KEYS, typename ARGS>
-cudaError_t forward(const ARGS& a) {
-  return a.d <= 32   ? forward<T, 32, KEYS>(a)
-         : a.d <= 64 ? forward<T, 64, KEYS>(a)
-         : a.d <= 96 ? forward<T, 96, KEYS>(a)
-                     : forward<T, 128, KEYS>(a);
+cudaError_t forward(const ARGS& a, int splits) {
+  return a.d <= 32   ? forward<T, 32, KEYS>(a, splits)
+         : a.d <= 64 ? forward<T, 64, KEYS>(a, splits)
+         : a.d <= 96 ? forward<T, 96, KEYS>(a, splits)
+                     : forward<T, 128, KEYS>(a, splits);
 }
 
 template <typename T, int DP>
@@ -615,16 +614,17 @@ cudaError_t backward(const AttnArgs& a) {
 }  // namespace
 
 cudaError_t simt_attn(const AttnArgs& a) {
-  return a.bf16 ? forward<__nv_bfloat16, DenseKeys<__nv_bfloat16>>(a)
-                : forward<float, DenseKeys<float>>(a);
+  const int splits = simt_splits(a);
+  return a.bf16 ? forward<__nv_bfloat16, DenseKeys<__nv_bfloat16>>(a, splits)
+                : forward<float, DenseKeys<float>>(a, splits);
 }
 
-cudaError_t simt_paged(const PagedAttnArgs& a) {
+cudaError_t simt_paged(const PagedAttnArgs& a, int splits) {
   if (a.page.e4m3)
-    return a.bf16 ? forward<__nv_bfloat16, PagedKeys<__nv_bfloat16, true>>(a)
-                  : forward<float, PagedKeys<float, true>>(a);
-  return a.bf16 ? forward<__nv_bfloat16, PagedKeys<__nv_bfloat16, false>>(a)
-                : forward<float, PagedKeys<float, false>>(a);
+    return a.bf16 ? forward<__nv_bfloat16, PagedKeys<__nv_bfloat16, true>>(a, splits)
+                  : forward<float, PagedKeys<float, true>>(a, splits);
+  return a.bf16 ? forward<__nv_bfloat16, PagedKeys<__nv_bfloat16, false>>(a, splits)
+                : forward<float, PagedKeys<float, false>>(a, splits);
 }
 
 cudaError_t simt_attn_grad(const AttnArgs& a) {

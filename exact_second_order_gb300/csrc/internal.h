@@ -207,7 +207,7 @@ cudaError_t cache_append(const AppendArgs& a);
 cudaError_t cache_read(const ReadArgs& a);
 size_t paged_workspace(const PagedAttnArgs& a);
 cudaError_t paged_attn(const PagedAttnArgs& a);
-cudaError_t simt_paged(const PagedAttnArgs& a);  // any d <= 128
+cudaError_t simt_paged(const PagedAttnArgs& a, int splits);  // any d <= 128
 bool tc_paged_supported(const PagedAttnArgs& a);  // bf16, d = 64 or 128
 int tc_paged_splits(const PagedAttnArgs& a);
 cudaError_t tc_paged(const PagedAttnArgs& a);

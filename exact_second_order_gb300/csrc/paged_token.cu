@@ -697,7 +697,13 @@ size_t paged_workspace(const PagedAttnArgs& a) {
 }
 
 cudaError_t paged_attn(const PagedAttnArgs& a) {
-  return token_supported(a) ? token_attn(a) : tc_paged_supported(a) ? tc_paged(a) : simt_paged(a);
+  // The tensor-core forms multiply sums of codes by tau / cap, the page's scale and Q's at
+  // once: fp32's smallest numbers times a cap beyond 2^80 would be seen in the scores.  A
+  // workspace is by sizes alone, so no runs of keys then.
+  if (a.page.e4m3 && a.cap > 0x1p80f) return simt_paged(a, 1);
+  return token_supported(a)      ? token_attn(a)
+         : tc_paged_supported(a) ? tc_paged(a)
+                                 : simt_paged(a, simt_splits(a));
 }
 
 }  // namespace flashbob

@@ -204,6 +204,8 @@ flashbob_status flashbob_attention_jvp(const void* Q, const void* K, const void*
  *   slopes: fp32 [H], |slopes[h] (pos_i - j)| below 2^60; NULL: no bias.  A
  *        constant: it has no gradient.
  *   tau, and where cap > 0 cap and tau / cap: within 2^-120 .. 2^120.
+ *   A row's largest score: below 2^26 in size (in 32 bits scores beyond that
+ *        are apart by more than weights can tell, and weights may overflow).
  *   Limits: as flashbob_prep; (H / Hkv) * Nq and Nk below 2^31 - 1024.
  *
  * flashbob_attention: O [B,H,Nq,d] of in_dtype, L [B,H,Nq] fp32.
@@ -352,7 +354,9 @@ flashbob_status flashbob_cache_read(const void* K, const void* V, const float* k
  * flashbob_attention over the keys and values of the pages, Nk = M T: the same
  * ranges, q_pos, slopes, tau, cap and causal, the same limits, and the same about
  * what nobody sees (the rest of a page, and pages behind the last token, may hold
- * anything).  One launch, and one more where the keys are cut into runs.
+ * anything).  With FLASHBOB_E4M3, tau (capped: tau / cap) times the largest
+ * magnitude of a query that sees a key: at most 2^60.  One launch, and one more where
+ * the keys are cut into runs.
  *   workspace: `forward` bytes of flashbob_attention_paged_workspace (may be NULL
  *        when that is 0); overwritten.
  */
