@@ -42,6 +42,7 @@ using namespace paged;
 constexpr int BM = kTcRows;
 constexpr uint32_t HALF_BLOCK = BM * 64 * 2;
 constexpr float kRescale = 8.f;
+constexpr float kLargeScore = 0x1p20f;  // from here on y and m are off by 1/16
 
 template <int DH, int MT, bool CODES>
 struct Cfg {
@@ -207,35 +208,47 @@ struct PagedScore {
       l = CODES ? fmaf(chunk[q].z, acc.x + acc.y, l) : l + (acc.x + acc.y);
     }
   }
-  // What the chunks of a tile with the least scales add to a row's sum, from the scores of
-  // their 16 columns in TMEM (from `at0` on), before weights take their place.  Rare, and a
-  // call: inlined it took the hot path's registers (capped prompts at d = 64 355 -> 387 us).
-  static __device__ __noinline__ float least(const PagedScore me, uint32_t at0,
-                                             const float4* chunk, int chunks, int jbase, int lo,
-                                             int hi, float dist, float m) {
-    float sum = 0.f;
+  // The same for a tile that has chunks of the least scales, whose part of l is summed apart
+  // (kLeastLog), or for scores so large that their rounding would be seen in y - m where the
+  // two are one fma: here y is rounded as it was for m, so that no weight is above 2^8.  A
+  // chunk of 16 columns at a time, from TMEM, and a call: inlined it took the hot path's
+  // registers (capped prompts at d = 64 355 -> 387 us).
+  static __device__ __noinline__ float careful(const PagedScore me, uint32_t tmem,
+                                               const float4* chunk, int chunks, int jbase, int lo,
+                                               int hi, float dist, float m, float l) {
 #pragma unroll 1
     for (int q = 0; q < chunks; ++q) {
-      if (chunk[q].z != 0.f) continue;
-      uint32_t s[1][16];
-      tmem_ld16(at0 + 16 * q, s[0]);
+      uint32_t s[1][16], pk[8];
+      tmem_ld16(tmem + 16 * q, s[0]);
       tmem_wait_ld();
+      const float4 c = chunk[q];
       if (CAP) {
-        const float f = me.c1 * chunk[q].x;
+        const float f = me.c1 * c.x;
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[0][e] = __float_as_uint(f * u2f(s[0][e]));
         me.sc.tanh_of(s, true);
       }
-      const float f = me.factor(chunk[q]);
+      const float f = me.factor(c);
+      const bool least = c.z == 0.f;
+      float sum = 0.f;
 #pragma unroll
       for (int e = 0; e < 16; e += 2) {
-        const float2 y = me.at(f2(s[0][e], s[0][e + 1]), f, -m, dist + (16 * q + e));
+        const float2 y = me.at(f2(s[0][e], s[0][e + 1]), f, c.y, dist + (16 * q + e));
         const int j = jbase + 16 * q + e;
-        if (j >= lo && j < hi) sum += ex2_approx(y.x);
-        if (j + 1 >= lo && j + 1 < hi) sum += ex2_approx(y.y);
+        const float x[2] = {y.x - m, y.y - m};
+        float p[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const bool seen = j + k >= lo && j + k < hi;
+          p[k] = seen ? ex2_approx(x[k]) : 0.f;
+          sum += !least ? p[k] : seen ? ex2_approx(x[k] - c.y) : 0.f;
+        }
+        pk[e >> 1] = pack<true>(p[0], p[1]);
       }
+      tmem_st8(tmem + 8 * q, pk);
+      l = least ? l + sum : fmaf(c.z, sum, l);
     }
-    return sum;
+    return l;
   }
 };
 
@@ -633,7 +646,13 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
         if (CODES) l *= pf.rest;
         m = mt;
       }
-      if (__any_sync(0xffffffffu, raise && fac < 1.f) && n > 0) {
+      // Tiles for careful().  Large references vote with the raised ones: a vote of their own
+      // is a wait between maximum and weights (2% at d = 128).
+      bool special = CODES && chunk[0].w != 0.f;
+      const bool large = CODES && m != -INFINITY && fabsf(m) > kLargeScore;
+      const bool any_raise = __any_sync(0xffffffffu, (raise && fac < 1.f) || large);
+      if (CODES && any_raise) special = special || __any_sync(0xffffffffu, large);
+      if (any_raise && n > 0) {
         // The products of this warpgroup's last unit.  S(u) was issued behind those of
         // unit u - NBUF, so of the barrier's phases only the last may be open.
         const int last = u - 2;
@@ -656,17 +675,20 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
         }
       }
       const float base = blind ? INFINITY : m == -INFINITY ? 0.f : m;  // nothing seen so far: 0
-      if (CODES && __builtin_expect(chunk[0].w != 0.f, 0))
-        l += PagedScore<CODES, CAP, BIAS>::least(score, sc, chunk, kChunks, col0, lo, hi, dist, base);
+      if (CODES && __builtin_expect(special, 0)) {
+        l = PagedScore<CODES, CAP, BIAS>::careful(score, sc, chunk, kChunks, col0, lo, hi, dist,
+                                                  base, l);
+      } else {
 #pragma unroll
-      for (int c = 0; c < BN; c += 64) {
-        if (c > 0) load(c);
-        if (!BIAS) score.sc.tanh_of(s, masked);
-        const float4* sca = chunk + c / 16;
-        if (masked)
-          score.template weights<true>(s, sca, col0 + c, lo, hi, dist + c, base, l, sc + c / 2);
-        else
-          score.template weights<false>(s, sca, col0 + c, lo, hi, dist + c, base, l, sc + c / 2);
+        for (int c = 0; c < BN; c += 64) {
+          if (c > 0) load(c);
+          if (!BIAS) score.sc.tanh_of(s, masked);
+          const float4* sca = chunk + c / 16;
+          if (masked)
+            score.template weights<true>(s, sca, col0 + c, lo, hi, dist + c, base, l, sc + c / 2);
+          else
+            score.template weights<false>(s, sca, col0 + c, lo, hi, dist + c, base, l, sc + c / 2);
+        }
       }
       ok = clear_hidden(t, col0);
       if (!ok) break;

@@ -70,3 +70,39 @@ def test_keys_of_zero(c, e, q, cap):
     Q, pools, values, table = build(c, q, 0)
     pools[0], values[0] = torch.zeros_like(pools[0]), torch.zeros_like(values[0])
     check(c, Q, pools, values, table, 2.0 ** e, cap)
+
+
+@pytest.mark.parametrize("e,q,k,cap,bias", [(12, 0, 0, 0, 0), (21, 0, 0, 0, 0), (12, 0, 0, 2.0 ** 20, 0), (12, 0, 0, 0, 2.0 ** 10),
+                                            (27, 0, 0, 0, 0), (27, 0, 0, 2.0 ** 60, 0), (40, 10, 0, 0, 0), (40, 10, 0, 0, 2.0 ** 40),
+                                            (40, 10, 0, 2.0 ** 60, 0), (20, 20, 40, 0, 0), (20, 20, 40, 0, 2.0 ** 40)])
+@pytest.mark.parametrize("c", CASES, ids=IDS)
+def test_scores_far_apart(c, e, q, k, cap, bias):
+    """Scores that fp32 holds to several units: the largest has all the weight."""
+    Q, pools, values, table = build(c, q, k)
+    B, H, Hkv, Nq, M, T, d = c[:7]
+    if c[8] is not E4M3 and e + q + k > 25:
+        return  # beyond what is asked of a 16-bit cache, as of dense keys
+    slopes = torch.full((H,), bias, device="cuda") if bias else None
+    q_pos = (M * T + torch.arange(Nq, device="cuda")).expand(B, Nq).int().contiguous()  # behind all keys
+    tau = 2.0 ** e
+    O, L = fb.attention_paged(Q, fb.PagedCache(*pools), table, tau, cap=cap, slopes=slopes, q_pos=q_pos)
+    ks, vs = (pag.dense(x, table).repeat_interleave(H // Hkv, dim=1) for x in values)
+    z = Q.double() @ ks.transpose(2, 3) * tau
+    # What 32-bit sums of the products and their roundings lose, here with a bias too.
+    err = (d + 8) * 2.0 ** -23 * (Q.double().abs() @ ks.abs().transpose(2, 3) * tau).amax(dim=3)
+    if cap:
+        z = cap * torch.tanh(z / cap)
+        err = err + z.abs().amax(dim=3) * 2.0 ** -20  # tanh's, relative (2^-21), and its factors'
+    if bias:
+        far = bias * (q_pos[:, None, :, None] - torch.arange(M * T, device="cuda")).double()
+        z = z - far
+        err = err + far.amax(dim=3) * 2.0 ** -22
+    top, at = z.topk(2, dim=3)
+    sure = top[..., 0] - top[..., 1] > 2 * err + 25
+    assert bool(sure.float().mean() > 0.5)
+    assert bool(((L.double() - top[..., 0]).abs() <= err + top[..., 0].abs() * 2.0 ** -21 + 12).all())
+    want = torch.gather(vs, 2, at[..., :1].expand(*at.shape[:3], vs.shape[3]))
+    assert bool(O.isfinite().all())
+    # The others' part: a weight of e^-25 at most each.
+    rest = M * T * math.exp(-25) * vs.abs().amax(dim=2)[:, :, None]
+    assert bool(((O.double() - want).abs() <= 2.0 ** -7 * want.abs() + rest)[sure].all())
