@@ -52,16 +52,18 @@ __device__ __forceinline__ float held_scale(float s) {
 // nothing that a row of 2^20 keys would notice), and the others get a second exponential.
 constexpr float kLeastLog = -20.f;
 
-// Parts of a row meet with factors 2^d (d <= 0).  References hold their pages' scales, so
-// a part may count although its factor is below 2^-126; then it takes two: `far` is 2^d, at
-// least 2^-100, and `rest` what is missing, 1 for all that are nearer.  The products with V
-// need `far` alone: what 2^-100 leaves of them is nothing beside the nearer part's.
+// Parts of a row meet with factors 2^d (d <= 0).  With codes, whose references hold their
+// pages' scales, a part's sum of weights may count although its factor is below 2^-126: the
+// factor is a square, too, and its root taken twice.  What a factor below 2^-126 leaves of
+// products with V is nothing beside the nearer part's.
+template <bool CODES>
 struct PartFactor {
-  float far, rest;
+  float root;
+  __device__ __forceinline__ explicit PartFactor(float d)
+      : root(tc::ex2_approx(CODES ? 0.5f * d : d)) {}
+  __device__ __forceinline__ float all() const { return CODES ? root * root : root; }
+  __device__ __forceinline__ float of(float l) const { return CODES ? l * root * root : l * root; }
 };
-__device__ __forceinline__ PartFactor part_factor(float d) {
-  return {tc::ex2_approx(fmaxf(d, -100.f)), tc::ex2_approx(fminf(d + 100.f, 0.f))};
-}
 
 // |x| for the largest magnitude: NaN and infinity do not count.
 __device__ __forceinline__ float finite_abs(float x) {

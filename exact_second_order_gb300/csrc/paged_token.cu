@@ -424,11 +424,10 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
           m = fmaxf(R[nt][e], m);
-          const PartFactor pf = part_factor(R[nt][e] - m);
-          const float f = R[nt][e] == -INFINITY ? 0.f : pf.far;
+          const PartFactor<CODES> pf(R[nt][e] == -INFINITY ? -INFINITY : R[nt][e] - m);
+          const float f = pf.all();
           R[nt][e] = m;
-          l[nt][e] *= f;
-          if (CODES) l[nt][e] *= pf.rest;
+          l[nt][e] = pf.of(l[nt][e]);
 #pragma unroll
           for (int i = 0; i < C::kMT; ++i) {
             O[nt][i][e] *= f;
@@ -559,10 +558,10 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
     for (int w = 0; w < NW; ++w) {
       const float* p = w0 + w * kStep;
       const float r = p[kRL + row];
-      const PartFactor pf = part_factor(r - m[i]);
-      const float f = r == -INFINITY ? 0.f : pf.far;
+      const PartFactor<CODES> pf(r == -INFINITY ? -INFINITY : r - m[i]);
+      const float f = pf.all();
       const float4 v = *reinterpret_cast<const float4*>(p + row * C::kPitch + c);
-      sum[i] = fmaf(f, p[kRL + kRowsPadded + row] * (CODES ? pf.rest : 1.f), sum[i]);
+      sum[i] = fmaf(pf.root, p[kRL + kRowsPadded + row] * (CODES ? pf.root : 1.f), sum[i]);
       o[i].x = fmaf(f, v.x, o[i].x), o[i].y = fmaf(f, v.y, o[i].y);
       o[i].z = fmaf(f, v.z, o[i].z), o[i].w = fmaf(f, v.w, o[i].w);
     }
@@ -595,9 +594,9 @@ __global__ void __launch_bounds__(32 * NW, (Tok<DH, CODES, NT>::kTwo ? 2 : 1))
         const float4 ml = tc::ld_shared_cluster_f4(tc::mapa_shared(here + (kRL + 4 * row) * 4, q));
         const float4 v =
             tc::ld_shared_cluster_f4(tc::mapa_shared(here + (row * C::kPitch + c) * 4, q));
-        const PartFactor pf = part_factor(ml.x - m[i]);
-        const float f = ml.x == -INFINITY ? 0.f : pf.far;
-        sum[i] = fmaf(f, ml.y * (CODES ? pf.rest : 1.f), sum[i]);
+        const PartFactor<CODES> pf(ml.x == -INFINITY ? -INFINITY : ml.x - m[i]);
+        const float f = pf.all();
+        sum[i] = fmaf(pf.root, ml.y * (CODES ? pf.root : 1.f), sum[i]);
         o[i].x = fmaf(f, v.x, o[i].x), o[i].y = fmaf(f, v.y, o[i].y);
         o[i].z = fmaf(f, v.z, o[i].z), o[i].w = fmaf(f, v.w, o[i].w);
       }

@@ -639,11 +639,10 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       load(0);
       mt = fmaxf(mt, max_of(0));
       const bool raise = !blind && mt > m + kRescale;
-      const PartFactor pf = part_factor(m - mt);
-      const float fac = raise ? (m == -INFINITY ? 0.f : pf.far) : 1.f;
+      const PartFactor<CODES> pf(m == -INFINITY ? -INFINITY : m - mt);
+      const float fac = raise ? pf.all() : 1.f;
       if (raise) {
-        l *= fac;
-        if (CODES) l *= pf.rest;
+        l = pf.of(l);
         m = mt;
       }
       // Tiles for careful().  Large references vote with the raised ones: a vote of their own
@@ -710,11 +709,10 @@ __global__ void __launch_bounds__((Cfg<DH, MT, CODES>::kThreads), 1)
       named_bar_sync(1, 256);
       const float m0 = sm.part_m[0][r], m1 = sm.part_m[1][r];
       mm = fmaxf(m0, m1);
-      const PartFactor f0 = part_factor(m0 - mm), f1 = part_factor(m1 - mm);
-      s0 = m0 == -INFINITY ? 0.f : f0.far;
-      s1 = m1 == -INFINITY ? 0.f : f1.far;
-      lsum = CODES ? s0 * (sm.part_l[0][r] * f0.rest) + s1 * (sm.part_l[1][r] * f1.rest)
-                   : s0 * sm.part_l[0][r] + s1 * sm.part_l[1][r];
+      const PartFactor<CODES> f0(m0 == -INFINITY ? -INFINITY : m0 - mm);
+      const PartFactor<CODES> f1(m1 == -INFINITY ? -INFINITY : m1 - mm);
+      s0 = f0.all(), s1 = f1.all();
+      lsum = f0.of(sm.part_l[0][r]) + f1.of(sm.part_l[1][r]);
     }
     if (blind) lsum = 0.f;
     const bool any0 = T > 0 && !blind, any1 = MT == 1 && T > 1 && !blind;

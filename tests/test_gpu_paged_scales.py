@@ -69,3 +69,30 @@ def test_every_key_counts(c, cap, bias, kind):
     assert bool(O.isfinite().all())
     assert ref.worst(L, val["L"], bound["L"]) <= 1
     assert ref.worst(O, val["O"], bound["O"]) <= 1
+
+
+@pytest.mark.parametrize("c", [(3, 6, 2, 150, 10, 16, 64, BF), (1, 4, 2, 100, 30, 32, 128, BF), (2, 8, 2, 1, 30, 16, 128, BF),
+                               (1, 8, 1, 3, 90, 64, 64, BF)], ids=lambda c: "-".join(str(v).replace("torch.", "") for v in c))
+@pytest.mark.parametrize("kind", [E4M3, BF])
+def test_a_key_far_ahead_has_all(c, kind):
+    """Scores hundreds above all others': what the others' values would add is no number of
+    32 bits, so an element of 0 stays 0."""
+    B, H, Hkv, Nq, M, T, d, dtype = c
+    pools, _ = pag.pools(B * M, Hkv, T, d, kind, spread=0.0)
+    table = pag.table_of(B, M, B * M)
+    page = table[:, M // 2].long()
+    Q = torch.ones((B, H, Nq, d), device="cuda").to(dtype)
+    for t in pools[:2]:  # token 3 of a page in the middle: keys of 2, values of 0 and 2
+        rows = torch.full((B, Hkv, d), 2.0, device="cuda")  # at most 448 scales, as a page's largest is above 1.75
+        if t is pools[1]:
+            rows = 2.0 * (torch.arange(d, device="cuda") % 2).expand(B, Hkv, d)
+        if kind is E4M3:
+            scale = (pools[2] if t is pools[0] else pools[3])[page][..., None]
+            t.view(torch.uint8)[page, :, 3] = (rows / scale).to(E4M3).view(torch.uint8)
+        else:
+            t[page, :, 3] = rows.to(BF)
+    O, L = fb.attention_paged(Q, fb.PagedCache(*pools), table, 3.0)
+    want = (2.0 * (torch.arange(d, device="cuda") % 2)).expand(O.shape)
+    assert torch.equal(O.float(), want)
+    # 3 times 2 d, with the sums of products and log2 e rounded in 32 bits.
+    assert bool(((L - 6.0 * d).abs() <= 6.0 * d * (d + 8) * 2.0 ** -24).all())
