@@ -27,10 +27,14 @@ using namespace paged;
 // flight; the page's largest magnitude meets in shuffles and, across warps, in shared
 // memory, and the rows are turned again for their codes (cheaper than to keep them: 64
 // registers and two blocks an SM).  Every element is read and written once.
-// Measured (two prompts of 8192 tokens, H32 Hkv8 d128, e4m3): 88 us, 4.2 TB/s of the 369 MB,
-// 62% of the copy rate.  It is bound by the bytes in flight and by issue (54% of the slots):
-// four eights with the next four behind them and 119 registers 118 us, sixteen lanes a row
-// 107, questions asked lane by lane (KIND 1) 105.
+// Measured (two prompts of 8192 tokens, H32 Hkv8 d128, e4m3): 87 to 88 us, 4.2 TB/s of the
+// 369 MB, 62% of the copy rate, with neither DRAM (48% of its peak) nor issue (53% of the
+// slots) full: a block asks for its next heads at the top of a round, and nothing is under
+// way while its warps meet, turn the rows again and write, in 2.5 waves of blocks.  Four
+// eights with the next four behind them and 119 registers took 118 us, sixteen lanes a row
+// 107.  Questions asked lane by lane (KIND 1): 93 with half of each head turning, 101 with
+// neighbouring pairs; normed 106; pages of 128 tokens, two tokens a slot, 105; a bf16 cache
+// 75, fp32 projections 168.
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 512;
 constexpr int kInFlight = 4;

@@ -5,9 +5,12 @@
 //   l = sum exp2(x - R),  O^T = (sum V^T p) / l,  L = (R + log2 l) ln 2,
 // where K and V are a page's codes: the scale of the keys goes into the scores, that
 // of the values into the exponent of the weights, so that a product's operands are
-// codes (exact in fp16) and weights of at most 2^8 (16 bits each, 11 significant),
-// however far the pages' scales are apart.  Q is scaled row by row, by a power of
-// two, into fp16's reach.
+// codes (exact in fp16) and weights of at most 2^8 (16 bits each, 11 significant), with
+// sums in 32 bits that hold however far the pages' scales are apart (paged.cuh).  Q is
+// scaled row by row, by a power of two, into fp16's reach.  With a bf16 cache weights are
+// bf16, as in the dense call: both operands of a product have one type, fp16 would not
+// hold what V may be, and two halves of a weight would double the products with V; l sums
+// them unrounded.
 //
 // The keys' bytes bound it (2 d bytes a key and head for e4m3), not the products: a
 // warp holds all rows and streams pages alone, 16 tokens at a time, through a ring of
@@ -20,8 +23,11 @@
 // of four tokens, paired by byte permutes); which token of a tile is which row of a
 // product (token_of) is chosen so that in the boxes' swizzle both reads are without bank
 // conflicts.  The weights go from accumulator to operand by two 8 x 8 transposes.
-// Measured: 32 requests of up to 8192 keys (H32 Hkv8 d128, e4m3) 55 us and 5 for the join,
-// 329 MB, 5.7 TB/s, 84% of the copy rate; 64 of 8192 keys 6.2 TB/s.
+// Measured: 32 requests of up to 8192 keys (H32 Hkv8 d128, e4m3) 54 to 55 us and 5 for the
+// join, 329 MB, 5.9 to 6.1 TB/s (5.5 with the join, 81% of the copy rate); 64 of 8192 keys,
+// after a flush, 185 us with the join, 5.8 TB/s; a bf16 cache 94 us, 655 MB, 7.0 TB/s of
+// which a part lay in the L2.  Drafted tokens (16 requests of 4, up to 4096 keys, H16
+// Hkv4) 28 us capped, 24 not: 128 blocks on 152 SMs, the longest with 2048 keys.
 // The warps' parts meet in shared memory.  A group's keys are cut into runs: where the
 // groups are few, as many as fill the SMs once, in clusters whose parts meet in
 // distributed shared memory (and across clusters in a second launch); where they are

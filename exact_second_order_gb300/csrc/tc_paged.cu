@@ -5,8 +5,12 @@
 //   l = sum exp2(score(S) - m),  O = (sum P~ V) / l,  L = (m + log2 l) ln 2,
 // where K and V are a page's codes: s_K goes into the score of its 16-column chunks
 // and s_V into the exponent of their weights, so the MMAs' operands are codes (exact in
-// fp16) and weights of at most 2^8, however far the pages' scales are apart.  Q is
-// scaled row by row, by a power of two, into fp16's reach; a bf16 cache runs in bf16.
+// fp16) and weights of at most 2^8 (11 significant bits), with sums in 32 bits that hold
+// however far the pages' scales are apart (paged.cuh).  Q is scaled row by row, by a power
+// of two, into fp16's reach.  A bf16 cache runs in bf16, its weights too, the MMA's other
+// operand V being bf16 (a product of two halves of P~ would double its MMAs); l sums them
+// unrounded, and O is off by 2.2e-3 in norm for that and its own rounding (alone 1.7e-3,
+// which is what 8-bit caches are off by).
 //
 // As in the dense kernel, two elementwise warpgroups work on score tiles in TMEM, P~
 // takes the scores' place as the A operand of P~ V, and one thread issues the MMAs.
@@ -23,13 +27,16 @@
 //   MT = 1: 128 rows, the warpgroups take alternate key tiles and merge their (m, l,
 //     O~) at the end; few blocks are also cut along the keys and joined by a second
 //     launch.
-// Measured (H32 Hkv8 d128, 2048 rows behind 14336 keys): 452 us, 1141 TFLOP/s, in 1.7 waves;
-// dense bf16 keys 429.  Four such prompts, padded, 1318 us, a bf16 cache 1111, dense keys
-// 1109 to 1125.  At d = 128 the MMAs of 64-key tiles cost 641 cycles for 512 of products and
-// shared memory gives them 100 of its 128 bytes a cycle: the converters' 32 KB a tile take
-// most of the rest, and 52% of the tensor pipe's cycles are busy (16-bit caches 64%).  Tiles
-// of 128 keys would cost less, but with two score buffers only a warpgroup waits for its
-// MMAs (749 us before the ring).
+// Measured (H32 Hkv8 d128, 2048 rows behind 14336 keys): 456 us, 1130 TFLOP/s, in 1.7 waves
+// (the longest SM has 480 key tiles where even shares are 408); dense bf16 keys 427, a bf16
+// cache 372.  Four such prompts, padded, 1328 us, a bf16 cache 1103, dense keys 1109.  At
+// d = 128 the MMAs of 64-key tiles cost 641 cycles for 512 of products and shared memory
+// gives them 100 of its 128 bytes a cycle: the converters' 32 KB a tile take most of the
+// rest, and 51% of the tensor pipe's cycles are busy (16-bit caches 64%).  Tiles of 128 keys
+// would cost less, but with two score buffers only a warpgroup waits for its MMAs (749 us
+// before the ring).  At d = 64 the same rows take 339 us, a bf16 cache 294, dense keys 290:
+// no pipe is full (tensor 35%, exponentials 35%, issue 57%), the hand-offs between MMAs and
+// elementwise warps bound it as in the dense kernel.
 #include "paged.cuh"
 #include "tc_attn.cuh"
 

@@ -309,9 +309,9 @@ flashbob_status flashbob_qk_norm_rope_grad(const void* QKV, const float* wq, con
  *        token are not read.  Batch entries may share pages that are only read.
  *   k_scale, v_scale: fp32 [P,Hkv] with FLASHBOB_E4M3, else NULL: a page's codes
  *        times its scale are its values.  Scales are powers of two within
- *        2^-60 .. 2^60, as flashbob_cache_append writes them; any have to be finite
- *        and > 0 (what the pages of a cache hold before the first append does not
- *        matter).  Where a scale is no power of two, values may be rounded to bf16
+ *        2^-60 .. 2^60, as flashbob_cache_append writes them; others within that
+ *        range are allowed (what the pages of a cache hold before the first append does
+ *        not matter).  Where a scale is no power of two, values may be rounded to bf16
  *        before a product.
  *
  * flashbob_cache_append: the projection, as flashbob_qk_norm_rope, into the pages.
@@ -327,7 +327,8 @@ flashbob_status flashbob_qk_norm_rope_grad(const void* QKV, const float* wq, con
  *   writes row 0 starts its page anew, and what lay behind the last new token of a
  *   page is lost with it.  Rounding is to nearest, ties to even; beyond 448 s
  *   (s at most 2^60, and infinities) becomes 448 s, NaN stays NaN.
- *   Two batch entries must not append to one page in one call.  One launch.
+ *   In one call a page is appended to through one entry of the table alone: not by
+ *   two batch entries, and not at two places of one.  One launch.
  */
 flashbob_status flashbob_cache_append(const void* QKV, const float* wq, const float* wk,
                                       const float* freqs, const int* positions,
@@ -354,7 +355,11 @@ flashbob_status flashbob_cache_read(const void* K, const void* V, const float* k
  * flashbob_attention over the keys and values of the pages, Nk = M T: the same
  * ranges, q_pos, slopes, tau, cap and causal, the same limits, and the same about
  * what nobody sees (the rest of a page, and pages behind the last token, may hold
- * anything).  With FLASHBOB_E4M3, tau (capped: tau / cap) times the largest
+ * anything).  In bf16 calls weights are rounded before the product with V, to 11
+ * significant bits with FLASHBOB_E4M3 (times the page's scale, in steps of 2^-24 of
+ * the row's largest at the finest; Q likewise in steps of 2^-24 of the row's largest
+ * element) and to 8, bf16, with a bf16 cache (head sizes 64 and 128).
+ *   With FLASHBOB_E4M3, tau (capped: tau / cap) times the largest
  * magnitude of a query that sees a key: at most 2^60.  One launch, and one more where
  * the keys are cut into runs.
  *   workspace: `forward` bytes of flashbob_attention_paged_workspace (may be NULL
