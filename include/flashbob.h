@@ -204,8 +204,9 @@ flashbob_status flashbob_attention_jvp(const void* Q, const void* K, const void*
  *   slopes: fp32 [H], |slopes[h] (pos_i - j)| below 2^60; NULL: no bias.  A
  *        constant: it has no gradient.
  *   tau, and where cap > 0 cap and tau / cap: within 2^-120 .. 2^120.
- *   A row's largest score: below 2^26 in size (in 32 bits scores beyond that
- *        are apart by more than weights can tell, and weights may overflow).
+ *   Scores are held in 32 bits, and weights are off by what those lose of a score
+ *        (2^-24 of it); a row's largest has to be below 2^26 in size, or weights
+ *        may overflow.
  *   Limits: as flashbob_prep; (H / Hkv) * Nq and Nk below 2^31 - 1024.
  *
  * flashbob_attention: O [B,H,Nq,d] of in_dtype, L [B,H,Nq] fp32.

@@ -138,3 +138,26 @@ def test_second_order_over_cached_keys(dtype, kind, H, d, N):
     tol = 2 * 2.0 ** -8 if dtype is BF else 1e-5
     for got, w in zip((Od, Ld), want):
         assert float((got.double() - w).norm() / w.norm()) <= tol
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,P", [(E4M3, (1 << 32) // (2 * 128 * 128) + 4), (BF, (1 << 31) // (2 * 128 * 128) + 4)])
+def test_appends_past_32_bit_offsets(kind, P):
+    """Pages behind 2^32 bytes and 2^31 elements get what pages of a small pool get."""
+    Hkv, T, d, N = 2, 128, 128, 300
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn((1, N, 4 + 2 * Hkv, d), generator=g, device="cuda").to(BF)
+    start = torch.tensor([50], dtype=torch.int32, device="cuda")
+    at = torch.tensor([[P - 1, 0, P - 3]], dtype=torch.int32, device="cuda")
+    small, far = fb.PagedCache.empty(3, Hkv, T, d, dtype=kind), fb.PagedCache.empty(P, Hkv, T, d, dtype=kind)
+    local = torch.arange(3, device="cuda")[None].int()
+    Q = [fb.cache_append(x, 4, c, t, kv_start=start) for c, t in ((small, local), (far, at))]
+    assert torch.equal(*Q)
+    for a, b in ((small.K, far.K), (small.V, far.V), (small.k_scale, far.k_scale), (small.v_scale, far.v_scale)):
+        if a is not None:
+            for i, p in enumerate(at[0].tolist()):
+                assert torch.equal(a[i].view(torch.uint8), b[p].view(torch.uint8))
+    for a, b in zip(fb.cache_read(small, local, 350), fb.cache_read(far, at, 350)):
+        assert torch.equal(a, b)
+    # and nothing else has been touched
+    assert not far.K.view(torch.uint8)[1:P - 3].any() and not far.V.view(torch.uint8)[P - 2].any()
